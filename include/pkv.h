@@ -420,6 +420,145 @@ PKV_API pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, c
                                            const pkv_decode_opts* opts, void* stream);
 
 /*
+ * pkv_multiquery_q8_workspace_size -- bytes of workspace
+ * pkv_multiquery_attention_q8 needs (zero-fill once before first use; completed
+ * calls leave its counters at zero; one workspace per call in flight). Returns 0
+ * for sizes the call rejects.
+ */
+PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                                int32_t max_query_len, const pkv_cache_desc* desc);
+
+/*
+ * pkv_multiquery_attention_q8 -- causal attention of a chunk of new tokens per
+ * sequence over the low-bit pools: pkv_multiquery_attention's result over the
+ * values the cached rows stand for (code * scale), for any number of queries up
+ * to 65536 per sequence and head_dim 64 or 128. With it a cache that
+ * pkv_append_q8 fills is prefilled in chunks as a bf16 cache is.
+ *
+ * Sequence i holds n = context_lens[i] tokens, the last nq = query_start[i+1] -
+ * query_start[i] of which are new (appended before the call); query t sits in row
+ * query_start[i] + t of q and out and attends to tokens 0 .. n - nq + t:
+ *     out[r][h] = sum_p softmax_p(scale * dot(q[r][h], K_j(p))) V_j(p),  p <= n - nq + t
+ * nq may be 0 (no rows) and may equal n (a prompt's first chunk). A token in a
+ * block whose id is out of range is absent (it has no weight; a row with no token
+ * at all is zero). Slots past a sequence's end, and tokens a row may not see, may
+ * hold anything, NaN and infinities included.
+ *
+ *   q, out        device, bf16 [query_start[batch]][num_q_heads][head_dim].
+ *                 Rows no sequence names are left as they were.
+ *   query_start   device, int32 [batch + 1], non-decreasing row offsets.
+ *   max_query_len host bound on nq, 1 .. 65536 (above: PKV_ERR_UNSUPPORTED).
+ *   workspace     >= pkv_multiquery_q8_workspace_size(...) bytes, 256-byte aligned,
+ *                 zero-filled before its first use.
+ * fp32 accumulation, one rounding to bf16. Up to 32 query rows per (sequence, KV
+ * head) at head_dim 128 run on pkv_decode_attention_q8's kernel with its
+ * roundings. Above that (and at head_dim 64) K enters the products exactly (codes
+ * and q in bf16, the K scale applied to the fp32 score); a V value is rounded to
+ * f16 relative to its step's largest V scale and a softmax weight to f16.
+ * Errors, checked mode and the device status bits as pkv_multiquery_attention.
+ */
+PKV_API pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes,
+                                               const float* scales, const int32_t* block_tables,
+                                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                               const int32_t* query_start, int32_t batch, int32_t num_q_heads,
+                                               int32_t max_query_len, float scale, void* out, void* workspace,
+                                               size_t workspace_bytes, const pkv_cache_desc* desc, uint32_t flags,
+                                               void* stream);
+
+/*
+ * pkv_gather -- read tokens back out of the paged cache.
+ *
+ * Sequence i's tokens token_start[i] .. token_start[i] + rows - 1, rows =
+ * row_start[i+1] - row_start[i], become rows row_start[i] .. row_start[i+1] - 1 of
+ * k_out and v_out ([num_rows][num_kv_heads][head_dim] of desc->dtype): the inverse
+ * of pkv_append, bit for bit.
+ *
+ *   token_start   device, int32 [batch], or NULL: every sequence from its token 0.
+ *   row_start     device, int32 [batch + 1], non-decreasing.
+ *   num_rows      rows k_out and v_out hold; >= 0, below 2^31. 0 enqueues nothing.
+ * A sequence whose token range leaves its context (token_start < 0, or
+ * token_start + rows > context_lens[i]), whose context leaves its table or whose
+ * rows leave [0, num_rows] is skipped and sets PKV_DEVERR_RANGE; so is a block
+ * whose id is out of range (its rows are left as they were). With
+ * PKV_FLAG_CHECKED the call returns PKV_ERR_RANGE instead, having written
+ * nothing (a block id is then checked over the whole context). Rows no sequence
+ * names are left as they were. Outputs must not overlap the pools. Other errors
+ * as pkv_append and pkv_decode_attention.
+ */
+PKV_API pkv_status pkv_gather(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                              int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* token_start,
+                              const int32_t* row_start, int32_t batch, int64_t num_rows, void* k_out, void* v_out,
+                              const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/*
+ * pkv_gather_q8 -- pkv_gather over the low-bit pools: the values the rows stand
+ * for, code * scale rounded once to float32 (out_dtype PKV_F32), and from there
+ * to bf16 (PKV_BF16). Arguments, checks and errors as pkv_gather.
+ */
+PKV_API pkv_status pkv_gather_q8(const void* k_codes, const void* v_codes, const float* scales,
+                                 const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, const int32_t* token_start, const int32_t* row_start,
+                                 int32_t batch, int64_t num_rows, void* k_out, void* v_out, int32_t out_dtype,
+                                 const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/*
+ * pkv_verify_drafts -- verification of drafted tokens against the target's
+ * probabilities, from given uniform numbers.
+ * (release page, Architectural Breakdown 2: rejection sampling over the K draft
+ * tokens that the target scored in one pass, leaving the target's output
+ * distribution unchanged.)
+ *
+ * Sequence i drafted k = draft_start[i+1] - draft_start[i] tokens x_0 .. x_{k-1}
+ * (rows draft_start[i] + j of draft_tokens, draft_probs and accept_uniform). The
+ * target scored k + 1 positions, rows query_start[i] + j of target_probs (the rows
+ * of the multi-query attention call that verifies them); p_j is the target's row
+ * j and q_j the draft's. With u_j = accept_uniform, w = sample_uniform[i]:
+ *   a  = the number of leading drafts with u_j * q_j(x_j) < p_j(x_j)
+ *        (the products compared exactly);
+ *   r  = max(p_a - q_a, 0) if a < k (float32; p_a itself if that is zero
+ *        everywhere), else p_k;
+ *   y  = the lowest index whose running sum of r exceeds w times the sum of r
+ *        (the last index with r > 0 if rounding leaves none).
+ * out_tokens[i] = x_0 .. x_{a-1}, y, then -1 up to max_draft_len + 1 entries;
+ * num_accepted[i] = a; new_context_lens[i] = context_lens[i] - (k - a): the
+ * context length (with the k + 1 new tokens of the verification) less the
+ * rejected drafts, whose cache slots the next append overwrites. An entry of r
+ * counts only if it is a finite number above zero; if none is, y is -1. Running
+ * sums carry at least 40 bits and their order is fixed, so a call's result never
+ * depends on scheduling.
+ *
+ *   target_probs  device, [num_target_rows][vocab] of `dtype` (PKV_F32 or
+ *                 PKV_BF16), rows target_stride elements apart (>= vocab).
+ *   draft_probs   the same for drafts ([num_draft_rows], draft_stride), or NULL:
+ *                 each draft was certain (q_j is 1 at x_j and 0 elsewhere).
+ *   draft_tokens  device, int32 [num_draft_rows]; accept_uniform float
+ *                 [num_draft_rows] in [0, 1). Unused (may be NULL) when
+ *                 num_draft_rows is 0.
+ *   query_start,
+ *   draft_start   device, int32 [batch + 1]. A sequence has k + 1 target rows, or
+ *                 no row and no draft (idle: num_accepted 0, tokens all -1).
+ *   sample_uniform device, float [batch] in [0, 1).
+ *   context_lens, new_context_lens  device, int32 [batch], both or neither NULL;
+ *                 may be the same array.
+ *   out_tokens    device, int32 [batch][max_draft_len + 1]; num_accepted int32 [batch].
+ *   max_draft_len host bound on k, 0 .. 65535; vocab 1 .. 2^20.
+ * Probability pointers are aligned to their element. A sequence whose rows leave
+ * the arrays, number other than k + 1, or whose k exceeds max_draft_len gets
+ * num_accepted -1, tokens -1 and its old context length, and sets
+ * PKV_DEVERR_RANGE; a draft token outside [0, vocab) sets it too and counts as
+ * rejected. With PKV_FLAG_CHECKED either returns PKV_ERR_RANGE, having written
+ * nothing. One launch, no workspace.
+ */
+PKV_API pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_stride, int64_t num_target_rows,
+                                     const void* draft_probs, int64_t draft_stride, int64_t num_draft_rows,
+                                     int32_t dtype, int32_t vocab, const int32_t* draft_tokens,
+                                     const float* accept_uniform, const float* sample_uniform,
+                                     const int32_t* query_start, const int32_t* draft_start, int32_t batch,
+                                     int32_t max_draft_len, const int32_t* context_lens,
+                                     int32_t* new_context_lens, int32_t* out_tokens, int32_t* num_accepted,
+                                     uint32_t flags, void* stream);
+
+/*
  * pkv_decode_attention_noalloc -- pkv_decode_attention without a
  * caller-provided workspace. The pages have no counterpart to this call; it
  * exists for callers that cannot allocate device memory: plugins running

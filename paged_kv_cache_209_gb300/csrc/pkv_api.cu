@@ -100,6 +100,61 @@ pkv_status check_desc_q8(const pkv_cache_desc* d, bool attention) {
     return PKV_OK;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Int8 multi-query calls: the split kernel of pkv_multiquery.cu takes what it can hold.
+bool split_kernel_takes(const pkv_cache_desc* d, int32_t max_query_len, int G) {
+    return d->head_dim == 128 && static_cast<int64_t>(max_query_len) * G <= kMqMaxRows;
+}
+
+// Both reading-back calls, after the checks of their descriptors.
+pkv_status run_gather(const void* k, const void* v, const float* scales, const int32_t* tables, int32_t max_blocks,
+                      const int32_t* lens, const int32_t* token_start, const int32_t* row_start, int32_t batch,
+                      int64_t num_rows, void* k_out, void* v_out, int32_t out_dtype, const pkv_cache_desc* desc,
+                      uint32_t flags, cudaStream_t s) {
+    if (flags & PKV_FLAG_TEST_STALL) return PKV_ERR_UNSUPPORTED;
+    if (batch < 0 || num_rows < 0 || num_rows >= (int64_t(1) << 31)) return PKV_ERR_SHAPE;
+    if (batch == 0 || num_rows == 0) return PKV_OK;
+    if (!table_width_ok(batch, max_blocks)) return PKV_ERR_SHAPE;
+    if (!k || !v || !tables || !lens || !row_start || !k_out || !v_out) return PKV_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(tables) ||
+        !aligned4(lens) || !aligned4(token_start) || !aligned4(row_start))
+        return PKV_ERR_ALIGN;
+    GatherArgs a{};
+    a.k = k;
+    a.v = v;
+    a.scales = scales;
+    a.tables = tables;
+    a.lens = lens;
+    a.token_start = token_start;
+    a.row_start = row_start;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.status = device_info().status;
+    a.num_blocks = desc->num_blocks;
+    a.num_rows = num_rows;
+    a.max_blocks = max_blocks;
+    a.batch = batch;
+    a.kv_heads = desc->num_kv_heads;
+    if (a.status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        const pkv_status st = run_checked([&](unsigned int* verdict) {
+            cudaError_t e = launch_check_decode(tables, max_blocks, lens, batch, desc->num_blocks, 0, verdict, s);
+            return e != cudaSuccess ? e : launch_check_gather(a, verdict, s);
+        }, s);
+        if (st != PKV_OK) return st;
+    }
+    for (int32_t b0 = 0; b0 < batch; b0 += kMaxBatchPerLaunch) {
+        a.tables = tables + static_cast<int64_t>(b0) * max_blocks;
+        a.lens = lens + b0;
+        a.token_start = token_start == nullptr ? nullptr : token_start + b0;
+        a.row_start = row_start + b0;
+        a.batch = batch - b0 < kMaxBatchPerLaunch ? batch - b0 : kMaxBatchPerLaunch;
+        if (launch_gather(a, *desc, out_dtype, s) != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
 }  // namespace
 
 int device_sm_count() {
@@ -652,6 +707,169 @@ pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, const voi
         if (launch_multiquery(a, s) != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;
+}
+
+size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                        int32_t max_query_len, const pkv_cache_desc* desc) {
+    if (check_desc_q8(desc, false) != PKV_OK || batch < 0 || !q_heads_ok(num_q_heads, desc)) return 0;
+    if (max_query_len < 1 || max_query_len > kMaxQueryLen) return 0;
+    const int G = num_q_heads / desc->num_kv_heads;
+    if (split_kernel_takes(desc, max_query_len, G))
+        return pkv_decode_q8_workspace_size(batch, num_q_heads, max_blocks_per_seq, max_query_len, desc, nullptr);
+    return chunk_q8_workspace_bytes(batch, desc->num_kv_heads, desc->head_dim);
+}
+
+pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t* context_lens, const int32_t* query_start, int32_t batch,
+                                       int32_t num_q_heads, int32_t max_query_len, float scale, void* out,
+                                       void* workspace, size_t workspace_bytes, const pkv_cache_desc* desc,
+                                       uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_multiquery_attention_q8");
+    pkv_status st = check_desc_q8(desc, false);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || !q_heads_ok(num_q_heads, desc)) return PKV_ERR_SHAPE;
+    if (!isfinite(scale) || max_query_len < 1) return PKV_ERR_SHAPE;
+    if (max_query_len > kMaxQueryLen) return PKV_ERR_UNSUPPORTED;
+    if (flags & PKV_FLAG_TEST_STALL) return PKV_ERR_UNSUPPORTED;  // the hook is pkv_decode_attention_q8's
+    if (batch == 0) return PKV_OK;
+    if (!table_width_ok(batch, max_blocks_per_seq)) return PKV_ERR_SHAPE;
+    if (!q || !k_codes || !v_codes || !scales || !block_tables || !context_lens || !query_start || !out || !workspace)
+        return PKV_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(scales) || !aligned16(out) ||
+        !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PKV_ERR_ALIGN;
+    const int G = num_q_heads / desc->num_kv_heads;
+    if (split_kernel_takes(desc, max_query_len, G))
+        return pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens,
+                                       query_start, batch, num_q_heads, max_query_len, scale, out, workspace,
+                                       workspace_bytes, desc, flags, nullptr, stream);
+    if (workspace_bytes < chunk_q8_workspace_bytes(batch, desc->num_kv_heads, desc->head_dim))
+        return PKV_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned int* status = device_info().status;
+    if (status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        st = run_checked([&](unsigned int* verdict) {
+            cudaError_t e = launch_check_decode(block_tables, max_blocks_per_seq, context_lens, batch,
+                                                desc->num_blocks, 0, verdict, s);
+            if (e != cudaSuccess) return e;
+            return launch_check_queries(context_lens, query_start, batch, max_query_len, verdict, s);
+        }, s);
+        if (st != PKV_OK) return st;
+    }
+    for (int32_t b0 = 0; b0 < batch; b0 += kMaxBatchPerLaunch) {
+        ChunkArgs a{};
+        a.q = q;
+        a.k_codes = k_codes;
+        a.v_codes = v_codes;
+        a.scales = scales;
+        a.tables = block_tables + static_cast<int64_t>(b0) * max_blocks_per_seq;
+        a.lens = context_lens + b0;
+        a.qstart = query_start + b0;
+        a.out = out;
+        a.workspace = workspace;
+        a.status = status;
+        a.num_blocks = desc->num_blocks;
+        a.max_blocks = max_blocks_per_seq;
+        a.batch = batch - b0 < kMaxBatchPerLaunch ? batch - b0 : kMaxBatchPerLaunch;
+        a.q_heads = num_q_heads;
+        a.kv_heads = desc->num_kv_heads;
+        a.head_dim = desc->head_dim;
+        a.group = G;
+        a.max_query_len = max_query_len;
+        a.scale = scale;
+        if (launch_chunk_q8(a, s) != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_gather(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* token_start,
+                      const int32_t* row_start, int32_t batch, int64_t num_rows, void* k_out, void* v_out,
+                      const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_gather");
+    const pkv_status st = check_desc(desc);
+    if (st != PKV_OK) return st;
+    return run_gather(k_cache, v_cache, nullptr, block_tables, max_blocks_per_seq, context_lens, token_start, row_start,
+                      batch, num_rows, k_out, v_out, desc->dtype, desc, flags, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_gather_q8(const void* k_codes, const void* v_codes, const float* scales, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* token_start,
+                         const int32_t* row_start, int32_t batch, int64_t num_rows, void* k_out, void* v_out,
+                         int32_t out_dtype, const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_gather_q8");
+    const pkv_status st = check_desc_q8(desc, false);
+    if (st != PKV_OK) return st;
+    if (out_dtype != PKV_F32 && out_dtype != PKV_BF16) return PKV_ERR_DTYPE;
+    if (num_rows > 0 && batch > 0) {
+        if (scales == nullptr) return PKV_ERR_NULL;
+        if (!aligned16(scales)) return PKV_ERR_ALIGN;
+    }
+    return run_gather(k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, token_start, row_start,
+                      batch, num_rows, k_out, v_out, out_dtype, desc, flags, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_stride, int64_t num_target_rows,
+                             const void* draft_probs, int64_t draft_stride, int64_t num_draft_rows, int32_t dtype,
+                             int32_t vocab, const int32_t* draft_tokens, const float* accept_uniform,
+                             const float* sample_uniform, const int32_t* query_start, const int32_t* draft_start,
+                             int32_t batch, int32_t max_draft_len, const int32_t* context_lens,
+                             int32_t* new_context_lens, int32_t* out_tokens, int32_t* num_accepted, uint32_t flags,
+                             void* stream) {
+    NvtxRange nvtx_range("pkv_verify_drafts");
+    if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_DTYPE;
+    if (flags & PKV_FLAG_TEST_STALL) return PKV_ERR_UNSUPPORTED;
+    if (batch < 0 || vocab < 1 || vocab > kMaxVocab || max_draft_len < 0 || max_draft_len > kMaxDraftLen)
+        return PKV_ERR_SHAPE;
+    if (num_target_rows < 0 || num_target_rows >= (int64_t(1) << 31) || num_draft_rows < 0 ||
+        num_draft_rows >= (int64_t(1) << 31))
+        return PKV_ERR_SHAPE;
+    // a row stride: at least the row, and such that the last row's offset stays far inside 64 bits
+    const int64_t most = int64_t(1) << 31;
+    if (num_target_rows > 0 && (target_stride < vocab || target_stride >= most)) return PKV_ERR_SHAPE;
+    if (draft_probs != nullptr && num_draft_rows > 0 && (draft_stride < vocab || draft_stride >= most))
+        return PKV_ERR_SHAPE;
+    if (batch == 0) return PKV_OK;
+    if (!sample_uniform || !query_start || !draft_start || !out_tokens || !num_accepted) return PKV_ERR_NULL;
+    if (num_target_rows > 0 && !target_probs) return PKV_ERR_NULL;
+    if (num_draft_rows > 0 && (!draft_tokens || !accept_uniform)) return PKV_ERR_NULL;
+    if ((context_lens == nullptr) != (new_context_lens == nullptr)) return PKV_ERR_NULL;
+    const uintptr_t elem = dtype == PKV_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(target_probs) & elem) || (reinterpret_cast<uintptr_t>(draft_probs) & elem) ||
+        !aligned4(draft_tokens) || !aligned4(accept_uniform) || !aligned4(sample_uniform) || !aligned4(query_start) ||
+        !aligned4(draft_start) || !aligned4(context_lens) || !aligned4(new_context_lens) || !aligned4(out_tokens) ||
+        !aligned4(num_accepted))
+        return PKV_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    VerifyArgs a{};
+    a.target = target_probs;
+    a.draft = draft_probs;
+    a.draft_tokens = draft_tokens;
+    a.accept = accept_uniform;
+    a.sample = sample_uniform;
+    a.query_start = query_start;
+    a.draft_start = draft_start;
+    a.lens = context_lens;
+    a.new_lens = new_context_lens;
+    a.out_tokens = out_tokens;
+    a.num_accepted = num_accepted;
+    a.status = device_info().status;
+    a.target_stride = target_stride;
+    a.draft_stride = draft_stride;
+    a.num_target_rows = num_target_rows;
+    a.num_draft_rows = num_draft_rows;
+    a.vocab = vocab;
+    a.batch = batch;
+    a.max_draft_len = max_draft_len;
+    if (a.status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        const pkv_status st = run_checked([&](unsigned int* verdict) { return launch_check_verify(a, verdict, s); }, s);
+        if (st != PKV_OK) return st;
+    }
+    return launch_verify(a, dtype, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_device_status(uint32_t* bits_out, int clear, void* stream) {

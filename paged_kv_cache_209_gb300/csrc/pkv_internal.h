@@ -223,4 +223,75 @@ cudaError_t launch_multiquery(const MqArgs& a, cudaStream_t s);
 cudaError_t launch_check_queries(const int32_t* lens, const int32_t* qstart, int32_t batch, int32_t max_query_len,
                                  unsigned int* verdict, cudaStream_t s);
 
+// ---------------------------------------------------------------- chunk attention over int8 pools
+// Causal queries of each sequence's new tokens, any number of rows; see pkv_chunk_q8.cu.
+struct ChunkArgs {
+    const void* q;  // [query_start[batch]][q_heads][head_dim] bf16
+    const void* k_codes;
+    const void* v_codes;
+    const float* scales;  // [num_blocks][kv_heads][2 (K, V)][16]
+    const int32_t* tables;
+    const int32_t* lens;
+    const int32_t* qstart;  // [batch + 1], absolute rows of q / out
+    void* out;
+    void* workspace;
+    unsigned int* status;
+    int64_t num_blocks;
+    int32_t max_blocks;
+    int32_t batch;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t group;
+    int32_t max_query_len;
+    float scale;
+};
+size_t chunk_q8_workspace_bytes(int batch, int kv_heads, int head_dim);
+cudaError_t launch_chunk_q8(const ChunkArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- reading the cache back
+struct GatherArgs {
+    const void* k;
+    const void* v;
+    const float* scales;  // int8 pools only
+    const int32_t* tables;
+    const int32_t* lens;
+    const int32_t* token_start;  // null: every sequence from token 0
+    const int32_t* row_start;    // [batch + 1], absolute rows of the outputs
+    void* k_out;
+    void* v_out;
+    unsigned int* status;
+    int64_t num_blocks;
+    int64_t num_rows;
+    int32_t max_blocks;
+    int32_t batch;
+    int32_t kv_heads;
+};
+cudaError_t launch_gather(const GatherArgs& a, const pkv_cache_desc& d, int out_dtype, cudaStream_t s);
+cudaError_t launch_check_gather(const GatherArgs& a, unsigned int* verdict, cudaStream_t s);
+
+// ---------------------------------------------------------------- draft verification
+struct VerifyArgs {
+    const void* target;
+    const void* draft;  // null: every draft was certain
+    const int32_t* draft_tokens;
+    const float* accept;
+    const float* sample;
+    const int32_t* query_start;
+    const int32_t* draft_start;
+    const int32_t* lens;
+    int32_t* new_lens;
+    int32_t* out_tokens;
+    int32_t* num_accepted;
+    unsigned int* status;
+    int64_t target_stride, draft_stride, num_target_rows, num_draft_rows;
+    int32_t vocab;
+    int32_t batch;
+    int32_t max_draft_len;
+};
+constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxDraftLen = 65535;
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_check_verify(const VerifyArgs& a, unsigned int* verdict, cudaStream_t s);
+
 }  // namespace pkv

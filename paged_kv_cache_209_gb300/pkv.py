@@ -57,7 +57,9 @@ _lib = None
 EXPORTS = ("pkv_append", "pkv_copy_blocks", "pkv_decode_workspace_size", "pkv_decode_attention",
            "pkv_decode_prefixed_workspace_size", "pkv_decode_attention_prefixed", "pkv_decode_attention_noalloc",
            "pkv_multiquery_workspace_size", "pkv_multiquery_attention",
-           "pkv_append_q8", "pkv_copy_blocks_q8", "pkv_decode_q8_workspace_size", "pkv_decode_attention_q8", "pkv_device_status", "pkv_status_string", "pkv_version",
+           "pkv_append_q8", "pkv_copy_blocks_q8", "pkv_decode_q8_workspace_size", "pkv_decode_attention_q8",
+           "pkv_multiquery_q8_workspace_size", "pkv_multiquery_attention_q8", "pkv_gather", "pkv_gather_q8",
+           "pkv_verify_drafts", "pkv_device_status", "pkv_status_string", "pkv_version",
            "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_add_sequence", "pkv_pool_append", "pkv_pool_append_batch",
            "pkv_pool_share_prefix", "pkv_pool_release", "pkv_pool_sequence_length", "pkv_pool_page_table",
            "pkv_pool_block_tables", "pkv_pool_get_stats", "pkv_pool_validate")
@@ -107,6 +109,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pkv_decode_attention_noalloc.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp,
                                                  desc_p, u32, opts_p, vp]
     lib.pkv_decode_attention_noalloc.restype = ctypes.c_int
+    lib.pkv_multiquery_q8_workspace_size.argtypes = [i32, i32, i32, i32, desc_p]
+    lib.pkv_multiquery_q8_workspace_size.restype = ctypes.c_size_t
+    lib.pkv_multiquery_attention_q8.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp,
+                                                ctypes.c_size_t, desc_p, u32, vp]
+    lib.pkv_multiquery_attention_q8.restype = ctypes.c_int
+    lib.pkv_gather.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, i64, vp, vp, desc_p, u32, vp]
+    lib.pkv_gather.restype = ctypes.c_int
+    lib.pkv_gather_q8.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, i32, i64, vp, vp, i32, desc_p, u32, vp]
+    lib.pkv_gather_q8.restype = ctypes.c_int
+    lib.pkv_verify_drafts.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp,
+                                      vp, u32, vp]
+    lib.pkv_verify_drafts.restype = ctypes.c_int
     lib.pkv_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, vp]
     lib.pkv_device_status.restype = ctypes.c_int
     lib.pkv_status_string.argtypes = [ctypes.c_int]
@@ -419,6 +433,175 @@ def pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, context_l
         _ptr(context_lens), _ptr(query_start), batch, q_heads, max_query_len, ctypes.c_float(scale), _ptr(out),
         _ptr(workspace), workspace.numel(), ctypes.byref(desc), flags, _opts(0, num_ctas), _stream(stream)))
     return out
+
+
+def _one_device(**tensors) -> None:
+    """Every tensor on the current CUDA device: the library launches there, on its current stream."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"libpkv takes CUDA tensors only ({name} is on {t.device})")
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+
+
+def _int32(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} is int32")
+
+
+def pkv_multiquery_q8_workspace_size(batch: int, num_q_heads: int, max_blocks_per_seq: int, max_query_len: int,
+                                     k_codes) -> int:
+    """Workspace bytes of the int8 multi-query call; allocate them zero-filled and reuse them."""
+    desc = q8_desc(k_codes)
+    return int(load_library().pkv_multiquery_q8_workspace_size(batch, num_q_heads, max_blocks_per_seq, max_query_len,
+                                                               ctypes.byref(desc)))
+
+
+def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, context_lens, query_start, scale: float,
+                                max_query_len: int, out=None, workspace=None, flags: int = 0, stream=None):
+    """Causal attention of each sequence's new tokens over the int8 pools, any number of them:
+    ``q``/``out`` are bf16 [rows][q_heads][head_dim], ``query_start`` int32 [batch + 1] their row
+    offsets. Returns ``out`` (rows no sequence names are left as they were)."""
+    lib = load_library()
+    desc = q8_desc(k_codes)
+    _check_q8_pools(k_codes, v_codes, scales)
+    if q.dim() != 3 or q.shape[2] != desc.head_dim or q.dtype != torch.bfloat16:
+        raise ValueError("q is bf16 [rows][q_heads][head_dim]")
+    rows, q_heads, _ = q.shape
+    batch = int(context_lens.shape[0])
+    _int32(block_tables=block_tables, context_lens=context_lens, query_start=query_start)
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or query_start.shape != (batch + 1,):
+        raise ValueError("block_tables is [batch][max_blocks], query_start [batch + 1]")
+    max_blocks = int(block_tables.shape[1])
+    if out is None:
+        out = torch.empty_like(q)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out is bf16 of q's shape")
+    if workspace is None:
+        need = pkv_multiquery_q8_workspace_size(batch, q_heads, max_blocks, max_query_len, k_codes)
+        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+    _one_device(q=q, k_codes=k_codes, v_codes=v_codes, scales=scales, block_tables=block_tables,
+                context_lens=context_lens, query_start=query_start, out=out, workspace=workspace)
+    if rows == 0:                                            # no query anywhere: no row to write
+        return out
+    _check("pkv_multiquery_attention_q8", lib.pkv_multiquery_attention_q8(
+        _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
+        _ptr(query_start), batch, q_heads, max_query_len, ctypes.c_float(scale), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), ctypes.byref(desc), flags, _stream(stream)))
+    return out
+
+
+def _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start, k_out, v_out, dtype, device):
+    batch = int(context_lens.shape[0])
+    _int32(block_tables=block_tables, context_lens=context_lens, row_start=row_start, token_start=token_start)
+    if block_tables.dim() != 2 or block_tables.shape[0] != batch or row_start.shape != (batch + 1,):
+        raise ValueError("block_tables is [batch][max_blocks], row_start [batch + 1]")
+    if token_start is not None and token_start.shape != (batch,):
+        raise ValueError("token_start is [batch]")
+    want = (int(num_rows), desc.num_kv_heads, desc.head_dim)
+    k_out = torch.empty(want, dtype=dtype, device=device) if k_out is None else k_out
+    v_out = torch.empty(want, dtype=dtype, device=device) if v_out is None else v_out
+    if tuple(k_out.shape) != want or tuple(v_out.shape) != want or k_out.dtype != dtype or v_out.dtype != dtype:
+        raise ValueError(f"k_out and v_out are {want} of {dtype}")
+    return batch, int(block_tables.shape[1]), k_out, v_out
+
+
+def pkv_gather(k_cache, v_cache, block_tables, context_lens, row_start, num_rows: int, token_start=None, k_out=None,
+               v_out=None, flags: int = 0, stream=None):
+    """Tokens ``token_start[i] ..`` of each sequence as rows ``row_start[i] .. row_start[i+1]-1``:
+    returns ``(k_out, v_out)``, [num_rows][kv_heads][head_dim] of the pool dtype."""
+    lib = load_library()
+    _same_pools(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    batch, max_blocks, k_out, v_out = _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start,
+                                                   k_out, v_out, k_cache.dtype, k_cache.device)
+    _one_device(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
+                row_start=row_start, token_start=token_start, k_out=k_out, v_out=v_out)
+    _check("pkv_gather", lib.pkv_gather(
+        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), _ptr(token_start),
+        _ptr(row_start), batch, int(num_rows), _ptr(k_out), _ptr(v_out), ctypes.byref(desc), flags, _stream(stream)))
+    return k_out, v_out
+
+
+def pkv_gather_q8(k_codes, v_codes, scales, block_tables, context_lens, row_start, num_rows: int, token_start=None,
+                  out_dtype=torch.bfloat16, k_out=None, v_out=None, flags: int = 0, stream=None):
+    """``pkv_gather`` over the int8 pools: the values (code * scale) as ``out_dtype``, bf16 or float32."""
+    lib = load_library()
+    desc = q8_desc(k_codes)
+    _check_q8_pools(k_codes, v_codes, scales)
+    code = _dtype_code(out_dtype)
+    batch, max_blocks, k_out, v_out = _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start,
+                                                   k_out, v_out, out_dtype, k_codes.device)
+    _one_device(k_codes=k_codes, v_codes=v_codes, scales=scales, block_tables=block_tables,
+                context_lens=context_lens, row_start=row_start, token_start=token_start, k_out=k_out, v_out=v_out)
+    _check("pkv_gather_q8", lib.pkv_gather_q8(
+        _ptr(k_codes), _ptr(v_codes), _ptr(scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
+        _ptr(token_start), _ptr(row_start), batch, int(num_rows), _ptr(k_out), _ptr(v_out), code, ctypes.byref(desc),
+        flags, _stream(stream)))
+    return k_out, v_out
+
+
+def _prob_rows(name, t):
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} is [rows][vocab] with consecutive entries in a row")
+    rows, vocab = t.shape
+    stride = int(t.stride(0)) if rows > 1 else int(vocab)
+    return (t.data_ptr() if rows else None), stride, int(rows)
+
+
+def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, sample_uniform, query_start,
+                      draft_start, max_draft_len: int, context_lens=None, out_tokens=None, num_accepted=None,
+                      new_context_lens=None, flags: int = 0, stream=None):
+    """Verify drafted tokens: returns ``(out_tokens int32 [batch][max_draft_len + 1], num_accepted
+    int32 [batch], new_context_lens)``, the last None without ``context_lens``.
+
+    ``target_probs`` [rows][vocab] holds k + 1 rows per sequence (``query_start``), ``draft_probs`` k
+    (``draft_start``), float32 or bf16, rows any stride apart; ``draft_probs`` None means certain drafts."""
+    lib = load_library()
+    batch = int(sample_uniform.shape[0])
+    code = _dtype_code(target_probs.dtype)
+    tp, ts, tr = _prob_rows("target_probs", target_probs)
+    dp, ds, dr = None, 0, int(draft_tokens.shape[0])
+    if draft_probs is not None:
+        if draft_probs.dtype != target_probs.dtype or draft_probs.shape != (dr, target_probs.shape[1]):
+            raise ValueError("draft_probs is [draft rows][vocab] of target_probs's dtype, one row per draft token")
+        dp, ds, dr = _prob_rows("draft_probs", draft_probs)
+    _int32(draft_tokens=draft_tokens, query_start=query_start, draft_start=draft_start, context_lens=context_lens,
+           out_tokens=out_tokens, num_accepted=num_accepted, new_context_lens=new_context_lens)
+    if accept_uniform.dtype != torch.float32 or sample_uniform.dtype != torch.float32:
+        raise ValueError("the uniform numbers are float32")
+    if accept_uniform.shape != draft_tokens.shape or draft_tokens.dim() != 1 or sample_uniform.dim() != 1:
+        raise ValueError("draft_tokens and accept_uniform are [draft rows], sample_uniform [batch]")
+    if query_start.shape != (batch + 1,) or draft_start.shape != (batch + 1,):
+        raise ValueError("query_start and draft_start are [batch + 1]")
+    if max_draft_len < 0:
+        raise ValueError("max_draft_len is at least 0")
+    if context_lens is None and new_context_lens is not None:
+        raise ValueError("new_context_lens needs context_lens")
+    dev = target_probs.device
+    if out_tokens is None:
+        out_tokens = torch.empty((batch, max_draft_len + 1), dtype=torch.int32, device=dev)
+    if num_accepted is None:
+        num_accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
+    if context_lens is not None and new_context_lens is None:
+        new_context_lens = torch.empty((batch,), dtype=torch.int32, device=dev)
+    if out_tokens.shape != (batch, max_draft_len + 1):
+        raise ValueError("out_tokens is [batch][max_draft_len + 1]")
+    if any(t is not None and t.shape != (batch,) for t in (num_accepted, context_lens, new_context_lens)):
+        raise ValueError("num_accepted, context_lens and new_context_lens are [batch]")
+    _one_device(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
+                accept_uniform=accept_uniform, sample_uniform=sample_uniform, query_start=query_start,
+                draft_start=draft_start, context_lens=context_lens, out_tokens=out_tokens, num_accepted=num_accepted,
+                new_context_lens=new_context_lens)
+    _check("pkv_verify_drafts", lib.pkv_verify_drafts(
+        tp, ts, tr, dp, ds, dr, code, int(target_probs.shape[1]), _ptr(draft_tokens) if dr else None,
+        _ptr(accept_uniform) if dr else None, _ptr(sample_uniform), _ptr(query_start), _ptr(draft_start), batch,
+        int(max_draft_len), _ptr(context_lens), _ptr(new_context_lens), _ptr(out_tokens), _ptr(num_accepted), flags,
+        _stream(stream)))
+    return out_tokens, num_accepted, new_context_lens
 
 
 def pkv_decode_attention_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float, out=None,

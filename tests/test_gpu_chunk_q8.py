@@ -1,0 +1,371 @@
+"""pkv_multiquery_attention_q8 against the float64 oracle over the values the
+cached rows stand for.
+
+Tolerance, per element, with A = sum_p softmax_p |V_p| of its row and B the
+largest scale * |q||K_p| a row's scores can reach (Cauchy-Schwarz):
+  * the output's rounding to bf16: 2^-8 |ref| (half a step, eps / 2);
+  * three roundings to f16 (the weight, the V scale, code * scale): 3 * 2^-11 A;
+  * the score: D + 2 float32 operations on products that sum to at most B in
+    size, 2^-22 each (a truncating adder loses a whole step), a relative change
+    of the weight, counted twice (numerator and denominator): 2 (D + 2) 2^-22 B A;
+  * exp2 and the running sums: 2^-20 A and n 2^-23 A.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cases
+from oracle import attention as OA
+from oracle import multiquery as OM
+from oracle import quant as OQ
+from paged_kv_cache_209_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_209_gb300 import pkv as P
+    P.load_library()
+    P.pkv_device_status(clear=True)
+    return P
+
+
+def make(seed, lens, nqs, q_heads, kv_heads, d, kscale=1.0, vscale=1.0):
+    c = cases.multiquery_case(seed, lens, nqs, q_heads, kv_heads, d, torch.bfloat16)
+    c["kc"], c["ks"] = OQ.quantize_rows(OA.bf16_bits_to_f64(cases.host_view(c["k_pool"])) * kscale)
+    c["vc"], c["vs"] = OQ.quantize_rows(OA.bf16_bits_to_f64(cases.host_view(c["v_pool"])) * vscale)
+    c["scale"] = float(np.float32(c["scale"]))
+    return c
+
+
+def live_slots(c):
+    live = np.zeros((c["kc"].shape[0], 16), dtype=bool)
+    for i, n in enumerate(c["lens"]):
+        for t in range(int(n)):
+            live[c["tables"][i, t // 16], t % 16] = True
+    return live
+
+
+def poison(c):
+    """Slots no sequence holds: NaN K scales, infinite V scales."""
+    live = live_slots(c)
+    c["ks"].transpose(0, 2, 1)[~live] = np.nan
+    c["vs"].transpose(0, 2, 1)[~live] = np.inf
+    return c
+
+
+def device(c):
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    return dict(q=c["q"].cuda(), kc=dev(c["kc"]), vc=dev(c["vc"].transpose(0, 1, 3, 2)),
+                sc=dev(np.stack([c["ks"], c["vs"]], axis=2)), tables=dev(c["tables"]), lens=dev(c["lens"]),
+                start=dev(c["query_start"]))
+
+
+def call(pkv, c, d=None, **kw):
+    d = d or device(c)
+    most = kw.pop("most", max(1, int(np.diff(c["query_start"]).max())))
+    return pkv.pkv_multiquery_attention_q8(d["q"], d["kc"], d["vc"], d["sc"], d["tables"], d["lens"], d["start"],
+                                           c["scale"], most, **kw)
+
+
+def reference(c):
+    """(output, tolerance) in float64."""
+    with np.errstate(invalid="ignore"):
+        kd, vd = OQ.dequantize_rows(c["kc"], c["ks"]), OQ.dequantize_rows(c["vc"], c["vs"])
+    dead = ~live_slots(c)
+    kd.transpose(0, 2, 1, 3)[dead] = 0
+    vd.transpose(0, 2, 1, 3)[dead] = 0
+    qf = OA.bf16_bits_to_f64(cases.host_view(c["q"]))
+    attend = lambda v: OM.multiquery_attention(qf, kd, v, c["tables"], c["lens"], c["query_start"], c["scale"],  # noqa: E731
+                                               c["kv_heads"], "f64")
+    ref, size = attend(vd), attend(np.abs(vd))
+    d, n = qf.shape[2], int(max(c["lens"]))
+    b = abs(c["scale"]) * np.linalg.norm(qf, axis=-1).max(initial=0) * np.linalg.norm(kd, axis=-1).max(initial=0)
+    return ref, 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + n * 2.0 ** -23)
+
+
+def check(out, c, want=None):
+    ref, tol = want or reference(c)
+    got = out.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), (np.argwhere(bad)[:5], np.abs(got - ref)[bad][:5], tol[bad][:5])
+
+
+SHAPES = [
+    # several sequences: a whole prompt, an empty one, one query, chunks behind a cached prefix
+    ([40, 200, 0, 1, 129, 700], [40, 33, 0, 1, 0, 70], 32, 8, 128),
+    ([40, 200, 0, 1, 129, 700], [40, 33, 0, 1, 0, 70], 16, 2, 64),
+    # around the kernel's steps of 128 tokens and tiles of 128 and 256 rows
+    ([127, 128, 129, 255, 256, 257], [127, 128, 129, 64, 65, 63], 8, 2, 128),
+    ([127, 128, 129, 255, 256, 257], [127, 128, 129, 255, 256, 257], 2, 2, 64),
+    ([300, 310, 640], [256, 257, 255], 1, 1, 128),
+    # group sizes that do not divide a tile
+    ([500, 77, 260], [90, 77, 201], 24, 8, 128),
+    ([500, 77, 260], [90, 77, 201], 10, 2, 64),
+    ([333, 90], [33, 19], 7, 1, 128),
+    ([200, 50, 18], [9, 5, 1], 128, 1, 128),
+    ([150, 40], [3, 2], 1024, 2, 64),
+    # single tokens and short drafts at head_dim 64 (no other int8 attention takes them)
+    ([1, 16, 17, 300, 1000, 64], [1, 1, 1, 1, 1, 1], 32, 8, 64),
+    ([30, 16, 170, 300], [4, 3, 0, 2], 8, 8, 64),
+    # few rows on long contexts (the context is split), and the split kernel's own cases
+    ([5000, 3000], [9, 12], 32, 8, 128),
+    ([4500], [70], 8, 8, 128),
+    ([700, 40, 129, 9], [8, 3, 0, 5], 32, 8, 128),
+]
+
+
+@pytest.mark.parametrize("lens,nqs,hq,hkv,d", SHAPES)
+def test_matches_oracle(pkv, lens, nqs, hq, hkv, d):
+    c = poison(make(sum(lens) + hq + d, lens, nqs, hq, hkv, d))
+    check(call(pkv, c), c)
+    assert pkv.pkv_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_attention_scales(pkv, d, scale):
+    c = make(3, [300, 65], [60, 65], 8, 2, d)
+    c["scale"] = scale
+    check(call(pkv, c), c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kscale,vscale", [(1e-3, 1e-3), (1.0, 1e-6), (8.0, 1e3), (1e-4, 1e8)])
+def test_value_ranges(pkv, d, kscale, vscale):
+    c = make(5, [400, 130], [70, 130], 8, 2, d, kscale, vscale)
+    check(call(pkv, c), c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("factor", [1e2, 1e5, 1e20])
+def test_v_rows_far_larger_than_the_others(pkv, d, factor):
+    """A fifth of the V rows larger by a factor that leaves f16, first seen at the
+    beginning of a context, in its middle or only at its end."""
+    c = make(6, [600, 500, 700, 90], [60, 90, 40, 90], 8, 2, d)
+    rng = np.random.default_rng(9)
+    for i, (a, b) in enumerate([(0, 600), (300, 500), (690, 700), (0, 90)]):
+        for t in range(a, b):
+            if rng.random() < 0.2 or t == b - 1:
+                c["vs"][c["tables"][i, t // 16], :, t % 16] *= np.float32(factor)
+    check(call(pkv, c), c)
+
+
+def test_zero_rows_and_wide_scales(pkv):
+    """Zero rows have scale 1; other rows' scales span four orders of magnitude."""
+    c = make(7, [300, 200], [80, 200], 8, 2, 128)
+    rng = np.random.default_rng(8)
+    c["ks"] = (c["ks"] * rng.uniform(1e-3, 3, c["ks"].shape)).astype(np.float32)
+    c["vs"] = (c["vs"] * rng.uniform(1e-2, 1e2, c["vs"].shape)).astype(np.float32)
+    for pool, scales in ((c["kc"], c["ks"]), (c["vc"], c["vs"])):
+        zero = rng.random(scales.shape) < 0.1
+        pool[zero] = 0
+        scales[zero] = 1.0
+    check(call(pkv, c), c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_scores(pkv, d):
+    """Peaked rows: scores in the hundreds, later tokens far above earlier ones."""
+    c = make(8, [500, 260], [50, 260], 8, 2, d)
+    ramp = np.linspace(0.5, 30, 500)
+    for i, n in enumerate(c["lens"]):
+        for t in range(int(n)):
+            c["ks"][c["tables"][i, t // 16], :, t % 16] *= np.float32(ramp[t])
+    check(call(pkv, c), c)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tokens_a_row_may_not_see_hold_anything(pkv, d):
+    """The chunk's last token has an infinite V scale and a NaN K scale: the rows
+    before it are right (its own row is not a number)."""
+    c = make(9, [140, 300], [140, 40], 8, 2, d)
+    want = reference(c)
+    for i, n in enumerate(c["lens"]):
+        b, s = c["tables"][i, (n - 1) // 16], (n - 1) % 16
+        c["ks"][b, :, s], c["vs"][b, :, s] = np.nan, np.inf
+    out = call(pkv, c)
+    keep = [r for r in range(180) if r not in (139, 179)]
+    check(out[keep], c, (want[0][keep], want[1][keep]))
+    assert bool(torch.isnan(out[[139, 179]].float()).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_outside_the_pool_are_absent(pkv, d):
+    """A bad block's tokens have no weight, the call reports it; a sequence whose
+    every block is bad gives zero rows."""
+    c = make(10, [300, 200, 60], [70, 50, 40], 8, 2, d)
+    nb = c["kc"].shape[0]
+    good = dict(c, tables=c["tables"].copy())
+    c["tables"][0, 3], c["tables"][1, 12], c["tables"][2, :4] = nb, -1, 2 ** 31 - 1
+    out = call(pkv, c)
+    assert pkv.pkv_device_status(clear=True) == pkv.PKV_DEVERR_RANGE
+    ref, tol = np.zeros((160, 8, d)), np.zeros((160, 8, d))
+    for i, bad in ((0, 3), (1, 12)):
+        # the same rows with the bad block's tokens cut out of the context
+        n, nq, q0 = int(c["lens"][i]), int(np.diff(c["query_start"])[i]), int(c["query_start"][i])
+        for t in range(nq):
+            seen = [p for p in range(n - nq + t + 1) if p // 16 != bad]
+            blocks = good["tables"][i, np.array(seen) // 16]
+            slots = np.array(seen) % 16
+            k = c["kc"][blocks, :, slots].astype(np.float64) * c["ks"][blocks, :, slots][..., None]
+            v = c["vc"][blocks, :, slots].astype(np.float64) * c["vs"][blocks, :, slots][..., None]
+            q = OA.bf16_bits_to_f64(cases.host_view(c["q"]))[q0 + t]
+            for h in range(8):
+                x = c["scale"] * k[:, h // 4] @ q[h]
+                w = np.exp(x - x.max())
+                w /= w.sum()
+                ref[q0 + t, h], size = w @ v[:, h // 4], w @ np.abs(v[:, h // 4])
+                b = c["scale"] * np.linalg.norm(q[h]) * np.linalg.norm(k[:, h // 4], axis=1).max()
+                tol[q0 + t, h] = 2.0 ** -8 * np.abs(ref[q0 + t, h]) + size * (
+                    3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + 300 * 2.0 ** -23)
+    check(out, c, (ref, tol))
+    assert bool((out[120:] == 0).all())
+    buf = torch.full_like(out, 5.0)
+    with pytest.raises(pkv.PkvError) as e:
+        call(pkv, c, out=buf, flags=pkv.PKV_FLAG_CHECKED)
+    assert e.value.name == "PKV_ERR_RANGE" and bool((buf == 5.0).all())
+    assert pkv.pkv_device_status(clear=True) == 0
+
+
+def test_malformed_query_ranges(pkv):
+    """More queries than tokens or than max_query_len, a negative range, a context
+    past its table: no rows for that sequence, the others right."""
+    c = make(11, [90, 60, 200], [40, 60, 50], 8, 2, 128)
+    ref, tol = reference(c)
+    rows = [slice(0, 40), slice(40, 100), slice(100, 150)]
+    for change in ("tokens", "most", "past"):
+        b = dict(c, lens=c["lens"].copy())
+        kw = {}
+        if change == "tokens":
+            b["lens"][1] = 59
+        if change == "past":
+            b["lens"][1] = 16 * c["tables"].shape[1] + 1
+        if change == "most":
+            kw["most"] = 59
+        buf = torch.full((150, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        call(pkv, b, out=buf, **kw)
+        assert pkv.pkv_device_status(clear=True) == pkv.PKV_DEVERR_RANGE
+        assert bool((buf[rows[1]] == 5.0).all())
+        for r in (rows[0], rows[2]):
+            check(buf[r], c, (ref[r], tol[r]))
+        buf.fill_(5.0)
+        with pytest.raises(pkv.PkvError) as e:
+            call(pkv, b, out=buf, flags=pkv.PKV_FLAG_CHECKED, **kw)
+        assert e.value.name == "PKV_ERR_RANGE" and bool((buf == 5.0).all())
+    b = dict(c, query_start=np.array([0, 40, 20, 70], dtype=np.int32))
+    call(pkv, b, most=60)
+    assert pkv.pkv_device_status(clear=True) == pkv.PKV_DEVERR_RANGE
+
+
+def test_rows_no_sequence_names_stay(pkv):
+    """Rows before the first and behind the last sequence keep their bytes; a
+    checked call is right."""
+    c = make(12, [90, 200], [40, 51], 8, 2, 128)
+    ref, tol = reference(c)
+    d = device(c)
+    d["q"] = torch.cat([d["q"][:7], d["q"], d["q"][:9]])
+    d["start"] = d["start"] + 7
+    buf = torch.full_like(d["q"], 5.0)
+    call(pkv, c, d, out=buf, flags=pkv.PKV_FLAG_CHECKED)
+    assert bool((buf[:7] == 5.0).all()) and bool((buf[98:] == 5.0).all())
+    check(buf[7:98], c, (ref, tol))
+
+
+def test_batch_above_one_launch(pkv):
+    rng = np.random.default_rng(13)
+    lens = rng.integers(0, 60, 1100)
+    nqs = np.minimum(lens, rng.integers(0, 40, 1100))
+    lens[1050], nqs[1050] = 900, 100
+    c = make(13, lens, nqs, 2, 1, 64)
+    check(call(pkv, c), c)
+
+
+def test_one_workspace_many_calls(pkv):
+    """One workspace, never cleared again, over calls of other shapes."""
+    first = make(14, [3000, 1500], [40, 70], 8, 2, 128)
+    second = make(15, [200, 1000, 64], [150, 20, 64], 8, 2, 128)
+    need = max(pkv.pkv_multiquery_q8_workspace_size(len(c["lens"]), 8, c["tables"].shape[1], 150, device(c)["kc"])
+               for c in (first, second))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    wants = {id(c): reference(c) for c in (first, second)}
+    for c in (first, second, first, second, second):
+        check(call(pkv, c, workspace=ws), c, wants[id(c)])
+    with pytest.raises(pkv.PkvError) as e:
+        call(pkv, first, workspace=ws[:128])
+    assert e.value.name == "PKV_ERR_WORKSPACE"
+
+
+def test_same_call_same_bytes(pkv):
+    c = make(16, [2500, 900, 10], [60, 300, 10], 24, 8, 128)
+    d = device(c)
+    a = call(pkv, c, d)
+    for _ in range(3):
+        assert torch.equal(call(pkv, c, d).view(torch.int16), a.view(torch.int16))
+
+
+def test_captured_and_replayed_and_two_streams(pkv):
+    """A captured call replayed on other lengths and offsets; two calls at once on
+    two streams, each on its own workspace."""
+    a, b = make(17, [400, 300], [50, 64], 8, 2, 128), make(18, [399, 290], [64, 50], 8, 2, 128)
+    d, wa, wb = device(a), reference(a), reference(b)
+    ws = torch.zeros(pkv.pkv_multiquery_q8_workspace_size(2, 8, a["tables"].shape[1], 64, d["kc"]), dtype=torch.uint8,
+                     device="cuda")
+    call(pkv, a, d, most=64, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(pkv, a, d, most=64, workspace=ws)
+    for c, want in ((b, wb), (a, wa), (b, wb)):
+        for key, v in device(c).items():
+            d[key].copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(out, c, want)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    da, db = device(a), device(b)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        for s, c, dd in ((streams[0], a, da), (streams[1], b, db)):
+            with torch.cuda.stream(s):
+                outs.append(call(pkv, c, dd))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        check(o, a if i % 2 == 0 else b, wa if i % 2 == 0 else wb)
+
+
+def test_prefill512_layer_sampled(pkv):
+    """The chunked-prefill workload over an int8 cache, every row of sampled heads
+    and queries (float64 on the device)."""
+    cfg = W.CONFIGS["prefill512"]
+    tables, lens, nb = W.workload_index("prefill512")
+    g = torch.Generator(device="cuda").manual_seed(19)
+    codes = lambda shape, s: W.int8_codes(shape, s, "cuda")  # noqa: E731
+    kc, vc = codes((nb, 8, 16, 128), 1), codes((nb, 8, 128, 16), 2)
+    sc = torch.rand((nb, 8, 2, 16), generator=g, device="cuda") * 0.01 + 0.02
+    q = torch.randn((8 * 512, 32, 128), generator=g, device="cuda").to(torch.bfloat16)
+    start = torch.arange(0, 8 * 512 + 1, 512, dtype=torch.int32, device="cuda")
+    t = torch.from_numpy(tables).cuda()
+    scale = 1 / math.sqrt(128)
+    out = pkv.pkv_multiquery_attention_q8(q, kc, vc, sc, t, torch.from_numpy(lens.astype(np.int32)).cuda(), start,
+                                          scale, cfg["queries"])
+    for i, h in ((0, 0), (3, 13), (7, 31)):
+        blk = t[i].long()
+        k = (kc[blk, h // 4].double() * sc[blk, h // 4, 0, :, None].double()).reshape(-1, 128)
+        v = (vc[blk, h // 4].double() * sc[blk, h // 4, 1, None].double()).transpose(1, 2).reshape(-1, 128)
+        qq = q[512 * i:512 * (i + 1), h].double()
+        x = scale * qq @ k.T
+        x = x.masked_fill(torch.arange(8192, device="cuda") > torch.arange(7680, 8192, device="cuda")[:, None], -math.inf)
+        w = torch.softmax(x, -1)
+        ref, size = w @ v, w @ v.abs()
+        b = scale * float(qq.norm(dim=1).max() * k.norm(dim=1).max())
+        tol = 2.0 ** -8 * ref.abs() + size * (3 * 2.0 ** -11 + 260 * 2.0 ** -22 * b + 2.0 ** -20 + 8192 * 2.0 ** -23)
+        assert bool(((out[512 * i:512 * (i + 1), h].double() - ref).abs() <= tol).all())
+    assert pkv.pkv_device_status(clear=True) == 0
