@@ -716,7 +716,7 @@ size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int3
     const int G = num_q_heads / desc->num_kv_heads;
     if (split_kernel_takes(desc, max_query_len, G))
         return pkv_decode_q8_workspace_size(batch, num_q_heads, max_blocks_per_seq, max_query_len, desc, nullptr);
-    return chunk_q8_workspace_bytes(batch, desc->num_kv_heads, desc->head_dim);
+    return chunk_q8_workspace_bytes(desc->head_dim);
 }
 
 pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
@@ -745,7 +745,7 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
         return pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens,
                                        query_start, batch, num_q_heads, max_query_len, scale, out, workspace,
                                        workspace_bytes, desc, flags, nullptr, stream);
-    if (workspace_bytes < chunk_q8_workspace_bytes(batch, desc->num_kv_heads, desc->head_dim))
+    if (workspace_bytes < chunk_q8_workspace_bytes(desc->head_dim))
         return PKV_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned int* status = device_info().status;

@@ -1,0 +1,176 @@
+// Work split of the int8 chunk attention (pkv_chunk_q8.cu).
+//
+// A unit is a tile of 256 query rows of one (sequence, KV head): rows
+// r = t G + g, query t and query head g of the KV head's group of G. It takes
+// ns steps of 128 tokens, up to the last token its last row sees. Units are
+// ordered sequence-major, then head, then tile; a launch gives CTA c of C the
+// steps between the cuts c and c + 1, placed by cost, so every CTA works about
+// equally long whatever the mix of contexts, chunks and causal limits. A cut
+// inside a unit leaves pieces that a second kernel combines.
+//
+// Cost of tile t of a sequence with n tokens, nq of them new: about the tokens
+// it sees plus a start-up worth kOverTokens, in units of 64 / G tokens, linear in
+// t so that a position is found by bisection over closed forms:
+//     w (a + 4 t),   a = ceil(((n - nq + kOverTokens) G + 256) / 64),
+// w = 2, or 1 for a last tile of at most 128 rows (one row half instead of two).
+// The cost only places cuts; a unit's steps are counted exactly.
+//
+// Plain integer arithmetic, compiled for the host as well, where a test checks
+// it against brute force.
+#pragma once
+
+#include <stdint.h>
+
+#ifndef PKV_HD
+#define PKV_HD __host__ __device__
+#endif
+
+namespace pkv {
+namespace {
+
+constexpr int kChunkRows = 256;   // query rows of a unit
+constexpr int kChunkStep = 128;   // tokens of a step
+constexpr int kOverTokens = 192;  // start-up of a unit (Q, the pipeline's fill, the output) in tokens
+constexpr int kMinPiece = 2;      // a cut leaves at least this many steps on either side
+constexpr int kMinSteps = 3;      // a CTA gets at least about this many two-half steps' cost
+
+struct ChunkShape {
+    const int32_t* lens;
+    const int32_t* qstart;
+    int batch, kv_heads, group, max_blocks, max_query_len;
+};
+
+struct ChunkSeq {
+    int n, nq, q0;  // tokens, new tokens, first query row
+};
+
+// A position between steps: step s of a unit (seq == batch: past the end).
+struct ChunkPos {
+    int seq, head, tile, s;
+    PKV_HD bool same_unit(const ChunkPos& o) const { return seq == o.seq && head == o.head && tile == o.tile; }
+    PKV_HD bool operator==(const ChunkPos& o) const { return same_unit(o) && s == o.s; }
+};
+
+// Reads sequence i; false (and no queries) when its lengths are malformed.
+PKV_HD inline bool chunk_seq(const ChunkShape& a, int i, ChunkSeq& q) {
+    q.n = a.lens[i];
+    q.q0 = a.qstart[i];
+    const int64_t nq = static_cast<int64_t>(a.qstart[i + 1]) - q.q0;
+    const bool ok = q.n >= 0 && q.n <= a.max_blocks * 16 && q.q0 >= 0 && nq >= 0 && nq <= q.n && nq <= a.max_query_len;
+    q.nq = ok ? static_cast<int>(nq) : 0;
+    return ok;
+}
+
+PKV_HD inline int chunk_tiles(const ChunkSeq& q, int group) { return (q.nq * group + kChunkRows - 1) / kChunkRows; }
+
+// Steps of tile t.
+PKV_HD inline int chunk_steps(const ChunkSeq& q, int group, int t) {
+    const int rows = q.nq * group;
+    const int end = (t + 1) * kChunkRows < rows ? (t + 1) * kChunkRows : rows;
+    return (q.n - q.nq + (end - 1) / group + 1 + kChunkStep - 1) / kChunkStep;
+}
+
+PKV_HD inline int64_t chunk_cost_base(const ChunkSeq& q, int group) {
+    return (static_cast<int64_t>(q.n - q.nq + kOverTokens) * group + kChunkRows + 63) / 64;
+}
+// Cost of the tiles before t (t < tiles), of tile t, and of all tiles of a head.
+PKV_HD inline int64_t chunk_cost_before(int64_t base, int64_t t) { return 2 * t * base + 4 * t * (t - 1); }
+PKV_HD inline int64_t chunk_tile_cost(const ChunkSeq& q, int group, int64_t base, int t, int tiles) {
+    const int w = t == tiles - 1 && q.nq * group - t * kChunkRows <= kChunkRows / 2 ? 1 : 2;
+    return w * (base + 4 * static_cast<int64_t>(t));
+}
+PKV_HD inline int64_t chunk_head_cost(const ChunkSeq& q, int group) {
+    const int tiles = chunk_tiles(q, group);
+    if (tiles == 0) return 0;
+    const int64_t base = chunk_cost_base(q, group);
+    return chunk_cost_before(base, tiles - 1) + chunk_tile_cost(q, group, base, tiles - 1, tiles);
+}
+
+// The next unit after `p` (prefix: cost before each sequence, [batch + 1]).
+PKV_HD inline ChunkPos chunk_next_unit(const ChunkShape& a, const int64_t* prefix, ChunkPos p, int tiles) {
+    p.s = 0;
+    if (++p.tile < tiles) return p;
+    p.tile = 0;
+    if (++p.head < a.kv_heads) return p;
+    p.head = 0;
+    do ++p.seq;
+    while (p.seq < a.batch && prefix[p.seq + 1] == prefix[p.seq]);
+    return p;
+}
+
+// The position at cost x.
+PKV_HD inline ChunkPos chunk_locate(const ChunkShape& a, const int64_t* prefix, int64_t x) {
+    ChunkPos p{a.batch, 0, 0, 0};
+    if (x >= prefix[a.batch]) return p;
+    int lo = 0, hi = a.batch - 1;  // the last sequence whose cost begins at or before x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    p.seq = lo;
+    ChunkSeq q;
+    chunk_seq(a, lo, q);
+    const int64_t head_cost = chunk_head_cost(q, a.group);
+    int64_t rem = x - prefix[lo];
+    p.head = static_cast<int>(rem / head_cost);
+    rem -= p.head * head_cost;
+    const int tiles = chunk_tiles(q, a.group);
+    const int64_t base = chunk_cost_base(q, a.group);
+    lo = 0, hi = tiles - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (chunk_cost_before(base, mid) <= rem)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    p.tile = lo;
+    rem -= chunk_cost_before(base, lo);
+    const int ns = chunk_steps(q, a.group, lo);
+    p.s = static_cast<int>(rem * ns / chunk_tile_cost(q, a.group, base, lo, tiles));
+    if (p.s < kMinPiece)
+        p.s = 0;
+    else if (ns - p.s < kMinPiece)
+        p = chunk_next_unit(a, prefix, p, tiles);
+    return p;
+}
+
+// CTAs (of `grid`) that get work, and the cut before CTA c of them.
+PKV_HD inline int chunk_ctas(int64_t total, int group, int grid) {
+    const int64_t most = total / (static_cast<int64_t>(kMinSteps) * 2 * kChunkStep * group / 64);
+    return most >= grid ? grid : (most < 1 ? 1 : static_cast<int>(most));
+}
+PKV_HD inline ChunkPos chunk_cut(const ChunkShape& a, const int64_t* prefix, int c, int ctas) {
+    const int64_t total = prefix[a.batch];
+    if (c >= ctas) return ChunkPos{a.batch, 0, 0, 0};
+    return chunk_locate(a, prefix, total / ctas * c + total % ctas * c / ctas);
+}
+
+// Walks the segments (unit, steps s0 .. s1 - 1) between two cuts.
+struct ChunkSegment {
+    ChunkPos at;  // unit; at.s is the first step
+    int s1, ns;   // one past the last step; the unit's steps
+    int tiles;
+    ChunkSeq q;
+    PKV_HD bool whole() const { return at.s == 0 && s1 == ns; }
+};
+PKV_HD inline bool chunk_segment(const ChunkShape& a, const ChunkPos& cur, const ChunkPos& end, ChunkSegment& g) {
+    if (cur == end || cur.seq >= a.batch) return false;
+    g.at = cur;
+    chunk_seq(a, cur.seq, g.q);
+    g.tiles = chunk_tiles(g.q, a.group);
+    g.ns = chunk_steps(g.q, a.group, cur.tile);
+    g.s1 = cur.same_unit(end) ? end.s : g.ns;
+    return true;
+}
+// The position after segment g.
+PKV_HD inline ChunkPos chunk_after(const ChunkShape& a, const int64_t* prefix, const ChunkSegment& g) {
+    if (g.s1 < g.ns) return ChunkPos{g.at.seq, g.at.head, g.at.tile, g.s1};
+    return chunk_next_unit(a, prefix, g.at, g.tiles);
+}
+
+}  // namespace
+}  // namespace pkv

@@ -246,7 +246,7 @@ struct ChunkArgs {
     int32_t max_query_len;
     float scale;
 };
-size_t chunk_q8_workspace_bytes(int batch, int kv_heads, int head_dim);
+size_t chunk_q8_workspace_bytes(int head_dim);
 cudaError_t launch_chunk_q8(const ChunkArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------- reading the cache back

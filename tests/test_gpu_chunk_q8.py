@@ -8,7 +8,14 @@ largest scale * |q||K_p| a row's scores can reach (Cauchy-Schwarz):
   * the score: D + 2 float32 operations on products that sum to at most B in
     size, 2^-22 each (a truncating adder loses a whole step), a relative change
     of the weight, counted twice (numerator and denominator): 2 (D + 2) 2^-22 B A;
-  * exp2 and the running sums: 2^-20 A and n 2^-23 A.
+  * exp2 and the running sums: 2^-20 A and n 2^-23 A;
+  * f16's smallest step, 2^-24, half of which a weight below the normal range may
+    lose: the largest weight of a row is at least 1 (the maximum that is
+    subtracted is never above it) and the sum with it, so the n seen tokens lose
+    at most n 2^-25 max|V_p[d]| together;
+  * the same for a scaled V value, 2^-25 2^E: a step keeps the scaled values only
+    if its V scales are at least 2^(E - 14), so that is at most 2^-11 vs_p, in
+    the weighted mean 2^-11 sum_p softmax_p vs_p.
 """
 
 import math
@@ -87,7 +94,17 @@ def reference(c):
     ref, size = attend(vd), attend(np.abs(vd))
     d, n = qf.shape[2], int(max(c["lens"]))
     b = abs(c["scale"]) * np.linalg.norm(qf, axis=-1).max(initial=0) * np.linalg.norm(kd, axis=-1).max(initial=0)
-    return ref, 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + n * 2.0 ** -23)
+    tol = 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + n * 2.0 ** -23)
+    scales = np.where(dead.reshape(-1, 1, 16), 0.0, np.abs(c["vs"].astype(np.float64)))
+    tol += 2.0 ** -11 * attend(np.broadcast_to(scales[..., None], vd.shape))
+    group = qf.shape[1] // c["kv_heads"]
+    for i, n in enumerate(c["lens"]):                          # the largest |V| among the tokens each row sees
+        q0, q1 = c["query_start"][i], c["query_start"][i + 1]
+        pos = np.arange(int(n))
+        rows = np.abs(vd[c["tables"][i, pos // 16], :, pos % 16])
+        top = np.maximum.accumulate(rows, axis=0)[int(n) - (q1 - q0):] if n else rows
+        tol[q0:q1] += n * 2.0 ** -25 * np.repeat(top, group, axis=1)
+    return ref, tol
 
 
 def check(out, c, want=None):
@@ -226,6 +243,7 @@ def test_blocks_outside_the_pool_are_absent(pkv, d):
                 b = c["scale"] * np.linalg.norm(q[h]) * np.linalg.norm(k[:, h // 4], axis=1).max()
                 tol[q0 + t, h] = 2.0 ** -8 * np.abs(ref[q0 + t, h]) + size * (
                     3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + 300 * 2.0 ** -23)
+                tol[q0 + t, h] += 300 * 2.0 ** -25 * np.abs(v[:, h // 4]).max() + 2.0 ** -11 * float(c["vs"].max())
     check(out, c, (ref, tol))
     assert bool((out[120:] == 0).all())
     buf = torch.full_like(out, 5.0)
@@ -367,5 +385,6 @@ def test_prefill512_layer_sampled(pkv):
         ref, size = w @ v, w @ v.abs()
         b = scale * float(qq.norm(dim=1).max() * k.norm(dim=1).max())
         tol = 2.0 ** -8 * ref.abs() + size * (3 * 2.0 ** -11 + 260 * 2.0 ** -22 * b + 2.0 ** -20 + 8192 * 2.0 ** -23)
+        tol = tol + 8192 * 2.0 ** -25 * v.abs().max() + 2.0 ** -11 * 0.03
         assert bool(((out[512 * i:512 * (i + 1), h].double() - ref).abs() <= tol).all())
     assert pkv.pkv_device_status(clear=True) == 0
