@@ -22,13 +22,14 @@
 // two row halves A and B of 128. A unit cut by a range leaves fp32 pieces
 // (O, m, l) in the workspace, which combine_kernel joins.
 //
-// Roles (16 warps). Warps 0-3 and 4-7: the softmax of halves A and B, one thread
-// per query row. Warps 8-11: converters; they load the codes of the next step
-// from global memory into registers, turn the previous loads into bf16 (K) and
-// scaled f16 (V) in the 128-byte-swizzled layout the tensor cores read, and
-// write the step's factors c_p. Warps 12-13: one thread each issues S = Q K^T of
-// A and of B; warps 14-15: O += P V of A and of B, in two parts of 64 tokens.
-// While the softmax of one half runs, the tensor cores work on the other.
+// Roles (20 warps). Warps 0-3 and 4-7: the softmax of halves A and B, one thread
+// per query row. Warps 8-11 and 12-15: the converters of K and of V; they load
+// the codes of the next step from global memory into registers while they turn
+// the previous loads into bf16 (K) or scaled f16 (V), in the 128-byte-swizzled
+// layout the tensor cores read; K's also write the step's factors c_p. Warps 16
+// and 17: one thread each issues S = Q K^T of A and of B; warps 18 and 19: O += P V
+// of A and of B, in two parts of 64 tokens. While the softmax of one half runs,
+// the tensor cores work on the other.
 //
 // Tensor memory (512 columns): S of A and B (128 fp32 columns each; P is written
 // over its first 64), O of A and B. Shared memory: Q 64 KB, two stages of K and
@@ -47,19 +48,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The factor c of an absent token (a block id outside the pool): a NaN that no
 // arithmetic produces.
 constexpr uint32_t kAbsent = 0x7fc0dead;
-constexpr int kAbsentFlag = 1;  // the step holds absent tokens
-constexpr int kWideFlag = 2;    // V scales move into the weights
 
 __device__ __forceinline__ float ninf() { return __int_as_float(0xff800000); }
 
 template <int D>
 struct Cx {
     static constexpr int kSoftmaxWarps = 8;
-    static constexpr int kConvertWarp = 8;  // 8 .. 11
-    static constexpr int kScoreWarp = 12;   // 12, 13
-    static constexpr int kValueWarp = 14;   // 14, 15
-    static constexpr int kThreads = 512;
-    static constexpr int kConverters = 128;
+    static constexpr int kConvertWarp = 8;  // K: 8 .. 11, V: 12 .. 15
+    static constexpr int kScoreWarp = 16;   // 16, 17
+    static constexpr int kValueWarp = 18;   // 18, 19
+    static constexpr int kThreads = 640;
+    static constexpr int kConverters = 128;  // threads that convert K, and V
     static constexpr int kStages = 2;     // K stages, and V stages
     static constexpr int kTables = 4;     // factor tables in flight
     static constexpr int kHalves = D / 64;                    // 128-byte column parts of a K or Q row
@@ -71,18 +70,19 @@ struct Cx {
     static constexpr int kOffK = kOffQ + 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffTable = kOffV + kStages * kVBytes;
-    // a table: c [128], log2(vs) - E [128] (wide steps), then 2^E and the flags
+    // a table: c [128], log2(vs) - E [128] (0 unless the step is wide; written for
+    // wide steps and for those with absent tokens), then 2^E and 1 for such a step
     static constexpr int kTableBytes = 2 * 128 * 4 + 16;
-    static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [128]
-    static constexpr int kOffReduce = kOffScale + 256;                   // [2][4 warps] of 16 bytes
-    static constexpr int kOffBars = kOffReduce + 128;
+    static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [2][128]
+    static constexpr int kOffReduce = kOffScale + 512;                   // K, V: [2][4 warps] of 16 bytes
+    static constexpr int kOffBars = kOffReduce + 256;
     // k_full, k_empty, v_full, v_empty per stage; q_full, s_full per half;
     // p_full, pv_done per half and token part; final per issuer
     static constexpr int kNumBars = 4 * kStages + 2 * 2 + 2 * 4 + 4;
     static constexpr int kOffPrefix = kOffBars + kNumBars * 8;
     static constexpr int kOffPlan = kOffPrefix + (kMaxBatchPerLaunch + 1) * 8;
-    static constexpr int kOffMisc = kOffPlan + 2 * 16;
-    static constexpr size_t kSmem = 1024 + kOffMisc + 16 * 8 + 16;
+    static constexpr int kOffMisc = kOffPlan + (2 + kThreads / 32) * 16;
+    static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
     static constexpr uint32_t kColS = 0;    // S of half x: 128 x
     static constexpr uint32_t kColO = 256;  // O of half x: 256 + 128 x
     static constexpr uint32_t kTmemCols = 512;
@@ -108,7 +108,7 @@ __device__ __forceinline__ ChunkShape shape_of(const ChunkArgs& a) {
     return ChunkShape{a.lens, a.qstart, a.batch, a.kv_heads, a.group, a.max_blocks, a.max_query_len};
 }
 
-// Cost before each sequence (all 512 threads; ends with __syncthreads).
+// Cost before each sequence (all threads, two sequences each; ends with __syncthreads).
 __device__ void sum_costs(const ChunkArgs& a, const ChunkShape& sh, int64_t* prefix, int64_t* warp_sum) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t mine[2], sum = 0;
@@ -136,7 +136,6 @@ __device__ void sum_costs(const ChunkArgs& a, const ChunkShape& sh, int64_t* pre
     for (int w = 0; w < warp; ++w) at += warp_sum[w];
     if (2 * threadIdx.x <= a.batch) prefix[2 * threadIdx.x] = at;
     if (2 * threadIdx.x + 1 <= a.batch) prefix[2 * threadIdx.x + 1] = at + mine[0];
-    if (threadIdx.x == 511 && a.batch == kMaxBatchPerLaunch) prefix[kMaxBatchPerLaunch] = at + sum;
     __syncthreads();
 }
 
@@ -194,28 +193,192 @@ __device__ __forceinline__ bool named_barrier_all(int id, int threads, bool ok) 
     return r != 0;
 }
 
-// ---------------------------------------------------------------- the steps a converter walks
-// One step of a segment, as the converters load it.
-struct Step {
-    ChunkPos cur;     // position after the segment
-    ChunkSegment g;
-    int step;         // step within the unit
-    bool live;
-};
-__device__ __forceinline__ void step_open(const ChunkShape& sh, const int64_t* prefix, const ChunkPos& end, Step& s) {
-    s.live = chunk_segment(sh, s.cur, end, s.g);
-    if (s.live) {
-        s.step = s.g.at.s;
-        s.cur = chunk_after(sh, prefix, s.g);
-    }
+// Eight scores of a step that is not plain, scaled, -inf where the token is absent or not
+// seen (columns taddr .. taddr + 7, factors c, the first `seen` of them seen).
+__device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, int seen, float (&x)[8]) {
+    uint32_t v[8];
+    tmem_ld8(taddr, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e];
 }
-__device__ __forceinline__ void step_next(const ChunkShape& sh, const int64_t* prefix, const ChunkPos& end, Step& s) {
-    if (++s.step >= s.g.s1) step_open(sh, prefix, end, s);
-}
-
 // mbar_wait by a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort));
+}
+
+// ---------------------------------------------------------------- converters
+// K's (IsV false) or V's four warps: every step of the CTA's range, one load
+// ahead. The V scales' range decides a step's mode and a segment's exponent; both
+// groups read the scales and decide alike.
+template <int D, bool IsV>
+__device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* smem, const int64_t* prefix,
+                             const ChunkPos* plan, ChunkPos* after, uint64_t* full, uint64_t* empty,
+                             volatile int* abort_flag) {
+    using C = Cx<D>;
+    const int lane = threadIdx.x & 31;
+    const int cw = (threadIdx.x >> 5) & 3;
+    const int tid = cw * 32 + lane;
+    constexpr int kVecs = 128 * D / 16 / C::kConverters;  // 16-code vectors per thread and step
+    constexpr int kBlockVecs = D;                         // vectors of one (block, head)
+    constexpr int kBarrier = IsV ? 2 : 1;
+    const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes);
+    uint32_t (*reduce)[4][4] = reinterpret_cast<uint32_t (*)[4][4]>(smem + C::kOffReduce + (IsV ? 128 : 0));
+    const float cscale = a.scale * kLog2e;
+
+    // the segment being loaded (the position after it: in shared memory, one per warp, read once per segment)
+    if (lane == 0) *after = plan[0];
+    __syncwarp();
+    int step = 0, last = 0;            // next step to load, one past the segment's last
+    int n = 0, head = 0;               // its tokens, KV head
+    const int32_t* trow = nullptr;     // its block table
+    int ids = 0, ids_next = 0;         // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
+    bool opens = false;                // the loaded step is its segment's first
+    auto id_at = [&](int b) {
+        if (b >= (n + 15) / 16) return -1;
+        const int id = __ldg(trow + b);
+        if (id >= 0 && id < a.num_blocks) return id;
+        if (!IsV) atomicOr(a.status, PKV_DEVERR_RANGE);
+        return -2;
+    };
+    auto open = [&]() {
+        ChunkSegment g;
+        const ChunkPos cur = *after;
+        __syncwarp();
+        if (!chunk_segment(sh, cur, plan[1], g)) return false;
+        if (lane == 0) *after = chunk_after(sh, prefix, g);
+        __syncwarp();
+        step = g.at.s;
+        last = g.s1;
+        n = g.q.n;
+        head = g.at.head;
+        trow = a.tables + static_cast<int64_t>(g.at.seq) * a.max_blocks;
+        ids = id_at(32 * (step >> 2) + lane);
+        ids_next = id_at(32 * (step >> 2) + 32 + lane);
+        opens = true;
+        return true;
+    };
+    // the loaded step: codes, scales of token `tid`, whether it exists or lies in a block outside the pool
+    uint4 w[kVecs];
+    float ks = 0.f, vs = 0.f;
+    bool present = false, missing = false;
+    auto load = [&]() {
+        const int b0 = (step & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int v = tid + i * C::kConverters;
+            // an absent block's codes may be any (its tokens carry no weight): block 0 exists
+            const int id = max(0, __shfl_sync(0xffffffffu, ids, b0 + v / kBlockVecs));
+            w[i] = __ldg(codes + (static_cast<int64_t>(id) * a.kv_heads + head) * kBlockVecs + v % kBlockVecs);
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, b0 + (tid >> 4));
+        present = id >= 0 && step * kChunkStep + tid < n;
+        missing = id == -2;
+        const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (tid & 15);
+        if (!IsV) ks = __ldg(rec);
+        vs = __ldg(rec + 16);
+    };
+    // moves on to the next step, if there is one, and loads it
+    auto advance = [&]() {
+        opens = false;
+        if (++step >= last) {
+            if (!open()) return false;
+        } else if ((step & 3) == 0) {
+            ids = ids_next;
+            ids_next = id_at(32 * (step >> 2) + 32 + lane);
+        }
+        load();
+        return true;
+    };
+
+    bool live = open();
+    if (live) load();
+    int exponent = 0;   // E of the segment
+    bool have = false;  // E is set
+    for (int it = 0; live; ++it) {
+        const int st = it & 1;
+        if (opens) have = false;
+        // ---- range of the V scales of the tokens that exist; absent tokens
+        const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
+        const uint32_t wmax = __reduce_max_sync(0xffffffffu, present ? vbits : 0u);
+        const uint32_t wmin = __reduce_min_sync(0xffffffffu, present ? vbits : 0xffffffffu);
+        const uint32_t wmiss = __any_sync(0xffffffffu, missing);
+        if (lane == 0) *reinterpret_cast<uint4*>(reduce[st][cw]) = make_uint4(wmax, wmin, wmiss, 0u);
+        __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 128 * st;
+        const float before = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+        if (IsV) factors[tid] = __float2half(present ? vs * before : 0.f);  // right unless E or the mode changes below
+        const bool go = mbar_wait(&empty[st], static_cast<uint32_t>((it >> 1) & 1) ^ 1u, a.status, abort_flag);
+        if (!named_barrier_all(kBarrier, C::kConverters, go)) break;
+        uint32_t vmax = 0, vmin = 0xffffffffu, miss = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 r = *reinterpret_cast<const uint4*>(reduce[st][i]);
+            vmax = max(vmax, r.x);
+            vmin = min(vmin, r.y);
+            miss |= r.z;
+        }
+        bool wide = false;
+        const int old = exponent;
+        if (vmin != 0xffffffffu) {
+            if (!have) {
+                // the first step with tokens: its largest scale (smallest, beside an infinity) goes to 1/2 .. 1
+                const uint32_t ref = vmax < 0x7f800000u ? vmax : (vmin < 0x7f800000u ? vmin : 0x3f800000u);
+                exponent = max(-125, min(125, static_cast<int>(ref >> 23) - 126));
+                have = true;
+            }
+            // outside [2^(E - 14), 2^(E + 8)] (bits compare as the floats do)
+            const int lo = max(exponent - 14, -126) + 127, hi = min(exponent + 8, 127) + 127;
+            wide = vmin < static_cast<uint32_t>(lo) << 23 || vmax > static_cast<uint32_t>(hi) << 23;
+        }
+        if (IsV) {
+            if (wide || exponent != old) {
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
+                factors[tid] = __float2half(!present ? 0.f : wide ? 1.f : vs * down);
+                if (!named_barrier_all(kBarrier, C::kConverters, true)) break;
+            }
+            // ---- coordinate rows, 64 tokens each
+            uint8_t* vd = smem + C::kOffV + st * C::kVBytes;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int v = tid + i * C::kConverters;
+                const int block = v / kBlockVecs, d = v % kBlockVecs;
+                const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * block);
+                uint8_t* rowp = vd + (block >> 2) * C::kVPartBytes + d * 128;
+                const int c0 = (block & 3) * 2;
+                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (d & 7)) << 4)) = codes8_f16(w[i].x, w[i].y, f[0]);
+                *reinterpret_cast<uint4*>(rowp + (((c0 + 1) ^ (d & 7)) << 4)) = codes8_f16(w[i].z, w[i].w, f[1]);
+            }
+        } else {
+            uint8_t* tab = smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes;
+            float* cs = reinterpret_cast<float*>(tab);
+            cs[tid] = missing ? __uint_as_float(kAbsent) : present ? ks * cscale : 0.f;
+            if (wide || miss)  // a scale below the normal range counts as its smallest number
+                cs[128 + tid] = present && wide ? log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(exponent) : 0.f;
+            if (tid == 0) {
+                cs[256] = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
+                reinterpret_cast<int*>(tab)[257] = wide || miss;
+            }
+            // ---- token rows
+            uint8_t* kd = smem + C::kOffK + st * C::kTileBytes;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const int v = tid + i * C::kConverters;
+                const int token = v / (D / 16), ch = v % (D / 16);
+                const uint4 lo = codes8_bf16(w[i].x, w[i].y), hi = codes8_bf16(w[i].z, w[i].w);
+                uint8_t* rowp = kd + (ch >> 2) * C::kPartBytes + token * 128;
+                // lanes of the second column part write their halves in the other order: no bank is hit twice
+                const int flip = (ch >> 2) & 1;
+                const int c0 = (ch & 3) * 2 + flip;
+                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (token & 7)) << 4)) = flip ? hi : lo;
+                *reinterpret_cast<uint4*>(rowp + (((c0 ^ 1) ^ (token & 7)) << 4)) = flip ? lo : hi;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+        live = advance();
+    }
 }
 
 template <int D>
@@ -233,10 +396,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     uint64_t* pv_done = p_full + 4;           // [half][part]: that product has completed
     uint64_t* final_bar = pv_done + 4;        // [issuer]: everything it issued has completed
     int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::kOffPrefix);
-    ChunkPos* plan = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // [0] first position, [1] end
+    ChunkPos* plan = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // [0] first position, [1] end, [2 + warp] where a warp is
     int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + C::kOffMisc);
-    volatile int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + 128);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 132);
+    volatile int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + C::kThreads / 32 * 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kThreads / 32 * 8 + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x;
@@ -284,10 +447,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // Registers: launched with 128 a thread; 2 x 128 softmax threads take 168,
-    // the converters keep 128, the issuers 48: 65536 together, as launched.
+    // Registers: launched with 96 a thread, 61440 together, which 256 softmax
+    // threads at 144, 256 converters at 72 and 128 issuers at 48 share.
     if (warp < C::kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it
         const int x = warp >> 2;
         const int rr = (warp & 3) * 32 + lane;
@@ -326,6 +489,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[x]);
             }
+            const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
             float m = ninf(), l = 0.f, unit = 1.f;
             for (int j = 0; j < steps; ++j, ++it, ++table) {
                 if (!warp_wait(&s_full[x], it & 1, a.status, abort_flag)) {
@@ -336,42 +500,39 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 const uint8_t* tab = smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes;
                 const float* cs = reinterpret_cast<const float*>(tab);
                 unit = cs[256];
-                const int marks = reinterpret_cast<const int*>(tab)[257];
+                const bool plain = reinterpret_cast<const int*>(tab)[257] == 0;
+                const int seen = lim - (g.at.s + j) * kChunkStep + 1;  // tokens of the step the row sees
+                const bool masked = (g.at.s + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    float sx[64];
-                    {
-                        uint32_t sv[32], sw[32];
-                        tmem_ld32(col_s + 64 * part, sv);
-                        tmem_ld32(col_s + 64 * part + 32, sw);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            sx[e] = __uint_as_float(sv[e]);
-                            sx[32 + e] = __uint_as_float(sw[e]);
-                        }
-                    }
-                    const int valid = lim - ((g.at.s + j) * kChunkStep + 64 * part) + 1;  // tokens of the part the row sees
                     const float* cp = cs + 64 * part;
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(cp + e);
-                        f32x2_unpack(f32x2_mul(f32x2_pack(sx[e], sx[e + 1]), c4.x), sx[e], sx[e + 1]);
-                        f32x2_unpack(f32x2_mul(f32x2_pack(sx[e + 2], sx[e + 3]), c4.y), sx[e + 2], sx[e + 3]);
-                    }
-                    if (__any_sync(0xffffffffu, valid < 64)) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (e >= valid) sx[e] = ninf();
-                    }
-                    if (marks & kAbsentFlag) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (__float_as_uint(cp[e]) == kAbsent) sx[e] = ninf();
-                    }
-                    const bool wide = (marks & kWideFlag) != 0;
+                    const int seen_part = seen - 64 * part;
+                    const uint32_t col = col_s + 64 * part;
+                    float sx[64];
                     float mx;
-                    if (!wide) {
+                    if (plain) {
+                        {
+                            uint32_t lo[32], hi[32];
+                            tmem_ld32(col, lo);
+                            tmem_ld32(col + 32, hi);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                sx[e] = __uint_as_float(lo[e]);
+                                sx[32 + e] = __uint_as_float(hi[e]);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 64; e += 4) {
+                            const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(cp + e);
+                            f32x2_unpack(f32x2_mul(f32x2_pack(sx[e], sx[e + 1]), c4.x), sx[e], sx[e + 1]);
+                            f32x2_unpack(f32x2_mul(f32x2_pack(sx[e + 2], sx[e + 3]), c4.y), sx[e + 2], sx[e + 3]);
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                if (e >= seen_part) sx[e] = ninf();
+                        }
                         float m1[21];
 #pragma unroll
                         for (int k = 0; k < 21; ++k) m1[k] = fmax3(sx[3 * k], sx[3 * k + 1], sx[3 * k + 2]);
@@ -380,47 +541,53 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                         mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63]));
                     } else {
                         mx = ninf();
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 8) {
+                            float xe[8];
+                            slow_scores(col + c, cp + c, seen_part - c, xe);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) mx = fmaxf(mx, sx[e] == ninf() ? ninf() : sx[e] + cp[128 + e]);
+                            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
+                        }
                     }
                     const bool resc = mx > m + 8.f;
-                    float alpha = 1.f;
-                    if (resc) {
-                        const float mn = fmaxf(m, mx);
-                        alpha = m == ninf() ? 0.f : ex2(m - mn);
-                        m = mn;
-                        l *= alpha;
+                    // O holds something once a part of this segment has been multiplied in
+                    if (__any_sync(0xffffffffu, resc)) {
+                        float alpha = 1.f;
+                        if (resc) {
+                            const float mn = fmaxf(m, mx);
+                            alpha = m == ninf() ? 0.f : ex2(m - mn);
+                            m = mn;
+                            l *= alpha;
+                        }
+                        if (j + part > 0) {
+                            // part 0: the products of the step before completed ahead of these scores
+                            if (part == 1 && !warp_wait(&pv_done[2 * x], it & 1, a.status, abort_flag)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t ov[16];
+                                tmem_ld16(col_o + c, ov);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                tmem_st16(col_o + c, ov);
+                            }
+                        }
                     }
                     const float base = m == ninf() ? 0.f : m;
-                    // O holds something once a part of this segment has been multiplied in
-                    if (__any_sync(0xffffffffu, resc && j + part > 0)) {
-                        // part 0: the products of the step before completed ahead of these scores
-                        if (part == 1 && !warp_wait(&pv_done[2 * x], it & 1, a.status, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t ov[16];
-                            tmem_ld16(col_o + c, ov);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            tmem_st16(col_o + c, ov);
-                        }
-                        tmem_st_wait();
-                    }
-                    if (!wide) {
+                    if (plain) {
                         const uint64_t nb2 = f32x2_pack(-base, -base);
                         uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4) {
-                            uint32_t pw[8];
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t pw[16];
 #pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
+                            for (int e = 0; e < 32; e += 2) {
                                 float a0, a1;
-                                f32x2_unpack(f32x2_add(f32x2_pack(sx[16 * q4 + e], sx[16 * q4 + e + 1]), nb2), a0, a1);
+                                f32x2_unpack(f32x2_add(f32x2_pack(sx[32 * half + e], sx[32 * half + e + 1]), nb2), a0, a1);
                                 const float p0 = ex2(a0), p1 = ex2(a1);
                                 pw[e / 2] = pack_f16x2(p0, p1);
                                 if ((e / 2) & 1)
@@ -428,28 +595,25 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 else
                                     acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
                             }
-                            tmem_st8(col_s + 32 * part + 8 * q4, pw);
+                            tmem_st16(col_s + 32 * part + 16 * half, pw);
                         }
                         float s0, s1;
                         f32x2_unpack(f32x2_add(acc0, acc1), s0, s1);
                         l += s0 + s1;
                     } else {
+                        // the weights overwrite scores that have been read
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 8) {
+                            float xe[8], w[8];
+                            slow_scores(col + c, cp + c, seen_part - c, xe);
 #pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4) {
-                            uint32_t pw[8];
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float w2[2];
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const float xe = sx[16 * q4 + e + u];
-                                    const bool seen = xe != ninf();
-                                    w2[u] = seen ? ex2(xe + cp[128 + 16 * q4 + e + u] - base) : 0.f;
-                                    l += seen ? ex2(xe - base) : 0.f;
-                                }
-                                pw[e / 2] = pack_f16x2(w2[0], w2[1]);
+                            for (int e = 0; e < 8; ++e) {
+                                w[e] = xe[e] == ninf() ? 0.f : ex2(xe[e] + cp[128 + c + e] - base);
+                                l += xe[e] == ninf() ? 0.f : ex2(xe[e] - base);
                             }
-                            tmem_st8(col_s + 32 * part + 8 * q4, pw);
+                            const uint32_t pw[4] = {pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
+                                                    pack_f16x2(w[6], w[7])};
+                            tmem_st4(col_s + 32 * part + c / 2, pw);
                         }
                     }
                     tmem_st_wait();
@@ -515,155 +679,12 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             info->flags = ok ? flags : 0;
         }
     } else if (warp < C::kScoreWarp) {
-        // ------------------------------------------------ converters
-        const int tid = threadIdx.x - 32 * C::kConvertWarp;
-        const int cw = warp - C::kConvertWarp;
-        constexpr int kVecs = 128 * D / 16 / C::kConverters;  // 16-code vectors of K (and of V) per thread and step
-        constexpr int kBlockVecs = D;                         // vectors of one (block, head)
-        uint4 kr[kVecs], vr[kVecs];
-        float ks = 0.f, vs = 0.f;
-        bool present = false;  // token tid of the loaded step exists
-        bool missing = false;  // it lies in a block outside the pool
-        Step s;
-        s.cur = first;
-        step_open(sh, prefix, end, s);
-        // lanes 0-7 hold the step's 8 block ids (-1: past the sequence's blocks)
-        auto load_ids = [&](const Step& st) {
-            const int b = st.step * 8 + (lane & 7);
-            if (!st.live || b >= (st.g.q.n + 15) / 16) return -1;
-            const int id = __ldg(a.tables + static_cast<int64_t>(st.g.at.seq) * a.max_blocks + b);
-            if (id >= 0 && id < a.num_blocks) return id;
-            if (lane < 8) atomicOr(a.status, PKV_DEVERR_RANGE);
-            return -2;
-        };
-        auto vector_of = [&](int ids, int head, int i, int64_t& at) {  // vector i of this thread; false if absent
-            const int block = (tid + i * C::kConverters) / kBlockVecs;
-            const int id = __shfl_sync(0xffffffffu, ids, block);
-            at = (static_cast<int64_t>(id) * a.kv_heads + head) * kBlockVecs + (tid + i * C::kConverters) % kBlockVecs;
-            return id >= 0;
-        };
-        auto load_k = [&](const Step& st, int ids) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                int64_t at;
-                kr[i] = vector_of(ids, st.g.at.head, i, at) ? __ldg(static_cast<const uint4*>(a.k_codes) + at) : make_uint4(0u, 0u, 0u, 0u);
-            }
-            const int id = __shfl_sync(0xffffffffu, ids, tid >> 4);
-            present = id >= 0 && st.step * kChunkStep + tid < st.g.q.n;
-            missing = id == -2;
-            const float* rec = a.scales + (static_cast<int64_t>(id) * a.kv_heads + st.g.at.head) * 32 + (tid & 15);
-            ks = present ? __ldg(rec) : 0.f;
-            vs = present ? __ldg(rec + 16) : 0.f;
-        };
-        auto load_v = [&](const Step& st, int ids) {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                int64_t at;
-                vr[i] = vector_of(ids, st.g.at.head, i, at) ? __ldg(static_cast<const uint4*>(a.v_codes) + at) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        int ids = load_ids(s);
-        load_k(s, ids);
-        load_v(s, ids);
-        const float cscale = a.scale * kLog2e;
-        int exponent = 0;       // E of the segment
-        bool have = false;      // E is set
-        uint32_t (*reduce)[4][4] = reinterpret_cast<uint32_t (*)[4][4]>(smem + C::kOffReduce);
-        __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale);
-        int it = 0;
-        while (s.live) {
-            const int st = it & 1;
-            const uint32_t free_parity = static_cast<uint32_t>((it >> 1) & 1) ^ 1u;
-            if (s.step == s.g.at.s) have = false;  // a new segment
-            Step nx = s;
-            step_next(sh, prefix, end, nx);
-            const int next_ids = load_ids(nx);
-            // ---- the step's V scales: range over the tokens that exist, and absent tokens
-            const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-            const uint32_t wmax = __reduce_max_sync(0xffffffffu, present ? vbits : 0u);
-            const uint32_t wmin = __reduce_min_sync(0xffffffffu, present ? vbits : 0xffffffffu);
-            const uint32_t wmiss = __any_sync(0xffffffffu, missing);
-            if (lane == 0) {
-                reduce[st][cw][0] = wmax;
-                reduce[st][cw][1] = wmin;
-                reduce[st][cw][2] = wmiss;
-            }
-            bool go = mbar_wait(&k_empty[st], free_parity, a.status, abort_flag);
-            if (!named_barrier_all(1, C::kConverters, go)) break;
-            uint32_t vmax = 0, vmin = 0xffffffffu, miss = 0;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                vmax = max(vmax, reduce[st][w][0]);
-                vmin = min(vmin, reduce[st][w][1]);
-                miss |= reduce[st][w][2];
-            }
-            bool wide = false;
-            if (vmin != 0xffffffffu) {
-                if (!have) {
-                    // the first step with tokens: its largest scale (smallest, beside an infinity) near 1/2 .. 1
-                    const uint32_t ref = vmax < 0x7f800000u ? vmax : (vmin < 0x7f800000u ? vmin : 0x3f800000u);
-                    exponent = max(-125, min(125, static_cast<int>(ref >> 23) - 126));
-                    have = true;
-                }
-                // outside [2^(E - 14), 2^(E + 8)] (bits compare as the floats do)
-                const int lo = max(exponent - 14, -126) + 127, hi = min(exponent + 8, 127) + 127;
-                wide = vmin < static_cast<uint32_t>(lo) << 23 || vmax > static_cast<uint32_t>(hi) << 23;
-            }
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);  // 2^-E
-            uint8_t* tab = smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes;
-            float* cs = reinterpret_cast<float*>(tab);
-            cs[tid] = missing ? __uint_as_float(kAbsent) : ks * cscale;
-            if (wide) {
-                // a scale below the normal range counts as its smallest number
-                cs[128 + tid] = present ? log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(exponent) : 0.f;
-                factors[tid] = __float2half(present ? 1.f : 0.f);
-            } else {
-                factors[tid] = __float2half(vs * down);
-            }
-            if (tid == 0) {
-                cs[256] = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
-                reinterpret_cast<int*>(tab)[257] = (miss ? kAbsentFlag : 0) | (wide ? kWideFlag : 0);
-            }
-            // ---- K: token rows
-            uint8_t* kd = smem + C::kOffK + st * C::kTileBytes;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int v = tid + i * C::kConverters;
-                const int token = v / (D / 16), ch = v % (D / 16);
-                const uint4 lo = codes8_bf16(kr[i].x, kr[i].y), hi = codes8_bf16(kr[i].z, kr[i].w);
-                uint8_t* rowp = kd + (ch >> 2) * C::kPartBytes + token * 128;
-                // lanes of the second column part write their halves in the other order: no bank is hit twice
-                const int flip = (ch >> 2) & 1;
-                const int c0 = (ch & 3) * 2 + flip;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (token & 7)) << 4)) = flip ? hi : lo;
-                *reinterpret_cast<uint4*>(rowp + (((c0 ^ 1) ^ (token & 7)) << 4)) = flip ? lo : hi;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_full[st]);
-            if (nx.live) load_k(nx, next_ids);
-            // ---- V: coordinate rows, 64 tokens each
-            go = mbar_wait(&v_empty[st], free_parity, a.status, abort_flag);
-            if (!named_barrier_all(1, C::kConverters, go)) break;  // also: the factors are written
-            uint8_t* vd = smem + C::kOffV + st * C::kVBytes;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int v = tid + i * C::kConverters;
-                const int block = v / kBlockVecs, d = v % kBlockVecs;
-                const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * block);
-                uint8_t* rowp = vd + (block >> 2) * C::kVPartBytes + d * 128;
-                const int c0 = (block & 3) * 2;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (d & 7)) << 4)) = codes8_f16(vr[i].x, vr[i].y, f[0]);
-                *reinterpret_cast<uint4*>(rowp + (((c0 + 1) ^ (d & 7)) << 4)) = codes8_f16(vr[i].z, vr[i].w, f[1]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_full[st]);
-            if (nx.live) load_v(nx, next_ids);
-            // the factors are read before the next step's first barrier, which every thread passes before writing them again
-            s = nx;
-            ++it;
-        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        ChunkPos* after = plan + 2 + warp;  // every warp its own
+        if (warp < C::kConvertWarp + 4)
+            convert_role<D, false>(a, sh, smem, prefix, plan, after, k_full, k_empty, abort_flag);
+        else
+            convert_role<D, true>(a, sh, smem, prefix, plan, after, v_full, v_empty, abort_flag);
     } else if (warp < C::kValueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // ------------------------------------------------ scores S = Q K^T of half x (one thread)
