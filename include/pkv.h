@@ -452,9 +452,10 @@ PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_hea
  *                 zero-filled before its first use.
  * fp32 accumulation, one rounding to bf16. Up to 32 query rows per (sequence, KV
  * head) at head_dim 128 run on pkv_decode_attention_q8's kernel with its
- * roundings. Above that (and at head_dim 64) K enters the products exactly (codes
- * and q in bf16, the K scale applied to the fp32 score); a V value is rounded to
- * f16 relative to its step's largest V scale and a softmax weight to f16.
+ * roundings. Above that (and at head_dim 64) the products run on f16 tensor cores:
+ * q enters exactly (scaled by a power of two per row), a K value is rounded to f16
+ * once (an eighth of a quantization step at most), a V value twice (scale, value), a
+ * softmax weight once. Scales of any size and spread are taken.
  * Errors, checked mode and the device status bits as pkv_multiquery_attention.
  */
 PKV_API pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes,

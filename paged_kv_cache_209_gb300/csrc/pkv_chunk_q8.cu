@@ -3,19 +3,26 @@
 // per (sequence, KV head) or head_dim 64.
 //
 // Mathematics, per query row and step of 128 tokens:
-//     s_p = q . kc_p                    bf16 x bf16 -> fp32 (q and the codes exact)
-//     x_p = s_p * c_p,  c_p = ks_p * scale * log2(e)                        fp32
-//     w_p = 2^(x_p - m)                 m: running maximum, moved only when a
-//                                       score exceeds it by more than 8 (w <= 2^8)
+//     s_p = q' . k_p                    f16 x f16 -> fp32; q' is q times a power of two
+//                                       per row (exact), k_p = kc_p (ks_p 2^-F) rounded
+//                                       to f16 once, an eighth of a quantization step
+//     x_p = s_p f                       f = |scale| log2(e) 2^F over the row's power
+//     w_p = 2^(x_p - m)                 m: running maximum, moved only when a score
+//                                       exceeds it by more than 8 (w <= 2^8)
 //     l  += w_p;   O += w_p v_p         w rounded to f16; v_p = vc_p (vs_p 2^-E)
 //                                       rounded to f16; fp32 sums
 //     out = 2^E O / l
-// E is one exponent per piece of work, taken from its first step, that puts V
-// into the f16 range whatever its size. A later step whose V scales leave
-// [2^-14, 2^8] 2^E (rows 2^22 apart; or infinities) takes the codes themselves as
-// v_p and moves the scale into the weight, w_p = 2^(x_p + log2(vs_p) - E - m), with
-// l summed apart: slower, and exact over the whole float range, because the
-// maximum is then taken over tokens the row sees.
+// F and E are one exponent each per piece of work, taken from its first step, that
+// put K and V into the f16 range whatever their size. A step whose scales leave
+// [2^-14, 2^8] times that (rows 2^22 apart; or infinities), or with absent tokens, is
+// slow: it takes K's codes themselves and x_p = s_p ks_p f in fp32, and, where it is V
+// that leaves the range, V's codes with w_p = 2^(x_p + log2(vs_p) - E - m) and l summed
+// apart. That is exact over the whole float range, because the maximum is then
+// taken over tokens the row sees.
+//
+// K's scale sits in the K operand, not in the softmax, because a factor per token
+// costs every row a multiplication and a shared-memory broadcast, 1024 of the 2048
+// cycles that a step's products take: the softmax would be the bound.
 //
 // Work (pkv_chunk_schedule.cuh): one persistent CTA per SM takes a range of
 // (unit, step) pairs, a unit being 256 query rows of a (sequence, KV head) as
@@ -25,8 +32,8 @@
 // Roles (20 warps). Warps 0-3 and 4-7: the softmax of halves A and B, one thread
 // per query row. Warps 8-11 and 12-15: the converters of K and of V; they load
 // the codes of the next step from global memory into registers while they turn
-// the previous loads into bf16 (K) or scaled f16 (V), in the 128-byte-swizzled
-// layout the tensor cores read; K's also write the step's factors c_p. Warps 16
+// the previous loads into scaled f16, in the 128-byte-swizzled layout the tensor
+// cores read; K's also write the step's exponents and, for a slow step, its factors. Warps 16
 // and 17: one thread each issues S = Q K^T of A and of B; warps 18 and 19: O += P V
 // of A and of B, in two parts of 64 tokens. While the softmax of one half runs,
 // the tensor cores work on the other.
@@ -45,7 +52,7 @@ namespace pkv {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-// The factor c of an absent token (a block id outside the pool): a NaN that no
+// The K factor of an absent token (a block id outside the pool): a NaN that no
 // arithmetic produces.
 constexpr uint32_t kAbsent = 0x7fc0dead;
 
@@ -70,12 +77,12 @@ struct Cx {
     static constexpr int kOffK = kOffQ + 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffTable = kOffV + kStages * kVBytes;
-    // a table: c [128], log2(vs) - E [128] (0 unless the step is wide; written for
-    // wide steps and for those with absent tokens), then 2^E and 1 for such a step
-    static constexpr int kTableBytes = 2 * 128 * 4 + 16;
+    // a step's table: 2^E, 2^F, 1 for a slow step; and for a slow step the K factors
+    // [128] and log2(vs) - E [128] (0 unless V's scales leave the range)
+    static constexpr int kTableBytes = 16 + 2 * 128 * 4;
     static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [2][128]
-    static constexpr int kOffReduce = kOffScale + 512;                   // K, V: [2][4 warps] of 16 bytes
-    static constexpr int kOffBars = kOffReduce + 256;
+    static constexpr int kOffReduce = kOffScale + 512;                   // K, V: [2][4 warps] of 32 bytes
+    static constexpr int kOffBars = kOffReduce + 512;
     // k_full, k_empty, v_full, v_empty per stage; q_full, s_full per half;
     // p_full, pv_done per half and token part; final per issuer
     static constexpr int kNumBars = 4 * kStages + 2 * 2 + 2 * 4 + 4;
@@ -140,39 +147,47 @@ __device__ void sum_costs(const ChunkArgs& a, const ChunkShape& sh, int64_t* pre
 }
 
 // ---------------------------------------------------------------- conversions
-// Two codes (bytes 0 and 2 of `h`, the others 0x43) -> bf16x2, exactly: the byte
-// under exponent 0x43 without its top bit is 128 + (code mod 128); the top bit
-// alone is 128, or 256 for a negative code.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t h) {
-    const uint32_t a = h & 0xff7fff7fu, b = h & 0xff80ff80u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Two codes + 128 (bytes 0 and 2, the others 0x64: 1024 + code + 128 in f16)
-// times two f16 factors.
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t h, uint32_t factors) {
+// Two codes (+ 128, bytes of f16s 1024 + code + 128) as f16x2, exactly.
+__device__ __forceinline__ __half2 codes_f16x2(uint32_t h) {
     const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), bias), *reinterpret_cast<const __half2*>(&factors));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    return __hsub2(*reinterpret_cast<const __half2*>(&h), bias);
 }
-__device__ __forceinline__ uint4 codes8_bf16(uint32_t w0, uint32_t w1) {
-    return make_uint4(codes_bf16x2(__byte_perm(w0, 0x43434343u, 0x5140)), codes_bf16x2(__byte_perm(w0, 0x43434343u, 0x7362)),
-                      codes_bf16x2(__byte_perm(w1, 0x43434343u, 0x5140)), codes_bf16x2(__byte_perm(w1, 0x43434343u, 0x7362)));
-}
-__device__ __forceinline__ uint4 codes8_f16(uint32_t w0, uint32_t w1, const uint4& f) {
+__device__ __forceinline__ uint32_t bits(const __half2& x) { return *reinterpret_cast<const uint32_t*>(&x); }
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+// Eight codes of one token times hi + lo (the scale to 22 bits): one rounding but for
+// that of the small term.
+__device__ __forceinline__ uint4 k_values(uint32_t w0, uint32_t w1, __half2 hi, __half2 lo) {
     w0 ^= 0x80808080u;
     w1 ^= 0x80808080u;
-    return make_uint4(codes_f16x2(__byte_perm(w0, 0x64646464u, 0x5140), f.x), codes_f16x2(__byte_perm(w0, 0x64646464u, 0x7362), f.y),
-                      codes_f16x2(__byte_perm(w1, 0x64646464u, 0x5140), f.z), codes_f16x2(__byte_perm(w1, 0x64646464u, 0x7362), f.w));
+    const __half2 c0 = codes_f16x2(__byte_perm(w0, 0x64646464u, 0x5140)), c1 = codes_f16x2(__byte_perm(w0, 0x64646464u, 0x7362));
+    const __half2 c2 = codes_f16x2(__byte_perm(w1, 0x64646464u, 0x5140)), c3 = codes_f16x2(__byte_perm(w1, 0x64646464u, 0x7362));
+    return make_uint4(bits(__hfma2(c0, hi, __hmul2(c0, lo))), bits(__hfma2(c1, hi, __hmul2(c1, lo))),
+                      bits(__hfma2(c2, hi, __hmul2(c2, lo))), bits(__hfma2(c3, hi, __hmul2(c3, lo))));
+}
+// Eight codes of one coordinate times their tokens' factors.
+__device__ __forceinline__ uint4 v_values(uint32_t w0, uint32_t w1, const uint4& f) {
+    w0 ^= 0x80808080u;
+    w1 ^= 0x80808080u;
+    return make_uint4(bits(__hmul2(codes_f16x2(__byte_perm(w0, 0x64646464u, 0x5140)), half2_of(f.x))),
+                      bits(__hmul2(codes_f16x2(__byte_perm(w0, 0x64646464u, 0x7362)), half2_of(f.y))),
+                      bits(__hmul2(codes_f16x2(__byte_perm(w1, 0x64646464u, 0x5140)), half2_of(f.z))),
+                      bits(__hmul2(codes_f16x2(__byte_perm(w1, 0x64646464u, 0x7362)), half2_of(f.w))));
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// The exponent a segment takes from its first step's scales (bits of the largest and
+// smallest): the largest, or beside an infinity the smallest, goes to 1/2 .. 1.
+__device__ __forceinline__ int range_exponent(uint32_t most, uint32_t least) {
+    const uint32_t ref = most < 0x7f800000u ? most : (least < 0x7f800000u ? least : 0x3f800000u);
+    return max(-125, min(125, static_cast<int>(ref >> 23) - 126));
+}
+// Whether scales leave [2^(e - 14), 2^(e + 8)] (bits compare as the floats do).
+__device__ __forceinline__ bool leaves_range(uint32_t most, uint32_t least, int e) {
+    return least < static_cast<uint32_t>(max(e - 14, -126) + 127) << 23 || most > static_cast<uint32_t>(min(e + 8, 127) + 127) << 23;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 // kind::f16 with f16 A and B, fp32 accumulator, both K-major.
@@ -193,15 +208,15 @@ __device__ __forceinline__ bool named_barrier_all(int id, int threads, bool ok) 
     return r != 0;
 }
 
-// Eight scores of a step that is not plain, scaled, -inf where the token is absent or not
-// seen (columns taddr .. taddr + 7, factors c, the first `seen` of them seen).
-__device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, int seen, float (&x)[8]) {
+// Eight scores of a slow step, scaled, -inf where the token is absent or not seen
+// (columns taddr .. taddr + 7, K factors c, row factor f, the first `seen` of them seen).
+__device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, float f, int seen, float (&x)[8]) {
     uint32_t v[8];
     tmem_ld8(taddr, v);
     tmem_ld_wait();
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e];
+        x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
 // mbar_wait by a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
@@ -210,8 +225,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
 
 // ---------------------------------------------------------------- converters
 // K's (IsV false) or V's four warps: every step of the CTA's range, one load
-// ahead. The V scales' range decides a step's mode and a segment's exponent; both
-// groups read the scales and decide alike.
+// ahead. Warp w takes tokens 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1), lane l
+// the scales of token 32 w + l. The range of the scales decides a step's mode and a
+// segment's exponents; both groups read V's scales and decide alike.
 template <int D, bool IsV>
 __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* smem, const int64_t* prefix,
                              const ChunkPos* plan, ChunkPos* after, uint64_t* full, uint64_t* empty,
@@ -219,22 +235,22 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
     using C = Cx<D>;
     const int lane = threadIdx.x & 31;
     const int cw = (threadIdx.x >> 5) & 3;
-    const int tid = cw * 32 + lane;
-    constexpr int kVecs = 128 * D / 16 / C::kConverters;  // 16-code vectors per thread and step
-    constexpr int kBlockVecs = D;                         // vectors of one (block, head)
+    constexpr int kVecs = 32 * D / 16 / 32;    // 16-code vectors per lane and step
+    constexpr int kPerBlock = kVecs / 2;       // of them in each of the warp's two blocks
+    constexpr int kLanes = D / 16;             // lanes that hold one token's K row
+    constexpr int kBlockVecs = D;              // vectors of one (block, head)
     constexpr int kBarrier = IsV ? 2 : 1;
     const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes);
-    uint32_t (*reduce)[4][4] = reinterpret_cast<uint32_t (*)[4][4]>(smem + C::kOffReduce + (IsV ? 128 : 0));
-    const float cscale = a.scale * kLog2e;
+    uint32_t (*reduce)[4][8] = reinterpret_cast<uint32_t (*)[4][8]>(smem + C::kOffReduce + (IsV ? 256 : 0));
 
     // the segment being loaded (the position after it: in shared memory, one per warp, read once per segment)
     if (lane == 0) *after = plan[0];
     __syncwarp();
-    int step = 0, last = 0;            // next step to load, one past the segment's last
-    int n = 0, head = 0;               // its tokens, KV head
-    const int32_t* trow = nullptr;     // its block table
-    int ids = 0, ids_next = 0;         // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
-    bool opens = false;                // the loaded step is its segment's first
+    int step = 0, last = 0;         // next step to load, one past the segment's last
+    int n = 0, head = 0;            // its tokens, KV head
+    const int32_t* trow = nullptr;  // its block table
+    int ids = 0, ids_next = 0;      // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
+    bool opens = false;             // the loaded step is its segment's first
     auto id_at = [&](int b) {
         if (b >= (n + 15) / 16) return -1;
         const int id = __ldg(trow + b);
@@ -259,23 +275,25 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
         opens = true;
         return true;
     };
-    // the loaded step: codes, scales of token `tid`, whether it exists or lies in a block outside the pool
+    // the loaded step: codes; scales of the lane's token, whether it exists or lies in a block outside the pool
     uint4 w[kVecs];
     float ks = 0.f, vs = 0.f;
     bool present = false, missing = false;
     auto load = [&]() {
-        const int b0 = (step & 3) * 8;
+        const int b0 = (step & 3) * 8 + 2 * cw;
+        const int id0 = __shfl_sync(0xffffffffu, ids, b0), id1 = __shfl_sync(0xffffffffu, ids, b0 + 1);
+        // an absent block's codes may be any (its tokens carry no weight): block 0 exists
+        const uint4* src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
+        const uint4* src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const int v = tid + i * C::kConverters;
-            // an absent block's codes may be any (its tokens carry no weight): block 0 exists
-            const int id = max(0, __shfl_sync(0xffffffffu, ids, b0 + v / kBlockVecs));
-            w[i] = __ldg(codes + (static_cast<int64_t>(id) * a.kv_heads + head) * kBlockVecs + v % kBlockVecs);
+        for (int i = 0; i < kPerBlock; ++i) {
+            w[i] = __ldg(src0 + 32 * i);
+            w[kPerBlock + i] = __ldg(src1 + 32 * i);
         }
-        const int id = __shfl_sync(0xffffffffu, ids, b0 + (tid >> 4));
-        present = id >= 0 && step * kChunkStep + tid < n;
+        const int id = lane < 16 ? id0 : id1;
+        present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
         missing = id == -2;
-        const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (tid & 15);
+        const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (lane & 15);
         if (!IsV) ks = __ldg(rec);
         vs = __ldg(rec + 16);
     };
@@ -294,84 +312,96 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
 
     bool live = open();
     if (live) load();
-    int exponent = 0;   // E of the segment
-    bool have = false;  // E is set
+    int ev = 0, ek = 0;  // E and F of the segment
+    bool have = false;   // they are set
     for (int it = 0; live; ++it) {
         const int st = it & 1;
         if (opens) have = false;
-        // ---- range of the V scales of the tokens that exist; absent tokens
+        // ---- range of the scales of the tokens that exist; absent tokens
         const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-        const uint32_t wmax = __reduce_max_sync(0xffffffffu, present ? vbits : 0u);
-        const uint32_t wmin = __reduce_min_sync(0xffffffffu, present ? vbits : 0xffffffffu);
-        const uint32_t wmiss = __any_sync(0xffffffffu, missing);
-        if (lane == 0) *reinterpret_cast<uint4*>(reduce[st][cw]) = make_uint4(wmax, wmin, wmiss, 0u);
-        __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 128 * st;
-        const float before = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-        if (IsV) factors[tid] = __float2half(present ? vs * before : 0.f);  // right unless E or the mode changes below
+        const uint32_t kbits = __float_as_uint(ks) & 0x7fffffffu;
+        {
+            const uint32_t vm = __reduce_max_sync(0xffffffffu, present ? vbits : 0u);
+            const uint32_t vl = __reduce_min_sync(0xffffffffu, present ? vbits : 0xffffffffu);
+            if (lane == 0) *reinterpret_cast<uint2*>(&reduce[st][cw][0]) = make_uint2(vm, vl);
+            if (!IsV) {
+                const uint32_t km = __reduce_max_sync(0xffffffffu, present ? kbits : 0u);
+                const uint32_t kl = __reduce_min_sync(0xffffffffu, present ? kbits : 0xffffffffu);
+                const uint32_t miss = __any_sync(0xffffffffu, missing);
+                if (lane == 0) *reinterpret_cast<uint4*>(&reduce[st][cw][4]) = make_uint4(km, kl, miss, 0u);
+            }
+        }
         const bool go = mbar_wait(&empty[st], static_cast<uint32_t>((it >> 1) & 1) ^ 1u, a.status, abort_flag);
         if (!named_barrier_all(kBarrier, C::kConverters, go)) break;
-        uint32_t vmax = 0, vmin = 0xffffffffu, miss = 0;
+        uint32_t vmax = 0, vmin = 0xffffffffu, kmax = 0, kmin = 0xffffffffu, miss = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint4 r = *reinterpret_cast<const uint4*>(reduce[st][i]);
+            const uint2 r = *reinterpret_cast<const uint2*>(&reduce[st][i][0]);
             vmax = max(vmax, r.x);
             vmin = min(vmin, r.y);
-            miss |= r.z;
+            if (!IsV) {
+                const uint4 t = *reinterpret_cast<const uint4*>(&reduce[st][i][4]);
+                kmax = max(kmax, t.x);
+                kmin = min(kmin, t.y);
+                miss |= t.z;
+            }
         }
-        bool wide = false;
-        const int old = exponent;
+        bool wide = false, slow = miss != 0;
         if (vmin != 0xffffffffu) {
-            if (!have) {
-                // the first step with tokens: its largest scale (smallest, beside an infinity) goes to 1/2 .. 1
-                const uint32_t ref = vmax < 0x7f800000u ? vmax : (vmin < 0x7f800000u ? vmin : 0x3f800000u);
-                exponent = max(-125, min(125, static_cast<int>(ref >> 23) - 126));
+            if (!have) {  // the segment's first step with tokens
+                ev = range_exponent(vmax, vmin);
+                if (!IsV) ek = range_exponent(kmax, kmin);
                 have = true;
             }
-            // outside [2^(E - 14), 2^(E + 8)] (bits compare as the floats do)
-            const int lo = max(exponent - 14, -126) + 127, hi = min(exponent + 8, 127) + 127;
-            wide = vmin < static_cast<uint32_t>(lo) << 23 || vmax > static_cast<uint32_t>(hi) << 23;
+            wide = leaves_range(vmax, vmin, ev);
+            if (!IsV) slow |= wide || leaves_range(kmax, kmin, ek);
         }
         if (IsV) {
-            if (wide || exponent != old) {
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - exponent) << 23);
-                factors[tid] = __float2half(!present ? 0.f : wide ? 1.f : vs * down);
-                if (!named_barrier_all(kBarrier, C::kConverters, true)) break;
-            }
-            // ---- coordinate rows, 64 tokens each
-            uint8_t* vd = smem + C::kOffV + st * C::kVBytes;
+            __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 128 * st + 32 * cw;
+            factors[lane] = __float2half(!present ? 0.f : wide ? 1.f : vs * exp2_int(-ev));
+            __syncwarp();
+            // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
+            uint8_t* vd = smem + C::kOffV + st * C::kVBytes + (cw >> 1) * C::kVPartBytes + lane * 128;
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const int v = tid + i * C::kConverters;
-                const int block = v / kBlockVecs, d = v % kBlockVecs;
-                const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * block);
-                uint8_t* rowp = vd + (block >> 2) * C::kVPartBytes + d * 128;
-                const int c0 = (block & 3) * 2;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (d & 7)) << 4)) = codes8_f16(w[i].x, w[i].y, f[0]);
-                *reinterpret_cast<uint4*>(rowp + (((c0 + 1) ^ (d & 7)) << 4)) = codes8_f16(w[i].z, w[i].w, f[1]);
+            for (int b = 0; b < 2; ++b) {
+                const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * b);
+                const uint4 f0 = f[0], f1 = f[1];
+                const int c0 = ((2 * cw + b) & 3) * 2;
+#pragma unroll
+                for (int i = 0; i < kPerBlock; ++i) {
+                    const uint4& x = w[b * kPerBlock + i];
+                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + ((c0 ^ (lane & 7)) << 4)) = v_values(x.x, x.y, f0);
+                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + (((c0 + 1) ^ (lane & 7)) << 4)) = v_values(x.z, x.w, f1);
+                }
             }
         } else {
-            uint8_t* tab = smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes;
-            float* cs = reinterpret_cast<float*>(tab);
-            cs[tid] = missing ? __uint_as_float(kAbsent) : present ? ks * cscale : 0.f;
-            if (wide || miss)  // a scale below the normal range counts as its smallest number
-                cs[128 + tid] = present && wide ? log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(exponent) : 0.f;
-            if (tid == 0) {
-                cs[256] = __uint_as_float(static_cast<uint32_t>(127 + exponent) << 23);
-                reinterpret_cast<int*>(tab)[257] = wide || miss;
+            float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
+            if (cw == 0 && lane == 0)
+                *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), slow ? 1.f : 0.f, 0.f);
+            if (slow) {
+                tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : present ? ks : 0.f;
+                // a scale below the normal range counts as its smallest number
+                tab[4 + 128 + 32 * cw + lane] = present && wide ? log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev) : 0.f;
             }
-            // ---- token rows
-            uint8_t* kd = smem + C::kOffK + st * C::kTileBytes;
+            const float factor = !present ? 0.f : slow ? 1.f : ks * exp2_int(-ek);
+            const __half hi = __float2half(factor);
+            const uint32_t pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));  // (hi, lo) of the lane's token
+            // ---- token rows: vector i of a lane lies in row 32 cw + i * (32 / kLanes) + lane / kLanes
+            const int ch = lane % kLanes, sub = lane / kLanes;
+            // lanes of the second column part write their halves in the other order: no bank is hit twice
+            const int flip = ch >> 2;
+            uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
+            const int c0 = (ch & 3) * 2 + flip;
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int v = tid + i * C::kConverters;
-                const int token = v / (D / 16), ch = v % (D / 16);
-                const uint4 lo = codes8_bf16(w[i].x, w[i].y), hi = codes8_bf16(w[i].z, w[i].w);
-                uint8_t* rowp = kd + (ch >> 2) * C::kPartBytes + token * 128;
-                // lanes of the second column part write their halves in the other order: no bank is hit twice
-                const int flip = (ch >> 2) & 1;
-                const int c0 = (ch & 3) * 2 + flip;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ (token & 7)) << 4)) = flip ? hi : lo;
-                *reinterpret_cast<uint4*>(rowp + (((c0 ^ 1) ^ (token & 7)) << 4)) = flip ? lo : hi;
+                // (the row modulo 8 alternates between two values at head_dim 128)
+                const int row8 = (i * (32 / kLanes) + sub) & 7;
+                const uint32_t f = __shfl_sync(0xffffffffu, pair, i * (32 / kLanes) + sub);
+                const __half2 fh = half2_of(__byte_perm(f, f, 0x1010)), fl = half2_of(__byte_perm(f, f, 0x3232));
+                const uint4 x0 = k_values(w[i].x, w[i].y, fh, fl), x1 = k_values(w[i].z, w[i].w, fh, fl);
+                uint8_t* rowp = kd + i * (32 / kLanes) * 128;
+                *reinterpret_cast<uint4*>(rowp + ((c0 ^ row8) << 4)) = flip ? x1 : x0;
+                *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = flip ? x0 : x1;
             }
         }
         fence_proxy_async_smem();
@@ -477,13 +507,31 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             const int t = (r0 + rr) / a.group;
             const int64_t row = (static_cast<int64_t>(g.q.q0) + t) * a.q_heads + h * a.group + (r0 + rr - t * a.group);
             const int lim = row_ok ? g.q.n - g.q.nq + t : -1;  // the last token the row sees
+            float row_f = 0.f;  // |scale| log2(e) over the power of two in q'
             {
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D);
+                uint4 v[D / 8];
+                uint32_t top = 0;  // largest |q|, per half word
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    v[c] = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                                 __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+                }
+                // the row's largest goes to 2^14 .. 2^15 (a row with infinities is left as it is);
+                // the scale's sign goes into q', a zero scale makes q' zero
+                const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // biased exponent
+                const int shift = ex == 255 || ex == 0 ? 0 : min(126, 141 - ex);  // -113 .. 126
+                const float mul = a.scale == 0.f ? 0.f : copysignf(exp2_int(shift), a.scale);
+                row_f = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * exp2_int(-shift);
                 uint8_t* qs = smem + C::kOffQ + x * C::kTileBytes + rr * 128;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(qs + (c >> 3) * C::kPartBytes + (((c & 7) ^ (rr & 7)) << 4)) = v;
+                    const uint4 h = make_uint4(pack_f16x2(bf16lo_to_f32(v[c].x) * mul, bf16hi_to_f32(v[c].x) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v[c].y) * mul, bf16hi_to_f32(v[c].y) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v[c].z) * mul, bf16hi_to_f32(v[c].z) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v[c].w) * mul, bf16hi_to_f32(v[c].w) * mul));
+                    *reinterpret_cast<uint4*>(qs + (c >> 3) * C::kPartBytes + (((c & 7) ^ (rr & 7)) << 4)) = h;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -497,15 +545,17 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     break;
                 }
                 tc_fence_after();
-                const uint8_t* tab = smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes;
-                const float* cs = reinterpret_cast<const float*>(tab);
-                unit = cs[256];
-                const bool plain = reinterpret_cast<const int*>(tab)[257] == 0;
+                const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes);
+                const float4 modes = *reinterpret_cast<const float4*>(tab);
+                unit = modes.x;
+                const bool plain = modes.z == 0.f;
+                // never 0 or infinite: a hidden score is -inf times it
+                const float f = plain ? fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f) : row_f;
                 const int seen = lim - (g.at.s + j) * kChunkStep + 1;  // tokens of the step the row sees
                 const bool masked = (g.at.s + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    const float* cp = cs + 64 * part;
+                    const float* cp = tab + 4 + 64 * part;  // of a slow step
                     const int seen_part = seen - 64 * part;
                     const uint32_t col = col_s + 64 * part;
                     float sx[64];
@@ -522,12 +572,6 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 sx[32 + e] = __uint_as_float(hi[e]);
                             }
                         }
-#pragma unroll
-                        for (int e = 0; e < 64; e += 4) {
-                            const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(cp + e);
-                            f32x2_unpack(f32x2_mul(f32x2_pack(sx[e], sx[e + 1]), c4.x), sx[e], sx[e + 1]);
-                            f32x2_unpack(f32x2_mul(f32x2_pack(sx[e + 2], sx[e + 3]), c4.y), sx[e + 2], sx[e + 3]);
-                        }
                         if (masked) {
 #pragma unroll
                             for (int e = 0; e < 64; ++e)
@@ -538,13 +582,13 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                         for (int k = 0; k < 21; ++k) m1[k] = fmax3(sx[3 * k], sx[3 * k + 1], sx[3 * k + 2]);
 #pragma unroll
                         for (int k = 0; k < 7; ++k) m1[k] = fmax3(m1[3 * k], m1[3 * k + 1], m1[3 * k + 2]);
-                        mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63]));
+                        mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63])) * f;
                     } else {
                         mx = ninf();
 #pragma unroll 1
                         for (int c = 0; c < 64; c += 8) {
                             float xe[8];
-                            slow_scores(col + c, cp + c, seen_part - c, xe);
+                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
                         }
@@ -579,7 +623,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     }
                     const float base = m == ninf() ? 0.f : m;
                     if (plain) {
-                        const uint64_t nb2 = f32x2_pack(-base, -base);
+                        const uint64_t nb2 = f32x2_pack(-base, -base), f2 = f32x2_pack(f, f);
                         uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
@@ -587,7 +631,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) {
                                 float a0, a1;
-                                f32x2_unpack(f32x2_add(f32x2_pack(sx[32 * half + e], sx[32 * half + e + 1]), nb2), a0, a1);
+                                f32x2_unpack(f32x2_fma(f32x2_pack(sx[32 * half + e], sx[32 * half + e + 1]), f2, nb2), a0, a1);
                                 const float p0 = ex2(a0), p1 = ex2(a1);
                                 pw[e / 2] = pack_f16x2(p0, p1);
                                 if ((e / 2) & 1)
@@ -605,7 +649,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 #pragma unroll 1
                         for (int c = 0; c < 64; c += 8) {
                             float xe[8], w[8];
-                            slow_scores(col + c, cp + c, seen_part - c, xe);
+                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
                                 w[e] = xe[e] == ninf() ? 0.f : ex2(xe[e] + cp[128 + c + e] - base);
@@ -690,7 +734,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         // ------------------------------------------------ scores S = Q K^T of half x (one thread)
         const int x = warp - C::kScoreWarp;
         if (lane == 0) {
-            constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idS = umma_idesc_f16(128, 128);
             const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
             int step = 0, it = 0, segs = 0;
             bool ok = true;

@@ -2,9 +2,13 @@
 cached rows stand for.
 
 Tolerance, per element, with A = sum_p softmax_p |V_p| of its row and B the
-largest scale * |q||K_p| a row's scores can reach (Cauchy-Schwarz):
+largest scale * |q||K_p| its scores can reach (Cauchy-Schwarz):
   * the output's rounding to bf16: 2^-8 |ref| (half a step, eps / 2);
   * three roundings to f16 (the weight, the V scale, code * scale): 3 * 2^-11 A;
+  * K's rounding to f16, half a step 2^-11 of each value: at most 2^-11 B in the score,
+    counted twice (numerator and denominator); below f16's normal range half its
+    smallest step, 2^-25 2^F <= 2^-11 ks (scales in plain steps are at least
+    2^(F - 14)), at most 2^-11 scale |q|_1 ks;
   * the score: D + 2 float32 operations on products that sum to at most B in
     size, 2^-22 each (a truncating adder loses a whole step), a relative change
     of the weight, counted twice (numerator and denominator): 2 (D + 2) 2^-22 B A;
@@ -81,6 +85,13 @@ def call(pkv, c, d=None, **kw):
                                            c["scale"], most, **kw)
 
 
+def score_error(scale, q, k_norm, k_scale):
+    """How far a score of each row may be off: f16 K values, float32 sums."""
+    d = q.shape[-1]
+    b = abs(scale) * np.linalg.norm(q, axis=-1) * k_norm
+    return b * (2.0 ** -11 + (d + 2) * 2.0 ** -22) + 2.0 ** -11 * abs(scale) * np.abs(q).sum(-1) * k_scale
+
+
 def reference(c):
     """(output, tolerance) in float64."""
     with np.errstate(invalid="ignore"):
@@ -93,9 +104,10 @@ def reference(c):
                                                c["kv_heads"], "f64")
     ref, size = attend(vd), attend(np.abs(vd))
     d, n = qf.shape[2], int(max(c["lens"]))
-    b = abs(c["scale"]) * np.linalg.norm(qf, axis=-1).max(initial=0) * np.linalg.norm(kd, axis=-1).max(initial=0)
-    tol = 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + n * 2.0 ** -23)
-    scales = np.where(dead.reshape(-1, 1, 16), 0.0, np.abs(c["vs"].astype(np.float64)))
+    alive = lambda x: np.where(dead.reshape(-1, 1, 16), 0.0, np.abs(x.astype(np.float64)))  # noqa: E731
+    b = score_error(c["scale"], qf, np.linalg.norm(kd, axis=-1).max(initial=0), alive(c["ks"]).max(initial=0))[..., None]
+    tol = 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * b + 2.0 ** -20 + n * 2.0 ** -23)
+    scales = alive(c["vs"])
     tol += 2.0 ** -11 * attend(np.broadcast_to(scales[..., None], vd.shape))
     group = qf.shape[1] // c["kv_heads"]
     for i, n in enumerate(c["lens"]):                          # the largest |V| among the tokens each row sees
@@ -240,9 +252,9 @@ def test_blocks_outside_the_pool_are_absent(pkv, d):
                 w = np.exp(x - x.max())
                 w /= w.sum()
                 ref[q0 + t, h], size = w @ v[:, h // 4], w @ np.abs(v[:, h // 4])
-                b = c["scale"] * np.linalg.norm(q[h]) * np.linalg.norm(k[:, h // 4], axis=1).max()
+                b = score_error(c["scale"], q[h], np.linalg.norm(k[:, h // 4], axis=1).max(), float(c["ks"].max()))
                 tol[q0 + t, h] = 2.0 ** -8 * np.abs(ref[q0 + t, h]) + size * (
-                    3 * 2.0 ** -11 + 2 * (d + 2) * 2.0 ** -22 * b + 2.0 ** -20 + 300 * 2.0 ** -23)
+                    3 * 2.0 ** -11 + 2 * b + 2.0 ** -20 + 300 * 2.0 ** -23)
                 tol[q0 + t, h] += 300 * 2.0 ** -25 * np.abs(v[:, h // 4]).max() + 2.0 ** -11 * float(c["vs"].max())
     check(out, c, (ref, tol))
     assert bool((out[120:] == 0).all())
@@ -383,8 +395,8 @@ def test_prefill512_layer_sampled(pkv):
         x = x.masked_fill(torch.arange(8192, device="cuda") > torch.arange(7680, 8192, device="cuda")[:, None], -math.inf)
         w = torch.softmax(x, -1)
         ref, size = w @ v, w @ v.abs()
-        b = scale * float(qq.norm(dim=1).max() * k.norm(dim=1).max())
-        tol = 2.0 ** -8 * ref.abs() + size * (3 * 2.0 ** -11 + 260 * 2.0 ** -22 * b + 2.0 ** -20 + 8192 * 2.0 ** -23)
+        b = torch.from_numpy(score_error(scale, qq.cpu().numpy(), float(k.norm(dim=1).max()), 0.03)).cuda()[:, None]
+        tol = 2.0 ** -8 * ref.abs() + size * (3 * 2.0 ** -11 + 2 * b + 2.0 ** -20 + 8192 * 2.0 ** -23)
         tol = tol + 8192 * 2.0 ** -25 * v.abs().max() + 2.0 ** -11 * 0.03
         assert bool(((out[512 * i:512 * (i + 1), h].double() - ref).abs() <= tol).all())
     assert pkv.pkv_device_status(clear=True) == 0
