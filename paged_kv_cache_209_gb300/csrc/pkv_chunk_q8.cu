@@ -7,18 +7,18 @@
 //                                       per row (exact), k_p = kc_p (ks_p 2^-F) rounded
 //                                       to f16 once, an eighth of a quantization step
 //     x_p = s_p f                       f = |scale| log2(e) 2^F over the row's power
-//     w_p = 2^(x_p - m)                 m: running maximum, moved only when a score
-//                                       exceeds it by more than 8 (w <= 2^8)
+//     w_p = 2^(x_p - m)                 m: running maximum, moved only when weights
+//                                       would sum to more than 2^14 in a part
 //     l  += w_p;   O += w_p v_p         w rounded to f16; v_p = vc_p (vs_p 2^-E)
 //                                       rounded to f16; fp32 sums
 //     out = 2^E O / l
-// F and E are one exponent each per piece of work, taken from its first step, that
-// put K and V into the f16 range whatever their size. A step whose scales leave
-// [2^-14, 2^8] times that (rows 2^22 apart; or infinities), or with absent tokens, is
-// slow: it takes K's codes themselves and x_p = s_p ks_p f in fp32, and, where it is V
-// that leaves the range, V's codes with w_p = 2^(x_p + log2(vs_p) - E - m) and l summed
-// apart. That is exact over the whole float range, because the maximum is then
-// taken over tokens the row sees.
+// F and E are one exponent each per piece of work, taken from the scales of its first
+// block, that put K and V into the f16 range whatever their size. 32 tokens whose
+// scales leave [2^-14, 2^8] times that (rows 2^22 apart; or infinities) are taken as
+// bare codes; a step that holds such tokens, or absent ones, is slow: it takes
+// x_p = s_p ks_p f in fp32, and w_p = 2^(x_p + log2(vs_p) - E - m) with l summed apart
+// where V's codes are bare. That is exact over the whole float range, because the
+// maximum is then taken over tokens the row sees.
 //
 // K's scale sits in the K operand, not in the softmax, because a factor per token
 // costs every row a multiplication and a shared-memory broadcast, 1024 of the 2048
@@ -58,6 +58,8 @@ constexpr uint32_t kAbsent = 0x7fc0dead;
 
 __device__ __forceinline__ float ninf() { return __int_as_float(0xff800000); }
 
+constexpr int kMaxPieces = 512;  // CTAs of a launch, and pieces of a unit, at most
+
 template <int D>
 struct Cx {
     static constexpr int kSoftmaxWarps = 8;
@@ -66,30 +68,36 @@ struct Cx {
     static constexpr int kValueWarp = 18;   // 18, 19
     static constexpr int kThreads = 640;
     static constexpr int kConverters = 128;  // threads that convert K, and V
-    static constexpr int kStages = 2;     // K stages, and V stages
-    static constexpr int kTables = 4;     // factor tables in flight
+    static constexpr int kStages = 2;   // K stages (a step each)
+    static constexpr int kParts = 3;    // V stages (64 tokens each)
+    // Tables in flight: K's converters run at most four steps ahead of the slower
+    // softmax half (a fifth needs scores that need V parts which that half's
+    // products have yet to release).
+    static constexpr int kTables = 8;
     static constexpr int kHalves = D / 64;                    // 128-byte column parts of a K or Q row
     static constexpr int kPartBytes = 128 * 128;              // 128 rows of one part
     static constexpr int kTileBytes = kHalves * kPartBytes;   // Q of one row half; one K stage
-    static constexpr int kVPartBytes = D * 128;               // 64 tokens of every coordinate
-    static constexpr int kVBytes = 2 * kVPartBytes;           // one V stage
+    static constexpr int kVPartBytes = D * 128;               // one V stage: 64 tokens of every coordinate
+    static constexpr int kVecs = D / 16;                      // 16-code vectors of a converter lane and step
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kOffTable = kOffV + kStages * kVBytes;
-    // a step's table: 2^E, 2^F, 1 for a slow step; and for a slow step the K factors
-    // [128] and log2(vs) - E [128] (0 unless V's scales leave the range)
+    static constexpr int kOffCodes = kOffV + kParts * kVPartBytes;  // the next step's codes: [8 warps][kVecs][32 lanes] vectors
+    static constexpr int kOffTable = kOffCodes + 8 * kVecs * 512;
+    // a step's table: 2^E, 2^F, a byte per converter warp that is 1 for a slow step;
+    // for slow steps the tokens' K factors [128] and, in log2, what their V values lack [128]
     static constexpr int kTableBytes = 16 + 2 * 128 * 4;
-    static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [2][128]
-    static constexpr int kOffReduce = kOffScale + 512;                   // K, V: [2][4 warps] of 32 bytes
-    static constexpr int kOffBars = kOffReduce + 512;
-    // k_full, k_empty, v_full, v_empty per stage; q_full, s_full per half;
-    // p_full, pv_done per half and token part; final per issuer
-    static constexpr int kNumBars = 4 * kStages + 2 * 2 + 2 * 4 + 4;
-    static constexpr int kOffPrefix = kOffBars + kNumBars * 8;
-    static constexpr int kOffPlan = kOffPrefix + (kMaxBatchPerLaunch + 1) * 8;
-    static constexpr int kOffMisc = kOffPlan + (2 + kThreads / 32) * 16;
+    static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [128]
+    static constexpr int kOffBars = kOffScale + 256;
+    // k_full, k_empty per K stage; v_full, v_empty per V stage; q_full per half;
+    // s_full per half; p_full, pv_done per half and part; final per issuer
+    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 * 2 + 2 * 4 + 4;
+    static constexpr int kOffPlan = kOffBars + (kNumBars + 1) / 2 * 16;
+    static constexpr int kOffMisc = kOffPlan + (2 * (kMaxRounds + 1) + 2 * kThreads / 32) * 16;
     static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
+    // scratch of the planning, over the operands: the rounds' cuts, then the costs before the sequences
+    static constexpr int kOffPrefix = (kMaxRounds * kMaxPieces + 1) * 8;
+    static_assert(kOffPrefix + (kMaxBatchPerLaunch + 1) * 8 <= kOffCodes, "planning scratch");
     static constexpr uint32_t kColS = 0;    // S of half x: 128 x
     static constexpr uint32_t kColO = 256;  // O of half x: 256 + 128 x
     static constexpr uint32_t kTmemCols = 512;
@@ -115,35 +123,81 @@ __device__ __forceinline__ ChunkShape shape_of(const ChunkArgs& a) {
     return ChunkShape{a.lens, a.qstart, a.batch, a.kv_heads, a.group, a.max_blocks, a.max_query_len};
 }
 
-// Cost before each sequence (all threads, two sequences each; ends with __syncthreads).
-__device__ void sum_costs(const ChunkArgs& a, const ChunkShape& sh, int64_t* prefix, int64_t* warp_sum) {
+// Exclusive prefix sum over the block's threads (all threads; contains
+// __syncthreads, and scratch is free again after one more).
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* scratch) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t mine[2], sum = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = 2 * threadIdx.x + e;
-        mine[e] = 0;
-        if (i < a.batch) {
-            ChunkSeq q;
-            if (chunk_seq(sh, i, q))
-                mine[e] = chunk_head_cost(q, a.group) * a.kv_heads;
-            else if (blockIdx.x == 0)
-                atomicOr(a.status, PKV_DEVERR_RANGE);
-        }
-        sum += mine[e];
-    }
-    int64_t incl = sum;
+    int64_t incl = x;
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t other = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += other;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int64_t at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += warp_sum[w];
-    if (2 * threadIdx.x <= a.batch) prefix[2 * threadIdx.x] = at;
-    if (2 * threadIdx.x + 1 <= a.batch) prefix[2 * threadIdx.x + 1] = at + mine[0];
+    int64_t at = incl - x;
+    for (int w = 0; w < warp; ++w) at += scratch[w];
+    return at;
+}
+
+// This CTA's ranges (all threads; ends with __syncthreads): returns their number,
+// 0 for a CTA without work. prefix: cost before each sequence; ranges: two cuts per
+// range; at: scratch for the rounds' cuts and the CTAs' dues.
+template <int kThreads>
+__device__ int plan_ranges(const ChunkArgs& a, const ChunkShape& sh, int64_t* prefix, ChunkPos* ranges, int64_t* at, int64_t* scratch) {
+    const int t = threadIdx.x, grid = gridDim.x, cta = blockIdx.x;
+    // two sequences per thread
+    int64_t mine[2], most = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * t + e;
+        mine[e] = 0;
+        if (i < a.batch) {
+            ChunkSeq q;
+            if (!chunk_seq(sh, i, q) && cta == 0) atomicOr(a.status, PKV_DEVERR_RANGE);
+            mine[e] = chunk_head_cost(q, a.group) * a.kv_heads;
+            most = max(most, chunk_most(q, a.group));
+        }
+    }
+    const int64_t before = block_sum(mine[0] + mine[1], scratch);
+    if (2 * t <= a.batch) prefix[2 * t] = before;
+    if (2 * t + 1 <= a.batch) prefix[2 * t + 1] = before + mine[0];
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     __syncthreads();
+    if ((t & 31) == 0) scratch[t >> 5] = most;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) most = max(most, scratch[w]);
+    const int64_t total = prefix[a.batch];
+    const int ctas = chunk_ctas(total, a.group, grid);
+    if (total == 0 || cta >= ctas) return 0;
+    const ChunkRounds r = chunk_rounds(total, most, ctas);
+    int64_t from = 0, due0 = cta, due1 = cta + 1, all = ctas;
+    if (r.rounds > 0) {
+        for (int i = t; i <= r.rounds * ctas; i += kThreads) {
+            int64_t cost;
+            chunk_unit_cut(sh, prefix, static_cast<int64_t>(i) * r.piece, cost);
+            at[i] = cost;
+        }
+        __syncthreads();
+        from = at[r.rounds * ctas];
+        const int64_t left = t < ctas ? total / ctas - chunk_dealt(at, r, t, ctas) : 0;
+        const int64_t due = block_sum(left > 0 ? left : 0, scratch);
+        __syncthreads();
+        if (t == cta) at[0] = due;
+        if (t == cta + 1) at[1] = due;
+        if (t == kThreads - 1) at[2] = due;  // a thread without a CTA: the sum of all
+        __syncthreads();
+        due0 = at[0];
+        due1 = at[1];
+        all = at[2];
+    }
+    if (t < 2 * (r.rounds + 1)) {
+        int64_t cost;
+        const int k = t >> 1, e = t & 1;
+        ranges[t] = k < r.rounds ? chunk_unit_cut(sh, prefix, (static_cast<int64_t>(k) * ctas + cta + e) * r.piece, cost)
+                                 : chunk_rest_cut(sh, prefix, from, e ? due1 : due0, all, cta + e, ctas);
+    }
+    __syncthreads();
+    return r.rounds + 1;
 }
 
 // ---------------------------------------------------------------- conversions
@@ -175,15 +229,11 @@ __device__ __forceinline__ uint4 v_values(uint32_t w0, uint32_t w1, const uint4&
 }
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-// The exponent a segment takes from its first step's scales (bits of the largest and
-// smallest): the largest, or beside an infinity the smallest, goes to 1/2 .. 1.
-__device__ __forceinline__ int range_exponent(uint32_t most, uint32_t least) {
-    const uint32_t ref = most < 0x7f800000u ? most : (least < 0x7f800000u ? least : 0x3f800000u);
-    return max(-125, min(125, static_cast<int>(ref >> 23) - 126));
-}
-// Whether scales leave [2^(e - 14), 2^(e + 8)] (bits compare as the floats do).
-__device__ __forceinline__ bool leaves_range(uint32_t most, uint32_t least, int e) {
-    return least < static_cast<uint32_t>(max(e - 14, -126) + 127) << 23 || most > static_cast<uint32_t>(min(e + 8, 127) + 127) << 23;
+// The exponent that takes the largest of some scales (its bits; not an infinity) to 1/2 .. 1.
+__device__ __forceinline__ int range_exponent(uint32_t most) { return max(-125, min(125, static_cast<int>(most >> 23) - 126)); }
+// Whether a scale leaves [2^(e - 14), 2^(e + 8)] (bits compare as the floats do).
+__device__ __forceinline__ bool leaves_range(uint32_t scale, int e) {
+    return scale < static_cast<uint32_t>(max(e - 14, -126) + 127) << 23 || scale > static_cast<uint32_t>(min(e + 8, 127) + 127) << 23;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
@@ -194,20 +244,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// All `threads` of named barrier `id` meet; true if `ok` held for every one.
-__device__ __forceinline__ bool named_barrier_all(int id, int threads, bool ok) {
-    int r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.s32 p, %3, 0;\n\t"
-        "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-        "selp.s32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(threads), "r"(static_cast<int>(ok))
-        : "memory");
-    return r != 0;
-}
-
 // Eight scores of a slow step, scaled, -inf where the token is absent or not seen
 // (columns taddr .. taddr + 7, K factors c, row factor f, the first `seen` of them seen).
 __device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, float f, int seen, float (&x)[8]) {
@@ -218,39 +254,54 @@ __device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, floa
     for (int e = 0; e < 8; ++e)
         x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
-// mbar_wait by a whole warp, with one answer for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, abort));
+// mbar_wait that looks at the clock and the abort flag at every 64th probe only (the
+// probes share issue slots with the warps that are waited for).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, status, abort);
 }
+// wait by a whole warp, with one answer for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
+    return __all_sync(0xffffffffu, wait(bar, parity, status, abort));
+}
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- converters
-// K's (IsV false) or V's four warps: every step of the CTA's range, one load
-// ahead. Warp w takes tokens 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1), lane l
-// the scales of token 32 w + l. The range of the scales decides a step's mode and a
-// segment's exponents; both groups read V's scales and decide alike.
+// K's (IsV false) or V's four warps: every step of the CTA's range. Warp w takes
+// tokens 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1), lane l the scales of
+// token 32 w + l. A lane copies the codes of the next step into its own slots of
+// shared memory as it takes the current ones out of them (asynchronous copies: a
+// step's time ahead, and no registers). The loops stay rolled: the warps of the four
+// roles on a scheduler share an instruction cache that their unrolled bodies
+// overflow. A warp decides by itself whether its tokens are taken as bare codes; both
+// groups read V's scales and decide alike.
 template <int D, bool IsV>
-__device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* smem, const int64_t* prefix,
-                             const ChunkPos* plan, ChunkPos* after, uint64_t* full, uint64_t* empty,
-                             volatile int* abort_flag) {
+__device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* smem, const ChunkPos* ranges, int count,
+                             ChunkWalk* where, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
     using C = Cx<D>;
     const int lane = threadIdx.x & 31;
     const int cw = (threadIdx.x >> 5) & 3;
-    constexpr int kVecs = 32 * D / 16 / 32;    // 16-code vectors per lane and step
-    constexpr int kPerBlock = kVecs / 2;       // of them in each of the warp's two blocks
+    constexpr int kPerBlock = C::kVecs / 2;    // vectors of a lane in each of the warp's two blocks
     constexpr int kLanes = D / 16;             // lanes that hold one token's K row
     constexpr int kBlockVecs = D;              // vectors of one (block, head)
-    constexpr int kBarrier = IsV ? 2 : 1;
     const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes);
-    uint32_t (*reduce)[4][8] = reinterpret_cast<uint32_t (*)[4][8]>(smem + C::kOffReduce + (IsV ? 256 : 0));
+    uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
 
-    // the segment being loaded (the position after it: in shared memory, one per warp, read once per segment)
-    if (lane == 0) *after = plan[0];
+    // the segment being loaded (the walk past it: in shared memory, one per warp, read once per segment)
+    if (lane == 0) *where = chunk_begin(ranges);
     __syncwarp();
     int step = 0, last = 0;         // next step to load, one past the segment's last
     int n = 0, head = 0;            // its tokens, KV head
     const int32_t* trow = nullptr;  // its block table
     int ids = 0, ids_next = 0;      // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
-    bool opens = false;             // the loaded step is its segment's first
+    int ev = 0, ek = 0;             // its E and F
     auto id_at = [&](int b) {
         if (b >= (n + 15) / 16) return -1;
         const int id = __ldg(trow + b);
@@ -260,10 +311,10 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
     };
     auto open = [&]() {
         ChunkSegment g;
-        const ChunkPos cur = *after;
+        ChunkWalk walk = *where;
         __syncwarp();
-        if (!chunk_segment(sh, cur, plan[1], g)) return false;
-        if (lane == 0) *after = chunk_after(sh, prefix, g);
+        if (!chunk_walk(sh, ranges, count, walk, g)) return false;
+        if (lane == 0) *where = walk;
         __syncwarp();
         step = g.at.s;
         last = g.s1;
@@ -272,24 +323,25 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
         trow = a.tables + static_cast<int64_t>(g.at.seq) * a.max_blocks;
         ids = id_at(32 * (step >> 2) + lane);
         ids_next = id_at(32 * (step >> 2) + 32 + lane);
-        opens = true;
+        // E and F from the scales of the first block's tokens (K's in lanes 0-15, V's in 16-31)
+        const int id = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
+        const uint32_t x = __float_as_uint(__ldg(a.scales + (static_cast<int64_t>(id) * a.kv_heads + head) * 32 + lane)) & 0x7fffffffu;
+        const bool use = x < 0x7f800000u && step * kChunkStep + (lane & 15) < n;
+        ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
+        ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
         return true;
     };
-    // the loaded step: codes; scales of the lane's token, whether it exists or lies in a block outside the pool
-    uint4 w[kVecs];
+    // where the step's two blocks lie; the scales of the lane's token, whether it
+    // exists or lies in a block outside the pool
+    const uint4 *src0 = nullptr, *src1 = nullptr;
     float ks = 0.f, vs = 0.f;
     bool present = false, missing = false;
-    auto load = [&]() {
+    auto find = [&]() {
         const int b0 = (step & 3) * 8 + 2 * cw;
         const int id0 = __shfl_sync(0xffffffffu, ids, b0), id1 = __shfl_sync(0xffffffffu, ids, b0 + 1);
         // an absent block's codes may be any (its tokens carry no weight): block 0 exists
-        const uint4* src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
-        const uint4* src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
-#pragma unroll
-        for (int i = 0; i < kPerBlock; ++i) {
-            w[i] = __ldg(src0 + 32 * i);
-            w[kPerBlock + i] = __ldg(src1 + 32 * i);
-        }
+        src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
+        src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
         const int id = lane < 16 ? id0 : id1;
         present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
         missing = id == -2;
@@ -297,118 +349,100 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
         if (!IsV) ks = __ldg(rec);
         vs = __ldg(rec + 16);
     };
-    // moves on to the next step, if there is one, and loads it
-    auto advance = [&]() {
-        opens = false;
+
+    bool live = open();
+    if (live) {
+        find();
+#pragma unroll 1
+        for (int i = 0; i < C::kVecs; ++i)
+            copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
+    }
+    copy_commit();
+    for (int it = 0; live; ++it) {
+        // this warp's stage: K's of the step, V's of the half that holds its tokens
+        const int part = 2 * it + (cw >> 1);
+        const int st = IsV ? part % C::kParts : it & 1;
+        const uint32_t parity = static_cast<uint32_t>((IsV ? part / C::kParts : it >> 1) & 1) ^ 1u;
+        if (!warp_wait(&empty[st], parity, a.status, abort_flag)) break;
+        // ---- the lane's token: its factor, and what the softmax needs
+        const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
+        const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
+        __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 32 * cw;
+        uint32_t pair = 0;  // K: (hi, lo) of the factor
+        if (IsV) {
+            factors[lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
+        } else {
+            const bool bare_k = __any_sync(0xffffffffu, present && leaves_range(__float_as_uint(ks) & 0x7fffffffu, ek));
+            const bool slow = bare_k || bare_v || __any_sync(0xffffffffu, missing);
+            float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
+            if (lane == 0) {
+                if (cw == 0) *reinterpret_cast<float2*>(tab) = make_float2(exp2_int(ev), exp2_int(ek));
+                reinterpret_cast<uint8_t*>(tab)[8 + cw] = slow;
+            }
+            tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
+            float lack = 0.f;
+            // (a scale below the normal range counts as its smallest number)
+            if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
+            tab[4 + 128 + 32 * cw + lane] = lack;
+            const float factor = !present ? 0.f : bare_k ? 1.f : ks * exp2_int(-ek);
+            const __half hi = __float2half(factor);
+            pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));
+        }
+        // ---- move on to the next step, if there is one; its scales are on their way during the conversion
         if (++step >= last) {
-            if (!open()) return false;
+            live = open();
         } else if ((step & 3) == 0) {
             ids = ids_next;
             ids_next = id_at(32 * (step >> 2) + 32 + lane);
         }
-        load();
-        return true;
-    };
-
-    bool live = open();
-    if (live) load();
-    int ev = 0, ek = 0;  // E and F of the segment
-    bool have = false;   // they are set
-    for (int it = 0; live; ++it) {
-        const int st = it & 1;
-        if (opens) have = false;
-        // ---- range of the scales of the tokens that exist; absent tokens
-        const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-        const uint32_t kbits = __float_as_uint(ks) & 0x7fffffffu;
-        {
-            const uint32_t vm = __reduce_max_sync(0xffffffffu, present ? vbits : 0u);
-            const uint32_t vl = __reduce_min_sync(0xffffffffu, present ? vbits : 0xffffffffu);
-            if (lane == 0) *reinterpret_cast<uint2*>(&reduce[st][cw][0]) = make_uint2(vm, vl);
-            if (!IsV) {
-                const uint32_t km = __reduce_max_sync(0xffffffffu, present ? kbits : 0u);
-                const uint32_t kl = __reduce_min_sync(0xffffffffu, present ? kbits : 0xffffffffu);
-                const uint32_t miss = __any_sync(0xffffffffu, missing);
-                if (lane == 0) *reinterpret_cast<uint4*>(&reduce[st][cw][4]) = make_uint4(km, kl, miss, 0u);
-            }
-        }
-        const bool go = mbar_wait(&empty[st], static_cast<uint32_t>((it >> 1) & 1) ^ 1u, a.status, abort_flag);
-        if (!named_barrier_all(kBarrier, C::kConverters, go)) break;
-        uint32_t vmax = 0, vmin = 0xffffffffu, kmax = 0, kmin = 0xffffffffu, miss = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 r = *reinterpret_cast<const uint2*>(&reduce[st][i][0]);
-            vmax = max(vmax, r.x);
-            vmin = min(vmin, r.y);
-            if (!IsV) {
-                const uint4 t = *reinterpret_cast<const uint4*>(&reduce[st][i][4]);
-                kmax = max(kmax, t.x);
-                kmin = min(kmin, t.y);
-                miss |= t.z;
-            }
-        }
-        bool wide = false, slow = miss != 0;
-        if (vmin != 0xffffffffu) {
-            if (!have) {  // the segment's first step with tokens
-                ev = range_exponent(vmax, vmin);
-                if (!IsV) ek = range_exponent(kmax, kmin);
-                have = true;
-            }
-            wide = leaves_range(vmax, vmin, ev);
-            if (!IsV) slow |= wide || leaves_range(kmax, kmin, ek);
-        }
+        if (live) find();
+        copy_wait_all();
+        __syncwarp();  // the factors too
         if (IsV) {
-            __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 128 * st + 32 * cw;
-            factors[lane] = __float2half(!present ? 0.f : wide ? 1.f : vs * exp2_int(-ev));
-            __syncwarp();
             // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
-            uint8_t* vd = smem + C::kOffV + st * C::kVBytes + (cw >> 1) * C::kVPartBytes + lane * 128;
-#pragma unroll
+            uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
+#pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * b);
                 const uint4 f0 = f[0], f1 = f[1];
-                const int c0 = ((2 * cw + b) & 3) * 2;
-#pragma unroll
+                const uint32_t c0 = (((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4);
+                const uint4* src = b ? src1 : src0;
+#pragma unroll 2
                 for (int i = 0; i < kPerBlock; ++i) {
-                    const uint4& x = w[b * kPerBlock + i];
-                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + ((c0 ^ (lane & 7)) << 4)) = v_values(x.x, x.y, f0);
-                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + (((c0 + 1) ^ (lane & 7)) << 4)) = v_values(x.z, x.w, f1);
+                    uint8_t* slot = mine + (b * kPerBlock + i) * 512;
+                    const uint4 x = *reinterpret_cast<const uint4*>(slot);
+                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + c0) = v_values(x.x, x.y, f0);
+                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + (c0 ^ 16)) = v_values(x.z, x.w, f1);
+                    if (live) copy16_async(smem_u32(slot), src + 32 * i);
                 }
             }
         } else {
-            float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
-            if (cw == 0 && lane == 0)
-                *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), slow ? 1.f : 0.f, 0.f);
-            if (slow) {
-                tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : present ? ks : 0.f;
-                // a scale below the normal range counts as its smallest number
-                tab[4 + 128 + 32 * cw + lane] = present && wide ? log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev) : 0.f;
-            }
-            const float factor = !present ? 0.f : slow ? 1.f : ks * exp2_int(-ek);
-            const __half hi = __float2half(factor);
-            const uint32_t pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));  // (hi, lo) of the lane's token
             // ---- token rows: vector i of a lane lies in row 32 cw + i * (32 / kLanes) + lane / kLanes
             const int ch = lane % kLanes, sub = lane / kLanes;
             // lanes of the second column part write their halves in the other order: no bank is hit twice
             const int flip = ch >> 2;
             uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
             const int c0 = (ch & 3) * 2 + flip;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                // (the row modulo 8 alternates between two values at head_dim 128)
+#pragma unroll 2
+            for (int i = 0; i < C::kVecs; ++i) {
                 const int row8 = (i * (32 / kLanes) + sub) & 7;
                 const uint32_t f = __shfl_sync(0xffffffffu, pair, i * (32 / kLanes) + sub);
                 const __half2 fh = half2_of(__byte_perm(f, f, 0x1010)), fl = half2_of(__byte_perm(f, f, 0x3232));
-                const uint4 x0 = k_values(w[i].x, w[i].y, fh, fl), x1 = k_values(w[i].z, w[i].w, fh, fl);
+                uint8_t* slot = mine + i * 512;
+                const uint4 x = *reinterpret_cast<const uint4*>(slot);
+                const uint4 x0 = k_values(x.x, x.y, fh, fl), x1 = k_values(x.z, x.w, fh, fl);
                 uint8_t* rowp = kd + i * (32 / kLanes) * 128;
                 *reinterpret_cast<uint4*>(rowp + ((c0 ^ row8) << 4)) = flip ? x1 : x0;
                 *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = flip ? x0 : x1;
+                if (live) copy16_async(smem_u32(slot), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
             }
         }
+        copy_commit();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
-        live = advance();
     }
+    copy_wait_all();
 }
 
 template <int D>
@@ -419,14 +453,14 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
     uint64_t* k_empty = k_full + C::kStages;
     uint64_t* v_full = k_empty + C::kStages;
-    uint64_t* v_empty = v_full + C::kStages;
-    uint64_t* q_full = v_empty + C::kStages;  // [half]: Q rows in place
+    uint64_t* v_empty = v_full + C::kParts;
+    uint64_t* q_full = v_empty + C::kParts;  // [half]: Q rows in place
     uint64_t* s_full = q_full + 2;            // [half]: scores in tensor memory
     uint64_t* p_full = s_full + 2;            // [half][part]: weights written
     uint64_t* pv_done = p_full + 4;           // [half][part]: that product has completed
     uint64_t* final_bar = pv_done + 4;        // [issuer]: everything it issued has completed
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::kOffPrefix);
-    ChunkPos* plan = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // [0] first position, [1] end, [2 + warp] where a warp is
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::kOffPrefix);  // while planning
+    ChunkPos* ranges = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // two cuts per range
     int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + C::kThreads / 32 * 8);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kThreads / 32 * 8 + 4);
@@ -437,7 +471,9 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&k_full[s], C::kConverters / 32);
             mbar_init(&k_empty[s], 2);  // both score issuers
-            mbar_init(&v_full[s], C::kConverters / 32);
+        }
+        for (int s = 0; s < C::kParts; ++s) {
+            mbar_init(&v_full[s], 2);   // the two warps that hold its tokens
             mbar_init(&v_empty[s], 2);  // both value issuers
         }
         for (int x = 0; x < 2; ++x) {
@@ -455,19 +491,19 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     grid_dependency_wait();  // lengths, tables, codes and the workspace may come from the kernel before
     allow_dependents();
     const ChunkShape sh = shape_of(a);
-    sum_costs(a, sh, prefix, warp_sum);
-    const int ctas = chunk_ctas(prefix[a.batch], a.group, grid);
-    if (lane == 0 && warp < 2) plan[warp] = chunk_cut(sh, prefix, static_cast<int>(blockIdx.x) + warp, ctas);
-    __syncthreads();
-    const ChunkPos first = plan[0], end = plan[1];
+    const int count = plan_ranges<C::kThreads>(a, sh, prefix, ranges, reinterpret_cast<int64_t*>(smem), warp_sum);
     PieceInfo* info = static_cast<PieceInfo*>(a.workspace) + blockIdx.x;
-    if (first == end || first.seq >= a.batch) {  // nothing here
+    ChunkWalk walk;
+    ChunkSegment g;
+    if (count > 0) walk = chunk_begin(ranges);
+    if (count == 0 || !chunk_walk(sh, ranges, count, walk, g)) {  // nothing here
         if (threadIdx.x == 0) {
-            info->start = first;
+            info->start = count > 0 ? ranges[2 * count - 2] : ChunkPos{a.batch, 0, 0, 0};
             info->flags = 0;
         }
         return;
     }
+    walk = chunk_begin(ranges);
     if (warp == C::kScoreWarp) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
@@ -491,10 +527,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         int table = 0;   // steps of the CTA
         int flags = 0;
         bool ok = true;
-        ChunkPos cur = first;
-        ChunkSegment g;
-        while (ok && chunk_segment(sh, cur, end, g)) {
-            cur = chunk_after(sh, prefix, g);
+        while (ok && chunk_walk(sh, ranges, count, walk, g)) {
             const int h = g.at.head;
             const int r0 = g.at.tile * kChunkRows + 128 * x;
             const int rows = g.q.nq * a.group - r0;  // rows of the half, if positive
@@ -510,13 +543,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             float row_f = 0.f;  // |scale| log2(e) over the power of two in q'
             {
                 const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D);
-                uint4 v[D / 8];
                 uint32_t top = 0;  // largest |q|, per half word
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    v[c] = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
-                                                 __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+                    const uint4 v = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
                 // the row's largest goes to 2^14 .. 2^15 (a row with infinities is left as it is);
                 // the scale's sign goes into q', a zero scale makes q' zero
@@ -527,10 +558,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 uint8_t* qs = smem + C::kOffQ + x * C::kTileBytes + rr * 128;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    const uint4 h = make_uint4(pack_f16x2(bf16lo_to_f32(v[c].x) * mul, bf16hi_to_f32(v[c].x) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v[c].y) * mul, bf16hi_to_f32(v[c].y) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v[c].z) * mul, bf16hi_to_f32(v[c].z) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v[c].w) * mul, bf16hi_to_f32(v[c].w) * mul));
+                    const uint4 v = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 h = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * mul, bf16hi_to_f32(v.x) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v.y) * mul, bf16hi_to_f32(v.y) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v.z) * mul, bf16hi_to_f32(v.z) * mul),
+                                               pack_f16x2(bf16lo_to_f32(v.w) * mul, bf16hi_to_f32(v.w) * mul));
                     *reinterpret_cast<uint4*>(qs + (c >> 3) * C::kPartBytes + (((c & 7) ^ (rr & 7)) << 4)) = h;
                 }
                 fence_proxy_async_smem();
@@ -548,19 +580,41 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes);
                 const float4 modes = *reinterpret_cast<const float4*>(tab);
                 unit = modes.x;
-                const bool plain = modes.z == 0.f;
+                const bool plain = __float_as_uint(modes.z) == 0u;
                 // never 0 or infinite: a hidden score is -inf times it
                 const float f = plain ? fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f) : row_f;
                 const int seen = lim - (g.at.s + j) * kChunkStep + 1;  // tokens of the step the row sees
                 const bool masked = (g.at.s + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    const float* cp = tab + 4 + 64 * part;  // of a slow step
                     const int seen_part = seen - 64 * part;
                     const uint32_t col = col_s + 64 * part;
-                    float sx[64];
-                    float mx;
+                    // O takes on another maximum (every lane its own factor; all lanes take part)
+                    auto rescale = [&](float mx) {
+                        float alpha = 1.f;
+                        if (mx > m + 8.f || (mx > m && m == ninf())) {
+                            alpha = m == ninf() ? 0.f : ex2(m - mx);
+                            m = mx;
+                            l *= alpha;
+                        }
+                        // O holds something once a part of this segment has been multiplied in;
+                        // part 0: the products of the step before completed ahead of these scores
+                        if (j + part == 0) return true;
+                        if (part == 1 && !warp_wait(&pv_done[2 * x], it & 1, a.status, abort_flag)) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t ov[16];
+                            tmem_ld16(col_o + c, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            tmem_st16(col_o + c, ov);
+                        }
+                        return true;
+                    };
                     if (plain) {
+                        float sx[64];
                         {
                             uint32_t lo[32], hi[32];
                             tmem_ld32(col, lo);
@@ -577,61 +631,32 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             for (int e = 0; e < 64; ++e)
                                 if (e >= seen_part) sx[e] = ninf();
                         }
-                        float m1[21];
-#pragma unroll
-                        for (int k = 0; k < 21; ++k) m1[k] = fmax3(sx[3 * k], sx[3 * k + 1], sx[3 * k + 2]);
-#pragma unroll
-                        for (int k = 0; k < 7; ++k) m1[k] = fmax3(m1[3 * k], m1[3 * k + 1], m1[3 * k + 2]);
-                        mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63])) * f;
-                    } else {
-                        mx = ninf();
+                        // Weights with the maximum as it stands; their sum tells whether it has
+                        // to move (the part is then done again): no pass over the scores for it.
+                        uint32_t pw[32];
+                        float sum;
+                        bool first = __any_sync(0xffffffffu, m == ninf() && seen_part > 0);
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 8) {
-                            float xe[8];
-                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
+                        for (int pass = 0;; ++pass) {
+                            if (first || pass > 0) {
+                                float m1[21];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
-                        }
-                    }
-                    const bool resc = mx > m + 8.f;
-                    // O holds something once a part of this segment has been multiplied in
-                    if (__any_sync(0xffffffffu, resc)) {
-                        float alpha = 1.f;
-                        if (resc) {
-                            const float mn = fmaxf(m, mx);
-                            alpha = m == ninf() ? 0.f : ex2(m - mn);
-                            m = mn;
-                            l *= alpha;
-                        }
-                        if (j + part > 0) {
-                            // part 0: the products of the step before completed ahead of these scores
-                            if (part == 1 && !warp_wait(&pv_done[2 * x], it & 1, a.status, abort_flag)) {
-                                ok = false;
-                                break;
+                                for (int k = 0; k < 21; ++k) m1[k] = fmax3(sx[3 * k], sx[3 * k + 1], sx[3 * k + 2]);
+#pragma unroll
+                                for (int k = 0; k < 7; ++k) m1[k] = fmax3(m1[3 * k], m1[3 * k + 1], m1[3 * k + 2]);
+                                const float mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63])) * f;
+                                if (!rescale(mx)) {
+                                    ok = false;
+                                    break;
+                                }
                             }
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t ov[16];
-                                tmem_ld16(col_o + c, ov);
-                                tmem_ld_wait();
+                            const float base = m == ninf() ? 0.f : m;
+                            const uint64_t nb2 = f32x2_pack(-base, -base), f2 = f32x2_pack(f, f);
+                            uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                                tmem_st16(col_o + c, ov);
-                            }
-                        }
-                    }
-                    const float base = m == ninf() ? 0.f : m;
-                    if (plain) {
-                        const uint64_t nb2 = f32x2_pack(-base, -base), f2 = f32x2_pack(f, f);
-                        uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t pw[16];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
+                            for (int e = 0; e < 64; e += 2) {
                                 float a0, a1;
-                                f32x2_unpack(f32x2_fma(f32x2_pack(sx[32 * half + e], sx[32 * half + e + 1]), f2, nb2), a0, a1);
+                                f32x2_unpack(f32x2_fma(f32x2_pack(sx[e], sx[e + 1]), f2, nb2), a0, a1);
                                 const float p0 = ex2(a0), p1 = ex2(a1);
                                 pw[e / 2] = pack_f16x2(p0, p1);
                                 if ((e / 2) & 1)
@@ -639,12 +664,30 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 else
                                     acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
                             }
-                            tmem_st16(col_s + 32 * part + 16 * half, pw);
+                            float s0, s1;
+                            f32x2_unpack(f32x2_add(acc0, acc1), s0, s1);
+                            sum = s0 + s1;
+                            // above 2^14 (or not a number) a weight may have left f16
+                            if (first || pass > 0 || !__any_sync(0xffffffffu, !(sum <= 16384.f))) break;
                         }
-                        float s0, s1;
-                        f32x2_unpack(f32x2_add(acc0, acc1), s0, s1);
-                        l += s0 + s1;
+                        if (!ok) break;
+                        l += sum;
+                        tmem_st32(col_s + 32 * part, pw);
                     } else {
+                        const float* cp = tab + 4 + 64 * part;
+                        float mx = ninf();
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 8) {
+                            float xe[8];
+                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
+                        }
+                        if (__any_sync(0xffffffffu, mx > m + 8.f) && !rescale(mx)) {
+                            ok = false;
+                            break;
+                        }
+                        const float base = m == ninf() ? 0.f : m;
                         // the weights overwrite scores that have been read
 #pragma unroll 1
                         for (int c = 0; c < 64; c += 8) {
@@ -719,16 +762,16 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             tc_fence_before();  // the next segment's products overwrite O after this half's next arrival
         }
         if (threadIdx.x == 0) {  // half A takes part in every segment
-            info->start = first;
+            info->start = ranges[2 * count - 2];
             info->flags = ok ? flags : 0;
         }
     } else if (warp < C::kScoreWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ChunkPos* after = plan + 2 + warp;  // every warp its own
+        ChunkWalk* where = reinterpret_cast<ChunkWalk*>(ranges + 2 * (kMaxRounds + 1) + 2 * warp);  // every warp its own
         if (warp < C::kConvertWarp + 4)
-            convert_role<D, false>(a, sh, smem, prefix, plan, after, k_full, k_empty, abort_flag);
+            convert_role<D, false>(a, sh, smem, ranges, count, where, k_full, k_empty, abort_flag);
         else
-            convert_role<D, true>(a, sh, smem, prefix, plan, after, v_full, v_empty, abort_flag);
+            convert_role<D, true>(a, sh, smem, ranges, count, where, v_full, v_empty, abort_flag);
     } else if (warp < C::kValueWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         // ------------------------------------------------ scores S = Q K^T of half x (one thread)
@@ -738,22 +781,19 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
             int step = 0, it = 0, segs = 0;
             bool ok = true;
-            ChunkPos cur = first;
-            ChunkSegment g;
-            while (ok && chunk_segment(sh, cur, end, g)) {
-                cur = chunk_after(sh, prefix, g);
+            while (ok && chunk_walk(sh, ranges, count, walk, g)) {
                 const bool mine = g.q.nq * a.group - g.at.tile * kChunkRows > 128 * x;
                 if (mine) {
-                    if (!mbar_wait(&q_full[x], segs & 1, a.status, abort_flag)) break;
+                    if (!wait(&q_full[x], segs & 1, a.status, abort_flag)) break;
                     ++segs;
                 }
                 for (int j = g.at.s; j < g.s1; ++j, ++step) {
                     const int st = step & 1;
-                    if (mine && it > 0 && !mbar_wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status, abort_flag)) {
+                    if (mine && it > 0 && !wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    if (!mbar_wait(&k_full[st], (step >> 1) & 1, a.status, abort_flag)) {
+                    if (!wait(&k_full[st], (step >> 1) & 1, a.status, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -785,41 +825,43 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         const int x = warp - C::kValueWarp;
         if (lane == 0) {
             constexpr uint32_t idO = umma_idesc_f16(128, D);
-            int step = 0, it = 0;
+            int st = 0, it = 0;
+            uint32_t phase = 0;
             bool ok = true;
-            ChunkPos cur = first;
-            ChunkSegment g;
-            while (ok && chunk_segment(sh, cur, end, g)) {
-                cur = chunk_after(sh, prefix, g);
+            while (ok && chunk_walk(sh, ranges, count, walk, g)) {
                 const bool mine = g.q.nq * a.group - g.at.tile * kChunkRows > 128 * x;
-                for (int j = g.at.s; ok && j < g.s1; ++j, ++step) {
-                    const int st = step & 1;
-                    if (!mbar_wait(&v_full[st], (step >> 1) & 1, a.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mine) {
-                        mbar_arrive(&v_empty[st]);
-                        continue;
-                    }
-                    const uint32_t v_base = smem_u32(smem + C::kOffV + st * C::kVBytes);
+                for (int j = g.at.s; ok && j < g.s1; ++j) {
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
-                        if (!mbar_wait(&p_full[2 * x + part], it & 1, a.status, abort_flag)) {
+                        const int now = st;
+                        const uint32_t parity = phase;
+                        if (++st == C::kParts) {
+                            st = 0;
+                            phase ^= 1u;
+                        }
+                        if (!wait(&v_full[now], parity, a.status, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!mine) {
+                            mbar_arrive(&v_empty[now]);
+                            continue;
+                        }
+                        if (!wait(&p_full[2 * x + part], it & 1, a.status, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                        const uint32_t v_base = smem_u32(smem + C::kOffV + now * C::kVPartBytes);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 32 * part + 8 * kk,
-                                         umma_desc_sw128(v_base + part * C::kVPartBytes + kk * 32, 16, 1024), idO,
+                                         umma_desc_sw128(v_base + kk * 32, 16, 1024), idO,
                                          (j > g.at.s || part > 0 || kk > 0) ? 1u : 0u);
                         umma_commit(&pv_done[2 * x + part]);
+                        umma_commit(&v_empty[now]);
                     }
-                    if (!ok) break;
-                    umma_commit(&v_empty[st]);
-                    ++it;
+                    if (mine) ++it;
                 }
             }
             umma_commit(&final_bar[2 + x]);
@@ -841,7 +883,6 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 // 32 y .. 32 y + 31, a warp per row: out = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
 constexpr int kCombineRows = 32;
 constexpr int kCombineThreads = 256;
-constexpr int kMaxPieces = 1024;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const ChunkArgs a, int grid) {

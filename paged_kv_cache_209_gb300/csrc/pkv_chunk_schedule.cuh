@@ -3,10 +3,17 @@
 // A unit is a tile of 256 query rows of one (sequence, KV head): rows
 // r = t G + g, query t and query head g of the KV head's group of G. It takes
 // ns steps of 128 tokens, up to the last token its last row sees. Units are
-// ordered sequence-major, then head, then tile; a launch gives CTA c of C the
-// steps between the cuts c and c + 1, placed by cost, so every CTA works about
-// equally long whatever the mix of contexts, chunks and causal limits. A cut
-// inside a unit leaves pieces that a second kernel combines.
+// ordered sequence-major, then head, then tile.
+//
+// A launch of C CTAs first deals whole units in `rounds` rounds: in round r, CTA c
+// takes the units that begin in piece r C + c of the cost axis, each piece as long
+// as the costliest unit. CTAs that run at the same time then work on neighbouring
+// units, the tiles of a few (sequence, KV head) pairs, whose K and V stay in L2:
+// dealt one contiguous range per CTA instead, the pairs of a large batch are all
+// read at once and evict one another (DRAM reads 7 times the cache's bytes on 8
+// sequences of 8192 tokens). The rest of the axis, one to two units per CTA, is
+// cut by steps so that every CTA's total comes out even; a unit that a cut
+// divides leaves pieces, which a second kernel joins. Small launches have no rounds.
 //
 // Cost of tile t of a sequence with n tokens, nq of them new: about the tokens
 // it sees plus a start-up worth kOverTokens, in units of 64 / G tokens, linear in
@@ -32,6 +39,7 @@ constexpr int kChunkRows = 256;   // query rows of a unit
 constexpr int kChunkStep = 128;   // tokens of a step
 constexpr int kOverTokens = 192;  // start-up of a unit (Q, the pipeline's fill, the output) in tokens
 constexpr int kMinPiece = 2;      // a cut leaves at least this many steps on either side
+constexpr int kMaxRounds = 8;     // rounds of whole units, at most
 constexpr int kMinSteps = 3;      // a CTA gets at least about this many two-half steps' cost
 
 struct ChunkShape {
@@ -86,22 +94,28 @@ PKV_HD inline int64_t chunk_head_cost(const ChunkSeq& q, int group) {
     return chunk_cost_before(base, tiles - 1) + chunk_tile_cost(q, group, base, tiles - 1, tiles);
 }
 
-// The next unit after `p` (prefix: cost before each sequence, [batch + 1]).
-PKV_HD inline ChunkPos chunk_next_unit(const ChunkShape& a, const int64_t* prefix, ChunkPos p, int tiles) {
+// The next unit after `p` of `tiles` in its head.
+PKV_HD inline ChunkPos chunk_next_unit(const ChunkShape& a, ChunkPos p, int tiles) {
     p.s = 0;
     if (++p.tile < tiles) return p;
     p.tile = 0;
     if (++p.head < a.kv_heads) return p;
     p.head = 0;
+    ChunkSeq q;
     do ++p.seq;
-    while (p.seq < a.batch && prefix[p.seq + 1] == prefix[p.seq]);
+    while (p.seq < a.batch && (!chunk_seq(a, p.seq, q) || q.nq == 0));
     return p;
 }
 
-// The position at cost x.
-PKV_HD inline ChunkPos chunk_locate(const ChunkShape& a, const int64_t* prefix, int64_t x) {
-    ChunkPos p{a.batch, 0, 0, 0};
-    if (x >= prefix[a.batch]) return p;
+// The unit at cost x, 0 <= x < total (prefix: cost before each sequence, [batch + 1]).
+struct ChunkPlace {
+    ChunkPos unit;
+    int64_t rem;         // x less the cost before the unit
+    int64_t cost;        // of the unit
+    int ns, tiles;       // its steps, the tiles of its head
+};
+PKV_HD inline ChunkPlace chunk_locate(const ChunkShape& a, const int64_t* prefix, int64_t x) {
+    ChunkPlace p;
     int lo = 0, hi = a.batch - 1;  // the last sequence whose cost begins at or before x
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -110,43 +124,94 @@ PKV_HD inline ChunkPos chunk_locate(const ChunkShape& a, const int64_t* prefix, 
         else
             hi = mid - 1;
     }
-    p.seq = lo;
     ChunkSeq q;
     chunk_seq(a, lo, q);
     const int64_t head_cost = chunk_head_cost(q, a.group);
-    int64_t rem = x - prefix[lo];
-    p.head = static_cast<int>(rem / head_cost);
-    rem -= p.head * head_cost;
-    const int tiles = chunk_tiles(q, a.group);
     const int64_t base = chunk_cost_base(q, a.group);
-    lo = 0, hi = tiles - 1;
+    p.unit = ChunkPos{lo, 0, 0, 0};
+    p.rem = x - prefix[lo];
+    p.unit.head = static_cast<int>(p.rem / head_cost);
+    p.rem -= p.unit.head * head_cost;
+    p.tiles = chunk_tiles(q, a.group);
+    lo = 0, hi = p.tiles - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (chunk_cost_before(base, mid) <= rem)
+        if (chunk_cost_before(base, mid) <= p.rem)
             lo = mid;
         else
             hi = mid - 1;
     }
-    p.tile = lo;
-    rem -= chunk_cost_before(base, lo);
-    const int ns = chunk_steps(q, a.group, lo);
-    p.s = static_cast<int>(rem * ns / chunk_tile_cost(q, a.group, base, lo, tiles));
-    if (p.s < kMinPiece)
-        p.s = 0;
-    else if (ns - p.s < kMinPiece)
-        p = chunk_next_unit(a, prefix, p, tiles);
+    p.unit.tile = lo;
+    p.rem -= chunk_cost_before(base, lo);
+    p.cost = chunk_tile_cost(q, a.group, base, lo, p.tiles);
+    p.ns = chunk_steps(q, a.group, lo);
     return p;
 }
+// The cut between steps at cost x.
+PKV_HD inline ChunkPos chunk_step_cut(const ChunkShape& a, const int64_t* prefix, int64_t x) {
+    if (x >= prefix[a.batch]) return ChunkPos{a.batch, 0, 0, 0};
+    ChunkPlace p = chunk_locate(a, prefix, x);
+    p.unit.s = static_cast<int>(p.rem * p.ns / p.cost);
+    if (p.unit.s < kMinPiece)
+        p.unit.s = 0;
+    else if (p.ns - p.unit.s < kMinPiece)
+        p.unit = chunk_next_unit(a, p.unit, p.tiles);
+    return p.unit;
+}
+// The cut between units nearest to cost x, and the cost before it.
+PKV_HD inline ChunkPos chunk_unit_cut(const ChunkShape& a, const int64_t* prefix, int64_t x, int64_t& at) {
+    at = prefix[a.batch];
+    if (x >= at) return ChunkPos{a.batch, 0, 0, 0};
+    ChunkPlace p = chunk_locate(a, prefix, x);
+    at = x - p.rem;
+    if (2 * p.rem < p.cost) return p.unit;
+    at += p.cost;
+    return chunk_next_unit(a, p.unit, p.tiles);
+}
 
-// CTAs (of `grid`) that get work, and the cut before CTA c of them.
+// CTAs (of `grid`) that get work.
 PKV_HD inline int chunk_ctas(int64_t total, int group, int grid) {
     const int64_t most = total / (static_cast<int64_t>(kMinSteps) * 2 * kChunkStep * group / 64);
     return most >= grid ? grid : (most < 1 ? 1 : static_cast<int>(most));
 }
-PKV_HD inline ChunkPos chunk_cut(const ChunkShape& a, const int64_t* prefix, int c, int ctas) {
-    const int64_t total = prefix[a.batch];
+// Costliest unit of a sequence.
+PKV_HD inline int64_t chunk_most(const ChunkSeq& q, int group) {
+    const int tiles = chunk_tiles(q, group);
+    if (tiles == 0) return 0;
+    const int64_t base = chunk_cost_base(q, group);
+    const int64_t last = chunk_tile_cost(q, group, base, tiles - 1, tiles);
+    const int64_t before = tiles > 1 ? chunk_tile_cost(q, group, base, tiles - 2, tiles) : 0;
+    return last > before ? last : before;
+}
+// Rounds of whole units, and the length of their pieces: a multiple of the
+// costliest unit, so that units of one size are dealt evenly. At least three
+// quarters of such a unit per CTA are left to even the totals out.
+struct ChunkRounds {
+    int rounds;
+    int64_t piece;
+};
+PKV_HD inline ChunkRounds chunk_rounds(int64_t total, int64_t most, int ctas) {
+    const int64_t share = total / ctas - most * 3 / 4;
+    ChunkRounds r{0, most};
+    if (share < most) return r;
+    const int64_t n = share / most;
+    r.rounds = static_cast<int>(n < kMaxRounds ? n : kMaxRounds);
+    if (n > kMaxRounds) r.piece = n / kMaxRounds * most;
+    return r;
+}
+// What the rounds give CTA c; at[i]: the cost before the i-th cut of the rounds.
+PKV_HD inline int64_t chunk_dealt(const int64_t* at, const ChunkRounds& r, int c, int ctas) {
+    int64_t sum = 0;
+    for (int k = 0; k < r.rounds; ++k) sum += at[k * ctas + c + 1] - at[k * ctas + c];
+    return sum;
+}
+// The cut before CTA c in what is left of the axis from cost `from` on; `due`: what
+// the CTAs before c still have to get, of `all`.
+PKV_HD inline ChunkPos chunk_rest_cut(const ChunkShape& a, const int64_t* prefix, int64_t from, int64_t due, int64_t all, int c,
+                                      int ctas) {
     if (c >= ctas) return ChunkPos{a.batch, 0, 0, 0};
-    return chunk_locate(a, prefix, total / ctas * c + total % ctas * c / ctas);
+    const double part = all > 0 ? static_cast<double>(due) / static_cast<double>(all) : 1.0;
+    return chunk_step_cut(a, prefix, from + static_cast<int64_t>(part * static_cast<double>(prefix[a.batch] - from)));
 }
 
 // Walks the segments (unit, steps s0 .. s1 - 1) between two cuts.
@@ -167,9 +232,23 @@ PKV_HD inline bool chunk_segment(const ChunkShape& a, const ChunkPos& cur, const
     return true;
 }
 // The position after segment g.
-PKV_HD inline ChunkPos chunk_after(const ChunkShape& a, const int64_t* prefix, const ChunkSegment& g) {
+PKV_HD inline ChunkPos chunk_after(const ChunkShape& a, const ChunkSegment& g) {
     if (g.s1 < g.ns) return ChunkPos{g.at.seq, g.at.head, g.at.tile, g.s1};
-    return chunk_next_unit(a, prefix, g.at, g.tiles);
+    return chunk_next_unit(a, g.at, g.tiles);
+}
+// Walks all segments of a CTA: `ranges` holds its rounds' and its last range, two cuts each.
+struct ChunkWalk {
+    ChunkPos cur;
+    int range;
+};
+PKV_HD inline ChunkWalk chunk_begin(const ChunkPos* ranges) { return ChunkWalk{ranges[0], 0}; }
+PKV_HD inline bool chunk_walk(const ChunkShape& a, const ChunkPos* ranges, int count, ChunkWalk& w, ChunkSegment& g) {
+    while (!chunk_segment(a, w.cur, ranges[2 * w.range + 1], g)) {
+        if (++w.range >= count) return false;
+        w.cur = ranges[2 * w.range];
+    }
+    w.cur = chunk_after(a, g);
+    return true;
 }
 
 }  // namespace
