@@ -38,8 +38,10 @@
 // of A and of B, in two parts of 64 tokens. While the softmax of one half runs,
 // the tensor cores work on the other.
 //
-// Tensor memory (512 columns): S of A and B (128 fp32 columns each; P is written
-// over its first 64), O of A and B. Shared memory: Q 64 KB, two stages of K and
+// Tensor memory (512 columns): S of A and B, in two parts of 64 tokens (64 fp32
+// columns each; the part's P is written over the first 32), O of A and B. The parts'
+// buffers are independent: while the softmax takes one, the other's products and
+// next scores run. Shared memory: Q 64 KB, two stages of K and
 // of V of 32 KB each.
 #include <math.h>
 
@@ -90,8 +92,8 @@ struct Cx {
     static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [128]
     static constexpr int kOffBars = kOffScale + 256;
     // k_full, k_empty per K stage; v_full, v_empty per V stage; q_full per half;
-    // s_full per half; p_full, pv_done per half and part; final per issuer
-    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 * 2 + 2 * 4 + 4;
+    // s_full, p_full, pv_done per half and part; final per issuer
+    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 + 3 * 4 + 4;
     static constexpr int kOffPlan = kOffBars + (kNumBars + 1) / 2 * 16;
     static constexpr int kOffMisc = kOffPlan + (2 * (kMaxRounds + 1) + 2 * kThreads / 32) * 16;
     static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
@@ -254,17 +256,52 @@ __device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, floa
     for (int e = 0; e < 8; ++e)
         x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
-// mbar_wait that looks at the clock and the abort flag at every 64th probe only (the
-// probes share issue slots with the warps that are waited for).
+// mbar_wait with up to 2^16 bare probes ahead of it: a warp that polls takes issue
+// slots from the warps it waits for, and mbar_wait's probe with its clock and abort
+// flag is some twenty instructions (measured: more than half of all executed).
+// kSleep > 0: that many nanoseconds between probes, for a warp that runs ahead.
+template <int kSleep = 0>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, status, abort);
+    const uint32_t addr = smem_u32(bar);
+    uint32_t done;
+    if constexpr (kSleep == 0) {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 0;\n\t"
+            "again:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra over;\n\t"
+            "add.u32 n, n, 1;\n\t"
+            "setp.lt.u32 q, n, 65536;\n\t"
+            "@q bra again;\n\t"
+            "over:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 0;\n\t"
+            "again:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra over;\n\t"
+            "nanosleep.u32 %3;\n\t"
+            "add.u32 n, n, 1;\n\t"
+            "setp.lt.u32 q, n, 65536;\n\t"
+            "@q bra again;\n\t"
+            "over:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity), "n"(kSleep)
+            : "memory");
+    }
+    return done != 0 || mbar_wait(bar, parity, status, abort);
 }
 // wait by a whole warp, with one answer for all its lanes.
+template <int kSleep = 0>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait(bar, parity, status, abort));
+    return __all_sync(0xffffffffu, wait<kSleep>(bar, parity, status, abort));
 }
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -363,7 +400,7 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
         const int part = 2 * it + (cw >> 1);
         const int st = IsV ? part % C::kParts : it & 1;
         const uint32_t parity = static_cast<uint32_t>((IsV ? part / C::kParts : it >> 1) & 1) ^ 1u;
-        if (!warp_wait(&empty[st], parity, a.status, abort_flag)) break;
+        if (!warp_wait<40>(&empty[st], parity, a.status, abort_flag)) break;
         // ---- the lane's token: its factor, and what the softmax needs
         const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
         const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
@@ -455,8 +492,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     uint64_t* v_full = k_empty + C::kStages;
     uint64_t* v_empty = v_full + C::kParts;
     uint64_t* q_full = v_empty + C::kParts;  // [half]: Q rows in place
-    uint64_t* s_full = q_full + 2;            // [half]: scores in tensor memory
-    uint64_t* p_full = s_full + 2;            // [half][part]: weights written
+    uint64_t* s_full = q_full + 2;            // [half][part]: scores in tensor memory
+    uint64_t* p_full = s_full + 4;            // [half][part]: weights written
     uint64_t* pv_done = p_full + 4;           // [half][part]: that product has completed
     uint64_t* final_bar = pv_done + 4;        // [issuer]: everything it issued has completed
     int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::kOffPrefix);  // while planning
@@ -478,8 +515,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&q_full[x], 4);
-            mbar_init(&s_full[x], 2);  // the products' completion, and the issuer itself (it has seen the step's table)
             for (int p = 0; p < 2; ++p) {
+                mbar_init(&s_full[2 * x + p], 2);  // the products' completion, and the issuer itself (it has seen the step's table)
                 mbar_init(&p_full[2 * x + p], 4);
                 mbar_init(&pv_done[2 * x + p], 1);
             }
@@ -572,21 +609,21 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
             float m = ninf(), l = 0.f, unit = 1.f;
             for (int j = 0; j < steps; ++j, ++it, ++table) {
-                if (!warp_wait(&s_full[x], it & 1, a.status, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
                 const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes);
-                const float4 modes = *reinterpret_cast<const float4*>(tab);
-                unit = modes.x;
-                const bool plain = __float_as_uint(modes.z) == 0u;
-                // never 0 or infinite: a hidden score is -inf times it
-                const float f = plain ? fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f) : row_f;
                 const int seen = lim - (g.at.s + j) * kChunkStep + 1;  // tokens of the step the row sees
                 const bool masked = (g.at.s + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
+                    if (!warp_wait(&s_full[2 * x + part], it & 1, a.status, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float4 modes = *reinterpret_cast<const float4*>(tab);
+                    unit = modes.x;
+                    const bool plain = __float_as_uint(modes.z) == 0u;
+                    // never 0 or infinite: a hidden score is -inf times it
+                    const float f = plain ? fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f) : row_f;
                     const int seen_part = seen - 64 * part;
                     const uint32_t col = col_s + 64 * part;
                     // O takes on another maximum (every lane its own factor; all lanes take part)
@@ -597,10 +634,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             m = mx;
                             l *= alpha;
                         }
-                        // O holds something once a part of this segment has been multiplied in;
-                        // part 0: the products of the step before completed ahead of these scores
+                        // O holds something once a part of this segment has been multiplied in:
+                        // the last one is the other part, of this step or of the one before
                         if (j + part == 0) return true;
-                        if (part == 1 && !warp_wait(&pv_done[2 * x], it & 1, a.status, abort_flag)) return false;
+                        if (!warp_wait(&pv_done[2 * x + (part ^ 1)], (it - 1 + part) & 1, a.status, abort_flag)) return false;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
@@ -672,7 +709,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                         }
                         if (!ok) break;
                         l += sum;
-                        tmem_st32(col_s + 32 * part, pw);
+                        tmem_st32(col, pw);
                     } else {
                         const float* cp = tab + 4 + 64 * part;
                         float mx = ninf();
@@ -700,7 +737,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             }
                             const uint32_t pw[4] = {pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
                                                     pack_f16x2(w[6], w[7])};
-                            tmem_st4(col_s + 32 * part + c / 2, pw);
+                            tmem_st4(col + c / 2, pw);
                         }
                     }
                     tmem_st_wait();
@@ -777,7 +814,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         // ------------------------------------------------ scores S = Q K^T of half x (one thread)
         const int x = warp - C::kScoreWarp;
         if (lane == 0) {
-            constexpr uint32_t idS = umma_idesc_f16(128, 128);
+            constexpr uint32_t idS = umma_idesc_f16(128, 64);
             const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
             int step = 0, it = 0, segs = 0;
             bool ok = true;
@@ -787,12 +824,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     if (!wait(&q_full[x], segs & 1, a.status, abort_flag)) break;
                     ++segs;
                 }
-                for (int j = g.at.s; j < g.s1; ++j, ++step) {
+                for (int j = g.at.s; ok && j < g.s1; ++j, ++step) {
                     const int st = step & 1;
-                    if (mine && it > 0 && !wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
                     if (!wait(&k_full[st], (step >> 1) & 1, a.status, abort_flag)) {
                         ok = false;
                         break;
@@ -801,17 +834,25 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                         mbar_arrive(&k_empty[st]);
                         continue;
                     }
-                    tc_fence_after();
                     const uint32_t k_base = smem_u32(smem + C::kOffK + st * C::kTileBytes);
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        // the part's weights of the step before lie over its scores
+                        if (it > 0 && !wait(&pv_done[2 * x + part], (it - 1) & 1, a.status, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * C::kPartBytes + (kk & 3) * 32;
-                        umma_bf16(tmem + C::kColS + 128 * x, umma_desc_sw128(q_base + off, 16, 1024),
-                                  umma_desc_sw128(k_base + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * C::kPartBytes + (kk & 3) * 32;
+                            umma_bf16(tmem + C::kColS + 128 * x + 64 * part, umma_desc_sw128(q_base + off, 16, 1024),
+                                      umma_desc_sw128(k_base + part * 64 * 128 + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                        }
+                        if (part == 1) umma_commit(&k_empty[st]);
+                        umma_commit(&s_full[2 * x + part]);
+                        mbar_arrive(&s_full[2 * x + part]);
                     }
-                    umma_commit(&k_empty[st]);
-                    umma_commit(&s_full[x]);
-                    mbar_arrive(&s_full[x]);
                     ++it;
                 }
             }
@@ -855,7 +896,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                         const uint32_t v_base = smem_u32(smem + C::kOffV + now * C::kVPartBytes);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 32 * part + 8 * kk,
+                            umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 64 * part + 8 * kk,
                                          umma_desc_sw128(v_base + kk * 32, 16, 1024), idO,
                                          (j > g.at.s || part > 0 || kk > 0) ? 1u : 0u);
                         umma_commit(&pv_done[2 * x + part]);
