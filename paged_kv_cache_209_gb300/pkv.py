@@ -435,21 +435,42 @@ def pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, context_l
     return out
 
 
-def _one_device(**tensors) -> None:
-    """Every tensor on the current CUDA device: the library launches there, on its current stream."""
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"libpkv takes CUDA tensors only ({name} is on {t.device})")
-    here = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != here:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{here}")
+# The calls below run between a serving loop's other launches, so their checks are
+# kept to a few attribute reads per tensor.
+def _here() -> int:
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):                   # no CUDA device: no tensor is on one
+        return -2
 
 
-def _int32(**tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{name} is int32")
+def _on(here: int, name: str, t: torch.Tensor, dtype=None, shape=None) -> int:
+    """Address of contiguous tensor ``t`` of this dtype and shape on CUDA device ``here``."""
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {str(dtype)[6:]}, not {str(t.dtype)[6:]}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} is {list(shape)}, not {list(t.shape)}")
+    if t.get_device() != here:
+        raise ValueError(f"libpkv takes CUDA tensors only, on the current device ({name} is on {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"libpkv takes contiguous tensors only ({name})")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, here: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
+
+
+def _q8_geometry(k_codes, v_codes, scales):
+    """(blocks, KV heads, head_dim) of int8 pools, after the checks of their shapes."""
+    if k_codes.dim() != 4 or k_codes.dtype != torch.int8:
+        raise ValueError("k_codes is int8 [num_blocks][num_kv_heads][16][head_dim]")
+    nb, hkv, bs, d = k_codes.shape
+    if v_codes.dtype != torch.int8 or v_codes.shape != (nb, hkv, d, bs):
+        raise ValueError("v_codes is int8 [num_blocks][num_kv_heads][head_dim][16]")
+    if scales.dtype != torch.float32 or scales.shape != (nb, hkv, 2, bs):
+        raise ValueError("scales are float32 [num_blocks][num_kv_heads][2][16] (K row, V row)")
+    return nb, hkv, bs, d
 
 
 def pkv_multiquery_q8_workspace_size(batch: int, num_q_heads: int, max_blocks_per_seq: int, max_query_len: int,
@@ -465,91 +486,94 @@ def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, conte
     """Causal attention of each sequence's new tokens over the int8 pools, any number of them:
     ``q``/``out`` are bf16 [rows][q_heads][head_dim], ``query_start`` int32 [batch + 1] their row
     offsets. Returns ``out`` (rows no sequence names are left as they were)."""
-    lib = load_library()
-    desc = q8_desc(k_codes)
-    _check_q8_pools(k_codes, v_codes, scales)
-    if q.dim() != 3 or q.shape[2] != desc.head_dim or q.dtype != torch.bfloat16:
+    lib = _lib or load_library()
+    nb, hkv, bs, d = _q8_geometry(k_codes, v_codes, scales)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d:
         raise ValueError("q is bf16 [rows][q_heads][head_dim]")
     rows, q_heads, _ = q.shape
-    batch = int(context_lens.shape[0])
-    _int32(block_tables=block_tables, context_lens=context_lens, query_start=query_start)
-    if block_tables.dim() != 2 or block_tables.shape[0] != batch or query_start.shape != (batch + 1,):
-        raise ValueError("block_tables is [batch][max_blocks], query_start [batch + 1]")
-    max_blocks = int(block_tables.shape[1])
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables is [batch][max_blocks]")
+    batch, max_blocks = block_tables.shape
     if out is None:
         out = torch.empty_like(q)
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out is bf16 of q's shape")
     if workspace is None:
         need = pkv_multiquery_q8_workspace_size(batch, q_heads, max_blocks, max_query_len, k_codes)
         workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
-    _one_device(q=q, k_codes=k_codes, v_codes=v_codes, scales=scales, block_tables=block_tables,
-                context_lens=context_lens, query_start=query_start, out=out, workspace=workspace)
+    here = _here()
+    args = (_on(here, "q", q), _on(here, "k_codes", k_codes), _on(here, "v_codes", v_codes),
+            _on(here, "scales", scales), _on(here, "block_tables", block_tables, torch.int32), max_blocks,
+            _on(here, "context_lens", context_lens, torch.int32, (batch,)),
+            _on(here, "query_start", query_start, torch.int32, (batch + 1,)), batch, q_heads, max_query_len, scale,
+            _on(here, "out", out, torch.bfloat16, q.shape), _on(here, "workspace", workspace),
+            workspace.numel() * workspace.element_size())
     if rows == 0:                                            # no query anywhere: no row to write
         return out
-    _check("pkv_multiquery_attention_q8", lib.pkv_multiquery_attention_q8(
-        _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
-        _ptr(query_start), batch, q_heads, max_query_len, ctypes.c_float(scale), _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), ctypes.byref(desc), flags, _stream(stream)))
+    status = lib.pkv_multiquery_attention_q8(*args, CacheDesc(nb, bs, hkv, d, PKV_INT8), flags,
+                                             _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_multiquery_attention_q8", status)
     return out
 
 
-def _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start, k_out, v_out, dtype, device):
-    batch = int(context_lens.shape[0])
-    _int32(block_tables=block_tables, context_lens=context_lens, row_start=row_start, token_start=token_start)
-    if block_tables.dim() != 2 or block_tables.shape[0] != batch or row_start.shape != (batch + 1,):
-        raise ValueError("block_tables is [batch][max_blocks], row_start [batch + 1]")
-    if token_start is not None and token_start.shape != (batch,):
-        raise ValueError("token_start is [batch]")
-    want = (int(num_rows), desc.num_kv_heads, desc.head_dim)
-    k_out = torch.empty(want, dtype=dtype, device=device) if k_out is None else k_out
-    v_out = torch.empty(want, dtype=dtype, device=device) if v_out is None else v_out
-    if tuple(k_out.shape) != want or tuple(v_out.shape) != want or k_out.dtype != dtype or v_out.dtype != dtype:
-        raise ValueError(f"k_out and v_out are {want} of {dtype}")
-    return batch, int(block_tables.shape[1]), k_out, v_out
+def _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out, v_out, dtype, like):
+    """Arguments of both reading-back calls from the tables on, and the outputs."""
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables is [batch][max_blocks]")
+    batch, max_blocks = block_tables.shape
+    want = (num_rows, hkv, d)
+    if k_out is None:
+        k_out = torch.empty(want, dtype=dtype, device=like.device)
+    if v_out is None:
+        v_out = torch.empty(want, dtype=dtype, device=like.device)
+    return (_on(here, "block_tables", block_tables, torch.int32), max_blocks,
+            _on(here, "context_lens", context_lens, torch.int32, (batch,)),
+            None if token_start is None else _on(here, "token_start", token_start, torch.int32, (batch,)),
+            _on(here, "row_start", row_start, torch.int32, (batch + 1,)), batch, num_rows,
+            _on(here, "k_out", k_out, dtype, want), _on(here, "v_out", v_out, dtype, want)), k_out, v_out
 
 
 def pkv_gather(k_cache, v_cache, block_tables, context_lens, row_start, num_rows: int, token_start=None, k_out=None,
                v_out=None, flags: int = 0, stream=None):
     """Tokens ``token_start[i] ..`` of each sequence as rows ``row_start[i] .. row_start[i+1]-1``:
     returns ``(k_out, v_out)``, [num_rows][kv_heads][head_dim] of the pool dtype."""
-    lib = load_library()
+    lib = _lib or load_library()
     _same_pools(k_cache, v_cache)
     desc = cache_desc(k_cache)
-    batch, max_blocks, k_out, v_out = _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start,
-                                                   k_out, v_out, k_cache.dtype, k_cache.device)
-    _one_device(k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, context_lens=context_lens,
-                row_start=row_start, token_start=token_start, k_out=k_out, v_out=v_out)
-    _check("pkv_gather", lib.pkv_gather(
-        _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), _ptr(token_start),
-        _ptr(row_start), batch, int(num_rows), _ptr(k_out), _ptr(v_out), ctypes.byref(desc), flags, _stream(stream)))
+    here = _here()
+    pools = _on(here, "k_cache", k_cache), _on(here, "v_cache", v_cache)
+    args, k_out, v_out = _gather_args(here, desc.num_kv_heads, desc.head_dim, block_tables, context_lens, row_start,
+                                      num_rows, token_start, k_out, v_out, k_cache.dtype, k_cache)
+    status = lib.pkv_gather(*pools, *args, desc, flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_gather", status)
     return k_out, v_out
 
 
 def pkv_gather_q8(k_codes, v_codes, scales, block_tables, context_lens, row_start, num_rows: int, token_start=None,
                   out_dtype=torch.bfloat16, k_out=None, v_out=None, flags: int = 0, stream=None):
     """``pkv_gather`` over the int8 pools: the values (code * scale) as ``out_dtype``, bf16 or float32."""
-    lib = load_library()
-    desc = q8_desc(k_codes)
-    _check_q8_pools(k_codes, v_codes, scales)
+    lib = _lib or load_library()
+    nb, hkv, bs, d = _q8_geometry(k_codes, v_codes, scales)
     code = _dtype_code(out_dtype)
-    batch, max_blocks, k_out, v_out = _gather_args(desc, block_tables, context_lens, row_start, num_rows, token_start,
-                                                   k_out, v_out, out_dtype, k_codes.device)
-    _one_device(k_codes=k_codes, v_codes=v_codes, scales=scales, block_tables=block_tables,
-                context_lens=context_lens, row_start=row_start, token_start=token_start, k_out=k_out, v_out=v_out)
-    _check("pkv_gather_q8", lib.pkv_gather_q8(
-        _ptr(k_codes), _ptr(v_codes), _ptr(scales), _ptr(block_tables), max_blocks, _ptr(context_lens),
-        _ptr(token_start), _ptr(row_start), batch, int(num_rows), _ptr(k_out), _ptr(v_out), code, ctypes.byref(desc),
-        flags, _stream(stream)))
+    here = _here()
+    pools = _on(here, "k_codes", k_codes), _on(here, "v_codes", v_codes), _on(here, "scales", scales)
+    args, k_out, v_out = _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out,
+                                      v_out, out_dtype, k_codes)
+    status = lib.pkv_gather_q8(*pools, *args, code, CacheDesc(nb, bs, hkv, d, PKV_INT8), flags,
+                               _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_gather_q8", status)
     return k_out, v_out
 
 
-def _prob_rows(name, t):
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+def _prob_rows(here, name, t):
+    """(address, row stride, rows) of probabilities whose rows may be any stride apart."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name} is [rows][vocab] with consecutive entries in a row")
+    if t.get_device() != here:
+        raise ValueError(f"libpkv takes CUDA tensors only, on the current device ({name} is on {t.device})")
     rows, vocab = t.shape
-    stride = int(t.stride(0)) if rows > 1 else int(vocab)
-    return (t.data_ptr() if rows else None), stride, int(rows)
+    return (t.data_ptr() if rows else None), (t.stride(0) if rows > 1 else vocab), rows
 
 
 def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, sample_uniform, query_start,
@@ -560,25 +584,19 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
 
     ``target_probs`` [rows][vocab] holds k + 1 rows per sequence (``query_start``), ``draft_probs`` k
     (``draft_start``), float32 or bf16, rows any stride apart; ``draft_probs`` None means certain drafts."""
-    lib = load_library()
-    batch = int(sample_uniform.shape[0])
+    lib = _lib or load_library()
     code = _dtype_code(target_probs.dtype)
-    tp, ts, tr = _prob_rows("target_probs", target_probs)
-    dp, ds, dr = None, 0, int(draft_tokens.shape[0])
+    here = _here()
+    if sample_uniform.dim() != 1 or draft_tokens.dim() != 1 or max_draft_len < 0:
+        raise ValueError("sample_uniform is [batch], draft_tokens [draft rows], max_draft_len at least 0")
+    batch, drafts = sample_uniform.shape[0], draft_tokens.shape[0]
+    vocab = target_probs.shape[-1]
+    tp, ts, tr = _prob_rows(here, "target_probs", target_probs)
+    dp, ds, dr = None, 0, drafts
     if draft_probs is not None:
-        if draft_probs.dtype != target_probs.dtype or draft_probs.shape != (dr, target_probs.shape[1]):
+        if draft_probs.dtype != target_probs.dtype or draft_probs.shape != (drafts, vocab):
             raise ValueError("draft_probs is [draft rows][vocab] of target_probs's dtype, one row per draft token")
-        dp, ds, dr = _prob_rows("draft_probs", draft_probs)
-    _int32(draft_tokens=draft_tokens, query_start=query_start, draft_start=draft_start, context_lens=context_lens,
-           out_tokens=out_tokens, num_accepted=num_accepted, new_context_lens=new_context_lens)
-    if accept_uniform.dtype != torch.float32 or sample_uniform.dtype != torch.float32:
-        raise ValueError("the uniform numbers are float32")
-    if accept_uniform.shape != draft_tokens.shape or draft_tokens.dim() != 1 or sample_uniform.dim() != 1:
-        raise ValueError("draft_tokens and accept_uniform are [draft rows], sample_uniform [batch]")
-    if query_start.shape != (batch + 1,) or draft_start.shape != (batch + 1,):
-        raise ValueError("query_start and draft_start are [batch + 1]")
-    if max_draft_len < 0:
-        raise ValueError("max_draft_len is at least 0")
+        dp, ds, dr = _prob_rows(here, "draft_probs", draft_probs)
     if context_lens is None and new_context_lens is not None:
         raise ValueError("new_context_lens needs context_lens")
     dev = target_probs.device
@@ -588,19 +606,20 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
         num_accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
     if context_lens is not None and new_context_lens is None:
         new_context_lens = torch.empty((batch,), dtype=torch.int32, device=dev)
-    if out_tokens.shape != (batch, max_draft_len + 1):
-        raise ValueError("out_tokens is [batch][max_draft_len + 1]")
-    if any(t is not None and t.shape != (batch,) for t in (num_accepted, context_lens, new_context_lens)):
-        raise ValueError("num_accepted, context_lens and new_context_lens are [batch]")
-    _one_device(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
-                accept_uniform=accept_uniform, sample_uniform=sample_uniform, query_start=query_start,
-                draft_start=draft_start, context_lens=context_lens, out_tokens=out_tokens, num_accepted=num_accepted,
-                new_context_lens=new_context_lens)
-    _check("pkv_verify_drafts", lib.pkv_verify_drafts(
-        tp, ts, tr, dp, ds, dr, code, int(target_probs.shape[1]), _ptr(draft_tokens) if dr else None,
-        _ptr(accept_uniform) if dr else None, _ptr(sample_uniform), _ptr(query_start), _ptr(draft_start), batch,
-        int(max_draft_len), _ptr(context_lens), _ptr(new_context_lens), _ptr(out_tokens), _ptr(num_accepted), flags,
-        _stream(stream)))
+    i32, one = torch.int32, (batch,)
+    tokens = _on(here, "draft_tokens", draft_tokens, i32)
+    accept = _on(here, "accept_uniform", accept_uniform, torch.float32, (drafts,))
+    status = lib.pkv_verify_drafts(
+        tp, ts, tr, dp, ds, dr, code, vocab, tokens if dr else None, accept if dr else None,
+        _on(here, "sample_uniform", sample_uniform, torch.float32),
+        _on(here, "query_start", query_start, i32, (batch + 1,)),
+        _on(here, "draft_start", draft_start, i32, (batch + 1,)), batch, max_draft_len,
+        None if context_lens is None else _on(here, "context_lens", context_lens, i32, one),
+        None if new_context_lens is None else _on(here, "new_context_lens", new_context_lens, i32, one),
+        _on(here, "out_tokens", out_tokens, i32, (batch, max_draft_len + 1)),
+        _on(here, "num_accepted", num_accepted, i32, one), flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_verify_drafts", status)
     return out_tokens, num_accepted, new_context_lens
 
 

@@ -118,37 +118,53 @@ def test_verify_refusals(lib):
     assert verify(lib, batch=0, p=None, out=None) == OK
 
 
-def test_binding_refuses_host_tensors_and_wrong_types():
+def test_binding_refuses_host_tensors(lib):
     from paged_kv_cache_209_gb300 import pkv
+    kc, vc = torch.zeros((3, 2, 16, 64), dtype=torch.int8), torch.zeros((3, 2, 64, 16), dtype=torch.int8)
+    sc, kp = torch.zeros((3, 2, 2, 16)), torch.zeros((3, 2, 16, 64))
+    t, n, st = (torch.zeros(s, dtype=torch.int32) for s in ((1, 2), (1,), (2,)))
+    q, ws, u = torch.zeros((5, 4, 64), dtype=torch.bfloat16), torch.zeros(1024, dtype=torch.uint8), torch.zeros(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.pkv_multiquery_attention_q8(q, kc, vc, sc, t, n, st, 0.1, 5, workspace=ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.pkv_gather_q8(kc, vc, sc, t, n, st, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.pkv_gather(kp, kp, t, n, st, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkv.pkv_verify_drafts(torch.zeros((2, 10)), torch.zeros((1, 10)), n, u, u, st, st, 1)
+
+
+def test_binding_refuses_wrong_types_and_shapes(lib, monkeypatch):
+    """The checks behind the device check, on host tensors (-1 is a host tensor's device number)."""
+    from paged_kv_cache_209_gb300 import pkv
+    monkeypatch.setattr(pkv, "_here", lambda: -1)
     kc, vc = torch.zeros((3, 2, 16, 64), dtype=torch.int8), torch.zeros((3, 2, 64, 16), dtype=torch.int8)
     sc = torch.zeros((3, 2, 2, 16))
     t, n, st = (torch.zeros(s, dtype=torch.int32) for s in ((1, 2), (1,), (2,)))
     q = torch.zeros((5, 4, 64), dtype=torch.bfloat16)
     ws = torch.zeros(1024, dtype=torch.uint8)
-    with pytest.raises(ValueError, match="CUDA"):
-        pkv.pkv_multiquery_attention_q8(q, kc, vc, sc, t, n, st, 0.1, 5, workspace=ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkv.pkv_multiquery_attention_q8(q.transpose(0, 1), kc, vc, sc, t, n, st, 0.1, 5, workspace=ws)
+    with pytest.raises(ValueError, match="v_codes"):
+        pkv.pkv_multiquery_attention_q8(q, kc, kc, sc, t, n, st, 0.1, 5, workspace=ws)
     with pytest.raises(ValueError, match="bf16"):
         pkv.pkv_multiquery_attention_q8(q.float(), kc, vc, sc, t, n, st, 0.1, 5, workspace=ws)
     with pytest.raises(ValueError, match="int32"):
         pkv.pkv_multiquery_attention_q8(q, kc, vc, sc, t.long(), n, st, 0.1, 5, workspace=ws)
     with pytest.raises(ValueError, match="out"):
         pkv.pkv_multiquery_attention_q8(q, kc, vc, sc, t, n, st, 0.1, 5, out=q[:4], workspace=ws)
-    with pytest.raises(ValueError, match="CUDA"):
-        pkv.pkv_gather_q8(kc, vc, sc, t, n, st, 4)
     with pytest.raises(ValueError, match="row_start"):
         pkv.pkv_gather_q8(kc, vc, sc, t, n, st[:1], 4)
-    with pytest.raises(ValueError, match="dtype"):
+    with pytest.raises(ValueError, match="unsupported"):
         pkv.pkv_gather_q8(kc, vc, sc, t, n, st, 4, out_dtype=torch.float16)
     kp = torch.zeros((3, 2, 16, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="k_out"):
         pkv.pkv_gather(kp, kp, t, n, st, 4, k_out=torch.zeros((3, 2, 64), dtype=torch.bfloat16))
     p, u = torch.zeros((2, 10)), torch.zeros(1)
     tok = torch.zeros(1, dtype=torch.int32)
-    with pytest.raises(ValueError, match="CUDA"):
-        pkv.pkv_verify_drafts(p, p[:1], tok, u, u, st, st, 1)
     with pytest.raises(ValueError, match="draft_probs"):
         pkv.pkv_verify_drafts(p, p, tok, u, u, st, st, 1)
     with pytest.raises(ValueError, match="consecutive"):
         pkv.pkv_verify_drafts(p.t(), None, tok, u, u, st, st, 1)
-    with pytest.raises(ValueError, match="float32"):
+    with pytest.raises(ValueError, match="accept_uniform is float32"):
         pkv.pkv_verify_drafts(p, p[:1], tok, u.double(), u, st, st, 1)
