@@ -780,6 +780,7 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
         a.group = G;
         a.max_query_len = max_query_len;
         a.scale = scale;
+        a.group_inverse = ((uint64_t(1) << 37) + G - 1) / G;
         if (launch_chunk_q8(a, s) != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;

@@ -35,14 +35,13 @@
 // the previous loads into scaled f16, in the 128-byte-swizzled layout the tensor
 // cores read; K's also write the step's exponents and, for a slow step, its factors. Warps 16
 // and 17: one thread each issues S = Q K^T of A and of B; warps 18 and 19: O += P V
-// of A and of B, in two parts of 64 tokens. While the softmax of one half runs,
-// the tensor cores work on the other.
+// of A and of B, in two parts of 64 tokens.
 //
 // Tensor memory (512 columns): S of A and B, in two parts of 64 tokens (64 fp32
 // columns each; the part's P is written over the first 32), O of A and B. The parts'
 // buffers are independent: while the softmax takes one, the other's products and
-// next scores run. Shared memory: Q 64 KB, two stages of K and
-// of V of 32 KB each.
+// next scores run. Shared memory: Q 64 KB, two stages of K of 32 KB each, three of V
+// of 16 KB, the next step's codes 32 KB.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -76,6 +75,7 @@ struct Cx {
     // softmax half (a fifth needs scores that need V parts which that half's
     // products have yet to release).
     static constexpr int kTables = 8;
+    static constexpr int kJobs = 8;     // segments laid out ahead
     static constexpr int kHalves = D / 64;                    // 128-byte column parts of a K or Q row
     static constexpr int kPartBytes = 128 * 128;              // 128 rows of one part
     static constexpr int kTileBytes = kHalves * kPartBytes;   // Q of one row half; one K stage
@@ -86,16 +86,18 @@ struct Cx {
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffCodes = kOffV + kParts * kVPartBytes;  // the next step's codes: [8 warps][kVecs][32 lanes] vectors
     static constexpr int kOffTable = kOffCodes + 8 * kVecs * 512;
-    // a step's table: 2^E, 2^F, a byte per converter warp that is 1 for a slow step;
-    // for slow steps the tokens' K factors [128] and, in log2, what their V values lack [128]
+    // a step's table: 2^E, 2^F, a byte per converter warp that is 1 for a slow step; the
+    // tokens' K factors [128] and, in log2, what their V values lack [128]
     static constexpr int kTableBytes = 16 + 2 * 128 * 4;
     static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [128]
     static constexpr int kOffBars = kOffScale + 256;
     // k_full, k_empty per K stage; v_full, v_empty per V stage; q_full per half;
-    // s_full, p_full, pv_done per half and part; final per issuer
-    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 + 3 * 4 + 4;
-    static constexpr int kOffPlan = kOffBars + (kNumBars + 1) / 2 * 16;
-    static constexpr int kOffMisc = kOffPlan + (2 * (kMaxRounds + 1) + 2 * kThreads / 32) * 16;
+    // s_full, p_full, pv_done per half and part; final per issuer; job_full, job_empty
+    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 + 3 * 4 + 4 + 2 * kJobs;
+    static constexpr int kOffJobs = kOffBars + (kNumBars + 1) / 2 * 16;
+    static constexpr int kOffWalk = kOffJobs + kJobs * 48;
+    static constexpr int kOffPlan = kOffWalk + (sizeof(ChunkWalk) + 15) / 16 * 16;
+    static constexpr int kOffMisc = kOffPlan + 2 * (kMaxRounds + 1) * 16;
     static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
     // scratch of the planning, over the operands: the rounds' cuts, then the costs before the sequences
     static constexpr int kOffPrefix = (kMaxRounds * kMaxPieces + 1) * 8;
@@ -109,6 +111,8 @@ struct Cx {
 // ---------------------------------------------------------------- workspace
 // Per CTA a descriptor (first position of its range, flags) and two piece slots:
 // 0 for a piece that begins inside a unit, 1 for one that begins a unit and is cut.
+// A slot: O as [D / 4][256 rows] of four floats (a warp's lanes, one row each, write
+// consecutive vectors), then the rows' m and l.
 struct PieceInfo {
     ChunkPos start;
     int flags;  // 1: slot 0 written, 2: slot 1 written
@@ -119,6 +123,16 @@ __host__ __device__ constexpr size_t slot_floats(int d) { return static_cast<siz
 __host__ __device__ constexpr size_t infos_bytes(int grid) { return (static_cast<size_t>(grid) * sizeof(PieceInfo) + 255) / 256 * 256; }
 __device__ __forceinline__ float* slot_of(void* workspace, int grid, int d, int cta, int slot) {
     return reinterpret_cast<float*>(static_cast<char*>(workspace) + infos_bytes(grid)) + (static_cast<size_t>(cta) * 2 + slot) * slot_floats(d);
+}
+
+// Query of row R of a unit's sequence, and that row's place in q and out. (A division
+// by the group as a multiplication: exact for rows below 2^26 and groups up to 1024.)
+__device__ __forceinline__ int query_of(const ChunkArgs& a, int R) {
+    return static_cast<int>((static_cast<uint64_t>(R) * a.group_inverse) >> 37);
+}
+__device__ __forceinline__ int64_t row_of_unit(const ChunkArgs& a, int q0, int head, int R) {
+    const int t = query_of(a, R);
+    return (static_cast<int64_t>(q0) + t) * a.q_heads + head * a.group + (R - t * a.group);
 }
 
 __device__ __forceinline__ ChunkShape shape_of(const ChunkArgs& a) {
@@ -181,7 +195,7 @@ __device__ int plan_ranges(const ChunkArgs& a, const ChunkShape& sh, int64_t* pr
         }
         __syncthreads();
         from = at[r.rounds * ctas];
-        const int64_t left = t < ctas ? total / ctas - chunk_dealt(at, r, t, ctas) : 0;
+        const int64_t left = t < ctas ? chunk_div(total, ctas) - chunk_dealt(at, r, t, ctas) : 0;
         const int64_t due = block_sum(left > 0 ? left : 0, scratch);
         __syncthreads();
         if (t == cta) at[0] = due;
@@ -246,62 +260,39 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Eight scores of a slow step, scaled, -inf where the token is absent or not seen
-// (columns taddr .. taddr + 7, K factors c, row factor f, the first `seen` of them seen).
-__device__ __forceinline__ void slow_scores(uint32_t taddr, const float* c, float f, int seen, float (&x)[8]) {
-    uint32_t v[8];
-    tmem_ld8(taddr, v);
+// Sixteen scaled scores, -inf where the token is absent or not seen (columns taddr ..
+// taddr + 15, K factors c, row factor f, the first `seen` of them seen).
+__device__ __forceinline__ void careful_scores(uint32_t taddr, const float* c, float f, int seen, float (&x)[16]) {
+    uint32_t v[16];
+    tmem_ld16(taddr, v);
     tmem_ld_wait();
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 16; ++e)
         x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
-// mbar_wait with up to 2^16 bare probes ahead of it: a warp that polls takes issue
-// slots from the warps it waits for, and mbar_wait's probe with its clock and abort
-// flag is some twenty instructions (measured: more than half of all executed).
+// Waits until the phase of this parity has completed, about two seconds at most;
+// then it reports PKV_DEVERR_TIMEOUT and the role gives up (and with it, in as much
+// time, every role that depends on it). A probe is a handful of instructions: a warp
+// that polls takes issue slots from the warps it waits for, and the kernel's two
+// dozen waits have to share the instruction cache with its loops.
 // kSleep > 0: that many nanoseconds between probes, for a warp that runs ahead.
+constexpr long long kWaitClocks = 4000000000ll;
 template <int kSleep = 0>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
-    const uint32_t addr = smem_u32(bar);
-    uint32_t done;
-    if constexpr (kSleep == 0) {
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, 0;\n\t"
-            "again:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra over;\n\t"
-            "add.u32 n, n, 1;\n\t"
-            "setp.lt.u32 q, n, 65536;\n\t"
-            "@q bra again;\n\t"
-            "over:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-            "mov.u32 n, 0;\n\t"
-            "again:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra over;\n\t"
-            "nanosleep.u32 %3;\n\t"
-            "add.u32 n, n, 1;\n\t"
-            "setp.lt.u32 q, n, 65536;\n\t"
-            "@q bra again;\n\t"
-            "over:\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity), "n"(kSleep)
-            : "memory");
-    }
-    return done != 0 || mbar_wait(bar, parity, status, abort);
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long begun = clock64();
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        if constexpr (kSleep > 0) __nanosleep(kSleep);
+    } while (clock64() - begun < kWaitClocks);
+    atomicOr(status, PKV_DEVERR_TIMEOUT);
+    return false;
 }
 // wait by a whole warp, with one answer for all its lanes.
 template <int kSleep = 0>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait<kSleep>(bar, parity, status, abort));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    return __all_sync(0xffffffffu, wait<kSleep>(bar, parity, status));
 }
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -310,18 +301,73 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
+// ---------------------------------------------------------------- segments
+// A segment as the roles need it. The first K converter, ahead of all others, walks
+// the CTA's ranges and lays the next segment out in shared memory; the others read it
+// there. (Walking in each role cost a dependent chain of global loads at every
+// segment, and its code.)
+struct __align__(16) Job {
+    int seq, head;
+    int s0, s1;   // steps; s1 == 0: no more segments
+    int n, q0;    // tokens and first query row of the sequence
+    int before;   // its tokens ahead of the chunk
+    int r0;       // first row of the unit
+    int rows;     // rows of the unit, at most 256
+    int piece;    // 0: the whole unit; 1: begins inside it (slot 0), 2: begins it and is cut (slot 1)
+    int pad[2];
+};
+static_assert(sizeof(Job) == 48, "layout");
+
+// The next segment of a warp's sequence of them (`count`: how many it has taken).
+// All lanes of the warp, or kLanes = 1: one thread.
+template <int D, int kLanes>
+__device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int& count, Job& job, unsigned int* status) {
+    using C = Cx<D>;
+    const int slot = count % C::kJobs;
+    const uint32_t parity = static_cast<uint32_t>(count / C::kJobs) & 1u;
+    if (!(kLanes == 32 ? warp_wait(&job_full[slot], parity, status) : wait(&job_full[slot], parity, status))) return false;
+    job = *reinterpret_cast<const Job*>(smem + C::kOffJobs + slot * sizeof(Job));
+    if (kLanes == 32) __syncwarp();
+    if (kLanes == 1 || (threadIdx.x & 31) == 0) mbar_arrive(&job_empty[slot]);
+    ++count;
+    return job.s1 > 0;
+}
+
+// Lays out the segment after `count` others (one thread).
+template <int D>
+__device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int ranges, int count) {
+    using C = Cx<D>;
+    const int slot = count % C::kJobs;
+    if (count >= C::kJobs && !wait<40>(&job_empty[slot], static_cast<uint32_t>(count / C::kJobs - 1) & 1u, a.status)) return;
+    ChunkWalk& walk = *reinterpret_cast<ChunkWalk*>(smem + C::kOffWalk);
+    ChunkSegment g;
+    Job job{};
+    if (chunk_walk(shape_of(a), reinterpret_cast<const ChunkPos*>(smem + C::kOffPlan), ranges, walk, g)) {
+        job.seq = g.at.seq;
+        job.head = g.at.head;
+        job.s0 = g.at.s;
+        job.s1 = g.s1;
+        job.n = g.q.n;
+        job.q0 = g.q.q0;
+        job.before = g.q.n - g.q.nq;
+        job.r0 = g.at.tile * kChunkRows;
+        job.rows = min(kChunkRows, g.q.nq * a.group - job.r0);
+        job.piece = g.whole() ? 0 : g.at.s > 0 ? 1 : 2;
+    }
+    *reinterpret_cast<Job*>(smem + C::kOffJobs + slot * sizeof(Job)) = job;
+    mbar_arrive(&job_full[slot]);
+}
+
 // ---------------------------------------------------------------- converters
 // K's (IsV false) or V's four warps: every step of the CTA's range. Warp w takes
 // tokens 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1), lane l the scales of
 // token 32 w + l. A lane copies the codes of the next step into its own slots of
 // shared memory as it takes the current ones out of them (asynchronous copies: a
-// step's time ahead, and no registers). The loops stay rolled: the warps of the four
-// roles on a scheduler share an instruction cache that their unrolled bodies
-// overflow. A warp decides by itself whether its tokens are taken as bare codes; both
-// groups read V's scales and decide alike.
+// step's time ahead, and no registers). A warp decides by itself whether its tokens
+// are taken as bare codes; both groups read V's scales and decide alike.
 template <int D, bool IsV>
-__device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* smem, const ChunkPos* ranges, int count,
-                             ChunkWalk* where, uint64_t* full, uint64_t* empty, volatile int* abort_flag) {
+__device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, int ranges, uint64_t* job_full, uint64_t* job_empty,
+                                             uint64_t* full, uint64_t* empty) {
     using C = Cx<D>;
     const int lane = threadIdx.x & 31;
     const int cw = (threadIdx.x >> 5) & 3;
@@ -331,126 +377,130 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
     const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes);
     uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
 
-    // the segment being loaded (the walk past it: in shared memory, one per warp, read once per segment)
-    if (lane == 0) *where = chunk_begin(ranges);
-    __syncwarp();
-    int step = 0, last = 0;         // next step to load, one past the segment's last
+    int jobs = 0;
+    int step = 0, last = 0;         // step being loaded, one past the segment's last
     int n = 0, head = 0;            // its tokens, KV head
     const int32_t* trow = nullptr;  // its block table
     int ids = 0, ids_next = 0;      // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
-    int ev = 0, ek = 0;             // its E and F
-    auto id_at = [&](int b) {
-        if (b >= (n + 15) / 16) return -1;
-        const int id = __ldg(trow + b);
-        if (id >= 0 && id < a.num_blocks) return id;
-        if (!IsV) atomicOr(a.status, PKV_DEVERR_RANGE);
-        return -2;
-    };
-    auto open = [&]() {
-        ChunkSegment g;
-        ChunkWalk walk = *where;
-        __syncwarp();
-        if (!chunk_walk(sh, ranges, count, walk, g)) return false;
-        if (lane == 0) *where = walk;
-        __syncwarp();
-        step = g.at.s;
-        last = g.s1;
-        n = g.q.n;
-        head = g.at.head;
-        trow = a.tables + static_cast<int64_t>(g.at.seq) * a.max_blocks;
-        ids = id_at(32 * (step >> 2) + lane);
-        ids_next = id_at(32 * (step >> 2) + 32 + lane);
-        // E and F from the scales of the first block's tokens (K's in lanes 0-15, V's in 16-31)
-        const int id = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
-        const uint32_t x = __float_as_uint(__ldg(a.scales + (static_cast<int64_t>(id) * a.kv_heads + head) * 32 + lane)) & 0x7fffffffu;
-        const bool use = x < 0x7f800000u && step * kChunkStep + (lane & 15) < n;
-        ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
-        ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
-        return true;
-    };
-    // where the step's two blocks lie; the scales of the lane's token, whether it
-    // exists or lies in a block outside the pool
-    const uint4 *src0 = nullptr, *src1 = nullptr;
+    int ev = 0, ek = 0;             // E and F of the segment being converted
+    float sample = 0.f;             // what they are taken from
+    bool opened = false;            // they are still to be taken
+    // the loaded step: the scales of the lane's token, whether it exists or lies in a block outside the pool
     float ks = 0.f, vs = 0.f;
     bool present = false, missing = false;
-    auto find = [&]() {
-        const int b0 = (step & 3) * 8 + 2 * cw;
-        const int id0 = __shfl_sync(0xffffffffu, ids, b0), id1 = __shfl_sync(0xffffffffu, ids, b0 + 1);
-        // an absent block's codes may be any (its tokens carry no weight): block 0 exists
-        src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
-        src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
-        const int id = lane < 16 ? id0 : id1;
-        present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
-        missing = id == -2;
-        const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (lane & 15);
-        if (!IsV) ks = __ldg(rec);
-        vs = __ldg(rec + 16);
-    };
-
-    bool live = open();
-    if (live) {
-        find();
-#pragma unroll 1
-        for (int i = 0; i < C::kVecs; ++i)
-            copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
-    }
-    copy_commit();
-    for (int it = 0; live; ++it) {
-        // this warp's stage: K's of the step, V's of the half that holds its tokens
-        const int part = 2 * it + (cw >> 1);
-        const int st = IsV ? part % C::kParts : it & 1;
-        const uint32_t parity = static_cast<uint32_t>((IsV ? part / C::kParts : it >> 1) & 1) ^ 1u;
-        if (!warp_wait<40>(&empty[st], parity, a.status, abort_flag)) break;
-        // ---- the lane's token: its factor, and what the softmax needs
-        const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-        const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
+    for (int it = -1;; ++it) {
+        const int st = IsV ? (2 * it + (cw >> 1)) % C::kParts : it & 1;  // K's stage of the step, V's of the half with this warp's tokens
+        uint32_t pair = 0;                                               // K: (hi, lo) of the lane's factor
         __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 32 * cw;
-        uint32_t pair = 0;  // K: (hi, lo) of the factor
-        if (IsV) {
-            factors[lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
-        } else {
-            const bool bare_k = __any_sync(0xffffffffu, present && leaves_range(__float_as_uint(ks) & 0x7fffffffu, ek));
-            const bool slow = bare_k || bare_v || __any_sync(0xffffffffu, missing);
-            float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
-            if (lane == 0) {
-                if (cw == 0) *reinterpret_cast<float2*>(tab) = make_float2(exp2_int(ev), exp2_int(ek));
-                reinterpret_cast<uint8_t*>(tab)[8 + cw] = slow;
+        if (it >= 0) {
+            const uint32_t parity = static_cast<uint32_t>((IsV ? (2 * it + (cw >> 1)) / C::kParts : it >> 1) & 1) ^ 1u;
+            if (!warp_wait<40>(&empty[st], parity, a.status)) break;
+            if (opened) {
+                const uint32_t x = __float_as_uint(sample) & 0x7fffffffu;
+                const bool use = x < 0x7f800000u;
+                ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
+                ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
+                opened = false;
             }
-            tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
-            float lack = 0.f;
-            // (a scale below the normal range counts as its smallest number)
-            if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
-            tab[4 + 128 + 32 * cw + lane] = lack;
-            const float factor = !present ? 0.f : bare_k ? 1.f : ks * exp2_int(-ek);
-            const __half hi = __float2half(factor);
-            pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));
+            // ---- the lane's token: its factor, and what the softmax needs
+            const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
+            const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
+            if (IsV) {
+                factors[lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
+            } else {
+                const bool bare_k = __any_sync(0xffffffffu, present && leaves_range(__float_as_uint(ks) & 0x7fffffffu, ek));
+                const bool slow = bare_k || bare_v || __any_sync(0xffffffffu, missing);
+                float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
+                if (lane == 0) {
+                    if (cw == 0) *reinterpret_cast<float2*>(tab) = make_float2(exp2_int(ev), exp2_int(ek));
+                    reinterpret_cast<uint8_t*>(tab)[8 + cw] = slow;
+                }
+                tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
+                float lack = 0.f;
+                // (a scale below the normal range counts as its smallest number)
+                if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
+                tab[4 + 128 + 32 * cw + lane] = lack;
+                const float factor = !present ? 0.f : bare_k ? 1.f : ks * exp2_int(-ek);
+                const __half hi = __float2half(factor);
+                pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));
+            }
         }
-        // ---- move on to the next step, if there is one; its scales are on their way during the conversion
+        // ---- the next step, if there is one; its scales are on their way during the conversion
+        bool live = true;
         if (++step >= last) {
-            live = open();
-        } else if ((step & 3) == 0) {
-            ids = ids_next;
-            ids_next = id_at(32 * (step >> 2) + 32 + lane);
+            if (!IsV && cw == 0) {
+                if (lane == 0) lay_out_job<D>(a, smem, job_full, job_empty, ranges, jobs);
+                __syncwarp();
+            }
+            Job job;
+            live = next_job<D, 32>(smem, job_full, job_empty, jobs, job, a.status);
+            step = job.s0;
+            last = job.s1;
+            n = job.n;
+            head = job.head;
+            trow = a.tables + static_cast<int64_t>(job.seq) * a.max_blocks;
+            opened = live;
         }
-        if (live) find();
+        if (live && (opened || (step & 3) == 0)) {
+            ids = ids_next;
+#pragma unroll 1
+            for (int k = opened ? 0 : 1; k < 2; ++k) {
+                const int b = 32 * ((step >> 2) + k) + lane;
+                int id = -1;
+                if (b < (n + 15) / 16) {
+                    id = __ldg(trow + b);
+                    if (id < 0 || id >= a.num_blocks) {
+                        if (!IsV) atomicOr(a.status, PKV_DEVERR_RANGE);
+                        id = -2;
+                    }
+                }
+                if (k == 0) ids = id;
+                ids_next = id;
+            }
+        }
+        const uint4 *src0 = nullptr, *src1 = nullptr;  // the step's two blocks of this warp
+        if (live) {
+            const int b0 = (step & 3) * 8 + 2 * cw;
+            const int id0 = __shfl_sync(0xffffffffu, ids, b0), id1 = __shfl_sync(0xffffffffu, ids, b0 + 1);
+            // an absent block's codes may be any (its tokens carry no weight): block 0 exists
+            src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
+            src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
+            const int id = lane < 16 ? id0 : id1;
+            present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
+            missing = id == -2;
+            const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (lane & 15);
+            if (!IsV) ks = __ldg(rec);
+            vs = __ldg(rec + 16);
+            if (opened) {  // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
+                const int first = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
+                const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + head) * 32 + lane);
+                sample = step * kChunkStep + (lane & 15) < n ? x : 0.f;
+            }
+        }
+        auto copy_code = [&](int i) { copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock)); };
+        if (it < 0) {
+            if (!live) return;
+#pragma unroll 1
+            for (int i = 0; i < C::kVecs; ++i) copy_code(i);
+            copy_commit();
+            continue;
+        }
         copy_wait_all();
         __syncwarp();  // the factors too
         if (IsV) {
             // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
             uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
-#pragma unroll 1
+#pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * b);
                 const uint4 f0 = f[0], f1 = f[1];
                 const uint32_t c0 = (((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4);
-                const uint4* src = b ? src1 : src0;
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < kPerBlock; ++i) {
-                    uint8_t* slot = mine + (b * kPerBlock + i) * 512;
-                    const uint4 x = *reinterpret_cast<const uint4*>(slot);
+                    const uint4 x = *reinterpret_cast<const uint4*>(mine + 512 * (b * kPerBlock + i));
                     *reinterpret_cast<uint4*>(vd + i * 32 * 128 + c0) = v_values(x.x, x.y, f0);
                     *reinterpret_cast<uint4*>(vd + i * 32 * 128 + (c0 ^ 16)) = v_values(x.z, x.w, f1);
-                    if (live) copy16_async(smem_u32(slot), src + 32 * i);
+                    if (live) copy_code(b * kPerBlock + i);
                 }
             }
         } else {
@@ -460,24 +510,24 @@ __device__ void convert_role(const ChunkArgs& a, const ChunkShape& sh, uint8_t* 
             const int flip = ch >> 2;
             uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
             const int c0 = (ch & 3) * 2 + flip;
-#pragma unroll 2
+#pragma unroll
             for (int i = 0; i < C::kVecs; ++i) {
                 const int row8 = (i * (32 / kLanes) + sub) & 7;
                 const uint32_t f = __shfl_sync(0xffffffffu, pair, i * (32 / kLanes) + sub);
                 const __half2 fh = half2_of(__byte_perm(f, f, 0x1010)), fl = half2_of(__byte_perm(f, f, 0x3232));
-                uint8_t* slot = mine + i * 512;
-                const uint4 x = *reinterpret_cast<const uint4*>(slot);
+                const uint4 x = *reinterpret_cast<const uint4*>(mine + 512 * i);
                 const uint4 x0 = k_values(x.x, x.y, fh, fl), x1 = k_values(x.z, x.w, fh, fl);
                 uint8_t* rowp = kd + i * (32 / kLanes) * 128;
                 *reinterpret_cast<uint4*>(rowp + ((c0 ^ row8) << 4)) = flip ? x1 : x0;
                 *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = flip ? x0 : x1;
-                if (live) copy16_async(smem_u32(slot), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
+                if (live) copy_code(i);
             }
         }
         copy_commit();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
+        if (!live) break;
     }
     copy_wait_all();
 }
@@ -491,16 +541,16 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     uint64_t* k_empty = k_full + C::kStages;
     uint64_t* v_full = k_empty + C::kStages;
     uint64_t* v_empty = v_full + C::kParts;
-    uint64_t* q_full = v_empty + C::kParts;  // [half]: Q rows in place
+    uint64_t* q_full = v_empty + C::kParts;   // [half]: Q rows in place
     uint64_t* s_full = q_full + 2;            // [half][part]: scores in tensor memory
     uint64_t* p_full = s_full + 4;            // [half][part]: weights written
     uint64_t* pv_done = p_full + 4;           // [half][part]: that product has completed
     uint64_t* final_bar = pv_done + 4;        // [issuer]: everything it issued has completed
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem + C::kOffPrefix);  // while planning
+    uint64_t* job_full = final_bar + 4;       // [slot]: segment laid out
+    uint64_t* job_empty = job_full + C::kJobs;  // [slot]: read by all 20 warps
     ChunkPos* ranges = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // two cuts per range
-    int64_t* warp_sum = reinterpret_cast<int64_t*>(smem + C::kOffMisc);
-    volatile int* abort_flag = reinterpret_cast<int*>(smem + C::kOffMisc + C::kThreads / 32 * 8);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kThreads / 32 * 8 + 4);
+    int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kOffMisc);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kThreads / 32 * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x;
@@ -513,34 +563,30 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             mbar_init(&v_full[s], 2);   // the two warps that hold its tokens
             mbar_init(&v_empty[s], 2);  // both value issuers
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&q_full[x], 4);
-            for (int p = 0; p < 2; ++p) {
-                mbar_init(&s_full[2 * x + p], 2);  // the products' completion, and the issuer itself (it has seen the step's table)
-                mbar_init(&p_full[2 * x + p], 4);
-                mbar_init(&pv_done[2 * x + p], 1);
-            }
+        for (int x = 0; x < 2; ++x) mbar_init(&q_full[x], 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 2);  // the products' completion, and the issuer itself (it has seen the step's table)
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&final_bar[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&final_bar[i], 1);
-        *abort_flag = 0;
+        for (int i = 0; i < C::kJobs; ++i) {
+            mbar_init(&job_full[i], 1);
+            mbar_init(&job_empty[i], 20);
+        }
         fence_barrier_init();
     }
     grid_dependency_wait();  // lengths, tables, codes and the workspace may come from the kernel before
     allow_dependents();
     const ChunkShape sh = shape_of(a);
-    const int count = plan_ranges<C::kThreads>(a, sh, prefix, ranges, reinterpret_cast<int64_t*>(smem), warp_sum);
+    const int count = plan_ranges<C::kThreads>(a, sh, reinterpret_cast<int64_t*>(smem + C::kOffPrefix), ranges, reinterpret_cast<int64_t*>(smem), scratch);
     PieceInfo* info = static_cast<PieceInfo*>(a.workspace) + blockIdx.x;
-    ChunkWalk walk;
-    ChunkSegment g;
-    if (count > 0) walk = chunk_begin(ranges);
-    if (count == 0 || !chunk_walk(sh, ranges, count, walk, g)) {  // nothing here
-        if (threadIdx.x == 0) {
-            info->start = count > 0 ? ranges[2 * count - 2] : ChunkPos{a.batch, 0, 0, 0};
-            info->flags = 0;
-        }
+    if (threadIdx.x == 0) info->start = count > 0 ? ranges[2 * count - 2] : ChunkPos{a.batch, 0, 0, 0};
+    if (count == 0) {  // nothing here
+        if (threadIdx.x == 0) info->flags = 0;
         return;
     }
-    walk = chunk_begin(ranges);
+    if (threadIdx.x == 0) *reinterpret_cast<ChunkWalk*>(smem + C::kOffWalk) = chunk_begin(ranges);
     if (warp == C::kScoreWarp) {
         tmem_alloc(tmem_slot, C::kTmemCols);
         tmem_relinquish();
@@ -550,8 +596,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // Registers: launched with 96 a thread, 61440 together, which 256 softmax
-    // threads at 144, 256 converters at 72 and 128 issuers at 48 share.
+    // Registers: launched with 96 a thread, 61440 together, which 256 softmax threads
+    // at 144, 256 converters at 72 and 128 issuers at 48 share.
     if (warp < C::kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it
@@ -560,47 +606,65 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lane_base + C::kColS + 128 * x;
         const uint32_t col_o = tmem + lane_base + C::kColO + 128 * x;
+        // A row of Q, of the output: kRowLanes lanes, 8 elements each; the warp's 32 rows
+        // kRowsAtOnce at a time.
+        constexpr int kRowLanes = D / 8, kRowsAtOnce = 32 / kRowLanes;
+        auto row_of_lane = [&](int i) { return (warp & 3) * 32 + i * kRowsAtOnce + lane / kRowLanes; };
+        auto row_slot = [&](int r, int chunk) {  // 16 bytes of row r of this half in shared memory
+            return smem + C::kOffQ + x * C::kTileBytes + (chunk >> 3) * C::kPartBytes + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+        };
         int it = 0;      // steps this half has taken
         int table = 0;   // steps of the CTA
-        int flags = 0;
+        int jobs = 0, flags = 0;
         bool ok = true;
-        while (ok && chunk_walk(sh, ranges, count, walk, g)) {
-            const int h = g.at.head;
-            const int r0 = g.at.tile * kChunkRows + 128 * x;
-            const int rows = g.q.nq * a.group - r0;  // rows of the half, if positive
-            const int steps = g.s1 - g.at.s;
+        Job job;
+        while (next_job<D, 32>(smem, job_full, job_empty, jobs, job, a.status)) {
+            const int rows = job.rows - 128 * x;  // rows of the half, if positive
+            const int steps = job.s1 - job.s0;
             if (rows <= 0) {
                 table += steps;
                 continue;
             }
+            const int r0 = job.r0 + 128 * x;
             const bool row_ok = rr < rows;
-            const int t = (r0 + rr) / a.group;
-            const int64_t row = (static_cast<int64_t>(g.q.q0) + t) * a.q_heads + h * a.group + (r0 + rr - t * a.group);
-            const int lim = row_ok ? g.q.n - g.q.nq + t : -1;  // the last token the row sees
+            const int lim = row_ok ? job.before + query_of(a, r0 + rr) : -1;  // the last token the row sees
             float row_f = 0.f;  // |scale| log2(e) over the power of two in q'
             {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + row * D);
-                uint32_t top = 0;  // largest |q|, per half word
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                // whole rows into the warp's own slots, then a row per lane, in place (loops
+                // rolled: this runs once per segment, mostly out of a cold instruction cache)
+#pragma unroll 2
+                for (int i = 0; i < kRowLanes; ++i) {
+                    const int r = row_of_lane(i);
+                    uint8_t* slot = row_slot(r, lane % kRowLanes);
+                    if (r < rows)
+                        copy16_async(smem_u32(slot), reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                                                    row_of_unit(a, job.q0, job.head, r0 + r) * D) + lane % kRowLanes);
+                    else
+                        *reinterpret_cast<uint4*>(slot) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                copy_commit();
+                copy_wait_all();
+                __syncwarp();
+                // The row's largest goes to 2^14 .. 2^15 (a row with infinities is left as
+                // it is); the scale's sign goes into q', a zero scale makes q' zero.
+                uint32_t top = 0;
+#pragma unroll 4
+                for (int c = 0; c < kRowLanes; ++c) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(row_slot(rr, c));
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
-                // the row's largest goes to 2^14 .. 2^15 (a row with infinities is left as it is);
-                // the scale's sign goes into q', a zero scale makes q' zero
                 const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // biased exponent
-                const int shift = ex == 255 || ex == 0 ? 0 : min(126, 141 - ex);  // -113 .. 126
+                const int shift = ex == 255 || ex == 0 ? 0 : min(126, 141 - ex);       // -113 .. 126
                 const float mul = a.scale == 0.f ? 0.f : copysignf(exp2_int(shift), a.scale);
                 row_f = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * exp2_int(-shift);
-                uint8_t* qs = smem + C::kOffQ + x * C::kTileBytes + rr * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = row_ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 h = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * mul, bf16hi_to_f32(v.x) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v.y) * mul, bf16hi_to_f32(v.y) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v.z) * mul, bf16hi_to_f32(v.z) * mul),
-                                               pack_f16x2(bf16lo_to_f32(v.w) * mul, bf16hi_to_f32(v.w) * mul));
-                    *reinterpret_cast<uint4*>(qs + (c >> 3) * C::kPartBytes + (((c & 7) ^ (rr & 7)) << 4)) = h;
+#pragma unroll 2
+                for (int c = 0; c < kRowLanes; ++c) {
+                    uint4* slot = reinterpret_cast<uint4*>(row_slot(rr, c));
+                    const uint4 v = *slot;
+                    *slot = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * mul, bf16hi_to_f32(v.x) * mul),
+                                       pack_f16x2(bf16lo_to_f32(v.y) * mul, bf16hi_to_f32(v.y) * mul),
+                                       pack_f16x2(bf16lo_to_f32(v.z) * mul, bf16hi_to_f32(v.z) * mul),
+                                       pack_f16x2(bf16lo_to_f32(v.w) * mul, bf16hi_to_f32(v.w) * mul));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -610,134 +674,129 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             float m = ninf(), l = 0.f, unit = 1.f;
             for (int j = 0; j < steps; ++j, ++it, ++table) {
                 const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes);
-                const int seen = lim - (g.at.s + j) * kChunkStep + 1;  // tokens of the step the row sees
-                const bool masked = (g.at.s + j + 1) * kChunkStep - 1 > warp_lim;
+                const int seen = lim - (job.s0 + j) * kChunkStep + 1;  // tokens of the step the row sees
+                const bool masked = (job.s0 + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    if (!warp_wait(&s_full[2 * x + part], it & 1, a.status, abort_flag)) {
+                    if (!warp_wait(&s_full[2 * x + part], it & 1, a.status)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const float4 modes = *reinterpret_cast<const float4*>(tab);
                     unit = modes.x;
-                    const bool plain = __float_as_uint(modes.z) == 0u;
                     // never 0 or infinite: a hidden score is -inf times it
-                    const float f = plain ? fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f) : row_f;
+                    const float f = fminf(fmaxf(row_f * modes.y, 1.2e-38f), 3e38f);
                     const int seen_part = seen - 64 * part;
                     const uint32_t col = col_s + 64 * part;
-                    // O takes on another maximum (every lane its own factor; all lanes take part)
-                    auto rescale = [&](float mx) {
-                        float alpha = 1.f;
-                        if (mx > m + 8.f || (mx > m && m == ninf())) {
-                            alpha = m == ninf() ? 0.f : ex2(m - mx);
-                            m = mx;
-                            l *= alpha;
-                        }
-                        // O holds something once a part of this segment has been multiplied in:
-                        // the last one is the other part, of this step or of the one before
-                        if (j + part == 0) return true;
-                        if (!warp_wait(&pv_done[2 * x + (part ^ 1)], (it - 1 + part) & 1, a.status, abort_flag)) return false;
-                        tc_fence_after();
+                    // Weights with the maximum as it stands: their sum tells whether it has to
+                    // move (no pass over the scores for it; then, and in slow steps, the part
+                    // is done with care, 16 tokens at a time).
+                    bool careful = __float_as_uint(modes.z) != 0u;
+                    if (!careful) {
+                        if (__any_sync(0xffffffffu, m == ninf() && seen_part > 0)) {
+                            // rows without a maximum (and so without weights yet): theirs is the part's
+                            float mx = ninf();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t ov[16];
-                            tmem_ld16(col_o + c, ov);
-                            tmem_ld_wait();
+                            for (int c = 0; c < 64; c += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(col + c, v);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            tmem_st16(col_o + c, ov);
-                        }
-                        return true;
-                    };
-                    if (plain) {
-                        float sx[64];
-                        {
-                            uint32_t lo[32], hi[32];
-                            tmem_ld32(col, lo);
-                            tmem_ld32(col + 32, hi);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                sx[e] = __uint_as_float(lo[e]);
-                                sx[32 + e] = __uint_as_float(hi[e]);
+                                for (int e = 0; e < 16; ++e) mx = e < seen_part - c ? fmaxf(mx, __uint_as_float(v[e])) : mx;
                             }
+                            if (m == ninf()) m = mx * f;
                         }
-                        if (masked) {
+                        uint32_t sv[32], pw[32];
+                        const float base = m == ninf() ? 0.f : m;
+                        const uint64_t nb2 = f32x2_pack(-base, -base), f2 = f32x2_pack(f, f);
+                        uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if (e >= seen_part) sx[e] = ninf();
-                        }
-                        // Weights with the maximum as it stands; their sum tells whether it has
-                        // to move (the part is then done again): no pass over the scores for it.
-                        uint32_t pw[32];
-                        float sum;
-                        bool first = __any_sync(0xffffffffu, m == ninf() && seen_part > 0);
-#pragma unroll 1
-                        for (int pass = 0;; ++pass) {
-                            if (first || pass > 0) {
-                                float m1[21];
+                        for (int half = 0; half < 2; ++half) {
+                            tmem_ld32(col + 32 * half, sv);
+                            tmem_ld_wait();
+                            if (masked) {
 #pragma unroll
-                                for (int k = 0; k < 21; ++k) m1[k] = fmax3(sx[3 * k], sx[3 * k + 1], sx[3 * k + 2]);
-#pragma unroll
-                                for (int k = 0; k < 7; ++k) m1[k] = fmax3(m1[3 * k], m1[3 * k + 1], m1[3 * k + 2]);
-                                const float mx = fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmaxf(m1[6], sx[63])) * f;
-                                if (!rescale(mx)) {
-                                    ok = false;
-                                    break;
-                                }
+                                for (int e = 0; e < 32; ++e)
+                                    if (e >= seen_part - 32 * half) sv[e] = 0xff800000u;
                             }
-                            const float base = m == ninf() ? 0.f : m;
-                            const uint64_t nb2 = f32x2_pack(-base, -base), f2 = f32x2_pack(f, f);
-                            uint64_t acc0 = f32x2_pack(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                            for (int e = 0; e < 64; e += 2) {
+                            for (int e = 0; e < 32; e += 2) {
                                 float a0, a1;
-                                f32x2_unpack(f32x2_fma(f32x2_pack(sx[e], sx[e + 1]), f2, nb2), a0, a1);
+                                f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), f2, nb2), a0, a1);
                                 const float p0 = ex2(a0), p1 = ex2(a1);
-                                pw[e / 2] = pack_f16x2(p0, p1);
+                                pw[16 * half + e / 2] = pack_f16x2(p0, p1);
                                 if ((e / 2) & 1)
                                     acc1 = f32x2_add(acc1, f32x2_pack(p0, p1));
                                 else
                                     acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
                             }
-                            float s0, s1;
-                            f32x2_unpack(f32x2_add(acc0, acc1), s0, s1);
-                            sum = s0 + s1;
-                            // above 2^14 (or not a number) a weight may have left f16
-                            if (first || pass > 0 || !__any_sync(0xffffffffu, !(sum <= 16384.f))) break;
                         }
-                        if (!ok) break;
-                        l += sum;
-                        tmem_st32(col, pw);
-                    } else {
+                        float s0, s1;
+                        f32x2_unpack(f32x2_add(acc0, acc1), s0, s1);
+                        const float sum = s0 + s1;
+                        // above 2^14 (or not a number) a weight may have left f16
+                        careful = __any_sync(0xffffffffu, !(sum <= 16384.f));
+                        if (!careful) {
+                            l += sum;
+                            tmem_st32(col, pw);
+                        }
+                    }
+                    if (careful) {
                         const float* cp = tab + 4 + 64 * part;
                         float mx = ninf();
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 8) {
-                            float xe[8];
-                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
+                        for (int c = 0; c < 64; c += 16) {
+                            float xe[16];
+                            careful_scores(col + c, cp + c, row_f, seen_part - c, xe);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
+                            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
                         }
-                        if (__any_sync(0xffffffffu, mx > m + 8.f) && !rescale(mx)) {
-                            ok = false;
-                            break;
+                        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                            float alpha = 1.f;
+                            if (mx > m + 8.f) {
+                                alpha = m == ninf() ? 0.f : ex2(m - mx);
+                                m = mx;
+                                l *= alpha;
+                            }
+                            // O holds something once a part of this segment has been multiplied in:
+                            // the last one is the other part, of this step or of the one before
+                            if (j + part > 0) {
+                                if (!warp_wait(&pv_done[2 * x + (part ^ 1)], (it - 1 + part) & 1, a.status)) {
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t ov[16];
+                                    tmem_ld16(col_o + c, ov);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                    tmem_st16(col_o + c, ov);
+                                }
+                            }
                         }
                         const float base = m == ninf() ? 0.f : m;
                         // the weights overwrite scores that have been read
 #pragma unroll 1
-                        for (int c = 0; c < 64; c += 8) {
-                            float xe[8], w[8];
-                            slow_scores(col + c, cp + c, f, seen_part - c, xe);
+                        for (int c = 0; c < 64; c += 16) {
+                            float xe[16];
+                            careful_scores(col + c, cp + c, row_f, seen_part - c, xe);
+                            uint32_t pw[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                w[e] = xe[e] == ninf() ? 0.f : ex2(xe[e] + cp[128 + c + e] - base);
-                                l += xe[e] == ninf() ? 0.f : ex2(xe[e] - base);
+                            for (int e = 0; e < 16; e += 2) {
+                                float w[2];
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const float xu = xe[e + u], lack = cp[128 + c + e + u];
+                                    w[u] = xu == ninf() ? 0.f : ex2(xu + lack - base);
+                                    l += xu == ninf() ? 0.f : lack == 0.f ? w[u] : ex2(xu - base);
+                                }
+                                pw[e / 2] = pack_f16x2(w[0], w[1]);
                             }
-                            const uint32_t pw[4] = {pack_f16x2(w[0], w[1]), pack_f16x2(w[2], w[3]), pack_f16x2(w[4], w[5]),
-                                                    pack_f16x2(w[6], w[7])};
-                            tmem_st4(col + c / 2, pw);
+                            tmem_st8(col + c / 2, pw);
                         }
                     }
                     tmem_st_wait();
@@ -749,44 +808,49 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             }
             if (!ok) break;
             // the products of the last step (part 1 completes after part 0)
-            if (!warp_wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status, abort_flag)) {
+            if (!warp_wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            if (g.whole()) {
+            if (job.piece == 0) {
+                // through the shared memory of this warp's rows of Q, which the scores no longer need
                 const float inv = l == 0.f ? 0.f : unit / l;
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row * D;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t ov[32];
-                    tmem_ld32(col_o + c, ov);
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t ov[16];
+                    tmem_ld16(col_o + c, ov);
                     tmem_ld_wait();
-                    if (row_ok) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                w[u] = pack_bf16x2(__uint_as_float(ov[e + 2 * u]) * inv, __uint_as_float(ov[e + 2 * u + 1]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(ov[8 * u + 2 * e]) * inv, __uint_as_float(ov[8 * u + 2 * e + 1]) * inv);
+                        *reinterpret_cast<uint4*>(row_slot(rr, c / 8 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                __syncwarp();
+#pragma unroll 2
+                for (int i = 0; i < kRowLanes; ++i) {
+                    const int r = row_of_lane(i);
+                    if (r < rows)
+                        *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_of_unit(a, job.q0, job.head, r0 + r) * D) + lane % kRowLanes) =
+                            *reinterpret_cast<const uint4*>(row_slot(r, lane % kRowLanes));
+                }
+                __syncwarp();
             } else {
-                const int slot = g.at.s > 0 ? 0 : 1;
-                flags |= 1 << slot;
-                float* piece = slot_of(a.workspace, grid, D, blockIdx.x, slot);
-                float* dst = piece + (128 * x + rr) * D;
+                flags |= job.piece;
+                float* piece = slot_of(a.workspace, grid, D, blockIdx.x, job.piece - 1);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t ov[32];
-                    tmem_ld32(col_o + c, ov);
+                for (int c = 0; c < D; c += 16) {
+                    uint32_t ov[16];
+                    tmem_ld16(col_o + c, ov);
                     tmem_ld_wait();
                     if (row_ok) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(dst + c + e) =
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4*>(piece + (c + e) * kChunkRows + 4 * (128 * x + rr)) =
                                 make_float4(__uint_as_float(ov[e]) * unit, __uint_as_float(ov[e + 1]) * unit,
                                             __uint_as_float(ov[e + 2]) * unit, __uint_as_float(ov[e + 3]) * unit);
                     }
@@ -798,115 +862,112 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             }
             tc_fence_before();  // the next segment's products overwrite O after this half's next arrival
         }
-        if (threadIdx.x == 0) {  // half A takes part in every segment
-            info->start = ranges[2 * count - 2];
-            info->flags = ok ? flags : 0;
-        }
+        if (threadIdx.x == 0) info->flags = ok ? flags : 0;  // half A takes part in every segment
     } else if (warp < C::kScoreWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        ChunkWalk* where = reinterpret_cast<ChunkWalk*>(ranges + 2 * (kMaxRounds + 1) + 2 * warp);  // every warp its own
         if (warp < C::kConvertWarp + 4)
-            convert_role<D, false>(a, sh, smem, ranges, count, where, k_full, k_empty, abort_flag);
+            convert_role<D, false>(a, smem, count, job_full, job_empty, k_full, k_empty);
         else
-            convert_role<D, true>(a, sh, smem, ranges, count, where, v_full, v_empty, abort_flag);
-    } else if (warp < C::kValueWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        // ------------------------------------------------ scores S = Q K^T of half x (one thread)
-        const int x = warp - C::kScoreWarp;
-        if (lane == 0) {
-            constexpr uint32_t idS = umma_idesc_f16(128, 64);
-            const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
-            int step = 0, it = 0, segs = 0;
-            bool ok = true;
-            while (ok && chunk_walk(sh, ranges, count, walk, g)) {
-                const bool mine = g.q.nq * a.group - g.at.tile * kChunkRows > 128 * x;
-                if (mine) {
-                    if (!wait(&q_full[x], segs & 1, a.status, abort_flag)) break;
-                    ++segs;
-                }
-                for (int j = g.at.s; ok && j < g.s1; ++j, ++step) {
-                    const int st = step & 1;
-                    if (!wait(&k_full[st], (step >> 1) & 1, a.status, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!mine) {
-                        mbar_arrive(&k_empty[st]);
-                        continue;
-                    }
-                    const uint32_t k_base = smem_u32(smem + C::kOffK + st * C::kTileBytes);
-#pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        // the part's weights of the step before lie over its scores
-                        if (it > 0 && !wait(&pv_done[2 * x + part], (it - 1) & 1, a.status, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * C::kPartBytes + (kk & 3) * 32;
-                            umma_bf16(tmem + C::kColS + 128 * x + 64 * part, umma_desc_sw128(q_base + off, 16, 1024),
-                                      umma_desc_sw128(k_base + part * 64 * 128 + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
-                        }
-                        if (part == 1) umma_commit(&k_empty[st]);
-                        umma_commit(&s_full[2 * x + part]);
-                        mbar_arrive(&s_full[2 * x + part]);
-                    }
-                    ++it;
-                }
-            }
-            umma_commit(&final_bar[x]);
-            mbar_wait(&final_bar[x], 0, a.status, nullptr);
-        }
-        __syncwarp();
+            convert_role<D, true>(a, smem, count, job_full, job_empty, v_full, v_empty);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        // ------------------------------------------------ values O += P V of half x (one thread)
-        const int x = warp - C::kValueWarp;
-        if (lane == 0) {
-            constexpr uint32_t idO = umma_idesc_f16(128, D);
-            int st = 0, it = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            while (ok && chunk_walk(sh, ranges, count, walk, g)) {
-                const bool mine = g.q.nq * a.group - g.at.tile * kChunkRows > 128 * x;
-                for (int j = g.at.s; ok && j < g.s1; ++j) {
-#pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        const int now = st;
-                        const uint32_t parity = phase;
-                        if (++st == C::kParts) {
-                            st = 0;
-                            phase ^= 1u;
-                        }
-                        if (!wait(&v_full[now], parity, a.status, abort_flag)) {
+        const int x = warp & 1;
+        if (warp < C::kValueWarp) {
+            // -------------------------------------------- scores S = Q K^T of half x (one thread)
+            if (lane == 0) {
+                constexpr uint32_t idS = umma_idesc_f16(128, 64);
+                const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
+                int step = 0, it = 0, segs = 0, jobs = 0;
+                bool ok = true;
+                Job job;
+                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job, a.status)) {
+                    const bool mine = job.rows > 128 * x;
+                    if (mine) {
+                        if (!wait(&q_full[x], segs & 1, a.status)) break;
+                        ++segs;
+                    }
+                    for (int j = job.s0; ok && j < job.s1; ++j, ++step) {
+                        const int st = step & 1;
+                        if (!wait(&k_full[st], (step >> 1) & 1, a.status)) {
                             ok = false;
                             break;
                         }
                         if (!mine) {
-                            mbar_arrive(&v_empty[now]);
+                            mbar_arrive(&k_empty[st]);
                             continue;
                         }
-                        if (!wait(&p_full[2 * x + part], it & 1, a.status, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t v_base = smem_u32(smem + C::kOffV + now * C::kVPartBytes);
+                        const uint32_t k_base = smem_u32(smem + C::kOffK + st * C::kTileBytes);
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            // the part's weights of the step before lie over its scores
+                            if (it > 0 && !wait(&pv_done[2 * x + part], (it - 1) & 1, a.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 64 * part + 8 * kk,
-                                         umma_desc_sw128(v_base + kk * 32, 16, 1024), idO,
-                                         (j > g.at.s || part > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&pv_done[2 * x + part]);
-                        umma_commit(&v_empty[now]);
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * C::kPartBytes + (kk & 3) * 32;
+                                umma_bf16(tmem + C::kColS + 128 * x + 64 * part, umma_desc_sw128(q_base + off, 16, 1024),
+                                          umma_desc_sw128(k_base + part * 64 * 128 + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                            }
+                            if (part == 1) umma_commit(&k_empty[st]);
+                            umma_commit(&s_full[2 * x + part]);
+                            mbar_arrive(&s_full[2 * x + part]);
+                        }
+                        ++it;
                     }
-                    if (mine) ++it;
                 }
+                umma_commit(&final_bar[x]);
+                wait(&final_bar[x], 0, a.status);
             }
-            umma_commit(&final_bar[2 + x]);
-            mbar_wait(&final_bar[2 + x], 0, a.status, nullptr);
+        } else {
+            // -------------------------------------------- values O += P V of half x (one thread)
+            if (lane == 0) {
+                constexpr uint32_t idO = umma_idesc_f16(128, D);
+                int st = 0, it = 0, jobs = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                Job job;
+                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job, a.status)) {
+                    const bool mine = job.rows > 128 * x;
+                    for (int j = job.s0; ok && j < job.s1; ++j) {
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            const int now = st;
+                            const uint32_t parity = phase;
+                            if (++st == C::kParts) {
+                                st = 0;
+                                phase ^= 1u;
+                            }
+                            if (!wait(&v_full[now], parity, a.status)) {
+                                ok = false;
+                                break;
+                            }
+                            if (!mine) {
+                                mbar_arrive(&v_empty[now]);
+                                continue;
+                            }
+                            if (!wait(&p_full[2 * x + part], it & 1, a.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint32_t v_base = smem_u32(smem + C::kOffV + now * C::kVPartBytes);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 64 * part + 8 * kk,
+                                             umma_desc_sw128(v_base + kk * 32, 16, 1024), idO,
+                                             (j > job.s0 || part > 0 || kk > 0) ? 1u : 0u);
+                            umma_commit(&pv_done[2 * x + part]);
+                            umma_commit(&v_empty[now]);
+                        }
+                        if (mine) ++it;
+                    }
+                }
+                umma_commit(&final_bar[2 + x]);
+                wait(&final_bar[2 + x], 0, a.status);
+            }
         }
         __syncwarp();
     }
@@ -920,13 +981,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 
 // ---------------------------------------------------------------- joining the pieces of cut units
 // CTA (c, y): the unit that begins in CTA c's range and is cut at its end (slot 1
-// of c, then slot 0 of the following CTAs while they begin inside it), rows
-// 32 y .. 32 y + 31, a warp per row: out = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
-constexpr int kCombineRows = 32;
-constexpr int kCombineThreads = 256;
-
+// of c, then slot 0 of the following CTAs while they begin inside it), columns
+// 8 y .. 8 y + 7, a thread per row: out = sum_i O_i 2^(m_i - M) / sum_i l_i 2^(m_i - M).
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const ChunkArgs a, int grid) {
+__global__ void __launch_bounds__(kChunkRows) combine_kernel(const ChunkArgs a, int grid) {
     __shared__ int pieces[kMaxPieces];  // 2 cta + slot
     __shared__ int count;
     grid_dependency_wait();
@@ -934,7 +992,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const ChunkArg
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x;
     const PieceInfo* infos = static_cast<const PieceInfo*>(a.workspace);
-    if (!(infos[c].flags & 2) || c + 1 >= grid) return;
+    if (c + 1 >= grid || !(infos[c].flags & 2)) return;
     const ChunkPos unit = infos[c + 1].start;
     if (warp == 0) {
         int n = 1;
@@ -953,40 +1011,32 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const ChunkArg
         }
         if (lane == 0) count = min(n, kMaxPieces);
     }
-    __syncthreads();
     const ChunkShape sh = shape_of(a);
     ChunkSeq q;
     chunk_seq(sh, unit.seq, q);
-    const int r0 = unit.tile * kChunkRows;
-    const int rows = min(kChunkRows, q.nq * a.group - r0);
-    constexpr int kPer = D / 32;
-    for (int r = blockIdx.y * kCombineRows + warp; r < min(rows, static_cast<int>(blockIdx.y + 1) * kCombineRows); r += kCombineThreads / 32) {
-        float top = ninf();
-        for (int i = lane; i < count; i += 32) {
-            const float* p = slot_of(a.workspace, grid, D, pieces[i] >> 1, pieces[i] & 1);
-            top = fmaxf(top, p[kChunkRows * D + r]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == ninf() ? 0.f : top;
-        float l = 0.f, acc[kPer];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-        for (int i = 0; i < count; ++i) {
-            const float* p = slot_of(a.workspace, grid, D, pieces[i] >> 1, pieces[i] & 1);
-            const float w = ex2(p[kChunkRows * D + r] - base);
-            l += w * p[kChunkRows * (D + 1) + r];
-            const float* src = p + r * D + lane * kPer;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += w * src[e];
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int t = (r0 + r) / a.group;
-        const int64_t row = (static_cast<int64_t>(q.q0) + t) * a.q_heads + unit.head * a.group + (r0 + r - t * a.group);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * D) + lane * (kPer / 2);
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    __syncthreads();
+    const int r = threadIdx.x, R = unit.tile * kChunkRows + r;
+    if (R >= q.nq * a.group) return;
+    float top = ninf();
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) top = fmaxf(top, slot_of(a.workspace, grid, D, pieces[i] >> 1, pieces[i] & 1)[kChunkRows * D + r]);
+    const float base = top == ninf() ? 0.f : top;
+    float l = 0.f, acc[8] = {};
+#pragma unroll 2
+    for (int i = 0; i < count; ++i) {
+        const float* p = slot_of(a.workspace, grid, D, pieces[i] >> 1, pieces[i] & 1);
+        const float4 o0 = *reinterpret_cast<const float4*>(p + (8 * blockIdx.y * kChunkRows + 4 * r));
+        const float4 o1 = *reinterpret_cast<const float4*>(p + ((8 * blockIdx.y + 4) * kChunkRows + 4 * r));
+        const float w = ex2(p[kChunkRows * D + r] - base);
+        l += w * p[kChunkRows * (D + 1) + r];
+        acc[0] += w * o0.x, acc[1] += w * o0.y, acc[2] += w * o0.z, acc[3] += w * o0.w;
+        acc[4] += w * o1.x, acc[5] += w * o1.y, acc[6] += w * o1.z, acc[7] += w * o1.w;
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t row = row_of_unit(a, q.q0, unit.head, R);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 8 * blockIdx.y) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
 }
 
 // CTAs of a launch: one per SM (piece lists hold at most kMaxPieces).
@@ -999,7 +1049,7 @@ cudaError_t run_chunk(const ChunkArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(chunk_q8_kernel<D>, dim3(grid), dim3(Cx<D>::kThreads), Cx<D>::kSmem, s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(combine_kernel<D>, dim3(grid, kChunkRows / kCombineRows), dim3(kCombineThreads), 0, s, a, grid);
+    return launch_pdl(combine_kernel<D>, dim3(grid, D / 8), dim3(kChunkRows), 0, s, a, grid);
 }
 
 }  // namespace

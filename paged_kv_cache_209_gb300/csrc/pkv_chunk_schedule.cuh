@@ -42,6 +42,13 @@ constexpr int kMinPiece = 2;      // a cut leaves at least this many steps on ei
 constexpr int kMaxRounds = 8;     // rounds of whole units, at most
 constexpr int kMinSteps = 3;      // a CTA gets at least about this many two-half steps' cost
 
+// a / b of non-negative numbers (a 64-bit division is a long loop on the GPU, and a
+// launch's planning waits for several).
+PKV_HD inline int64_t chunk_div(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 struct ChunkShape {
     const int32_t* lens;
     const int32_t* qstart;
@@ -130,7 +137,7 @@ PKV_HD inline ChunkPlace chunk_locate(const ChunkShape& a, const int64_t* prefix
     const int64_t base = chunk_cost_base(q, a.group);
     p.unit = ChunkPos{lo, 0, 0, 0};
     p.rem = x - prefix[lo];
-    p.unit.head = static_cast<int>(p.rem / head_cost);
+    p.unit.head = static_cast<int>(chunk_div(p.rem, head_cost));
     p.rem -= p.unit.head * head_cost;
     p.tiles = chunk_tiles(q, a.group);
     lo = 0, hi = p.tiles - 1;
@@ -151,7 +158,7 @@ PKV_HD inline ChunkPlace chunk_locate(const ChunkShape& a, const int64_t* prefix
 PKV_HD inline ChunkPos chunk_step_cut(const ChunkShape& a, const int64_t* prefix, int64_t x) {
     if (x >= prefix[a.batch]) return ChunkPos{a.batch, 0, 0, 0};
     ChunkPlace p = chunk_locate(a, prefix, x);
-    p.unit.s = static_cast<int>(p.rem * p.ns / p.cost);
+    p.unit.s = static_cast<int>(chunk_div(p.rem * p.ns, p.cost));
     if (p.unit.s < kMinPiece)
         p.unit.s = 0;
     else if (p.ns - p.unit.s < kMinPiece)
@@ -171,7 +178,7 @@ PKV_HD inline ChunkPos chunk_unit_cut(const ChunkShape& a, const int64_t* prefix
 
 // CTAs (of `grid`) that get work.
 PKV_HD inline int chunk_ctas(int64_t total, int group, int grid) {
-    const int64_t most = total / (static_cast<int64_t>(kMinSteps) * 2 * kChunkStep * group / 64);
+    const int64_t most = chunk_div(total, static_cast<int64_t>(kMinSteps) * 2 * kChunkStep * group / 64);
     return most >= grid ? grid : (most < 1 ? 1 : static_cast<int>(most));
 }
 // Costliest unit of a sequence.
@@ -191,10 +198,10 @@ struct ChunkRounds {
     int64_t piece;
 };
 PKV_HD inline ChunkRounds chunk_rounds(int64_t total, int64_t most, int ctas) {
-    const int64_t share = total / ctas - most * 3 / 4;
+    const int64_t share = chunk_div(total, ctas) - most * 3 / 4;
     ChunkRounds r{0, most};
     if (share < most) return r;
-    const int64_t n = share / most;
+    const int64_t n = chunk_div(share, most);
     r.rounds = static_cast<int>(n < kMaxRounds ? n : kMaxRounds);
     if (n > kMaxRounds) r.piece = n / kMaxRounds * most;
     return r;
@@ -210,8 +217,10 @@ PKV_HD inline int64_t chunk_dealt(const int64_t* at, const ChunkRounds& r, int c
 PKV_HD inline ChunkPos chunk_rest_cut(const ChunkShape& a, const int64_t* prefix, int64_t from, int64_t due, int64_t all, int c,
                                       int ctas) {
     if (c >= ctas) return ChunkPos{a.batch, 0, 0, 0};
-    const double part = all > 0 ? static_cast<double>(due) / static_cast<double>(all) : 1.0;
-    return chunk_step_cut(a, prefix, from + static_cast<int64_t>(part * static_cast<double>(prefix[a.batch] - from)));
+    const int64_t rest = prefix[a.batch] - from;
+    if (all <= 0) return chunk_step_cut(a, prefix, prefix[a.batch]);
+    if ((rest >> 31) == 0 && (all >> 31) == 0) return chunk_step_cut(a, prefix, from + due * rest / all);
+    return chunk_step_cut(a, prefix, from + static_cast<int64_t>(static_cast<double>(due) / static_cast<double>(all) * static_cast<double>(rest)));
 }
 
 // Walks the segments (unit, steps s0 .. s1 - 1) between two cuts.

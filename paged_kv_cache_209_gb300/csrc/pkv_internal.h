@@ -245,6 +245,7 @@ struct ChunkArgs {
     int32_t group;
     int32_t max_query_len;
     float scale;
+    uint64_t group_inverse;  // ceil(2^37 / group)
 };
 size_t chunk_q8_workspace_bytes(int head_dim);
 cudaError_t launch_chunk_q8(const ChunkArgs& a, cudaStream_t s);
