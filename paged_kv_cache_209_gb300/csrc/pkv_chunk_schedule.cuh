@@ -18,8 +18,11 @@
 // Cost of tile t of a sequence with n tokens, nq of them new: about the tokens
 // it sees plus a start-up worth kOverTokens, in units of 64 / G tokens, linear in
 // t so that a position is found by bisection over closed forms:
-//     w (a + 4 t),   a = ceil(((n - nq + kOverTokens) G + 256) / 64),
-// w = 2, or 1 for a last tile of at most 128 rows (one row half instead of two).
+//     a + 4 t,   a = ceil(((n - nq + kOverTokens) G + 256) / 64).
+// A last tile of few rows costs as much as a full one: converting a step's codes takes
+// as long as its products for both row halves, and the products wait for it. (Counting
+// a tile of one row half as half the work: ragged chunks of 1 to 512 tokens 181 us
+// instead of 147; a start-up of 192 tokens 166, of 640 148, of 1024 149.)
 // The cost only places cuts; a unit's steps are counted exactly.
 //
 // Plain integer arithmetic, compiled for the host as well, where a test checks
@@ -37,10 +40,10 @@ namespace {
 
 constexpr int kChunkRows = 256;   // query rows of a unit
 constexpr int kChunkStep = 128;   // tokens of a step
-constexpr int kOverTokens = 192;  // start-up of a unit (Q, the pipeline's fill, the output) in tokens
+constexpr int kOverTokens = 384;  // start-up of a unit (Q, the pipeline's fill, the output) in tokens
 constexpr int kMinPiece = 2;      // a cut leaves at least this many steps on either side
 constexpr int kMaxRounds = 8;     // rounds of whole units, at most
-constexpr int kMinSteps = 3;      // a CTA gets at least about this many two-half steps' cost
+constexpr int kMinSteps = 3;      // a CTA gets at least about this many steps' cost
 
 // a / b of non-negative numbers (a 64-bit division is a long loop on the GPU, and a
 // launch's planning waits for several).
@@ -89,16 +92,10 @@ PKV_HD inline int64_t chunk_cost_base(const ChunkSeq& q, int group) {
     return (static_cast<int64_t>(q.n - q.nq + kOverTokens) * group + kChunkRows + 63) / 64;
 }
 // Cost of the tiles before t (t < tiles), of tile t, and of all tiles of a head.
-PKV_HD inline int64_t chunk_cost_before(int64_t base, int64_t t) { return 2 * t * base + 4 * t * (t - 1); }
-PKV_HD inline int64_t chunk_tile_cost(const ChunkSeq& q, int group, int64_t base, int t, int tiles) {
-    const int w = t == tiles - 1 && q.nq * group - t * kChunkRows <= kChunkRows / 2 ? 1 : 2;
-    return w * (base + 4 * static_cast<int64_t>(t));
-}
+PKV_HD inline int64_t chunk_cost_before(int64_t base, int64_t t) { return t * base + 2 * t * (t - 1); }
+PKV_HD inline int64_t chunk_tile_cost(int64_t base, int t) { return base + 4 * static_cast<int64_t>(t); }
 PKV_HD inline int64_t chunk_head_cost(const ChunkSeq& q, int group) {
-    const int tiles = chunk_tiles(q, group);
-    if (tiles == 0) return 0;
-    const int64_t base = chunk_cost_base(q, group);
-    return chunk_cost_before(base, tiles - 1) + chunk_tile_cost(q, group, base, tiles - 1, tiles);
+    return chunk_cost_before(chunk_cost_base(q, group), chunk_tiles(q, group));
 }
 
 // The next unit after `p` of `tiles` in its head.
@@ -150,7 +147,7 @@ PKV_HD inline ChunkPlace chunk_locate(const ChunkShape& a, const int64_t* prefix
     }
     p.unit.tile = lo;
     p.rem -= chunk_cost_before(base, lo);
-    p.cost = chunk_tile_cost(q, a.group, base, lo, p.tiles);
+    p.cost = chunk_tile_cost(base, lo);
     p.ns = chunk_steps(q, a.group, lo);
     return p;
 }
@@ -178,17 +175,14 @@ PKV_HD inline ChunkPos chunk_unit_cut(const ChunkShape& a, const int64_t* prefix
 
 // CTAs (of `grid`) that get work.
 PKV_HD inline int chunk_ctas(int64_t total, int group, int grid) {
-    const int64_t most = chunk_div(total, static_cast<int64_t>(kMinSteps) * 2 * kChunkStep * group / 64);
+    const int64_t most = chunk_div(total, static_cast<int64_t>(kMinSteps) * kChunkStep * group / 64);
     return most >= grid ? grid : (most < 1 ? 1 : static_cast<int>(most));
 }
 // Costliest unit of a sequence.
 PKV_HD inline int64_t chunk_most(const ChunkSeq& q, int group) {
     const int tiles = chunk_tiles(q, group);
     if (tiles == 0) return 0;
-    const int64_t base = chunk_cost_base(q, group);
-    const int64_t last = chunk_tile_cost(q, group, base, tiles - 1, tiles);
-    const int64_t before = tiles > 1 ? chunk_tile_cost(q, group, base, tiles - 2, tiles) : 0;
-    return last > before ? last : before;
+    return chunk_tile_cost(chunk_cost_base(q, group), tiles - 1);
 }
 // Rounds of whole units, and the length of their pieces: a multiple of the
 // costliest unit, so that units of one size are dealt evenly. At least three

@@ -59,7 +59,7 @@ void check_case(const std::vector<int>& lens, const std::vector<int>& start, int
         for (int64_t r0 = 0; r0 < rows; r0 += kChunkRows) {
             const int t = static_cast<int>(r0 / kChunkRows);
             CHECK(chunk_cost_before(base, t) == cost, "cost before tile %d", t);
-            cost += ((rows - r0 <= 128) ? 1 : 2) * (base + 4 * t);
+            cost += base + 4 * t;
             // the last token any row of the tile sees
             int seen = 0;
             for (int64_t r = r0; r < r0 + kChunkRows && r < rows; ++r) {
@@ -82,7 +82,7 @@ void check_case(const std::vector<int>& lens, const std::vector<int>& start, int
         chunk_seq(a, i, q);
         int64_t top = 0;
         for (int t = 0; t < chunk_tiles(q, group); ++t) {
-            const int64_t c = chunk_tile_cost(q, group, chunk_cost_base(q, group), t, chunk_tiles(q, group));
+            const int64_t c = chunk_tile_cost(chunk_cost_base(q, group), t);
             if (c > top) top = c;
         }
         CHECK(chunk_most(q, group) == top, "costliest unit of sequence %d", i);
@@ -117,7 +117,7 @@ void check_case(const std::vector<int>& lens, const std::vector<int>& start, int
     int done = 0;
     std::vector<double> work(ctas, 0.0);
     double sum = 0, biggest = 0;
-    for (const Unit& w : units) biggest = w.ns + 1.5 > biggest ? w.ns + 1.5 : biggest;
+    for (const Unit& w : units) biggest = w.ns + 3.0 > biggest ? w.ns + 3.0 : biggest;
     for (int k = 0; k < count; ++k)
         for (int c = 0; c < ctas; ++c) {
             ChunkPos cur = ranges[c][2 * k];
@@ -139,9 +139,7 @@ void check_case(const std::vector<int>& lens, const std::vector<int>& start, int
                     CHECK((g.at.s == 0 || g.at.s >= kMinPiece) && (g.s1 == g.ns || g.ns - g.s1 >= kMinPiece), "cut at %d or %d of %d",
                           g.at.s, g.s1, g.ns);
                 CHECK(n == 0 || g.at.s == 0, "a segment in the middle of a range begins inside a unit");
-                const ChunkSeq& q = g.q;
-                const int half = q.nq * group - g.at.tile * kChunkRows <= 128 ? 1 : 2;
-                work[c] += half * 0.5 * (g.s1 - g.at.s + 1.5);
+                work[c] += g.s1 - g.at.s + 3;
                 done = g.s1;
                 if (done == w.ns) {
                     ++u;
