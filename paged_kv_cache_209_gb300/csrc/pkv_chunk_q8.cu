@@ -67,14 +67,17 @@ struct Cx {
     static constexpr int kConvertWarp = 8;  // K: 8 .. 11, V: 12 .. 15
     static constexpr int kScoreWarp = 16;   // 16, 17
     static constexpr int kValueWarp = 18;   // 18, 19
-    static constexpr int kThreads = 640;
+    static constexpr int kScaleWarp = 20;   // 20 .. 23
+    static constexpr int kThreads = 768;
     static constexpr int kConverters = 128;  // threads that convert K, and V
     static constexpr int kStages = 2;   // K stages (a step each)
     static constexpr int kParts = 3;    // V stages (64 tokens each)
-    // Tables in flight: K's converters run at most four steps ahead of the slower
-    // softmax half (a fifth needs scores that need V parts which that half's
-    // products have yet to release).
-    static constexpr int kTables = 8;
+    static constexpr int kRecords = 3;  // steps whose factors are laid out
+    // Tables in flight: the scale warps write step n once the converters are done with
+    // step n - kRecords; K's then are at most four steps ahead of the slower softmax
+    // half (a fifth needs scores that need V parts which that half's products have
+    // yet to release).
+    static constexpr int kTables = kRecords + 5;
     static constexpr int kJobs = 8;     // segments laid out ahead
     static constexpr int kHalves = D / 64;                    // 128-byte column parts of a K or Q row
     static constexpr int kPartBytes = 128 * 128;              // 128 rows of one part
@@ -89,11 +92,15 @@ struct Cx {
     // a step's table: 2^E, 2^F, a byte per converter warp that is 1 for a slow step; the
     // tokens' K factors [128] and, in log2, what their V values lack [128]
     static constexpr int kTableBytes = 16 + 2 * 128 * 4;
-    static constexpr int kOffScale = kOffTable + kTables * kTableBytes;  // f16 V factors [128]
-    static constexpr int kOffBars = kOffScale + 256;
+    // a step's record: per token (hi, hi, lo, lo) of K's factor in f16 [128], V's factor in
+    // f16 [128]; its 8 blocks' place in the pools, in vectors; whether there is such a step
+    static constexpr int kOffRecord = kOffTable + kTables * kTableBytes;
+    static constexpr int kRecordBytes = 128 * 8 + 128 * 2 + 8 * 8 + 16;
+    static constexpr int kOffBars = kOffRecord + kRecords * kRecordBytes;
     // k_full, k_empty per K stage; v_full, v_empty per V stage; q_full per half;
-    // s_full, p_full, pv_done per half and part; final per issuer; job_full, job_empty
-    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 + 3 * 4 + 4 + 2 * kJobs;
+    // s_full, p_full, pv_done per half and part; final per issuer; job_full, job_empty;
+    // record_full, record_empty
+    static constexpr int kNumBars = 2 * kStages + 2 * kParts + 2 + 3 * 4 + 4 + 2 * kJobs + 2 * kRecords;
     static constexpr int kOffJobs = kOffBars + (kNumBars + 1) / 2 * 16;
     static constexpr int kOffWalk = kOffJobs + kJobs * 48;
     static constexpr int kOffPlan = kOffWalk + (sizeof(ChunkWalk) + 15) / 16 * 16;
@@ -292,7 +299,15 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned in
 // wait by a whole warp, with one answer for all its lanes.
 template <int kSleep = 0>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    return __all_sync(0xffffffffu, wait<kSleep>(bar, parity, status));
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const long long begun = clock64();
+#pragma unroll 1
+    do {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if constexpr (kSleep > 0) __nanosleep(kSleep);
+    } while (__any_sync(0xffffffffu, clock64() - begun < kWaitClocks));
+    atomicOr(status, PKV_DEVERR_TIMEOUT);
+    return false;
 }
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
@@ -302,7 +317,7 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // ---------------------------------------------------------------- segments
-// A segment as the roles need it. The first K converter, ahead of all others, walks
+// A segment as the roles need it. The first of the scale warps, ahead of all others, walks
 // the CTA's ranges and lays the next segment out in shared memory; the others read it
 // there. (Walking in each role cost a dependent chain of global loads at every
 // segment, and its code.)
@@ -358,77 +373,83 @@ __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, u
     mbar_arrive(&job_full[slot]);
 }
 
-// ---------------------------------------------------------------- converters
-// K's (IsV false) or V's four warps: every step of the CTA's range. Warp w takes
-// tokens 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1), lane l the scales of
-// token 32 w + l. A lane copies the codes of the next step into its own slots of
-// shared memory as it takes the current ones out of them (asynchronous copies: a
-// step's time ahead, and no registers). A warp decides by itself whether its tokens
-// are taken as bare codes; both groups read V's scales and decide alike.
-template <int D, bool IsV>
-__device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, int ranges, uint64_t* job_full, uint64_t* job_empty,
-                                             uint64_t* full, uint64_t* empty) {
+// ---------------------------------------------------------------- scales
+// Four warps, ahead of all others: block ids, scales, and what follows from them,
+// for every step of the CTA. Warp w takes tokens 32 w .. 32 w + 31 of a step (blocks
+// 2 w, 2 w + 1), lane l token 32 w + l. They decide whether 32 tokens are taken as
+// bare codes. (In the converters' own loop this was 2000 of 5200 cycles a step, and
+// that loop was what everything waited for.)
+template <int D>
+__device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, int ranges, uint64_t* job_full, uint64_t* job_empty,
+                                           uint64_t* full, uint64_t* empty) {
     using C = Cx<D>;
     const int lane = threadIdx.x & 31;
     const int cw = (threadIdx.x >> 5) & 3;
-    constexpr int kPerBlock = C::kVecs / 2;    // vectors of a lane in each of the warp's two blocks
-    constexpr int kLanes = D / 16;             // lanes that hold one token's K row
-    constexpr int kBlockVecs = D;              // vectors of one (block, head)
-    const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes);
-    uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
-
     int jobs = 0;
     int step = 0, last = 0;         // step being loaded, one past the segment's last
     int n = 0, head = 0;            // its tokens, KV head
     const int32_t* trow = nullptr;  // its block table
     int ids = 0, ids_next = 0;      // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
-    int ev = 0, ek = 0;             // E and F of the segment being converted
+    int ev = 0, ek = 0;             // E and F of the segment
     float sample = 0.f;             // what they are taken from
     bool opened = false;            // they are still to be taken
-    // the loaded step: the scales of the lane's token, whether it exists or lies in a block outside the pool
+    // the loaded step: the token's scales, its block's row of the pools, whether it exists or lies in a block outside the pool
     float ks = 0.f, vs = 0.f;
-    bool present = false, missing = false;
+    int64_t row = 0;
+    bool present = false, missing = false, live = false;
+    int slot = 0, table = 0;
+    uint32_t parity = 1;
     for (int it = -1;; ++it) {
-        const int st = IsV ? (2 * it + (cw >> 1)) % C::kParts : it & 1;  // K's stage of the step, V's of the half with this warp's tokens
-        uint32_t pair = 0;                                               // K: (hi, lo) of the lane's factor
-        __half* factors = reinterpret_cast<__half*>(smem + C::kOffScale) + 32 * cw;
         if (it >= 0) {
-            const uint32_t parity = static_cast<uint32_t>((IsV ? (2 * it + (cw >> 1)) / C::kParts : it >> 1) & 1) ^ 1u;
-            if (!warp_wait<40>(&empty[st], parity, a.status)) break;
-            if (opened) {
-                const uint32_t x = __float_as_uint(sample) & 0x7fffffffu;
-                const bool use = x < 0x7f800000u;
-                ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
-                ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
-                opened = false;
-            }
-            // ---- the lane's token: its factor, and what the softmax needs
-            const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-            const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
-            if (IsV) {
-                factors[lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
-            } else {
+            if (!warp_wait<20>(&empty[slot], parity, a.status)) break;
+            uint8_t* record = smem + C::kOffRecord + slot * C::kRecordBytes;
+            if (live) {
+                if (opened) {
+                    const uint32_t x = __float_as_uint(sample) & 0x7fffffffu;
+                    const bool use = x < 0x7f800000u;
+                    ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
+                    ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
+                    opened = false;
+                }
+                const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
+                const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
                 const bool bare_k = __any_sync(0xffffffffu, present && leaves_range(__float_as_uint(ks) & 0x7fffffffu, ek));
                 const bool slow = bare_k || bare_v || __any_sync(0xffffffffu, missing);
-                float* tab = reinterpret_cast<float*>(smem + C::kOffTable + (it & (C::kTables - 1)) * C::kTableBytes);
+                float* tab = reinterpret_cast<float*>(smem + C::kOffTable + table * C::kTableBytes);
                 if (lane == 0) {
                     if (cw == 0) *reinterpret_cast<float2*>(tab) = make_float2(exp2_int(ev), exp2_int(ek));
                     reinterpret_cast<uint8_t*>(tab)[8 + cw] = slow;
                 }
-                tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
-                float lack = 0.f;
-                // (a scale below the normal range counts as its smallest number)
-                if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
-                tab[4 + 128 + 32 * cw + lane] = lack;
+                if (slow) {
+                    tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
+                    float lack = 0.f;
+                    // (a scale below the normal range counts as its smallest number)
+                    if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
+                    tab[4 + 128 + 32 * cw + lane] = lack;
+                } else {
+                    tab[4 + 32 * cw + lane] = exp2_int(ek);  // another warp's tokens may make the step slow
+                    tab[4 + 128 + 32 * cw + lane] = 0.f;
+                }
                 const float factor = !present ? 0.f : bare_k ? 1.f : ks * exp2_int(-ek);
-                const __half hi = __float2half(factor);
-                pair = bits(__halves2half2(hi, __float2half(factor - __half2float(hi))));
+                const __half hi = __float2half(factor), lo = __float2half(factor - __half2float(hi));
+                *reinterpret_cast<uint2*>(record + (32 * cw + lane) * 8) = make_uint2(bits(__halves2half2(hi, hi)), bits(__halves2half2(lo, lo)));
+                reinterpret_cast<__half*>(record + 1024)[32 * cw + lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
+                if ((lane & 15) == 0) reinterpret_cast<int64_t*>(record + 1280)[2 * cw + lane / 16] = row * D;
             }
+            if (lane == 0) reinterpret_cast<int*>(record + 1344)[cw] = live;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]);
+            if (!live) break;
+            if (++slot == C::kRecords) {
+                slot = 0;
+                parity ^= 1u;
+            }
+            if (++table == C::kTables) table = 0;
         }
-        // ---- the next step, if there is one; its scales are on their way during the conversion
-        bool live = true;
+        // ---- the next step, if there is one
+        live = true;
         if (++step >= last) {
-            if (!IsV && cw == 0) {
+            if (cw == 0) {
                 if (lane == 0) lay_out_job<D>(a, smem, job_full, job_empty, ranges, jobs);
                 __syncwarp();
             }
@@ -441,7 +462,8 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
             trow = a.tables + static_cast<int64_t>(job.seq) * a.max_blocks;
             opened = live;
         }
-        if (live && (opened || (step & 3) == 0)) {
+        if (!live) continue;
+        if (opened || (step & 3) == 0) {
             ids = ids_next;
 #pragma unroll 1
             for (int k = opened ? 0 : 1; k < 2; ++k) {
@@ -450,7 +472,7 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                 if (b < (n + 15) / 16) {
                     id = __ldg(trow + b);
                     if (id < 0 || id >= a.num_blocks) {
-                        if (!IsV) atomicOr(a.status, PKV_DEVERR_RANGE);
+                        atomicOr(a.status, PKV_DEVERR_RANGE);
                         id = -2;
                     }
                 }
@@ -458,76 +480,151 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                 ids_next = id;
             }
         }
-        const uint4 *src0 = nullptr, *src1 = nullptr;  // the step's two blocks of this warp
-        if (live) {
-            const int b0 = (step & 3) * 8 + 2 * cw;
-            const int id0 = __shfl_sync(0xffffffffu, ids, b0), id1 = __shfl_sync(0xffffffffu, ids, b0 + 1);
-            // an absent block's codes may be any (its tokens carry no weight): block 0 exists
-            src0 = codes + (static_cast<int64_t>(max(0, id0)) * a.kv_heads + head) * kBlockVecs + lane;
-            src1 = codes + (static_cast<int64_t>(max(0, id1)) * a.kv_heads + head) * kBlockVecs + lane;
-            const int id = lane < 16 ? id0 : id1;
-            present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
-            missing = id == -2;
-            const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + head) * 32 + (lane & 15);
-            if (!IsV) ks = __ldg(rec);
-            vs = __ldg(rec + 16);
-            if (opened) {  // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
-                const int first = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
-                const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + head) * 32 + lane);
-                sample = step * kChunkStep + (lane & 15) < n ? x : 0.f;
-            }
+        const int id = __shfl_sync(0xffffffffu, ids, (step & 3) * 8 + 2 * cw + lane / 16);
+        present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
+        missing = id == -2;
+        // an absent block's codes may be any (its tokens carry no weight): block 0 exists
+        row = static_cast<int64_t>(max(0, id)) * a.kv_heads + head;
+        const float* rec = a.scales + row * 32 + (lane & 15);
+        ks = __ldg(rec);
+        vs = __ldg(rec + 16);
+        if (opened) {  // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
+            const int first = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
+            const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + head) * 32 + lane);
+            sample = step * kChunkStep + (lane & 15) < n ? x : 0.f;
         }
-        auto copy_code = [&](int i) { copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock)); };
+    }
+}
+
+// ---------------------------------------------------------------- converters
+// K's (IsV false) or V's four warps: every step of the CTA. Warp w takes tokens
+// 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1). A lane copies the codes of the
+// next step into its own slots of shared memory as it takes the current ones out of
+// them (asynchronous copies: a step's time ahead, and no registers).
+template <int D, bool IsV>
+__device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, uint64_t* rec_full, uint64_t* rec_empty, uint64_t* full,
+                                             uint64_t* empty) {
+    using C = Cx<D>;
+    const int lane = threadIdx.x & 31;
+    const int cw = (threadIdx.x >> 5) & 3;
+    constexpr int kPerBlock = C::kVecs / 2;    // vectors of a lane in each of the warp's two blocks
+    constexpr int kLanes = D / 16;             // lanes that hold one token's K row
+    const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes) + lane;
+    uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
+    const uint4 *src0 = nullptr, *src1 = nullptr;  // the next step's two blocks of this warp
+    auto copy_code = [&](int i) { copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock)); };
+    int slot = 0, next_slot = 0;     // records of the step and of the next
+    uint32_t parity = 0;             // of the next record
+    int st = IsV ? cw >> 1 : 0;      // stage: V's of the half with this warp's tokens
+    uint32_t st_parity = 1;
+    for (int it = -1;; ++it) {
+        if (!warp_wait<20>(&rec_full[next_slot], parity, a.status)) break;
+        const uint8_t* next = smem + C::kOffRecord + next_slot * C::kRecordBytes;
+        const bool live = reinterpret_cast<const int*>(next + 1344)[cw] != 0;
+        if (live) {
+            const longlong2 rows = *reinterpret_cast<const longlong2*>(next + 1280 + 16 * cw);
+            src0 = codes + rows.x;
+            src1 = codes + rows.y;
+        }
+        const uint8_t* record = smem + C::kOffRecord + slot * C::kRecordBytes;
         if (it < 0) {
             if (!live) return;
 #pragma unroll 1
             for (int i = 0; i < C::kVecs; ++i) copy_code(i);
             copy_commit();
-            continue;
-        }
-        copy_wait_all();
-        __syncwarp();  // the factors too
-        if (IsV) {
-            // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
-            uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint4* f = reinterpret_cast<const uint4*>(factors + 16 * b);
-                const uint4 f0 = f[0], f1 = f[1];
-                const uint32_t c0 = (((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4);
-#pragma unroll
-                for (int i = 0; i < kPerBlock; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(mine + 512 * (b * kPerBlock + i));
-                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + c0) = v_values(x.x, x.y, f0);
-                    *reinterpret_cast<uint4*>(vd + i * 32 * 128 + (c0 ^ 16)) = v_values(x.z, x.w, f1);
-                    if (live) copy_code(b * kPerBlock + i);
+        } else {
+            if (!warp_wait<20>(&empty[st], st_parity, a.status)) break;
+            copy_wait_all();
+            // Two vectors at a time, the next two on their way out of shared memory; in
+            // rolled loops: unrolled, the kernel's loops leave the instruction cache
+            // (prefill of 8 sequences by 512 tokens: 627 us, this way 546).
+            if (IsV) {
+                // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
+                uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
+                const uint8_t* factors = record + 1024 + 64 * cw;
+                uint4 x0 = *reinterpret_cast<const uint4*>(mine), x1 = *reinterpret_cast<const uint4*>(mine + 512);
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b) {
+                    const uint4 f0 = *reinterpret_cast<const uint4*>(factors + 32 * b), f1 = *reinterpret_cast<const uint4*>(factors + 32 * b + 16);
+                    uint8_t* c0 = vd + (((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4);
+                    uint8_t* c1 = vd + ((((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4) ^ 16);
+                    const uint4* src = b == 0 ? src0 : src1;
+                    uint8_t* in = mine + 512 * kPerBlock * b;
+#pragma unroll 1
+                    for (int i = 0; i < kPerBlock; i += 2) {
+                        const uint8_t* ahead = b * kPerBlock + i + 2 < C::kVecs ? in + 512 * (i + 2) : in;
+                        const uint4 y0 = *reinterpret_cast<const uint4*>(ahead), y1 = *reinterpret_cast<const uint4*>(ahead + 512);
+                        *reinterpret_cast<uint4*>(c0 + i * 32 * 128) = v_values(x0.x, x0.y, f0);
+                        *reinterpret_cast<uint4*>(c1 + i * 32 * 128) = v_values(x0.z, x0.w, f1);
+                        *reinterpret_cast<uint4*>(c0 + (i + 1) * 32 * 128) = v_values(x1.x, x1.y, f0);
+                        *reinterpret_cast<uint4*>(c1 + (i + 1) * 32 * 128) = v_values(x1.z, x1.w, f1);
+                        if (live) {
+                            copy16_async(smem_u32(in + 512 * i), src + 32 * i);
+                            copy16_async(smem_u32(in + 512 * (i + 1)), src + 32 * (i + 1));
+                        }
+                        x0 = y0;
+                        x1 = y1;
+                    }
+                }
+            } else {
+                // ---- token rows: vector i of a lane lies in row 32 cw + i * (32 / kLanes) + lane / kLanes
+                const int ch = lane % kLanes, sub = lane / kLanes;
+                // lanes of the second column part take their halves in the other order: no bank is hit twice
+                const int flip = ch >> 2;
+                uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
+                const int c0 = (ch & 3) * 2 + flip;
+                const uint8_t* first = mine + 8 * flip;
+                const uint8_t* second = mine + 8 * (flip ^ 1);
+                const uint8_t* factors = record + (32 * cw + sub) * 8;
+                constexpr int kRows = 32 / kLanes;  // token rows of a vector index
+                struct Two {
+                    uint2 x, y, f;
+                };
+                auto take = [&](int i) {
+                    return Two{*reinterpret_cast<const uint2*>(first + 512 * i), *reinterpret_cast<const uint2*>(second + 512 * i),
+                               *reinterpret_cast<const uint2*>(factors + i * kRows * 8)};
+                };
+                auto put = [&](int i, const Two& t) {
+                    const int row8 = (i * kRows + sub) & 7;
+                    uint8_t* rowp = kd + i * kRows * 128;
+                    *reinterpret_cast<uint4*>(rowp + ((c0 ^ row8) << 4)) = k_values(t.x.x, t.x.y, half2_of(t.f.x), half2_of(t.f.y));
+                    *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = k_values(t.y.x, t.y.y, half2_of(t.f.x), half2_of(t.f.y));
+                };
+                Two t0 = take(0), t1 = take(1);
+#pragma unroll 1
+                for (int i = 0; i < C::kVecs; i += 2) {
+                    const int ahead = (i + 2) % C::kVecs;  // (after the last, values that are not used)
+                    const Two n0 = take(ahead), n1 = take(ahead + 1);
+                    put(i, t0);
+                    put(i + 1, t1);
+                    if (live) {
+                        const uint4* src = i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock);
+                        copy16_async(smem_u32(mine + 512 * i), src);
+                        copy16_async(smem_u32(mine + 512 * (i + 1)), src + 32);
+                    }
+                    t0 = n0;
+                    t1 = n1;
                 }
             }
-        } else {
-            // ---- token rows: vector i of a lane lies in row 32 cw + i * (32 / kLanes) + lane / kLanes
-            const int ch = lane % kLanes, sub = lane / kLanes;
-            // lanes of the second column part write their halves in the other order: no bank is hit twice
-            const int flip = ch >> 2;
-            uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
-            const int c0 = (ch & 3) * 2 + flip;
-#pragma unroll
-            for (int i = 0; i < C::kVecs; ++i) {
-                const int row8 = (i * (32 / kLanes) + sub) & 7;
-                const uint32_t f = __shfl_sync(0xffffffffu, pair, i * (32 / kLanes) + sub);
-                const __half2 fh = half2_of(__byte_perm(f, f, 0x1010)), fl = half2_of(__byte_perm(f, f, 0x3232));
-                const uint4 x = *reinterpret_cast<const uint4*>(mine + 512 * i);
-                const uint4 x0 = k_values(x.x, x.y, fh, fl), x1 = k_values(x.z, x.w, fh, fl);
-                uint8_t* rowp = kd + i * (32 / kLanes) * 128;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ row8) << 4)) = flip ? x1 : x0;
-                *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = flip ? x0 : x1;
-                if (live) copy_code(i);
+            copy_commit();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&full[st]);
+                mbar_arrive(&rec_empty[slot]);
+            }
+            if (!live) break;
+            st += IsV ? 2 : 1;
+            if (st >= (IsV ? C::kParts : C::kStages)) {
+                st -= IsV ? C::kParts : C::kStages;
+                st_parity ^= 1u;
             }
         }
-        copy_commit();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-        if (!live) break;
+        slot = next_slot;
+        if (++next_slot == C::kRecords) {
+            next_slot = 0;
+            parity ^= 1u;
+        }
     }
     copy_wait_all();
 }
@@ -547,7 +644,9 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     uint64_t* pv_done = p_full + 4;           // [half][part]: that product has completed
     uint64_t* final_bar = pv_done + 4;        // [issuer]: everything it issued has completed
     uint64_t* job_full = final_bar + 4;       // [slot]: segment laid out
-    uint64_t* job_empty = job_full + C::kJobs;  // [slot]: read by all 20 warps
+    uint64_t* job_empty = job_full + C::kJobs;  // [slot]: read by the softmax, issuer and scale warps
+    uint64_t* rec_full = job_empty + C::kJobs;  // [slot]: a step's factors laid out
+    uint64_t* rec_empty = rec_full + C::kRecords;  // [slot]: read by the converters
     ChunkPos* ranges = reinterpret_cast<ChunkPos*>(smem + C::kOffPlan);  // two cuts per range
     int64_t* scratch = reinterpret_cast<int64_t*>(smem + C::kOffMisc);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + C::kThreads / 32 * 8);
@@ -572,7 +671,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         }
         for (int i = 0; i < C::kJobs; ++i) {
             mbar_init(&job_full[i], 1);
-            mbar_init(&job_empty[i], 20);
+            mbar_init(&job_empty[i], 16);
+        }
+        for (int i = 0; i < C::kRecords; ++i) {
+            mbar_init(&rec_full[i], 4);
+            mbar_init(&rec_empty[i], 8);
         }
         fence_barrier_init();
     }
@@ -596,10 +699,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // Registers: launched with 96 a thread, 61440 together, which 256 softmax threads
-    // at 144, 256 converters at 72 and 128 issuers at 48 share.
+    // Registers: launched with 80 a thread, 61440 together, which 256 softmax threads at
+    // 120, 256 converters at 72, 128 issuers at 40 and 128 threads for the scales at 56
+    // share: none spills in its loop. (A few spilled words there cost a tenth.)
     if (warp < C::kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it
         const int x = warp >> 2;
         const int rr = (warp & 3) * 32 + lane;
@@ -614,7 +718,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             return smem + C::kOffQ + x * C::kTileBytes + (chunk >> 3) * C::kPartBytes + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
         };
         int it = 0;      // steps this half has taken
-        int table = 0;   // steps of the CTA
+        uint32_t table = 0;   // steps of the CTA
         int jobs = 0, flags = 0;
         bool ok = true;
         Job job;
@@ -673,7 +777,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             const int warp_lim = __reduce_min_sync(0xffffffffu, lim);
             float m = ninf(), l = 0.f, unit = 1.f;
             for (int j = 0; j < steps; ++j, ++it, ++table) {
-                const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table & (C::kTables - 1)) * C::kTableBytes);
+                const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table % C::kTables) * C::kTableBytes);
                 const int seen = lim - (job.s0 + j) * kChunkStep + 1;  // tokens of the step the row sees
                 const bool masked = (job.s0 + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
@@ -866,11 +970,14 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     } else if (warp < C::kScoreWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp < C::kConvertWarp + 4)
-            convert_role<D, false>(a, smem, count, job_full, job_empty, k_full, k_empty);
+            convert_role<D, false>(a, smem, rec_full, rec_empty, k_full, k_empty);
         else
-            convert_role<D, true>(a, smem, count, job_full, job_empty, v_full, v_empty);
+            convert_role<D, true>(a, smem, rec_full, rec_empty, v_full, v_empty);
+    } else if (warp >= C::kScaleWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        scale_role<D>(a, smem, count, job_full, job_empty, rec_full, rec_empty);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         const int x = warp & 1;
         if (warp < C::kValueWarp) {
             // -------------------------------------------- scores S = Q K^T of half x (one thread)
