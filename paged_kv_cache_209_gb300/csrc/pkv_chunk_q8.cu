@@ -21,7 +21,7 @@
 // maximum is then taken over tokens the row sees.
 //
 // K's scale sits in the K operand, not in the softmax, because a factor per token
-// costs every row a multiplication and a shared-memory broadcast, 1024 of the 2048
+// costs every row a multiplication and a shared-memory broadcast, 1024 of the 2500
 // cycles that a step's products take: the softmax would be the bound.
 //
 // Work (pkv_chunk_schedule.cuh): one persistent CTA per SM takes a range of
@@ -29,19 +29,29 @@
 // two row halves A and B of 128. A unit cut by a range leaves fp32 pieces
 // (O, m, l) in the workspace, which combine_kernel joins.
 //
-// Roles (20 warps). Warps 0-3 and 4-7: the softmax of halves A and B, one thread
-// per query row. Warps 8-11 and 12-15: the converters of K and of V; they load
-// the codes of the next step from global memory into registers while they turn
-// the previous loads into scaled f16, in the 128-byte-swizzled layout the tensor
-// cores read; K's also write the step's exponents and, for a slow step, its factors. Warps 16
-// and 17: one thread each issues S = Q K^T of A and of B; warps 18 and 19: O += P V
-// of A and of B, in two parts of 64 tokens.
+// Roles (24 warps). Warps 0-3 and 4-7: the softmax of halves A and B, one thread
+// per query row. Warps 8-11 and 12-15: the converters of K and of V: codes and
+// factors to scaled f16, in the 128-byte-swizzled layout the tensor cores read.
+// Warps 16 and 17: one thread each issues S = Q K^T of A and of B; warps 18 and 19:
+// O += P V of A and of B, in two parts of 64 tokens. Warps 20-23 run ahead: the
+// segments, block ids, scales and the factors that follow from them.
 //
 // Tensor memory (512 columns): S of A and B, in two parts of 64 tokens (64 fp32
 // columns each; the part's P is written over the first 32), O of A and B. The parts'
 // buffers are independent: while the softmax takes one, the other's products and
 // next scores run. Shared memory: Q 64 KB, two stages of K of 32 KB each, three of V
 // of 16 KB, the next step's codes 32 KB.
+//
+// What bounds it: instructions. A step's products would take 2500 cycles of the
+// tensor cores at the rate a large matrix product reaches; the step takes about 4050,
+// in which the schedulers issue two of three slots: 1000 of 2700 instructions per
+// scheduler for the softmax, 900 for the conversion. Both loops are that long with
+// every instruction they need at 7 cycles a warp, the cost of sharing a scheduler and
+// the instruction cache. So the loops are short rather than unrolled, and everything
+// that is done once per step or segment sits in warps of its own. 8 sequences of 8192
+// tokens, 512 of them new, 32 query heads on 8 of 128: 502 us, 1061 TFLOP/s of the
+// visible pairs (the cuBLAS rate is 1956); 32768 tokens, 2048 new: 485 us, 1130.
+// Eight warps for K instead of four (56 registers for a converter): 518 us.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -69,7 +79,6 @@ struct Cx {
     static constexpr int kValueWarp = 18;   // 18, 19
     static constexpr int kScaleWarp = 20;   // 20 .. 23
     static constexpr int kThreads = 768;
-    static constexpr int kConverters = 128;  // threads that convert K, and V
     static constexpr int kStages = 2;   // K stages (a step each)
     static constexpr int kParts = 3;    // V stages (64 tokens each)
     static constexpr int kRecords = 3;  // steps whose factors are laid out
@@ -436,7 +445,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 reinterpret_cast<__half*>(record + 1024)[32 * cw + lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
                 if ((lane & 15) == 0) reinterpret_cast<int64_t*>(record + 1280)[2 * cw + lane / 16] = row * D;
             }
-            if (lane == 0) reinterpret_cast<int*>(record + 1344)[cw] = live;
+            if (cw == 0 && lane == 0) *reinterpret_cast<int*>(record + 1344) = live;
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
             if (!live) break;
@@ -512,7 +521,6 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
     const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes) + lane;
     uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
     const uint4 *src0 = nullptr, *src1 = nullptr;  // the next step's two blocks of this warp
-    auto copy_code = [&](int i) { copy16_async(smem_u32(mine) + 512 * i, i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock)); };
     int slot = 0, next_slot = 0;     // records of the step and of the next
     uint32_t parity = 0;             // of the next record
     int st = IsV ? cw >> 1 : 0;      // stage: V's of the half with this warp's tokens
@@ -520,7 +528,7 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
     for (int it = -1;; ++it) {
         if (!warp_wait<20>(&rec_full[next_slot], parity, a.status)) break;
         const uint8_t* next = smem + C::kOffRecord + next_slot * C::kRecordBytes;
-        const bool live = reinterpret_cast<const int*>(next + 1344)[cw] != 0;
+        const bool live = *reinterpret_cast<const int*>(next + 1344) != 0;
         if (live) {
             const longlong2 rows = *reinterpret_cast<const longlong2*>(next + 1280 + 16 * cw);
             src0 = codes + rows.x;
@@ -530,14 +538,15 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
         if (it < 0) {
             if (!live) return;
 #pragma unroll 1
-            for (int i = 0; i < C::kVecs; ++i) copy_code(i);
+            for (int i = 0; i < C::kVecs; ++i)
+                copy16_async(smem_u32(mine + 512 * i), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
             copy_commit();
         } else {
             if (!warp_wait<20>(&empty[st], st_parity, a.status)) break;
             copy_wait_all();
             // Two vectors at a time, the next two on their way out of shared memory; in
-            // rolled loops: unrolled, the kernel's loops leave the instruction cache
-            // (prefill of 8 sequences by 512 tokens: 627 us, this way 546).
+            // rolled loops: unrolled, the kernel's loops leave the instruction cache (8
+            // sequences by 512 new tokens: 627 us unrolled, 546 rolled, 503 in this form).
             if (IsV) {
                 // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
                 uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
@@ -655,7 +664,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     const int grid = gridDim.x;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&k_full[s], C::kConverters / 32);
+            mbar_init(&k_full[s], 4);
             mbar_init(&k_empty[s], 2);  // both score issuers
         }
         for (int s = 0; s < C::kParts; ++s) {
