@@ -422,8 +422,11 @@ PKV_API pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, c
 /*
  * pkv_multiquery_q8_workspace_size -- bytes of workspace
  * pkv_multiquery_attention_q8 needs (zero-fill once before first use; completed
- * calls leave its counters at zero; one workspace per call in flight). Returns 0
- * for sizes the call rejects.
+ * calls leave its counters at zero; one workspace per call in flight, and none
+ * shared with other calls; zero it again after PKV_DEVERR_TIMEOUT). A workspace
+ * of the size for the largest batch and max_query_len serves all smaller calls
+ * over pools of the same num_kv_heads and head_dim, in any order. Returns 0 for
+ * sizes the call rejects.
  */
 PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
                                                 int32_t max_query_len, const pkv_cache_desc* desc);

@@ -634,38 +634,23 @@ size_t pkv_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t 
                               mq_num_ctas(desc->head_dim, batch, opts, true), &co, &po);
 }
 
-pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
-                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                   const int32_t* context_lens, const int32_t* query_start, int32_t batch,
-                                   int32_t num_q_heads, int32_t max_query_len, float scale, void* out,
-                                   void* workspace, size_t workspace_bytes, const pkv_cache_desc* desc,
-                                   uint32_t flags, const pkv_decode_opts* opts, void* stream) {
-    NvtxRange nvtx_range("pkv_decode_attention_q8");
-    pkv_status st = check_desc_q8(desc, true);
-    if (st != PKV_OK) return st;
-    if (batch < 0 || !q_heads_ok(num_q_heads, desc)) return PKV_ERR_SHAPE;
-    if (!isfinite(scale) || max_query_len < 1) return PKV_ERR_SHAPE;
-    if (opts != nullptr && opts->num_ctas < 0) return PKV_ERR_SHAPE;
+// The split kernel over int8 pools (arguments checked). The workspace holds the
+// counters of `counted` sequences, then the pieces.
+static pkv_status run_split_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* query_start, int32_t batch, int32_t num_q_heads, int32_t max_query_len,
+                               float scale, void* out, void* workspace, size_t workspace_bytes, int32_t counted,
+                               const pkv_cache_desc* desc, uint32_t flags, const pkv_decode_opts* opts, void* stream) {
     const int G = num_q_heads / desc->num_kv_heads;
-    if (max_query_len * G > kMqMaxRows) return PKV_ERR_UNSUPPORTED;
-    if (query_start == nullptr && max_query_len != 1) return PKV_ERR_SHAPE;
-    if (batch == 0) return PKV_OK;
-    if (!table_width_ok(batch, max_blocks_per_seq)) return PKV_ERR_SHAPE;
-    if (!q || !k_codes || !v_codes || !scales || !block_tables || !context_lens || !out || !workspace)
-        return PKV_ERR_NULL;
-    if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(scales) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
-        (reinterpret_cast<uintptr_t>(context_lens) & 3u) || (reinterpret_cast<uintptr_t>(query_start) & 3u) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return PKV_ERR_ALIGN;
     const int num_ctas = mq_num_ctas(desc->head_dim, batch, opts, true);
     size_t co = 0, po = 0;
-    const size_t need = mq_workspace_bytes(batch, desc->num_kv_heads, desc->head_dim, num_ctas, &co, &po);
+    const size_t need = mq_workspace_bytes(counted, desc->num_kv_heads, desc->head_dim, num_ctas, &co, &po);
     if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned int* status = device_info().status;
     if (status == nullptr) return PKV_ERR_CUDA;
     if (flags & PKV_FLAG_CHECKED) {
-        st = run_checked([&](unsigned int* verdict) {
+        const pkv_status st = run_checked([&](unsigned int* verdict) {
             cudaError_t e = launch_check_decode(block_tables, max_blocks_per_seq, context_lens, batch,
                                                 desc->num_blocks, query_start ? 0 : 1, verdict, s);
             if (e != cudaSuccess || query_start == nullptr) return e;
@@ -709,14 +694,47 @@ pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, const voi
     return PKV_OK;
 }
 
+pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_start, int32_t batch,
+                                   int32_t num_q_heads, int32_t max_query_len, float scale, void* out,
+                                   void* workspace, size_t workspace_bytes, const pkv_cache_desc* desc,
+                                   uint32_t flags, const pkv_decode_opts* opts, void* stream) {
+    NvtxRange nvtx_range("pkv_decode_attention_q8");
+    pkv_status st = check_desc_q8(desc, true);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || !q_heads_ok(num_q_heads, desc)) return PKV_ERR_SHAPE;
+    if (!isfinite(scale) || max_query_len < 1) return PKV_ERR_SHAPE;
+    if (opts != nullptr && opts->num_ctas < 0) return PKV_ERR_SHAPE;
+    const int G = num_q_heads / desc->num_kv_heads;
+    if (max_query_len * G > kMqMaxRows) return PKV_ERR_UNSUPPORTED;
+    if (query_start == nullptr && max_query_len != 1) return PKV_ERR_SHAPE;
+    if (batch == 0) return PKV_OK;
+    if (!table_width_ok(batch, max_blocks_per_seq)) return PKV_ERR_SHAPE;
+    if (!q || !k_codes || !v_codes || !scales || !block_tables || !context_lens || !out || !workspace)
+        return PKV_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(scales) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+        (reinterpret_cast<uintptr_t>(context_lens) & 3u) || (reinterpret_cast<uintptr_t>(query_start) & 3u) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PKV_ERR_ALIGN;
+    return run_split_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, query_start, batch,
+                        num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, batch, desc, flags, opts, stream);
+}
+
 size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
                                         int32_t max_query_len, const pkv_cache_desc* desc) {
     if (check_desc_q8(desc, false) != PKV_OK || batch < 0 || !q_heads_ok(num_q_heads, desc)) return 0;
     if (max_query_len < 1 || max_query_len > kMaxQueryLen) return 0;
+    (void)max_blocks_per_seq;
+    // The counters of a launch's most sequences lie first, whatever the batch, so that one
+    // workspace serves calls of all sizes on either kernel: none writes another's counters.
     const int G = num_q_heads / desc->num_kv_heads;
-    if (split_kernel_takes(desc, max_query_len, G))
-        return pkv_decode_q8_workspace_size(batch, num_q_heads, max_blocks_per_seq, max_query_len, desc, nullptr);
-    return chunk_q8_workspace_bytes(desc->head_dim);
+    size_t co = 0, po = 0;
+    const int ctas = desc->head_dim == 128 ? mq_num_ctas(128, batch, nullptr, true) : 0;
+    const size_t split = mq_workspace_bytes(kMaxBatchPerLaunch, desc->num_kv_heads, desc->head_dim, ctas, &co, &po);
+    if (split_kernel_takes(desc, max_query_len, G)) return split;
+    const size_t tiles = po + chunk_q8_workspace_bytes(desc->head_dim);
+    return split > tiles ? split : tiles;
 }
 
 pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
@@ -742,11 +760,12 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
         return PKV_ERR_ALIGN;
     const int G = num_q_heads / desc->num_kv_heads;
     if (split_kernel_takes(desc, max_query_len, G))
-        return pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens,
-                                       query_start, batch, num_q_heads, max_query_len, scale, out, workspace,
-                                       workspace_bytes, desc, flags, nullptr, stream);
-    if (workspace_bytes < chunk_q8_workspace_bytes(desc->head_dim))
-        return PKV_ERR_WORKSPACE;
+        return run_split_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, query_start, batch,
+                            num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, kMaxBatchPerLaunch, desc,
+                            flags, nullptr, stream);
+    size_t co = 0, po = 0;
+    mq_workspace_bytes(kMaxBatchPerLaunch, desc->num_kv_heads, desc->head_dim, 0, &co, &po);
+    if (workspace_bytes < po + chunk_q8_workspace_bytes(desc->head_dim)) return PKV_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned int* status = device_info().status;
     if (status == nullptr) return PKV_ERR_CUDA;
@@ -769,7 +788,7 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
         a.lens = context_lens + b0;
         a.qstart = query_start + b0;
         a.out = out;
-        a.workspace = workspace;
+        a.workspace = static_cast<char*>(workspace) + po;
         a.status = status;
         a.num_blocks = desc->num_blocks;
         a.max_blocks = max_blocks_per_seq;

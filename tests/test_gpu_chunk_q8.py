@@ -400,3 +400,22 @@ def test_prefill512_layer_sampled(pkv):
         tol = tol + 8192 * 2.0 ** -25 * v.abs().max() + 2.0 ** -11 * 0.03
         assert bool(((out[512 * i:512 * (i + 1), h].double() - ref).abs() <= tol).all())
     assert pkv.pkv_device_status(clear=True) == 0
+
+
+def test_one_workspace_for_calls_of_all_sizes_on_both_kernels(pkv):
+    """The size for the largest call serves every smaller one, in any order: each
+    result is the one a workspace of its own gives, bit for bit."""
+    mixes = [([700, 900, 65], [300, 40, 65]), ([2000, 77, 31, 5000, 900], [4, 1, 4, 2, 3]), ([300] * 70, [2] * 70),
+             ([900, 2500], [8, 8]), ([40, 3000], [40, 100])]
+    built = [make(90 + i, lens, nqs, 16, 4, 128) for i, (lens, nqs) in enumerate(mixes)]
+    on = [device(c) for c in built]
+    need = pkv.pkv_multiquery_q8_workspace_size(70, 16, 313, 300, on[0]["kc"])
+    shared = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    want = [call(pkv, c, d) for c, d in zip(built, on)]
+    for i in [0, 1, 2, 1, 3, 0, 2, 4, 3, 2, 1]:
+        size = pkv.pkv_multiquery_q8_workspace_size(len(built[i]["lens"]), 16, on[i]["tables"].shape[1],
+                                                    int(np.diff(built[i]["query_start"]).max()), on[i]["kc"])
+        assert size <= need
+        got = call(pkv, built[i], on[i], workspace=shared)
+        assert torch.equal(got, want[i]), i
+    assert pkv.pkv_device_status(clear=True) == 0
