@@ -425,8 +425,8 @@ PKV_API pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, c
  * calls leave its counters at zero; one workspace per call in flight, and none
  * shared with other calls; zero it again after PKV_DEVERR_TIMEOUT). A workspace
  * of the size for the largest batch and max_query_len serves all smaller calls
- * over pools of the same num_kv_heads and head_dim, in any order. Returns 0 for
- * sizes the call rejects.
+ * over pools of the same num_kv_heads and head_dim, in any order (the size is one
+ * constant for such pools: some 40 MB). Returns 0 for sizes the call rejects.
  */
 PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
                                                 int32_t max_query_len, const pkv_cache_desc* desc);
@@ -453,9 +453,9 @@ PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_hea
  *   max_query_len host bound on nq, 1 .. 65536 (above: PKV_ERR_UNSUPPORTED).
  *   workspace     >= pkv_multiquery_q8_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use.
- * fp32 accumulation, one rounding to bf16. Up to 32 query rows per (sequence, KV
- * head) at head_dim 128 run on pkv_decode_attention_q8's kernel with its
- * roundings. Above that (and at head_dim 64) the products run on f16 tensor cores:
+ * fp32 accumulation, one rounding to bf16. Up to 16 query rows per (sequence, KV
+ * head) at head_dim 128 and wide tables run on pkv_decode_attention_q8's kernel with
+ * its roundings. All else runs in tiles on f16 tensor cores:
  * q enters exactly (scaled by a power of two per row), a K value is rounded to f16
  * once (an eighth of a quantization step at most), a V value twice (scale, value), a
  * softmax weight once. Scales of any size and spread are taken.

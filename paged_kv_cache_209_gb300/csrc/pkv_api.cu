@@ -102,9 +102,25 @@ pkv_status check_desc_q8(const pkv_cache_desc* d, bool attention) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Int8 multi-query calls: the split kernel of pkv_multiquery.cu takes what it can hold.
-bool split_kernel_takes(const pkv_cache_desc* d, int32_t max_query_len, int G) {
-    return d->head_dim == 128 && static_cast<int64_t>(max_query_len) * G <= kMqMaxRows;
+// Int8 multi-query calls: which of the two kernels. The one that splits the cache
+// (pkv_multiquery.cu) holds 32 rows per (sequence, KV head) of 128; beside the tile
+// kernel, which turns the codes into f16 once for all rows, it is ahead where rows are
+// few and the caches long. 32 query heads on 8, split : tile in us,
+//     sequences x tokens   4 rows       16 rows      32 rows
+//     1 x 1024                          46 : 21      60 : 21
+//     1 x 4096             37 : 27      49 : 27      56 : 28
+//     1 x 32768            43 : 52      64 : 52      80 : 51
+//     8 x 4096             33 : 49      48 : 49      64 : 49
+//     8 x 32768           102 : 237    170 : 237    304 : 234
+//     32 x 4096            58 : 140     95 : 141    159 : 141
+//     64 x 8192           179 : 469    308 : 471    582 : 466
+// Lengths are the device's: the table's width stands in for them, and only a call whose
+// tables could not hold 65536 (token, KV head) pairs is taken as short.
+bool split_kernel_takes(const pkv_cache_desc* d, int32_t batch, int32_t max_blocks, int32_t max_query_len, int G) {
+    constexpr int kMostRows = 16;
+    static_assert(kMostRows <= kMqMaxRows, "rows of the split kernel");
+    return d->head_dim == 128 && static_cast<int64_t>(max_query_len) * G <= kMostRows &&
+           static_cast<int64_t>(max_blocks) * 16 * d->num_kv_heads > 65536 / batch;
 }
 
 // Both reading-back calls, after the checks of their descriptors.
@@ -728,11 +744,9 @@ size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int3
     (void)max_blocks_per_seq;
     // The counters of a launch's most sequences lie first, whatever the batch, so that one
     // workspace serves calls of all sizes on either kernel: none writes another's counters.
-    const int G = num_q_heads / desc->num_kv_heads;
     size_t co = 0, po = 0;
     const int ctas = desc->head_dim == 128 ? mq_num_ctas(128, batch, nullptr, true) : 0;
     const size_t split = mq_workspace_bytes(kMaxBatchPerLaunch, desc->num_kv_heads, desc->head_dim, ctas, &co, &po);
-    if (split_kernel_takes(desc, max_query_len, G)) return split;
     const size_t tiles = po + chunk_q8_workspace_bytes(desc->head_dim);
     return split > tiles ? split : tiles;
 }
@@ -759,7 +773,7 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return PKV_ERR_ALIGN;
     const int G = num_q_heads / desc->num_kv_heads;
-    if (split_kernel_takes(desc, max_query_len, G))
+    if (split_kernel_takes(desc, batch, max_blocks_per_seq, max_query_len, G))
         return run_split_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, query_start, batch,
                             num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, kMaxBatchPerLaunch, desc,
                             flags, nullptr, stream);

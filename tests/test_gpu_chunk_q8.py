@@ -144,11 +144,24 @@ SHAPES = [
     # single tokens and short drafts at head_dim 64 (no other int8 attention takes them)
     ([1, 16, 17, 300, 1000, 64], [1, 1, 1, 1, 1, 1], 32, 8, 64),
     ([30, 16, 170, 300], [4, 3, 0, 2], 8, 8, 64),
-    # few rows on long contexts (the context is split), and the split kernel's own cases
+    # few rows on long contexts (the context is split)
     ([5000, 3000], [9, 12], 32, 8, 128),
     ([4500], [70], 8, 8, 128),
     ([700, 40, 129, 9], [8, 3, 0, 5], 32, 8, 128),
 ]
+
+
+@pytest.mark.parametrize("nqs,hq", [([1, 1, 1, 1, 1], 32), ([4, 3, 0, 2, 4], 32), ([2, 1, 2, 2, 0], 64)])
+def test_few_rows_and_wide_tables(pkv, nqs, hq):
+    """Up to 16 rows: the kernel that splits the cache where the tables are wide, tiles where they are not."""
+    c = make(hq + nqs[0], [700, 40, 129, 9, 3000], nqs, hq, 8, 128)
+    want = reference(c)
+    narrow = call(pkv, c)
+    c["tables"] = np.pad(c["tables"], ((0, 0), (0, 600)), constant_values=-1)      # entries no sequence uses
+    wide = call(pkv, c)
+    check(narrow, c, want)
+    check(wide, c, want)
+    assert pkv.pkv_device_status(clear=True) == 0
 
 
 @pytest.mark.parametrize("lens,nqs,hq,hkv,d", SHAPES)

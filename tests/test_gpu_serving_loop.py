@@ -9,7 +9,7 @@ same tokens and the same cache.
 Tolerances: tokens, lengths, cache contents and rows read back are exact (the
 probabilities are multiples of 2^-30, so every sum of a row is exact in 64 bits);
 attention as derived in test_gpu_chunk_q8, and as the other tests of the kernel
-for up to 32 rows have it.
+that splits the cache have it.
 """
 
 import numpy as np
@@ -38,7 +38,7 @@ def pkv():
 class Server:
     """Sequences with blocks of their own and a one-layer model with random weights."""
 
-    def __init__(self, pkv, prompts, drafts, q_heads, kv_heads, d, steps, vocab=211):
+    def __init__(self, pkv, prompts, drafts, q_heads, kv_heads, d, steps, least_width=0, vocab=211):
         self.pkv, self.k, self.hq, self.hkv, self.d, self.vocab = pkv, drafts, q_heads, kv_heads, d, vocab
         self.batch, self.steps = len(prompts), steps
         gen = torch.Generator().manual_seed(17 * drafts + d)
@@ -49,7 +49,7 @@ class Server:
         self.head = (rand(q_heads * d, vocab) * (3.0 / (q_heads * d) ** 0.5)).cuda()
         self.draft_logits = (2 * rand(vocab, vocab)).cuda()
         self.prompts = [torch.randint(0, vocab, (n,), generator=gen) for n in prompts]
-        width = (max(prompts) + (steps + 1) * (drafts + 1) + 15) // 16
+        width = max(least_width, (max(prompts) + (steps + 1) * (drafts + 1) + 15) // 16)
         blocks = self.batch * width + 3
         self.tables = torch.randperm(blocks, generator=gen)[:self.batch * width].reshape(self.batch, width).to(torch.int32).cuda()
         self.kc = torch.zeros((blocks, kv_heads, 16, d), dtype=torch.int8, device="cuda")
@@ -149,7 +149,7 @@ class Mirror:
                  scale=float(np.float32(s.d ** -0.5)))
         ref, tol = reference(c)
         got = r["out"].float().cpu().numpy().astype(np.float64)
-        if s.d == 128 and np.diff(c["query_start"]).max() * s.hq // s.hkv <= 32:
+        if s.d == 128 and np.diff(c["query_start"]).max() * s.hq // s.hkv <= 16:
             ma, rl = cases.attention_errors(r["out"], ref)
             assert ma <= 1e-2 and rl <= 2e-3
         else:
@@ -166,17 +166,18 @@ class Mirror:
         return int(kept.sum()), int(rejected.sum())
 
 
-SHAPES = [  # prompts, drafts, query heads, KV heads, head_dim
-    ([38, 1, 131, 16, 2], 3, 8, 2, 128),      # 16 rows per KV head: the kernel that splits the cache
-    ([38, 1, 131, 16, 2], 9, 8, 2, 128),      # 40 rows: tiles
-    ([5, 200, 17], 3, 6, 2, 64),
-    ([300, 1], 0, 4, 4, 64),                  # no drafts: each step samples one token
+SHAPES = [  # prompts, drafts, query heads, KV heads, head_dim, least table width
+    ([38, 1, 131, 16, 2], 3, 8, 2, 128, 512),    # 16 rows per KV head, wide tables: the kernel that splits the cache
+    ([38, 1, 131, 16, 2], 3, 8, 2, 128, 0),      # the same on tiles
+    ([38, 1, 131, 16, 2], 9, 8, 2, 128, 0),      # 40 rows
+    ([5, 200, 17], 3, 6, 2, 64, 0),
+    ([300, 1], 0, 4, 4, 64, 0),                  # no drafts: each step samples one token
 ]
 
 
-@pytest.mark.parametrize("prompts,drafts,hq,hkv,d", SHAPES)
-def test_loop_against_the_oracle(pkv, prompts, drafts, hq, hkv, d):
-    s = Server(pkv, prompts, drafts, hq, hkv, d, steps=6)
+@pytest.mark.parametrize("prompts,drafts,hq,hkv,d,width", SHAPES)
+def test_loop_against_the_oracle(pkv, prompts, drafts, hq, hkv, d, width):
+    s = Server(pkv, prompts, drafts, hq, hkv, d, steps=6, least_width=width)
     m = Mirror(s)
     m.check(s.prefill())
     kept = rejected = 0
@@ -196,12 +197,12 @@ def test_loop_against_the_oracle(pkv, prompts, drafts, hq, hkv, d):
     assert pkv.pkv_device_status(clear=True) == 0
 
 
-@pytest.mark.parametrize("prompts,drafts,hq,hkv,d", SHAPES[:3])
-def test_loop_as_a_graph(pkv, prompts, drafts, hq, hkv, d):
-    eager = Server(pkv, prompts, drafts, hq, hkv, d, steps=6)
+@pytest.mark.parametrize("prompts,drafts,hq,hkv,d,width", SHAPES[:4])
+def test_loop_as_a_graph(pkv, prompts, drafts, hq, hkv, d, width):
+    eager = Server(pkv, prompts, drafts, hq, hkv, d, steps=6, least_width=width)
     eager.prefill()
     want = [eager.step(eager.uniform[i], eager.choice[i]) for i in range(eager.steps)]
-    s = Server(pkv, prompts, drafts, hq, hkv, d, steps=6)
+    s = Server(pkv, prompts, drafts, hq, hkv, d, steps=6, least_width=width)
     s.prefill()
     uniform, choice = s.uniform[0].clone(), s.choice[0].clone()
     state = [x.clone() for x in (s.lens, s.last)]
