@@ -1164,7 +1164,8 @@ cudaError_t run_chunk(const ChunkArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(chunk_q8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Cx<D>::kSmem));
     if (e != cudaSuccess) return e;
     e = launch_pdl(chunk_q8_kernel<D>, dim3(grid), dim3(Cx<D>::kThreads), Cx<D>::kSmem, s, a);
-    if (e != cudaSuccess) return e;
+    // a unit of three steps is never cut: tables that hold no more leave nothing to join
+    if (e != cudaSuccess || a.max_blocks * 16 < 2 * kMinPiece * kChunkStep - kChunkStep + 1) return e;
     return launch_pdl(combine_kernel<D>, dim3(grid, D / 8), dim3(kChunkRows), 0, s, a, grid);
 }
 
