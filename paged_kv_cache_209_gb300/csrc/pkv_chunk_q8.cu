@@ -155,20 +155,26 @@ __device__ __forceinline__ ChunkShape shape_of(const ChunkArgs& a) {
     return ChunkShape{a.lens, a.qstart, a.batch, a.kv_heads, a.group, a.max_blocks, a.max_query_len};
 }
 
-// Exclusive prefix sum over the block's threads (all threads; contains
-// __syncthreads, and scratch is free again after one more).
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* scratch) {
+// Sum of x over the threads before this one, the sum of all in `total` (one
+// __syncthreads; scratch: an int64 per warp, free again after the next one).
+template <int kThreads>
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* scratch, int64_t& total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t incl = x;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t other = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += other;
-    }
+    auto scan = [lane](int64_t v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t other = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += other;
+        }
+        return v;
+    };
+    const int64_t incl = scan(x);
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int64_t at = incl - x;
-    for (int w = 0; w < warp; ++w) at += scratch[w];
-    return at;
+    const int64_t warps = scan(lane < kThreads / 32 ? scratch[lane] : 0);
+    total = __shfl_sync(0xffffffffu, warps, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, warps, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + incl - x;
 }
 
 // This CTA's ranges (all threads; ends with __syncthreads): returns their number,
@@ -190,15 +196,19 @@ __device__ int plan_ranges(const ChunkArgs& a, const ChunkShape& sh, int64_t* pr
             most = max(most, chunk_most(q, a.group));
         }
     }
-    const int64_t before = block_sum(mine[0] + mine[1], scratch);
+    auto largest = [](int64_t v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    };
+    most = largest(most);
+    if ((t & 31) == 0) at[t >> 5] = most;  // (not yet used for the cuts)
+    int64_t total;
+    const int64_t before = block_sum<kThreads>(mine[0] + mine[1], scratch, total);
+    most = largest((t & 31) < kThreads / 32 ? at[t & 31] : 0);
     if (2 * t <= a.batch) prefix[2 * t] = before;
     if (2 * t + 1 <= a.batch) prefix[2 * t + 1] = before + mine[0];
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     __syncthreads();
-    if ((t & 31) == 0) scratch[t >> 5] = most;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) most = max(most, scratch[w]);
-    const int64_t total = prefix[a.batch];
     const int ctas = chunk_ctas(total, a.group, grid);
     if (total == 0 || cta >= ctas) return 0;
     const ChunkRounds r = chunk_rounds(total, most, ctas);
@@ -212,15 +222,13 @@ __device__ int plan_ranges(const ChunkArgs& a, const ChunkShape& sh, int64_t* pr
         __syncthreads();
         from = at[r.rounds * ctas];
         const int64_t left = t < ctas ? chunk_div(total, ctas) - chunk_dealt(at, r, t, ctas) : 0;
-        const int64_t due = block_sum(left > 0 ? left : 0, scratch);
+        const int64_t due = block_sum<kThreads>(left > 0 ? left : 0, scratch, all);
         __syncthreads();
         if (t == cta) at[0] = due;
         if (t == cta + 1) at[1] = due;
-        if (t == kThreads - 1) at[2] = due;  // a thread without a CTA: the sum of all
         __syncthreads();
         due0 = at[0];
         due1 = at[1];
-        all = at[2];
     }
     if (t < 2 * (r.rounds + 1)) {
         int64_t cost;
@@ -366,7 +374,8 @@ __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, u
     ChunkWalk& walk = *reinterpret_cast<ChunkWalk*>(smem + C::kOffWalk);
     ChunkSegment g;
     Job job{};
-    if (chunk_walk(shape_of(a), reinterpret_cast<const ChunkPos*>(smem + C::kOffPlan), ranges, walk, g)) {
+    const bool more = chunk_walk_to(shape_of(a), reinterpret_cast<const ChunkPos*>(smem + C::kOffPlan), ranges, walk, g);
+    if (more) {
         job.seq = g.at.seq;
         job.head = g.at.head;
         job.s0 = g.at.s;
@@ -380,6 +389,7 @@ __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, u
     }
     *reinterpret_cast<Job*>(smem + C::kOffJobs + slot * sizeof(Job)) = job;
     mbar_arrive(&job_full[slot]);
+    if (more) walk.cur = chunk_after(shape_of(a), g);  // while the others begin with this one
 }
 
 // ---------------------------------------------------------------- scales
@@ -741,17 +751,18 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             const int r0 = job.r0 + 128 * x;
             const bool row_ok = rr < rows;
             const int lim = row_ok ? job.before + query_of(a, r0 + rr) : -1;  // the last token the row sees
+            // where the lane's row begins in q and out; rows are moved by several lanes each
+            const int64_t own = row_ok ? row_of_unit(a, job.q0, job.head, r0 + rr) * D : -1;
             float row_f = 0.f;  // |scale| log2(e) over the power of two in q'
             {
                 // whole rows into the warp's own slots, then a row per lane, in place (loops
                 // rolled: this runs once per segment, mostly out of a cold instruction cache)
 #pragma unroll 2
                 for (int i = 0; i < kRowLanes; ++i) {
-                    const int r = row_of_lane(i);
-                    uint8_t* slot = row_slot(r, lane % kRowLanes);
-                    if (r < rows)
-                        copy16_async(smem_u32(slot), reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                                                    row_of_unit(a, job.q0, job.head, r0 + r) * D) + lane % kRowLanes);
+                    uint8_t* slot = row_slot(row_of_lane(i), lane % kRowLanes);
+                    const int64_t from = __shfl_sync(0xffffffffu, own, row_of_lane(i) & 31);
+                    if (from >= 0)
+                        copy16_async(smem_u32(slot), static_cast<const __nv_bfloat16*>(a.q) + from + 8 * (lane % kRowLanes));
                     else
                         *reinterpret_cast<uint4*>(slot) = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -946,10 +957,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 __syncwarp();
 #pragma unroll 2
                 for (int i = 0; i < kRowLanes; ++i) {
-                    const int r = row_of_lane(i);
-                    if (r < rows)
-                        *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row_of_unit(a, job.q0, job.head, r0 + r) * D) + lane % kRowLanes) =
-                            *reinterpret_cast<const uint4*>(row_slot(r, lane % kRowLanes));
+                    const int64_t to = __shfl_sync(0xffffffffu, own, row_of_lane(i) & 31);
+                    if (to >= 0)
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + to + 8 * (lane % kRowLanes)) =
+                            *reinterpret_cast<const uint4*>(row_slot(row_of_lane(i), lane % kRowLanes));
                 }
                 __syncwarp();
             } else {

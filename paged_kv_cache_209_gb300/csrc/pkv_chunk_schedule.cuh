@@ -240,16 +240,21 @@ PKV_HD inline ChunkPos chunk_after(const ChunkShape& a, const ChunkSegment& g) {
     return chunk_next_unit(a, g.at, g.tiles);
 }
 // Walks all segments of a CTA: `ranges` holds its rounds' and its last range, two cuts each.
+// chunk_walk_to finds the segment at the walker, chunk_walk also moves it on.
 struct ChunkWalk {
     ChunkPos cur;
     int range;
 };
 PKV_HD inline ChunkWalk chunk_begin(const ChunkPos* ranges) { return ChunkWalk{ranges[0], 0}; }
-PKV_HD inline bool chunk_walk(const ChunkShape& a, const ChunkPos* ranges, int count, ChunkWalk& w, ChunkSegment& g) {
+PKV_HD inline bool chunk_walk_to(const ChunkShape& a, const ChunkPos* ranges, int count, ChunkWalk& w, ChunkSegment& g) {
     while (!chunk_segment(a, w.cur, ranges[2 * w.range + 1], g)) {
         if (++w.range >= count) return false;
         w.cur = ranges[2 * w.range];
     }
+    return true;
+}
+PKV_HD inline bool chunk_walk(const ChunkShape& a, const ChunkPos* ranges, int count, ChunkWalk& w, ChunkSegment& g) {
+    if (!chunk_walk_to(a, ranges, count, w, g)) return false;
     w.cur = chunk_after(a, g);
     return true;
 }
