@@ -11,6 +11,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -457,6 +458,12 @@ def _on(here: int, name: str, t: torch.Tensor, dtype=None, shape=None) -> int:
     return t.data_ptr()
 
 
+@functools.lru_cache(maxsize=64)
+def _desc(nb: int, bs: int, hkv: int, d: int, dtype: int) -> CacheDesc:
+    """The descriptor of pools of this geometry (read only: calls share it)."""
+    return CacheDesc(nb, bs, hkv, d, dtype)
+
+
 def _raw_stream(stream, here: int) -> int:
     return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
 
@@ -494,7 +501,8 @@ def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, conte
     if block_tables.dim() != 2:
         raise ValueError("block_tables is [batch][max_blocks]")
     batch, max_blocks = block_tables.shape
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty_like(q)
     if workspace is None:
         need = pkv_multiquery_q8_workspace_size(batch, q_heads, max_blocks, max_query_len, k_codes)
@@ -504,11 +512,11 @@ def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, conte
             _on(here, "scales", scales), _on(here, "block_tables", block_tables, torch.int32), max_blocks,
             _on(here, "context_lens", context_lens, torch.int32, (batch,)),
             _on(here, "query_start", query_start, torch.int32, (batch + 1,)), batch, q_heads, max_query_len, scale,
-            _on(here, "out", out, torch.bfloat16, q.shape), _on(here, "workspace", workspace),
+            out.data_ptr() if new else _on(here, "out", out, torch.bfloat16, q.shape), _on(here, "workspace", workspace),
             workspace.numel() * workspace.element_size())
     if rows == 0:                                            # no query anywhere: no row to write
         return out
-    status = lib.pkv_multiquery_attention_q8(*args, CacheDesc(nb, bs, hkv, d, PKV_INT8), flags,
+    status = lib.pkv_multiquery_attention_q8(*args, _desc(nb, bs, hkv, d, PKV_INT8), flags,
                                              _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_multiquery_attention_q8", status)
@@ -523,13 +531,18 @@ def _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, 
     want = (num_rows, hkv, d)
     if k_out is None:
         k_out = torch.empty(want, dtype=dtype, device=like.device)
+        k_at = k_out.data_ptr()
+    else:
+        k_at = _on(here, "k_out", k_out, dtype, want)
     if v_out is None:
         v_out = torch.empty(want, dtype=dtype, device=like.device)
+        v_at = v_out.data_ptr()
+    else:
+        v_at = _on(here, "v_out", v_out, dtype, want)
     return (_on(here, "block_tables", block_tables, torch.int32), max_blocks,
             _on(here, "context_lens", context_lens, torch.int32, (batch,)),
             None if token_start is None else _on(here, "token_start", token_start, torch.int32, (batch,)),
-            _on(here, "row_start", row_start, torch.int32, (batch + 1,)), batch, num_rows,
-            _on(here, "k_out", k_out, dtype, want), _on(here, "v_out", v_out, dtype, want)), k_out, v_out
+            _on(here, "row_start", row_start, torch.int32, (batch + 1,)), batch, num_rows, k_at, v_at), k_out, v_out
 
 
 def pkv_gather(k_cache, v_cache, block_tables, context_lens, row_start, num_rows: int, token_start=None, k_out=None,
@@ -559,7 +572,7 @@ def pkv_gather_q8(k_codes, v_codes, scales, block_tables, context_lens, row_star
     pools = _on(here, "k_codes", k_codes), _on(here, "v_codes", v_codes), _on(here, "scales", scales)
     args, k_out, v_out = _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out,
                                       v_out, out_dtype, k_codes)
-    status = lib.pkv_gather_q8(*pools, *args, code, CacheDesc(nb, bs, hkv, d, PKV_INT8), flags,
+    status = lib.pkv_gather_q8(*pools, *args, code, _desc(nb, bs, hkv, d, PKV_INT8), flags,
                                _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_gather_q8", status)
@@ -599,25 +612,33 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
         dp, ds, dr = _prob_rows(here, "draft_probs", draft_probs)
     if context_lens is None and new_context_lens is not None:
         raise ValueError("new_context_lens needs context_lens")
-    dev = target_probs.device
-    if out_tokens is None:
-        out_tokens = torch.empty((batch, max_draft_len + 1), dtype=torch.int32, device=dev)
-    if num_accepted is None:
-        num_accepted = torch.empty((batch,), dtype=torch.int32, device=dev)
-    if context_lens is not None and new_context_lens is None:
-        new_context_lens = torch.empty((batch,), dtype=torch.int32, device=dev)
-    i32, one = torch.int32, (batch,)
+    i32, one, dev = torch.int32, (batch,), target_probs.device
     tokens = _on(here, "draft_tokens", draft_tokens, i32)
     accept = _on(here, "accept_uniform", accept_uniform, torch.float32, (drafts,))
+    if out_tokens is None:
+        out_tokens = torch.empty((batch, max_draft_len + 1), dtype=i32, device=dev)
+        out_at = out_tokens.data_ptr()
+    else:
+        out_at = _on(here, "out_tokens", out_tokens, i32, (batch, max_draft_len + 1))
+    if num_accepted is None:
+        num_accepted = torch.empty(one, dtype=i32, device=dev)
+        kept_at = num_accepted.data_ptr()
+    else:
+        kept_at = _on(here, "num_accepted", num_accepted, i32, one)
+    lens_at = new_at = None
+    if context_lens is not None:
+        lens_at = _on(here, "context_lens", context_lens, i32, one)
+        if new_context_lens is None:
+            new_context_lens = torch.empty(one, dtype=i32, device=dev)
+            new_at = new_context_lens.data_ptr()
+        else:
+            new_at = _on(here, "new_context_lens", new_context_lens, i32, one)
     status = lib.pkv_verify_drafts(
         tp, ts, tr, dp, ds, dr, code, vocab, tokens if dr else None, accept if dr else None,
         _on(here, "sample_uniform", sample_uniform, torch.float32),
         _on(here, "query_start", query_start, i32, (batch + 1,)),
-        _on(here, "draft_start", draft_start, i32, (batch + 1,)), batch, max_draft_len,
-        None if context_lens is None else _on(here, "context_lens", context_lens, i32, one),
-        None if new_context_lens is None else _on(here, "new_context_lens", new_context_lens, i32, one),
-        _on(here, "out_tokens", out_tokens, i32, (batch, max_draft_len + 1)),
-        _on(here, "num_accepted", num_accepted, i32, one), flags, _raw_stream(stream, here))
+        _on(here, "draft_start", draft_start, i32, (batch + 1,)), batch, max_draft_len, lens_at, new_at, out_at, kept_at,
+        flags, _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_verify_drafts", status)
     return out_tokens, num_accepted, new_context_lens
