@@ -49,9 +49,13 @@
 // every instruction they need at 7 cycles a warp, the cost of sharing a scheduler and
 // the instruction cache. So the loops are short rather than unrolled, and everything
 // that is done once per step or segment sits in warps of its own. 8 sequences of 8192
-// tokens, 512 of them new, 32 query heads on 8 of 128: 502 us, 1061 TFLOP/s of the
-// visible pairs (the cuBLAS rate is 1956); 32768 tokens, 2048 new: 485 us, 1130.
-// Eight warps for K instead of four (56 registers for a converter): 518 us.
+// tokens, 512 of them new, 32 query heads on 8 of 128: 487 us, 1094 TFLOP/s of the
+// visible pairs (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8:
+// 485 us, 1130. Eight warps for K instead of four (56 registers for a converter):
+// 518 us for the first; scores as one product of 128 tokens: 593.
+// Small calls are bound by the chain before the first product: 2.7 us to plan, 4 for
+// the table, the scales and the codes, one after another; 15.1 us for 40 new tokens
+// on 200.
 #include <math.h>
 
 #include "pkv_device.cuh"

@@ -13,6 +13,9 @@
 // Int8 V codes lie coordinate by coordinate ([D][16 tokens]): a lane loads the
 // 16 tokens of D / 32 neighbouring coordinates and the warp writes one token's
 // whole row at a time.
+//
+// 32 sequences of 8192 int8 tokens, 8 KV heads of 128: 1.63 GB in 257 us, 94 % of
+// the measured copy rate; 64 ragged bf16 sequences 126 us, 97 %; 300 tokens 5 us.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -21,7 +24,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 8;
+// Four times the CTAs that fit an SM, so that the last ones even the SMs out. bf16, 64
+// ragged sequences / int8, 32 of 8192 tokens, in us: 8 per SM 133 / 260, 16 128 / 259,
+// 32 126 / 257, 64 126 / 263, one item per warp 126 / 282 (each CTA sums the block
+// counts anew).
+constexpr int kCtasPerSm = 32;
 
 // The token range of sequence i; false when it leaves the context, the table or
 // the outputs.

@@ -20,7 +20,10 @@
 // leave their sums in shared memory; the CTAs read one another's totals through
 // distributed shared memory, and the one whose slice holds the draw finds the segment
 // and scans its entries again (from L2). One launch, nothing in global memory but
-// the results.
+// the results. What bounds it: a few sequences, the chain of the acceptance test, the
+// row, the totals and the segment (7.3 us for one of 32000 entries); many, the
+// instructions of the paired sums (32 of 131072 float32 entries: 11.5 us, 39 % of the
+// copy rate).
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -341,7 +344,9 @@ __global__ void check_verify_kernel(const VerifyArgs a, unsigned int* verdict) {
 }  // namespace
 
 // CTAs of a cluster: one load of every warp each, fewer when the sequences alone
-// come to several CTAs per SM.
+// come to several CTAs per SM. One sequence of 32000 entries / 32 of 131072 / 200 of
+// 50001 in bf16, in us: 1 CTA each 13.9 / 41.0 / 24.2, 2 10.3 / 24.1 / 19.4,
+// 4 8.4 / 15.0 / 19.2, 8 7.6 / 11.6 / 24.1, by this rule 7.6 / 11.6 / 19.1.
 static int cluster_of(const VerifyArgs& a) {
     const int segs = (a.vocab + kSeg - 1) / kSeg;
     int c = kMaxCtas;
