@@ -527,9 +527,10 @@ PKV_API pkv_status pkv_gather_q8(const void* k_codes, const void* v_codes, const
  * num_accepted[i] = a; new_context_lens[i] = context_lens[i] - (k - a): the
  * context length (with the k + 1 new tokens of the verification) less the
  * rejected drafts, whose cache slots the next append overwrites. An entry of r
- * counts only if it is a finite number above zero; if none is, y is -1. Running
- * sums carry at least 40 bits and their order is fixed, so a call's result never
- * depends on scheduling.
+ * counts only if it is a finite number above zero; if none is, y is -1 (some index
+ * or -1 for a row whose sum leaves the float32 range). Running sums carry at
+ * least 40 bits and their order is fixed, so a call's result never depends on
+ * scheduling.
  *
  *   target_probs  device, [num_target_rows][vocab] of `dtype` (PKV_F32 or
  *                 PKV_BF16), rows target_stride elements apart (>= vocab).

@@ -432,3 +432,41 @@ def test_one_workspace_for_calls_of_all_sizes_on_both_kernels(pkv):
         got = call(pkv, built[i], on[i], workspace=shared)
         assert torch.equal(got, want[i]), i
     assert pkv.pkv_device_status(clear=True) == 0
+
+
+def test_pools_past_32_bits(pkv):
+    """Blocks more than 2^32 bytes into the pools: the result of the same rows in a small pool."""
+    c = make(99, [700, 40, 300], [90, 3, 300], 8, 8, 128)
+    d = device(c)
+    want = call(pkv, c, d)
+    few = d["kc"].shape[0]
+    nb = 300_000                                             # 4.9 GB of codes in each pool
+    big = {"kc": torch.empty((nb, 8, 16, 128), dtype=torch.int8, device="cuda"),
+           "vc": torch.empty((nb, 8, 128, 16), dtype=torch.int8, device="cuda"),
+           "sc": torch.empty((nb, 8, 2, 16), device="cuda")}
+    at = torch.cat([torch.arange(few // 2), torch.arange(nb - few + few // 2, nb)]).cuda()    # some first, some last
+    for name, pool in big.items():
+        pool[at] = d[name]
+    d.update(big, tables=at.to(torch.int32)[d["tables"].long().clamp_(min=0)])
+    assert torch.equal(call(pkv, c, d), want)
+    start = torch.tensor([0, 700, 740, 1040], dtype=torch.int32, device="cuda")
+    read = lambda d: pkv.pkv_gather_q8(d["kc"], d["vc"], d["sc"], d["tables"], d["lens"], start, 1040)  # noqa: E731
+    assert all(torch.equal(a, b) for a, b in zip(read(d), read(device(c))))
+    assert pkv.pkv_device_status(clear=True) == 0
+
+
+def test_many_more_units_than_ctas(pkv):
+    """Some 5000 units: every round of whole units is in use; sampled sequences against the oracle."""
+    rng = np.random.default_rng(6)
+    nqs = rng.integers(200, 700, 250)
+    lens = nqs + rng.integers(0, 200, 250)
+    c = make(6, [int(n) for n in lens], [int(n) for n in nqs], 8, 8, 64)
+    out = call(pkv, c)
+    some = [0, 97, 151, 249]
+    start = c["query_start"]
+    rows = np.concatenate([np.arange(start[i], start[i + 1]) for i in some])
+    part = dict(c, tables=c["tables"][some], lens=c["lens"][some], q=c["q"][rows],
+                query_start=np.concatenate([[0], np.cumsum(nqs[some])]).astype(np.int32))
+    check(out[torch.from_numpy(rows).cuda()], part)
+    assert torch.isfinite(out).all()
+    assert pkv.pkv_device_status(clear=True) == 0

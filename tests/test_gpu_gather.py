@@ -196,3 +196,19 @@ def test_captured_and_replayed(pkv):
         torch.cuda.synchronize()
         wk, wv = plain(c, f, [20, 40], torch.bfloat16)
         assert same(k, wk) and same(v, wv)
+
+
+def test_rows_past_32_bits(pkv):
+    """Pools and outputs of more than 2^32 bytes each, the tokens at their far ends."""
+    nb, rows, heads, d = 140_000, 2_200_000, 8, 128
+    k, v = (torch.empty((nb, heads, 16, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = torch.tensor([nb - 1, 0, nb - 2], device="cuda")
+    k[ids], v[ids] = torch.randn(2, 3, heads, 16, d, device="cuda").to(torch.bfloat16)
+    ko, vo = (torch.zeros((rows, heads, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pkv.pkv_gather(k, v, ids.to(torch.int32)[None], torch.tensor([45], **i32), torch.tensor([rows - 40, rows], **i32), rows,
+                   token_start=torch.tensor([5], **i32), k_out=ko, v_out=vo)
+    for out, pool in ((ko, k), (vo, v)):
+        want = pool[ids].permute(0, 2, 1, 3).reshape(48, heads, d)[5:45]
+        assert torch.equal(out[-40:], want) and not out[:-40].any()
+    assert pkv.pkv_device_status(clear=True) == 0

@@ -226,3 +226,28 @@ def test_captured_and_replayed_and_another_stream(pkv):
         torch.cuda.synchronize()
         for g, w in zip(out, oracle(c)):
             assert np.array_equal(g.cpu().numpy(), w)
+
+
+def test_rows_past_32_bits(pkv):
+    """The last rows of 4.4 billion probabilities."""
+    c = case(12, [4], 262144, torch.bfloat16)
+    rows = 17_000
+    d = device(c)
+    p = torch.empty((rows, 262144), dtype=torch.bfloat16, device="cuda")
+    p[-5:] = d["p"]
+    got = pkv.pkv_verify_drafts(p, d["q"], d["tokens"], d["accept"], d["sample"], d["qs"] + (rows - 5), d["ds"], c["most"],
+                                context_lens=d["lens"])
+    for g, w in zip(got, oracle(c)):
+        assert np.array_equal(g.cpu().numpy(), w)
+    assert pkv.pkv_device_status(clear=True) == 0
+
+
+def test_sums_past_float32_still_name_a_token(pkv):
+    """Rows that are no probabilities at all: some index or -1, and nothing left unwritten."""
+    v = 5000
+    p = torch.full((2, v), 3e38, device="cuda")
+    z = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = torch.full((2, 1), 12345, dtype=torch.int32, device="cuda")
+    pkv.pkv_verify_drafts(p, None, none[:0], p[0, :0], torch.tensor([0.5, 0.0], device="cuda"), z, none, 0, out_tokens=out)
+    assert ((out >= -1) & (out < v)).all()
