@@ -298,38 +298,27 @@ __device__ __forceinline__ void careful_scores(uint32_t taddr, const float* c, f
     for (int e = 0; e < 16; ++e)
         x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
-// Waits until the phase of this parity has completed, about two seconds at most;
-// then it reports PKV_DEVERR_TIMEOUT and the role gives up (and with it, in as much
-// time, every role that depends on it). A probe is a handful of instructions: a warp
-// that polls takes issue slots from the warps it waits for, and the kernel's two
-// dozen waits have to share the instruction cache with its loops.
-// kSleep > 0: that many nanoseconds between probes, for a warp that runs ahead.
-constexpr long long kWaitClocks = 4000000000ll;
-template <int kSleep = 0>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long begun = clock64();
+// Waits until the phase of this parity has completed, for kProbes probes at most (a
+// failing one holds the thread for 1.4 us: 1.5 s together); false: it has not, and the
+// role gives up, as does, in as much time, every role that depends on it. One probe in
+// a loop is all there is: the kernel's two dozen waits share the instruction cache with
+// its loops, and a role reports at its end (a clock and the report in each wait: 487 us
+// instead of 481 for 8 sequences by 512 new tokens).
+constexpr int kProbes = 1 << 20;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-    do {
+    for (int n = 0; n < kProbes; ++n)
         if (mbar_try_wait(bar, parity)) return true;
-        if constexpr (kSleep > 0) __nanosleep(kSleep);
-    } while (clock64() - begun < kWaitClocks);
-    atomicOr(status, PKV_DEVERR_TIMEOUT);
     return false;
 }
 // wait by a whole warp, with one answer for all its lanes.
-template <int kSleep = 0>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const long long begun = clock64();
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-    do {
+    for (int n = 0; n < kProbes; ++n)
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if constexpr (kSleep > 0) __nanosleep(kSleep);
-    } while (__any_sync(0xffffffffu, clock64() - begun < kWaitClocks));
-    atomicOr(status, PKV_DEVERR_TIMEOUT);
     return false;
 }
+__device__ __forceinline__ void report_timeout(const ChunkArgs& a) { atomicOr(a.status, PKV_DEVERR_TIMEOUT); }
 // 16 bytes from global to shared memory, asynchronously.
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -355,13 +344,17 @@ struct __align__(16) Job {
 static_assert(sizeof(Job) == 48, "layout");
 
 // The next segment of a warp's sequence of them (`count`: how many it has taken).
-// All lanes of the warp, or kLanes = 1: one thread.
+// All lanes of the warp, or kLanes = 1: one thread. False at the end (job.s1 == 0) and
+// where the wait ran out (job.s1 < 0).
 template <int D, int kLanes>
-__device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int& count, Job& job, unsigned int* status) {
+__device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int& count, Job& job) {
     using C = Cx<D>;
     const int slot = count % C::kJobs;
     const uint32_t parity = static_cast<uint32_t>(count / C::kJobs) & 1u;
-    if (!(kLanes == 32 ? warp_wait(&job_full[slot], parity, status) : wait(&job_full[slot], parity, status))) return false;
+    if (!(kLanes == 32 ? warp_wait(&job_full[slot], parity) : wait(&job_full[slot], parity))) {
+        job.s1 = -1;
+        return false;
+    }
     job = *reinterpret_cast<const Job*>(smem + C::kOffJobs + slot * sizeof(Job));
     if (kLanes == 32) __syncwarp();
     if (kLanes == 1 || (threadIdx.x & 31) == 0) mbar_arrive(&job_empty[slot]);
@@ -374,7 +367,7 @@ template <int D>
 __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int ranges, int count) {
     using C = Cx<D>;
     const int slot = count % C::kJobs;
-    if (count >= C::kJobs && !wait<40>(&job_empty[slot], static_cast<uint32_t>(count / C::kJobs - 1) & 1u, a.status)) return;
+    if (count >= C::kJobs && !wait(&job_empty[slot], static_cast<uint32_t>(count / C::kJobs - 1) & 1u)) return;
     ChunkWalk& walk = *reinterpret_cast<ChunkWalk*>(smem + C::kOffWalk);
     ChunkSegment g;
     Job job{};
@@ -424,7 +417,10 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
     uint32_t parity = 1;
     for (int it = -1;; ++it) {
         if (it >= 0) {
-            if (!warp_wait<20>(&empty[slot], parity, a.status)) break;
+            if (!warp_wait(&empty[slot], parity)) {
+                report_timeout(a);
+                break;
+            }
             uint8_t* record = smem + C::kOffRecord + slot * C::kRecordBytes;
             if (live) {
                 if (opened) {
@@ -477,7 +473,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 __syncwarp();
             }
             Job job;
-            live = next_job<D, 32>(smem, job_full, job_empty, jobs, job, a.status);
+            live = next_job<D, 32>(smem, job_full, job_empty, jobs, job);
             step = job.s0;
             last = job.s1;
             n = job.n;
@@ -539,8 +535,12 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
     uint32_t parity = 0;             // of the next record
     int st = IsV ? cw >> 1 : 0;      // stage: V's of the half with this warp's tokens
     uint32_t st_parity = 1;
+    bool failed = false;
     for (int it = -1;; ++it) {
-        if (!warp_wait<20>(&rec_full[next_slot], parity, a.status)) break;
+        if (!warp_wait(&rec_full[next_slot], parity)) {
+            failed = true;
+            break;
+        }
         const uint8_t* next = smem + C::kOffRecord + next_slot * C::kRecordBytes;
         const bool live = *reinterpret_cast<const int*>(next + 1344) != 0;
         if (live) {
@@ -556,7 +556,10 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                 copy16_async(smem_u32(mine + 512 * i), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
             copy_commit();
         } else {
-            if (!warp_wait<20>(&empty[st], st_parity, a.status)) break;
+            if (!warp_wait(&empty[st], st_parity)) {
+                failed = true;
+                break;
+            }
             copy_wait_all();
             // Two vectors at a time, the next two on their way out of shared memory; in
             // rolled loops: unrolled, the kernel's loops leave the instruction cache (8
@@ -649,6 +652,7 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
             parity ^= 1u;
         }
     }
+    if (failed) report_timeout(a);
     copy_wait_all();
 }
 
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         int jobs = 0, flags = 0;
         bool ok = true;
         Job job;
-        while (next_job<D, 32>(smem, job_full, job_empty, jobs, job, a.status)) {
+        while (next_job<D, 32>(smem, job_full, job_empty, jobs, job)) {
             const int rows = job.rows - 128 * x;  // rows of the half, if positive
             const int steps = job.s1 - job.s0;
             if (rows <= 0) {
@@ -806,7 +810,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 const bool masked = (job.s0 + j + 1) * kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    if (!warp_wait(&s_full[2 * x + part], it & 1, a.status)) {
+                    if (!warp_wait(&s_full[2 * x + part], it & 1)) {
                         ok = false;
                         break;
                     }
@@ -890,7 +894,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             // O holds something once a part of this segment has been multiplied in:
                             // the last one is the other part, of this step or of the one before
                             if (j + part > 0) {
-                                if (!warp_wait(&pv_done[2 * x + (part ^ 1)], (it - 1 + part) & 1, a.status)) {
+                                if (!warp_wait(&pv_done[2 * x + (part ^ 1)], (it - 1 + part) & 1)) {
                                     ok = false;
                                     break;
                                 }
@@ -936,7 +940,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             }
             if (!ok) break;
             // the products of the last step (part 1 completes after part 0)
-            if (!warp_wait(&pv_done[2 * x + 1], (it - 1) & 1, a.status)) {
+            if (!warp_wait(&pv_done[2 * x + 1], (it - 1) & 1)) {
                 ok = false;
                 break;
             }
@@ -991,6 +995,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             tc_fence_before();  // the next segment's products overwrite O after this half's next arrival
         }
         if (threadIdx.x == 0) info->flags = ok ? flags : 0;  // half A takes part in every segment
+        if (!ok || job.s1 != 0) report_timeout(a);
     } else if (warp < C::kScoreWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp < C::kConvertWarp + 4)
@@ -1011,15 +1016,15 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 int step = 0, it = 0, segs = 0, jobs = 0;
                 bool ok = true;
                 Job job;
-                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job, a.status)) {
+                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job)) {
                     const bool mine = job.rows > 128 * x;
                     if (mine) {
-                        if (!wait(&q_full[x], segs & 1, a.status)) break;
+                        ok = wait(&q_full[x], segs & 1);
                         ++segs;
                     }
                     for (int j = job.s0; ok && j < job.s1; ++j, ++step) {
                         const int st = step & 1;
-                        if (!wait(&k_full[st], (step >> 1) & 1, a.status)) {
+                        if (!wait(&k_full[st], (step >> 1) & 1)) {
                             ok = false;
                             break;
                         }
@@ -1031,7 +1036,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part) {
                             // the part's weights of the step before lie over its scores
-                            if (it > 0 && !wait(&pv_done[2 * x + part], (it - 1) & 1, a.status)) {
+                            if (it > 0 && !wait(&pv_done[2 * x + part], (it - 1) & 1)) {
                                 ok = false;
                                 break;
                             }
@@ -1050,7 +1055,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     }
                 }
                 umma_commit(&final_bar[x]);
-                wait(&final_bar[x], 0, a.status);
+                if (!wait(&final_bar[x], 0) || !ok || job.s1 != 0) report_timeout(a);
             }
         } else {
             // -------------------------------------------- values O += P V of half x (one thread)
@@ -1060,7 +1065,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 uint32_t phase = 0;
                 bool ok = true;
                 Job job;
-                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job, a.status)) {
+                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job)) {
                     const bool mine = job.rows > 128 * x;
                     for (int j = job.s0; ok && j < job.s1; ++j) {
 #pragma unroll 1
@@ -1071,7 +1076,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 st = 0;
                                 phase ^= 1u;
                             }
-                            if (!wait(&v_full[now], parity, a.status)) {
+                            if (!wait(&v_full[now], parity)) {
                                 ok = false;
                                 break;
                             }
@@ -1079,7 +1084,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 mbar_arrive(&v_empty[now]);
                                 continue;
                             }
-                            if (!wait(&p_full[2 * x + part], it & 1, a.status)) {
+                            if (!wait(&p_full[2 * x + part], it & 1)) {
                                 ok = false;
                                 break;
                             }
@@ -1097,7 +1102,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     }
                 }
                 umma_commit(&final_bar[2 + x]);
-                wait(&final_bar[2 + x], 0, a.status);
+                if (!wait(&final_bar[2 + x], 0) || !ok || job.s1 != 0) report_timeout(a);
             }
         }
         __syncwarp();
