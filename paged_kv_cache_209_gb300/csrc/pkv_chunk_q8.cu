@@ -660,7 +660,8 @@ template <int D>
 __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const ChunkArgs a) {
     using C = Cx<D>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // by an offset: through an integer the compiler would lose that this is shared memory
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
     uint64_t* k_empty = k_full + C::kStages;
     uint64_t* v_full = k_empty + C::kStages;
@@ -1012,7 +1013,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             // -------------------------------------------- scores S = Q K^T of half x (one thread)
             if (lane == 0) {
                 constexpr uint32_t idS = umma_idesc_f16(128, 64);
-                const uint32_t q_base = smem_u32(smem + C::kOffQ + x * C::kTileBytes);
+                const uint64_t q_desc = umma_desc_sw128(smem_u32(smem + C::kOffQ + x * C::kTileBytes), 16, 1024);
+                const uint64_t k_desc = umma_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
                 int step = 0, it = 0, segs = 0, jobs = 0;
                 bool ok = true;
                 Job job;
@@ -1032,7 +1034,6 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             mbar_arrive(&k_empty[st]);
                             continue;
                         }
-                        const uint32_t k_base = smem_u32(smem + C::kOffK + st * C::kTileBytes);
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part) {
                             // the part's weights of the step before lie over its scores
@@ -1041,11 +1042,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 break;
                             }
                             tc_fence_after();
+                            const uint64_t kd = k_desc + ((st * C::kTileBytes + part * 64 * 128) >> 4);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t off = (kk >> 2) * C::kPartBytes + (kk & 3) * 32;
-                                umma_bf16(tmem + C::kColS + 128 * x + 64 * part, umma_desc_sw128(q_base + off, 16, 1024),
-                                          umma_desc_sw128(k_base + part * 64 * 128 + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+                                umma_bf16(tmem + C::kColS + 128 * x + 64 * part, q_desc + (off >> 4), kd + (off >> 4), idS, kk > 0 ? 1u : 0u);
                             }
                             if (part == 1) umma_commit(&k_empty[st]);
                             umma_commit(&s_full[2 * x + part]);
@@ -1061,6 +1062,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             // -------------------------------------------- values O += P V of half x (one thread)
             if (lane == 0) {
                 constexpr uint32_t idO = umma_idesc_f16(128, D);
+                const uint64_t v_desc = umma_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
                 int st = 0, it = 0, jobs = 0;
                 uint32_t phase = 0;
                 bool ok = true;
@@ -1089,11 +1091,11 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                                 break;
                             }
                             tc_fence_after();
-                            const uint32_t v_base = smem_u32(smem + C::kOffV + now * C::kVPartBytes);
+                            const uint64_t vd = v_desc + (now * C::kVPartBytes >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 umma_bf16_ts(tmem + C::kColO + 128 * x, tmem + C::kColS + 128 * x + 64 * part + 8 * kk,
-                                             umma_desc_sw128(v_base + kk * 32, 16, 1024), idO,
+                                             vd + 2 * kk, idO,
                                              (j > job.s0 || part > 0 || kk > 0) ? 1u : 0u);
                             umma_commit(&pv_done[2 * x + part]);
                             umma_commit(&v_empty[now]);
