@@ -43,19 +43,20 @@
 // of 16 KB, the next step's codes 32 KB.
 //
 // What bounds it: instructions. A step's products would take 2500 cycles of the
-// tensor cores at the rate a large matrix product reaches; the step takes about 4050,
-// in which the schedulers issue two of three slots: 1000 of 2700 instructions per
-// scheduler for the softmax, 900 for the conversion. Both loops are that long with
-// every instruction they need at 7 cycles a warp, the cost of sharing a scheduler and
-// the instruction cache. So the loops are short rather than unrolled, and everything
-// that is done once per step or segment sits in warps of its own. 8 sequences of 8192
-// tokens, 512 of them new, 32 query heads on 8 of 128: 487 us, 1094 TFLOP/s of the
-// visible pairs (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8:
-// 485 us, 1130. Eight warps for K instead of four (56 registers for a converter):
-// 518 us for the first; scores as one product of 128 tokens: 593.
+// tensor cores at the rate a large matrix product reaches; the step takes about 3850,
+// in which the schedulers issue two of three slots: some 900 instructions per scheduler
+// for the softmax, 900 for the conversion, most of the rest waits. Each instruction of
+// the two loops costs a warp 7 cycles, the price of sharing a scheduler and the
+// instruction cache. So the loops are short rather than unrolled, and everything that is
+// done once per step or segment sits in warps of its own. 8 sequences of 8192 tokens,
+// 512 of them new, 32 query heads on 8 of 128: 465 us, 1145 TFLOP/s of the visible pairs
+// (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8: 455 us, 1205.
+// Slower, for the first (before the last few steps, against 502): eight warps for K
+// instead of four (56 registers for a converter) 518 us; scores as one product of 128
+// tokens 593.
 // Small calls are bound by the chain before the first product: 2.7 us to plan, 4 for
-// the table, the scales and the codes, one after another; 15.1 us for 40 new tokens
-// on 200.
+// the table, the scales and the codes, one after another; 15 us for 40 new tokens on
+// 200.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -298,13 +299,16 @@ __device__ __forceinline__ void careful_scores(uint32_t taddr, const float* c, f
     for (int e = 0; e < 16; ++e)
         x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
 }
-// Waits until the phase of this parity has completed, for kProbes probes at most (a
-// failing one holds the thread for 1.4 us: 1.5 s together); false: it has not, and the
-// role gives up, as does, in as much time, every role that depends on it. One probe in
-// a loop is all there is: the kernel's two dozen waits share the instruction cache with
-// its loops, and a role reports at its end (a clock and the report in each wait: 487 us
+// Waits until the phase of this parity has completed, for kProbes probes at most; false:
+// it has not, and the role gives up, as does, in as much time, every role that depends
+// on it. A failing probe holds the thread for 1.4 us where nothing happens (6 s together)
+// and for 150 cycles or so where barriers of the CTA are arrived at, as in the longest
+// wait there is: half B's for the next segment, while A takes one of up to 110000 steps
+// (2^31 tokens on 152 CTAs; 0.2 s, a third of what the probes last). One probe in a loop
+// is all there is: the kernel's two dozen waits share the instruction cache with its
+// loops, and a role reports at its end (a clock and the report in each wait: 487 us
 // instead of 481 for 8 sequences by 512 new tokens).
-constexpr int kProbes = 1 << 20;
+constexpr int kProbes = 1 << 22;
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
     for (int n = 0; n < kProbes; ++n)
@@ -325,6 +329,15 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// One lane of a converged warp. Where the issuers choose theirs this way, and not as
+// lane 0, the compiler knows that the branch holds one thread and keeps its loop in
+// uniform registers (8 sequences by 512 new tokens: 444 us, as lane 0 465).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 // ---------------------------------------------------------------- segments
 // A segment as the roles need it. The first of the scale warps, ahead of all others, walks
@@ -1011,7 +1024,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         const int x = warp & 1;
         if (warp < C::kValueWarp) {
             // -------------------------------------------- scores S = Q K^T of half x (one thread)
-            if (lane == 0) {
+            if (elect_one()) {
                 constexpr uint32_t idS = umma_idesc_f16(128, 64);
                 const uint64_t q_desc = umma_desc_sw128(smem_u32(smem + C::kOffQ + x * C::kTileBytes), 16, 1024);
                 const uint64_t k_desc = umma_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
@@ -1060,7 +1073,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             }
         } else {
             // -------------------------------------------- values O += P V of half x (one thread)
-            if (lane == 0) {
+            if (elect_one()) {
                 constexpr uint32_t idO = umma_idesc_f16(128, D);
                 const uint64_t v_desc = umma_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
                 int st = 0, it = 0, jobs = 0;
