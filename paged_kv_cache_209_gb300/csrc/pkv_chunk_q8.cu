@@ -574,22 +574,22 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                 break;
             }
             copy_wait_all();
-            // Two vectors at a time, the next two on their way out of shared memory; in
-            // rolled loops: unrolled, the kernel's loops leave the instruction cache (8
-            // sequences by 512 new tokens: 627 us unrolled, 546 rolled, 503 in this form).
+            // Two vectors at a time, the next two on their way out of shared memory. (8
+            // sequences by 512 new tokens: 425 us unrolled, rolled 444. It was the other way
+            // round while the issuers' and the waits' code was twice as long: 627 and 546.)
             if (IsV) {
                 // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
                 uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
                 const uint8_t* factors = record + 1024 + 64 * cw;
                 uint4 x0 = *reinterpret_cast<const uint4*>(mine), x1 = *reinterpret_cast<const uint4*>(mine + 512);
-#pragma unroll 1
+#pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const uint4 f0 = *reinterpret_cast<const uint4*>(factors + 32 * b), f1 = *reinterpret_cast<const uint4*>(factors + 32 * b + 16);
                     uint8_t* c0 = vd + (((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4);
                     uint8_t* c1 = vd + ((((((2 * cw + b) & 3) * 2) ^ (lane & 7)) << 4) ^ 16);
                     const uint4* src = b == 0 ? src0 : src1;
                     uint8_t* in = mine + 512 * kPerBlock * b;
-#pragma unroll 1
+#pragma unroll
                     for (int i = 0; i < kPerBlock; i += 2) {
                         const uint8_t* ahead = b * kPerBlock + i + 2 < C::kVecs ? in + 512 * (i + 2) : in;
                         const uint4 y0 = *reinterpret_cast<const uint4*>(ahead), y1 = *reinterpret_cast<const uint4*>(ahead + 512);
@@ -630,7 +630,7 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                     *reinterpret_cast<uint4*>(rowp + ((c0 ^ 1 ^ row8) << 4)) = k_values(t.y.x, t.y.y, half2_of(t.f.x), half2_of(t.f.y));
                 };
                 Two t0 = take(0), t1 = take(1);
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < C::kVecs; i += 2) {
                     const int ahead = (i + 2) % C::kVecs;  // (after the last, values that are not used)
                     const Two n0 = take(ahead), n1 = take(ahead + 1);
@@ -741,10 +741,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     const uint32_t tmem = *tmem_slot;
 
     // Registers: launched with 80 a thread, 61440 together, which 256 softmax threads at
-    // 120, 256 converters at 72, 128 issuers at 40 and 128 threads for the scales at 56
+    // 128, 256 converters at 64, 128 issuers at 40 and 128 threads for the scales at 56
     // share: none spills in its loop. (A few spilled words there cost a tenth.)
     if (warp < C::kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it
         const int x = warp >> 2;
         const int rr = (warp & 3) * 32 + lane;
@@ -1011,7 +1011,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         if (threadIdx.x == 0) info->flags = ok ? flags : 0;  // half A takes part in every segment
         if (!ok || job.s1 != 0) report_timeout(a);
     } else if (warp < C::kScoreWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp < C::kConvertWarp + 4)
             convert_role<D, false>(a, smem, rec_full, rec_empty, k_full, k_empty);
         else
