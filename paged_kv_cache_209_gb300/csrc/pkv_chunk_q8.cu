@@ -86,7 +86,7 @@ struct Cx {
     static constexpr int kThreads = 768;
     static constexpr int kStages = 2;   // K stages (a step each)
     static constexpr int kParts = 3;    // V stages (64 tokens each)
-    static constexpr int kRecords = 3;  // steps whose factors are laid out
+    static constexpr int kRecords = 4;  // steps whose factors are laid out
     // Tables in flight: the scale warps write step n once the converters are done with
     // step n - kRecords; K's then are at most four steps ahead of the slower softmax
     // half (a fifth needs scores that need V parts which that half's products have
@@ -103,8 +103,8 @@ struct Cx {
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffCodes = kOffV + kParts * kVPartBytes;  // the next step's codes: [8 warps][kVecs][32 lanes] vectors
     static constexpr int kOffTable = kOffCodes + 8 * kVecs * 512;
-    // a step's table: 2^E, 2^F, a byte per converter warp that is 1 for a slow step; the
-    // tokens' K factors [128] and, in log2, what their V values lack [128]
+    // a step's table: 2^E, 2^F, whether it is a slow step; the tokens' K factors [128] and,
+    // in log2, what their V values lack [128] (for parts done with care)
     static constexpr int kTableBytes = 16 + 2 * 128 * 4;
     // a step's record: per token (hi, hi, lo, lo) of K's factor in f16 [128], V's factor in
     // f16 [128]; its 8 blocks' place in the pools, in vectors; whether there is such a step
@@ -403,128 +403,120 @@ __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, u
 }
 
 // ---------------------------------------------------------------- scales
-// Four warps, ahead of all others: block ids, scales, and what follows from them,
-// for every step of the CTA. Warp w takes tokens 32 w .. 32 w + 31 of a step (blocks
-// 2 w, 2 w + 1), lane l token 32 w + l. They decide whether 32 tokens are taken as
-// bare codes. (In the converters' own loop this was 2000 of 5200 cycles a step, and
-// that loop was what everything waited for.)
+// Four warps, ahead of all others: block ids, scales, and what follows from them. Warp w
+// takes the CTA's steps w, w + 4, ...: four steps' chains of loads (id, then scales) are
+// in flight, and none holds up the converters. (In the converters' own loop this was
+// 2000 of 5200 cycles a step; with a quarter of every step per warp 2900 of 3300 where
+// one row half is in use, because each step's chain then followed on the last one's.)
+// Lane l holds tokens l, 32 + l, 64 + l, 96 + l; 32 of them at a time are taken as bare codes.
 template <int D>
 __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, int ranges, uint64_t* job_full, uint64_t* job_empty,
                                            uint64_t* full, uint64_t* empty) {
     using C = Cx<D>;
     const int lane = threadIdx.x & 31;
-    const int cw = (threadIdx.x >> 5) & 3;
+    const int w = (threadIdx.x >> 5) & 3;
     int jobs = 0;
-    int step = 0, last = 0;         // step being loaded, one past the segment's last
-    int n = 0, head = 0;            // its tokens, KV head
-    const int32_t* trow = nullptr;  // its block table
-    int ids = 0, ids_next = 0;      // lane l: id of block 32 b + l (-1: past the end, -2: outside the pool), b = step / 4; b + 1
-    int ev = 0, ek = 0;             // E and F of the segment
-    float sample = 0.f;             // what they are taken from
-    bool opened = false;            // they are still to be taken
-    // the loaded step: the token's scales, its block's row of the pools, whether it exists or lies in a block outside the pool
-    float ks = 0.f, vs = 0.f;
-    int64_t row = 0;
-    bool present = false, missing = false, live = false;
-    int slot = 0, table = 0;
-    uint32_t parity = 1;
-    for (int it = -1;; ++it) {
-        if (it >= 0) {
-            if (!warp_wait(&empty[slot], parity)) {
+    int base = 0;  // steps of the segments before
+    int at = w;    // the warp's next step, of all the CTA's
+    Job job;
+    while (true) {
+        if (w == 0) {
+            if (lane == 0) lay_out_job<D>(a, smem, job_full, job_empty, ranges, jobs);
+            __syncwarp();
+        }
+        if (!next_job<D, 32>(smem, job_full, job_empty, jobs, job)) break;
+        const int steps = job.s1 - job.s0;
+        const int32_t* trow = a.tables + static_cast<int64_t>(job.seq) * a.max_blocks;
+        const int blocks = (job.n + 15) / 16;
+        int ev = 0, ek = 0;  // E and F of the segment
+        bool opened = false;
+        for (; at < base + steps; at += 4) {
+            const int step = job.s0 + at - base;
+            // ---- its blocks (lanes 0 - 7); -1: past the end, -2: outside the pool
+            int mine = -1, first = 0;
+            const bool inside = lane < 8 && 8 * step + lane < blocks;
+            if (inside) mine = __ldg(trow + 8 * step + lane);
+            if (!opened) first = __ldg(trow + 8 * job.s0);
+            if (inside && (mine < 0 || mine >= a.num_blocks)) {
+                atomicOr(a.status, PKV_DEVERR_RANGE);
+                mine = -2;
+            }
+            // an absent block's codes may be any (its tokens carry no weight): block 0 exists
+            const int64_t row = static_cast<int64_t>(max(0, mine)) * a.kv_heads + job.head;
+            float ks[4], vs[4];
+            bool present[4], missing[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int id = __shfl_sync(0xffffffffu, mine, 2 * g + lane / 16);
+                present[g] = id >= 0 && step * kChunkStep + 32 * g + lane < job.n;
+                missing[g] = id == -2;
+                const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + job.head) * 32 + (lane & 15);
+                ks[g] = __ldg(rec);
+                vs[g] = __ldg(rec + 16);
+            }
+            if (!opened) {
+                // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
+                opened = true;
+                if (first < 0 || first >= a.num_blocks) first = 0;
+                const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + job.head) * 32 + lane);
+                const uint32_t size = __float_as_uint(job.s0 * kChunkStep + (lane & 15) < job.n ? x : 0.f) & 0x7fffffffu;
+                const bool use = size < 0x7f800000u;
+                ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? size : 0u));
+                ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? size : 0u));
+            }
+            const int slot = at % C::kRecords;
+            if (!warp_wait(&empty[slot], (static_cast<uint32_t>(at / C::kRecords) & 1u) ^ 1u)) {
                 report_timeout(a);
-                break;
+                return;
             }
             uint8_t* record = smem + C::kOffRecord + slot * C::kRecordBytes;
-            if (live) {
-                if (opened) {
-                    const uint32_t x = __float_as_uint(sample) & 0x7fffffffu;
-                    const bool use = x < 0x7f800000u;
-                    ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? x : 0u));
-                    ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? x : 0u));
-                    opened = false;
-                }
-                const uint32_t vbits = __float_as_uint(vs) & 0x7fffffffu;
-                const bool bare_v = __any_sync(0xffffffffu, present && leaves_range(vbits, ev));
-                const bool bare_k = __any_sync(0xffffffffu, present && leaves_range(__float_as_uint(ks) & 0x7fffffffu, ek));
-                const bool slow = bare_k || bare_v || __any_sync(0xffffffffu, missing);
-                float* tab = reinterpret_cast<float*>(smem + C::kOffTable + table * C::kTableBytes);
-                if (lane == 0) {
-                    if (cw == 0) *reinterpret_cast<float2*>(tab) = make_float2(exp2_int(ev), exp2_int(ek));
-                    reinterpret_cast<uint8_t*>(tab)[8 + cw] = slow;
-                }
-                if (slow) {
-                    tab[4 + 32 * cw + lane] = missing ? __uint_as_float(kAbsent) : bare_k ? ks : exp2_int(ek);
-                    float lack = 0.f;
-                    // (a scale below the normal range counts as its smallest number)
-                    if (bare_v && present) lack = log2f(vbits < 0x00800000u ? 1.17549435e-38f : vs) - static_cast<float>(ev);
-                    tab[4 + 128 + 32 * cw + lane] = lack;
-                } else {
-                    tab[4 + 32 * cw + lane] = exp2_int(ek);  // another warp's tokens may make the step slow
-                    tab[4 + 128 + 32 * cw + lane] = 0.f;
-                }
-                const float factor = !present ? 0.f : bare_k ? 1.f : ks * exp2_int(-ek);
+            float* tab = reinterpret_cast<float*>(smem + C::kOffTable + static_cast<uint32_t>(at) % C::kTables * C::kTableBytes);
+            bool bare_k[4], bare_v[4], slow = false;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                bare_k[g] = __any_sync(0xffffffffu, present[g] && leaves_range(__float_as_uint(ks[g]) & 0x7fffffffu, ek));
+                bare_v[g] = __any_sync(0xffffffffu, present[g] && leaves_range(__float_as_uint(vs[g]) & 0x7fffffffu, ev));
+                slow = slow || bare_k[g] || bare_v[g] || missing[g];
+                const float factor = !present[g] ? 0.f : bare_k[g] ? 1.f : ks[g] * exp2_int(-ek);
                 const __half hi = __float2half(factor), lo = __float2half(factor - __half2float(hi));
-                *reinterpret_cast<uint2*>(record + (32 * cw + lane) * 8) = make_uint2(bits(__halves2half2(hi, hi)), bits(__halves2half2(lo, lo)));
-                reinterpret_cast<__half*>(record + 1024)[32 * cw + lane] = __float2half(!present ? 0.f : bare_v ? 1.f : vs * exp2_int(-ev));
-                if ((lane & 15) == 0) reinterpret_cast<int64_t*>(record + 1280)[2 * cw + lane / 16] = row * D;
+                *reinterpret_cast<uint2*>(record + (32 * g + lane) * 8) = make_uint2(bits(__halves2half2(hi, hi)), bits(__halves2half2(lo, lo)));
+                reinterpret_cast<__half*>(record + 1024)[32 * g + lane] =
+                    __float2half(!present[g] ? 0.f : bare_v[g] ? 1.f : vs[g] * exp2_int(-ev));
             }
-            if (cw == 0 && lane == 0) *reinterpret_cast<int*>(record + 1344) = live;
+            slow = __any_sync(0xffffffffu, slow);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                tab[4 + 32 * g + lane] = missing[g] ? __uint_as_float(kAbsent) : bare_k[g] ? ks[g] : exp2_int(ek);
+                tab[4 + 128 + 32 * g + lane] = 0.f;
+            }
+            if (slow) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    // (a scale below the normal range counts as its smallest number)
+                    const bool tiny = (__float_as_uint(vs[g]) & 0x7fffffffu) < 0x00800000u;
+                    if (bare_v[g] && present[g])
+                        tab[4 + 128 + 32 * g + lane] = log2f(tiny ? 1.17549435e-38f : vs[g]) - static_cast<float>(ev);
+                }
+            }
+            if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * D;
+            if (lane == 0) {
+                *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), __uint_as_float(slow ? 1u : 0u), 0.f);
+                *reinterpret_cast<int*>(record + 1344) = 1;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
-            if (!live) break;
-            if (++slot == C::kRecords) {
-                slot = 0;
-                parity ^= 1u;
-            }
-            if (++table == C::kTables) table = 0;
         }
-        // ---- the next step, if there is one
-        live = true;
-        if (++step >= last) {
-            if (cw == 0) {
-                if (lane == 0) lay_out_job<D>(a, smem, job_full, job_empty, ranges, jobs);
-                __syncwarp();
-            }
-            Job job;
-            live = next_job<D, 32>(smem, job_full, job_empty, jobs, job);
-            step = job.s0;
-            last = job.s1;
-            n = job.n;
-            head = job.head;
-            trow = a.tables + static_cast<int64_t>(job.seq) * a.max_blocks;
-            opened = live;
-        }
-        if (!live) continue;
-        if (opened || (step & 3) == 0) {
-            ids = ids_next;
-#pragma unroll 1
-            for (int k = opened ? 0 : 1; k < 2; ++k) {
-                const int b = 32 * ((step >> 2) + k) + lane;
-                int id = -1;
-                if (b < (n + 15) / 16) {
-                    id = __ldg(trow + b);
-                    if (id < 0 || id >= a.num_blocks) {
-                        atomicOr(a.status, PKV_DEVERR_RANGE);
-                        id = -2;
-                    }
-                }
-                if (k == 0) ids = id;
-                ids_next = id;
-            }
-        }
-        const int id = __shfl_sync(0xffffffffu, ids, (step & 3) * 8 + 2 * cw + lane / 16);
-        present = id >= 0 && step * kChunkStep + 32 * cw + lane < n;
-        missing = id == -2;
-        // an absent block's codes may be any (its tokens carry no weight): block 0 exists
-        row = static_cast<int64_t>(max(0, id)) * a.kv_heads + head;
-        const float* rec = a.scales + row * 32 + (lane & 15);
-        ks = __ldg(rec);
-        vs = __ldg(rec + 16);
-        if (opened) {  // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
-            const int first = max(0, __shfl_sync(0xffffffffu, ids, (step & 3) * 8));
-            const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + head) * 32 + lane);
-            sample = step * kChunkStep + (lane & 15) < n ? x : 0.f;
-        }
+        base += steps;
+    }
+    if (at != base) return;  // the record after the last says that there is none
+    const int slot = at % C::kRecords;
+    if (!warp_wait(&empty[slot], (static_cast<uint32_t>(at / C::kRecords) & 1u) ^ 1u)) {
+        report_timeout(a);
+        return;
+    }
+    if (lane == 0) {
+        *reinterpret_cast<int*>(smem + C::kOffRecord + slot * C::kRecordBytes + 1344) = 0;
+        mbar_arrive(&full[slot]);
     }
 }
 
@@ -715,7 +707,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             mbar_init(&job_empty[i], 16);
         }
         for (int i = 0; i < C::kRecords; ++i) {
-            mbar_init(&rec_full[i], 4);
+            mbar_init(&rec_full[i], 1);
             mbar_init(&rec_empty[i], 8);
         }
         fence_barrier_init();
