@@ -43,19 +43,19 @@
 // of 16 KB, the next step's codes 32 KB.
 //
 // What bounds it: instructions. A step's products would take 2500 cycles of the
-// tensor cores at the rate a large matrix product reaches; the step takes about 3850,
+// tensor cores at the rate a large matrix product reaches; the step takes about 3700,
 // in which the schedulers issue two of three slots: some 900 instructions per scheduler
-// for the softmax, 900 for the conversion, most of the rest waits. Each instruction of
-// the two loops costs a warp 7 cycles, the price of sharing a scheduler and the
-// instruction cache. So the loops are short rather than unrolled, and everything that is
-// done once per step or segment sits in warps of its own. 8 sequences of 8192 tokens,
-// 512 of them new, 32 query heads on 8 of 128: 465 us, 1145 TFLOP/s of the visible pairs
-// (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8: 455 us, 1205.
-// Slower, for the first (before the last few steps, against 502): eight warps for K
-// instead of four (56 registers for a converter) 518 us; scores as one product of 128
-// tokens 593.
-// Small calls are bound by the chain before the first product: 2.7 us to plan, 4 for
-// the table, the scales and the codes, one after another; 15 us for 40 new tokens on
+// for the softmax, 900 for the conversion, the rest waits and set-up. An instruction of
+// those loops costs a warp 7 cycles, the price of sharing a scheduler and the
+// instruction cache. So everything that is done once per step or segment sits in warps
+// of its own, and waits and issuing loops are as short as they go. 8 sequences of 8192
+// tokens, 512 of them new, 32 query heads on 8 of 128: 419 us, 1271 TFLOP/s of the
+// visible pairs (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8:
+// 415 us, 1322. Slower, for the first: scores as one product of 128 tokens 520 (against
+// 425: a half's softmax waits for all of it); eight warps for K instead of four 518
+// (against 502).
+// Small calls are bound by the chain before the first product: 2.5 us to plan, 4 for
+// the table, the scales and the codes, one after another; 14 us for 40 new tokens on
 // 200.
 #include <math.h>
 
@@ -733,10 +733,10 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     const uint32_t tmem = *tmem_slot;
 
     // Registers: launched with 80 a thread, 61440 together, which 256 softmax threads at
-    // 128, 256 converters at 64, 128 issuers at 40 and 128 threads for the scales at 56
-    // share: none spills in its loop. (A few spilled words there cost a tenth.)
+    // 120, 256 converters at 64, 128 issuers at 40 and 128 threads for the scales at 72
+    // share: none spills. (A few spilled words in a loop cost up to a tenth.)
     if (warp < C::kSoftmaxWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it
         const int x = warp >> 2;
         const int rr = (warp & 3) * 32 + lane;
@@ -1009,7 +1009,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         else
             convert_role<D, true>(a, smem, rec_full, rec_empty, v_full, v_empty);
     } else if (warp >= C::kScaleWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         scale_role<D>(a, smem, count, job_full, job_empty, rec_full, rec_empty);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");

@@ -20,9 +20,10 @@
 // t so that a position is found by bisection over closed forms:
 //     a + 4 t,   a = ceil(((n - nq + kOverTokens) G + 256) / 64).
 // A last tile of few rows costs as much as a full one: converting a step's codes takes
-// as long as its products for both row halves, and the products wait for it. (Counting
-// a tile of one row half as half the work: ragged chunks of 1 to 512 tokens 181 us
-// instead of 147; a start-up of 192 tokens 166, of 640 148, of 1024 149.)
+// about as long as its products for both row halves, and the products wait for it.
+// (Ragged chunks of 1 to 777 tokens when a tile of one row half counted half: 181 us,
+// like this 147. With a start-up of 256 tokens they now take 126 us, of 384 106, 512
+// 102, 768 102; 24 new tokens on ragged contexts 45, 37, 39 and 40.)
 // The cost only places cuts; a unit's steps are counted exactly.
 //
 // Plain integer arithmetic, compiled for the host as well, where a test checks
