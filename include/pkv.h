@@ -454,8 +454,8 @@ PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_hea
  *   workspace     >= pkv_multiquery_q8_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use.
  * fp32 accumulation, one rounding to bf16. Up to 16 query rows per (sequence, KV
- * head) at head_dim 128 and wide tables run on pkv_decode_attention_q8's kernel with
- * its roundings. All else runs in tiles on f16 tensor cores:
+ * head) at head_dim 128 with tables for many tokens run on pkv_decode_attention_q8's
+ * kernel with its roundings. All else runs in tiles on f16 tensor cores:
  * q enters exactly (scaled by a power of two per row), a K value is rounded to f16
  * once (an eighth of a quantization step at most), a V value twice (scale, value), a
  * softmax weight once. Scales of any size and spread are taken.

@@ -106,22 +106,22 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // (pkv_multiquery.cu) holds 32 rows per (sequence, KV head) of 128; beside the tile
 // kernel, which turns the codes into f16 once for all rows, it is ahead where rows are
 // few and the caches long. 32 query heads on 8, split : tile in us,
-//     sequences x tokens   4 rows       16 rows      32 rows
-//     1 x 1024                          46 : 21      60 : 21
-//     1 x 4096             37 : 27      49 : 27      56 : 28
-//     1 x 32768            43 : 52      64 : 52      80 : 51
-//     8 x 4096             33 : 49      48 : 49      64 : 49
-//     8 x 32768           102 : 237    170 : 237    304 : 234
-//     32 x 4096            58 : 140     95 : 141    159 : 141
-//     64 x 8192           179 : 469    308 : 471    582 : 466
-// Lengths are the device's: the table's width stands in for them, and only a call whose
-// tables could not hold 65536 (token, KV head) pairs is taken as short.
+//     sequences x tokens   4 or 8 rows   16 rows      32 rows
+//     1 x 1024              36 : 18       46 : 18      60 : 19
+//     1 x 4096              37 : 24       49 : 25      56 : 25
+//     1 x 32768             44 : 45       63 : 46      80 : 46
+//     8 x 4096              33 : 42       48 : 42      64 : 42
+//     32 x 4096             58 : 119      95 : 120    159 : 120
+//     8 x 32768            102 : 197     170 : 197    304 : 196
+//     64 x 8192            178 : 398     308 : 402    582 : 397
+// Lengths are the device's: what the tables could hold stands in for them, in (token,
+// KV head) pairs.
 bool split_kernel_takes(const pkv_cache_desc* d, int32_t batch, int32_t max_blocks, int32_t max_query_len, int G) {
-    constexpr int kMostRows = 16;
-    static_assert(kMostRows <= kMqMaxRows, "rows of the split kernel");
-    return d->head_dim == 128 && static_cast<int64_t>(max_query_len) * G <= kMostRows &&
-           static_cast<int64_t>(max_blocks) * 16 * d->num_kv_heads > 65536 / batch;
+    const int64_t rows = static_cast<int64_t>(max_query_len) * G;
+    const int64_t most = rows <= 8 ? 65536 : 524288;  // pairs that tiles take in less time
+    return d->head_dim == 128 && rows <= 16 && static_cast<int64_t>(max_blocks) * 16 * d->num_kv_heads > most / batch;
 }
+static_assert(16 <= kMqMaxRows, "rows of the split kernel");
 
 // Both reading-back calls, after the checks of their descriptors.
 pkv_status run_gather(const void* k, const void* v, const float* scales, const int32_t* tables, int32_t max_blocks,

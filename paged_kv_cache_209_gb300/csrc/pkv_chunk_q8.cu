@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
             for (int j = 0; j < steps; ++j, ++it, ++table) {
                 const float* tab = reinterpret_cast<const float*>(smem + C::kOffTable + (table % C::kTables) * C::kTableBytes);
                 const int seen = lim - (job.s0 + j) * kChunkStep + 1;  // tokens of the step the row sees
-                const bool masked = (job.s0 + j + 1) * kChunkStep - 1 > warp_lim;
+                const bool masked = (job.s0 + j) * kChunkStep + kChunkStep - 1 > warp_lim;
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     if (!warp_wait(&s_full[2 * x + part], it & 1)) {

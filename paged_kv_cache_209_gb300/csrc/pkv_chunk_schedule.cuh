@@ -86,7 +86,7 @@ PKV_HD inline int chunk_tiles(const ChunkSeq& q, int group) { return (q.nq * gro
 PKV_HD inline int chunk_steps(const ChunkSeq& q, int group, int t) {
     const int rows = q.nq * group;
     const int end = (t + 1) * kChunkRows < rows ? (t + 1) * kChunkRows : rows;
-    return (q.n - q.nq + (end - 1) / group + 1 + kChunkStep - 1) / kChunkStep;
+    return (q.n - q.nq + (end - 1) / group) / kChunkStep + 1;  // (the last token's index: below 2^31)
 }
 
 PKV_HD inline int64_t chunk_cost_base(const ChunkSeq& q, int group) {

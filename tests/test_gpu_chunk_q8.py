@@ -157,7 +157,7 @@ def test_few_rows_and_wide_tables(pkv, nqs, hq):
     c = make(hq + nqs[0], [700, 40, 129, 9, 3000], nqs, hq, 8, 128)
     want = reference(c)
     narrow = call(pkv, c)
-    c["tables"] = np.pad(c["tables"], ((0, 0), (0, 600)), constant_values=-1)      # entries no sequence uses
+    c["tables"] = np.pad(c["tables"], ((0, 0), (0, 1200)), constant_values=-1)      # entries no sequence uses
     wide = call(pkv, c)
     check(narrow, c, want)
     check(wide, c, want)
@@ -418,7 +418,7 @@ def test_prefill512_layer_sampled(pkv):
 def test_one_workspace_for_calls_of_all_sizes_on_both_kernels(pkv):
     """The size for the largest call serves every smaller one, in any order: each
     result is the one a workspace of its own gives, bit for bit."""
-    mixes = [([700, 900, 65], [300, 40, 65]), ([2000, 77, 31, 5000, 900], [4, 1, 4, 2, 3]), ([300] * 70, [2] * 70),
+    mixes = [([700, 900, 65], [300, 40, 65]), ([2000, 77, 31, 5000, 900], [2, 1, 2, 2, 1]), ([300] * 70, [2] * 70),
              ([900, 2500], [8, 8]), ([40, 3000], [40, 100])]
     built = [make(90 + i, lens, nqs, 16, 4, 128) for i, (lens, nqs) in enumerate(mixes)]
     on = [device(c) for c in built]

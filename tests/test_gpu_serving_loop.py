@@ -167,8 +167,8 @@ class Mirror:
 
 
 SHAPES = [  # prompts, drafts, query heads, KV heads, head_dim, least table width
-    ([38, 1, 131, 16, 2], 3, 8, 2, 128, 512),    # 16 rows per KV head, wide tables: the kernel that splits the cache
-    ([38, 1, 131, 16, 2], 3, 8, 2, 128, 0),      # the same on tiles
+    ([38, 1, 131, 16, 2], 1, 8, 2, 128, 512),    # 8 rows per KV head, wide tables: the kernel that splits the cache
+    ([38, 1, 131, 16, 2], 1, 8, 2, 128, 0),      # the same on tiles
     ([38, 1, 131, 16, 2], 9, 8, 2, 128, 0),      # 40 rows
     ([5, 200, 17], 3, 6, 2, 64, 0),
     ([300, 1], 0, 4, 4, 64, 0),                  # no drafts: each step samples one token
