@@ -42,18 +42,19 @@
 // next scores run. Shared memory: Q 64 KB, two stages of K of 32 KB each, three of V
 // of 16 KB, the next step's codes 32 KB.
 //
-// What bounds it: instructions. A step's products would take 2500 cycles of the
-// tensor cores at the rate a large matrix product reaches; the step takes about 3700,
-// in which the schedulers issue two of three slots: some 900 instructions per scheduler
-// for the softmax, 900 for the conversion, the rest waits and set-up. An instruction of
-// those loops costs a warp 7 cycles, the price of sharing a scheduler and the
+// What bounds it: the tensor pipe is busy 72 % of the time (56 % at its product rate: a
+// score product of 64 tokens reads 6 KB of operands for 32 cycles), the schedulers issue
+// in 60 % of the slots, and both halves' chains of scores, softmax and products are
+// about as long as a step, 3700 cycles against 2500 for the products alone. An
+// instruction costs a warp 7 cycles, the price of sharing a scheduler and the
 // instruction cache. So everything that is done once per step or segment sits in warps
 // of its own, and waits and issuing loops are as short as they go. 8 sequences of 8192
 // tokens, 512 of them new, 32 query heads on 8 of 128: 419 us, 1271 TFLOP/s of the
 // visible pairs (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8:
 // 415 us, 1322. Slower, for the first: scores as one product of 128 tokens 520 (against
-// 425: a half's softmax waits for all of it); eight warps for K instead of four 518
-// (against 502).
+// 425: a half's softmax waits for all of it); the halves' softmax in turns 535, half B
+// held back by a part 442 (against 423); eight warps for K instead of four 518 (against
+// 502).
 // Small calls are bound by the chain before the first product: 2.5 us to plan, 4 for
 // the table, the scales and the codes, one after another; 14 us for 40 new tokens on
 // 200.
