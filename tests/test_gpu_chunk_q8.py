@@ -470,3 +470,21 @@ def test_many_more_units_than_ctas(pkv):
     check(out[torch.from_numpy(rows).cuda()], part)
     assert torch.isfinite(out).all()
     assert pkv.pkv_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(pkv, seed):
+    """Lengths, chunks, groups and the size of the cached rows drawn at random, some rows far larger or smaller."""
+    rng = np.random.default_rng(700 + seed)
+    hkv, d = int(rng.choice([1, 2, 4])), int(rng.choice([64, 128]))
+    group = int(rng.choice([1, 2, 3, 4, 5, 8, 12]))
+    lens = [int(n) for n in np.exp(rng.uniform(0, np.log(2500), rng.integers(1, 7)))]
+    nqs = [int(rng.integers(0, min(n, 300) + 1)) for n in lens]
+    c = make(seed, lens, nqs, group * hkv, hkv, d, kscale=2.0 ** rng.integers(-6, 2), vscale=2.0 ** rng.integers(-20, 20))
+    if seed % 2:                                             # tokens whose scales leave the range of the others
+        odd = rng.random(c["ks"].shape) < 0.01
+        c["ks"][odd] *= np.float32(2.0) ** np.float32(-20)
+        odd = rng.random(c["vs"].shape) < 0.01
+        c["vs"][odd] *= np.float32(2.0) ** rng.choice([-26, 12], odd.sum()).astype(np.float32)
+    check(call(pkv, poison(c)), c)
+    assert pkv.pkv_device_status(clear=True) == 0
