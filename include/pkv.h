@@ -405,7 +405,8 @@ PKV_API size_t pkv_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, 
  * stand for (code * scale). q and out are bf16 as in those calls; fp32
  * accumulation, one rounding to bf16. The products run on f16 tensor cores:
  * the codes and q (each row scaled by a power of two) are exact there, the
- * softmax weights times the V scale are rounded to f16. head_dim 128, at most
+ * softmax weights times the V scale are rounded to f16 (a product below 2^-25 is
+ * lost; pkv_multiquery_attention_q8 takes scales of any size). head_dim 128, at most
  * 32 query rows per (sequence, KV head). Errors, checked mode and the device
  * status bits as in pkv_multiquery_attention; query_start NULL with
  * max_query_len != 1 is PKV_ERR_SHAPE.
@@ -453,12 +454,13 @@ PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_hea
  *   max_query_len host bound on nq, 1 .. 65536 (above: PKV_ERR_UNSUPPORTED).
  *   workspace     >= pkv_multiquery_q8_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use.
- * fp32 accumulation, one rounding to bf16. Up to 16 query rows per (sequence, KV
- * head) at head_dim 128 with tables for many tokens run on pkv_decode_attention_q8's
- * kernel with its roundings. All else runs in tiles on f16 tensor cores:
- * q enters exactly (scaled by a power of two per row), a K value is rounded to f16
- * once (an eighth of a quantization step at most), a V value twice (scale, value), a
- * softmax weight once. Scales of any size and spread are taken.
+ * fp32 accumulation, one rounding to bf16. Scales of any size and spread are taken.
+ * Up to 16 query rows per (sequence, KV head) at head_dim 128 with tables for many
+ * tokens run on pkv_decode_attention_q8's kernel: codes and q (scaled by a power of two
+ * per row) enter exactly, a softmax weight times its V scale is rounded to f16 once.
+ * All else runs in tiles on f16 tensor cores: q enters exactly in the same way, a K
+ * value is rounded to f16 once (an eighth of a quantization step at most), a V value
+ * twice (scale, value), a softmax weight once.
  * Errors, checked mode and the device status bits as pkv_multiquery_attention.
  */
 PKV_API pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes,

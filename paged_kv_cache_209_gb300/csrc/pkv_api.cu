@@ -651,12 +651,12 @@ size_t pkv_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t 
 }
 
 // The split kernel over int8 pools (arguments checked). The workspace holds the
-// counters of `counted` sequences, then the pieces.
+// counters of `counted` sequences, then the pieces. wide: scales of any size.
 static pkv_status run_split_q8(const void* q, const void* k_codes, const void* v_codes, const float* scales,
                                const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
                                const int32_t* query_start, int32_t batch, int32_t num_q_heads, int32_t max_query_len,
                                float scale, void* out, void* workspace, size_t workspace_bytes, int32_t counted,
-                               const pkv_cache_desc* desc, uint32_t flags, const pkv_decode_opts* opts, void* stream) {
+                               bool wide, const pkv_cache_desc* desc, uint32_t flags, const pkv_decode_opts* opts, void* stream) {
     const int G = num_q_heads / desc->num_kv_heads;
     const int num_ctas = mq_num_ctas(desc->head_dim, batch, opts, true);
     size_t co = 0, po = 0;
@@ -687,6 +687,7 @@ static pkv_status run_split_q8(const void* q, const void* k_codes, const void* v
         a.v_cache = v_codes;
         a.scales = scales;
         a.q8 = 1;
+        a.wide = wide ? 1 : 0;
         a.tables = block_tables + static_cast<int64_t>(b0) * max_blocks_per_seq;
         a.lens = context_lens + b0;
         a.partials = reinterpret_cast<float*>(ws + po);
@@ -734,7 +735,7 @@ pkv_status pkv_decode_attention_q8(const void* q, const void* k_codes, const voi
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return PKV_ERR_ALIGN;
     return run_split_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, query_start, batch,
-                        num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, batch, desc, flags, opts, stream);
+                        num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, batch, false, desc, flags, opts, stream);
 }
 
 size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
@@ -775,8 +776,8 @@ pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const
     const int G = num_q_heads / desc->num_kv_heads;
     if (split_kernel_takes(desc, batch, max_blocks_per_seq, max_query_len, G))
         return run_split_q8(q, k_codes, v_codes, scales, block_tables, max_blocks_per_seq, context_lens, query_start, batch,
-                            num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, kMaxBatchPerLaunch, desc,
-                            flags, nullptr, stream);
+                            num_q_heads, max_query_len, scale, out, workspace, workspace_bytes, kMaxBatchPerLaunch, true,
+                            desc, flags, nullptr, stream);
     size_t co = 0, po = 0;
     mq_workspace_bytes(kMaxBatchPerLaunch, desc->num_kv_heads, desc->head_dim, 0, &co, &po);
     if (workspace_bytes < po + chunk_q8_workspace_bytes(desc->head_dim)) return PKV_ERR_WORKSPACE;

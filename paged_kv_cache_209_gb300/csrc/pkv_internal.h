@@ -212,6 +212,7 @@ struct MqArgs {
     // pool: [num_blocks][kv_heads][2 (K, V)][16] float
     const float* scales;
     int32_t q8;
+    int32_t wide;        // int8 pools: scales of any size (see mq_tc_kernel)
     int32_t test_stall;  // PKV_FLAG_TEST_STALL: the producer issues nothing
 };
 constexpr int kMqMaxRows = 32;      // query rows per (sequence, KV head) of the mma.sync kernel

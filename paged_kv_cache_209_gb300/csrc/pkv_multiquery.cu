@@ -203,7 +203,28 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D, int NST, bool Q8>
+// Wide (int8 only; pkv_multiquery_attention_q8): q, K scales and V scales of any size
+// and spread, and any scale on tokens that a row may not see.
+//  * q rows are scaled by a power of two in both directions, K's factor and the row's
+//    are multiplied first, so that neither q nor a score leaves the range in between;
+//  * a row's base m is the maximum not of its scores but of score + log2 |V scale|, less
+//    kWideHeadroom: what is rounded to f16, P' = 2^(x - m) v, then lies high in the f16
+//    range for the tokens that make up the output, however large the V scales are and
+//    however much weight a token of small V takes (an attention sink). l sums
+//    2^(x - m) in fp32 and cancels m. A V scale counts as kWideTinyV at least, so that l
+//    stays below 2^(16 + 96) times the tokens;
+//  * where the base may have to move, rows of zero codes (their scale is 1 by definition)
+//    leave the maximum;
+//  * P' is 0, not 0 times the V scale, where the row does not see the token.
+// The vote that finds such blocks replaces the one on the running maximum, so that it costs
+// nothing: 32 query heads on 8, 8 sequences of 32768 tokens, 8 rows 103 us with it and 103
+// without, 16 rows 170 and 170; 64 of 8192, 8 rows 177 and 178.
+constexpr float kWideHeadroom = 8.f;
+constexpr float kWideMost = 65504.f;     // the largest f16
+constexpr float kWideTinyV = 1.2621774e-29f;  // 2^-96
+constexpr float kWideUnset = -3.0e38f;   // base of a row that has seen no token
+
+template <int D, int NST, bool Q8, bool Wide>
 __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
     mq_tc_kernel(const MqArgs a, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ CUtensorMap tmS) {
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
             } else {
                 // f16 operands: coordinates 4 tig .. 4 tig + 3 of each 16 (the
                 // contraction order of the int8 K fragments), the row scaled by
-                // 2^-e so that its largest magnitude stays below 2^15
+                // 2^-e so that its largest magnitude stays below 2^15 (Wide: reaches 2^14)
                 float qv[D / 16][4];
                 float qmax = 0.f;
 #pragma unroll
@@ -448,7 +469,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                 qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 1));
                 qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 2));
                 const int ex = static_cast<int>((__float_as_uint(qmax) >> 23) & 0xffu) - 127;
-                const int e = ex > 14 ? ex - 14 : 0;
+                const int e = Wide ? max(ex - 14, -126) : ex > 14 ? ex - 14 : 0;
                 const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                 const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                 float qsum = 0.f;  // of the f16 operands as rounded
@@ -473,7 +494,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
         const int rc0 = rg * 8 + 2 * tig, rc1 = rc0 + 1;
         const int lim0 = rc0 < rows ? n_ctx - nq + rc0 / G : -1;
         const int lim1 = rc1 < rows ? n_ctx - nq + rc1 / G : -1;
-        float m0 = ninf(), m1 = ninf(), l0 = 0.f, l1 = 0.f;
+        float m0 = Wide ? kWideUnset : ninf(), m1 = m0, l0 = 0.f, l1 = 0.f;
         float o[D / 16][4];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -601,66 +622,120 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                 // [0] (token tokA, row 2tig) [1] (tokA, 2tig+1) [2] (tokB, 2tig) [3] (tokB, 2tig+1)
                 const int pA = blk * 16 + tokA, pB = blk * 16 + tokB;
                 const float kA = ksc[tokA], kB = ksc[tokB];
-                const float x0 = pA <= lim0 ? (sa[0] + sb[0] - kb0) * kA * cf0 : ninf();
-                const float x1 = pA <= lim1 ? (sa[1] + sb[1] - kb1) * kA * cf1 : ninf();
-                const float x2 = pB <= lim0 ? (sa[2] + sb[2] - kb0) * kB * cf0 : ninf();
-                const float x3 = pB <= lim1 ? (sa[3] + sb[3] - kb1) * kB * cf1 : ninf();
+                // the factors of a score: in Wide one product, or the two would leave the range apart
+                const float fA0 = Wide ? kA * cf0 : kA, fA1 = Wide ? kA * cf1 : kA;
+                const float fB0 = Wide ? kB * cf0 : kB, fB1 = Wide ? kB * cf1 : kB;
+                const float g0 = Wide ? 1.f : cf0, g1 = Wide ? 1.f : cf1;
+                const float x0 = pA <= lim0 ? (sa[0] + sb[0] - kb0) * fA0 * g0 : ninf();
+                const float x1 = pA <= lim1 ? (sa[1] + sb[1] - kb1) * fA1 * g1 : ninf();
+                const float x2 = pB <= lim0 ? (sa[2] + sb[2] - kb0) * fB0 * g0 : ninf();
+                const float x3 = pB <= lim1 ? (sa[3] + sb[3] - kb1) * fB1 * g1 : ninf();
                 if (!mbar_wait(&full[C::kStages + s], par, a.status, abort_flag, wlim)) return;
-                // P' = P times the V scale of its token (zero past the context), as f16
-                float vA = pA < n_ctx ? vsc[tokA] : 0.f, vB = pB < n_ctx ? vsc[tokB] : 0.f;
-                // P <= 2^8 under the lazy rescale, so P' stays below the f16
-                // maximum while every V scale is at most kVScaleF16Safe. A block
-                // with a larger scale (rows with max |v| above ~32 000) runs its
-                // product on P' 2^-k and O 2^-k, and O is scaled back by 2^k
-                // afterwards: powers of two, exact in fp32. One vote covers both
-                // rare cases (a new running maximum, a large V scale): a second
-                // vote and branch per block cost 1.6 % of the call.
-                float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+                uint32_t bh0, bh1;
                 float o_back = 1.f;
-                if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || fmaxf(vA, vB) > kVScaleF16Safe)) {
+                if (Wide) {
+                    float vA = vsc[tokA], vB = vsc[tokB];
+                    float wA = fmaxf(fabsf(vA), kWideTinyV), wB = fmaxf(fabsf(vB), kWideTinyV);  // (of NaN: the bound)
+                    float e0 = ex2(x0 - m0), e1 = ex2(x1 - m1), e2 = ex2(x2 - m0), e3 = ex2(x3 - m1);
+                    if (__any_sync(0xffffffffu, fmaxf(fmaxf(e0 * wA, e1 * wA), fmaxf(e2 * wB, e3 * wB)) > kWideMost)) {
+                        // tokens whose V codes are all zero: the bytes of 16 ors over the coordinates
+                        const uint4* vcodes = reinterpret_cast<const uint4*>(smem + s * C::kStageBytes + 16 * D);
+                        uint4 any = vcodes[lane];
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) {
-                        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-                        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-                    }
-                    // a rescale to the running maximum (exact whether or not it moved)
-                    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-                    const float nb0 = mn0 == ninf() ? 0.f : mn0;
-                    const float nb1 = mn1 == ninf() ? 0.f : mn1;
-                    float al0 = m0 == ninf() ? 0.f : ex2(m0 - nb0);
-                    float al1 = m1 == ninf() ? 0.f : ex2(m1 - nb1);
-                    l0 *= al0;
-                    l1 *= al1;
-                    m0 = mn0;
-                    m1 = mn1;
-                    // and the block's V-scale shift, folded into the same pass over O
-                    float vm = fmaxf(vA, vB);
+                        for (int i = 1; i < D / 32; ++i) {
+                            const uint4 w = vcodes[32 * i + lane];
+                            any = make_uint4(any.x | w.x, any.y | w.y, any.z | w.z, any.w | w.w);
+                        }
+                        any = make_uint4(__reduce_or_sync(0xffffffffu, any.x), __reduce_or_sync(0xffffffffu, any.y),
+                                         __reduce_or_sync(0xffffffffu, any.z), __reduce_or_sync(0xffffffffu, any.w));
+                        auto zero = [&](int tok, float v) {  // (a zero times an infinite scale is none)
+                            const uint32_t w = tok < 4 ? any.x : tok < 8 ? any.y : tok < 12 ? any.z : any.w;
+                            return ((w >> (8 * (tok & 3))) & 0xffu) == 0u && fabsf(v) <= 3.402823466e38f;
+                        };
+                        if (zero(tokA, vA)) vA = 0.f, wA = kWideTinyV;
+                        if (zero(tokB, vB)) vB = 0.f, wB = kWideTinyV;
+                        const float jA = fminf(__log2f(wA), 128.f), jB = fminf(__log2f(wB), 128.f);
+                        float j0 = fmaxf(x0 + jA, x2 + jB), j1 = fmaxf(x1 + jA, x3 + jB);
 #pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
-                    if (vm > kVScaleF16Safe && vm <= 3.0e38f) {
-                        const int k2 = pow2_shift_to_fit(vm);
-                        const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
-                        o_back = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
-                        vA *= down;
-                        vB *= down;
-                        al0 *= down;
-                        al1 *= down;
-                    }
+                        for (int off = 4; off < 32; off <<= 1) {
+                            j0 = fmaxf(j0, __shfl_xor_sync(0xffffffffu, j0, off));
+                            j1 = fmaxf(j1, __shfl_xor_sync(0xffffffffu, j1, off));
+                        }
+                        const float mn0 = fmaxf(m0, j0 - kWideHeadroom), mn1 = fmaxf(m1, j1 - kWideHeadroom);
+                        const float al0 = ex2(m0 - mn0), al1 = ex2(m1 - mn1);
+                        l0 *= al0;
+                        l1 *= al1;
+                        m0 = mn0;
+                        m1 = mn1;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        o[i][0] *= al0;
-                        o[i][1] *= al1;
-                        o[i][2] *= al0;
-                        o[i][3] *= al1;
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i][0] *= al0;
+                            o[i][1] *= al1;
+                            o[i][2] *= al0;
+                            o[i][3] *= al1;
+                        }
+                        e0 = ex2(x0 - m0), e1 = ex2(x1 - m1), e2 = ex2(x2 - m0), e3 = ex2(x3 - m1);
                     }
+                    l0 += e0 + e2;
+                    l1 += e1 + e3;
+                    bh0 = movmatrix_trans(pack_f16x2(pA <= lim0 ? e0 * vA : 0.f, pA <= lim1 ? e1 * vA : 0.f));
+                    bh1 = movmatrix_trans(pack_f16x2(pB <= lim0 ? e2 * vB : 0.f, pB <= lim1 ? e3 * vB : 0.f));
+                } else {
+                    // P' = P times the V scale of its token (zero past the context), as f16
+                    float vA = pA < n_ctx ? vsc[tokA] : 0.f, vB = pB < n_ctx ? vsc[tokB] : 0.f;
+                    // P <= 2^8 under the lazy rescale, so P' stays below the f16
+                    // maximum while every V scale is at most kVScaleF16Safe. A block
+                    // with a larger scale (rows with max |v| above ~32 000) runs its
+                    // product on P' 2^-k and O 2^-k, and O is scaled back by 2^k
+                    // afterwards: powers of two, exact in fp32. One vote covers both
+                    // rare cases (a new running maximum, a large V scale): a second
+                    // vote and branch per block cost 1.6 % of the call.
+                    float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
+                    if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || fmaxf(vA, vB) > kVScaleF16Safe)) {
+    #pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) {
+                            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+                            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+                        }
+                        // a rescale to the running maximum (exact whether or not it moved)
+                        const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+                        const float nb0 = mn0 == ninf() ? 0.f : mn0;
+                        const float nb1 = mn1 == ninf() ? 0.f : mn1;
+                        float al0 = m0 == ninf() ? 0.f : ex2(m0 - nb0);
+                        float al1 = m1 == ninf() ? 0.f : ex2(m1 - nb1);
+                        l0 *= al0;
+                        l1 *= al1;
+                        m0 = mn0;
+                        m1 = mn1;
+                        // and the block's V-scale shift, folded into the same pass over O
+                        float vm = fmaxf(vA, vB);
+    #pragma unroll
+                        for (int off = 1; off < 32; off <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
+                        if (vm > kVScaleF16Safe && vm <= 3.0e38f) {
+                            const int k2 = pow2_shift_to_fit(vm);
+                            const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
+                            o_back = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+                            vA *= down;
+                            vB *= down;
+                            al0 *= down;
+                            al1 *= down;
+                        }
+    #pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[i][0] *= al0;
+                            o[i][1] *= al1;
+                            o[i][2] *= al0;
+                            o[i][3] *= al1;
+                        }
+                    }
+                    const float b0 = m0 == ninf() ? 0.f : m0;
+                    const float b1 = m1 == ninf() ? 0.f : m1;
+                    const float e0 = ex2(x0 - b0), e1 = ex2(x1 - b1), e2 = ex2(x2 - b0), e3 = ex2(x3 - b1);
+                    l0 += e0 + e2;
+                    l1 += e1 + e3;
+                    bh0 = movmatrix_trans(pack_f16x2(e0 * vA, e1 * vA));
+                    bh1 = movmatrix_trans(pack_f16x2(e2 * vB, e3 * vB));
                 }
-                const float b0 = m0 == ninf() ? 0.f : m0;
-                const float b1 = m1 == ninf() ? 0.f : m1;
-                const float e0 = ex2(x0 - b0), e1 = ex2(x1 - b1), e2 = ex2(x2 - b0), e3 = ex2(x3 - b1);
-                l0 += e0 + e2;
-                l1 += e1 + e3;
-                const uint32_t bh0 = movmatrix_trans(pack_f16x2(e0 * vA, e1 * vA));
-                const uint32_t bh1 = movmatrix_trans(pack_f16x2(e2 * vB, e3 * vB));
                 // ---- O^T += V^T P'^T: V coordinate rows of 16 token codes
 #pragma unroll
                 for (int ii = 0; ii < D / 32; ++ii) {
@@ -674,7 +749,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                     codes_to_f16x2(w3, a1, a3);
                     mma_f16_16816(o[2 * ii + 1], a0, a1, a2, a3, bh0, bh1);
                 }
-                if (o_back != 1.f) {
+                if (!Wide && o_back != 1.f) {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         o[i][0] *= o_back;
@@ -842,7 +917,7 @@ constexpr int kMq8Stages = PKV_MQ8_STAGES;
 template <bool Q8>
 constexpr int mq_stages() { return Q8 ? kMq8Stages : kMqStages; }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool Wide = false>
 cudaError_t run_mq(const MqArgs& a, int grid, cudaStream_t s) {
     using C = Mq<D, mq_stages<Q8>(), Q8>;
     CUtensorMap tmK, tmV, tmS;
@@ -864,9 +939,9 @@ cudaError_t run_mq(const MqArgs& a, int grid, cudaStream_t s) {
         tmS = tmK;  // unused by the bf16 path
     }
     const size_t smem = C::smem_bytes(a.batch);
-    cudaFuncSetAttribute(mq_tc_kernel<D, mq_stages<Q8>(), Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(mq_tc_kernel<D, mq_stages<Q8>(), Q8, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          static_cast<int>(smem));
-    return launch_pdl(mq_tc_kernel<D, mq_stages<Q8>(), Q8>, dim3(grid), dim3(C::kThreads), smem, s, a, tmK, tmV, tmS);
+    return launch_pdl(mq_tc_kernel<D, mq_stages<Q8>(), Q8, Wide>, dim3(grid), dim3(C::kThreads), smem, s, a, tmK, tmV, tmS);
 }
 
 }  // namespace
@@ -885,13 +960,13 @@ int mq_num_ctas(int head_dim, int batch, const pkv_decode_opts* opts, bool q8) {
     if (slot == 0) {
         // occupancy at the largest launch (the per-sequence arrays grow with the batch)
         if (q8)
-            slot = mq_occupancy(mq_tc_kernel<128, kMq8Stages, true>, Mq<128, kMq8Stages, true>::kThreads,
+            slot = mq_occupancy(mq_tc_kernel<128, kMq8Stages, true, false>, Mq<128, kMq8Stages, true>::kThreads,
                                 Mq<128, kMq8Stages, true>::smem_bytes(kMaxBatchPerLaunch));
         else if (head_dim == 128)
-            slot = mq_occupancy(mq_tc_kernel<128, kMqStages, false>, Mq<128, kMqStages>::kThreads,
+            slot = mq_occupancy(mq_tc_kernel<128, kMqStages, false, false>, Mq<128, kMqStages>::kThreads,
                                 Mq<128, kMqStages>::smem_bytes(kMaxBatchPerLaunch));
         else
-            slot = mq_occupancy(mq_tc_kernel<64, kMqStages, false>, Mq<64, kMqStages>::kThreads,
+            slot = mq_occupancy(mq_tc_kernel<64, kMqStages, false, false>, Mq<64, kMqStages>::kThreads,
                                 Mq<64, kMqStages>::smem_bytes(kMaxBatchPerLaunch));
     }
     return slot * device_sm_count();
@@ -926,6 +1001,7 @@ cudaError_t launch_check_queries(const int32_t* lens, const int32_t* qstart, int
 }
 
 cudaError_t launch_multiquery(const MqArgs& a, cudaStream_t s) {
+    if (a.q8 && a.wide) return run_mq<128, true, true>(a, a.num_ctas, s);
     if (a.q8) return run_mq<128, true>(a, a.num_ctas, s);
     return a.head_dim == 128 ? run_mq<128, false>(a, a.num_ctas, s) : run_mq<64, false>(a, a.num_ctas, s);
 }
