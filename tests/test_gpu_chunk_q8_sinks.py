@@ -3,7 +3,8 @@ its value is nothing: the row is what the tail of small weights adds up to.
 
 Tolerance per element: that of tests/test_gpu_chunk_q8.py but for the smallest weights.
 There f16's smallest step counts as 2^-25 of the row's largest weight. The tile kernel
-holds the largest weight at 2^7 or more, so that n tokens lose at most n 2^-32 max|V|.
+holds a weight that stands out this far at 2^9, the largest where none does at 2^0 or
+more: here n tokens lose at most n 2^-34 max|V| (n 2^-32 is allowed).
 Where the cache is split, the weight times the V scale is what is rounded, rows of zero
 codes aside, and the largest of these is 2^8 or more: n tokens lose at most
 2^-33 n max_p w_p vs_p times a code of at most 2^7, which is less than
@@ -57,6 +58,14 @@ def reference(c, few):
     tol = 2.0 ** -8 * np.abs(ref) + size * (3 * 2.0 ** -11 + 2 * b + 2.0 ** -20 + n * 2.0 ** -23)
     tol += 2.0 ** -11 * attend(np.broadcast_to(vs[..., None], vd.shape))
     return ref, tol if few else tol + n * 2.0 ** -32 * np.abs(vd).max()
+
+
+@pytest.mark.parametrize("nats", [10.0, 17.0, 18.0])
+@pytest.mark.parametrize("n,nq,d,where", [(1200, 40, 64, 0), (1200, 40, 128, 0), (1200, 40, 128, 700), (8000, 200, 128, 3)])
+def test_sink_of_zero_value(pkv, n, nq, d, where, nats):  # noqa: F811
+    c = sink_case(31, [n], [nq], 1, d, nats, where)
+    T.check(T.call(pkv, c), c, reference(c, False))
+    assert pkv.pkv_device_status(clear=True) == 0
 
 
 @pytest.mark.parametrize("nats", [10.0, 17.0, 18.0, 30.0])
