@@ -90,7 +90,7 @@ PKV_HD inline int chunk_steps(const ChunkSeq& q, int group, int t) {
 }
 
 PKV_HD inline int64_t chunk_cost_base(const ChunkSeq& q, int group) {
-    return (static_cast<int64_t>(q.n - q.nq + kOverTokens) * group + kChunkRows + 63) / 64;
+    return ((static_cast<int64_t>(q.n) - q.nq + kOverTokens) * group + kChunkRows + 63) / 64;  // (n + kOverTokens may pass 2^31)
 }
 // Cost of the tiles before t (t < tiles), of tile t, and of all tiles of a head.
 PKV_HD inline int64_t chunk_cost_before(int64_t base, int64_t t) { return t * base + 2 * t * (t - 1); }
