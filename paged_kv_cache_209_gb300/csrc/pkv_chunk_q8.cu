@@ -132,6 +132,7 @@ struct Cx {
     static constexpr int kOffWalk = kOffJobs + kJobs * 48;
     static constexpr int kOffPlan = kOffWalk + (sizeof(ChunkWalk) + 15) / 16 * 16;
     static constexpr int kOffMisc = kOffPlan + 2 * (kMaxRounds + 1) * 16;
+    static constexpr int kOffLaidOut = kOffMisc + kThreads / 32 * 8 + 4;  // the last step laid out (any of the scale warps')
     static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
     // scratch of the planning, over the operands: the rounds' cuts, then the costs before the sequences
     static constexpr int kOffPrefix = (kMaxRounds * kMaxPieces + 1) * 8;
@@ -315,12 +316,13 @@ __device__ __forceinline__ void careful_scores(uint32_t taddr, const float* c, f
 // Waits until the phase of this parity has completed, for kProbes probes at most; false:
 // it has not, and the role gives up, as does, in as much time, every role that depends
 // on it. A failing probe holds the thread for 1.4 us where nothing happens (6 s together)
-// and for 150 cycles or so where barriers of the CTA are arrived at, as in the longest
-// wait there is: half B's for the next segment, while A takes one of up to 110000 steps
-// (2^31 tokens on 152 CTAs; 0.2 s, a third of what the probes last). One probe in a loop
-// is all there is: the kernel's two dozen waits share the instruction cache with its
-// loops, and a role reports at its end (a clock and the report in each wait: 487 us
-// instead of 481 for 8 sequences by 512 new tokens).
+// and for 150 cycles or so where barriers of the CTA are arrived at (0.3 s together). That
+// is thousands of steps, and every wait but one lasts a few steps at most; the one is half
+// B's for the next segment while half A alone takes one of any length (next_job, which
+// renews it as long as steps are laid out). One probe in a loop is all there is: the
+// kernel's two dozen waits share the instruction cache with its loops, and a role reports
+// at its end (a clock and the report in each wait: 487 us instead of 481 for 8 sequences by
+// 512 new tokens).
 constexpr int kProbes = 1 << 22;
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
@@ -371,13 +373,25 @@ static_assert(sizeof(Job) == 48, "layout");
 
 // The next segment of a warp's sequence of them (`count`: how many it has taken).
 // All lanes of the warp, or kLanes = 1: one thread. False at the end (job.s1 == 0) and
-// where the wait ran out (job.s1 < 0).
-template <int D, int kLanes>
+// where the wait ran out (job.s1 < 0): with kWhileSteps, where no step was laid out for the
+// CTA while it lasted (the scale warps stay a few steps ahead of the products).
+template <int D, int kLanes, bool kWhileSteps = false>
 __device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int& count, Job& job) {
     using C = Cx<D>;
     const int slot = count % C::kJobs;
     const uint32_t parity = static_cast<uint32_t>(count / C::kJobs) & 1u;
-    if (!(kLanes == 32 ? warp_wait(&job_full[slot], parity) : wait(&job_full[slot], parity))) {
+    if (kWhileSteps) {
+        const volatile int* laid_out = reinterpret_cast<const volatile int*>(smem + C::kOffLaidOut);
+        int before = -1;
+        while (!warp_wait(&job_full[slot], parity)) {
+            const int now = __shfl_sync(0xffffffffu, *laid_out, 0);
+            if (now == before) {
+                job.s1 = -1;
+                return false;
+            }
+            before = now;
+        }
+    } else if (!(kLanes == 32 ? warp_wait(&job_full[slot], parity) : wait(&job_full[slot], parity))) {
         job.s1 = -1;
         return false;
     }
@@ -515,6 +529,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
             if (lane == 0) {
                 *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), __uint_as_float(slow ? 1u : 0u), 0.f);
                 *reinterpret_cast<int*>(record + 1344) = 1;
+                *reinterpret_cast<volatile int*>(smem + C::kOffLaidOut) = at;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
@@ -700,6 +715,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x;
     if (threadIdx.x == 0) {
+        *reinterpret_cast<volatile int*>(smem + C::kOffLaidOut) = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&k_full[s], 4);
             mbar_init(&k_empty[s], 2);  // both score issuers
@@ -768,7 +784,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         int jobs = 0, flags = 0;
         bool ok = true;
         Job job;
-        while (next_job<D, 32>(smem, job_full, job_empty, jobs, job)) {
+        while (next_job<D, 32, true>(smem, job_full, job_empty, jobs, job)) {
             const int rows = job.rows - 128 * x;  // rows of the half, if positive
             const int steps = job.s1 - job.s0;
             if (rows <= 0) {
