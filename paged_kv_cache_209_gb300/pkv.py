@@ -6,6 +6,9 @@ passed through, and a non-OK status raises ``PkvError``. Every step of the
 decode path runs in the library's CUDA kernels. There is no fallback: if
 ``libpkv.so`` is missing or a tensor is not on a CUDA device, the call
 raises.
+
+With ``stream=`` (a torch stream or a raw handle) a call runs there: its inputs
+have to be ready on that stream, and outputs that it allocates are.
 """
 
 from __future__ import annotations
@@ -171,6 +174,22 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(stream, make, *args, **kw) -> torch.Tensor:
+    """A tensor that a call makes itself, an output or a workspace: it is allocated, and filled, on
+    the stream the call runs on. (On the current one, nothing would order its fill, or what used its
+    memory before, with the call's kernels.) It also stays until what the current stream does with
+    it is over."""
+    if stream is None:
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.float32:
         return PKV_F32
@@ -252,10 +271,10 @@ def pkv_decode_attention(q, k_cache, v_cache, block_tables, context_lens, scale:
         raise ValueError("block_tables is [batch][max_blocks], context_lens [batch]")
     max_blocks = int(block_tables.shape[1])
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     need = pkv_decode_workspace_size(batch, q_heads, max_blocks, k_cache, kernel, num_ctas, stages)
     if workspace is None:
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     _check("pkv_decode_attention", lib.pkv_decode_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), batch,
         q_heads, ctypes.c_float(scale), _ptr(out), _ptr(workspace), workspace.numel(), ctypes.byref(desc), flags,
@@ -301,11 +320,11 @@ def pkv_decode_attention_prefixed(q, k_cache, v_cache, block_tables, context_len
     max_blocks = int(block_tables.shape[1])
     num_groups = int(group_blocks.shape[0])
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     need = pkv_decode_prefixed_workspace_size(batch, q_heads, max_blocks, num_groups, max_group_blocks, k_cache,
                                               kernel, num_ctas, stages, prefix_kernel)
     if workspace is None:
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     _check("pkv_decode_attention_prefixed", lib.pkv_decode_attention_prefixed(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), batch,
         q_heads, ctypes.c_float(scale), _ptr(prefix_group), _ptr(group_blocks), num_groups, max_group_blocks,
@@ -346,10 +365,10 @@ def pkv_multiquery_attention(q, k_cache, v_cache, block_tables, context_lens, qu
         raise ValueError("block_tables is [batch][max_blocks], query_start [batch + 1]")
     max_blocks = int(block_tables.shape[1])
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
         need = pkv_multiquery_workspace_size(batch, q_heads, max_blocks, max_query_len, k_cache, num_ctas)
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     _check("pkv_multiquery_attention", lib.pkv_multiquery_attention(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens),
         _ptr(query_start), batch, q_heads, max_query_len, ctypes.c_float(scale), _ptr(out), _ptr(workspace),
@@ -425,10 +444,10 @@ def pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, context_l
         raise ValueError("query_start is int32 [batch + 1]")
     max_blocks = int(block_tables.shape[1])
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
         need = pkv_decode_q8_workspace_size(batch, q_heads, max_blocks, k_codes, max_query_len, num_ctas)
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     _check("pkv_decode_attention_q8", lib.pkv_decode_attention_q8(
         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(scales), _ptr(block_tables), max_blocks,
         _ptr(context_lens), _ptr(query_start), batch, q_heads, max_query_len, ctypes.c_float(scale), _ptr(out),
@@ -503,10 +522,10 @@ def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, conte
     batch, max_blocks = block_tables.shape
     new = out is None
     if new:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
         need = pkv_multiquery_q8_workspace_size(batch, q_heads, max_blocks, max_query_len, k_codes)
-        workspace = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     here = _here()
     args = (_on(here, "q", q), _on(here, "k_codes", k_codes), _on(here, "v_codes", v_codes),
             _on(here, "scales", scales), _on(here, "block_tables", block_tables, torch.int32), max_blocks,
@@ -523,19 +542,20 @@ def pkv_multiquery_attention_q8(q, k_codes, v_codes, scales, block_tables, conte
     return out
 
 
-def _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out, v_out, dtype, like):
+def _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out, v_out, dtype, like,
+                 stream):
     """Arguments of both reading-back calls from the tables on, and the outputs."""
     if block_tables.dim() != 2:
         raise ValueError("block_tables is [batch][max_blocks]")
     batch, max_blocks = block_tables.shape
     want = (num_rows, hkv, d)
     if k_out is None:
-        k_out = torch.empty(want, dtype=dtype, device=like.device)
+        k_out = _made(stream, torch.empty, want, dtype=dtype, device=like.device)
         k_at = k_out.data_ptr()
     else:
         k_at = _on(here, "k_out", k_out, dtype, want)
     if v_out is None:
-        v_out = torch.empty(want, dtype=dtype, device=like.device)
+        v_out = _made(stream, torch.empty, want, dtype=dtype, device=like.device)
         v_at = v_out.data_ptr()
     else:
         v_at = _on(here, "v_out", v_out, dtype, want)
@@ -555,7 +575,7 @@ def pkv_gather(k_cache, v_cache, block_tables, context_lens, row_start, num_rows
     here = _here()
     pools = _on(here, "k_cache", k_cache), _on(here, "v_cache", v_cache)
     args, k_out, v_out = _gather_args(here, desc.num_kv_heads, desc.head_dim, block_tables, context_lens, row_start,
-                                      num_rows, token_start, k_out, v_out, k_cache.dtype, k_cache)
+                                      num_rows, token_start, k_out, v_out, k_cache.dtype, k_cache, stream)
     status = lib.pkv_gather(*pools, *args, desc, flags, _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_gather", status)
@@ -571,7 +591,7 @@ def pkv_gather_q8(k_codes, v_codes, scales, block_tables, context_lens, row_star
     here = _here()
     pools = _on(here, "k_codes", k_codes), _on(here, "v_codes", v_codes), _on(here, "scales", scales)
     args, k_out, v_out = _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out,
-                                      v_out, out_dtype, k_codes)
+                                      v_out, out_dtype, k_codes, stream)
     status = lib.pkv_gather_q8(*pools, *args, code, _desc(nb, bs, hkv, d, PKV_INT8), flags,
                                _raw_stream(stream, here))
     if status:
@@ -616,12 +636,12 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
     tokens = _on(here, "draft_tokens", draft_tokens, i32)
     accept = _on(here, "accept_uniform", accept_uniform, torch.float32, (drafts,))
     if out_tokens is None:
-        out_tokens = torch.empty((batch, max_draft_len + 1), dtype=i32, device=dev)
+        out_tokens = _made(stream, torch.empty, (batch, max_draft_len + 1), dtype=i32, device=dev)
         out_at = out_tokens.data_ptr()
     else:
         out_at = _on(here, "out_tokens", out_tokens, i32, (batch, max_draft_len + 1))
     if num_accepted is None:
-        num_accepted = torch.empty(one, dtype=i32, device=dev)
+        num_accepted = _made(stream, torch.empty, one, dtype=i32, device=dev)
         kept_at = num_accepted.data_ptr()
     else:
         kept_at = _on(here, "num_accepted", num_accepted, i32, one)
@@ -629,7 +649,7 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
     if context_lens is not None:
         lens_at = _on(here, "context_lens", context_lens, i32, one)
         if new_context_lens is None:
-            new_context_lens = torch.empty(one, dtype=i32, device=dev)
+            new_context_lens = _made(stream, torch.empty, one, dtype=i32, device=dev)
             new_at = new_context_lens.data_ptr()
         else:
             new_at = _on(here, "new_context_lens", new_context_lens, i32, one)
@@ -659,7 +679,7 @@ def pkv_decode_attention_noalloc(q, k_cache, v_cache, block_tables, context_lens
     if block_tables.dim() != 2 or block_tables.shape[0] != batch or context_lens.shape != (batch,):
         raise ValueError("block_tables is [batch][max_blocks], context_lens [batch]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     _check("pkv_decode_attention_noalloc", lib.pkv_decode_attention_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), int(block_tables.shape[1]), _ptr(context_lens),
         batch, q_heads, ctypes.c_float(scale), _ptr(out), ctypes.byref(desc), flags, _opts(kernel, num_ctas),
