@@ -742,7 +742,7 @@ size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_heads, int3
                                         int32_t max_query_len, const pkv_cache_desc* desc) {
     if (check_desc_q8(desc, false) != PKV_OK || batch < 0 || !q_heads_ok(num_q_heads, desc)) return 0;
     if (max_query_len < 1 || max_query_len > kMaxQueryLen) return 0;
-    (void)max_blocks_per_seq;
+    if (batch > 0 && !table_width_ok(batch, max_blocks_per_seq)) return 0;
     // The counters of a launch's most sequences lie first, whatever the batch, so that one
     // workspace serves calls of all sizes on either kernel: none writes another's counters.
     size_t co = 0, po = 0;
