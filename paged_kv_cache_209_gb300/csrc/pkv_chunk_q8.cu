@@ -304,14 +304,15 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Sixteen scaled scores, -inf where the token is absent or not seen (columns taddr ..
-// taddr + 15, K factors c, row factor f, the first `seen` of them seen).
+// taddr + 15, K factors c, row factor f, the first `seen` of them seen). The factors are
+// multiplied first: one of them may be as large as the other is small.
 __device__ __forceinline__ void careful_scores(uint32_t taddr, const float* c, float f, int seen, float (&x)[16]) {
     uint32_t v[16];
     tmem_ld16(taddr, v);
     tmem_ld_wait();
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-        x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * c[e] * f;
+        x[e] = e >= seen || __float_as_uint(c[e]) == kAbsent ? ninf() : __uint_as_float(v[e]) * (c[e] * f);
 }
 // Waits until the phase of this parity has completed, for kProbes probes at most; false:
 // it has not, and the role gives up, as does, in as much time, every role that depends
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                 }
                 const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // biased exponent
-                const int shift = ex == 255 || ex == 0 ? 0 : min(126, 141 - ex);       // -113 .. 126
+                const int shift = ex == 255 ? 0 : min(126, 141 - ex);                  // -113 .. 126
                 const float mul = a.scale == 0.f ? 0.f : copysignf(exp2_int(shift), a.scale);
                 row_f = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e * exp2_int(-shift);
 #pragma unroll 2
