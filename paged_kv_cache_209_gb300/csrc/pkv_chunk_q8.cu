@@ -86,6 +86,13 @@ __device__ __forceinline__ float ninf() { return __int_as_float(0xff800000); }
 // that m then moves.
 constexpr float kHeadroom = 9.f;
 constexpr float kMostSum = 65504.f;
+// Where V's codes are bare, m is the maximum of x_p + log2(vs_p) - E, and l, which takes
+// 2^(x_p - m), may leave the float range. So that it does not, that logarithm counts as
+// kLeastLack at least in the maximum (of a V scale 2^-96 of the others' or zero: its
+// values have that much less weight in the f16 range), and |E| is at most kMostLack (l
+// holds 2^-112 and more beside V scales of up to 2^52, whatever the first block's).
+constexpr float kLeastLack = -96.f;
+constexpr int kMostLack = 60;
 
 constexpr int kMaxPieces = 512;  // CTAs of a launch, and pieces of a unit, at most
 
@@ -490,7 +497,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 const uint32_t size = __float_as_uint(job.s0 * kChunkStep + (lane & 15) < job.n ? x : 0.f) & 0x7fffffffu;
                 const bool use = size < 0x7f800000u;
                 ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? size : 0u));
-                ev = range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? size : 0u));
+                ev = max(-kMostLack, min(kMostLack, range_exponent(__reduce_max_sync(0xffffffffu, use && lane >= 16 ? size : 0u))));
             }
             const int slot = at % C::kRecords;
             if (!warp_wait(&empty[slot], (static_cast<uint32_t>(at / C::kRecords) & 1u) ^ 1u)) {
@@ -509,7 +516,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 const __half hi = __float2half(factor), lo = __float2half(factor - __half2float(hi));
                 *reinterpret_cast<uint2*>(record + (32 * g + lane) * 8) = make_uint2(bits(__halves2half2(hi, hi)), bits(__halves2half2(lo, lo)));
                 reinterpret_cast<__half*>(record + 1024)[32 * g + lane] =
-                    __float2half(!present[g] ? 0.f : bare_v[g] ? 1.f : vs[g] * exp2_int(-ev));
+                    __float2half(!present[g] ? 0.f : bare_v[g] ? copysignf(1.f, vs[g]) : vs[g] * exp2_int(-ev));
             }
             slow = __any_sync(0xffffffffu, slow);
 #pragma unroll
@@ -519,12 +526,8 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
             }
             if (slow) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    // (a scale below the normal range counts as its smallest number)
-                    const bool tiny = (__float_as_uint(vs[g]) & 0x7fffffffu) < 0x00800000u;
-                    if (bare_v[g] && present[g])
-                        tab[4 + 128 + 32 * g + lane] = log2f(tiny ? 1.17549435e-38f : vs[g]) - static_cast<float>(ev);
-                }
+                for (int g = 0; g < 4; ++g)  // (-inf for a scale of zero)
+                    if (bare_v[g] && present[g]) tab[4 + 128 + 32 * g + lane] = log2f(fabsf(vs[g])) - static_cast<float>(ev);
             }
             if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * D;
             if (lane == 0) {
@@ -921,7 +924,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                             float xe[16], group = ninf();
                             careful_scores(col + c, cp + c, row_f, seen_part - c, xe);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) group = fmaxf(group, xe[e] == ninf() ? ninf() : xe[e] + cp[128 + c + e]);
+                            for (int e = 0; e < 16; ++e)
+                                group = fmaxf(group, xe[e] == ninf() ? ninf() : xe[e] + fmaxf(cp[128 + c + e], kLeastLack));
                             second = fmaxf(second, fminf(mx, group));
                             mx = fmaxf(mx, group);
                         }
@@ -1031,7 +1035,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 }
                 if (row_ok) {
                     piece[kChunkRows * D + 128 * x + rr] = m;
-                    piece[kChunkRows * (D + 1) + 128 * x + rr] = l;
+                    // (finite, or the joining would take 0 times it where the piece has no weight)
+                    piece[kChunkRows * (D + 1) + 128 * x + rr] = fminf(l, 3e38f);
                 }
             }
             tc_fence_before();  // the next segment's products overwrite O after this half's next arrival
