@@ -123,7 +123,7 @@ struct Cx {
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
     static constexpr int kOffCodes = kOffV + kParts * kVPartBytes;  // the next step's codes: [8 warps][kVecs][32 lanes] vectors
     static constexpr int kOffTable = kOffCodes + 8 * kVecs * 512;
-    // a step's table: 2^E, 2^F, whether it is a slow step; the tokens' K factors [128] and,
+    // a step's table: 2^E, 2^F, whether it is a slow step, its number; the tokens' K factors [128] and,
     // in log2, what their V values lack [128] (for parts done with care)
     static constexpr int kTableBytes = 16 + 2 * 128 * 4;
     // a step's record: per token (hi, hi, lo, lo) of K's factor in f16 [128], V's factor in
@@ -139,7 +139,6 @@ struct Cx {
     static constexpr int kOffWalk = kOffJobs + kJobs * 48;
     static constexpr int kOffPlan = kOffWalk + (sizeof(ChunkWalk) + 15) / 16 * 16;
     static constexpr int kOffMisc = kOffPlan + 2 * (kMaxRounds + 1) * 16;
-    static constexpr int kOffLaidOut = kOffMisc + kThreads / 32 * 8 + 4;  // the last step laid out (any of the scale warps')
     static constexpr size_t kSmem = 1024 + kOffMisc + kThreads / 32 * 8 + 16;
     // scratch of the planning, over the operands: the rounds' cuts, then the costs before the sequences
     static constexpr int kOffPrefix = (kMaxRounds * kMaxPieces + 1) * 8;
@@ -389,11 +388,14 @@ __device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint
     const int slot = count % C::kJobs;
     const uint32_t parity = static_cast<uint32_t>(count / C::kJobs) & 1u;
     if (kWhileSteps) {
-        const volatile int* laid_out = reinterpret_cast<const volatile int*>(smem + C::kOffLaidOut);
-        int before = -1;
-        while (!warp_wait(&job_full[slot], parity)) {
-            const int now = __shfl_sync(0xffffffffu, *laid_out, 0);
-            if (now == before) {
+        uint32_t before = 0;
+        for (bool again = false; !warp_wait(&job_full[slot], parity); again = true) {
+            uint32_t now = 0;  // the steps in the tables add up to more with every one
+#pragma unroll 1
+            for (int t = 0; t < C::kTables; ++t)
+                now += *reinterpret_cast<const volatile uint32_t*>(smem + C::kOffTable + t * C::kTableBytes + 12);
+            now = __shfl_sync(0xffffffffu, now, 0);
+            if (again && now == before) {
                 job.s1 = -1;
                 return false;
             }
@@ -531,9 +533,8 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
             }
             if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * D;
             if (lane == 0) {
-                *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), __uint_as_float(slow ? 1u : 0u), 0.f);
+                *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), __uint_as_float(slow ? 1u : 0u), __int_as_float(at));
                 *reinterpret_cast<int*>(record + 1344) = 1;
-                *reinterpret_cast<volatile int*>(smem + C::kOffLaidOut) = at;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
@@ -719,7 +720,6 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int grid = gridDim.x;
     if (threadIdx.x == 0) {
-        *reinterpret_cast<volatile int*>(smem + C::kOffLaidOut) = 0;
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&k_full[s], 4);
             mbar_init(&k_empty[s], 2);  // both score issuers
