@@ -454,13 +454,18 @@ PKV_API size_t pkv_multiquery_q8_workspace_size(int32_t batch, int32_t num_q_hea
  *   max_query_len host bound on nq, 1 .. 65536 (above: PKV_ERR_UNSUPPORTED).
  *   workspace     >= pkv_multiquery_q8_workspace_size(...) bytes, 256-byte aligned,
  *                 zero-filled before its first use.
- * fp32 accumulation, one rounding to bf16. Scales of any size and spread are taken.
+ * fp32 accumulation, one rounding to bf16. K scales may be of any size and spread, V
+ * scales of any size from 1e-35 on, zero or negative too, as long as those of one
+ * sequence lie within 2^100 of each other (values farther apart may be lost).
  * Up to 16 query rows per (sequence, KV head) at head_dim 128 with tables for many
  * tokens run on pkv_decode_attention_q8's kernel: codes and q (scaled by a power of two
- * per row) enter exactly, a softmax weight times its V scale is rounded to f16 once.
- * All else runs in tiles on f16 tensor cores: q enters exactly in the same way, a K
- * value is rounded to f16 once (an eighth of a quantization step at most), a V value
- * twice (scale, value), a softmax weight once.
+ * per row) enter exactly, a softmax weight times its V scale is rounded to f16 once (11
+ * bits down to 2^-22 of the row's largest such product over rows that are not all zero,
+ * fewer to 2^-33). All else runs in tiles on f16 tensor cores: q enters exactly in the
+ * same way, a K value is rounded to f16 once (an eighth of a quantization step at most),
+ * a V value twice (scale, value), a softmax weight once (11 bits down to 2^-14 of the
+ * row's largest, fewer to 2^-25; behind one token that stands out, an attention sink,
+ * 2^-23 and 2^-34 of its weight).
  * Errors, checked mode and the device status bits as pkv_multiquery_attention.
  */
 PKV_API pkv_status pkv_multiquery_attention_q8(const void* q, const void* k_codes, const void* v_codes,

@@ -1,6 +1,7 @@
 // Causal attention of a chunk of new tokens over the int8 pools
-// (pkv_multiquery_attention_q8 in include/pkv.h), for more than 32 query rows
-// per (sequence, KV head) or head_dim 64.
+// (pkv_multiquery_attention_q8 in include/pkv.h): all its calls but those of up to 16
+// query rows per (sequence, KV head) of 128 on tables for many tokens, which run on the
+// kernel that splits the cache (split_kernel_takes in pkv_api.cu).
 //
 // Mathematics, per query row and step of 128 tokens:
 //     s_p = q' . k_p                    f16 x f16 -> fp32; q' is q times a power of two
@@ -12,7 +13,7 @@
 //     l  += w_p;   O += w_p v_p         w rounded to f16; v_p = vc_p (vs_p 2^-E)
 //                                       rounded to f16; fp32 sums
 // (m is the second largest of the maxima of a part's four groups of 16 tokens, but at most
-// 9 below the largest. Behind an attention sink m lies 9 below it, so that f16 holds the
+// 9 below the largest. Behind one attention sink m lies 9 below it, so that f16 holds the
 // weights of the tail: 11 bits down to 2^-23 of the sink's, some to 2^-34. Where no
 // token stands out m is about the maximum, and a later token may outweigh it by 2^14 or
 // so before m has to move, which costs about a step. With 7 below it everywhere, chunks of
@@ -55,9 +56,14 @@
 // instruction costs a warp 7 cycles, the price of sharing a scheduler and the
 // instruction cache. So everything that is done once per step or segment sits in warps
 // of its own, and waits and issuing loops are as short as they go. 8 sequences of 8192
-// tokens, 512 of them new, 32 query heads on 8 of 128: 419 us, 1271 TFLOP/s of the
-// visible pairs (the cuBLAS rate is 1956); one of 65536 tokens, 256 new, 64 heads on 8:
-// 415 us, 1322. Slower, for the first: scores as one product of 128 tokens 520 (against
+// tokens, 512 of them new, 32 query heads on 8 of 128: 421 to 426 us in a captured graph,
+// 1250 to 1265 TFLOP/s of the visible pairs (the cuBLAS rate is 1956), and 453 us, 1176,
+// called among other work; one of 65536 tokens, 256 new, 64 heads on 8: 413 to 419 and
+// 461 us, 1310 to 1329 and 1190 TFLOP/s. Chunks of other sizes are also bound by how
+// evenly the work is split (pkv_chunk_schedule.cuh). Tiles of at most 128 rows are not
+// bound by the products: half B idles, and half A's chain takes 1.6 us a step, about as
+// long as a step of both halves. Scores far apart take longer, because m has to move:
+// of standard deviation 3, 439 us for the first, of 6, 1620. Slower, for the first: scores as one product of 128 tokens 520 (against
 // 425: a half's softmax waits for all of it); the halves' softmax in turns 535, half B
 // held back by a part 442 (against 423); eight warps for K instead of four 518 (against
 // 502).
@@ -767,7 +773,8 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
 
     // Registers: launched with 80 a thread, 61440 together, which 256 softmax threads at
     // 120, 256 converters at 64, 128 issuers at 40 and 128 threads for the scales at 72
-    // share: none spills. (A few spilled words in a loop cost up to a tenth.)
+    // share. The kernel for D = 128 spills nothing, that for 64 56 bytes. (A few spilled
+    // words in a loop cost up to a tenth.)
     if (warp < C::kSoftmaxWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         // ------------------------------------------------ softmax: half x, query row 32 (warp % 4) + lane of it

@@ -26,6 +26,17 @@
 // 102, 768 102; 24 new tokens on ragged contexts 45, 37, 39 and 40.)
 // The cost only places cuts; a unit's steps are counted exactly.
 //
+// How even it comes out depends on the sizes. A round's piece is as long as the costliest
+// unit, so that pieces drift against the units and some hold two; where that repeats at one
+// CTA, what it has too much the rest cannot take back. The slowest CTA's steps (and three
+// for each segment) over the even share, 32 query heads on 8, 152 CTAs: 8 sequences of 8192
+// tokens with 512 new ones 1.01, 777 1.27, 1000 1.43, 1024 1.33; 4 of 8192 with 1024 1.20;
+// 8 of 4096 with 512 1.16; whole prompts, one of 1000 tokens 1.48, one of 2048 1.11, 8 of
+// 2048 1.17. (With kOverTokens at 448 the first is 1.18: the sizes at which drift repeats
+// move with it.) It shows: 1266 TFLOP/s of the visible pairs with 512 new ones on 8 of
+// 8192, 998 with 777, 927 with 1000, 1023 with 1024; 1097 with 1024 on 4 of 8192, 1011
+// with 512 on 8 of 4096; 606 for one prompt of 2048, 791 for 8.
+//
 // Plain integer arithmetic, compiled for the host as well, where a test checks
 // it against brute force.
 #pragma once

@@ -21,9 +21,11 @@
 // distributed shared memory, and the one whose slice holds the draw finds the segment
 // and scans its entries again (from L2). One launch, nothing in global memory but
 // the results. What bounds it: a few sequences, the chain of the acceptance test, the
-// row, the totals and the segment (7.3 us for one of 32000 entries); many, the
-// instructions of the paired sums (32 of 131072 float32 entries: 11.5 us, 39 % of the
-// copy rate).
+// row, the totals and the segment (7.3 us for one of 32000 entries); many, the latency of
+// the loads with few warps to hide it: 32 sequences are 256 CTAs of 4 warps, under 7 warps
+// an SM, whose loads are of one element a lane (32 of 131072 float32 entries: 11.5 us,
+// 39 % of the copy rate; issue slots 18 % used, ALU and FMA pipes 10 %, DRAM 18 %, the
+// stalls are long-scoreboard and barrier).
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
