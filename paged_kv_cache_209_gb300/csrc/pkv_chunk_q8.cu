@@ -62,11 +62,11 @@
 // 461 us, 1310 to 1329 and 1190 TFLOP/s. Chunks of other sizes are also bound by how
 // evenly the work is split (pkv_chunk_schedule.cuh). Tiles of at most 128 rows are not
 // bound by the products: half B idles, and half A's chain takes 1.6 us a step, about as
-// long as a step of both halves. Scores far apart take longer, because m has to move:
-// of standard deviation 3, 439 us for the first, of 6, 1620. Slower, for the first: scores as one product of 128 tokens 520 (against
-// 425: a half's softmax waits for all of it); the halves' softmax in turns 535, half B
-// held back by a part 442 (against 423); eight warps for K instead of four 518 (against
-// 502).
+// long as a step of both halves. Scores far apart take longer, because m has to move: of
+// standard deviation 3, 439 us for the first, of 6, 1620. Slower, for the first: scores as
+// one product of 128 tokens 520 (against 425: a half's softmax waits for all of it); the
+// halves' softmax in turns 535, half B held back by a part 442 (against 423); eight warps
+// for K instead of four 518 (against 502).
 // Small calls are bound by the chain before the first product: 2.5 us to plan, 4 for
 // the table, the scales and the codes, one after another; 14 us for 40 new tokens on
 // 200.

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                     // vote and branch per block cost 1.6 % of the call.
                     float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
                     if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || fmaxf(vA, vB) > kVScaleF16Safe)) {
-    #pragma unroll
+#pragma unroll
                         for (int off = 4; off < 32; off <<= 1) {
                             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                         m1 = mn1;
                         // and the block's V-scale shift, folded into the same pass over O
                         float vm = fmaxf(vA, vB);
-    #pragma unroll
+#pragma unroll
                         for (int off = 1; off < 32; off <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
                         if (vm > kVScaleF16Safe && vm <= 3.0e38f) {
                             const int k2 = pow2_shift_to_fit(vm);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                             al0 *= down;
                             al1 *= down;
                         }
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             o[i][0] *= al0;
                             o[i][1] *= al1;
