@@ -81,8 +81,9 @@ typedef enum {
 } pkv_status;
 
 /* PKV_INT8: the low-bit pools of pkv_append_q8 / pkv_decode_attention_q8
- * (int8 codes plus one float32 scale per token row of a KV head). */
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_INT8 = 2 } pkv_dtype;
+ * (int8 codes plus one float32 scale per token row of a KV head). PKV_INT4: the
+ * 4-bit cache of pkv_append_q4, one pool of records (layout there). */
+typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_INT8 = 2, PKV_INT4 = 3 } pkv_dtype;
 
 /* Geometry of one layer's K and V pools. */
 typedef struct {
@@ -570,6 +571,217 @@ PKV_API pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_st
                                      int32_t max_draft_len, const int32_t* context_lens,
                                      int32_t* new_context_lens, int32_t* out_tokens, int32_t* num_accepted,
                                      uint32_t flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit cache. (Notebook section 8 on fewer bits per coordinate; project
+ * demo `fake_quantize_rows`.) One pool holds K, V and scales:
+ *     cache[num_blocks][num_kv_heads][PKV_Q4_RECORD_BYTES(head_dim)]
+ * in bytes, 16-byte aligned (128 recommended), desc->dtype = PKV_INT4. A record, the
+ * 16 tokens of one block and KV head, holds 8 head_dim bytes of K codes, as many of V
+ * codes, then 16 K scales and 16 V scales in float32. A row (head_dim coordinates of
+ * one token of one KV head) is quantized symmetrically: scale = max|x| times
+ * float32(1/7), rounded to float32 (0 for a zero row), code = clip(rint(x / scale), -7, 7), the
+ * exact quotient rounded half to even; it stands for the values code * scale. A code
+ * is the nibble code + 8 (0 .. 15; code -8 is valid where a record comes from
+ * elsewhere):
+ *     K, token t: word w of its head_dim / 8 words (32 bits, at byte t head_dim / 2 + 4 w)
+ *         holds dimension 8 w + 2 (p % 4) + p / 4 in nibble p (bits 4 p .. 4 p + 3);
+ *     V: word (o, q, j), o < head_dim / 8, q < 4, j < 4, at byte 8 head_dim + 64 o + 16 q +
+ *         4 j, holds dimension 8 o + 2 j + p % 2 of token 2 q + p / 4 + 8 (p / 2 % 2) in
+ *         nibble p.
+ * head_dim 64 or 128. A slot that no token was written to may hold anything.
+ * ---------------------------------------------------------------------- */
+#define PKV_Q4_RECORD_BYTES(head_dim) (16 * (head_dim) + 128)
+
+/*
+ * pkv_append_q4 -- quantizing slot-mapped append of bf16 k, v
+ * ([num_tokens][num_kv_heads][head_dim]) into the 4-bit cache. Arguments, checks and
+ * errors as pkv_append.
+ */
+PKV_API pkv_status pkv_append_q4(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
+                                 void* cache, const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/* pkv_copy_blocks_q4 -- pkv_copy_blocks for the 4-bit cache. */
+PKV_API pkv_status pkv_copy_blocks_q4(const int64_t* src_dst_pairs, int64_t num_pairs, void* cache,
+                                      const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/*
+ * pkv_gather_q4 -- pkv_gather_q8 for the 4-bit cache: code * scale rounded once to
+ * float32 (out_dtype PKV_F32), and from there to bf16 (PKV_BF16).
+ */
+PKV_API pkv_status pkv_gather_q4(const void* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                 const int32_t* context_lens, const int32_t* token_start, const int32_t* row_start,
+                                 int32_t batch, int64_t num_rows, void* k_out, void* v_out, int32_t out_dtype,
+                                 const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/*
+ * pkv_multiquery_q4_workspace_size -- bytes of workspace that
+ * pkv_multiquery_attention_q4, and pkv_decode_attention_q4 (max_query_len 1), need.
+ * Zero-fill it once before its first use (completed calls leave its counters at zero);
+ * one workspace per call in flight, shared with no other calls; zero it again after
+ * PKV_DEVERR_TIMEOUT. A workspace of the size for the largest call serves all smaller
+ * ones over caches of the same num_kv_heads and head_dim, in any order. Returns 0 for
+ * sizes the calls reject.
+ */
+PKV_API size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                                int32_t max_query_len, const pkv_cache_desc* desc);
+
+/*
+ * pkv_decode_attention_q4 -- pkv_decode_attention over the values the 4-bit cache's
+ * rows stand for: q and out are bf16 [batch][num_q_heads][head_dim], a sequence without
+ * tokens gives a zero row (rejected by PKV_FLAG_CHECKED). At most 32 query heads per KV
+ * head (else PKV_ERR_UNSUPPORTED). Precision and scales as
+ * pkv_multiquery_attention_q4; errors as pkv_decode_attention.
+ */
+PKV_API pkv_status pkv_decode_attention_q4(const void* q, const void* cache, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                           int32_t num_q_heads, float scale, void* out, void* workspace,
+                                           size_t workspace_bytes, const pkv_cache_desc* desc, uint32_t flags,
+                                           void* stream);
+
+/*
+ * pkv_multiquery_attention_q4 -- pkv_multiquery_attention_q8's result over the values
+ * the 4-bit cache's rows stand for: causal attention of each sequence's last
+ * query_start[i+1] - query_start[i] tokens, up to 65536 of them. Arguments, limits,
+ * errors, checked mode and the device status bits as pkv_multiquery_attention_q8.
+ */
+PKV_API pkv_status pkv_multiquery_attention_q4(const void* q, const void* cache, const int32_t* block_tables,
+                                               int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                               const int32_t* query_start, int32_t batch, int32_t num_q_heads,
+                                               int32_t max_query_len, float scale, void* out, void* workspace,
+                                               size_t workspace_bytes, const pkv_cache_desc* desc, uint32_t flags,
+                                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions. (Notebook section 0 takes K as it is cached, with its position
+ * in it; these calls put it there.)
+ * ---------------------------------------------------------------------- */
+
+/* How frequencies are stretched for contexts longer than a model was trained on. */
+typedef enum {
+    PKV_ROTARY_PLAIN = 0,  /* f_i = base^(-2 i / R)                                    */
+    PKV_ROTARY_LINEAR = 1, /* f_i / stretch                                           */
+    PKV_ROTARY_BASE = 2,   /* base grown by stretch^(R / (R - 2)), R > 2               */
+    PKV_ROTARY_TURNS = 3,  /* by the turns n_i = original_context f_i / (2 pi): f_i where
+                              n_i >= high_turns, f_i / stretch where n_i <= low_turns,
+                              between them the mix linear in n_i                       */
+    PKV_ROTARY_RAMP = 4    /* the mix linear in i between the dimensions that make
+                              high_turns (rounded down) and low_turns (rounded up)     */
+} pkv_rotary_kind;
+
+typedef struct {
+    int32_t kind;            /* pkv_rotary_kind                                        */
+    double stretch;          /* >= 1                                                   */
+    double original_context; /* TURNS and RAMP: tokens, > 0                            */
+    double low_turns;        /* TURNS and RAMP: 0 < low_turns < high_turns             */
+    double high_turns;
+} pkv_rotary_scaling;
+
+/*
+ * pkv_rotary_frequencies -- angles per position of R = rotary_dim dimensions, R / 2
+ * numbers, into host memory. base > 1; R even, 2 .. 8192; scaling NULL: PKV_ROTARY_PLAIN.
+ */
+PKV_API pkv_status pkv_rotary_frequencies(int32_t rotary_dim, double base, const pkv_rotary_scaling* scaling,
+                                          double* frequencies);
+
+/*
+ * pkv_rotary_table -- cosines and sines of positions first_position ..
+ * first_position + num_positions - 1: row p of `table` holds factor * cos(p f_i), i < R /
+ * 2, then factor * sin(p f_i), within 2^-22 |factor| of the exact values (of the angle
+ * with f_i / (2 pi) rounded to float64).
+ *
+ *   frequencies   device, double [rotary_dim / 2], finite.
+ *   table         device, float [num_positions][rotary_dim], 16-byte aligned.
+ *   rotary_dim    even, 2 .. 8192; first_position >= 0 and num_positions >= 0, their sum
+ *                 at most 2^31 - 1; factor finite.
+ */
+PKV_API pkv_status pkv_rotary_table(const double* frequencies, int32_t rotary_dim, int64_t first_position,
+                                    int64_t num_positions, float factor, float* table, void* stream);
+
+/*
+ * pkv_append_rotary -- rotary positions on a step's q and k, and their append: the
+ * first R = rotary_dim dimensions of every head of q and k turn by their token's
+ * position,
+ *     y_a = x_a c_i - x_b s_i,   y_b = x_b c_i + x_a s_i,   i < R / 2,
+ * (a, b) = (i, i + R / 2), or (2 i, 2 i + 1) with `interleaved`, c_i and s_i in row
+ * `position` of the table; the other dimensions stay. q's rows go to q_out, k's turned
+ * rows and v's rows into slot slot_mapping[t] of the cache as pkv_append (PKV_F32,
+ * PKV_BF16), pkv_append_q8 (PKV_INT8) and pkv_append_q4 (PKV_INT4) put them there. Each y
+ * is computed in float64 (the products are exact), rounded to float32 and from there to
+ * bf16, whatever the order of work, and a quantizing cache takes the row so rounded: its
+ * codes are a function of the inputs. Float32 rows (PKV_F32): off by at most 2^-23 (|x_a c_i| +
+ * |x_b s_i|).
+ *
+ *   q, k, v       device, rows of num_q_heads (num_kv_heads) heads of head_dim elements,
+ *                 q_stride (k_stride, v_stride) elements from a token to the next: parts of
+ *                 one product's output as they are. float32 for PKV_F32, else bf16; 16-byte
+ *                 aligned, and so are the strides.
+ *   num_q_heads   0: k and v only (q and q_out unused). At most PKV_MAX_Q_HEADS.
+ *   q_out         rows q_out_stride apart; may be q itself with the same stride, else it
+ *                 overlaps none of the inputs.
+ *   positions     device, int32 [num_tokens].
+ *   table         device, float [num_positions][rotary_dim] (pkv_rotary_table from position
+ *                 0), 16-byte aligned.
+ *   rotary_dim    even, 2 .. head_dim.
+ *   slot_mapping  device, int64 [num_tokens]; a negative slot skips k and v.
+ *   k_cache, v_cache, scales  the pools. PKV_INT4: the cache as k_cache, v_cache NULL.
+ *                 scales: PKV_INT8 only, else NULL.
+ * A position outside the table leaves its token's rows unwritten and sets
+ * PKV_DEVERR_RANGE, as does a slot beyond the pool for k and v; a negative position with
+ * a negative slot is padding (nothing is written, no error). With PKV_FLAG_CHECKED these
+ * return PKV_ERR_RANGE. Other errors as pkv_append.
+ */
+PKV_API pkv_status pkv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                     int64_t v_stride, const int32_t* positions, const float* table,
+                                     int32_t num_positions, int32_t rotary_dim, int32_t interleaved,
+                                     const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                                     void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, float* scales,
+                                     const pkv_cache_desc* desc, uint32_t flags, void* stream);
+
+/*
+ * pkv_plan_step -- where a step's new tokens go, from the sequences' lengths, on the
+ * device: a step after pkv_verify_drafts needs no host.
+ * (notebook section 5 `append`: blocks are added when a sequence crosses a block
+ * boundary, counted before any is taken; freed blocks are reused most recently freed
+ * first.)
+ *
+ * Sequence i holds n = context_lens[i] tokens in held_blocks[i] blocks (the first
+ * entries of its table; more than the tokens need is fine, as after rejected drafts) and
+ * gets m = new_tokens[i] more. free_blocks[0 .. *free_count - 1] is a stack of free
+ * blocks, its top last. In sequence order each takes max(0, ceil((n + m) / 16) -
+ * held_blocks[i]) blocks off the top, into its table. With r rows before it, its token
+ * n + t gets row r + t:
+ *     slot_mapping[r + t] = block * 16 + (n + t) % 16,   positions[r + t] = n + t
+ * and query_start[i] = r, new_context_lens[i] = n + m, new_held_blocks[i]. Rows past the
+ * last one get slot -1 and position -1 (pkv_append and pkv_append_rotary skip them).
+ * result[0] = rows planned, result[1] = blocks missing. If blocks are missing, or there are
+ * more than num_rows rows (which sets PKV_DEVERR_RANGE), the step is not planned at all:
+ * no table entry is written, lengths and counts stay, no sequence has rows.
+ *
+ *   context_lens, new_tokens, held_blocks  device, int32 [batch]. A sequence with a number
+ *                 below zero, fewer blocks than its tokens need, or more tokens or blocks
+ *                 than its table holds gets no rows and sets PKV_DEVERR_RANGE.
+ *   free_blocks   device, int32 [free_capacity]; free_count device, int32, 0 ..
+ *                 free_capacity (else PKV_DEVERR_RANGE, and nothing is planned).
+ *   block_tables  device, int32 [batch][max_blocks_per_seq]; entries from held_blocks[i]
+ *                 on are written. No other output may overlap an input or another output
+ *                 (PKV_ERR_OVERLAP): lengths, counts and the stack's count take turns in
+ *                 two buffers.
+ *   num_rows      rows slot_mapping (int64) and positions (int32) hold, below 2^31.
+ *   num_blocks    of the cache, or 0: not known. A block id outside it is not handed on
+ *                 (slot -1, table entry -1) and sets PKV_DEVERR_RANGE.
+ *   query_start   device, int32 [batch + 1]; new_free_count int32; result int32 [2].
+ * batch 0 .. PKV_MAX_PLAN_BATCH (more: PKV_ERR_UNSUPPORTED); 0 plans no rows. One launch,
+ * no workspace. With PKV_FLAG_CHECKED a sequence, count or number of rows as above returns
+ * PKV_ERR_RANGE and missing blocks PKV_ERR_OUT_OF_BLOCKS, having written nothing.
+ */
+#define PKV_MAX_PLAN_BATCH 16384
+PKV_API pkv_status pkv_plan_step(const int32_t* context_lens, const int32_t* new_tokens, const int32_t* held_blocks,
+                                 const int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count,
+                                 int32_t* block_tables, int32_t max_blocks_per_seq, int32_t batch, int64_t num_rows,
+                                 int64_t num_blocks, int64_t* slot_mapping, int32_t* positions, int32_t* query_start,
+                                 int32_t* new_context_lens, int32_t* new_held_blocks, int32_t* new_free_count,
+                                 int32_t* result, uint32_t flags, void* stream);
 
 /*
  * pkv_decode_attention_noalloc -- pkv_decode_attention without a

@@ -88,7 +88,24 @@ pkv_status run_checked(F launch, cudaStream_t s) {
     if (cudaStreamSynchronize(s) != cudaSuccess) return PKV_ERR_CUDA;
     if (host & kVerdictRange) return PKV_ERR_RANGE;
     if (host & kVerdictOverlap) return PKV_ERR_OVERLAP;
+    if (host & kVerdictBlocks) return PKV_ERR_OUT_OF_BLOCKS;
     return PKV_OK;
+}
+
+pkv_status check_desc_q4(const pkv_cache_desc* d) {
+    if (d == nullptr) return PKV_ERR_NULL;
+    if (d->block_size != 16 || d->num_blocks < 1 || d->num_kv_heads < 1) return PKV_ERR_SHAPE;
+    if (d->head_dim != 64 && d->head_dim != 128) return PKV_ERR_SHAPE;
+    if (d->dtype != PKV_INT4) return PKV_ERR_DTYPE;
+    // block ids are 32-bit; records are addressed in 64 bits
+    if (d->num_blocks >= (int64_t(1) << 31) || d->num_blocks * d->num_kv_heads >= (int64_t(1) << 31)) return PKV_ERR_SHAPE;
+    return PKV_OK;
+}
+
+// Whether n bytes at p and m bytes at q share one.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return n > 0 && m > 0 && a < b + m && b < a + n;
 }
 
 pkv_status check_desc_q8(const pkv_cache_desc* d, bool attention) {
@@ -905,6 +922,305 @@ pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_stride, in
         if (st != PKV_OK) return st;
     }
     return launch_verify(a, dtype, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_append_q4(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens, void* cache,
+                         const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_append_q4");
+    pkv_status st = check_desc_q4(desc);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_tokens * 2 * desc->num_kv_heads >= (int64_t(1) << 31)) return PKV_ERR_SHAPE;
+    if (cache == nullptr) return PKV_ERR_NULL;
+    if (!aligned16(cache)) return PKV_ERR_ALIGN;
+    if (num_tokens == 0) return PKV_OK;
+    if (k == nullptr || v == nullptr || slot_mapping == nullptr) return PKV_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u)) return PKV_ERR_ALIGN;
+    if ((flags & PKV_FLAG_CHECKED) && num_tokens > 16384) return PKV_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RotaryAppendArgs a{};
+    a.k = k;
+    a.v = v;
+    a.k_stride = a.v_stride = static_cast<int64_t>(desc->num_kv_heads) * desc->head_dim;
+    a.slots = slot_mapping;
+    a.k_cache = cache;
+    a.status = device_info().status;
+    a.num_tokens = num_tokens;
+    a.num_slots = desc->num_blocks * 16;
+    a.kv_heads = desc->num_kv_heads;
+    if (a.status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        st = run_checked([&](unsigned int* verdict) { return launch_check_slots(slot_mapping, num_tokens, a.num_slots, verdict, s); }, s);
+        if (st != PKV_OK) return st;
+    }
+    return launch_append_rotary(a, *desc, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_copy_blocks_q4(const int64_t* pairs, int64_t num_pairs, void* cache, const pkv_cache_desc* desc,
+                              uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_copy_blocks_q4");
+    pkv_status st = check_desc_q4(desc);
+    if (st != PKV_OK) return st;
+    if (num_pairs < 0) return PKV_ERR_SHAPE;
+    if (cache == nullptr) return PKV_ERR_NULL;
+    if (!aligned16(cache)) return PKV_ERR_ALIGN;
+    if (num_pairs == 0) return PKV_OK;
+    if (pairs == nullptr) return PKV_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(pairs) & 7u) return PKV_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned int* status = device_info().status;
+    if (status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        if (num_pairs > 16384) return PKV_ERR_UNSUPPORTED;
+        st = run_checked([&](unsigned int* verdict) { return launch_check_pairs(pairs, num_pairs, desc->num_blocks, verdict, s); }, s);
+        if (st != PKV_OK) return st;
+    }
+    const int64_t block_vecs = static_cast<int64_t>(desc->num_kv_heads) * (PKV_Q4_RECORD_BYTES(desc->head_dim) / 16);
+    return launch_copy_pool(pairs, num_pairs, cache, desc->num_blocks, block_vecs, status, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_gather_q4(const void* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                         const int32_t* context_lens, const int32_t* token_start, const int32_t* row_start, int32_t batch,
+                         int64_t num_rows, void* k_out, void* v_out, int32_t out_dtype, const pkv_cache_desc* desc,
+                         uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_gather_q4");
+    const pkv_status st = check_desc_q4(desc);
+    if (st != PKV_OK) return st;
+    if (out_dtype != PKV_F32 && out_dtype != PKV_BF16) return PKV_ERR_DTYPE;
+    return run_gather(cache, cache, nullptr, block_tables, max_blocks_per_seq, context_lens, token_start, row_start, batch,
+                      num_rows, k_out, v_out, out_dtype, desc, flags, static_cast<cudaStream_t>(stream));
+}
+
+size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                        int32_t max_query_len, const pkv_cache_desc* desc) {
+    if (check_desc_q4(desc) != PKV_OK || batch < 0 || !q_heads_ok(num_q_heads, desc)) return 0;
+    if (max_query_len < 1 || max_query_len > kMaxQueryLen) return 0;
+    if (batch > 0 && !table_width_ok(batch, max_blocks_per_seq)) return 0;
+    return 256;
+}
+
+// Both attention calls over the 4-bit cache, after the checks of their own.
+static pkv_status run_attention_q4(const void* q, const void* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_start, int32_t batch, int32_t num_q_heads,
+                                   int32_t max_query_len, float scale, void* out, void* workspace, size_t workspace_bytes,
+                                   const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    if (!isfinite(scale)) return PKV_ERR_SHAPE;
+    if (flags & PKV_FLAG_TEST_STALL) return PKV_ERR_UNSUPPORTED;
+    if (batch == 0) return PKV_OK;
+    if (!table_width_ok(batch, max_blocks_per_seq)) return PKV_ERR_SHAPE;
+    if (!q || !cache || !block_tables || !context_lens || !out || !workspace) return PKV_ERR_NULL;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned4(block_tables) || !aligned4(context_lens) ||
+        !aligned4(query_start) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PKV_ERR_ALIGN;
+    if (workspace_bytes < pkv_multiquery_q4_workspace_size(batch, num_q_heads, max_blocks_per_seq, max_query_len, desc))
+        return PKV_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    unsigned int* status = device_info().status;
+    if (status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        const pkv_status st = run_checked([&](unsigned int* verdict) {
+            cudaError_t e = launch_check_decode(block_tables, max_blocks_per_seq, context_lens, batch, desc->num_blocks,
+                                                query_start ? 0 : 1, verdict, s);
+            if (e != cudaSuccess || query_start == nullptr) return e;
+            return launch_check_queries(context_lens, query_start, batch, max_query_len, verdict, s);
+        }, s);
+        if (st != PKV_OK) return st;
+    }
+    const int64_t row = static_cast<int64_t>(num_q_heads) * desc->head_dim * 2;
+    for (int32_t b0 = 0; b0 < batch; b0 += kMaxBatchPerLaunch) {
+        Q4Args a{};
+        // with query offsets the rows are absolute; without, row i of this launch is sequence b0 + i
+        a.q = query_start ? q : static_cast<const char*>(q) + b0 * row;
+        a.out = query_start ? out : static_cast<char*>(out) + b0 * row;
+        a.qstart = query_start ? query_start + b0 : nullptr;
+        a.cache = cache;
+        a.tables = block_tables + static_cast<int64_t>(b0) * max_blocks_per_seq;
+        a.lens = context_lens + b0;
+        a.status = status;
+        a.num_blocks = desc->num_blocks;
+        a.max_blocks = max_blocks_per_seq;
+        a.batch = batch - b0 < kMaxBatchPerLaunch ? batch - b0 : kMaxBatchPerLaunch;
+        a.q_heads = num_q_heads;
+        a.kv_heads = desc->num_kv_heads;
+        a.head_dim = desc->head_dim;
+        a.group = num_q_heads / desc->num_kv_heads;
+        a.max_query_len = max_query_len;
+        a.scale = scale;
+        if (launch_attend_q4(a, s) != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_decode_attention_q4(const void* q, const void* cache, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t batch,
+                                   int32_t num_q_heads, float scale, void* out, void* workspace, size_t workspace_bytes,
+                                   const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_decode_attention_q4");
+    const pkv_status st = check_desc_q4(desc);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || !q_heads_ok(num_q_heads, desc)) return PKV_ERR_SHAPE;
+    if (num_q_heads / desc->num_kv_heads > kMqMaxRows) return PKV_ERR_UNSUPPORTED;
+    return run_attention_q4(q, cache, block_tables, max_blocks_per_seq, context_lens, nullptr, batch, num_q_heads, 1, scale, out,
+                            workspace, workspace_bytes, desc, flags, stream);
+}
+
+pkv_status pkv_multiquery_attention_q4(const void* q, const void* cache, const int32_t* block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* query_start,
+                                       int32_t batch, int32_t num_q_heads, int32_t max_query_len, float scale, void* out,
+                                       void* workspace, size_t workspace_bytes, const pkv_cache_desc* desc, uint32_t flags,
+                                       void* stream) {
+    NvtxRange nvtx_range("pkv_multiquery_attention_q4");
+    const pkv_status st = check_desc_q4(desc);
+    if (st != PKV_OK) return st;
+    if (batch < 0 || !q_heads_ok(num_q_heads, desc) || max_query_len < 1) return PKV_ERR_SHAPE;
+    if (max_query_len > kMaxQueryLen) return PKV_ERR_UNSUPPORTED;
+    if (batch > 0 && query_start == nullptr) return PKV_ERR_NULL;
+    return run_attention_q4(q, cache, block_tables, max_blocks_per_seq, context_lens, query_start, batch, num_q_heads, max_query_len,
+                            scale, out, workspace, workspace_bytes, desc, flags, stream);
+}
+
+pkv_status pkv_rotary_frequencies(int32_t rotary_dim, double base, const pkv_rotary_scaling* scaling, double* frequencies) {
+    if (frequencies == nullptr) return PKV_ERR_NULL;
+    return rotary_frequencies(rotary_dim, base, scaling, frequencies) ? PKV_OK : PKV_ERR_SHAPE;
+}
+
+pkv_status pkv_rotary_table(const double* frequencies, int32_t rotary_dim, int64_t first_position, int64_t num_positions,
+                            float factor, float* table, void* stream) {
+    NvtxRange nvtx_range("pkv_rotary_table");
+    const int64_t most = (int64_t(1) << 31) - 1;
+    if (rotary_dim < 2 || rotary_dim > 8192 || rotary_dim % 2 || !isfinite(factor)) return PKV_ERR_SHAPE;
+    if (first_position < 0 || num_positions < 0 || first_position > most || num_positions > most - first_position) return PKV_ERR_SHAPE;
+    if (num_positions == 0) return PKV_OK;
+    if (!frequencies || !table) return PKV_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(frequencies) & 7u) || !aligned16(table)) return PKV_ERR_ALIGN;
+    return launch_rotary_table(frequencies, rotary_dim / 2, first_position, num_positions, factor, table,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* positions, const float* table, int32_t num_positions, int32_t rotary_dim,
+                             int32_t interleaved, const int64_t* slot_mapping, int64_t num_tokens, int32_t num_q_heads,
+                             void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache, float* scales,
+                             const pkv_cache_desc* desc, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_append_rotary");
+    if (desc == nullptr) return PKV_ERR_NULL;
+    pkv_status st = desc->dtype == PKV_INT4 ? check_desc_q4(desc) : desc->dtype == PKV_INT8 ? check_desc_q8(desc, false) : check_desc(desc);
+    if (st != PKV_OK) return st;
+    if (num_q_heads < 0 || num_q_heads > PKV_MAX_Q_HEADS || rotary_dim < 2 || rotary_dim > desc->head_dim || rotary_dim % 2 ||
+        num_positions < 1 || num_tokens < 0)
+        return PKV_ERR_SHAPE;
+    // rows are counted in 32 bits
+    if (num_tokens >= (int64_t(1) << 31) / (num_q_heads + 2 * static_cast<int64_t>(desc->num_kv_heads))) return PKV_ERR_SHAPE;
+    if (!k_cache || (desc->dtype != PKV_INT4 && !v_cache) || (desc->dtype == PKV_INT8 && !scales)) return PKV_ERR_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(scales)) return PKV_ERR_ALIGN;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !positions || !table || !slot_mapping || (num_q_heads > 0 && (!q || !q_out))) return PKV_ERR_NULL;
+    const int64_t per_vector = desc->dtype == PKV_F32 ? 4 : 8;  // elements of 16 bytes
+    const int64_t q_row = static_cast<int64_t>(num_q_heads) * desc->head_dim, kv_row = static_cast<int64_t>(desc->num_kv_heads) * desc->head_dim;
+    const int64_t strides[4] = {num_q_heads > 0 ? q_stride : q_row, num_q_heads > 0 ? q_out_stride : q_row, k_stride, v_stride};
+    const int64_t rows[4] = {q_row, q_row, kv_row, kv_row};
+    for (int i = 0; i < 4; ++i) {
+        if (num_tokens > 1 && (strides[i] < rows[i] || strides[i] >= (int64_t(1) << 31))) return PKV_ERR_SHAPE;
+        if (num_tokens > 1 && strides[i] % per_vector) return PKV_ERR_ALIGN;
+    }
+    if ((num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out))) || !aligned16(k) || !aligned16(v) || !aligned16(table) ||
+        !aligned4(positions) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+        return PKV_ERR_ALIGN;
+    if ((flags & PKV_FLAG_CHECKED) && num_tokens > 16384) return PKV_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    RotaryAppendArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.positions = positions;
+    a.table = table;
+    a.slots = slot_mapping;
+    a.q_out = q_out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.scales = scales;
+    a.status = device_info().status;
+    a.q_stride = strides[0];
+    a.q_out_stride = strides[1];
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.num_tokens = num_tokens;
+    a.num_slots = desc->num_blocks * 16;
+    a.num_positions = num_positions;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.q_heads = num_q_heads;
+    a.kv_heads = desc->num_kv_heads;
+    if (a.status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        st = run_checked([&](unsigned int* verdict) {
+            const cudaError_t e = launch_check_slots(slot_mapping, num_tokens, a.num_slots, verdict, s);
+            return e != cudaSuccess ? e : launch_check_positions(positions, slot_mapping, num_tokens, num_positions, verdict, s);
+        }, s);
+        if (st != PKV_OK) return st;
+    }
+    return launch_append_rotary(a, *desc, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_plan_step(const int32_t* context_lens, const int32_t* new_tokens, const int32_t* held_blocks,
+                         const int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count, int32_t* block_tables,
+                         int32_t max_blocks_per_seq, int32_t batch, int64_t num_rows, int64_t num_blocks, int64_t* slot_mapping,
+                         int32_t* positions, int32_t* query_start, int32_t* new_context_lens, int32_t* new_held_blocks,
+                         int32_t* new_free_count, int32_t* result, uint32_t flags, void* stream) {
+    NvtxRange nvtx_range("pkv_plan_step");
+    const int64_t bound = int64_t(1) << 31;
+    if (flags & PKV_FLAG_TEST_STALL) return PKV_ERR_UNSUPPORTED;
+    if (batch < 0 || num_rows < 0 || num_rows >= bound || free_capacity < 0 || free_capacity >= bound || num_blocks < 0) return PKV_ERR_SHAPE;
+    if (batch > PKV_MAX_PLAN_BATCH) return PKV_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq < 1 || static_cast<int64_t>(max_blocks_per_seq) * 16 >= bound) return PKV_ERR_SHAPE;
+    if (!free_count || !query_start || !new_free_count || !result) return PKV_ERR_NULL;
+    if (batch > 0 && (!context_lens || !new_tokens || !held_blocks || !block_tables || !new_context_lens || !new_held_blocks)) return PKV_ERR_NULL;
+    if (free_capacity > 0 && !free_blocks) return PKV_ERR_NULL;
+    if (num_rows > 0 && (!slot_mapping || !positions)) return PKV_ERR_NULL;
+    const size_t per_seq = 4 * static_cast<size_t>(batch);
+    const struct {
+        const void* p;
+        size_t n;
+    } in[] = {{context_lens, per_seq}, {new_tokens, per_seq}, {held_blocks, per_seq}, {free_blocks, 4 * static_cast<size_t>(free_capacity)}, {free_count, 4}},
+      out[] = {{block_tables, per_seq * max_blocks_per_seq}, {slot_mapping, 8 * static_cast<size_t>(num_rows)}, {positions, 4 * static_cast<size_t>(num_rows)},
+               {query_start, per_seq + 4}, {new_context_lens, per_seq}, {new_held_blocks, per_seq}, {new_free_count, 4}, {result, 8}};
+    for (const auto& x : in)
+        if (!aligned4(x.p)) return PKV_ERR_ALIGN;
+    for (const auto& x : out)
+        if (!aligned4(x.p)) return PKV_ERR_ALIGN;
+    if (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) return PKV_ERR_ALIGN;
+    for (const auto& x : out) {
+        for (const auto& y : in)
+            if (overlap(x.p, x.n, y.p, y.n)) return PKV_ERR_OVERLAP;
+        for (const auto& y : out)
+            if (&x != &y && overlap(x.p, x.n, y.p, y.n)) return PKV_ERR_OVERLAP;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PlanArgs a{};
+    a.lens = context_lens;
+    a.new_tokens = new_tokens;
+    a.held = held_blocks;
+    a.free_blocks = free_blocks;
+    a.free_count = free_count;
+    a.tables = block_tables;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.query_start = query_start;
+    a.new_lens = new_context_lens;
+    a.new_held = new_held_blocks;
+    a.new_free_count = new_free_count;
+    a.result = result;
+    a.status = device_info().status;
+    a.free_capacity = free_capacity;
+    a.num_blocks = num_blocks > 0 && num_blocks < bound ? num_blocks : bound;
+    a.num_rows = num_rows;
+    a.batch = batch;
+    a.max_blocks = max_blocks_per_seq;
+    if (a.status == nullptr) return PKV_ERR_CUDA;
+    if (flags & PKV_FLAG_CHECKED) {
+        const pkv_status st = run_checked([&](unsigned int* verdict) { return launch_check_plan(a, verdict, s); }, s);
+        if (st != PKV_OK) return st;
+    }
+    return launch_plan(a, s) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_device_status(uint32_t* bits_out, int clear, void* stream) {

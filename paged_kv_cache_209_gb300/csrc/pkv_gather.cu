@@ -1,5 +1,5 @@
-// Reading tokens back out of the paged cache (pkv_gather, pkv_gather_q8 in
-// include/pkv.h): a token range of each sequence becomes packed rows
+// Reading tokens back out of the paged cache (pkv_gather, pkv_gather_q8 and
+// pkv_gather_q4 in include/pkv.h): a token range of each sequence becomes packed rows
 // [row][KV head][head_dim] of K and of V. Pure data movement, bound by HBM: per
 // row 2 Hkv D elements written and as many read (2 Hkv (D + 4) bytes for int8).
 //
@@ -18,6 +18,7 @@
 // the measured copy rate; 64 ragged bf16 sequences 126 us, 97 %; 300 tokens 5 us.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_q4.cuh"
 
 namespace pkv {
 namespace {
@@ -205,6 +206,70 @@ __global__ void __launch_bounds__(kThreads) gather_q8_kernel(const GatherArgs a)
     }
 }
 
+// Nibble p of a word of 4-bit codes (code + 8), as the code, exactly: 2^23 + nibble has it
+// in its lowest bits.
+__device__ __forceinline__ float nibble_f32(uint32_t w, int p) {
+    return __uint_as_float((w >> (4 * p) & 15u) | 0x4B000000u) - 8388616.f;
+}
+
+// A 4-bit record is 16 lines of 8 words of K and as many of V. A lane takes K words w, w +
+// 32, ... (8 dimensions of one token) and V words (16 bytes at 16 lane: an octet's four
+// tokens of one quad), and writes 8 dimensions of a token at a time.
+template <int D, typename Out>
+__global__ void __launch_bounds__(kThreads) gather_q4_kernel(const GatherArgs a) {
+    __shared__ int prefix[kMaxBatchPerLaunch + 1];
+    grid_dependency_wait();
+    allow_dependents();
+    count_blocks(a, prefix);
+    const int lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(prefix[a.batch]) * a.kv_heads;
+    const int64_t stride = static_cast<int64_t>(a.kv_heads) * D;  // elements from a token's row to the next
+    constexpr int kWords = D / 16;   // K words of a lane
+    constexpr int kVecs = D / 64;    // V vectors of a lane
+    for (int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); x < items;
+         x += static_cast<int64_t>(gridDim.x) * kWarps) {
+        Item it;
+        if (!item_of(a, prefix, x, lane, it)) continue;
+        const uint8_t* rec = static_cast<const uint8_t*>(a.k) + it.chunk * q4_record_bytes(D);
+        const uint32_t* kw = reinterpret_cast<const uint32_t*>(rec);
+        const uint4* vw = reinterpret_cast<const uint4*>(rec + q4_v_offset(D));
+        const float sc = __ldg(reinterpret_cast<const float*>(rec + q4_scales_offset(D)) + lane);  // K's in lanes 0-15, V's in 16-31
+        uint32_t k[kWords];
+        uint4 v[kVecs];
+#pragma unroll
+        for (int r = 0; r < kWords; ++r) k[r] = __ldcs(kw + 32 * r + lane);
+#pragma unroll
+        for (int r = 0; r < kVecs; ++r) v[r] = __ldcs(vw + 32 * r + lane);
+        Out* ko = static_cast<Out*>(a.k_out) + it.row * stride + it.head * D;
+        Out* vo = static_cast<Out*>(a.v_out) + it.row * stride + it.head * D;
+#pragma unroll
+        for (int r = 0; r < kWords; ++r) {
+            const int word = 32 * r + lane, t = word / (D / 8);
+            const float s = __shfl_sync(0xffffffffu, sc, t);
+            if (t < it.lo || t >= it.hi) continue;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = nibble_f32(k[r], e / 2 + 4 * (e & 1)) * s;
+            store8(ko + t * stride + word % (D / 8) * 8, y);
+        }
+#pragma unroll
+        for (int r = 0; r < kVecs; ++r) {
+            const int vec = 32 * r + lane, quad = vec & 3, o = vec >> 2;
+            const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {  // tokens 2 quad, + 1, + 8, + 9
+                const int t = 2 * quad + (u & 1) + 8 * (u >> 1);
+                const float s = __shfl_sync(0xffffffffu, sc, 16 + t);
+                if (t < it.lo || t >= it.hi) continue;
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = nibble_f32(w[e / 2], 4 * (u & 1) + 2 * (u >> 1) + (e & 1)) * s;
+                store8(vo + t * stride + 8 * o, y);
+            }
+        }
+    }
+}
+
 // Rows of kVecs 16-byte vectors, copied as they are: an item's rows are 16 kVecs
 // consecutive vectors of the pool.
 template <int kVecs>
@@ -257,6 +322,12 @@ cudaError_t launch_gather(const GatherArgs& a, const pkv_cache_desc& d, int out_
         return wide ? launch_pdl(gather_kernel<32>, grid, block, 0, s, a) : launch_pdl(gather_kernel<16>, grid, block, 0, s, a);
     if (d.dtype == PKV_BF16)
         return wide ? launch_pdl(gather_kernel<16>, grid, block, 0, s, a) : launch_pdl(gather_kernel<8>, grid, block, 0, s, a);
+    if (d.dtype == PKV_INT4 && out_dtype == PKV_F32)
+        return wide ? launch_pdl(gather_q4_kernel<128, float>, grid, block, 0, s, a)
+                    : launch_pdl(gather_q4_kernel<64, float>, grid, block, 0, s, a);
+    if (d.dtype == PKV_INT4)
+        return wide ? launch_pdl(gather_q4_kernel<128, __nv_bfloat16>, grid, block, 0, s, a)
+                    : launch_pdl(gather_q4_kernel<64, __nv_bfloat16>, grid, block, 0, s, a);
     if (out_dtype == PKV_F32)
         return wide ? launch_pdl(gather_q8_kernel<128, float>, grid, block, 0, s, a)
                     : launch_pdl(gather_q8_kernel<64, float>, grid, block, 0, s, a);

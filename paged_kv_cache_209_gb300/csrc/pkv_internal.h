@@ -44,6 +44,7 @@ cudaError_t launch_check_decode(const int32_t* tables, int32_t max_blocks, const
 
 constexpr unsigned int kVerdictRange = 1u;
 constexpr unsigned int kVerdictOverlap = 2u;
+constexpr unsigned int kVerdictBlocks = 4u;  // not enough free blocks
 
 // ---------------------------------------------------------------- decode
 struct DecodeArgs {
@@ -182,6 +183,87 @@ cudaError_t launch_append_q8(const void* k, const void* v, const int64_t* slots,
                              unsigned int* status, cudaStream_t s);
 cudaError_t launch_copy_scales(const int64_t* pairs, int64_t num_pairs, float* scales,
                                const pkv_cache_desc& d, unsigned int* status, cudaStream_t s);
+// Copies of whole blocks within one pool of num_blocks blocks of block_vecs 16-byte vectors.
+cudaError_t launch_copy_pool(const int64_t* pairs, int64_t num_pairs, void* pool, int64_t num_blocks, int64_t block_vecs,
+                             unsigned int* status, cudaStream_t s);
+
+// ---------------------------------------------------------------- 4-bit cache
+// Attention of each sequence's last tokens; see pkv_q4.cu.
+struct Q4Args {
+    const void* q;          // [rows][q_heads][head_dim] bf16
+    const void* cache;      // [num_blocks][kv_heads] records (pkv_q4.cuh)
+    const int32_t* tables;
+    const int32_t* lens;
+    const int32_t* qstart;  // [batch + 1], absolute rows of q / out; null: one query per sequence, row i
+    void* out;
+    unsigned int* status;
+    int64_t num_blocks;
+    int32_t max_blocks;
+    int32_t batch;
+    int32_t q_heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t group;
+    int32_t max_query_len;
+    float scale;
+};
+cudaError_t launch_attend_q4(const Q4Args& a, cudaStream_t s);
+
+// ---------------------------------------------------------------- rotary positions
+struct RotaryAppendArgs {
+    const void* q;  // [num_tokens] rows q_stride elements apart, of q_heads head_dim elements; k, v alike
+    const void* k;
+    const void* v;
+    const int32_t* positions;
+    const float* table;  // [num_positions][rotary_dim]: cosines, then sines
+    const int64_t* slots;
+    void* q_out;
+    void* k_cache;  // the records of a 4-bit cache
+    void* v_cache;
+    float* scales;  // int8 pools only
+    unsigned int* status;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;  // in elements
+    int64_t num_tokens;
+    int64_t num_slots;
+    int32_t num_positions;
+    int32_t rotary_dim;  // 0: nothing turns
+    int32_t interleaved;
+    int32_t q_heads;
+    int32_t kv_heads;
+};
+cudaError_t launch_append_rotary(const RotaryAppendArgs& a, const pkv_cache_desc& d, cudaStream_t s);
+// Checked mode: positions inside the table (below zero only beside a slot below zero).
+cudaError_t launch_check_positions(const int32_t* positions, const int64_t* slots, int64_t num_tokens, int32_t num_positions,
+                                   unsigned int* verdict, cudaStream_t s);
+// Angles per position (host); false for arguments that the call rejects.
+bool rotary_frequencies(int rotary_dim, double base, const pkv_rotary_scaling* scaling, double* out);
+cudaError_t launch_rotary_table(const double* frequencies, int half, int64_t first, int64_t positions, float factor, float* table,
+                                cudaStream_t s);
+
+// ---------------------------------------------------------------- planning a step
+struct PlanArgs {
+    const int32_t* lens;
+    const int32_t* new_tokens;
+    const int32_t* held;
+    const int32_t* free_blocks;
+    const int32_t* free_count;
+    int32_t* tables;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* query_start;
+    int32_t* new_lens;
+    int32_t* new_held;
+    int32_t* new_free_count;
+    int32_t* result;  // rows planned, blocks missing
+    unsigned int* status;
+    int64_t free_capacity;
+    int64_t num_blocks;  // ids at or above it are refused
+    int64_t num_rows;
+    int32_t batch;
+    int32_t max_blocks;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s);
+cudaError_t launch_check_plan(const PlanArgs& a, unsigned int* verdict, cudaStream_t s);
 
 // ---------------------------------------------------------------- multi-query decode
 // Several causal queries per sequence; see pkv_multiquery.cu.
@@ -256,6 +338,7 @@ struct GatherArgs {
     const void* k;
     const void* v;
     const float* scales;  // int8 pools only
+    // (a 4-bit cache: k, its records)
     const int32_t* tables;
     const int32_t* lens;
     const int32_t* token_start;  // null: every sequence from token 0

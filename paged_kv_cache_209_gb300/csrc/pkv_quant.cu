@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(64) append_q8_kernel(const __nv_bfloat16* __re
     }
 }
 
-// Copy-on-write of the scales: a block's records are kv_heads * 32 contiguous
-// floats (K and V rows of every head), moved as float4.
-__global__ void __launch_bounds__(256) copy_scales_kernel(const int64_t* __restrict__ pairs, int64_t num_pairs,
-                                                          float4* __restrict__ scales, int64_t num_blocks,
-                                                          int per_block, unsigned int* status) {
+// Copy-on-write within one pool whose blocks are `per_block` contiguous vectors: the
+// scales (kv_heads * 32 floats, K and V rows of every head), or a 4-bit cache's records.
+__global__ void __launch_bounds__(256) copy_pool_kernel(const int64_t* __restrict__ pairs, int64_t num_pairs,
+                                                        uint4* __restrict__ pool, int64_t num_blocks,
+                                                        int64_t per_block, unsigned int* status) {
     grid_dependency_wait();
     allow_dependents();
     const int64_t total = num_pairs * per_block;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) copy_scales_kernel(const int64_t* __restr
             if (c == 0) atomicOr(status, PKV_DEVERR_RANGE);
             continue;
         }
-        scales[dst * per_block + c] = scales[src * per_block + c];
+        pool[dst * per_block + c] = pool[src * per_block + c];
     }
 }
 
@@ -145,12 +145,16 @@ cudaError_t launch_append_q8(const void* k, const void* v, const int64_t* slots,
                       num_slots, d.num_kv_heads, status);
 }
 
+cudaError_t launch_copy_pool(const int64_t* pairs, int64_t num_pairs, void* pool, int64_t num_blocks, int64_t block_vecs,
+                             unsigned int* status, cudaStream_t s) {
+    const int grid = grid_of(num_pairs * block_vecs, 256);
+    return launch_pdl(copy_pool_kernel, dim3(grid), dim3(256), 0, s, pairs, num_pairs, static_cast<uint4*>(pool), num_blocks,
+                      block_vecs, status);
+}
+
 cudaError_t launch_copy_scales(const int64_t* pairs, int64_t num_pairs, float* scales, const pkv_cache_desc& d,
                                unsigned int* status, cudaStream_t s) {
-    const int per_block = d.num_kv_heads * 32 / 4;  // float4 per block
-    const int grid = grid_of(num_pairs * per_block, 256);
-    return launch_pdl(copy_scales_kernel, dim3(grid), dim3(256), 0, s, pairs, num_pairs,
-                      reinterpret_cast<float4*>(scales), d.num_blocks, per_block, status);
+    return launch_copy_pool(pairs, num_pairs, scales, d.num_blocks, d.num_kv_heads * 32 / 4, status, s);
 }
 
 }  // namespace pkv

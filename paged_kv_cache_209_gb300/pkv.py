@@ -51,6 +51,11 @@ class PoolStats(ctypes.Structure):
         "logical_tokens", "internal_waste_tokens", "sharing_savings_tokens", "sequences")]
 
 
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("stretch", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double)]
+
+
 class DecodeOpts(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("stages", ctypes.c_int32),
                 ("prefix_kernel", ctypes.c_int32)]
@@ -63,7 +68,9 @@ EXPORTS = ("pkv_append", "pkv_copy_blocks", "pkv_decode_workspace_size", "pkv_de
            "pkv_multiquery_workspace_size", "pkv_multiquery_attention",
            "pkv_append_q8", "pkv_copy_blocks_q8", "pkv_decode_q8_workspace_size", "pkv_decode_attention_q8",
            "pkv_multiquery_q8_workspace_size", "pkv_multiquery_attention_q8", "pkv_gather", "pkv_gather_q8",
-           "pkv_verify_drafts", "pkv_device_status", "pkv_status_string", "pkv_version",
+           "pkv_verify_drafts", "pkv_append_q4", "pkv_copy_blocks_q4", "pkv_gather_q4", "pkv_multiquery_q4_workspace_size",
+           "pkv_decode_attention_q4", "pkv_multiquery_attention_q4", "pkv_rotary_frequencies", "pkv_rotary_table",
+           "pkv_append_rotary", "pkv_plan_step", "pkv_device_status", "pkv_status_string", "pkv_version",
            "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_add_sequence", "pkv_pool_append", "pkv_pool_append_batch",
            "pkv_pool_share_prefix", "pkv_pool_release", "pkv_pool_sequence_length", "pkv_pool_page_table",
            "pkv_pool_block_tables", "pkv_pool_get_stats", "pkv_pool_validate")
@@ -125,6 +132,29 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pkv_verify_drafts.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp,
                                       vp, u32, vp]
     lib.pkv_verify_drafts.restype = ctypes.c_int
+    lib.pkv_append_q4.argtypes = [vp, vp, vp, i64, vp, desc_p, u32, vp]
+    lib.pkv_append_q4.restype = ctypes.c_int
+    lib.pkv_copy_blocks_q4.argtypes = [vp, i64, vp, desc_p, u32, vp]
+    lib.pkv_copy_blocks_q4.restype = ctypes.c_int
+    lib.pkv_gather_q4.argtypes = [vp, vp, i32, vp, vp, vp, i32, i64, vp, vp, i32, desc_p, u32, vp]
+    lib.pkv_gather_q4.restype = ctypes.c_int
+    lib.pkv_multiquery_q4_workspace_size.argtypes = [i32, i32, i32, i32, desc_p]
+    lib.pkv_multiquery_q4_workspace_size.restype = ctypes.c_size_t
+    lib.pkv_decode_attention_q4.argtypes = [vp, vp, vp, i32, vp, i32, i32, ctypes.c_float, vp, vp, ctypes.c_size_t, desc_p,
+                                            u32, vp]
+    lib.pkv_decode_attention_q4.restype = ctypes.c_int
+    lib.pkv_multiquery_attention_q4.argtypes = [vp, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp,
+                                                ctypes.c_size_t, desc_p, u32, vp]
+    lib.pkv_multiquery_attention_q4.restype = ctypes.c_int
+    lib.pkv_rotary_frequencies.argtypes = [i32, ctypes.c_double, ctypes.POINTER(RotaryScaling), vp]
+    lib.pkv_rotary_frequencies.restype = ctypes.c_int
+    lib.pkv_rotary_table.argtypes = [vp, i32, i64, i64, ctypes.c_float, vp, vp]
+    lib.pkv_rotary_table.restype = ctypes.c_int
+    lib.pkv_append_rotary.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, i64, i32, vp, i64, vp, vp, vp,
+                                      desc_p, u32, vp]
+    lib.pkv_append_rotary.restype = ctypes.c_int
+    lib.pkv_plan_step.argtypes = [vp, vp, vp, vp, i64, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, u32, vp]
+    lib.pkv_plan_step.restype = ctypes.c_int
     lib.pkv_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, vp]
     lib.pkv_device_status.restype = ctypes.c_int
     lib.pkv_status_string.argtypes = [ctypes.c_int]
@@ -662,6 +692,264 @@ def pkv_verify_drafts(target_probs, draft_probs, draft_tokens, accept_uniform, s
     if status:
         raise PkvError("pkv_verify_drafts", status)
     return out_tokens, num_accepted, new_context_lens
+
+
+PKV_INT4 = 3
+
+
+def pkv_q4_record_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit cache's record (16 tokens of one block and KV head)."""
+    return 16 * head_dim + 128
+
+
+def _q4_geometry(cache):
+    """(blocks, KV heads, head_dim) of a 4-bit cache [num_blocks][kv_heads][record bytes]."""
+    if cache.dim() != 3 or cache.dtype != torch.uint8 or cache.shape[2] not in (16 * 64 + 128, 16 * 128 + 128):
+        raise ValueError("a 4-bit cache is uint8 [num_blocks][num_kv_heads][16 * head_dim + 128], head_dim 64 or 128")
+    nb, hkv, record = cache.shape
+    return nb, hkv, (record - 128) // 16
+
+
+def pkv_append_q4(k, v, slot_mapping, cache, flags: int = 0, stream=None) -> None:
+    """Quantizing slot-mapped append of bf16 k/v [tokens][kv_heads][head_dim] into the 4-bit cache."""
+    lib = _lib or load_library()
+    nb, hkv, d = _q4_geometry(cache)
+    here = _here()
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping is [tokens]")
+    tokens = slot_mapping.shape[0]
+    want = (tokens, hkv, d)
+    status = lib.pkv_append_q4(_on(here, "k", k, torch.bfloat16, want), _on(here, "v", v, torch.bfloat16, want),
+                               _on(here, "slot_mapping", slot_mapping, torch.int64), tokens, _on(here, "cache", cache),
+                               _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_append_q4", status)
+
+
+def pkv_copy_blocks_q4(src_dst_pairs, cache, flags: int = 0, stream=None) -> None:
+    """Copy block src onto block dst of the 4-bit cache for every int64 (src, dst) row."""
+    lib = _lib or load_library()
+    nb, hkv, d = _q4_geometry(cache)
+    here = _here()
+    n = src_dst_pairs.shape[0]
+    status = lib.pkv_copy_blocks_q4(_on(here, "src_dst_pairs", src_dst_pairs, torch.int64, (n, 2)), n,
+                                    _on(here, "cache", cache), _desc(nb, 16, hkv, d, PKV_INT4), flags,
+                                    _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_copy_blocks_q4", status)
+
+
+def pkv_gather_q4(cache, block_tables, context_lens, row_start, num_rows: int, token_start=None,
+                  out_dtype=torch.bfloat16, k_out=None, v_out=None, flags: int = 0, stream=None):
+    """``pkv_gather`` over the 4-bit cache: the values (code * scale) as ``out_dtype``, bf16 or float32."""
+    lib = _lib or load_library()
+    nb, hkv, d = _q4_geometry(cache)
+    code = _dtype_code(out_dtype)
+    here = _here()
+    pool = _on(here, "cache", cache)
+    args, k_out, v_out = _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out,
+                                      v_out, out_dtype, cache, stream)
+    status = lib.pkv_gather_q4(pool, *args, code, _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_gather_q4", status)
+    return k_out, v_out
+
+
+def pkv_multiquery_q4_workspace_size(batch: int, num_q_heads: int, max_blocks_per_seq: int, max_query_len: int,
+                                     cache) -> int:
+    """Workspace bytes of the 4-bit attention calls (decode: ``max_query_len`` 1); allocate them zero-filled and
+    reuse them."""
+    nb, hkv, d = _q4_geometry(cache)
+    return int((_lib or load_library()).pkv_multiquery_q4_workspace_size(
+        batch, num_q_heads, max_blocks_per_seq, max_query_len, _desc(nb, 16, hkv, d, PKV_INT4)))
+
+
+def _attention_q4(name, q, cache, block_tables, context_lens, query_start, scale, max_query_len, out, workspace, flags,
+                  stream):
+    lib = _lib or load_library()
+    nb, hkv, d = _q4_geometry(cache)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q is bf16 [rows][q_heads][head_dim]")
+    rows, q_heads, _ = q.shape
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables is [batch][max_blocks]")
+    batch, max_blocks = block_tables.shape
+    if query_start is None and rows != batch:
+        raise ValueError("q has one row per sequence")
+    new = out is None
+    if new:
+        out = _made(stream, torch.empty_like, q)
+    if workspace is None:
+        need = pkv_multiquery_q4_workspace_size(batch, q_heads, max_blocks, max_query_len, cache)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
+    here = _here()
+    lens = _on(here, "context_lens", context_lens, torch.int32, (batch,))
+    middle = (batch, q_heads) if query_start is None else \
+        (_on(here, "query_start", query_start, torch.int32, (batch + 1,)), batch, q_heads, max_query_len)
+    args = (_on(here, "q", q), _on(here, "cache", cache), _on(here, "block_tables", block_tables, torch.int32), max_blocks,
+            lens, *middle, scale, out.data_ptr() if new else _on(here, "out", out, torch.bfloat16, q.shape),
+            _on(here, "workspace", workspace), workspace.numel() * workspace.element_size())
+    if rows == 0:                                            # no query anywhere: no row to write
+        return out
+    status = getattr(lib, name)(*args, _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError(name, status)
+    return out
+
+
+def pkv_decode_attention_q4(q, cache, block_tables, context_lens, scale: float, out=None, workspace=None,
+                            flags: int = 0, stream=None):
+    """Decode attention over the 4-bit cache; returns ``out`` (bf16 [batch][q_heads][head_dim])."""
+    return _attention_q4("pkv_decode_attention_q4", q, cache, block_tables, context_lens, None, scale, 1, out, workspace,
+                         flags, stream)
+
+
+def pkv_multiquery_attention_q4(q, cache, block_tables, context_lens, query_start, scale: float, max_query_len: int,
+                                out=None, workspace=None, flags: int = 0, stream=None):
+    """Causal attention of each sequence's new tokens over the 4-bit cache, any number of them:
+    ``q``/``out`` are bf16 [rows][q_heads][head_dim], ``query_start`` int32 [batch + 1] their row
+    offsets. Returns ``out`` (rows no sequence names are left as they were)."""
+    return _attention_q4("pkv_multiquery_attention_q4", q, cache, block_tables, context_lens, query_start, scale,
+                         max_query_len, out, workspace, flags, stream)
+
+
+ROTARY_KINDS = {"plain": 0, "linear": 1, "base": 2, "turns": 3, "ramp": 4}
+
+
+def pkv_rotary_frequencies(rotary_dim: int, base: float = 10000.0, kind: str = "plain", stretch: float = 1.0,
+                           original_context: float = 0.0, low_turns: float = 0.0, high_turns: float = 0.0):
+    """Angles per position of ``rotary_dim`` dimensions, a float64 host tensor [rotary_dim // 2]; ``kind`` says how
+    they are stretched for long contexts (include/pkv.h, pkv_rotary_kind)."""
+    if kind not in ROTARY_KINDS:
+        raise ValueError(f"kind is one of {sorted(ROTARY_KINDS)}")
+    out = torch.empty(max(rotary_dim // 2, 1), dtype=torch.float64)
+    how = RotaryScaling(ROTARY_KINDS[kind], stretch, original_context, low_turns, high_turns)
+    _check("pkv_rotary_frequencies", load_library().pkv_rotary_frequencies(rotary_dim, base, ctypes.byref(how),
+                                                                           out.data_ptr()))
+    return out
+
+
+def pkv_rotary_table(frequencies, num_positions: int, first_position: int = 0, factor: float = 1.0, out=None,
+                     stream=None):
+    """``factor`` times the cosines, then the sines, of positions ``first_position ..``: float32
+    [num_positions][rotary_dim]; ``frequencies`` float64 [rotary_dim // 2] on the device."""
+    lib = _lib or load_library()
+    here = _here()
+    if frequencies.dim() != 1:
+        raise ValueError("frequencies are [rotary_dim / 2]")
+    dim = 2 * frequencies.shape[0]
+    want = (num_positions, dim)
+    at = _on(here, "frequencies", frequencies, torch.float64)
+    if out is None:
+        out = _made(stream, torch.empty, want, dtype=torch.float32, device=frequencies.device)
+    status = lib.pkv_rotary_table(at, dim, first_position, num_positions, factor, _on(here, "out", out, torch.float32, want),
+                                  _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_rotary_table", status)
+    return out
+
+
+def _token_rows(here, name, t, dtype, shape):
+    """(address, stride between tokens) of rows [tokens][heads][head_dim] that may lie apart."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} is {str(dtype)[6:]} {list(shape)}, not {str(t.dtype)[6:]} {list(t.shape)}")
+    if t.get_device() != here:
+        raise ValueError(f"libpkv takes CUDA tensors only, on the current device ({name} is on {t.device})")
+    tokens, heads, d = shape
+    if tokens and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"a token's heads in {name} follow one another")
+    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
+
+
+def pkv_append_rotary(q, k, v, positions, table, slot_mapping, k_cache, v_cache=None, scales=None,
+                      interleaved: bool = False, q_out=None, flags: int = 0, stream=None):
+    """Rotary positions on q and k (the first ``table.shape[1]`` dimensions of a head), k and v appended: into bf16
+    or float32 pools (``k_cache``, ``v_cache``), int8 pools (with ``scales``) or a 4-bit cache (``k_cache`` alone).
+    q, k and v are [tokens][heads][head_dim], a token's heads together, tokens any stride apart; q may be None.
+    Returns q's turned rows (``q_out``, which may be q itself; None without q)."""
+    lib = _lib or load_library()
+    here = _here()
+    if scales is not None:
+        nb, hkv, bs, d = _q8_geometry(k_cache, v_cache, scales)
+        dtype, code = torch.bfloat16, PKV_INT8
+    elif v_cache is None:
+        nb, hkv, d = _q4_geometry(k_cache)
+        bs, dtype, code = 16, torch.bfloat16, PKV_INT4
+    else:
+        _same_pools(k_cache, v_cache)
+        if k_cache.dim() != 4:
+            raise ValueError("a pool is [num_blocks][num_kv_heads][16][head_dim]")
+        nb, hkv, bs, d = k_cache.shape
+        dtype, code = k_cache.dtype, _dtype_code(k_cache.dtype)
+    if slot_mapping.dim() != 1 or table.dim() != 2:
+        raise ValueError("slot_mapping is [tokens], table [positions][rotary_dim]")
+    tokens = slot_mapping.shape[0]
+    k_at, k_stride = _token_rows(here, "k", k, dtype, (tokens, hkv, d))
+    v_at, v_stride = _token_rows(here, "v", v, dtype, (tokens, hkv, d))
+    heads = q_stride = out_stride = 0
+    q_at = out_at = None
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q is [tokens][q_heads][head_dim]")
+        heads = q.shape[1]
+        q_at, q_stride = _token_rows(here, "q", q, dtype, (tokens, heads, d))
+        if q_out is None:
+            q_out = _made(stream, torch.empty, (tokens, heads, d), dtype=dtype, device=q.device)
+        out_at, out_stride = _token_rows(here, "q_out", q_out, dtype, (tokens, heads, d))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    status = lib.pkv_append_rotary(
+        q_at, q_stride, k_at, k_stride, v_at, v_stride, _on(here, "positions", positions, torch.int32, (tokens,)),
+        _on(here, "table", table, torch.float32), table.shape[0], table.shape[1], int(interleaved),
+        _on(here, "slot_mapping", slot_mapping, torch.int64), tokens, heads, out_at, out_stride,
+        _on(here, "k_cache", k_cache), None if v_cache is None else _on(here, "v_cache", v_cache),
+        None if scales is None else _on(here, "scales", scales), _desc(nb, bs, hkv, d, code), flags,
+        _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_append_rotary", status)
+    return q_out
+
+
+def pkv_plan_step(context_lens, new_tokens, held_blocks, free_blocks, free_count, block_tables, num_rows: int,
+                  num_blocks: int = 0, flags: int = 0, stream=None, out=None):
+    """Where a step's new tokens go: returns ``(slot_mapping int64 [num_rows], positions int32 [num_rows], query_start
+    int32 [batch + 1], new_context_lens, new_held_blocks int32 [batch], new_free_count int32 [1], result int32 [2])``
+    and writes the new entries of ``block_tables``; ``result`` holds the rows planned and the blocks missing.
+    ``out`` takes such a tuple to write into."""
+    lib = _lib or load_library()
+    here = _here()
+    i32, dev = torch.int32, block_tables.device
+    if block_tables.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("block_tables is [batch][max_blocks], free_blocks [capacity]")
+    batch, max_blocks = block_tables.shape
+    one = (batch,)
+    at = (_on(here, "context_lens", context_lens, i32, one), _on(here, "new_tokens", new_tokens, i32, one),
+          _on(here, "held_blocks", held_blocks, i32, one), _on(here, "free_blocks", free_blocks, i32),
+          free_blocks.shape[0], _on(here, "free_count", free_count, i32, (1,)),
+          _on(here, "block_tables", block_tables, i32), max_blocks, batch, num_rows, num_blocks)
+    if out is None:
+        # one allocation: rows of 8 bytes, then everything of 4, each part on a 16-byte boundary
+        parts = [(num_rows, torch.int64)] + [(n, i32) for n in (num_rows, batch + 1, batch, batch, 1, 2)]
+        sizes = [(n * t.itemsize + 15) // 16 * 16 for n, t in parts]
+        memory = _made(stream, torch.empty, max(16, sum(sizes)), dtype=torch.uint8, device=dev)
+        out, where = [], 0
+        for (n, t), size in zip(parts, sizes):
+            out.append(memory[where:where + n * t.itemsize].view(t))
+            where += size
+        out = tuple(out)
+        outs = [t.data_ptr() for t in out]
+    else:
+        shapes = ((num_rows,), (num_rows,), (batch + 1,), one, one, (1,), (2,))
+        names = ("slot_mapping", "positions", "query_start", "new_context_lens", "new_held_blocks", "new_free_count",
+                 "result")
+        outs = [_on(here, name, t, torch.int64 if i == 0 else i32, shape)
+                for i, (name, t, shape) in enumerate(zip(names, out, shapes))]
+        if len(outs) != 7:
+            raise ValueError(f"out holds {', '.join(names)}")
+    status = lib.pkv_plan_step(*at, *outs, flags, _raw_stream(stream, here))
+    if status:
+        raise PkvError("pkv_plan_step", status)
+    return out
 
 
 def pkv_decode_attention_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float, out=None,
