@@ -990,12 +990,29 @@ pkv_status pkv_gather_q4(const void* cache, const int32_t* block_tables, int32_t
                       num_rows, k_out, v_out, out_dtype, desc, flags, static_cast<cudaStream_t>(stream));
 }
 
+static size_t q4_counters_bytes(const pkv_cache_desc* desc) {
+    return (static_cast<size_t>(kMaxBatchPerLaunch) * desc->num_kv_heads * 4 * sizeof(int) + 255) / 256 * 256;
+}
+
 size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_heads, int32_t max_blocks_per_seq,
                                         int32_t max_query_len, const pkv_cache_desc* desc) {
     if (check_desc_q4(desc) != PKV_OK || batch < 0 || !q_heads_ok(num_q_heads, desc)) return 0;
     if (max_query_len < 1 || max_query_len > kMaxQueryLen) return 0;
     if (batch > 0 && !table_width_ok(batch, max_blocks_per_seq)) return 0;
-    return 256;
+    // the counters of a launch's most sequences lie first, whatever the sizes, so that one workspace
+    // serves calls of all sizes on either kernel
+    const int64_t rows = static_cast<int64_t>(max_query_len) * (num_q_heads / desc->num_kv_heads);
+    const size_t tiles = chunk_q8_workspace_bytes(desc->head_dim);
+    const size_t split = q4_partials_bytes(desc->head_dim, q4_plan(desc->head_dim, rows < kMq4Rows ? static_cast<int>(rows) : kMq4Rows));
+    return q4_counters_bytes(desc) + (split > tiles ? split : tiles);
+}
+
+// 4-bit multi-query calls: whether the kernel that splits the cache takes them, or the one that works in tiles.
+static bool split_takes_q4(const pkv_cache_desc* d, int32_t batch, int32_t max_blocks, int64_t rows) {
+    (void)d;
+    (void)batch;
+    (void)max_blocks;
+    return rows <= kMq4Rows;
 }
 
 // Both attention calls over the 4-bit cache, after the checks of their own.
@@ -1025,8 +1042,38 @@ static pkv_status run_attention_q4(const void* q, const void* cache, const int32
         }, s);
         if (st != PKV_OK) return st;
     }
+    const int G = num_q_heads / desc->num_kv_heads;
+    const int64_t rows = static_cast<int64_t>(max_query_len) * G;
+    char* ws = static_cast<char*>(workspace);
+    const size_t pieces = q4_counters_bytes(desc);
+    const bool tiles = query_start != nullptr && !split_takes_q4(desc, batch, max_blocks_per_seq, rows);
+    const Q4Plan plan = tiles ? Q4Plan{} : q4_plan(desc->head_dim, static_cast<int>(rows));
     const int64_t row = static_cast<int64_t>(num_q_heads) * desc->head_dim * 2;
     for (int32_t b0 = 0; b0 < batch; b0 += kMaxBatchPerLaunch) {
+        const int32_t nb = batch - b0 < kMaxBatchPerLaunch ? batch - b0 : kMaxBatchPerLaunch;
+        if (tiles) {
+            ChunkArgs a{};
+            a.q = q;
+            a.k_codes = cache;
+            a.tables = block_tables + static_cast<int64_t>(b0) * max_blocks_per_seq;
+            a.lens = context_lens + b0;
+            a.qstart = query_start + b0;
+            a.out = out;
+            a.workspace = ws + pieces;
+            a.status = status;
+            a.num_blocks = desc->num_blocks;
+            a.max_blocks = max_blocks_per_seq;
+            a.batch = nb;
+            a.q_heads = num_q_heads;
+            a.kv_heads = desc->num_kv_heads;
+            a.head_dim = desc->head_dim;
+            a.group = G;
+            a.max_query_len = max_query_len;
+            a.scale = scale;
+            a.group_inverse = ((uint64_t(1) << 37) + G - 1) / G;
+            if (launch_chunk_q4(a, s) != cudaSuccess) return PKV_ERR_CUDA;
+            continue;
+        }
         Q4Args a{};
         // with query offsets the rows are absolute; without, row i of this launch is sequence b0 + i
         a.q = query_start ? q : static_cast<const char*>(q) + b0 * row;
@@ -1038,14 +1085,19 @@ static pkv_status run_attention_q4(const void* q, const void* cache, const int32
         a.status = status;
         a.num_blocks = desc->num_blocks;
         a.max_blocks = max_blocks_per_seq;
-        a.batch = batch - b0 < kMaxBatchPerLaunch ? batch - b0 : kMaxBatchPerLaunch;
+        a.batch = nb;
         a.q_heads = num_q_heads;
         a.kv_heads = desc->num_kv_heads;
         a.head_dim = desc->head_dim;
-        a.group = num_q_heads / desc->num_kv_heads;
+        a.group = G;
         a.max_query_len = max_query_len;
         a.scale = scale;
-        if (launch_attend_q4(a, s) != cudaSuccess) return PKV_ERR_CUDA;
+        a.counters = reinterpret_cast<int*>(ws);
+        a.partials = reinterpret_cast<float*>(ws + pieces);
+        a.num_ctas = plan.num_ctas;
+        a.tiles = plan.tiles;
+        a.warps_per_unit = plan.warps_per_unit;
+        if (launch_mq4(a, plan, s) != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;
 }

@@ -74,6 +74,7 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_q4.cuh"
 
 #include "pkv_chunk_schedule.cuh"
 
@@ -102,7 +103,9 @@ constexpr int kMostLack = 60;
 
 constexpr int kMaxPieces = 512;  // CTAs of a launch, and pieces of a unit, at most
 
-template <int D>
+// Q4: over the 4-bit cache, whose codes the converters take out of its records (all else
+// is the same).
+template <int D, bool Q4>
 struct Cx {
     static constexpr int kSoftmaxWarps = 8;
     static constexpr int kConvertWarp = 8;  // K: 8 .. 11, V: 12 .. 15
@@ -123,7 +126,10 @@ struct Cx {
     static constexpr int kPartBytes = 128 * 128;              // 128 rows of one part
     static constexpr int kTileBytes = kHalves * kPartBytes;   // Q of one row half; one K stage
     static constexpr int kVPartBytes = D * 128;               // one V stage: 64 tokens of every coordinate
-    static constexpr int kVecs = D / 16;                      // 16-code vectors of a converter lane and step
+    static constexpr int kVecs = Q4 ? D / 32 : D / 16;        // 16-byte vectors of a converter lane and step
+    // vectors from one (block, KV head) to the next, and V's codes after K's (Q4: in the same record)
+    static constexpr int kChunkVecs = Q4 ? q4_record_bytes(D) / 16 : D;
+    static constexpr int kVOffset = Q4 ? q4_v_offset(D) / 16 : 0;
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
@@ -298,6 +304,27 @@ __device__ __forceinline__ uint4 v_values(uint32_t w0, uint32_t w1, const uint4&
                       bits(__hmul2(codes_f16x2(__byte_perm(w1, 0x64646464u, 0x5140)), half2_of(f.z))),
                       bits(__hmul2(codes_f16x2(__byte_perm(w1, 0x64646464u, 0x7362)), half2_of(f.w))));
 }
+// Nibbles p and p + 4 of a word of 4-bit codes (code + 8) as two f16 codes, exactly, p = 0
+// or 1: they become the low mantissa bits of the f16 1024, p = 1 sixteen times as large.
+template <int p>
+__device__ __forceinline__ __half2 nibbles_f16x2(uint32_t w) {
+    const uint32_t h = w & (p ? 0x00f000f0u : 0x000f000fu) | 0x64006400u;
+    const __half2 less = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));    // 1032
+    const __half2 part = __halves2half2(__ushort_as_half(0x2c00), __ushort_as_half(0x2c00));    // 1 / 16
+    const __half2 minus = __halves2half2(__ushort_as_half(0xd480), __ushort_as_half(0xd480));   // -72
+    return p ? __hfma2(half2_of(h), part, minus) : __hsub2(half2_of(h), less);
+}
+// Eight dimensions of a token times hi + lo.
+__device__ __forceinline__ uint4 k_nibbles(uint32_t w, __half2 hi, __half2 lo) {
+    const __half2 c0 = nibbles_f16x2<0>(w), c1 = nibbles_f16x2<1>(w), c2 = nibbles_f16x2<0>(w >> 8), c3 = nibbles_f16x2<1>(w >> 8);
+    return make_uint4(bits(__hfma2(c0, hi, __hmul2(c0, lo))), bits(__hfma2(c1, hi, __hmul2(c1, lo))),
+                      bits(__hfma2(c2, hi, __hmul2(c2, lo))), bits(__hfma2(c3, hi, __hmul2(c3, lo))));
+}
+// Eight tokens of a dimension, nibbles `shift` / 4 and 4 above of four words, times their factors.
+__device__ __forceinline__ uint4 v_nibbles(const uint32_t (&w)[4], const uint4& f, int shift) {
+    return make_uint4(bits(__hmul2(nibbles_f16x2<0>(w[0] >> shift), half2_of(f.x))), bits(__hmul2(nibbles_f16x2<0>(w[1] >> shift), half2_of(f.y))),
+                      bits(__hmul2(nibbles_f16x2<0>(w[2] >> shift), half2_of(f.z))), bits(__hmul2(nibbles_f16x2<0>(w[3] >> shift), half2_of(f.w))));
+}
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 // The exponent that takes the largest of some scales (its bits; not an infinity) to 1/2 .. 1.
@@ -388,9 +415,8 @@ static_assert(sizeof(Job) == 48, "layout");
 // All lanes of the warp, or kLanes = 1: one thread. False at the end (job.s1 == 0) and
 // where the wait ran out (job.s1 < 0): with kWhileSteps, where no step was laid out for the
 // CTA while it lasted (the scale warps stay a few steps ahead of the products).
-template <int D, int kLanes, bool kWhileSteps = false>
+template <typename C, int kLanes, bool kWhileSteps = false>
 __device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int& count, Job& job) {
-    using C = Cx<D>;
     const int slot = count % C::kJobs;
     const uint32_t parity = static_cast<uint32_t>(count / C::kJobs) & 1u;
     if (kWhileSteps) {
@@ -419,9 +445,8 @@ __device__ __forceinline__ bool next_job(uint8_t* smem, uint64_t* job_full, uint
 }
 
 // Lays out the segment after `count` others (one thread).
-template <int D>
+template <typename C>
 __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, uint64_t* job_full, uint64_t* job_empty, int ranges, int count) {
-    using C = Cx<D>;
     const int slot = count % C::kJobs;
     if (count >= C::kJobs && !wait(&job_empty[slot], static_cast<uint32_t>(count / C::kJobs - 1) & 1u)) return;
     ChunkWalk& walk = *reinterpret_cast<ChunkWalk*>(smem + C::kOffWalk);
@@ -452,10 +477,16 @@ __device__ __forceinline__ void lay_out_job(const ChunkArgs& a, uint8_t* smem, u
 // 2000 of 5200 cycles a step; with a quarter of every step per warp 2900 of 3300 where
 // one row half is in use, because each step's chain then followed on the last one's.)
 // Lane l holds tokens l, 32 + l, 64 + l, 96 + l; 32 of them at a time are taken as bare codes.
-template <int D>
+template <int D, bool Q4>
+__device__ __forceinline__ const float* scales_of(const ChunkArgs& a, int id, int head) {  // 16 K scales, then 16 V scales
+    const int64_t chunk = static_cast<int64_t>(id) * a.kv_heads + head;
+    if (Q4) return reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.k_codes) + chunk * q4_record_bytes(D) + q4_scales_offset(D));
+    return a.scales + chunk * 32;
+}
+template <int D, bool Q4>
 __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, int ranges, uint64_t* job_full, uint64_t* job_empty,
                                            uint64_t* full, uint64_t* empty) {
-    using C = Cx<D>;
+    using C = Cx<D, Q4>;
     const int lane = threadIdx.x & 31;
     const int w = (threadIdx.x >> 5) & 3;
     int jobs = 0;
@@ -464,10 +495,10 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
     Job job;
     while (true) {
         if (w == 0) {
-            if (lane == 0) lay_out_job<D>(a, smem, job_full, job_empty, ranges, jobs);
+            if (lane == 0) lay_out_job<C>(a, smem, job_full, job_empty, ranges, jobs);
             __syncwarp();
         }
-        if (!next_job<D, 32>(smem, job_full, job_empty, jobs, job)) break;
+        if (!next_job<C, 32>(smem, job_full, job_empty, jobs, job)) break;
         const int steps = job.s1 - job.s0;
         const int32_t* trow = a.tables + static_cast<int64_t>(job.seq) * a.max_blocks;
         const int blocks = (job.n + 15) / 16;
@@ -493,7 +524,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 const int id = __shfl_sync(0xffffffffu, mine, 2 * g + lane / 16);
                 present[g] = id >= 0 && step * kChunkStep + 32 * g + lane < job.n;
                 missing[g] = id == -2;
-                const float* rec = a.scales + (static_cast<int64_t>(max(0, id)) * a.kv_heads + job.head) * 32 + (lane & 15);
+                const float* rec = scales_of<D, Q4>(a, max(0, id), job.head) + (lane & 15);
                 ks[g] = __ldg(rec);
                 vs[g] = __ldg(rec + 16);
             }
@@ -501,7 +532,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 // the scales of the segment's first block, K's in lanes 0-15 and V's in 16-31, give E and F
                 opened = true;
                 if (first < 0 || first >= a.num_blocks) first = 0;
-                const float x = __ldg(a.scales + (static_cast<int64_t>(first) * a.kv_heads + job.head) * 32 + lane);
+                const float x = __ldg(scales_of<D, Q4>(a, first, job.head) + lane);
                 const uint32_t size = __float_as_uint(job.s0 * kChunkStep + (lane & 15) < job.n ? x : 0.f) & 0x7fffffffu;
                 const bool use = size < 0x7f800000u;
                 ek = range_exponent(__reduce_max_sync(0xffffffffu, use && lane < 16 ? size : 0u));
@@ -537,7 +568,7 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
                 for (int g = 0; g < 4; ++g)  // (-inf for a scale of zero)
                     if (bare_v[g] && present[g]) tab[4 + 128 + 32 * g + lane] = log2f(fabsf(vs[g])) - static_cast<float>(ev);
             }
-            if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * D;
+            if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * C::kChunkVecs;
             if (lane == 0) {
                 *reinterpret_cast<float4*>(tab) = make_float4(exp2_int(ev), exp2_int(ek), __uint_as_float(slow ? 1u : 0u), __int_as_float(at));
                 *reinterpret_cast<int*>(record + 1344) = 1;
@@ -564,16 +595,26 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
 // 32 w .. 32 w + 31 of a step (blocks 2 w, 2 w + 1). A lane copies the codes of the
 // next step into its own slots of shared memory as it takes the current ones out of
 // them (asynchronous copies: a step's time ahead, and no registers).
-template <int D, bool IsV>
+//
+// Q4: a lane's K vector is 32 dimensions of one token. A vector of V holds an octet of
+// dimensions of one quad of tokens; a lane converts the words of one pair of dimensions of
+// all four quads, which make whole 16-byte pieces of two coordinate rows. So vectors
+// change lanes in shared memory, in an order (quad ^ octet / 2 % 4) that meets every bank
+// once.
+template <int D, bool Q4, bool IsV>
 __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, uint64_t* rec_full, uint64_t* rec_empty, uint64_t* full,
                                              uint64_t* empty) {
-    using C = Cx<D>;
+    using C = Cx<D, Q4>;
     const int lane = threadIdx.x & 31;
     const int cw = (threadIdx.x >> 5) & 3;
     constexpr int kPerBlock = C::kVecs / 2;    // vectors of a lane in each of the warp's two blocks
-    constexpr int kLanes = D / 16;             // lanes that hold one token's K row
-    const uint4* codes = static_cast<const uint4*>(IsV ? a.v_codes : a.k_codes) + lane;
+    constexpr int kLanes = Q4 ? D / 32 : D / 16;  // lanes that hold one token's K row
+    const uint4* codes = static_cast<const uint4*>(!IsV || Q4 ? a.k_codes : a.v_codes) + (IsV ? C::kVOffset : 0) + lane;
     uint8_t* mine = smem + C::kOffCodes + (((IsV ? 4 : 0) + cw) * C::kVecs * 32 + lane) * 16;  // vector i at + 512 i
+    // (Q4: V's vectors in another order within each 512 bytes, the word of pair `lane` % 4 of quad 0)
+    const int octet = lane >> 2;  // and 8 more for the second vector of a block
+    const int pair = C::kOffCodes + ((IsV ? 4 : 0) + cw) * C::kVecs * 512 + octet * 64 + (octet >> 1 & 3) * 16 + (lane & 3) * 4;
+    if (Q4 && IsV) mine += ((lane & 3) ^ (octet >> 1 & 3)) * 16 - (lane & 3) * 16;
     const uint4 *src0 = nullptr, *src1 = nullptr;  // the next step's two blocks of this warp
     int slot = 0, next_slot = 0;     // records of the step and of the next
     uint32_t parity = 0;             // of the next record
@@ -605,10 +646,62 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
                 break;
             }
             copy_wait_all();
+            if (Q4 && IsV) __syncwarp();  // the other lanes' vectors
             // Two vectors at a time, the next two on their way out of shared memory. (8
             // sequences by 512 new tokens: 425 us unrolled, rolled 444. It was the other way
             // round while the issuers' and the waits' code was twice as long: 627 and 546.)
-            if (IsV) {
+            if (Q4 && IsV) {
+                // ---- coordinate rows 8 octet + 2 (lane % 4) and the next one; this warp's tokens are 32 cw .. 32 cw + 31
+                uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + (8 * octet + 2 * (lane & 3)) * 128;
+                const uint8_t* factors = record + 1024 + 64 * cw;
+                const int odd = octet & 1;  // lanes that begin with the odd row: no bank is hit twice
+                const int row8 = 2 * (lane & 3) + odd;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint4 f0 = *reinterpret_cast<const uint4*>(factors + 32 * b), f1 = *reinterpret_cast<const uint4*>(factors + 32 * b + 16);
+                    const int chunk = ((2 * cw + b) & 3) * 2;
+#pragma unroll
+                    for (int i = 0; i < kPerBlock; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = *reinterpret_cast<const uint32_t*>(smem + (pair ^ (q * 16)) + 512 * (b * kPerBlock + i));
+                        uint8_t* row = vd + 64 * i * 128;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint8_t* to = row + (odd ^ u) * 128;
+                            const int shift = 4 * (odd ^ u);
+                            *reinterpret_cast<uint4*>(to + ((chunk ^ row8 ^ u) << 4)) = v_nibbles(w, f0, shift);
+                            *reinterpret_cast<uint4*>(to + ((chunk ^ 1 ^ row8 ^ u) << 4)) = v_nibbles(w, f1, shift + 8);
+                        }
+                    }
+                }
+                __syncwarp();  // every lane has read: the next vectors may come
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < C::kVecs; ++i) copy16_async(smem_u32(mine + 512 * i), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
+                }
+            } else if (Q4) {
+                // ---- token rows: vector i of a lane lies in row 32 cw + i * (32 / kLanes) + lane / kLanes, dimensions 32 (lane % kLanes) ..
+                const int ch = lane % kLanes, sub = lane / kLanes;
+                // lanes of the second column part take their words in another order: no bank is hit twice
+                const int flip = ch >> 1;
+                uint8_t* kd = smem + C::kOffK + st * C::kTileBytes + flip * C::kPartBytes + (32 * cw + sub) * 128;
+                constexpr int kRows = 32 / kLanes;
+                const uint8_t* factors = record + (32 * cw + sub) * 8;
+#pragma unroll
+                for (int i = 0; i < C::kVecs; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(mine + 512 * i);
+                    const uint2 f = *reinterpret_cast<const uint2*>(factors + i * kRows * 8);
+                    const uint32_t w[4] = {flip ? v.z : v.x, flip ? v.w : v.y, flip ? v.x : v.z, flip ? v.y : v.w};
+                    const int row8 = (i * kRows + sub) & 7;
+                    uint8_t* rowp = kd + i * kRows * 128;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(rowp + (((4 * (ch & 1) + (e ^ (2 * flip))) ^ row8) << 4)) = k_nibbles(w[e], half2_of(f.x), half2_of(f.y));
+                    if (live) copy16_async(smem_u32(mine + 512 * i), i < kPerBlock ? src0 + 32 * i : src1 + 32 * (i - kPerBlock));
+                }
+            } else if (IsV) {
                 // ---- coordinate rows, 64 tokens each: this warp's are 32 cw .. 32 cw + 31
                 uint8_t* vd = smem + C::kOffV + st * C::kVPartBytes + lane * 128;
                 const uint8_t* factors = record + 1024 + 64 * cw;
@@ -700,9 +793,9 @@ __device__ __forceinline__ void convert_role(const ChunkArgs& a, uint8_t* smem, 
     copy_wait_all();
 }
 
-template <int D>
-__global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const ChunkArgs a) {
-    using C = Cx<D>;
+template <int D, bool Q4>
+__global__ void __launch_bounds__(Cx<D, Q4>::kThreads, 1) chunk_q8_kernel(const ChunkArgs a) {
+    using C = Cx<D, Q4>;
     extern __shared__ uint8_t smem_raw[];
     // by an offset: through an integer the compiler would lose that this is shared memory
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
@@ -795,7 +888,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
         int jobs = 0, flags = 0;
         bool ok = true;
         Job job;
-        while (next_job<D, 32, true>(smem, job_full, job_empty, jobs, job)) {
+        while (next_job<C, 32, true>(smem, job_full, job_empty, jobs, job)) {
             const int rows = job.rows - 128 * x;  // rows of the half, if positive
             const int steps = job.s1 - job.s0;
             if (rows <= 0) {
@@ -1053,12 +1146,12 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
     } else if (warp < C::kScoreWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp < C::kConvertWarp + 4)
-            convert_role<D, false>(a, smem, rec_full, rec_empty, k_full, k_empty);
+            convert_role<D, Q4, false>(a, smem, rec_full, rec_empty, k_full, k_empty);
         else
-            convert_role<D, true>(a, smem, rec_full, rec_empty, v_full, v_empty);
+            convert_role<D, Q4, true>(a, smem, rec_full, rec_empty, v_full, v_empty);
     } else if (warp >= C::kScaleWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        scale_role<D>(a, smem, count, job_full, job_empty, rec_full, rec_empty);
+        scale_role<D, Q4>(a, smem, count, job_full, job_empty, rec_full, rec_empty);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         const int x = warp & 1;
@@ -1071,7 +1164,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 int step = 0, it = 0, segs = 0, jobs = 0;
                 bool ok = true;
                 Job job;
-                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job)) {
+                while (ok && next_job<C, 1>(smem, job_full, job_empty, jobs, job)) {
                     const bool mine = job.rows > 128 * x;
                     if (mine) {
                         ok = wait(&q_full[x], segs & 1);
@@ -1120,7 +1213,7 @@ __global__ void __launch_bounds__(Cx<D>::kThreads, 1) chunk_q8_kernel(const Chun
                 uint32_t phase = 0;
                 bool ok = true;
                 Job job;
-                while (ok && next_job<D, 1>(smem, job_full, job_empty, jobs, job)) {
+                while (ok && next_job<C, 1>(smem, job_full, job_empty, jobs, job)) {
                     const bool mine = job.rows > 128 * x;
                     for (int j = job.s0; ok && j < job.s1; ++j) {
 #pragma unroll 1
@@ -1233,12 +1326,13 @@ __global__ void __launch_bounds__(kChunkRows) combine_kernel(const ChunkArgs a, 
 // CTAs of a launch: one per SM (piece lists hold at most kMaxPieces).
 int chunk_q8_ctas() { return device_sm_count() < kMaxPieces ? device_sm_count() : kMaxPieces; }
 
-template <int D>
+template <int D, bool Q4>
 cudaError_t run_chunk(const ChunkArgs& a, cudaStream_t s) {
+    using C = Cx<D, Q4>;
     const int grid = chunk_q8_ctas();
-    cudaError_t e = cudaFuncSetAttribute(chunk_q8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Cx<D>::kSmem));
+    cudaError_t e = cudaFuncSetAttribute(chunk_q8_kernel<D, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(chunk_q8_kernel<D>, dim3(grid), dim3(Cx<D>::kThreads), Cx<D>::kSmem, s, a);
+    e = launch_pdl(chunk_q8_kernel<D, Q4>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a);
     // a unit of three steps is never cut: tables that hold no more leave nothing to join
     if (e != cudaSuccess || a.max_blocks * 16 < 2 * kMinPiece * kChunkStep - kChunkStep + 1) return e;
     return launch_pdl(combine_kernel<D>, dim3(grid, D / 8), dim3(kChunkRows), 0, s, a, grid);
@@ -1252,7 +1346,11 @@ size_t chunk_q8_workspace_bytes(int head_dim) {
 }
 
 cudaError_t launch_chunk_q8(const ChunkArgs& a, cudaStream_t s) {
-    return a.head_dim == 128 ? run_chunk<128>(a, s) : run_chunk<64>(a, s);
+    return a.head_dim == 128 ? run_chunk<128, false>(a, s) : run_chunk<64, false>(a, s);
+}
+
+cudaError_t launch_chunk_q4(const ChunkArgs& a, cudaStream_t s) {
+    return a.head_dim == 128 ? run_chunk<128, true>(a, s) : run_chunk<64, true>(a, s);
 }
 
 }  // namespace pkv

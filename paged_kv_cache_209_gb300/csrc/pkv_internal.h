@@ -206,8 +206,23 @@ struct Q4Args {
     int32_t group;
     int32_t max_query_len;
     float scale;
+    float* partials;         // pieces of cut segments
+    int* counters;           // [batch][kv_heads][4]; zero between calls
+    int32_t num_ctas;
+    int32_t tiles;           // row tiles of 8 that a piece holds
+    int32_t warps_per_unit;  // warps that share a block: 1 or 2
 };
-cudaError_t launch_attend_q4(const Q4Args& a, cudaStream_t s);
+constexpr int kMq4Rows = 32;  // query rows per (sequence, KV head) of that kernel, at most
+// Which variant takes up to `rows` query rows, and on how many CTAs.
+struct Q4Plan {
+    int row_tiles;  // tiles of 8 rows of a warp: 1 or 2
+    int warps_per_unit;
+    int tiles;
+    int num_ctas;
+};
+Q4Plan q4_plan(int head_dim, int rows);
+size_t q4_partials_bytes(int head_dim, const Q4Plan& p);
+cudaError_t launch_mq4(const Q4Args& a, const Q4Plan& p, cudaStream_t s);
 
 // ---------------------------------------------------------------- rotary positions
 struct RotaryAppendArgs {
@@ -332,6 +347,7 @@ struct ChunkArgs {
 };
 size_t chunk_q8_workspace_bytes(int head_dim);
 cudaError_t launch_chunk_q8(const ChunkArgs& a, cudaStream_t s);
+cudaError_t launch_chunk_q4(const ChunkArgs& a, cudaStream_t s);  // k_codes: the records of a 4-bit cache
 
 // ---------------------------------------------------------------- reading the cache back
 struct GatherArgs {

@@ -1,84 +1,646 @@
-// Attention over the 4-bit cache (pkv_decode_attention_q4, pkv_multiquery_attention_q4 in
-// include/pkv.h).
+// Attention over the 4-bit cache, few query rows per (sequence, KV head)
+// (pkv_decode_attention_q4, and pkv_multiquery_attention_q4 up to kMq4Rows rows; more
+// rows run in tiles, pkv_chunk_q8.cu).
 //
-// One warp per query row and head: an online softmax over the row's tokens, a lane
-// holding D / 32 dimensions.
+// Work: (sequence, KV head, block) units split over the CTAs by cost (pkv_schedule.cuh);
+// a segment that a cut divides leaves pieces, which the last CTA to finish one merges.
+// Bound by HBM: a unit is one record of 16 D + 128 bytes, read once.
+//
+// A record is contiguous, so a producer warp fetches each with one bulk copy into a ring
+// of stages of two records (32 tokens); the query rows of a segment come the same way,
+// ahead of its first records. Four consumer warps take stages in turn. Per stage, with
+// the query rows of a (sequence, KV head) in tiles of 8:
+//     S^T[16 tokens][8 rows] = K[16][D] Q^T[D][8]     (mma m16n8k16, f16 -> fp32)
+//     x = log2(e) scale S k_p,  P' = 2^(x - m) v_p,  l += 2^(x - m)
+//     O^T[D][8] += V^T[D][16] P'^T[16][8]
+// k_p and v_p are the tokens' scales; m is a base, not a maximum, moved only where a P'
+// would leave f16 (below).
+//
+// Codes become f16 by one mask: a nibble n (code + 8) alone in the low bits of an f16 is
+// the subnormal n 2^-24, four bits higher 16 n 2^-24, which the tensor cores take
+// exactly. For K the 8 stays: S = 2^24 S' - 8 sum(q), q's halves over 16 where the codes
+// are 16-fold. For V it goes, by one exact subtraction per pair, because O runs over the
+// whole context, where the sum of the eights would take the low bits of the rest. q rows
+// are scaled by a power of two to a largest magnitude of 2^14 .. 2^15; sums are fp32.
 #include <math.h>
+#include <mutex>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q4.cuh"
+#include "pkv_schedule.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kConsumers = 4;
+constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kIssueLanes = 8;  // stages whose copies are issued together
+constexpr int kQSlots = 2;      // segments whose query rows are on their way
+// A CTA gets at least about this many blocks: fewer CTAs then, and fewer pieces to merge.
+constexpr int kLeastBlocks = 8;
+// Cost of a segment shorter than kShortBlocks beside its blocks, in blocks.
+constexpr int kSegmentCost = 6, kShortBlocks = 256;
 
-__device__ __forceinline__ float ninf() { return __int_as_float(0xff800000); }
+// The base m of a row: where some P' = 2^(x - m) v would leave f16 it moves to the largest
+// x + log2 |v| less kHeadroom, so that what is rounded to f16 lies high in its range for
+// the tokens that make up the output, whatever the scales. A V scale counts as
+// kTinyScale at least, so that l stays below 2^(16 + 96) times the tokens.
+constexpr float kHeadroom = 8.f;
+constexpr float kMost = 65504.f;                 // the largest f16
+constexpr float kTinyScale = 1.2621774e-29f;     // 2^-96
+constexpr float kUnset = -3.0e38f;               // base of a row that has seen no token
 
+// D: head_dim, R: tiles of 8 query rows of a warp.
+template <int D, int R>
+struct M4 {
+    static constexpr int kRecord = q4_record_bytes(D);
+    static constexpr int kStageBytes = 2 * kRecord;
+    static constexpr int kStages = D == 128 ? 8 : 16;
+    static constexpr int kRows = 8 * R;                       // query rows of a warp
+    static constexpr int kStateFloats = kRows * (D + 2);      // a warp's O, m and l
+    static constexpr int kOffBars = kStages * kStageBytes;    // full, empty per stage; q_full, q_empty per slot; piece
+    static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 1;
+    static constexpr int kOffFlags = kOffBars + (kNumBars + 1) / 2 * 16;  // per stage: which of its blocks exist; abort
+    static constexpr int kOffState = (kOffFlags + (kStages + 1) * 4 + 15) / 16 * 16;  // two buffers, alternating between pieces
+    static constexpr int kOffQ = kOffState + 2 * kConsumers * kStateFloats * 4;
+    static size_t smem_bytes(int warps_per_unit, int batch) {
+        return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + 3 * static_cast<size_t>(batch) * 4;
+    }
+    static_assert(kOffBars % 16 == 0 && kOffQ % 16 == 0, "alignment");
+};
+
+// Bulk copy of `bytes` contiguous bytes (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float f16x2_sum(uint32_t h) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return f.x + f.y;
+}
+// Two nibbles, 0 .. 15 (`bits` = 0x000f000f) or 16-fold (0x00f000f0), as the f16s code 2^-24 (2^-20).
+__device__ __forceinline__ uint32_t v_codes(uint32_t w, uint32_t bits, uint32_t eights) {
+    const uint32_t h = w & bits;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&eights));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Workspace of one piece: per row tile O [8][D], then per consumer warp (each merges D / 4
+// dimensions on its own) the rows' m [8] and l [8].
+__host__ __device__ constexpr int piece_floats(int d) { return 8 * d + 4 * 16; }
+__device__ __forceinline__ float* piece_of(const Q4Args& a, int d, long long cta, int slot, int tile) {
+    return a.partials + ((cta * 2 + slot) * a.tiles + tile) * static_cast<long long>(piece_floats(d));
+}
+
+// D / 16 values of row `rr` of a segment, dimensions d0 .., as bf16.
 template <int D>
-__global__ void __launch_bounds__(128) attend_q4_kernel(const Q4Args a) {
-    constexpr int kPer = D / 32;
+__device__ __forceinline__ void write_part(const Q4Args& a, int q0, int head, int rr, int d0, const float (&o)[D / 16], float l) {
+    const int t = rr / a.group;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.out) +
+                         ((static_cast<long long>(q0) + t) * a.q_heads + head * a.group + (rr - t * a.group)) * D + d0;
+#pragma unroll
+    for (int e = 0; e < D / 16; e += 4)
+        *reinterpret_cast<uint2*>(row + e) = make_uint2(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv));
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4Args a) {
+    using C = M4<D, R>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 127u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
+    uint64_t* empty = full + C::kStages;
+    uint64_t* q_full = empty + C::kStages;
+    uint64_t* q_empty = q_full + kQSlots;
+    uint64_t* piece_bar = q_empty + kQSlots;  // every consumer warp has published its state of the piece
+    int* present = reinterpret_cast<int*>(smem + C::kOffFlags);
+    volatile int* abort_flag = present + C::kStages;
+    float* state = reinterpret_cast<float*>(smem + C::kOffState);
+    const int W = a.warps_per_unit, UL = kConsumers / W;  // unit lanes: stages in work at a time
+    const int q_bytes = C::kRows * W * D * 2;
+    uint8_t* q_rows = smem + C::kOffQ;
+    int32_t* s_pre = reinterpret_cast<int32_t*>(q_rows + kQSlots * q_bytes);  // blocks, cost up to and with each sequence; length
+    int32_t* s_cost = s_pre + a.batch;
+    int32_t* s_len = s_cost + a.batch;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], W);
+        }
+        for (int s = 0; s < kQSlots; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], kConsumers);
+        }
+        mbar_init(piece_bar, kConsumers);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
     grid_dependency_wait();
     allow_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t items = static_cast<int64_t>(a.batch) * a.max_query_len * a.q_heads;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5); x < items; x += static_cast<int64_t>(gridDim.x) * 4) {
-        const int h = static_cast<int>(x % a.q_heads);
-        const int t = static_cast<int>(x / a.q_heads % a.max_query_len);
-        const int i = static_cast<int>(x / a.q_heads / a.max_query_len);
-        const int64_t n = a.lens[i];
-        const int64_t q0 = a.qstart ? a.qstart[i] : i, nq = a.qstart ? a.qstart[i + 1] - q0 : 1;
-        if (n < 0 || n > static_cast<int64_t>(a.max_blocks) * 16 || q0 < 0 || nq < 0 || (a.qstart && nq > n) || nq > a.max_query_len) {
-            if (t == 0 && h == 0 && lane == 0) atomicOr(a.status, PKV_DEVERR_RANGE);
-            continue;
+    const int cap = a.max_blocks * 16;
+    for (int i = threadIdx.x; i < a.batch; i += kThreads) {
+        int n = a.lens[i];
+        bool bad = n < 0 || n > cap;
+        n = n < 0 ? 0 : (n > cap ? cap : n);
+        // without query offsets: one query per sequence (row i), none for an empty context
+        const int q0 = a.qstart != nullptr ? a.qstart[i] : i;
+        long long nq = a.qstart != nullptr ? static_cast<long long>(a.qstart[i + 1]) - q0 : (n > 0 ? 1 : 0);
+        if (q0 < 0 || nq < 0 || nq > n || nq > a.max_query_len) {
+            bad = true;
+            nq = 0;
         }
-        if (t >= nq) continue;
-        const int head = h / a.group;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((q0 + t) * a.q_heads + h) * D + lane * kPer;
-        float qv[kPer], o[kPer] = {}, m = ninf(), l = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) qv[e] = __bfloat162float(q[e]) * a.scale * kLog2e;
-        const int64_t last = a.qstart ? n - nq + t : n - 1;
-        for (int64_t p = 0; p <= last; ++p) {
-            const int32_t id = a.tables[static_cast<int64_t>(i) * a.max_blocks + (p >> 4)];
-            if (id < 0 || id >= a.num_blocks) {
-                if (lane == 0) atomicOr(a.status, PKV_DEVERR_RANGE);
-                continue;
-            }
-            const uint8_t* rec = static_cast<const uint8_t*>(a.cache) + (static_cast<int64_t>(id) * a.kv_heads + head) * q4_record_bytes(D);
-            const int s = static_cast<int>(p & 15);
-            const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
-            float dot = 0.f, v[kPer];
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int d = lane * kPer + e, w = d & 7, nib = (w >> 1) + 4 * (w & 1);
-                dot += qv[e] * static_cast<float>(((rec[s * (D / 2) + (d >> 3) * 4 + (nib >> 1)] >> (4 * (nib & 1))) & 15) - 8);
-                v[e] = static_cast<float>(((rec[q4_v_offset(D) + q4_v_byte(d >> 3, w >> 1, s)] >> (4 * (w & 1))) & 15) - 8);
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-            const float x2 = dot * scales[s], to = fmaxf(m, x2);
-            const float keep = m == ninf() ? 0.f : ex2(m - to), e2 = ex2(x2 - to);
-            l = l * keep + e2;
-            m = to;
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) o[e] = o[e] * keep + e2 * (v[e] * scales[16 + s]);
+        if (bad) {
+            if (blockIdx.x == 0) atomicOr(a.status, PKV_DEVERR_RANGE);
+            if (a.qstart != nullptr) nq = 0;  // a malformed sequence has no queries
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((q0 + t) * a.q_heads + h) * D + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
+        s_len[i] = n;
+        s_pre[i] = nq > 0 ? (n + 15) >> 4 : 0;
     }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int blocks = 0, cost = 0;
+        for (int base = 0; base < a.batch; base += 32) {
+            int x = base + lane < a.batch ? s_pre[base + lane] : 0;
+            int y = x > 0 && x < kShortBlocks ? x + kSegmentCost : x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x1 = __shfl_up_sync(0xffffffffu, x, o), y1 = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) x += x1, y += y1;
+            }
+            if (base + lane < a.batch) {
+                s_pre[base + lane] = x + blocks;
+                s_cost[base + lane] = y + cost;
+            }
+            blocks += __shfl_sync(0xffffffffu, x, 31);
+            cost += __shfl_sync(0xffffffffu, y, 31);
+        }
+    }
+    __syncthreads();
+    if (a.qstart == nullptr) {
+        // one query per sequence: an empty context gives a zero row
+        const int vecs = a.q_heads * D / 8;
+        for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
+            if (s_len[i] != 0) continue;
+            uint4* o = static_cast<uint4*>(a.out) + static_cast<long long>(i) * vecs;
+            for (int e = threadIdx.x; e < vecs; e += kThreads) o[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    const long long U = static_cast<long long>(a.kv_heads) * s_pre[a.batch - 1];
+    const long long cta = blockIdx.x;
+    const long long wanted = U / kLeastBlocks;
+    CostSplit split;
+    split.init(s_pre, s_cost, a.batch, a.kv_heads, 1 + kSegmentCost, wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
+    if (U == 0 || cta >= split.C) return;
+    const long long ua = split.start(cta), ub = split.start(cta + 1);
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------ producer
+        const uint64_t policy = l2_evict_first_policy();
+        const uint8_t* cache = static_cast<const uint8_t*>(a.cache);
+        Walker wk;
+        wk.init(s_pre, a.batch, a.kv_heads, ua, ub);
+        uint32_t k = 0;  // stages issued
+        uint32_t pieces = 0;
+        Piece pc;
+        bool ok = true;
+        while (ok && wk.next(pc)) {
+            const int32_t* trow = a.tables + static_cast<long long>(pc.seq) * a.max_blocks + pc.blk_from;
+            const int blocks = pc.blk_to - pc.blk_from;
+            int cur = lane < blocks ? __ldg(trow + lane) : 0;
+            {  // the segment's query rows: G of each query are contiguous
+                const int slot = pieces % kQSlots;
+                if (lane == 0 && pieces >= kQSlots) ok = mbar_wait(&q_empty[slot], (pieces / kQSlots - 1) & 1, a.status, abort_flag);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const int q0 = a.qstart != nullptr ? a.qstart[pc.seq] : pc.seq;
+                const int nq = a.qstart != nullptr ? a.qstart[pc.seq + 1] - q0 : 1;
+                if (lane == 0) mbar_arrive_expect_tx(&q_full[slot], nq * G * D * 2);
+                __syncwarp();
+                if (lane < nq)
+                    bulk_load(q_rows + slot * q_bytes + lane * G * D * 2,
+                              static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<long long>(q0) + lane) * a.q_heads + pc.head * G) * D, G * D * 2,
+                              &q_full[slot], l2_evict_last_policy());
+                ++pieces;
+            }
+            for (int b0 = 0; ok && b0 < blocks; b0 += 32) {
+                const int nidx = b0 + 32 + lane;
+                const int nxt = nidx < blocks ? __ldg(trow + nidx) : 0;
+                const int stages = (min(32, blocks - b0) + 1) / 2;
+                // in order, as many stages at once as are free from the first on, one a lane
+                for (int e0 = 0; e0 < stages;) {
+                    const int e = e0 + lane;
+                    const uint32_t kk = k + lane;
+                    const int s = static_cast<int>(kk % C::kStages);
+                    const uint32_t par = ((kk / C::kStages) & 1) ^ 1u;
+                    const bool probe = lane < kIssueLanes && e < stages && mbar_test_wait(&empty[s], par);
+                    int n = __ffs(~__ballot_sync(0xffffffffu, probe)) - 1;
+                    if (n == 0) {
+                        bool waited = true;
+                        if (lane == 0) waited = mbar_wait(&empty[s], par, a.status, abort_flag);
+                        if (!__shfl_sync(0xffffffffu, waited, 0)) {  // nothing of this batch was issued
+                            ok = false;
+                            break;
+                        }
+                        n = 1;
+                    }
+                    const int id0 = __shfl_sync(0xffffffffu, cur, 2 * e & 31), id1 = __shfl_sync(0xffffffffu, cur, 2 * e + 1 & 31);
+                    if (lane < n) {
+                        const bool in1 = b0 + 2 * e + 1 < blocks;
+                        const bool load0 = id0 >= 0 && id0 < a.num_blocks, load1 = in1 && id1 >= 0 && id1 < a.num_blocks;
+                        if (!load0 || (in1 && !load1)) atomicOr(a.status, PKV_DEVERR_RANGE);
+                        present[s] = (load0 ? 1 : 0) | (load1 ? 2 : 0);
+                        if (load0 || load1)
+                            mbar_arrive_expect_tx(&full[s], (load0 ? C::kRecord : 0) + (load1 ? C::kRecord : 0));
+                        else
+                            mbar_arrive(&full[s]);
+                        uint8_t* st = smem + s * C::kStageBytes;
+                        if (load0) bulk_load(st, cache + (static_cast<long long>(id0) * a.kv_heads + pc.head) * C::kRecord, C::kRecord, &full[s], policy);
+                        if (load1)
+                            bulk_load(st + C::kRecord, cache + (static_cast<long long>(id1) * a.kv_heads + pc.head) * C::kRecord, C::kRecord, &full[s], policy);
+                    }
+                    __syncwarp();
+                    k += n;
+                    e0 += n;
+                }
+                cur = nxt;
+            }
+        }
+        if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies still in flight
+            for (uint32_t u = k > C::kStages ? k - C::kStages : 0; u < k; ++u)
+                mbar_wait(&full[u % C::kStages], (u / C::kStages) & 1, a.status, nullptr);
+            for (uint32_t u = pieces > kQSlots ? pieces - kQSlots : 0; u < pieces; ++u)
+                mbar_wait(&q_full[u % kQSlots], (u / kQSlots) & 1, a.status, nullptr);
+        }
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int rg = warp % W;  // this warp's query rows: 8 R rg ..
+    const int ul = warp / W;
+    const int gid = lane >> 2, tig = lane & 3;
+    const float scale_log2 = a.scale * kLog2e;
+    Walker wk;
+    wk.init(s_pre, a.batch, a.kv_heads, ua, ub);
+    uint32_t k = 0, pieces = 0;
+    Piece pc, pending[2];
+    int npending = 0;
+    while (wk.next(pc)) {
+        const int n_ctx = s_len[pc.seq];
+        const int q0 = a.qstart != nullptr ? a.qstart[pc.seq] : pc.seq;
+        const int nq = a.qstart != nullptr ? a.qstart[pc.seq + 1] - q0 : 1;
+        const int rows = nq * G;
+        const bool active = rg * C::kRows < rows;
+        const int slot = pieces % kQSlots;
+        if (!mbar_wait(&q_full[slot], (pieces / kQSlots) & 1, a.status, abort_flag)) return;
+        uint32_t qf[R][D / 16][2];
+        float cf[R][2], kb[R][2];  // per column: the power of two and the scale; eight times the row's sum
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int rr = rg * C::kRows + r * 8 + gid;
+            const uint4* row = reinterpret_cast<const uint4*>(q_rows + slot * q_bytes + rr * (D * 2) + tig * (D / 2));
+            uint4 w[D / 32];
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                w[c] = rr < rows ? row[c] : make_uint4(0u, 0u, 0u, 0u);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu), __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu)));
+            }
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = max(static_cast<int>(max(top >> 16, top & 0xffffu) >> 7) - 127 - 14, -126);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            float sum = 0.f;  // of the operands as rounded
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t lo = h ? w[c].z : w[c].x, hi = h ? w[c].w : w[c].y;
+                    qf[r][2 * c + h][0] = pack_f16x2(bf16lo_to_f32(lo) * down, bf16hi_to_f32(lo) * down);
+                    qf[r][2 * c + h][1] = pack_f16x2(bf16lo_to_f32(hi) * down * 0.0625f, bf16hi_to_f32(hi) * down * 0.0625f);
+                    sum += f16x2_sum(qf[r][2 * c + h][0]) + 16.f * f16x2_sum(qf[r][2 * c + h][1]);
+                }
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            // S^T columns 2 tig, 2 tig + 1 are the rows of lanes 8 tig and 8 tig + 4
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                cf[r][c] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * c) * scale_log2;
+                kb[r][c] = -8.f * __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * c);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_empty[slot]);
+        ++pieces;
+        // the last token each of the lane's columns sees
+        int lim[R][2], least = 0x7fffffff;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int rr = rg * C::kRows + r * 8 + 2 * tig + c;
+                lim[r][c] = rr < rows ? n_ctx - nq + rr / G : -1;
+                if (rr < rows) least = min(least, lim[r][c]);
+            }
+        least = __reduce_min_sync(0xffffffffu, least);
+        float m[R][2], l[R][2], o[R][D / 16][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r][0] = m[r][1] = kUnset;
+            l[r][0] = l[r][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
+        }
+        const uint32_t k_end = k + (pc.blk_to - pc.blk_from + 1) / 2;
+        const int skip = (ul - static_cast<int>(k & (UL - 1))) & (UL - 1);
+        k += skip;
+        for (int blk = pc.blk_from + 2 * skip; blk < pc.blk_to; blk += 2 * UL, k += UL) {
+            const int s = static_cast<int>(k % C::kStages);
+            if (!mbar_wait(&full[s], (k / C::kStages) & 1, a.status, abort_flag)) return;
+            const int there = present[s];
+            if (active && there) {
+                const uint8_t* st = smem + s * C::kStageBytes;
+                // every token of the stage exists and every row sees it
+                const bool whole = there == 3 && blk * 16 + 31 <= least;
+                float x[R][8];  // [2 tokens gid, gid + 8 of each block][2 columns]
+                float sv[4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint8_t* rec = st + b * C::kRecord;
+                    uint32_t wa[D / 32], wb[D / 32];
+                    if (D == 128) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(rec + gid * 64 + tig * 16), v = *reinterpret_cast<const uint4*>(rec + (gid + 8) * 64 + tig * 16);
+                        wa[0] = u.x, wa[1] = u.y, wa[D / 32 - 2] = u.z, wa[D / 32 - 1] = u.w;
+                        wb[0] = v.x, wb[1] = v.y, wb[D / 32 - 2] = v.z, wb[D / 32 - 1] = v.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(rec + gid * 32 + tig * 8), v = *reinterpret_cast<const uint2*>(rec + (gid + 8) * 32 + tig * 8);
+                        wa[0] = u.x, wa[1] = u.y;
+                        wb[0] = v.x, wb[1] = v.y;
+                    }
+                    float sc[R][2][4] = {};
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t u = h ? wa[c] >> 8 : wa[c], v = h ? wb[c] >> 8 : wb[c];
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                mma_f16_16816(sc[r][h], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
+                                              qf[r][2 * c + h][1]);
+                        }
+                    }
+                    const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
+                    const float ka = scales[gid], kc = scales[gid + 8];
+                    sv[2 * b] = scales[16 + gid];
+                    sv[2 * b + 1] = scales[24 + gid];
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[r][4 * b + e] = fmaf(sc[r][0][e] + sc[r][1][e], 16777216.f, kb[r][e & 1]) * ((e & 2 ? kc : ka) * cf[r][e & 1]);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = blk * 16 + 16 * (i >> 1) + 8 * (i & 1) + gid;
+                        const bool in = (there >> (i >> 1) & 1) != 0;
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) x[r][2 * i + c] = in && p <= lim[r][c] ? x[r][2 * i + c] : __int_as_float(0xff800000);
+                    }
+                }
+                float size[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) size[i] = fmaxf(fabsf(sv[i]), kTinyScale);
+                float e[R][8];
+                float most = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        e[r][i] = ex2(x[r][i] - m[r][i & 1]);
+                        most = fmaxf(most, e[r][i] * size[i >> 1]);
+                    }
+                if (__any_sync(0xffffffffu, most > kMost)) {
+                    float lg[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lg[i] = fminf(__log2f(size[i]), 128.f);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float j = fmaxf(fmaxf(x[r][c] + lg[0], x[r][2 + c] + lg[1]), fmaxf(x[r][4 + c] + lg[2], x[r][6 + c] + lg[3]));
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) j = fmaxf(j, __shfl_xor_sync(0xffffffffu, j, off));
+                            const float to = fmaxf(m[r][c], j - kHeadroom), al = ex2(m[r][c] - to);
+                            m[r][c] = to;
+                            l[r][c] *= al;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                o[r][i][c] *= al;
+                                o[r][i][2 + c] *= al;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) e[r][i + c] = ex2(x[r][i + c] - to);
+                        }
+                }
+                uint32_t p[R][2][2];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) l[r][i & 1] += e[r][i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
+                        if (!whole) {  // what a row does not see has no weight, whatever its scale
+                            w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
+                            w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
+                        }
+                        p[r][i >> 1][i & 1] = movmatrix_trans(pack_f16x2(w0, w1));
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint8_t* v = st + b * C::kRecord + q4_v_offset(D) + gid * 64 + tig * 16;
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(v + h * 512);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a0 = v_codes(w[j], 0x000f000fu, 0x00080008u), a1 = v_codes(w[j], 0x00f000f0u, 0x00800080u);
+                            const uint32_t a2 = v_codes(w[j] >> 8, 0x000f000fu, 0x00080008u), a3 = v_codes(w[j] >> 8, 0x00f000f0u, 0x00800080u);
+#pragma unroll
+                            for (int r = 0; r < R; ++r) mma_f16_16816(o[r][4 * h + j], a0, a1, a2, a3, p[r][b][0], p[r][b][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+        }
+        k = k_end;
+        // ---- end of the piece: this warp's state into shared memory (O over 2^-24)
+        float* buf = state + (pieces & 1) * (kConsumers * C::kStateFloats);
+        float* own = buf + warp * C::kStateFloats;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], off);
+                const int row = r * 8 + 2 * tig + c;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    *reinterpret_cast<float2*>(own + row * D + 8 * (gid + 8 * (i >> 2)) + 2 * (i & 3)) =
+                        make_float2(o[r][i][c] * 16777216.f, o[r][i][2 + c] * 1048576.f);
+                if (gid == 0) {
+                    own[C::kRows * D + row] = m[r][c];
+                    own[C::kRows * (D + 1) + row] = l[r][c];
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_bar);
+        if (!mbar_wait(piece_bar, (pieces - 1) & 1, a.status, abort_flag)) return;
+        // ---- all unit lanes together; a warp takes D / 4 dimensions, a lane a quarter of them of one row of a tile
+        const int tiles = (rows + 7) / 8;
+        constexpr int kPer = D / 16;
+        const int row8 = lane >> 2, d0 = warp * (D / 4) + (lane & 3) * kPer;
+        for (int tile = 0; tile < tiles; ++tile) {
+            const int row = tile % R * 8 + row8, group = tile / R;  // among the rows of that group's warps
+            float M = kUnset, L = 0.f, O[kPer] = {};
+            for (int u = 0; u < UL; ++u) M = fmaxf(M, buf[(u * W + group) * C::kStateFloats + C::kRows * D + row]);
+            for (int u = 0; u < UL; ++u) {
+                const float* su = buf + (u * W + group) * C::kStateFloats;
+                const float wu = ex2(su[C::kRows * D + row] - M);
+                L += wu * su[C::kRows * (D + 1) + row];
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(su + row * D + d0 + e);
+                    O[e] += wu * v.x, O[e + 1] += wu * v.y, O[e + 2] += wu * v.z, O[e + 3] += wu * v.w;
+                }
+            }
+            const int rr = tile * 8 + row8;
+            if (pc.complete) {
+                if (rr < rows) write_part<D>(a, q0, pc.head, rr, d0, O, L);
+            } else {
+                float* sl = piece_of(a, D, cta, pc.first ? 0 : 1, tile);
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) *reinterpret_cast<float4*>(sl + row8 * D + d0 + e) = make_float4(O[e], O[e + 1], O[e + 2], O[e + 3]);
+                if ((lane & 3) == 0) {
+                    sl[8 * D + warp * 16 + row8] = M;
+                    sl[8 * D + warp * 16 + 8 + row8] = L;
+                }
+            }
+        }
+        if (!pc.complete) pending[npending++] = pc;
+    }
+    // ---- announce this warp's share of the cut pieces; the warp that completes a count merges them
+    if (npending == 0) return;
+    __threadfence();
+    __syncwarp();
+    for (int i = 0; i < npending; ++i) {
+        const Piece& pp = pending[i];
+        const long long c0 = split.cta_of(pp.seg_start), c1 = split.cta_of(pp.seg_start + pp.seg_len - 1);
+        const int np = split.pieces(c0, c1);
+        int* counter = a.counters + (static_cast<long long>(pp.seq) * a.kv_heads + pp.head) * kConsumers + warp;
+        int old = 0;
+        if (lane == 0) old = atomicAdd(counter, 1);
+        old = __shfl_sync(0xffffffffu, old, 0);
+        if (old != np - 1) continue;
+        __threadfence();
+        const int slot0 = pp.seg_start == split.start(c0) ? 0 : 1;
+        const int q0 = a.qstart != nullptr ? a.qstart[pp.seq] : pp.seq;
+        const int rows = (a.qstart != nullptr ? a.qstart[pp.seq + 1] - q0 : 1) * G;
+        constexpr int kPer = D / 16;
+        const int row8 = lane >> 2, d0 = warp * (D / 4) + (lane & 3) * kPer;
+        for (int tile = 0; tile * 8 < rows; ++tile) {
+            float M = kUnset, L = 0.f, O[kPer] = {};
+#pragma unroll 4
+            for (int p = 0; p < np; ++p) {
+                const float* sl = piece_of(a, D, split.piece_cta(c0, p), p == 0 ? slot0 : 0, tile);
+                const float mp = __ldcg(sl + 8 * D + warp * 16 + row8), lp = __ldcg(sl + 8 * D + warp * 16 + 8 + row8);
+                const float to = fmaxf(M, mp), keep = ex2(M - to), w = ex2(mp - to);
+                M = to;
+                L = L * keep + w * lp;
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + row8 * D + d0 + e));
+                    O[e] = O[e] * keep + w * v.x, O[e + 1] = O[e + 1] * keep + w * v.y;
+                    O[e + 2] = O[e + 2] * keep + w * v.z, O[e + 3] = O[e + 3] * keep + w * v.w;
+                }
+            }
+            if (tile * 8 + row8 < rows) write_part<D>(a, q0, pp.head, tile * 8 + row8, d0, O, L);
+        }
+        if (lane == 0) *counter = 0;
+    }
+}
+
+template <int D, int R>
+cudaError_t run_mq4(const Q4Args& a, cudaStream_t s) {
+    using C = M4<D, R>;
+    const size_t smem = C::smem_bytes(a.warps_per_unit, a.batch);
+    const cudaError_t e = cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(mq4_kernel<D, R>, dim3(a.num_ctas), dim3(kThreads), smem, s, a);
+}
+
+// Resident CTAs of an SM, at the largest launch.
+template <int D, int R>
+int resident(int warps_per_unit) {
+    const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, kMaxBatchPerLaunch);
+    int n = 0;
+    cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mq4_kernel<D, R>, kThreads, smem) != cudaSuccess || n < 1) n = 1;
+    return n;
 }
 
 }  // namespace
 
-cudaError_t launch_attend_q4(const Q4Args& a, cudaStream_t s) {
-    const int64_t items = static_cast<int64_t>(a.batch) * a.max_query_len * a.q_heads;
-    const int64_t want = (items + 3) / 4, most = static_cast<int64_t>(device_sm_count()) * 64;
-    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-    return a.head_dim == 128 ? launch_pdl(attend_q4_kernel<128>, grid, dim3(128), 0, s, a) : launch_pdl(attend_q4_kernel<64>, grid, dim3(128), 0, s, a);
+Q4Plan q4_plan(int head_dim, int rows) {
+    Q4Plan p;
+    p.tiles = (rows + 7) / 8;
+    p.row_tiles = p.tiles == 1 ? 1 : 2;
+    p.warps_per_unit = p.tiles <= 2 ? 1 : 2;
+    p.tiles = p.row_tiles * p.warps_per_unit;
+    static std::mutex mu;
+    static int cache[2][3][64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) dev = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int& per_sm = cache[head_dim == 128][p.row_tiles + p.warps_per_unit - 2][dev];
+    if (per_sm == 0) {
+        if (head_dim == 128)
+            per_sm = p.row_tiles == 1 ? resident<128, 1>(1) : resident<128, 2>(p.warps_per_unit);
+        else
+            per_sm = p.row_tiles == 1 ? resident<64, 1>(1) : resident<64, 2>(p.warps_per_unit);
+    }
+    p.num_ctas = per_sm * device_sm_count();
+    return p;
+}
+
+size_t q4_partials_bytes(int head_dim, const Q4Plan& p) {
+    return static_cast<size_t>(p.num_ctas) * 2 * p.tiles * piece_floats(head_dim) * sizeof(float);
+}
+
+cudaError_t launch_mq4(const Q4Args& a, const Q4Plan& p, cudaStream_t s) {
+    if (a.head_dim == 128) return p.row_tiles == 1 ? run_mq4<128, 1>(a, s) : run_mq4<128, 2>(a, s);
+    return p.row_tiles == 1 ? run_mq4<64, 1>(a, s) : run_mq4<64, 2>(a, s);
 }
 
 }  // namespace pkv
