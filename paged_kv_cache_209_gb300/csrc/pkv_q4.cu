@@ -37,34 +37,58 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kIssueLanes = 8;  // stages whose copies are issued together
-constexpr int kQSlots = 2;      // segments whose query rows are on their way
 // A CTA gets at least about this many blocks: fewer CTAs then, and fewer pieces to merge.
 constexpr int kLeastBlocks = 8;
 // Cost of a segment shorter than kShortBlocks beside its blocks, in blocks.
 constexpr int kSegmentCost = 6, kShortBlocks = 256;
+// (so no CTA's range is empty, and a segment's pieces lie in consecutive CTAs)
+static_assert(kLeastBlocks >= 1 + kSegmentCost, "a range covers the dearest unit");
 
 // The base m of a row: where some P' = 2^(x - m) v would leave f16 it moves to the largest
 // x + log2 |v| less kHeadroom, so that what is rounded to f16 lies high in its range for
 // the tokens that make up the output, whatever the scales. A V scale counts as
 // kTinyScale at least, so that l stays below 2^(16 + 96) times the tokens.
 constexpr float kHeadroom = 8.f;
-constexpr float kMost = 65504.f;                 // the largest f16
+constexpr float kMostSum = 5.1922969e33f;        // 2^112
 constexpr float kTinyScale = 1.2621774e-29f;     // 2^-96
+// Stages (32 tokens) whose eights are summed in O before they are taken out again.
+constexpr int kFold = 8;
 constexpr float kUnset = -3.0e38f;               // base of a row that has seen no token
+
+// A piece of a segment, as the producer lays it out for the consumers.
+struct __align__(16) Piece4 {
+    int seq, head, q0, rows;        // rows: query rows of the segment, (query, head) pairs
+    int n, nq, blk_from, blk_to;    // tokens and queries of the sequence; the piece's blocks (blk_to 0: no more pieces)
+    int cut;                        // 0: the whole segment; else the workspace slot of the piece, plus 1
+    int first_cta, pieces, slot0;   // (cut ones, at the end) where the segment's pieces lie: that CTA's slot slot0, then slot 0
+                                    // of the following CTAs
+};
+static_assert(sizeof(Piece4) == 48, "layout");
 
 // D: head_dim, R: tiles of 8 query rows of a warp.
 template <int D, int R>
 struct M4 {
     static constexpr int kRecord = q4_record_bytes(D);
     static constexpr int kStageBytes = 2 * kRecord;
-    static constexpr int kStages = D == 128 ? 8 : 16;
+#ifndef MQ4_STAGES
+#define MQ4_STAGES 8
+#endif
+#ifndef MQ4_BATCH
+#define MQ4_BATCH kMaxBatchPerLaunch
+#endif
+#ifndef MQ4_CTAS
+#define MQ4_CTAS 3
+#endif
+    static constexpr int kStages = D == 128 ? MQ4_STAGES : 16;
     static constexpr int kRows = 8 * R;                       // query rows of a warp
+    static constexpr int kQSlots = R == 1 ? 4 : 2;            // segments whose query rows are in work or on their way
     static constexpr int kStateFloats = kRows * (D + 2);      // a warp's O, m and l
-    static constexpr int kOffBars = kStages * kStageBytes;    // full, empty per stage; q_full, q_empty per slot; piece
-    static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 1;
+    static constexpr int kOffBars = kStages * kStageBytes;    // full, empty per stage; q_full, q_empty per slot; state_full, state_empty
+    static constexpr int kNumBars = 2 * kStages + 2 * kQSlots + 2;
     static constexpr int kOffFlags = kOffBars + (kNumBars + 1) / 2 * 16;  // per stage: which of its blocks exist; abort
-    static constexpr int kOffState = (kOffFlags + (kStages + 1) * 4 + 15) / 16 * 16;  // two buffers, alternating between pieces
-    static constexpr int kOffQ = kOffState + 2 * kConsumers * kStateFloats * 4;
+    static constexpr int kOffState = (kOffFlags + (kStages + 1) * 4 + 15) / 16 * 16;
+    static constexpr int kOffPieces = kOffState + kConsumers * kStateFloats * 4;  // per slot; then the cut ones, and their number
+    static constexpr int kOffQ = kOffPieces + (kQSlots + 2) * sizeof(Piece4) + 16;
     static size_t smem_bytes(int warps_per_unit, int batch) {
         return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + 3 * static_cast<size_t>(batch) * 4;
     }
@@ -86,18 +110,26 @@ __device__ __forceinline__ float f16x2_sum(uint32_t h) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return f.x + f.y;
 }
-// Two nibbles, 0 .. 15 (`bits` = 0x000f000f) or 16-fold (0x00f000f0), as the f16s code 2^-24 (2^-20).
-__device__ __forceinline__ uint32_t v_codes(uint32_t w, uint32_t bits, uint32_t eights) {
-    const uint32_t h = w & bits;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&eights));
-    return *reinterpret_cast<const uint32_t*>(&r);
+// D = A B + C for f16 A (16 x 16) and B (16 x 8), C and D apart.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                             float c0, float c1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// Larger of the halves' magnitudes; a NaN stays.
+__device__ __forceinline__ uint32_t largest_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+    return r;
 }
 
 // Workspace of one piece: per row tile O [8][D], then per consumer warp (each merges D / 4
 // dimensions on its own) the rows' m [8] and l [8].
 __host__ __device__ constexpr int piece_floats(int d) { return 8 * d + 4 * 16; }
-__device__ __forceinline__ float* piece_of(const Q4Args& a, int d, long long cta, int slot, int tile) {
-    return a.partials + ((cta * 2 + slot) * a.tiles + tile) * static_cast<long long>(piece_floats(d));
+__device__ __forceinline__ float* piece_of(const Q4Args& a, int d, int cta, int slot, int tile) {
+    return a.partials + static_cast<long long>((cta * 2 + slot) * a.tiles + tile) * piece_floats(d);
 }
 
 // D / 16 values of row `rr` of a segment, dimensions d0 .., as bf16.
@@ -113,22 +145,26 @@ __device__ __forceinline__ void write_part(const Q4Args& a, int q0, int head, in
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(const Q4Args a) {
     using C = M4<D, R>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 127u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBars);
     uint64_t* empty = full + C::kStages;
     uint64_t* q_full = empty + C::kStages;
-    uint64_t* q_empty = q_full + kQSlots;
-    uint64_t* piece_bar = q_empty + kQSlots;  // every consumer warp has published its state of the piece
+    uint64_t* q_empty = q_full + C::kQSlots;
+    uint64_t* state_full = q_empty + C::kQSlots;  // every consumer warp has published its state of the piece
+    uint64_t* state_empty = state_full + 1;    // and every one has taken its share of them
     int* present = reinterpret_cast<int*>(smem + C::kOffFlags);
     volatile int* abort_flag = present + C::kStages;
     float* state = reinterpret_cast<float*>(smem + C::kOffState);
+    Piece4* slots = reinterpret_cast<Piece4*>(smem + C::kOffPieces);
+    Piece4* cuts = slots + C::kQSlots;
+    int* num_cuts = reinterpret_cast<int*>(cuts + 2);
     const int W = a.warps_per_unit, UL = kConsumers / W;  // unit lanes: stages in work at a time
     const int q_bytes = C::kRows * W * D * 2;
     uint8_t* q_rows = smem + C::kOffQ;
-    int32_t* s_pre = reinterpret_cast<int32_t*>(q_rows + kQSlots * q_bytes);  // blocks, cost up to and with each sequence; length
+    int32_t* s_pre = reinterpret_cast<int32_t*>(q_rows + C::kQSlots * q_bytes);  // blocks, cost up to and with each sequence; length
     int32_t* s_cost = s_pre + a.batch;
     int32_t* s_len = s_cost + a.batch;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,11 +175,12 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], W);
         }
-        for (int s = 0; s < kQSlots; ++s) {
+        for (int s = 0; s < C::kQSlots; ++s) {
             mbar_init(&q_full[s], 1);
             mbar_init(&q_empty[s], kConsumers);
         }
-        mbar_init(piece_bar, kConsumers);
+        mbar_init(state_full, kConsumers);
+        mbar_init(state_empty, kConsumers);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -198,42 +235,58 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
         }
     }
     const long long U = static_cast<long long>(a.kv_heads) * s_pre[a.batch - 1];
-    const long long cta = blockIdx.x;
+    const int cta = blockIdx.x;
     const long long wanted = U / kLeastBlocks;
-    CostSplit split;
-    split.init(s_pre, s_cost, a.batch, a.kv_heads, 1 + kSegmentCost, wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x);
-    if (U == 0 || cta >= split.C) return;
-    const long long ua = split.start(cta), ub = split.start(cta + 1);
+    const long long ctas = wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x;
+    if (U == 0 || cta >= ctas) return;
 
     if (warp == kConsumers) {
         // ------------------------------------------------ producer
-        const uint64_t policy = l2_evict_first_policy();
+        const uint64_t policy = l2_evict_first_policy(), q_policy = l2_evict_last_policy();
         const uint8_t* cache = static_cast<const uint8_t*>(a.cache);
+        CostSplit split;
+        split.init(s_pre, s_cost, a.batch, a.kv_heads, 1 + kSegmentCost, ctas);
         Walker wk;
-        wk.init(s_pre, a.batch, a.kv_heads, ua, ub);
+        wk.init(s_pre, a.batch, a.kv_heads, split.start(cta), split.start(cta + 1));
         uint32_t k = 0;  // stages issued
         uint32_t pieces = 0;
+        int ncut = 0;
         Piece pc;
         bool ok = true;
-        while (ok && wk.next(pc)) {
+        while (ok) {
+            const bool more = wk.next(pc);
             const int32_t* trow = a.tables + static_cast<long long>(pc.seq) * a.max_blocks + pc.blk_from;
-            const int blocks = pc.blk_to - pc.blk_from;
+            const int blocks = more ? pc.blk_to - pc.blk_from : 0;
             int cur = lane < blocks ? __ldg(trow + lane) : 0;
-            {  // the segment's query rows: G of each query are contiguous
-                const int slot = pieces % kQSlots;
-                if (lane == 0 && pieces >= kQSlots) ok = mbar_wait(&q_empty[slot], (pieces / kQSlots - 1) & 1, a.status, abort_flag);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                const int q0 = a.qstart != nullptr ? a.qstart[pc.seq] : pc.seq;
-                const int nq = a.qstart != nullptr ? a.qstart[pc.seq + 1] - q0 : 1;
-                if (lane == 0) mbar_arrive_expect_tx(&q_full[slot], nq * G * D * 2);
-                __syncwarp();
-                if (lane < nq)
-                    bulk_load(q_rows + slot * q_bytes + lane * G * D * 2,
-                              static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<long long>(q0) + lane) * a.q_heads + pc.head * G) * D, G * D * 2,
-                              &q_full[slot], l2_evict_last_policy());
-                ++pieces;
+            const int slot = pieces % C::kQSlots;
+            if (lane == 0 && pieces >= C::kQSlots) ok = mbar_wait(&q_empty[slot], (pieces / C::kQSlots - 1) & 1, a.status, abort_flag);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (!more) {
+                if (lane == 0) {
+                    slots[slot].blk_to = 0;
+                    *num_cuts = ncut;
+                    mbar_arrive(&q_full[slot]);
+                }
+                break;
             }
+            const int q0 = a.qstart != nullptr ? a.qstart[pc.seq] : pc.seq;
+            const int nq = a.qstart != nullptr ? a.qstart[pc.seq + 1] - q0 : 1;
+            if (lane == 0) {
+                Piece4 p{pc.seq, pc.head, q0, nq * G, s_len[pc.seq], nq, pc.blk_from, pc.blk_to, 0, 0, 0, 0};
+                if (!pc.complete) {
+                    p.cut = pc.first ? 1 : 2;
+                    cuts[ncut] = p;
+                }
+                slots[slot] = p;
+                mbar_arrive_expect_tx(&q_full[slot], nq * G * D * 2);
+            }
+            __syncwarp();
+            if (lane < nq)  // G rows of each query are contiguous
+                bulk_load(q_rows + slot * q_bytes + lane * G * D * 2,
+                          static_cast<const __nv_bfloat16*>(a.q) + ((static_cast<long long>(q0) + lane) * a.q_heads + pc.head * G) * D, G * D * 2,
+                          &q_full[slot], q_policy);
+            ++pieces;
             for (int b0 = 0; ok && b0 < blocks; b0 += 32) {
                 const int nidx = b0 + 32 + lane;
                 const int nxt = nidx < blocks ? __ldg(trow + nidx) : 0;
@@ -276,12 +329,21 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                 }
                 cur = nxt;
             }
+            if (!pc.complete) {  // where the segment's pieces lie (several divisions: not ahead of the copies)
+                if (lane == 0) {
+                    Piece4& p = cuts[ncut];
+                    p.first_cta = static_cast<int>(split.cta_of(pc.seg_start));
+                    p.pieces = static_cast<int>(split.cta_of(pc.seg_start + pc.seg_len - 1)) - p.first_cta + 1;
+                    p.slot0 = pc.seg_start == split.start(p.first_cta) ? 0 : 1;
+                }
+                ++ncut;
+            }
         }
         if (!ok && lane == 0) {  // after an abort: wait (bounded) for the copies still in flight
             for (uint32_t u = k > C::kStages ? k - C::kStages : 0; u < k; ++u)
                 mbar_wait(&full[u % C::kStages], (u / C::kStages) & 1, a.status, nullptr);
-            for (uint32_t u = pieces > kQSlots ? pieces - kQSlots : 0; u < pieces; ++u)
-                mbar_wait(&q_full[u % kQSlots], (u / kQSlots) & 1, a.status, nullptr);
+            for (uint32_t u = pieces > C::kQSlots ? pieces - C::kQSlots : 0; u < pieces; ++u)
+                mbar_wait(&q_full[u % C::kQSlots], (u / C::kQSlots) & 1, a.status, nullptr);
         }
         return;
     }
@@ -291,21 +353,17 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
     const int ul = warp / W;
     const int gid = lane >> 2, tig = lane & 3;
     const float scale_log2 = a.scale * kLog2e;
-    Walker wk;
-    wk.init(s_pre, a.batch, a.kv_heads, ua, ub);
-    uint32_t k = 0, pieces = 0;
-    Piece pc, pending[2];
-    int npending = 0;
-    while (wk.next(pc)) {
-        const int n_ctx = s_len[pc.seq];
-        const int q0 = a.qstart != nullptr ? a.qstart[pc.seq] : pc.seq;
-        const int nq = a.qstart != nullptr ? a.qstart[pc.seq + 1] - q0 : 1;
-        const int rows = nq * G;
+    uint32_t k = 0;
+    for (uint32_t pieces = 0;; ++pieces) {
+        const int slot = pieces % C::kQSlots;
+        if (!mbar_wait(&q_full[slot], (pieces / C::kQSlots) & 1, a.status, abort_flag)) return;
+        const Piece4* pc = slots + slot;
+        const int blk_to = pc->blk_to;
+        if (blk_to == 0) break;
+        const int rows = pc->rows;
         const bool active = rg * C::kRows < rows;
-        const int slot = pieces % kQSlots;
-        if (!mbar_wait(&q_full[slot], (pieces / kQSlots) & 1, a.status, abort_flag)) return;
         uint32_t qf[R][D / 16][2];
-        float cf[R][2], kb[R][2];  // per column: the power of two and the scale; eight times the row's sum
+        float cf[R][2], kb[R][2];  // per column: 2^24, the power of two and the scale; what the eights add, 2^-24 of it
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int rr = rg * C::kRows + r * 8 + gid;
@@ -337,13 +395,10 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
             // S^T columns 2 tig, 2 tig + 1 are the rows of lanes 8 tig and 8 tig + 4
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                cf[r][c] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * c) * scale_log2;
-                kb[r][c] = -8.f * __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * c);
+                cf[r][c] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * c) * scale_log2 * 16777216.f;
+                kb[r][c] = -4.76837158e-7f * __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * c);  // 2^-21
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_empty[slot]);
-        ++pieces;
         // the last token each of the lane's columns sees
         int lim[R][2], least = 0x7fffffff;
 #pragma unroll
@@ -351,22 +406,38 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int rr = rg * C::kRows + r * 8 + 2 * tig + c;
-                lim[r][c] = rr < rows ? n_ctx - nq + rr / G : -1;
+                lim[r][c] = rr < rows ? pc->n - pc->nq + rr / G : -1;
                 if (rr < rows) least = min(least, lim[r][c]);
             }
         least = __reduce_min_sync(0xffffffffu, least);
-        float m[R][2], l[R][2], o[R][D / 16][4];
+        // O and z hold what the codes' eights add too, in o and in z alike; fold() takes it out
+        float m[R][2], l[R][2], o[R][D / 16][4], z[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r][0] = m[r][1] = kUnset;
             l[r][0] = l[r][1] = 0.f;
+            z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
         }
-        const uint32_t k_end = k + (pc.blk_to - pc.blk_from + 1) / 2;
+        auto fold = [&]() {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    o[r][i][0] -= z[r][0];
+                    o[r][i][1] -= z[r][1];
+                    o[r][i][2] = fmaf(-16.f, z[r][0], o[r][i][2]);
+                    o[r][i][3] = fmaf(-16.f, z[r][1], o[r][i][3]);
+                }
+                z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.f;
+            }
+        };
+        const uint32_t k_end = k + (blk_to - pc->blk_from + 1) / 2;
         const int skip = (ul - static_cast<int>(k & (UL - 1))) & (UL - 1);
         k += skip;
-        for (int blk = pc.blk_from + 2 * skip; blk < pc.blk_to; blk += 2 * UL, k += UL) {
+        int unfolded = 0;
+        for (int blk = pc->blk_from + 2 * skip; blk < blk_to; blk += 2 * UL, k += UL) {
             const int s = static_cast<int>(k % C::kStages);
             if (!mbar_wait(&full[s], (k / C::kStages) & 1, a.status, abort_flag)) return;
             const int there = present[s];
@@ -374,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                 const uint8_t* st = smem + s * C::kStageBytes;
                 // every token of the stage exists and every row sees it
                 const bool whole = there == 3 && blk * 16 + 31 <= least;
-                float x[R][8];  // [2 tokens gid, gid + 8 of each block][2 columns]
+                float sc[R][2][4];  // per block: tokens gid, gid + 8 by 2 columns
+                float f[R][8];      // the scores' factors
                 float sv[4];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -389,16 +461,20 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                         wa[0] = u.x, wa[1] = u.y;
                         wb[0] = v.x, wb[1] = v.y;
                     }
-                    float sc[R][2][4] = {};
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t u = h ? wa[c] >> 8 : wa[c], v = h ? wb[c] >> 8 : wb[c];
 #pragma unroll
-                            for (int r = 0; r < R; ++r)
-                                mma_f16_16816(sc[r][h], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
-                                              qf[r][2 * c + h][1]);
+                            for (int r = 0; r < R; ++r) {
+                                if (c + h == 0)
+                                    mma_f16_from(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][0][0], qf[r][0][1],
+                                                 kb[r][0], kb[r][1]);
+                                else
+                                    mma_f16_16816(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
+                                                  qf[r][2 * c + h][1]);
+                            }
                         }
                     }
                     const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
@@ -408,10 +484,17 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[r][4 * b + e] = fmaf(sc[r][0][e] + sc[r][1][e], 16777216.f, kb[r][e & 1]) * ((e & 2 ? kc : ka) * cf[r][e & 1]);
+                        for (int e = 0; e < 4; ++e) f[r][4 * b + e] = (e & 2 ? kc : ka) * cf[r][e & 1];
                 }
-                if (!whole) {
+                uint4 vw[2][D / 64];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        vw[b][h] = *reinterpret_cast<const uint4*>(st + b * C::kRecord + q4_v_offset(D) + gid * 64 + tig * 16 + h * 512);
+                __syncwarp();  // everything is in registers
+                if (lane == 0) mbar_arrive(&empty[s]);
+                if (!whole) {  // what a row does not see: a score of -inf
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int p = blk * 16 + 16 * (i >> 1) + 8 * (i & 1) + gid;
@@ -419,83 +502,104 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c) x[r][2 * i + c] = in && p <= lim[r][c] ? x[r][2 * i + c] : __int_as_float(0xff800000);
+                            for (int c = 0; c < 2; ++c)
+                                if (!in || p > lim[r][c]) {
+                                    sc[r][i >> 1][2 * (i & 1) + c] = __int_as_float(0xff800000);
+                                    f[r][2 * i + c] = 1.f;
+                                }
                     }
                 }
-                float size[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) size[i] = fmaxf(fabsf(sv[i]), kTinyScale);
-                float e[R][8];
+                float e[R][8], sum[R][2];
+                uint32_t p[R][4];
+                uint32_t top = 0;
                 float most = 0.f;
+                auto weights = [&]() {
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                    for (int r = 0; r < R; ++r) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        e[r][i] = ex2(x[r][i] - m[r][i & 1]);
-                        most = fmaxf(most, e[r][i] * size[i >> 1]);
+                        for (int i = 0; i < 8; ++i) e[r][i] = ex2(fmaf(sc[r][i >> 2][i & 3], f[r][i], -m[r][i & 1]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
+                            if (!whole) {  // no weight, whatever the scale
+                                w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
+                                w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
+                            }
+                            p[r][i] = pack_f16x2(w0, w1);
+                            top = largest_f16x2(top, p[r][i]);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            sum[r][c] = l[r][c] + ((e[r][c] + e[r][2 + c]) + (e[r][4 + c] + e[r][6 + c]));
+                            most = fmaxf(most, sum[r][c]);
+                        }
                     }
-                if (__any_sync(0xffffffffu, most > kMost)) {
+                };
+                weights();
+                // some P' has left f16 (its exponent is full), or l grows beside tiny V scales
+                if (__any_sync(0xffffffffu, ((top + 0x04000400u) & 0x80008000u) != 0u || most > kMostSum)) {
                     float lg[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) lg[i] = fminf(__log2f(size[i]), 128.f);
+                    for (int i = 0; i < 4; ++i) lg[i] = fminf(__log2f(fmaxf(fabsf(sv[i]), kTinyScale)), 128.f);
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            float j = fmaxf(fmaxf(x[r][c] + lg[0], x[r][2 + c] + lg[1]), fmaxf(x[r][4 + c] + lg[2], x[r][6 + c] + lg[3]));
+                            float j = kUnset;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) j = fmaxf(j, sc[r][i >> 1][2 * (i & 1) + c] * f[r][2 * i + c] + lg[i]);
 #pragma unroll
                             for (int off = 4; off < 32; off <<= 1) j = fmaxf(j, __shfl_xor_sync(0xffffffffu, j, off));
                             const float to = fmaxf(m[r][c], j - kHeadroom), al = ex2(m[r][c] - to);
                             m[r][c] = to;
                             l[r][c] *= al;
+                            z[r][c] *= al;
+                            z[r][2 + c] *= al;
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i) {
                                 o[r][i][c] *= al;
                                 o[r][i][2 + c] *= al;
                             }
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) e[r][i + c] = ex2(x[r][i + c] - to);
                         }
+                    weights();
                 }
-                uint32_t p[R][2][2];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    l[r][0] = sum[r][0];
+                    l[r][1] = sum[r][1];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) l[r][i & 1] += e[r][i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
-                        if (!whole) {  // what a row does not see has no weight, whatever its scale
-                            w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
-                            w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
-                        }
-                        p[r][i >> 1][i & 1] = movmatrix_trans(pack_f16x2(w0, w1));
-                    }
+                    for (int i = 0; i < 4; ++i) p[r][i] = movmatrix_trans(p[r][i]);
                 }
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const uint8_t* v = st + b * C::kRecord + q4_v_offset(D) + gid * 64 + tig * 16;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) mma_f16_16816(z[r], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[r][2 * b], p[r][2 * b + 1]);
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(v + h * 512);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        const uint32_t w[4] = {vw[b][h].x, vw[b][h].y, vw[b][h].z, vw[b][h].w};
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t a0 = v_codes(w[j], 0x000f000fu, 0x00080008u), a1 = v_codes(w[j], 0x00f000f0u, 0x00800080u);
-                            const uint32_t a2 = v_codes(w[j] >> 8, 0x000f000fu, 0x00080008u), a3 = v_codes(w[j] >> 8, 0x00f000f0u, 0x00800080u);
 #pragma unroll
-                            for (int r = 0; r < R; ++r) mma_f16_16816(o[r][4 * h + j], a0, a1, a2, a3, p[r][b][0], p[r][b][1]);
+                            for (int r = 0; r < R; ++r)
+                                mma_f16_16816(o[r][4 * h + j], w[j] & 0x000f000fu, w[j] & 0x00f000f0u, w[j] >> 8 & 0x000f000fu, w[j] >> 8 & 0x00f000f0u,
+                                              p[r][2 * b], p[r][2 * b + 1]);
                         }
                     }
                 }
+                if (++unfolded == kFold) {
+                    fold();
+                    unfolded = 0;
+                }
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
         }
+        fold();
         k = k_end;
         // ---- end of the piece: this warp's state into shared memory (O over 2^-24)
-        float* buf = state + (pieces & 1) * (kConsumers * C::kStateFloats);
-        float* own = buf + warp * C::kStateFloats;
+        if (pieces > 0 && !mbar_wait(state_empty, (pieces - 1) & 1, a.status, abort_flag)) return;
+        float* own = state + warp * C::kStateFloats;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
 #pragma unroll
@@ -514,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
             }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(piece_bar);
-        if (!mbar_wait(piece_bar, (pieces - 1) & 1, a.status, abort_flag)) return;
+        if (lane == 0) mbar_arrive(state_full);
+        if (!mbar_wait(state_full, pieces & 1, a.status, abort_flag)) return;
         // ---- all unit lanes together; a warp takes D / 4 dimensions, a lane a quarter of them of one row of a tile
         const int tiles = (rows + 7) / 8;
         constexpr int kPer = D / 16;
@@ -523,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
         for (int tile = 0; tile < tiles; ++tile) {
             const int row = tile % R * 8 + row8, group = tile / R;  // among the rows of that group's warps
             float M = kUnset, L = 0.f, O[kPer] = {};
-            for (int u = 0; u < UL; ++u) M = fmaxf(M, buf[(u * W + group) * C::kStateFloats + C::kRows * D + row]);
+            for (int u = 0; u < UL; ++u) M = fmaxf(M, state[(u * W + group) * C::kStateFloats + C::kRows * D + row]);
             for (int u = 0; u < UL; ++u) {
-                const float* su = buf + (u * W + group) * C::kStateFloats;
+                const float* su = state + (u * W + group) * C::kStateFloats;
                 const float wu = ex2(su[C::kRows * D + row] - M);
                 L += wu * su[C::kRows * (D + 1) + row];
 #pragma unroll
@@ -535,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                 }
             }
             const int rr = tile * 8 + row8;
-            if (pc.complete) {
-                if (rr < rows) write_part<D>(a, q0, pc.head, rr, d0, O, L);
+            if (pc->cut == 0) {
+                if (rr < rows) write_part<D>(a, pc->q0, pc->head, rr, d0, O, L);
             } else {
-                float* sl = piece_of(a, D, cta, pc.first ? 0 : 1, tile);
+                float* sl = piece_of(a, D, cta, pc->cut - 1, tile);
 #pragma unroll
                 for (int e = 0; e < kPer; e += 4) *reinterpret_cast<float4*>(sl + row8 * D + d0 + e) = make_float4(O[e], O[e + 1], O[e + 2], O[e + 3]);
                 if ((lane & 3) == 0) {
@@ -547,32 +651,30 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                 }
             }
         }
-        if (!pc.complete) pending[npending++] = pc;
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(state_empty);
+            mbar_arrive(&q_empty[slot]);
+        }
     }
     // ---- announce this warp's share of the cut pieces; the warp that completes a count merges them
-    if (npending == 0) return;
+    const int ncut = *num_cuts;
+    if (ncut == 0) return;
     __threadfence();
     __syncwarp();
-    for (int i = 0; i < npending; ++i) {
-        const Piece& pp = pending[i];
-        const long long c0 = split.cta_of(pp.seg_start), c1 = split.cta_of(pp.seg_start + pp.seg_len - 1);
-        const int np = split.pieces(c0, c1);
-        int* counter = a.counters + (static_cast<long long>(pp.seq) * a.kv_heads + pp.head) * kConsumers + warp;
-        int old = 0;
-        if (lane == 0) old = atomicAdd(counter, 1);
-        old = __shfl_sync(0xffffffffu, old, 0);
-        if (old != np - 1) continue;
+    int old = 0;
+    if (lane < ncut) old = atomicAdd(a.counters + (static_cast<long long>(cuts[lane].seq) * a.kv_heads + cuts[lane].head) * kConsumers + warp, 1);
+    for (int i = 0; i < ncut; ++i) {
+        const Piece4& pc = cuts[i];
+        if (__shfl_sync(0xffffffffu, old, i) != pc.pieces - 1) continue;
         __threadfence();
-        const int slot0 = pp.seg_start == split.start(c0) ? 0 : 1;
-        const int q0 = a.qstart != nullptr ? a.qstart[pp.seq] : pp.seq;
-        const int rows = (a.qstart != nullptr ? a.qstart[pp.seq + 1] - q0 : 1) * G;
         constexpr int kPer = D / 16;
         const int row8 = lane >> 2, d0 = warp * (D / 4) + (lane & 3) * kPer;
-        for (int tile = 0; tile * 8 < rows; ++tile) {
+        for (int tile = 0; tile * 8 < pc.rows; ++tile) {
             float M = kUnset, L = 0.f, O[kPer] = {};
 #pragma unroll 4
-            for (int p = 0; p < np; ++p) {
-                const float* sl = piece_of(a, D, split.piece_cta(c0, p), p == 0 ? slot0 : 0, tile);
+            for (int p = 0; p < pc.pieces; ++p) {
+                const float* sl = piece_of(a, D, pc.first_cta + p, p == 0 ? pc.slot0 : 0, tile);
                 const float mp = __ldcg(sl + 8 * D + warp * 16 + row8), lp = __ldcg(sl + 8 * D + warp * 16 + 8 + row8);
                 const float to = fmaxf(M, mp), keep = ex2(M - to), w = ex2(mp - to);
                 M = to;
@@ -584,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? 3 : 2) mq4_kernel(const Q4A
                     O[e + 2] = O[e + 2] * keep + w * v.z, O[e + 3] = O[e + 3] * keep + w * v.w;
                 }
             }
-            if (tile * 8 + row8 < rows) write_part<D>(a, q0, pp.head, tile * 8 + row8, d0, O, L);
+            if (tile * 8 + row8 < pc.rows) write_part<D>(a, pc.q0, pc.head, tile * 8 + row8, d0, O, L);
         }
-        if (lane == 0) *counter = 0;
+        if (lane == 0) a.counters[(static_cast<long long>(pc.seq) * a.kv_heads + pc.head) * kConsumers + warp] = 0;
     }
 }
 
@@ -602,7 +704,7 @@ cudaError_t run_mq4(const Q4Args& a, cudaStream_t s) {
 // Resident CTAs of an SM, at the largest launch.
 template <int D, int R>
 int resident(int warps_per_unit) {
-    const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, kMaxBatchPerLaunch);
+    const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, MQ4_BATCH);
     int n = 0;
     cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mq4_kernel<D, R>, kThreads, smem) != cudaSuccess || n < 1) n = 1;
