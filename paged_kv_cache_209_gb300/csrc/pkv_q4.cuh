@@ -37,22 +37,5 @@ __host__ __device__ constexpr int q4_v_byte(int o, int j, int t) {
 // against the stored scale either way.)
 constexpr float kQ4Step = 0.142857149243354797f;
 
-// Nearest integer to the exact x / scale, ties to even, clipped to +-limit, where |x| <=
-// (limit + 1/2) scale: a float32 quotient is within one of it, and the signs of two fused
-// multiply-adds decide the sides of c - 1/2 and c + 1/2 exactly. Both are taken far above
-// the subnormal range first, where a fused difference could round to zero.
-__device__ __forceinline__ int exact_code(float x, float scale, float limit) {
-    const float lift = scale < 1e-20f ? 1.2089258e24f : 1.f;  // 2^80
-    x *= lift;
-    scale *= lift;
-    float c = rintf(__fdiv_rn(x, scale));
-    const float up = fmaf(-(c + 0.5f), scale, x);  // sign of x - (c + 1/2) scale
-    const float dn = fmaf(-(c - 0.5f), scale, x);  // sign of x - (c - 1/2) scale
-    const bool odd = (static_cast<int>(c) & 1) != 0;
-    if (up > 0.f || (up == 0.f && odd)) c += 1.f;
-    else if (dn < 0.f || (dn == 0.f && odd)) c -= 1.f;
-    return static_cast<int>(fminf(fmaxf(c, -limit), limit));
-}
-
 }  // namespace
 }  // namespace pkv

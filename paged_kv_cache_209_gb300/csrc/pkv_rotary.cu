@@ -20,8 +20,30 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef ROT_BATCH
+#define ROT_BATCH 2
+#endif
+#ifndef ROT_FEW
+#define ROT_FEW 64
+#endif
+#ifndef ROT_THREADS
+#define ROT_THREADS 128
+#endif
+constexpr int kThreads = ROT_THREADS;
 
+// x c - y s rounded to float32 and to bf16. The exact value is s1 + lo, but for an error of lo's last
+// bit: products and difference by their errors, which fused operations give exactly. Where that
+// leaves open which float32 is nearest (one value in a thousand that come here), and near the ends of
+// the float range, float64 decides.
+__device__ __noinline__ float turned_exactly(float x, float c, float y, float s) {
+    const float h = x * c, p = y * s, s1 = h - p, back = s1 - h;
+    const float lo = ((h - (s1 - back)) - (p + back)) + (fmaf(x, c, -h) - fmaf(y, s, -p));
+    const float r = s1 + lo, t = lo - (r - s1);
+    const float half_step = __uint_as_float(__float_as_uint(r) & 0x7f800000u) * 5.9604645e-8f;  // 2^-24
+    if (fabsf(lo) <= 4e-4f * fabsf(s1) && fabsf(t) < 0.999f * half_step && fabsf(r) > 1e-28f && fabsf(r) < 1e38f)
+        return __bfloat162float(__float2bfloat16_rn(r));
+    return __bfloat162float(__float2bfloat16_rn(static_cast<float>(static_cast<double>(x) * c - static_cast<double>(y) * s)));
+}
 // x c - y s as described above, for bf16 x and y held in float32: a bf16 in float32.
 __device__ __forceinline__ float turned(__nv_bfloat16, float x, float c, float y, float s) {
     const float p = y * s;
@@ -30,8 +52,7 @@ __device__ __forceinline__ float turned(__nv_bfloat16, float x, float c, float y
     const float off = fmaf(fabsf(p) + fabsf(r), 1.1920929e-7f, 2.8026e-45f);
     const uint32_t ends = pack_bf16x2(r - off, r + off);
     if ((ends & 0xffffu) == ends >> 16) return bf16hi_to_f32(ends);
-    const double exact = static_cast<double>(x) * c - static_cast<double>(y) * s;
-    return __bfloat162float(__float2bfloat16_rn(static_cast<float>(exact)));
+    return turned_exactly(x, c, y, s);
 }
 // float32 rows: the product's error joins the sum (one rounding, and one of a small term).
 __device__ __forceinline__ float turned(float, float x, float c, float y, float s) {
@@ -39,27 +60,38 @@ __device__ __forceinline__ float turned(float, float x, float c, float y, float 
     return fmaf(x, c, -p) - fmaf(y, s, -p);
 }
 
-// Eight elements of a row, in float32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    x[0] = bf16lo_to_f32(w.x), x[1] = bf16hi_to_f32(w.x), x[2] = bf16lo_to_f32(w.y), x[3] = bf16hi_to_f32(w.y);
-    x[4] = bf16lo_to_f32(w.z), x[5] = bf16hi_to_f32(w.z), x[6] = bf16lo_to_f32(w.w), x[7] = bf16hi_to_f32(w.w);
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                              pack_bf16x2(x[6], x[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
+// Eight elements of a row as they are stored: words of two (bf16), or one each.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const void* p) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    __device__ __forceinline__ void store(void* p) const { *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+    __device__ __forceinline__ float get(int e) const { return e & 1 ? bf16hi_to_f32(w[e / 2]) : bf16lo_to_f32(w[e / 2]); }
+    __device__ __forceinline__ void set(int e, float x) {  // (of a value that bf16 holds)
+        w[e / 2] = e & 1 ? w[e / 2] & 0xffffu | __float_as_uint(x) : w[e / 2] & 0xffff0000u | __float_as_uint(x) >> 16;
+    }
+};
+template <>
+struct Eight<float> {
+    float w[8];
+    __device__ __forceinline__ void load(const void* p) {
+        const float4 u = static_cast<const float4*>(p)[0], v = static_cast<const float4*>(p)[1];
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
+    }
+    __device__ __forceinline__ void store(void* p) const {
+        static_cast<float4*>(p)[0] = make_float4(w[0], w[1], w[2], w[3]);
+        static_cast<float4*>(p)[1] = make_float4(w[4], w[5], w[6], w[7]);
+    }
+    __device__ __forceinline__ float get(int e) const { return w[e]; }
+    __device__ __forceinline__ void set(int e, float x) { w[e] = x; }
+};
 __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float value(float x) { return x; }
-
 enum { kWhole = 0, kHalves = 1, kNeighbours = 2, kAny = 3 };
 
 // A lane takes two vectors of 8 dimensions of a row: va and vb. Where pairs lie R / 2
@@ -77,132 +109,255 @@ __device__ __forceinline__ Place place_of(int lane, int R) {
     return {2 * lane, 2 * lane + 1, false};
 }
 
-// The turned row (`row`: its first element; `cs`: its table row), in the lane's vectors.
-template <int kMode, typename T>
-__device__ __forceinline__ void turn(const T* row, const float* cs, int R, bool interleaved, const Place& at, float (&a)[8], float (&b)[8]) {
-    load8(row + 8 * at.va, a);
-    load8(row + 8 * at.vb, b);
-    if (kMode == kWhole) return;
+// The lane's cosines and sines of a token: kHalves of the pairs of both vectors, kNeighbours
+// of va's four pairs, then vb's.
+template <int kMode>
+__device__ __forceinline__ void load_angles(const float* cs, int R, const Place& at, float (&c)[8], float (&s)[8]) {
     const int half = R / 2;
+    auto four = [](const float* p, float (&x)[8], int to) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        x[to] = v.x, x[to + 1] = v.y, x[to + 2] = v.z, x[to + 3] = v.w;
+    };
+    if (kMode == kHalves && at.turns) {
+        four(cs + 8 * at.va, c, 0), four(cs + 8 * at.va + 4, c, 4);
+        four(cs + half + 8 * at.va, s, 0), four(cs + half + 8 * at.va + 4, s, 4);
+    }
+    if (kMode == kNeighbours) {
+        if (8 * at.va < R) four(cs + 4 * at.va, c, 0), four(cs + half + 4 * at.va, s, 0);
+        if (8 * at.vb < R) four(cs + 4 * at.vb, c, 4), four(cs + half + 4 * at.vb, s, 4);
+    }
+}
+
+// Two values r, off by at most `off` each, as bf16; false if a rounding is not decided by that.
+__device__ __forceinline__ bool decided(uint64_t r, uint64_t off, uint32_t& word) {
+    float a, b, c, d;
+    f32x2_unpack(f32x2_sub(r, off), a, b);
+    f32x2_unpack(f32x2_add(r, off), c, d);
+    word = pack_bf16x2(c, d);
+    return pack_bf16x2(a, b) == word;
+}
+
+// Turns the lane's vectors of a row of bf16s, two elements at a time. `size`: the largest of the
+// lane's |c| and |s|. With X the larger of a pair's magnitudes, |y s| <= X size and |r| <= 2
+// X size, so r = x c - y s is off by at most 2^-24 (|y s| + |r|) <= 3 2^-24 X size (and 2^-149
+// below the normal range).
+template <int kMode>
+__device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat16>& b, const float (&c)[8], const float (&s)[8], float size,
+                                     const Place& at, int R) {
+    const float k = 2.0e-7f * size;  // (3.36 2^-24)
     if (kMode == kHalves) {
         if (!at.turns) return;
-        float c[8], s[8];
-        load8(cs + 8 * at.va, c);
-        load8(cs + half + 8 * at.va, s);
+        uint32_t open = 0;
+        Eight<__nv_bfloat16> x = a, y = b;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = a[e], y = b[e];
-            a[e] = turned(T{}, x, c[e], y, s[e]);
-            b[e] = turned(T{}, y, c[e], x, -s[e]);
+        for (int i = 0; i < 4; ++i) {
+            const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1), y0 = y.get(2 * i), y1 = y.get(2 * i + 1);
+            const uint64_t xx = f32x2_pack(x0, x1), yy = f32x2_pack(y0, y1), cc = f32x2_pack(c[2 * i], c[2 * i + 1]);
+            const uint64_t off = f32x2_pack(fmaf(fmaxf(fabsf(x0), fabsf(y0)), k, 2.8026e-45f), fmaf(fmaxf(fabsf(x1), fabsf(y1)), k, 2.8026e-45f));
+            if (!decided(f32x2_fma(xx, cc, f32x2_mul(yy, f32x2_pack(-s[2 * i], -s[2 * i + 1]))), off, a.w[i])) open |= 1u << i;
+            if (!decided(f32x2_fma(yy, cc, f32x2_mul(xx, f32x2_pack(s[2 * i], s[2 * i + 1]))), off, b.w[i])) open |= 16u << i;
+        }
+        if (open) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (open >> (e / 2) & 1) a.set(e, turned_exactly(x.get(e), c[e], y.get(e), s[e]));
+                if (open >> (4 + e / 2) & 1) b.set(e, turned_exactly(y.get(e), c[e], x.get(e), -s[e]));
+            }
         }
     } else if (kMode == kNeighbours) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            float (&v)[8] = u ? b : a;
-            const int first = 8 * (u ? at.vb : at.va);
-            if (first >= R) break;
-            const float4 c = *reinterpret_cast<const float4*>(cs + first / 2), s = *reinterpret_cast<const float4*>(cs + half + first / 2);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+            Eight<__nv_bfloat16>& v = u ? b : a;
+            if (8 * (u ? at.vb : at.va) >= R) break;
+            uint32_t open = 0;
+            const Eight<__nv_bfloat16> x = v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = v[2 * e], y = v[2 * e + 1];
-                v[2 * e] = turned(T{}, x, cc[e], y, ss[e]);
-                v[2 * e + 1] = turned(T{}, y, cc[e], x, -ss[e]);
+            for (int i = 0; i < 4; ++i) {
+                const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1), cc = c[4 * u + i], ss = s[4 * u + i];
+                const float o = fmaf(fmaxf(fabsf(x0), fabsf(x1)), k, 2.8026e-45f);
+                if (!decided(f32x2_fma(f32x2_pack(x0, x1), f32x2_pack(cc, cc), f32x2_mul(f32x2_pack(x1, x0), f32x2_pack(-ss, ss))), f32x2_pack(o, o), v.w[i]))
+                    open |= 1u << i;
             }
-        }
-    } else {
-        // any even R: the partner of every dimension is read apart
+            if (open) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float (&v)[8] = u ? b : a;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = 8 * (u ? at.vb : at.va) + e;
-                if (d >= R) continue;
-                const int i = interleaved ? d / 2 : d % half;
-                const bool second = interleaved ? (d & 1) != 0 : d >= half;
-                const int other = interleaved ? d ^ 1 : second ? d - half : d + half;
-                const float y = value(row[other]), c = cs[i], s = cs[half + i];
-                v[e] = turned(T{}, v[e], c, y, second ? -s : s);
+                for (int i = 0; i < 4; ++i)
+                    if (open >> i & 1) {
+                        const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1);
+                        v.set(2 * i, turned_exactly(x0, c[4 * u + i], x1, s[4 * u + i]));
+                        v.set(2 * i + 1, turned_exactly(x1, c[4 * u + i], x0, -s[4 * u + i]));
+                    }
             }
         }
     }
 }
+template <int kMode>
+__device__ __forceinline__ void turn(Eight<float>& a, Eight<float>& b, const float (&c)[8], const float (&s)[8], float, const Place& at, int R) {
+    if (kMode == kHalves) {
+        if (!at.turns) return;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = a.w[e], y = b.w[e];
+            a.w[e] = turned(x, x, c[e], y, s[e]);
+            b.w[e] = turned(x, y, c[e], x, -s[e]);
+        }
+    } else if (kMode == kNeighbours) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            Eight<float>& v = u ? b : a;
+            if (8 * (u ? at.vb : at.va) >= R) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = v.w[2 * e], y = v.w[2 * e + 1];
+                v.w[2 * e] = turned(x, x, c[4 * u + e], y, s[4 * u + e]);
+                v.w[2 * e + 1] = turned(x, y, c[4 * u + e], x, -s[4 * u + e]);
+            }
+        }
+    }
+}
+// Any even R: the partner of every dimension is read apart (`row`: the row's first element, `cs`: the table's row).
+template <typename T>
+__device__ __forceinline__ void turn_any(Eight<T>& a, Eight<T>& b, const Place& at, int R, const T* row, const float* cs, bool interleaved) {
+    const int half = R / 2;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        Eight<T>& v = u ? b : a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int d = 8 * (u ? at.vb : at.va) + e;
+            if (d >= R) continue;
+            const int i = interleaved ? d / 2 : d % half;
+            const bool second = interleaved ? (d & 1) != 0 : d >= half;
+            const int other = interleaved ? d ^ 1 : second ? d - half : d + half;
+            const float y = value(row[other]), w = cs[half + i];
+            v.set(e, turned(T{}, v.get(e), cs[i], y, second ? -w : w));
+        }
+    }
+}
 
-// Words of a 4-bit record for 8 dimensions: K's word, and V's bytes.
-__device__ __forceinline__ uint32_t k_word(const int (&c)[8]) {
+// The codes of a row of bf16s, int8 (two's complement) or 4-bit (code + 8): the nearest
+// integer c to x / scale, ties to even. x times 1 / scale gives c or a neighbour. x - c scale is
+// exact in float32 (a multiple of the scale's last bit, below twice the scale; both taken
+// far above the subnormal range first), and its magnitude against scale / 2 says whether
+// c has to move: the two compare as integers, where an odd c counts as one more, which
+// breaks ties to even. Needs no clipping: |x| <= limit scale but for a rounding.
+template <int kCache>
+struct Codes {
+    float scale, inverse, lift;
+    int half;
+    __device__ __forceinline__ explicit Codes(float s) {
+        lift = s < 1e-20f ? 1.2089258e24f : 1.f;  // 2^80
+        scale = s * lift;
+        inverse = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
+        half = __float_as_int(scale * 0.5f);
+    }
+    __device__ __forceinline__ uint32_t operator()(float x) const {
+        constexpr float kShift = 12582912.f + (kCache == PKV_INT4 ? 8.f : 0.f);  // 1.5 2^23: an integer sits in its low bits
+        x *= lift;
+        const float shifted = fmaf(x, inverse, kShift);
+        const float rest = fmaf(-(shifted - kShift), scale, x);
+        int c = __float_as_int(shifted);
+        if ((__float_as_int(rest) & 0x7fffffff) + (c & 1) > half) c += __float_as_int(rest) >> 31 | 1;
+        return static_cast<uint32_t>(c) & (kCache == PKV_INT4 ? 15u : 255u);
+    }
+};
+__device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {  // of a 4-bit record
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= static_cast<uint32_t>(c[e] + 8) << (4 * (e / 2 + 4 * (e & 1)));
+    for (int e = 0; e < 8; ++e) w |= c[e] << (4 * (e / 2 + 4 * (e & 1)));
     return w;
 }
 
-// One row per D / 16 lanes: q's rows, then k's, then v's of a token. kCache: the pkv_dtype
-// of the pools, or PKV_INT4.
-template <int D, int kMode, int kCache, typename T>
+// One warp takes a unit: kBatch times kRows heads of one token, all of q, of k or of v, D / 16 lanes a
+// row, all of its loads in flight at once. Units are numbered token by token, so that what runs at
+// a time reads and writes memory that lies together. kCache: the pkv_dtype of the pools, or PKV_INT4.
+template <int D, int kMode, int kCache, typename T, int kBatch>
 __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryAppendArgs a) {
     constexpr int kLanes = D / 16;
-    constexpr int kRows = kThreads / kLanes;  // rows of a CTA
+    constexpr int kRows = 32 / kLanes;
+    constexpr int kHeads = kBatch * kRows;
     grid_dependency_wait();  // q, k, v, and a block copied onto the slots' block, come from the kernels before
     allow_dependents();
-    const int lane = threadIdx.x % kLanes;
-    const uint32_t heads = a.q_heads + 2 * a.kv_heads;
-    const uint32_t rows = static_cast<uint32_t>(a.num_tokens) * heads;
+    const uint32_t lane = threadIdx.x % kLanes, row = threadIdx.x % 32 / kLanes;
+    const uint32_t q_units = (a.q_heads + kHeads - 1) / kHeads, kv_units = (a.kv_heads + kHeads - 1) / kHeads;
+    const uint32_t units = q_units + 2 * kv_units;  // of a token
+    const uint32_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const uint32_t token = w / units, unit = w - token * units;
+    if (token >= static_cast<uint32_t>(a.num_tokens)) return;
     const Place at = place_of<kMode>(lane, a.rotary_dim);
-    // (whole warps take part in every turn of the loop)
-    for (uint32_t r0 = blockIdx.x * kRows; r0 < rows; r0 += gridDim.x * kRows) {
-        const uint32_t r = r0 + threadIdx.x / kLanes;
-        const uint32_t token = min(r, rows - 1) / heads;
-        const int h = static_cast<int>(min(r, rows - 1) - token * heads);
-        const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
-        const int head = is_q ? h : is_v ? h - a.q_heads - a.kv_heads : h - a.q_heads;
-        const int64_t slot = a.slots[token];
-        const int pos = kMode == kWhole ? 0 : a.positions[token];
-        const bool placed = kMode == kWhole || (pos >= 0 && pos < a.num_positions);
-        const bool bad = slot >= a.num_slots || (!placed && (pos >= a.num_positions || slot >= 0));
-        if (bad && h == 0 && lane == 0 && r < rows) atomicOr(a.status, PKV_DEVERR_RANGE);
-        const bool live = r < rows && placed && (is_q || (slot >= 0 && slot < a.num_slots));
-        const T* row = is_q ? static_cast<const T*>(a.q) + token * a.q_stride : is_v ? static_cast<const T*>(a.v) + token * a.v_stride
-                                                                                  : static_cast<const T*>(a.k) + token * a.k_stride;
-        row += head * D;
-        float x[8] = {}, y[8] = {};
-        if (live) {
-            if (is_v)
-                turn<kWhole>(row, nullptr, 0, false, at, x, y);
-            else
-                turn<kMode>(row, a.table + static_cast<int64_t>(pos) * a.rotary_dim, a.rotary_dim, a.interleaved != 0, at, x, y);
+    const bool is_q = unit < q_units, is_v = unit >= q_units + kv_units;
+    const int heads = is_q ? a.q_heads : a.kv_heads;
+    const int head0 = (unit - (is_q ? 0 : is_v ? q_units + kv_units : q_units)) * kHeads + row;  // of this lane's heads, kRows apart
+    const T* from = (is_q ? static_cast<const T*>(a.q) + token * a.q_stride
+                          : is_v ? static_cast<const T*>(a.v) + token * a.v_stride : static_cast<const T*>(a.k) + token * a.k_stride) + head0 * D;
+    Eight<T> in[kBatch][2];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+        if (head0 + b * kRows < heads) {
+            in[b][0].load(from + b * kRows * D + 8 * at.va);
+            in[b][1].load(from + b * kRows * D + 8 * at.vb);
         }
-        if (kMode == kAny) __syncwarp();  // q may turn in place, and its dimensions are read by two lanes
+    const int64_t slot = a.slots[token];
+    const int pos = kMode == kWhole ? 0 : a.positions[token];
+    const bool placed = kMode == kWhole || (pos >= 0 && pos < a.num_positions);
+    const bool bad = slot >= a.num_slots || (!placed && (pos >= a.num_positions || slot >= 0));
+    if (bad && unit == 0 && lane + row == 0) atomicOr(a.status, PKV_DEVERR_RANGE);
+    if (!placed || (!is_q && (slot < 0 || slot >= a.num_slots))) return;  // (the whole warp)
+    const float* cs = a.table + static_cast<int64_t>(pos) * a.rotary_dim;
+    float c[8] = {}, s[8] = {}, size = 0.f;
+    if ((kMode == kHalves || kMode == kNeighbours) && !is_v) {
+        load_angles<kMode>(cs, a.rotary_dim, at, c, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) size = fmax3(size, fabsf(c[e]), fabsf(s[e]));
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+        const int head = head0 + b * kRows;
+        if (head - static_cast<int>(row) >= heads) break;  // (no row of the warp)
+        const bool live = head < heads;
+        Eight<T> x{}, y{};
+        if (live) {
+            x = in[b][0];
+            y = in[b][1];
+            if (!is_v) {
+                if (kMode == kAny)
+                    turn_any<T>(x, y, at, a.rotary_dim, from + b * kRows * D, cs, a.interleaved != 0);
+                else if (kMode != kWhole)
+                    turn<kMode>(x, y, c, s, size, at, a.rotary_dim);
+            }
+        }
+        if (kMode == kAny) __syncwarp();  // q may turn in place, its dimensions read by two lanes
         if (is_q) {
             if (live) {
                 T* out = static_cast<T*>(a.q_out) + token * a.q_out_stride + head * D;
-                store8(out + 8 * at.va, x);
-                store8(out + 8 * at.vb, y);
+                x.store(out + 8 * at.va);
+                y.store(out + 8 * at.vb);
             }
+            continue;
         }
         if (kCache == PKV_F32 || kCache == PKV_BF16) {
-            if (!is_q && live) {
+            if (live) {
                 T* out = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + (((slot >> 4) * a.kv_heads + head) * 16 + (slot & 15)) * D;
-                store8(out + 8 * at.va, x);
-                store8(out + 8 * at.vb, y);
+                x.store(out + 8 * at.va);
+                y.store(out + 8 * at.vb);
             }
             continue;
         }
         // ---- quantized: the row's largest over its lanes (all lanes of the warp are here)
         float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[e]), fabsf(y[e])));
+        for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x.get(e)), fabsf(y.get(e)));
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (is_q || !live) continue;
+        if (!live) continue;
         constexpr float kLimit = kCache == PKV_INT4 ? 7.f : 127.f;
         // (a zero row's scale is 0 in a 4-bit cache, 1 in an int8 one)
         const float scale = kCache == PKV_INT4 ? top * kQ4Step : top > 0.f ? __fdiv_rn(top, kLimit) : 1.f;
-        int cx[8], cy[8];
+        const Codes<kCache> code(scale);
+        uint32_t cx[8], cy[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            cx[e] = scale > 0.f ? exact_code(x[e], scale, kLimit) : 0;
-            cy[e] = scale > 0.f ? exact_code(y[e], scale, kLimit) : 0;
+            cx[e] = code(x.get(e));
+            cy[e] = code(y.get(e));
         }
         const int64_t chunk = (slot >> 4) * a.kv_heads + head;
         const int t = static_cast<int>(slot & 15);
@@ -212,8 +367,8 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryApp
                 uint8_t* v = rec + q4_v_offset(D);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[q4_v_byte(at.va, j, t)] = static_cast<uint8_t>((cx[2 * j] + 8) | (cx[2 * j + 1] + 8) << 4);
-                    v[q4_v_byte(at.vb, j, t)] = static_cast<uint8_t>((cy[2 * j] + 8) | (cy[2 * j + 1] + 8) << 4);
+                    v[q4_v_byte(at.va, j, t)] = static_cast<uint8_t>(cx[2 * j] | cx[2 * j + 1] << 4);
+                    v[q4_v_byte(at.vb, j, t)] = static_cast<uint8_t>(cy[2 * j] | cy[2 * j + 1] << 4);
                 }
             } else {
                 uint32_t* k = reinterpret_cast<uint32_t*>(rec + t * (D / 2));
@@ -231,9 +386,7 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryApp
                 }
             } else {
                 int8_t* k = static_cast<int8_t*>(a.k_cache) + (chunk * 16 + t) * D;
-                auto word = [](const int* c) {
-                    return (c[0] & 255u) | (c[1] & 255u) << 8 | (c[2] & 255u) << 16 | static_cast<uint32_t>(c[3]) << 24;
-                };
+                auto word = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
                 *reinterpret_cast<uint2*>(k + 8 * at.va) = make_uint2(word(cx), word(cx + 4));
                 *reinterpret_cast<uint2*>(k + 8 * at.vb) = make_uint2(word(cy), word(cy + 4));
             }
@@ -242,12 +395,19 @@ __global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryApp
     }
 }
 
+template <int D, int kMode, int kCache, typename T, int kBatch>
+cudaError_t run_batch(const RotaryAppendArgs& a, cudaStream_t s) {
+    constexpr int kHeads = kBatch * 32 / (D / 16), kWarps = kThreads / 32;
+    const int64_t units = a.num_tokens * ((a.q_heads + kHeads - 1) / kHeads + 2 * ((a.kv_heads + kHeads - 1) / kHeads));
+    return launch_pdl(append_rotary_kernel<D, kMode, kCache, T, kBatch>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, a);
+}
 template <int D, int kMode, int kCache, typename T>
 cudaError_t run_append(const RotaryAppendArgs& a, cudaStream_t s) {
+    constexpr int kBatch = kMode == kAny ? 1 : sizeof(T) == 4 ? 2 : ROT_BATCH;
+    // few rows: every warp takes as few as it can, so that they spread over the SMs
     const int64_t rows = a.num_tokens * (a.q_heads + 2 * a.kv_heads);
-    constexpr int kRows = kThreads / (D / 16);
-    const int64_t want = (rows + kRows - 1) / kRows, most = static_cast<int64_t>(device_sm_count()) * 16;
-    return launch_pdl(append_rotary_kernel<D, kMode, kCache, T>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kThreads), 0, s, a);
+    if (kBatch == 1 || rows < static_cast<int64_t>(device_sm_count()) * ROT_FEW) return run_batch<D, kMode, kCache, T, 1>(a, s);
+    return run_batch<D, kMode, kCache, T, kBatch>(a, s);
 }
 template <int D, int kCache, typename T>
 cudaError_t run_mode(const RotaryAppendArgs& a, cudaStream_t s) {
@@ -261,26 +421,64 @@ cudaError_t run_mode(const RotaryAppendArgs& a, cudaStream_t s) {
 // ---------------------------------------------------------------- the table
 // Row p: factor cos(p f_i), i < half, then factor sin(p f_i). The angle in turns is p f_i
 // / (2 pi) modulo 1: with g = f_i / (2 pi) as a 64-bit binary fraction that is p g modulo
-// 2^64, an integer product, exact however far p is (g is off by 2^-53 of itself).
+// 2^64, an integer product, exact however far p is (g is off by 2^-53 of itself). A thread
+// keeps kV neighbouring frequencies and adds (step g) from one of its rows to the next.
+// Of the fraction the upper 32 bits give the quarter turn and the angle from there, at most
+// an eighth of a turn, whose sine and cosine are their Taylor polynomials of degree 9 and 8
+// (off by 1.8e-9 and 2.5e-8 at most).
 __device__ __forceinline__ uint64_t turn_fraction(double frequency) {
     const double turns = fabs(frequency) * 0.15915494309189533577;
     const uint64_t g = static_cast<uint64_t>((turns - floor(turns)) * 18446744073709551616.0);  // (an exact difference)
     return frequency < 0.0 ? 0 - g : g;
 }
+__device__ __forceinline__ void cos_sin(uint64_t part, float factor, float& c, float& s) {
+    const uint32_t u = static_cast<uint32_t>(part >> 32);
+    const uint32_t quarter = (u + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<int32_t>(u - (quarter << 30))) * 1.46291807926716e-9f;  // 2 pi / 2^32
+    const float t = x * x;
+    float ps = fmaf(t, 1.f / 362880.f, -1.f / 5040.f), pc = fmaf(t, 1.f / 40320.f, -1.f / 720.f);
+    ps = fmaf(t, ps, 1.f / 120.f), pc = fmaf(t, pc, 1.f / 24.f);
+    ps = fmaf(t, ps, -1.f / 6.f), pc = fmaf(t, pc, -0.5f);
+    ps = fmaf(t * x, ps, x), pc = fmaf(t, pc, 1.f);
+    const bool swap = (quarter & 1) != 0;
+    c = __uint_as_float(__float_as_uint((swap ? ps : pc) * factor) ^ ((quarter + 1) & 2) << 30);
+    s = __uint_as_float(__float_as_uint((swap ? pc : ps) * factor) ^ (quarter & 2) << 30);
+}
+template <int kV>
 __global__ void __launch_bounds__(kThreads) rotary_table_kernel(const double* __restrict__ frequencies, int half, int64_t first,
                                                                 int64_t positions, float factor, float* __restrict__ table) {
+    extern __shared__ uint64_t turns[];  // double arithmetic is slow here: once a frequency
     grid_dependency_wait();
     allow_dependents();
-    const int64_t all = positions * half;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; x < all; x += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t p = x / half;
-        const int i = static_cast<int>(x - p * half);
-        const uint64_t g = turn_fraction(frequencies[i]);
-        const int64_t part = static_cast<int64_t>(static_cast<uint64_t>(first + p) * g);  // of a turn, -1/2 .. 1/2
-        float s, c;
-        sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
-        table[p * 2 * half + i] = c * factor;
-        table[p * 2 * half + half + i] = s * factor;
+    for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn_fraction(frequencies[i]);
+    __syncthreads();
+    const int64_t per_row = half / kV;
+    const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads / per_row;  // rows (the last threads may have none)
+    int64_t p = thread / per_row;
+    const int i = static_cast<int>(thread - p * per_row) * kV;
+    if (p >= step || p >= positions) return;
+    uint64_t at[kV], by[kV];
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+        at[e] = static_cast<uint64_t>(first + p) * turns[i + e];
+        by[e] = static_cast<uint64_t>(step) * turns[i + e];
+    }
+    float* row = table + p * 2 * half + i;
+    for (; p < positions; p += step, row += step * 2 * half) {
+        float c[kV], s[kV];
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            cos_sin(at[e], factor, c[e], s[e]);
+            at[e] += by[e];
+        }
+        if (kV == 4) {
+            *reinterpret_cast<float4*>(row) = make_float4(c[0], c[1], c[2], c[kV - 1]);
+            *reinterpret_cast<float4*>(row + half) = make_float4(s[0], s[1], s[2], s[kV - 1]);
+        } else {
+            row[0] = c[0];
+            row[half] = s[0];
+        }
     }
 }
 
@@ -347,9 +545,14 @@ cudaError_t launch_append_rotary(const RotaryAppendArgs& a, const pkv_cache_desc
 
 cudaError_t launch_rotary_table(const double* frequencies, int half, int64_t first, int64_t positions, float factor, float* table,
                                 cudaStream_t s) {
-    const int64_t want = (positions * half + kThreads - 1) / kThreads, most = static_cast<int64_t>(device_sm_count()) * 16;
-    return launch_pdl(rotary_table_kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kThreads), 0, s, frequencies, half,
-                      first, positions, factor, table);
+    const int64_t threads = positions * half / (half % 4 ? 1 : 4);
+    const int64_t want = (threads + kThreads - 1) / kThreads, most = static_cast<int64_t>(device_sm_count()) * 8;
+    // (at least a row's threads)
+    const int64_t row = (half / (half % 4 ? 1 : 4) + kThreads - 1) / kThreads;
+    const dim3 grid(static_cast<unsigned>(want < row ? row : want < most ? want : most));
+    const size_t smem = static_cast<size_t>(half) * sizeof(uint64_t);
+    if (half % 4) return launch_pdl(rotary_table_kernel<1>, grid, dim3(kThreads), smem, s, frequencies, half, first, positions, factor, table);
+    return launch_pdl(rotary_table_kernel<4>, grid, dim3(kThreads), smem, s, frequencies, half, first, positions, factor, table);
 }
 
 }  // namespace pkv

@@ -489,13 +489,16 @@ def pkv_decode_attention_q8(q, k_codes, v_codes, scales, block_tables, context_l
 # kept to a few attribute reads per tensor.
 def _here() -> int:
     try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):                   # no CUDA device: no tensor is on one
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):                   # no CUDA device: no tensor is on one
         return -2
 
 
 def _on(here: int, name: str, t: torch.Tensor, dtype=None, shape=None) -> int:
     """Address of contiguous tensor ``t`` of this dtype and shape on CUDA device ``here``."""
+    if (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape) and t.get_device() == here and \
+            t.is_contiguous():
+        return t.data_ptr()
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} is {str(dtype)[6:]}, not {str(t.dtype)[6:]}")
     if shape is not None and t.shape != shape:
@@ -851,14 +854,15 @@ def pkv_rotary_table(frequencies, num_positions: int, first_position: int = 0, f
 
 def _token_rows(here, name, t, dtype, shape):
     """(address, stride between tokens) of rows [tokens][heads][head_dim] that may lie apart."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} is {str(dtype)[6:]} {list(shape)}, not {str(t.dtype)[6:]} {list(t.shape)}")
     if t.get_device() != here:
         raise ValueError(f"libpkv takes CUDA tensors only, on the current device ({name} is on {t.device})")
     tokens, heads, d = shape
-    if tokens and heads and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    token, head, one = t.stride()
+    if tokens and heads and (one != 1 or (heads > 1 and head != d)):
         raise ValueError(f"a token's heads in {name} follow one another")
-    return t.data_ptr(), t.stride(0) if tokens > 1 else heads * d
+    return t.data_ptr(), token if tokens > 1 else heads * d
 
 
 def pkv_append_rotary(q, k, v, positions, table, slot_mapping, k_cache, v_cache=None, scales=None,
@@ -928,16 +932,17 @@ def pkv_plan_step(context_lens, new_tokens, held_blocks, free_blocks, free_count
           free_blocks.shape[0], _on(here, "free_count", free_count, i32, (1,)),
           _on(here, "block_tables", block_tables, i32), max_blocks, batch, num_rows, num_blocks)
     if out is None:
-        # one allocation: rows of 8 bytes, then everything of 4, each part on a 16-byte boundary
-        parts = [(num_rows, torch.int64)] + [(n, i32) for n in (num_rows, batch + 1, batch, batch, 1, 2)]
-        sizes = [(n * t.itemsize + 15) // 16 * 16 for n, t in parts]
-        memory = _made(stream, torch.empty, max(16, sum(sizes)), dtype=torch.uint8, device=dev)
-        out, where = [], 0
-        for (n, t), size in zip(parts, sizes):
-            out.append(memory[where:where + n * t.itemsize].view(t))
-            where += size
-        out = tuple(out)
-        outs = [t.data_ptr() for t in out]
+        sizes = (num_rows, batch + 1, batch, batch, 1, 2)
+        if num_rows < 0:
+            raise ValueError("num_rows is at least 0")
+        slots = _made(stream, torch.empty, num_rows, dtype=torch.int64, device=dev)
+        rest = _made(stream, torch.empty, num_rows + 3 * batch + 4, dtype=i32, device=dev)
+        out = (slots, *rest.split(sizes))
+        start = rest.data_ptr()
+        outs = [slots.data_ptr()]
+        for n in sizes:
+            outs.append(start)
+            start += 4 * n
     else:
         shapes = ((num_rows,), (num_rows,), (batch + 1,), one, one, (1,), (2,))
         names = ("slot_mapping", "positions", "query_start", "new_context_lens", "new_held_blocks", "new_free_count",
