@@ -37,12 +37,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kIssueLanes = 8;  // stages whose copies are issued together
-// A CTA gets at least about this many blocks: fewer CTAs then, and fewer pieces to merge.
-constexpr int kLeastBlocks = 8;
-// Cost of a segment shorter than kShortBlocks beside its blocks, in blocks.
-constexpr int kSegmentCost = 6, kShortBlocks = 256;
-// (so no CTA's range is empty, and a segment's pieces lie in consecutive CTAs)
-static_assert(kLeastBlocks >= 1 + kSegmentCost, "a range covers the dearest unit");
+// Cost of a segment shorter than kShortBlocks beside its blocks, in blocks, where there are
+// blocks enough for every CTA.
+#ifndef MQ4_SEG
+#define MQ4_SEG 16
+#endif
+#ifndef MQ4_LEAST
+#define MQ4_LEAST 8
+#endif
+constexpr int kSegmentCost = MQ4_SEG, kShortBlocks = 256;
+// Where there are not, a CTA gets about this many blocks.
+constexpr int kLeastBlocks = MQ4_LEAST;
 
 // The base m of a row: where some P' = 2^(x - m) v would leave f16 it moves to the largest
 // x + log2 |v| less kHeadroom, so that what is rounded to f16 lies high in its range for
@@ -53,6 +58,7 @@ constexpr float kMostSum = 5.1922969e33f;        // 2^112
 constexpr float kTinyScale = 1.2621774e-29f;     // 2^-96
 // Stages (32 tokens) whose eights are summed in O before they are taken out again.
 constexpr int kFold = 8;
+constexpr int kMergeAhead = 8;  // pieces whose loads a merge has in flight
 constexpr float kUnset = -3.0e38f;               // base of a row that has seen no token
 
 // A piece of a segment, as the producer lays it out for the consumers.
@@ -90,7 +96,7 @@ struct M4 {
     static constexpr int kOffPieces = kOffState + kConsumers * kStateFloats * 4;  // per slot; then the cut ones, and their number
     static constexpr int kOffQ = kOffPieces + (kQSlots + 2) * sizeof(Piece4) + 16;
     static size_t smem_bytes(int warps_per_unit, int batch) {
-        return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + 3 * static_cast<size_t>(batch) * 4;
+        return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + (3 * static_cast<size_t>(batch) + 1) * 4;
     }
     static_assert(kOffBars % 16 == 0 && kOffQ % 16 == 0, "alignment");
 };
@@ -109,6 +115,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float f16x2_sum(uint32_t h) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return f.x + f.y;
+}
+// Adds to a counter, ordered after what the warp has written and before what it reads next.
+__device__ __forceinline__ int add_acq_rel(int* p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 // D = A B + C for f16 A (16 x 16) and B (16 x 8), C and D apart.
 __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
@@ -167,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
     int32_t* s_pre = reinterpret_cast<int32_t*>(q_rows + C::kQSlots * q_bytes);  // blocks, cost up to and with each sequence; length
     int32_t* s_cost = s_pre + a.batch;
     int32_t* s_len = s_cost + a.batch;
+    int32_t* s_active = s_len + a.batch;  // sequences with blocks
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group;
 
@@ -207,10 +220,11 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int blocks = 0, cost = 0;
+        int blocks = 0, cost = 0, active = 0;
         for (int base = 0; base < a.batch; base += 32) {
             int x = base + lane < a.batch ? s_pre[base + lane] : 0;
             int y = x > 0 && x < kShortBlocks ? x + kSegmentCost : x;
+            active += __popc(__ballot_sync(0xffffffffu, x > 0));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x1 = __shfl_up_sync(0xffffffffu, x, o), y1 = __shfl_up_sync(0xffffffffu, y, o);
@@ -223,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
             blocks += __shfl_sync(0xffffffffu, x, 31);
             cost += __shfl_sync(0xffffffffu, y, 31);
         }
+        if (lane == 0) *s_active = active;
     }
     __syncthreads();
     if (a.qstart == nullptr) {
@@ -235,17 +250,28 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
         }
     }
     const long long U = static_cast<long long>(a.kv_heads) * s_pre[a.batch - 1];
+    if (U == 0) return;
     const int cta = blockIdx.x;
-    const long long wanted = U / kLeastBlocks;
-    const long long ctas = wanted < 1 ? 1 : wanted < gridDim.x ? wanted : gridDim.x;
-    if (U == 0 || cta >= ctas) return;
+    // Few blocks: fewer CTAs, as many for each segment, whose cuts then fall between segments of one
+    // length (a CTA with two pieces takes them one after the other). (No range is empty, so a segment's
+    // pieces lie in consecutive CTAs.)
+    long long ctas = quotient(U, kLeastBlocks);
+    const bool few = ctas < gridDim.x;
+    if (few) {
+        const long long segments = static_cast<long long>(a.kv_heads) * *s_active;
+        ctas = ctas < 1 ? 1 : ctas >= segments ? quotient(ctas, segments) * segments : ctas;
+    } else {
+        ctas = gridDim.x;
+    }
+    const bool weighted = !few && static_cast<long long>(a.kv_heads) * s_cost[a.batch - 1] >= ctas * (1 + kSegmentCost);
+    if (cta >= ctas) return;
 
     if (warp == kConsumers) {
         // ------------------------------------------------ producer
         const uint64_t policy = l2_evict_first_policy(), q_policy = l2_evict_last_policy();
         const uint8_t* cache = static_cast<const uint8_t*>(a.cache);
         CostSplit split;
-        split.init(s_pre, s_cost, a.batch, a.kv_heads, 1 + kSegmentCost, ctas);
+        split.init(s_pre, weighted ? s_cost : s_pre, a.batch, a.kv_heads, weighted ? 1 + kSegmentCost : 1, ctas);
         Walker wk;
         wk.init(s_pre, a.batch, a.kv_heads, split.start(cta), split.start(cta + 1));
         uint32_t k = 0;  // stages issued
@@ -660,30 +686,47 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
     // ---- announce this warp's share of the cut pieces; the warp that completes a count merges them
     const int ncut = *num_cuts;
     if (ncut == 0) return;
-    __threadfence();
     __syncwarp();
     int old = 0;
-    if (lane < ncut) old = atomicAdd(a.counters + (static_cast<long long>(cuts[lane].seq) * a.kv_heads + cuts[lane].head) * kConsumers + warp, 1);
+    if (lane < ncut) old = add_acq_rel(a.counters + (static_cast<long long>(cuts[lane].seq) * a.kv_heads + cuts[lane].head) * kConsumers + warp, 1);
+    __syncwarp();
     for (int i = 0; i < ncut; ++i) {
         const Piece4& pc = cuts[i];
         if (__shfl_sync(0xffffffffu, old, i) != pc.pieces - 1) continue;
-        __threadfence();
         constexpr int kPer = D / 16;
         const int row8 = lane >> 2, d0 = warp * (D / 4) + (lane & 3) * kPer;
         for (int tile = 0; tile * 8 < pc.rows; ++tile) {
             float M = kUnset, L = 0.f, O[kPer] = {};
-#pragma unroll 4
-            for (int p = 0; p < pc.pieces; ++p) {
-                const float* sl = piece_of(a, D, pc.first_cta + p, p == 0 ? pc.slot0 : 0, tile);
-                const float mp = __ldcg(sl + 8 * D + warp * 16 + row8), lp = __ldcg(sl + 8 * D + warp * 16 + 8 + row8);
-                const float to = fmaxf(M, mp), keep = ex2(M - to), w = ex2(mp - to);
-                M = to;
-                L = L * keep + w * lp;
+            for (int p0 = 0; p0 < pc.pieces; p0 += kMergeAhead) {
+                // several pieces' loads in flight at once (past the last: the last again, without weight)
+                float mp[kMergeAhead], lp[kMergeAhead];
+                float4 v[kMergeAhead][kPer / 4];
 #pragma unroll
-                for (int e = 0; e < kPer; e += 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + row8 * D + d0 + e));
-                    O[e] = O[e] * keep + w * v.x, O[e + 1] = O[e + 1] * keep + w * v.y;
-                    O[e + 2] = O[e + 2] * keep + w * v.z, O[e + 3] = O[e + 3] * keep + w * v.w;
+                for (int u = 0; u < kMergeAhead; ++u) {
+                    const int p = min(p0 + u, pc.pieces - 1);
+                    const float* sl = piece_of(a, D, pc.first_cta + p, p == 0 ? pc.slot0 : 0, tile);
+                    mp[u] = p0 + u < pc.pieces ? __ldcg(sl + 8 * D + warp * 16 + row8) : kUnset;
+                    lp[u] = __ldcg(sl + 8 * D + warp * 16 + 8 + row8);
+#pragma unroll
+                    for (int e = 0; e < kPer; e += 4) v[u][e / 4] = __ldcg(reinterpret_cast<const float4*>(sl + row8 * D + d0 + e));
+                }
+                float to = M;
+#pragma unroll
+                for (int u = 0; u < kMergeAhead; ++u) to = fmaxf(to, mp[u]);
+                const float keep = ex2(M - to);
+                M = to;
+                L *= keep;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) O[e] *= keep;
+#pragma unroll
+                for (int u = 0; u < kMergeAhead; ++u) {
+                    const float w = p0 + u < pc.pieces ? ex2(mp[u] - to) : 0.f;
+                    L += w * lp[u];
+#pragma unroll
+                    for (int e = 0; e < kPer; e += 4) {
+                        O[e] += w * v[u][e / 4].x, O[e + 1] += w * v[u][e / 4].y;
+                        O[e + 2] += w * v[u][e / 4].z, O[e + 3] += w * v[u][e / 4].w;
+                    }
                 }
             }
             if (tile * 8 + row8 < pc.rows) write_part<D>(a, pc.q0, pc.head, tile * 8 + row8, d0, O, L);
