@@ -1,5 +1,6 @@
 """Build libpkv.so in-tree: every .cu (and host-only .cpp) under csrc/,
-compiled for sm_103a.
+compiled for sm_103a; and _pkv_calls.so, the serving calls' binding to torch
+tensors (binding/pkv_calls.cpp, host code, against the installed torch).
 
 Usage: ``python -m paged_kv_cache_209_gb300.build`` (or call ``build()``).
 Objects go to ``_build/`` beside this file; the shared library lands next to
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
+BINDING = os.path.join(HERE, "binding", "pkv_calls.cpp")
+CALLS = os.path.join(HERE, "_pkv_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -47,6 +51,31 @@ def _compile(src: str, obj: str, extra: list[str]) -> tuple[str, int, str]:
     return src, p.returncode, (p.stdout + p.stderr)
 
 
+def _binding_command() -> list[str]:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+            "-I", INCLUDE, "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING, "-o", CALLS, "-L", os.path.join(home, "lib"),
+            # (libpkv's symbols are found when the binding is loaded, beside it)
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
+def _binding_stale() -> bool:
+    import torch
+    inputs = [BINDING, torch.version.__file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return not os.path.exists(CALLS) or os.path.getmtime(CALLS) < max(os.path.getmtime(p) for p in inputs)
+
+
+def _build_binding(force: bool) -> None:
+    if force or _binding_stale():
+        p = subprocess.run(_binding_command(), capture_output=True, text=True)
+        if p.returncode:
+            raise RuntimeError("g++ failed on " + BINDING + "\n" + p.stdout + p.stderr)
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
           defines: dict | None = None, out_dir: str | None = None) -> str:
     """Compile and link ``libpkv.so``; returns its path. Raises on failure.
@@ -70,6 +99,10 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
             os.path.getmtime(obj) < max(os.path.getmtime(src), hdr_time)
         if stale:
             jobs.append((src, obj))
+    binding = None
+    binder = cf.ThreadPoolExecutor(max_workers=1)
+    if out_dir is None:
+        binding = binder.submit(_build_binding, force)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             for src, rc, log in ex.map(lambda j: _compile(j[0], j[1], extra), jobs):
@@ -83,6 +116,9 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
         p = subprocess.run(cmd, capture_output=True, text=True)
         if p.returncode:
             raise RuntimeError("link failed:\n" + p.stdout + p.stderr)
+    if binding is not None:
+        binding.result()
+    binder.shutdown()
     return lib_path
 
 

@@ -62,6 +62,7 @@ class DecodeOpts(ctypes.Structure):
 
 
 _lib = None
+_native = None
 
 EXPORTS = ("pkv_append", "pkv_copy_blocks", "pkv_decode_workspace_size", "pkv_decode_attention",
            "pkv_decode_prefixed_workspace_size", "pkv_decode_attention_prefixed", "pkv_decode_attention_noalloc",
@@ -181,6 +182,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+def _calls():
+    """The native binding (binding/pkv_calls.cpp) of the calls whose launches are shorter than their marshalling
+    in Python."""
+    global _native
+    if _native is None:
+        load_library()
+        path = os.path.join(_HERE, "_pkv_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with paged_kv_cache_209_gb300.build.build()")
+        # its calls resolve against libpkv.so, which is loaded for everything that comes after
+        ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_GLOBAL)
+        from . import _pkv_calls
+        _native = _pkv_calls
+    return _native
 
 
 def _check(fn: str, status: int) -> None:
@@ -517,7 +534,9 @@ def _desc(nb: int, bs: int, hkv: int, d: int, dtype: int) -> CacheDesc:
 
 
 def _raw_stream(stream, here: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
+    if stream is not None:
+        return _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(here) if here >= 0 else 0
 
 
 def _q8_geometry(k_codes, v_codes, scales):
@@ -715,16 +734,9 @@ def _q4_geometry(cache):
 
 def pkv_append_q4(k, v, slot_mapping, cache, flags: int = 0, stream=None) -> None:
     """Quantizing slot-mapped append of bf16 k/v [tokens][kv_heads][head_dim] into the 4-bit cache."""
-    lib = _lib or load_library()
-    nb, hkv, d = _q4_geometry(cache)
     here = _here()
-    if slot_mapping.dim() != 1:
-        raise ValueError("slot_mapping is [tokens]")
-    tokens = slot_mapping.shape[0]
-    want = (tokens, hkv, d)
-    status = lib.pkv_append_q4(_on(here, "k", k, torch.bfloat16, want), _on(here, "v", v, torch.bfloat16, want),
-                               _on(here, "slot_mapping", slot_mapping, torch.int64), tokens, _on(here, "cache", cache),
-                               _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    _, status = (_native or _calls()).append_rotary(here, None, k, v, None, None, slot_mapping, cache, None, None, False, None, flags,
+                                                    _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_append_q4", status)
 
@@ -745,17 +757,16 @@ def pkv_copy_blocks_q4(src_dst_pairs, cache, flags: int = 0, stream=None) -> Non
 def pkv_gather_q4(cache, block_tables, context_lens, row_start, num_rows: int, token_start=None,
                   out_dtype=torch.bfloat16, k_out=None, v_out=None, flags: int = 0, stream=None):
     """``pkv_gather`` over the 4-bit cache: the values (code * scale) as ``out_dtype``, bf16 or float32."""
-    lib = _lib or load_library()
-    nb, hkv, d = _q4_geometry(cache)
-    code = _dtype_code(out_dtype)
     here = _here()
-    pool = _on(here, "cache", cache)
-    args, k_out, v_out = _gather_args(here, hkv, d, block_tables, context_lens, row_start, num_rows, token_start, k_out,
-                                      v_out, out_dtype, cache, stream)
-    status = lib.pkv_gather_q4(pool, *args, code, _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    if stream is not None:
+        nb, hkv, d = _q4_geometry(cache)
+        k_out, v_out = (_made(stream, torch.empty, (num_rows, hkv, d), dtype=out_dtype, device=cache.device) if t is None else t
+                        for t in (k_out, v_out))
+    out, status = (_native or _calls()).gather_q4(here, cache, block_tables, context_lens, row_start, num_rows, token_start,
+                                                  _dtype_code(out_dtype), k_out, v_out, flags, _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_gather_q4", status)
-    return k_out, v_out
+    return out
 
 
 def pkv_multiquery_q4_workspace_size(batch: int, num_q_heads: int, max_blocks_per_seq: int, max_query_len: int,
@@ -769,32 +780,16 @@ def pkv_multiquery_q4_workspace_size(batch: int, num_q_heads: int, max_blocks_pe
 
 def _attention_q4(name, q, cache, block_tables, context_lens, query_start, scale, max_query_len, out, workspace, flags,
                   stream):
-    lib = _lib or load_library()
-    nb, hkv, d = _q4_geometry(cache)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != d:
-        raise ValueError("q is bf16 [rows][q_heads][head_dim]")
-    rows, q_heads, _ = q.shape
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables is [batch][max_blocks]")
-    batch, max_blocks = block_tables.shape
-    if query_start is None and rows != batch:
-        raise ValueError("q has one row per sequence")
-    new = out is None
-    if new:
-        out = _made(stream, torch.empty_like, q)
-    if workspace is None:
-        need = pkv_multiquery_q4_workspace_size(batch, q_heads, max_blocks, max_query_len, cache)
-        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
     here = _here()
-    lens = _on(here, "context_lens", context_lens, torch.int32, (batch,))
-    middle = (batch, q_heads) if query_start is None else \
-        (_on(here, "query_start", query_start, torch.int32, (batch + 1,)), batch, q_heads, max_query_len)
-    args = (_on(here, "q", q), _on(here, "cache", cache), _on(here, "block_tables", block_tables, torch.int32), max_blocks,
-            lens, *middle, scale, out.data_ptr() if new else _on(here, "out", out, torch.bfloat16, q.shape),
-            _on(here, "workspace", workspace), workspace.numel() * workspace.element_size())
-    if rows == 0:                                            # no query anywhere: no row to write
-        return out
-    status = getattr(lib, name)(*args, _desc(nb, 16, hkv, d, PKV_INT4), flags, _raw_stream(stream, here))
+    if workspace is None:
+        if q.dim() != 3 or block_tables.dim() != 2:
+            raise ValueError("q is bf16 [rows][q_heads][head_dim], block_tables [batch][max_blocks]")
+        need = pkv_multiquery_q4_workspace_size(block_tables.shape[0], q.shape[1], block_tables.shape[1], max_query_len, cache)
+        workspace = _made(stream, torch.zeros, max(need, 256), dtype=torch.uint8, device=q.device)
+    if out is None and stream is not None:
+        out = _made(stream, torch.empty_like, q)
+    out, status = (_native or _calls()).attention_q4(here, q, cache, block_tables, context_lens, query_start, scale, max_query_len,
+                                                     out, workspace, flags, _raw_stream(stream, here))
     if status:
         raise PkvError(name, status)
     return out
@@ -836,33 +831,14 @@ def pkv_rotary_table(frequencies, num_positions: int, first_position: int = 0, f
                      stream=None):
     """``factor`` times the cosines, then the sines, of positions ``first_position ..``: float32
     [num_positions][rotary_dim]; ``frequencies`` float64 [rotary_dim // 2] on the device."""
-    lib = _lib or load_library()
     here = _here()
-    if frequencies.dim() != 1:
-        raise ValueError("frequencies are [rotary_dim / 2]")
-    dim = 2 * frequencies.shape[0]
-    want = (num_positions, dim)
-    at = _on(here, "frequencies", frequencies, torch.float64)
-    if out is None:
-        out = _made(stream, torch.empty, want, dtype=torch.float32, device=frequencies.device)
-    status = lib.pkv_rotary_table(at, dim, first_position, num_positions, factor, _on(here, "out", out, torch.float32, want),
-                                  _raw_stream(stream, here))
+    if out is None and stream is not None:
+        out = _made(stream, torch.empty, (num_positions, 2 * frequencies.shape[0]), dtype=torch.float32, device=frequencies.device)
+    out, status = (_native or _calls()).rotary_table(here, frequencies, num_positions, first_position, factor, out,
+                                                     _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_rotary_table", status)
     return out
-
-
-def _token_rows(here, name, t, dtype, shape):
-    """(address, stride between tokens) of rows [tokens][heads][head_dim] that may lie apart."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} is {str(dtype)[6:]} {list(shape)}, not {str(t.dtype)[6:]} {list(t.shape)}")
-    if t.get_device() != here:
-        raise ValueError(f"libpkv takes CUDA tensors only, on the current device ({name} is on {t.device})")
-    tokens, heads, d = shape
-    token, head, one = t.stride()
-    if tokens and heads and (one != 1 or (heads > 1 and head != d)):
-        raise ValueError(f"a token's heads in {name} follow one another")
-    return t.data_ptr(), token if tokens > 1 else heads * d
 
 
 def pkv_append_rotary(q, k, v, positions, table, slot_mapping, k_cache, v_cache=None, scales=None,
@@ -871,44 +847,11 @@ def pkv_append_rotary(q, k, v, positions, table, slot_mapping, k_cache, v_cache=
     or float32 pools (``k_cache``, ``v_cache``), int8 pools (with ``scales``) or a 4-bit cache (``k_cache`` alone).
     q, k and v are [tokens][heads][head_dim], a token's heads together, tokens any stride apart; q may be None.
     Returns q's turned rows (``q_out``, which may be q itself; None without q)."""
-    lib = _lib or load_library()
     here = _here()
-    if scales is not None:
-        nb, hkv, bs, d = _q8_geometry(k_cache, v_cache, scales)
-        dtype, code = torch.bfloat16, PKV_INT8
-    elif v_cache is None:
-        nb, hkv, d = _q4_geometry(k_cache)
-        bs, dtype, code = 16, torch.bfloat16, PKV_INT4
-    else:
-        _same_pools(k_cache, v_cache)
-        if k_cache.dim() != 4:
-            raise ValueError("a pool is [num_blocks][num_kv_heads][16][head_dim]")
-        nb, hkv, bs, d = k_cache.shape
-        dtype, code = k_cache.dtype, _dtype_code(k_cache.dtype)
-    if slot_mapping.dim() != 1 or table.dim() != 2:
-        raise ValueError("slot_mapping is [tokens], table [positions][rotary_dim]")
-    tokens = slot_mapping.shape[0]
-    k_at, k_stride = _token_rows(here, "k", k, dtype, (tokens, hkv, d))
-    v_at, v_stride = _token_rows(here, "v", v, dtype, (tokens, hkv, d))
-    heads = q_stride = out_stride = 0
-    q_at = out_at = None
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q is [tokens][q_heads][head_dim]")
-        heads = q.shape[1]
-        q_at, q_stride = _token_rows(here, "q", q, dtype, (tokens, heads, d))
-        if q_out is None:
-            q_out = _made(stream, torch.empty, (tokens, heads, d), dtype=dtype, device=q.device)
-        out_at, out_stride = _token_rows(here, "q_out", q_out, dtype, (tokens, heads, d))
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    status = lib.pkv_append_rotary(
-        q_at, q_stride, k_at, k_stride, v_at, v_stride, _on(here, "positions", positions, torch.int32, (tokens,)),
-        _on(here, "table", table, torch.float32), table.shape[0], table.shape[1], int(interleaved),
-        _on(here, "slot_mapping", slot_mapping, torch.int64), tokens, heads, out_at, out_stride,
-        _on(here, "k_cache", k_cache), None if v_cache is None else _on(here, "v_cache", v_cache),
-        None if scales is None else _on(here, "scales", scales), _desc(nb, bs, hkv, d, code), flags,
-        _raw_stream(stream, here))
+    if q is not None and q_out is None and stream is not None:
+        q_out = _made(stream, torch.empty, q.shape, dtype=q.dtype, device=q.device)
+    q_out, status = (_native or _calls()).append_rotary(here, q, k, v, positions, table, slot_mapping, k_cache, v_cache, scales,
+                                                        interleaved, q_out, flags, _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_append_rotary", status)
     return q_out
@@ -920,38 +863,13 @@ def pkv_plan_step(context_lens, new_tokens, held_blocks, free_blocks, free_count
     int32 [batch + 1], new_context_lens, new_held_blocks int32 [batch], new_free_count int32 [1], result int32 [2])``
     and writes the new entries of ``block_tables``; ``result`` holds the rows planned and the blocks missing.
     ``out`` takes such a tuple to write into."""
-    lib = _lib or load_library()
     here = _here()
-    i32, dev = torch.int32, block_tables.device
-    if block_tables.dim() != 2 or free_blocks.dim() != 1:
-        raise ValueError("block_tables is [batch][max_blocks], free_blocks [capacity]")
-    batch, max_blocks = block_tables.shape
-    one = (batch,)
-    at = (_on(here, "context_lens", context_lens, i32, one), _on(here, "new_tokens", new_tokens, i32, one),
-          _on(here, "held_blocks", held_blocks, i32, one), _on(here, "free_blocks", free_blocks, i32),
-          free_blocks.shape[0], _on(here, "free_count", free_count, i32, (1,)),
-          _on(here, "block_tables", block_tables, i32), max_blocks, batch, num_rows, num_blocks)
-    if out is None:
-        sizes = (num_rows, batch + 1, batch, batch, 1, 2)
-        if num_rows < 0:
-            raise ValueError("num_rows is at least 0")
-        slots = _made(stream, torch.empty, num_rows, dtype=torch.int64, device=dev)
-        rest = _made(stream, torch.empty, num_rows + 3 * batch + 4, dtype=i32, device=dev)
-        out = (slots, *rest.split(sizes))
-        start = rest.data_ptr()
-        outs = [slots.data_ptr()]
-        for n in sizes:
-            outs.append(start)
-            start += 4 * n
-    else:
-        shapes = ((num_rows,), (num_rows,), (batch + 1,), one, one, (1,), (2,))
-        names = ("slot_mapping", "positions", "query_start", "new_context_lens", "new_held_blocks", "new_free_count",
-                 "result")
-        outs = [_on(here, name, t, torch.int64 if i == 0 else i32, shape)
-                for i, (name, t, shape) in enumerate(zip(names, out, shapes))]
-        if len(outs) != 7:
-            raise ValueError(f"out holds {', '.join(names)}")
-    status = lib.pkv_plan_step(*at, *outs, flags, _raw_stream(stream, here))
+    if out is None and stream is not None:
+        batch, dev = block_tables.shape[0], block_tables.device
+        out = tuple(_made(stream, torch.empty, n, dtype=t, device=dev) for n, t in (
+            (num_rows, torch.int64), *((n, torch.int32) for n in (num_rows, batch + 1, batch, batch, 1, 2))))
+    out, status = (_native or _calls()).plan_step(here, context_lens, new_tokens, held_blocks, free_blocks, free_count, block_tables,
+                                                  num_rows, num_blocks, out, flags, _raw_stream(stream, here))
     if status:
         raise PkvError("pkv_plan_step", status)
     return out
