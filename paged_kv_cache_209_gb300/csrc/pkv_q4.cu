@@ -471,144 +471,153 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
                 const uint8_t* st = smem + s * C::kStageBytes;
                 // every token of the stage exists and every row sees it
                 const bool whole = there == 3 && blk * 16 + 31 <= least;
-                float sc[R][2][4];  // per block: tokens gid, gid + 8 by 2 columns
-                float f[R][8];      // the scores' factors
-                float sv[4];
+                // (two blocks at a time with one tile of rows, to have several chains in flight; one with two tiles, for the registers)
+                constexpr int kAt = R == 1 ? 2 : 1;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint8_t* rec = st + b * C::kRecord;
-                    uint32_t wa[D / 32], wb[D / 32];
-                    if (D == 128) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(rec + gid * 64 + tig * 16), v = *reinterpret_cast<const uint4*>(rec + (gid + 8) * 64 + tig * 16);
-                        wa[0] = u.x, wa[1] = u.y, wa[D / 32 - 2] = u.z, wa[D / 32 - 1] = u.w;
-                        wb[0] = v.x, wb[1] = v.y, wb[D / 32 - 2] = v.z, wb[D / 32 - 1] = v.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(rec + gid * 32 + tig * 8), v = *reinterpret_cast<const uint2*>(rec + (gid + 8) * 32 + tig * 8);
-                        wa[0] = u.x, wa[1] = u.y;
-                        wb[0] = v.x, wb[1] = v.y;
-                    }
+                for (int b0 = 0; b0 < 2; b0 += kAt) {
+                    float sc[R][kAt][4];  // per block: tokens gid, gid + 8 by 2 columns
+                    float f[R][4 * kAt];  // the scores' factors
+                    float sv[2 * kAt];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
+                    for (int b = 0; b < kAt; ++b) {
+                        const uint8_t* rec = st + (b0 + b) * C::kRecord;
+                        uint32_t wa[D / 32], wb[D / 32];
+                        if (D == 128) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(rec + gid * 64 + tig * 16), v = *reinterpret_cast<const uint4*>(rec + (gid + 8) * 64 + tig * 16);
+                            wa[0] = u.x, wa[1] = u.y, wa[D / 32 - 2] = u.z, wa[D / 32 - 1] = u.w;
+                            wb[0] = v.x, wb[1] = v.y, wb[D / 32 - 2] = v.z, wb[D / 32 - 1] = v.w;
+                        } else {
+                            const uint2 u = *reinterpret_cast<const uint2*>(rec + gid * 32 + tig * 8), v = *reinterpret_cast<const uint2*>(rec + (gid + 8) * 32 + tig * 8);
+                            wa[0] = u.x, wa[1] = u.y;
+                            wb[0] = v.x, wb[1] = v.y;
+                        }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t u = h ? wa[c] >> 8 : wa[c], v = h ? wb[c] >> 8 : wb[c];
+                        for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
-                            for (int r = 0; r < R; ++r) {
-                                if (c + h == 0)
-                                    mma_f16_from(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][0][0], qf[r][0][1],
-                                                 kb[r][0], kb[r][1]);
-                                else
-                                    mma_f16_16816(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
-                                                  qf[r][2 * c + h][1]);
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t u = h ? wa[c] >> 8 : wa[c], v = h ? wb[c] >> 8 : wb[c];
+#pragma unroll
+                                for (int r = 0; r < R; ++r) {
+                                    if (c + h == 0)
+                                        mma_f16_from(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][0][0], qf[r][0][1],
+                                                     kb[r][0], kb[r][1]);
+                                    else
+                                        mma_f16_16816(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
+                                                      qf[r][2 * c + h][1]);
+                                }
                             }
                         }
-                    }
-                    const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
-                    const float ka = scales[gid], kc = scales[gid + 8];
-                    sv[2 * b] = scales[16 + gid];
-                    sv[2 * b + 1] = scales[24 + gid];
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[r][4 * b + e] = (e & 2 ? kc : ka) * cf[r][e & 1];
-                }
-                uint4 vw[2][D / 64];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-                        vw[b][h] = *reinterpret_cast<const uint4*>(st + b * C::kRecord + q4_v_offset(D) + gid * 64 + tig * 16 + h * 512);
-                __syncwarp();  // everything is in registers
-                if (lane == 0) mbar_arrive(&empty[s]);
-                if (!whole) {  // what a row does not see: a score of -inf
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = blk * 16 + 16 * (i >> 1) + 8 * (i & 1) + gid;
-                        const bool in = (there >> (i >> 1) & 1) != 0;
+                        const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
+                        const float ka = scales[gid], kc = scales[gid + 8];
+                        sv[2 * b] = scales[16 + gid];
+                        sv[2 * b + 1] = scales[24 + gid];
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                if (!in || p > lim[r][c]) {
-                                    sc[r][i >> 1][2 * (i & 1) + c] = __int_as_float(0xff800000);
-                                    f[r][2 * i + c] = 1.f;
-                                }
+                            for (int e = 0; e < 4; ++e) f[r][4 * b + e] = (e & 2 ? kc : ka) * cf[r][e & 1];
                     }
-                }
-                float e[R][8], sum[R][2];
-                uint32_t p[R][4];
-                uint32_t top = 0;
-                float most = 0.f;
-                auto weights = [&]() {
+                    uint4 vw[kAt][D / 64];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
+                    for (int b = 0; b < kAt; ++b)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) e[r][i] = ex2(fmaf(sc[r][i >> 2][i & 3], f[r][i], -m[r][i & 1]));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
-                            if (!whole) {  // no weight, whatever the scale
-                                w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
-                                w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
-                            }
-                            p[r][i] = pack_f16x2(w0, w1);
-                            top = largest_f16x2(top, p[r][i]);
-                        }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            sum[r][c] = l[r][c] + ((e[r][c] + e[r][2 + c]) + (e[r][4 + c] + e[r][6 + c]));
-                            most = fmaxf(most, sum[r][c]);
-                        }
+                        for (int h = 0; h < D / 64; ++h)
+                            vw[b][h] = *reinterpret_cast<const uint4*>(st + (b0 + b) * C::kRecord + q4_v_offset(D) + gid * 64 + tig * 16 + h * 512);
+                    if (b0 + kAt == 2) {
+                        __syncwarp();  // everything is in registers
+                        if (lane == 0) mbar_arrive(&empty[s]);
                     }
-                };
-                weights();
-                // some P' has left f16 (its exponent is full), or l grows beside tiny V scales
-                if (__any_sync(0xffffffffu, ((top + 0x04000400u) & 0x80008000u) != 0u || most > kMostSum)) {
-                    float lg[4];
+                    if (!whole) {  // what a row does not see: a score of -inf
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) lg[i] = fminf(__log2f(fmaxf(fabsf(sv[i]), kTinyScale)), 128.f);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float j = kUnset;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) j = fmaxf(j, sc[r][i >> 1][2 * (i & 1) + c] * f[r][2 * i + c] + lg[i]);
-#pragma unroll
-                            for (int off = 4; off < 32; off <<= 1) j = fmaxf(j, __shfl_xor_sync(0xffffffffu, j, off));
-                            const float to = fmaxf(m[r][c], j - kHeadroom), al = ex2(m[r][c] - to);
-                            m[r][c] = to;
-                            l[r][c] *= al;
-                            z[r][c] *= al;
-                            z[r][2 + c] *= al;
-#pragma unroll
-                            for (int i = 0; i < D / 16; ++i) {
-                                o[r][i][c] *= al;
-                                o[r][i][2 + c] *= al;
-                            }
-                        }
-                    weights();
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    l[r][0] = sum[r][0];
-                    l[r][1] = sum[r][1];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[r][i] = movmatrix_trans(p[r][i]);
-                }
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) mma_f16_16816(z[r], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[r][2 * b], p[r][2 * b + 1]);
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const uint32_t w[4] = {vw[b][h].x, vw[b][h].y, vw[b][h].z, vw[b][h].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int i = 0; i < 2 * kAt; ++i) {
+                            const int p = (blk + b0 + (i >> 1)) * 16 + 8 * (i & 1) + gid;
+                            const bool in = (there >> (b0 + (i >> 1)) & 1) != 0;
 #pragma unroll
                             for (int r = 0; r < R; ++r)
-                                mma_f16_16816(o[r][4 * h + j], w[j] & 0x000f000fu, w[j] & 0x00f000f0u, w[j] >> 8 & 0x000f000fu, w[j] >> 8 & 0x00f000f0u,
-                                              p[r][2 * b], p[r][2 * b + 1]);
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (!in || p > lim[r][c]) {
+                                        sc[r][i >> 1][2 * (i & 1) + c] = __int_as_float(0xff800000);
+                                        f[r][2 * i + c] = 1.f;
+                                    }
+                        }
+                    }
+                    float e[R][4 * kAt], sum[R][2];
+                    uint32_t p[R][2 * kAt];
+                    uint32_t top = 0;
+                    float most = 0.f;
+                    auto weights = [&]() {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+#pragma unroll
+                            for (int i = 0; i < 4 * kAt; ++i) e[r][i] = ex2(fmaf(sc[r][i >> 2][i & 3], f[r][i], -m[r][i & 1]));
+#pragma unroll
+                            for (int i = 0; i < 2 * kAt; ++i) {
+                                float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
+                                if (!whole) {  // no weight, whatever the scale
+                                    w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
+                                    w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
+                                }
+                                p[r][i] = pack_f16x2(w0, w1);
+                                top = largest_f16x2(top, p[r][i]);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                sum[r][c] = e[r][c] + e[r][2 + c];
+                                if (kAt == 2) sum[r][c] += e[r][4 * kAt - 4 + c] + e[r][4 * kAt - 2 + c];
+                                sum[r][c] += l[r][c];
+                                most = fmaxf(most, sum[r][c]);
+                            }
+                        }
+                    };
+                    weights();
+                    // some P' has left f16 (its exponent is full), or l grows beside tiny V scales
+                    if (__any_sync(0xffffffffu, ((top + 0x04000400u) & 0x80008000u) != 0u || most > kMostSum)) {
+                        float lg[2 * kAt];
+#pragma unroll
+                        for (int i = 0; i < 2 * kAt; ++i) lg[i] = fminf(__log2f(fmaxf(fabsf(sv[i]), kTinyScale)), 128.f);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float j = kUnset;
+#pragma unroll
+                                for (int i = 0; i < 2 * kAt; ++i) j = fmaxf(j, sc[r][i >> 1][2 * (i & 1) + c] * f[r][2 * i + c] + lg[i]);
+#pragma unroll
+                                for (int off = 4; off < 32; off <<= 1) j = fmaxf(j, __shfl_xor_sync(0xffffffffu, j, off));
+                                const float to = fmaxf(m[r][c], j - kHeadroom), al = ex2(m[r][c] - to);
+                                m[r][c] = to;
+                                l[r][c] *= al;
+                                z[r][c] *= al;
+                                z[r][2 + c] *= al;
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    o[r][i][c] *= al;
+                                    o[r][i][2 + c] *= al;
+                                }
+                            }
+                        weights();
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        l[r][0] = sum[r][0];
+                        l[r][1] = sum[r][1];
+#pragma unroll
+                        for (int i = 0; i < 2 * kAt; ++i) p[r][i] = movmatrix_trans(p[r][i]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < kAt; ++b) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) mma_f16_16816(z[r], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[r][2 * b], p[r][2 * b + 1]);
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) {
+                            const uint32_t w[4] = {vw[b][h].x, vw[b][h].y, vw[b][h].z, vw[b][h].w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                                for (int r = 0; r < R; ++r)
+                                    mma_f16_16816(o[r][4 * h + j], w[j] & 0x000f000fu, w[j] & 0x00f000f0u, w[j] >> 8 & 0x000f000fu, w[j] >> 8 & 0x00f000f0u,
+                                                  p[r][2 * b], p[r][2 * b + 1]);
+                            }
                         }
                     }
                 }
