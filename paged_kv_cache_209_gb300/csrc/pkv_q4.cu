@@ -38,16 +38,12 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kIssueLanes = 8;  // stages whose copies are issued together
 // Cost of a segment shorter than kShortBlocks beside its blocks, in blocks, where there are
-// blocks enough for every CTA.
-#ifndef MQ4_SEG
-#define MQ4_SEG 16
-#endif
-#ifndef MQ4_LEAST
-#define MQ4_LEAST 8
-#endif
-constexpr int kSegmentCost = MQ4_SEG, kShortBlocks = 256;
-// Where there are not, a CTA gets about this many blocks.
-constexpr int kLeastBlocks = MQ4_LEAST;
+// blocks enough for every CTA (64 contexts of 1 to 8191 tokens: 38.9 us, 45.4 without; many
+// equal short ones lose by it, 256 of 100 tokens 33.9 against 30.8, being cut more rarely).
+constexpr int kSegmentCost = 16, kShortBlocks = 256;
+// Where there are not, a CTA gets about this many blocks (one of 1000 tokens: 9.4 us; 11.6
+// with 2, 9.7 with 32; its four queries a sequence 12.3, 16.4 and 14.2).
+constexpr int kLeastBlocks = 8;
 
 // The base m of a row: where some P' = 2^(x - m) v would leave f16 it moves to the largest
 // x + log2 |v| less kHeadroom, so that what is rounded to f16 lies high in its range for
@@ -76,16 +72,8 @@ template <int D, int R>
 struct M4 {
     static constexpr int kRecord = q4_record_bytes(D);
     static constexpr int kStageBytes = 2 * kRecord;
-#ifndef MQ4_STAGES
-#define MQ4_STAGES 8
-#endif
-#ifndef MQ4_BATCH
-#define MQ4_BATCH kMaxBatchPerLaunch
-#endif
-#ifndef MQ4_CTAS
-#define MQ4_CTAS 3
-#endif
-    static constexpr int kStages = D == 128 ? MQ4_STAGES : 16;
+    static constexpr int kCtas = R == 1 ? 3 : 2;              // an SM's, at 128 and 168 registers a thread
+    static constexpr int kStages = D == 128 ? 8 : 16;
     static constexpr int kRows = 8 * R;                       // query rows of a warp
     static constexpr int kQSlots = R == 1 ? 4 : 2;            // segments whose query rows are in work or on their way
     static constexpr int kStateFloats = kRows * (D + 2);      // a warp's O, m and l
@@ -130,11 +118,10 @@ __device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
-// Larger of the halves' magnitudes; a NaN stays.
-__device__ __forceinline__ uint32_t largest_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
-    return r;
+// Larger, half by half, of a (not negative) and b's magnitude; a NaN stays.
+__device__ __forceinline__ uint32_t larger_f16x2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&a), __habs2(*reinterpret_cast<const __half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Workspace of one piece: per row tile O [8][D], then per consumer warp (each merges D / 4
@@ -157,7 +144,7 @@ __device__ __forceinline__ void write_part(const Q4Args& a, int q0, int head, in
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(const Q4Args a) {
+__global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4Args a) {
     using C = M4<D, R>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 127u);
@@ -270,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
         // ------------------------------------------------ producer
         const uint64_t policy = l2_evict_first_policy(), q_policy = l2_evict_last_policy();
         const uint8_t* cache = static_cast<const uint8_t*>(a.cache);
+        const long long block_bytes = static_cast<long long>(a.kv_heads) * C::kRecord;
         CostSplit split;
         split.init(s_pre, weighted ? s_cost : s_pre, a.batch, a.kv_heads, weighted ? 1 + kSegmentCost : 1, ctas);
         Walker wk;
@@ -283,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
             const bool more = wk.next(pc);
             const int32_t* trow = a.tables + static_cast<long long>(pc.seq) * a.max_blocks + pc.blk_from;
             const int blocks = more ? pc.blk_to - pc.blk_from : 0;
+            const uint8_t* head = cache + static_cast<long long>(pc.head) * C::kRecord;
             int cur = lane < blocks ? __ldg(trow + lane) : 0;
             const int slot = pieces % C::kQSlots;
             if (lane == 0 && pieces >= C::kQSlots) ok = mbar_wait(&q_empty[slot], (pieces / C::kQSlots - 1) & 1, a.status, abort_flag);
@@ -345,9 +334,8 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
                         else
                             mbar_arrive(&full[s]);
                         uint8_t* st = smem + s * C::kStageBytes;
-                        if (load0) bulk_load(st, cache + (static_cast<long long>(id0) * a.kv_heads + pc.head) * C::kRecord, C::kRecord, &full[s], policy);
-                        if (load1)
-                            bulk_load(st + C::kRecord, cache + (static_cast<long long>(id1) * a.kv_heads + pc.head) * C::kRecord, C::kRecord, &full[s], policy);
+                        if (load0) bulk_load(st, head + id0 * block_bytes, C::kRecord, &full[s], policy);
+                        if (load1) bulk_load(st + C::kRecord, head + id1 * block_bytes, C::kRecord, &full[s], policy);
                     }
                     __syncwarp();
                     k += n;
@@ -462,10 +450,18 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
         const uint32_t k_end = k + (blk_to - pc->blk_from + 1) / 2;
         const int skip = (ul - static_cast<int>(k & (UL - 1))) & (UL - 1);
         k += skip;
+        int s = static_cast<int>(k % C::kStages);
+        uint32_t parity = (k / C::kStages) & 1;
+        auto next_stage = [&]() {
+            s += UL;
+            if (s >= C::kStages) {
+                s -= C::kStages;
+                parity ^= 1u;
+            }
+        };
         int unfolded = 0;
-        for (int blk = pc->blk_from + 2 * skip; blk < blk_to; blk += 2 * UL, k += UL) {
-            const int s = static_cast<int>(k % C::kStages);
-            if (!mbar_wait(&full[s], (k / C::kStages) & 1, a.status, abort_flag)) return;
+        for (int blk = pc->blk_from + 2 * skip; blk < blk_to; blk += 2 * UL, next_stage()) {
+            if (!mbar_wait(&full[s], parity, a.status, abort_flag)) return;
             const int there = present[s];
             if (active && there) {
                 const uint8_t* st = smem + s * C::kStageBytes;
@@ -552,13 +548,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
                             for (int i = 0; i < 4 * kAt; ++i) e[r][i] = ex2(fmaf(sc[r][i >> 2][i & 3], f[r][i], -m[r][i & 1]));
 #pragma unroll
                             for (int i = 0; i < 2 * kAt; ++i) {
-                                float w0 = e[r][2 * i] * sv[i], w1 = e[r][2 * i + 1] * sv[i];
-                                if (!whole) {  // no weight, whatever the scale
-                                    w0 = e[r][2 * i] > 0.f ? w0 : 0.f;
-                                    w1 = e[r][2 * i + 1] > 0.f ? w1 : 0.f;
-                                }
-                                p[r][i] = pack_f16x2(w0, w1);
-                                top = largest_f16x2(top, p[r][i]);
+                                p[r][i] = pack_f16x2(e[r][2 * i] * sv[i], e[r][2 * i + 1] * sv[i]);
                             }
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
@@ -569,7 +559,20 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
                             }
                         }
                     };
+                    // what a row does not see has no weight, whatever its scale
+                    auto mask = [&]() {
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int i = 0; i < 2 * kAt; ++i)
+                                p[r][i] &= (e[r][2 * i] > 0.f ? 0x0000ffffu : 0u) | (e[r][2 * i + 1] > 0.f ? 0xffff0000u : 0u);
+                    };
                     weights();
+                    if (!whole) mask();
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int i = 0; i < 2 * kAt; ++i) top = larger_f16x2(top, p[r][i]);
                     // some P' has left f16 (its exponent is full), or l grows beside tiny V scales
                     if (__any_sync(0xffffffffu, ((top + 0x04000400u) & 0x80008000u) != 0u || most > kMostSum)) {
                         float lg[2 * kAt];
@@ -596,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, R == 1 ? MQ4_CTAS : 2) mq4_kernel(co
                                 }
                             }
                         weights();
+                        if (!whole) mask();
                     }
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
@@ -756,7 +760,7 @@ cudaError_t run_mq4(const Q4Args& a, cudaStream_t s) {
 // Resident CTAs of an SM, at the largest launch.
 template <int D, int R>
 int resident(int warps_per_unit) {
-    const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, MQ4_BATCH);
+    const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, kMaxBatchPerLaunch);
     int n = 0;
     cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mq4_kernel<D, R>, kThreads, smem) != cudaSuccess || n < 1) n = 1;

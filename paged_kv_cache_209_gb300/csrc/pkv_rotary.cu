@@ -20,16 +20,12 @@
 namespace pkv {
 namespace {
 
-#ifndef ROT_BATCH
-#define ROT_BATCH 2
-#endif
-#ifndef ROT_FEW
-#define ROT_FEW 64
-#endif
-#ifndef ROT_THREADS
-#define ROT_THREADS 128
-#endif
-constexpr int kThreads = ROT_THREADS;
+constexpr int kThreads = 128;       // of the append's CTAs
+constexpr int kTableThreads = 256;  // of the table's, at most kTableCtas an SM
+constexpr int kTableCtas = 8;       // (131072 x 64 angles: 11.3 us; 12.7 with 4, 12.1 with 16)
+// Rows of an SM below which a warp takes one batch of heads, not two: a decode step's 32 tokens of
+// 32 + 2 x 8 heads take 6.5 us so with their gather, 7.2 with two.
+constexpr int kFew = 64;
 
 // x c - y s rounded to float32 and to bf16. The exact value is s1 + lo, but for an error of lo's last
 // bit: products and difference by their errors, which fused operations give exactly. Where that
@@ -403,10 +399,12 @@ cudaError_t run_batch(const RotaryAppendArgs& a, cudaStream_t s) {
 }
 template <int D, int kMode, int kCache, typename T>
 cudaError_t run_append(const RotaryAppendArgs& a, cudaStream_t s) {
-    constexpr int kBatch = kMode == kAny ? 1 : sizeof(T) == 4 ? 2 : ROT_BATCH;
+    // two batches of a warp's loads in flight (8192 tokens of 32 + 2 x 8 heads, a 4-bit cache, with their gather: 47.8 us;
+    // 52.4 with one, 49.6 with four)
+    constexpr int kBatch = kMode == kAny ? 1 : 2;
     // few rows: every warp takes as few as it can, so that they spread over the SMs
     const int64_t rows = a.num_tokens * (a.q_heads + 2 * a.kv_heads);
-    if (kBatch == 1 || rows < static_cast<int64_t>(device_sm_count()) * ROT_FEW) return run_batch<D, kMode, kCache, T, 1>(a, s);
+    if (kBatch == 1 || rows < static_cast<int64_t>(device_sm_count()) * kFew) return run_batch<D, kMode, kCache, T, 1>(a, s);
     return run_batch<D, kMode, kCache, T, kBatch>(a, s);
 }
 template <int D, int kCache, typename T>
@@ -445,16 +443,16 @@ __device__ __forceinline__ void cos_sin(uint64_t part, float factor, float& c, f
     s = __uint_as_float(__float_as_uint((swap ? pc : ps) * factor) ^ (quarter & 2) << 30);
 }
 template <int kV>
-__global__ void __launch_bounds__(kThreads) rotary_table_kernel(const double* __restrict__ frequencies, int half, int64_t first,
+__global__ void __launch_bounds__(kTableThreads) rotary_table_kernel(const double* __restrict__ frequencies, int half, int64_t first,
                                                                 int64_t positions, float factor, float* __restrict__ table) {
     extern __shared__ uint64_t turns[];  // double arithmetic is slow here: once a frequency
     grid_dependency_wait();
     allow_dependents();
-    for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn_fraction(frequencies[i]);
+    for (int i = threadIdx.x; i < half; i += kTableThreads) turns[i] = turn_fraction(frequencies[i]);
     __syncthreads();
     const int64_t per_row = half / kV;
-    const int64_t thread = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads / per_row;  // rows (the last threads may have none)
+    const int64_t thread = static_cast<int64_t>(blockIdx.x) * kTableThreads + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kTableThreads / per_row;  // rows (the last threads may have none)
     int64_t p = thread / per_row;
     const int i = static_cast<int>(thread - p * per_row) * kV;
     if (p >= step || p >= positions) return;
@@ -546,13 +544,13 @@ cudaError_t launch_append_rotary(const RotaryAppendArgs& a, const pkv_cache_desc
 cudaError_t launch_rotary_table(const double* frequencies, int half, int64_t first, int64_t positions, float factor, float* table,
                                 cudaStream_t s) {
     const int64_t threads = positions * half / (half % 4 ? 1 : 4);
-    const int64_t want = (threads + kThreads - 1) / kThreads, most = static_cast<int64_t>(device_sm_count()) * 8;
+    const int64_t want = (threads + kTableThreads - 1) / kTableThreads, most = static_cast<int64_t>(device_sm_count()) * kTableCtas;
     // (at least a row's threads)
-    const int64_t row = (half / (half % 4 ? 1 : 4) + kThreads - 1) / kThreads;
+    const int64_t row = (half / (half % 4 ? 1 : 4) + kTableThreads - 1) / kTableThreads;
     const dim3 grid(static_cast<unsigned>(want < row ? row : want < most ? want : most));
     const size_t smem = static_cast<size_t>(half) * sizeof(uint64_t);
-    if (half % 4) return launch_pdl(rotary_table_kernel<1>, grid, dim3(kThreads), smem, s, frequencies, half, first, positions, factor, table);
-    return launch_pdl(rotary_table_kernel<4>, grid, dim3(kThreads), smem, s, frequencies, half, first, positions, factor, table);
+    if (half % 4) return launch_pdl(rotary_table_kernel<1>, grid, dim3(kTableThreads), smem, s, frequencies, half, first, positions, factor, table);
+    return launch_pdl(rotary_table_kernel<4>, grid, dim3(kTableThreads), smem, s, frequencies, half, first, positions, factor, table);
 }
 
 }  // namespace pkv
