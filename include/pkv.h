@@ -644,6 +644,18 @@ PKV_API pkv_status pkv_decode_attention_q4(const void* q, const void* cache, con
  * the 4-bit cache's rows stand for: causal attention of each sequence's last
  * query_start[i+1] - query_start[i] tokens, up to 65536 of them. Arguments, limits,
  * errors, checked mode and the device status bits as pkv_multiquery_attention_q8.
+ *
+ * fp32 accumulation, one rounding to bf16. K scales may be of any size and spread, V
+ * scales of any size from 1e-28 on, zero or negative too, as long as those of one
+ * sequence lie within 2^100 of each other (values farther apart may be lost).
+ * Up to 32 query rows per (sequence, KV head): codes and q (scaled by a power of two per
+ * row) enter exactly, a score is summed to 2^-15 |scale| (K scale) sum|q|; a softmax weight
+ * times its V scale is rounded to f16 once (11 bits down to 2^-22 of the row's largest
+ * such product, fewer to 2^-32), and the sums over tokens, which run over code + 8, are
+ * off by some 2^-14 of the sum of these products. More rows run in tiles, as those of
+ * pkv_multiquery_attention_q8: a K value is rounded to f16 once, a V value twice, a
+ * softmax weight once. A token that is not a number, or infinite, spoils the rows that
+ * see it and no others.
  */
 PKV_API pkv_status pkv_multiquery_attention_q4(const void* q, const void* cache, const int32_t* block_tables,
                                                int32_t max_blocks_per_seq, const int32_t* context_lens,

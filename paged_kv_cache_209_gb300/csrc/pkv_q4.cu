@@ -135,7 +135,7 @@ __device__ __forceinline__ float* piece_of(const Q4Args& a, int d, int cta, int 
 template <int D>
 __device__ __forceinline__ void write_part(const Q4Args& a, int q0, int head, int rr, int d0, const float (&o)[D / 16], float l) {
     const int t = rr / a.group;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN, of a token that the row sees, stays)
     __nv_bfloat16* row = static_cast<__nv_bfloat16*>(a.out) +
                          ((static_cast<long long>(q0) + t) * a.q_heads + head * a.group + (rr - t * a.group)) * D + d0;
 #pragma unroll
