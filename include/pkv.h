@@ -730,7 +730,8 @@ PKV_API pkv_status pkv_rotary_table(const double* frequencies, int32_t rotary_di
  *                 aligned, and so are the strides.
  *   num_q_heads   0: k and v only (q and q_out unused). At most PKV_MAX_Q_HEADS.
  *   q_out         rows q_out_stride apart; may be q itself with the same stride, else it
- *                 overlaps none of the inputs.
+ *                 overlaps none of the inputs nor the pools (PKV_ERR_OVERLAP; its rows may
+ *                 lie between q's, k's or v's where the strides are the same).
  *   positions     device, int32 [num_tokens].
  *   table         device, float [num_positions][rotary_dim] (pkv_rotary_table from position
  *                 0), 16-byte aligned.

@@ -108,6 +108,18 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
     return n > 0 && m > 0 && a < b + m && b < a + n;
 }
 
+// The same of `count` rows of n bytes at p, `ps` bytes apart, and of m bytes at q, `qs` apart. (Rows
+// of other strides that lie between one another count as sharing.)
+bool overlap_rows(int64_t count, const void* p, size_t n, size_t ps, const void* q, size_t m, size_t qs) {
+    const size_t all = static_cast<size_t>(count) - 1;
+    if (n == 0 || m == 0 || !overlap(p, all * ps + n, q, all * qs + m)) return false;
+    if (all == 0 || ps != qs) return true;
+    // one stride: where the spans meet, rows share bytes unless those of one begin behind the other's
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const size_t from = b >= a ? (b - a) % ps : (ps - (a - b) % ps) % ps;  // q's first byte in p's rows
+    return from < n || ps - from < m;
+}
+
 pkv_status check_desc_q8(const pkv_cache_desc* d, bool attention) {
     if (d == nullptr) return PKV_ERR_NULL;
     if (d->block_size != 16 || d->num_blocks < 1 || d->num_kv_heads < 1) return PKV_ERR_SHAPE;
@@ -1178,6 +1190,24 @@ pkv_status pkv_append_rotary(const void* q, int64_t q_stride, const void* k, int
         !aligned4(positions) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
         return PKV_ERR_ALIGN;
     if ((flags & PKV_FLAG_CHECKED) && num_tokens > 16384) return PKV_ERR_UNSUPPORTED;
+    if (num_q_heads > 0) {
+        const size_t size = 16 / per_vector, count = static_cast<size_t>(num_tokens);
+        const size_t q_bytes = q_row * size, kv_bytes = kv_row * size;
+        auto step = [&](int i) { return num_tokens > 1 ? strides[i] * size : rows[i] * size; };
+        if ((q_out != q || step(0) != step(1)) && overlap_rows(num_tokens, q_out, q_bytes, step(1), q, q_bytes, step(0))) return PKV_ERR_OVERLAP;
+        if (overlap_rows(num_tokens, q_out, q_bytes, step(1), k, kv_bytes, step(2)) || overlap_rows(num_tokens, q_out, q_bytes, step(1), v, kv_bytes, step(3)))
+            return PKV_ERR_OVERLAP;
+        const size_t records = static_cast<size_t>(desc->num_blocks) * desc->num_kv_heads, codes = 16 * static_cast<size_t>(desc->head_dim);
+        const bool q4 = desc->dtype == PKV_INT4;
+        const size_t pool = records * (q4 ? PKV_Q4_RECORD_BYTES(desc->head_dim) : desc->dtype == PKV_INT8 ? codes : codes * size);
+        const struct {
+            const void* p;
+            size_t n;
+        } others[] = {{positions, 4 * count}, {slot_mapping, 8 * count}, {table, 4 * static_cast<size_t>(num_positions) * rotary_dim},
+                      {k_cache, pool}, {v_cache, q4 ? 0 : pool}, {scales, desc->dtype == PKV_INT8 ? records * 128 : 0}};
+        for (const auto& x : others)
+            if (overlap(q_out, (count - 1) * step(1) + q_bytes, x.p, x.n)) return PKV_ERR_OVERLAP;
+    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     RotaryAppendArgs a{};
     a.q = q;

@@ -110,6 +110,18 @@ def test_rotary(lib):
             assert app(dtype, **bad) == SHAPE, bad
         assert app(dtype, qs=4097) == app(dtype, ks=1026) == ALIGN
         assert app(dtype, n=0) == 0 and app(dtype, fl=1, n=20000) == UNSUPPORTED
+    # q_out over an input or a pool (the host refuses before anything is launched)
+    far = {name: FAKE + (i << 32) for i, name in enumerate(("q", "k", "v", "p", "t", "s", "kc", "vc", "sc"), 1)}
+    step = 2 * 4096                                         # bytes of a row of q
+    for dtype in (1, 2, 3):
+        for out in (far["q"] + 16, far["q"] - 16, far["q"] + 4 * step - 16, far["k"], far["k"] - 4 * step + 16, far["v"] + 16, far["p"],
+                    far["t"] + 100 * 512 - 16, far["s"] + 16, far["kc"], *([far["vc"]] if dtype != 3 else [])):
+            assert app(dtype, **{**far, "o": out}) == OVERLAP, hex(out)
+        # parts of one product's output: a wide row, q_out between the parts
+        wide = dict(q=FAKE, k=FAKE + 8192, v=FAKE + 10240, qs=8192, ks=8192, vs=8192, os=8192)
+        for out in (FAKE + 16, FAKE + 8192, FAKE + 12288 - 16, FAKE + 16384 - 16, FAKE + 3 * 16384 + 16, FAKE - 16):
+            assert app(dtype, **{**far, **wide, "o": out}) == OVERLAP, hex(out)
+        assert app(dtype, **{**far, **wide, "os": 8200}) == OVERLAP
     assert app(1, vc=None) == app(2, vc=None) == app(2, sc=None) == NULL
     assert app(2, sc=FAKE + 4) == ALIGN
     assert app(7) == DTYPE
