@@ -15,7 +15,9 @@
 // whole row at a time.
 //
 // 32 sequences of 8192 int8 tokens, 8 KV heads of 128: 1.63 GB in 257 us, 94 % of
-// the measured copy rate; 64 ragged bf16 sequences 126 us, 97 %; 300 tokens 5 us.
+// the measured copy rate; 64 ragged bf16 sequences 126 us, 97 %; 300 tokens 5 us. The
+// same 32 sequences of a 4-bit cache: 1.36 GB in 221 us, 91 %, 2.43 GB in float32 in 381 us,
+// 94 %; 300 tokens 3.5 us (one warp for both sides of a record: 225, 376, 4.3).
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_q4.cuh"
@@ -212,9 +214,13 @@ __device__ __forceinline__ float nibble_f32(uint32_t w, int p) {
     return __uint_as_float((w >> (4 * p) & 15u) | 0x4B000000u) - 8388616.f;
 }
 
-// A 4-bit record is 16 lines of 8 words of K and as many of V. A lane takes K words w, w +
-// 32, ... (8 dimensions of one token) and V words (16 bytes at 16 lane: an octet's four
-// tokens of one quad), and writes 8 dimensions of a token at a time.
+__device__ __forceinline__ void store16(float* dst, const float (&x)[4]) { store_coords(dst, x); }
+__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float (&x)[8]) { store8(dst, x); }
+
+// A 4-bit record is 16 rows of D / 8 words of K and D / 8 octets of 16 words of V (pkv_q4.cuh). A
+// warp takes one side of a record: K's rows as they come, of V 16 bytes at a time, an octet's four tokens
+// of one quad. A lane writes 16 bytes at a time, an octet in bf16, half of one in float32 (whose
+// halves lie in neighbouring lanes, so that every line that a store touches is written whole).
 template <int D, typename Out>
 __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const GatherArgs a) {
     __shared__ int prefix[kMaxBatchPerLaunch + 1];
@@ -222,49 +228,60 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const GatherArgs a)
     allow_dependents();
     count_blocks(a, prefix);
     const int lane = threadIdx.x & 31;
-    const int64_t items = static_cast<int64_t>(prefix[a.batch]) * a.kv_heads;
+    const int64_t items = static_cast<int64_t>(prefix[a.batch]) * a.kv_heads * 2;
     const int64_t stride = static_cast<int64_t>(a.kv_heads) * D;  // elements from a token's row to the next
-    constexpr int kWords = D / 16;   // K words of a lane
-    constexpr int kVecs = D / 64;    // V vectors of a lane
+    constexpr int kDims = 16 / sizeof(Out);  // of a store
+    constexpr int kParts = 8 / kDims;        // of an octet
+    constexpr int kWords = D / 16;           // K words of a lane
+    const int part = lane % kParts;
     for (int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); x < items;
          x += static_cast<int64_t>(gridDim.x) * kWarps) {
         Item it;
-        if (!item_of(a, prefix, x, lane, it)) continue;
+        if (!item_of(a, prefix, x >> 1, lane, it)) continue;
+        const bool is_v = (x & 1) != 0;
         const uint8_t* rec = static_cast<const uint8_t*>(a.k) + it.chunk * q4_record_bytes(D);
-        const uint32_t* kw = reinterpret_cast<const uint32_t*>(rec);
-        const uint4* vw = reinterpret_cast<const uint4*>(rec + q4_v_offset(D));
-        const float sc = __ldg(reinterpret_cast<const float*>(rec + q4_scales_offset(D)) + lane);  // K's in lanes 0-15, V's in 16-31
-        uint32_t k[kWords];
-        uint4 v[kVecs];
+        const float sc = __ldg(reinterpret_cast<const float*>(rec + q4_scales_offset(D)) + 16 * is_v + (lane & 15));
+        Out* out = static_cast<Out*>(is_v ? a.v_out : a.k_out) + it.row * stride + it.head * D + kDims * part;
+        if (!is_v) {
+            uint32_t k[kWords];
 #pragma unroll
-        for (int r = 0; r < kWords; ++r) k[r] = __ldcs(kw + 32 * r + lane);
+            for (int r = 0; r < kWords; ++r) k[r] = __ldcs(reinterpret_cast<const uint32_t*>(rec) + 32 * r + lane);
 #pragma unroll
-        for (int r = 0; r < kVecs; ++r) v[r] = __ldcs(vw + 32 * r + lane);
-        Out* ko = static_cast<Out*>(a.k_out) + it.row * stride + it.head * D;
-        Out* vo = static_cast<Out*>(a.v_out) + it.row * stride + it.head * D;
+            for (int r = 0; r < kWords * kParts; ++r) {
+                const int word = (32 * r + lane) / kParts, t = word / (D / 8);
+                const float s = __shfl_sync(0xffffffffu, sc, t);
+                const uint32_t w = __shfl_sync(0xffffffffu, k[r / kParts], word % 32) >> (2 * kDims * part);
+                float y[kDims];
 #pragma unroll
-        for (int r = 0; r < kWords; ++r) {
-            const int word = 32 * r + lane, t = word / (D / 8);
-            const float s = __shfl_sync(0xffffffffu, sc, t);
-            if (t < it.lo || t >= it.hi) continue;
-            float y[8];
+                for (int e = 0; e < kDims; ++e) y[e] = nibble_f32(w, e / 2 + 4 * (e & 1)) * s;
+                if (t >= it.lo && t < it.hi) store16(out + t * stride + word % (D / 8) * 8, y);
+            }
+        } else {
+            constexpr int kLoads = D / 64 * kParts;  // of kDims / 2 words each
+            uint32_t v[kLoads][kDims / 2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = nibble_f32(k[r], e / 2 + 4 * (e & 1)) * s;
-            store8(ko + t * stride + word % (D / 8) * 8, y);
-        }
+            for (int r = 0; r < kLoads; ++r) {
+                const uint32_t* from = reinterpret_cast<const uint32_t*>(rec + q4_v_offset(D)) + (32 * r + lane) * (kDims / 2);
+                if (kDims == 8) {
+                    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(from));
+                    v[r][0] = w.x, v[r][1] = w.y, v[r][kDims / 2 - 2] = w.z, v[r][kDims / 2 - 1] = w.w;
+                } else {
+                    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(from));
+                    v[r][0] = w.x, v[r][1] = w.y;
+                }
+            }
 #pragma unroll
-        for (int r = 0; r < kVecs; ++r) {
-            const int vec = 32 * r + lane, quad = vec & 3, o = vec >> 2;
-            const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+            for (int r = 0; r < kLoads; ++r) {
+                const int vec = (32 * r + lane) / kParts, quad = vec & 3, o = vec >> 2;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {  // tokens 2 quad, + 1, + 8, + 9
-                const int t = 2 * quad + (u & 1) + 8 * (u >> 1);
-                const float s = __shfl_sync(0xffffffffu, sc, 16 + t);
-                if (t < it.lo || t >= it.hi) continue;
-                float y[8];
+                for (int u = 0; u < 4; ++u) {  // tokens 2 quad, + 1, + 8, + 9
+                    const int t = 2 * quad + (u & 1) + 8 * (u >> 1);
+                    const float s = __shfl_sync(0xffffffffu, sc, t);
+                    float y[kDims];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = nibble_f32(w[e / 2], 4 * (u & 1) + 2 * (u >> 1) + (e & 1)) * s;
-                store8(vo + t * stride + 8 * o, y);
+                    for (int e = 0; e < kDims; ++e) y[e] = nibble_f32(v[r][e / 2], 4 * (u & 1) + 2 * (u >> 1) + (e & 1)) * s;
+                    if (t >= it.lo && t < it.hi) store16(out + t * stride + 8 * o, y);
+                }
             }
         }
     }
@@ -312,8 +329,8 @@ __global__ void check_gather_kernel(const GatherArgs a, unsigned int* verdict) {
 }  // namespace
 
 cudaError_t launch_gather(const GatherArgs& a, const pkv_cache_desc& d, int out_dtype, cudaStream_t s) {
-    // at most one item per KV head for every 16 rows, and two more per sequence
-    const int64_t units = a.num_rows / 16 + 2 * static_cast<int64_t>(a.batch);
+    // at most one item per KV head for every 16 rows, and two more per sequence; two warps an item of a 4-bit cache
+    const int64_t units = (a.num_rows / 16 + 2 * static_cast<int64_t>(a.batch)) * (d.dtype == PKV_INT4 ? 2 : 1);
     const int64_t want = (units * d.num_kv_heads + kWarps - 1) / kWarps;
     const int64_t most = static_cast<int64_t>(device_sm_count()) * kCtasPerSm;
     const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(kThreads);
