@@ -20,7 +20,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;       // of the append's CTAs
+constexpr int kThreads = 64;        // of the append's CTAs
+constexpr int kAppendCtas = 14;     // an SM's at least: 72 registers a thread (28 warps an SM at 72 38.2 us, 20 at 96 39.9: see below)
 constexpr int kTableThreads = 256;  // of the table's, at most kTableCtas an SM
 constexpr int kTableCtas = 8;       // (131072 x 64 angles: 11.3 us; 12.7 with 4, 12.1 with 16)
 // Rows of an SM below which a warp takes one batch of heads, not two: a decode step's 32 tokens of
@@ -267,7 +268,7 @@ __device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {  // of a 4-
 // row, all of its loads in flight at once. Units are numbered token by token, so that what runs at
 // a time reads and writes memory that lies together. kCache: the pkv_dtype of the pools, or PKV_INT4.
 template <int D, int kMode, int kCache, typename T, int kBatch>
-__global__ void __launch_bounds__(kThreads) append_rotary_kernel(const RotaryAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(const RotaryAppendArgs a) {
     constexpr int kLanes = D / 16;
     constexpr int kRows = 32 / kLanes;
     constexpr int kHeads = kBatch * kRows;
@@ -399,8 +400,8 @@ cudaError_t run_batch(const RotaryAppendArgs& a, cudaStream_t s) {
 }
 template <int D, int kMode, int kCache, typename T>
 cudaError_t run_append(const RotaryAppendArgs& a, cudaStream_t s) {
-    // two batches of a warp's loads in flight (8192 tokens of 32 + 2 x 8 heads, a 4-bit cache, with their gather: 47.8 us;
-    // 52.4 with one, 49.6 with four)
+    // two batches of a warp's loads in flight (4096 tokens of 32 + 2 x 8 heads, a 4-bit cache, with their gather: 38.2 us;
+    // 4.6 more with one, 1.8 with four)
     constexpr int kBatch = kMode == kAny ? 1 : 2;
     // few rows: every warp takes as few as it can, so that they spread over the SMs
     const int64_t rows = a.num_tokens * (a.q_heads + 2 * a.kv_heads);
