@@ -1019,13 +1019,12 @@ size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_heads, int3
     return q4_counters_bytes(desc) + (split > tiles ? split : tiles);
 }
 
-// 4-bit multi-query calls: whether the kernel that splits the cache takes them, or the one that works in tiles.
-static bool split_takes_q4(const pkv_cache_desc* d, int32_t batch, int32_t max_blocks, int64_t rows) {
-    (void)d;
-    (void)batch;
-    (void)max_blocks;
-    return rows <= kMq4Rows;
-}
+// 4-bit multi-query calls: up to kMq4Rows query rows per (sequence, KV head) run on the
+// kernel that splits the cache (pkv_q4.cu), more in tiles (pkv_chunk_q8.cu), whose 128 rows
+// cost the same however many are used. Split / tiles in us, 32 rows of 128 but as noted:
+// 32 sequences of 8192 154 / 209 (16 rows 85 / 211; 16 rows of 64 57 / 184), one of 32768 40 /
+// 46, of 1024 15.7 / 18.6, 64 of 300 43 / 48, 4 of 300 16.5 / 14.4.
+static bool split_takes_q4(int64_t rows) { return rows <= kMq4Rows; }
 
 // Both attention calls over the 4-bit cache, after the checks of their own.
 static pkv_status run_attention_q4(const void* q, const void* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -1058,7 +1057,7 @@ static pkv_status run_attention_q4(const void* q, const void* cache, const int32
     const int64_t rows = static_cast<int64_t>(max_query_len) * G;
     char* ws = static_cast<char*>(workspace);
     const size_t pieces = q4_counters_bytes(desc);
-    const bool tiles = query_start != nullptr && !split_takes_q4(desc, batch, max_blocks_per_seq, rows);
+    const bool tiles = query_start != nullptr && !split_takes_q4(rows);
     const Q4Plan plan = tiles ? Q4Plan{} : q4_plan(desc->head_dim, static_cast<int>(rows));
     const int64_t row = static_cast<int64_t>(num_q_heads) * desc->head_dim * 2;
     for (int32_t b0 = 0; b0 < batch; b0 += kMaxBatchPerLaunch) {

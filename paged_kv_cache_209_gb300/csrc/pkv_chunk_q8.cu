@@ -1,7 +1,8 @@
 // Causal attention of a chunk of new tokens over the int8 pools
 // (pkv_multiquery_attention_q8 in include/pkv.h): all its calls but those of up to 16
 // query rows per (sequence, KV head) of 128 on tables for many tokens, which run on the
-// kernel that splits the cache (split_kernel_takes in pkv_api.cu).
+// kernel that splits the cache (split_kernel_takes in pkv_api.cu). And over the 4-bit
+// cache (pkv_multiquery_attention_q4), calls of more than 32 rows (split_takes_q4).
 //
 // Mathematics, per query row and step of 128 tokens:
 //     s_p = q' . k_p                    f16 x f16 -> fp32; q' is q times a power of two
@@ -67,6 +68,12 @@
 // one product of 128 tokens 520 (against 425: a half's softmax waits for all of it); the
 // halves' softmax in turns 535, half B held back by a part 442 (against 423); eight warps
 // for K instead of four 518 (against 502).
+//
+// A 4-bit cache (Q4) differs in the converters alone: they take nibbles out of records
+// (pkv_q4.cuh) by masks, into the mantissas of f16s, and the 8 off again before the factor.
+// 8 x 512 new tokens on 8192: 413 us in a captured graph, 1290 TFLOP/s of the visible pairs,
+// bound as above; the same work over int8 codes takes 421 to 426.
+//
 // Small calls are bound by the chain before the first product: 2.5 us to plan, 4 for
 // the table, the scales and the codes, one after another; 14 us for 40 new tokens on
 // 200.

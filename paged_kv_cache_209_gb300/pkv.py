@@ -1,11 +1,13 @@
-"""Thin ctypes binding of libpkv.so (include/pkv.h), same function names.
+"""Thin binding of libpkv.so (include/pkv.h), same function names.
 
 Only argument marshalling happens here: tensors become device pointers, the
 cache geometry becomes a ``pkv_cache_desc``, the current torch stream is
 passed through, and a non-OK status raises ``PkvError``. Every step of the
 decode path runs in the library's CUDA kernels. There is no fallback: if
 ``libpkv.so`` is missing or a tensor is not on a CUDA device, the call
-raises.
+raises. Calls go through ctypes, but those of the 4-bit cache, the rotary and
+the planning calls through ``_pkv_calls.so`` (binding/pkv_calls.cpp), whose host
+side takes a third of the time.
 
 With ``stream=`` (a torch stream or a raw handle) a call runs there: its inputs
 have to be ready on that stream, and outputs that it allocates are.
