@@ -233,7 +233,7 @@ PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 14, [&]() -> PyObject* {
         const Call c{integer32("here", a[0])};
         pkv_cache_desc desc;
-        const void *v_cache = nullptr, *scales = nullptr;
+        void *v_cache = nullptr, *scales = nullptr;
         const Tensor& pool = tensor("k_cache", a[7]);
         if (a[8] == Py_None) {
             if (a[9] != Py_None) throw Refused("scales need v_cache");
@@ -246,8 +246,8 @@ PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 throw Refused(q8 ? "k_codes is int8 [num_blocks][num_kv_heads][16][head_dim]" : "unsupported dtype of the pools");
             const int64_t nb = pool.size(0), kv = pool.size(1), bs = pool.size(2), d = pool.size(3);
             c.whole("k_cache", a[7], type);
-            v_cache = c.whole("v_cache", a[8], type, q8 ? at::IntArrayRef({nb, kv, d, bs}) : pool.sizes()).const_data_ptr();
-            if (q8) scales = c.whole("scales", a[9], at::kFloat, {nb, kv, 2, bs}).const_data_ptr();
+            v_cache = c.whole("v_cache", a[8], type, q8 ? at::IntArrayRef({nb, kv, d, bs}) : pool.sizes()).mutable_data_ptr();
+            if (q8) scales = c.whole("scales", a[9], at::kFloat, {nb, kv, 2, bs}).mutable_data_ptr();
             desc = pkv_cache_desc{nb, static_cast<int32_t>(bs), static_cast<int32_t>(kv), static_cast<int32_t>(d),
                                   q8 ? PKV_INT8 : type == at::kFloat ? PKV_F32 : PKV_BF16};
         }
@@ -299,8 +299,8 @@ PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return pkv_append_rotary(q_at, q_stride, k.t.const_data_ptr(), k.stride, v.t.const_data_ptr(), v.stride, positions,
                                      static_cast<const float*>(table.const_data_ptr()), static_cast<int32_t>(table.size(0)), static_cast<int32_t>(table.size(1)),
                                      interleaved, static_cast<const int64_t*>(slots.const_data_ptr()), tokens, heads,
-                                     out.defined() ? out.mutable_data_ptr() : nullptr, out_stride, pool_at, const_cast<void*>(v_cache),
-                                     static_cast<float*>(const_cast<void*>(scales)), &desc, flags, stream);
+                                     out.defined() ? out.mutable_data_ptr() : nullptr, out_stride, pool_at, v_cache, static_cast<float*>(scales),
+                                     &desc, flags, stream);
         });
         return result(!out.defined() ? none() : a[11] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[11]), status);
     });
@@ -366,7 +366,7 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const uint32_t flags = static_cast<uint32_t>(integer("flags", a[10]));
         void* stream = pointer(a[11]);
         const int status = call(flags, [&]() -> int {
-            return pkv_plan_step(lens, more, held, static_cast<const int32_t*>(free.const_data_ptr()), free.size(0), count, const_cast<int32_t*>(t.at), t.width,
+            return pkv_plan_step(lens, more, held, static_cast<const int32_t*>(free.const_data_ptr()), free.size(0), count, static_cast<int32_t*>(THPVariable_Unpack(a[6]).mutable_data_ptr()), t.width,
                                  t.batch, rows, blocks, static_cast<int64_t*>(at[0]), ints(1), ints(2), ints(3), ints(4), ints(5), ints(6), flags, stream);
         });
         if (a[9] != Py_None) return result(Py_NewRef(a[9]), status);

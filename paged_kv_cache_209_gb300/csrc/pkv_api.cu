@@ -941,7 +941,7 @@ pkv_status pkv_append_q4(const void* k, const void* v, const int64_t* slot_mappi
     NvtxRange nvtx_range("pkv_append_q4");
     pkv_status st = check_desc_q4(desc);
     if (st != PKV_OK) return st;
-    if (num_tokens < 0 || num_tokens * 2 * desc->num_kv_heads >= (int64_t(1) << 31)) return PKV_ERR_SHAPE;
+    if (num_tokens < 0 || num_tokens >= (int64_t(1) << 31) / (2 * static_cast<int64_t>(desc->num_kv_heads))) return PKV_ERR_SHAPE;  // rows are counted in 32 bits
     if (cache == nullptr) return PKV_ERR_NULL;
     if (!aligned16(cache)) return PKV_ERR_ALIGN;
     if (num_tokens == 0) return PKV_OK;
@@ -972,7 +972,7 @@ pkv_status pkv_copy_blocks_q4(const int64_t* pairs, int64_t num_pairs, void* cac
     NvtxRange nvtx_range("pkv_copy_blocks_q4");
     pkv_status st = check_desc_q4(desc);
     if (st != PKV_OK) return st;
-    if (num_pairs < 0) return PKV_ERR_SHAPE;
+    if (num_pairs < 0 || num_pairs >= (int64_t(1) << 31)) return PKV_ERR_SHAPE;  // (destinations are distinct blocks)
     if (cache == nullptr) return PKV_ERR_NULL;
     if (!aligned16(cache)) return PKV_ERR_ALIGN;
     if (num_pairs == 0) return PKV_OK;

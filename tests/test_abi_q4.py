@@ -47,11 +47,11 @@ def test_append_copy_gather(lib):
     app = lambda k=FAKE, v=FAKE, s=FAKE, n=4, c=FAKE: lib.pkv_append_q4(k, v, s, n, c, d, 0, None)  # noqa: E731
     assert app(k=None) == app(v=None) == app(s=None) == app(c=None) == NULL
     assert app(k=FAKE + 2) == app(v=FAKE + 8) == app(s=FAKE + 4) == app(c=FAKE + 8) == ALIGN
-    assert app(n=-1) == app(n=1 << 28) == SHAPE
+    assert app(n=-1) == app(n=1 << 28) == app(n=(1 << 62) + 4) == SHAPE
     assert app(k=None, v=None, s=None, n=0) == 0
     assert lib.pkv_append_q4(FAKE, FAKE, FAKE, 4, FAKE, None, 0, None) == NULL
     cp = lambda p=FAKE, n=1, c=FAKE: lib.pkv_copy_blocks_q4(p, n, c, d, 0, None)  # noqa: E731
-    assert cp(p=None) == cp(c=None) == NULL and cp(p=FAKE + 4) == cp(c=FAKE + 4) == ALIGN and cp(n=-1) == SHAPE and cp(n=0) == 0
+    assert cp(p=None) == cp(c=None) == NULL and cp(p=FAKE + 4) == cp(c=FAKE + 4) == ALIGN and cp(n=-1) == cp(n=1 << 60) == SHAPE and cp(n=0) == 0
     ga = lambda **kw: lib.pkv_gather_q4(kw.get("c", FAKE), FAKE, kw.get("w", 4), FAKE, None, kw.get("r", FAKE), 2,  # noqa: E731
                                         kw.get("n", 8), kw.get("o", FAKE), FAKE, kw.get("t", 1), d, kw.get("f", 0), None)
     assert ga(c=None) == ga(r=None) == ga(o=None) == NULL and ga(o=FAKE + 8) == ga(c=FAKE + 4) == ALIGN
@@ -105,7 +105,7 @@ def test_rotary(lib):
             assert app(dtype, **{name: None}) == NULL, name
         for name, off in (("q", 8), ("k", 2), ("v", 4), ("p", 2), ("t", 8), ("s", 4), ("o", 8), ("kc", 8), ("vc", 8)):
             assert app(dtype, **{name: FAKE + off}) == ALIGN, name
-        for bad in (dict(r=0), dict(r=3), dict(r=130), dict(np=0), dict(n=-1), dict(n=1 << 26), dict(h=-1), dict(h=1025),
+        for bad in (dict(r=0), dict(r=3), dict(r=130), dict(np=0), dict(n=-1), dict(n=1 << 26), dict(n=1 << 62), dict(h=-1), dict(h=1025),
                     dict(qs=4088), dict(ks=1016), dict(vs=0), dict(os=-4096), dict(ks=1 << 31), dict(d=dict(head_dim=96))):
             assert app(dtype, **bad) == SHAPE, bad
         assert app(dtype, qs=4097) == app(dtype, ks=1026) == ALIGN
