@@ -256,11 +256,11 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
     // Few blocks: fewer CTAs, as many for each segment, whose cuts then fall between segments of one
     // length (a CTA with two pieces takes them one after the other). (No range is empty, so a segment's
     // pieces lie in consecutive CTAs.)
-    long long ctas = quotient(U, kLeastBlocks);
+    long long ctas = U / kLeastBlocks;
     const bool few = ctas < gridDim.x;
     if (few) {
         const long long segments = static_cast<long long>(a.kv_heads) * *s_active;
-        ctas = ctas < 1 ? 1 : ctas >= segments ? quotient(ctas, segments) * segments : ctas;
+        ctas = ctas < 1 ? 1 : ctas >= segments ? ctas / segments * segments : ctas;
     } else {
         ctas = gridDim.x;
     }

@@ -18,13 +18,6 @@
 namespace pkv {
 namespace {
 
-// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is a long
-// loop on the GPU, and a CTA's start waits for several).
-PKV_HD __forceinline__ long long quotient(long long a, long long b) {
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
 struct Piece {
     int seq, head;
     int blk_from, blk_to;  // blocks [from, to) of the sequence
@@ -60,7 +53,7 @@ struct Walker {
         const int excl = i ? pre[i - 1] : 0;
         nb = pre[i] - excl;
         seg_base = static_cast<long long>(kvh) * excl;
-        h = static_cast<int>(quotient(u - seg_base, nb));
+        h = static_cast<int>((u - seg_base) / nb);
     }
 
     PKV_HD bool next(Piece& p) {
@@ -92,7 +85,7 @@ struct Walker {
     }
 };
 
-PKV_HD __forceinline__ long long range_start(long long c, long long U, long long C) { return quotient(c * U, C); }
+PKV_HD __forceinline__ long long range_start(long long c, long long U, long long C) { return c * U / C; }
 
 // The same split weighted by cost: a segment of nb blocks costs nb + e(nb),
 // e >= 0 being the work of a segment outside its blocks (loading q,
@@ -140,23 +133,23 @@ struct CostSplit {
         const int p0 = i ? pre[i - 1] : 0, q0 = i ? cost[i - 1] : 0;
         const int nb = pre[i] - p0, e = cost[i] - q0 - nb;
         const long long u0 = static_cast<long long>(kvh) * p0;
-        const long long h = quotient(u - u0, nb), b = u - u0 - h * nb;
+        const long long h = (u - u0) / nb, b = u - u0 - h * nb;
         return static_cast<long long>(kvh) * q0 + h * (nb + e) + (b > 0 ? e + b : 0);
     }
     PKV_HD long long start(long long c) const {
-        const long long t = quotient(c * T, C);
+        const long long t = c * T / C;
         if (T == U) return t;
         if (t >= T) return U;
         const int i = seq_of(cost, t);
         const int p0 = i ? pre[i - 1] : 0, q0 = i ? cost[i - 1] : 0;
         const int nb = pre[i] - p0, e = cost[i] - q0 - nb;
         const long long k0 = static_cast<long long>(kvh) * q0;
-        const long long h = quotient(t - k0, nb + e), rr = t - k0 - h * (nb + e);
+        const long long h = (t - k0) / (nb + e), rr = t - k0 - h * (nb + e);
         const long long s0 = static_cast<long long>(kvh) * p0 + h * nb;
         return rr == 0 ? s0 : s0 + (rr - e > 1 ? rr - e : 1);
     }
     // the CTA whose range holds unit u: max c with start(c) <= u
-    PKV_HD long long cta_of(long long u) const { return quotient((cost_before(u) + 1) * C - 1, T); }
+    PKV_HD long long cta_of(long long u) const { return ((cost_before(u) + 1) * C - 1) / T; }
     // every range is non-empty when a range's cost share covers the dearest unit
     PKV_HD bool dense() const { return T >= C * max_unit; }
     // pieces of a segment whose units lie in CTAs c0 .. c1 (the non-empty ranges among them)
@@ -176,7 +169,7 @@ struct CostSplit {
 };
 
 // The CTA whose range holds unit u: max c with range_start(c) <= u.
-PKV_HD __forceinline__ long long cta_of(long long u, long long U, long long C) { return quotient((u + 1) * C - 1, U); }
+PKV_HD __forceinline__ long long cta_of(long long u, long long U, long long C) { return ((u + 1) * C - 1) / U; }
 
 // Pieces of one segment: every CTA whose unit range meets [S0, S1).
 PKV_HD __forceinline__ int pieces_of_segment(long long c0, long long c1, long long U, long long C) {
