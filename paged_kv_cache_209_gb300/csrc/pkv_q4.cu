@@ -88,6 +88,9 @@ struct M4 {
     static constexpr int kStageBytes = 2 * kRecord;
     static constexpr int kCtas = R == 1 ? 3 : 2;              // an SM's, at 128 and 168 registers a thread
     static constexpr int kStages = D == 128 ? 8 : 16;
+    // A stage always meets the same warp (one that ran ahead of the copies into another's stage would take the
+    // parity of the round before for its own), and stages issued together are different ones.
+    static_assert(kStages % kConsumers == 0 && kStages >= kIssueLanes, "ring");
     static constexpr int kRows = 8 * R;                       // query rows of a warp
     static constexpr int kQSlots = R == 1 ? 4 : 2;            // segments whose query rows are in work or on their way
     static constexpr int kStateFloats = kRows * (D + 2);      // a warp's O, m and l
