@@ -14,13 +14,11 @@
 // pairs decides, and float64 where that leaves a tie open.
 //
 // The append is pure streaming by its bytes (q in and out, k and v in, the pools' share
-// out), and bound by its instructions where it quantizes: 20 an element and lane in the mean,
-// a third of them the exact rounding, another the codes (the maximum, the exact quotient,
-// the nibbles). Measured in a captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a
-// 4-bit cache 27.9 us, 88 MB at 3.2 TB/s (3.5 of them are V's single bytes: a token holds a byte
-// of every word); ragged prompts of 24 + 2 x 8 heads into bf16 pools 27.7 us, 5.3 TB/s; a
-// decode step of 32 tokens 2.5 us. A warp that goes from unit to unit with the next one's rows on
-// their way took 29.7 and 30.9 for the first two.
+// out), and bound by its instructions, most of all by the exact rounding. Measured in a
+// captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a 4-bit cache 23.3 us, 88 MB
+// at 3.8 TB/s (27.9 while V's codes went byte by byte); ragged prompts of 24 + 2 x 8 heads into
+// bf16 pools 27.6 us, 5.3 TB/s; a decode step of 32 tokens 2.5 us. A warp that goes from unit
+// to unit with the next one's rows on their way took 1.8 us more for the first, 2.7 for the second.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -31,8 +29,8 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 64;        // of the append's CTAs
-constexpr int kAppendCtas = 14;     // an SM's at least: 72 registers a thread (4096 tokens into a 4-bit cache and their gather 38.2
-                                    // us; 39.4 at 96 registers, 10 CTAs)
+constexpr int kAppendCtas = 14;     // an SM's at least: 72 registers a thread (at 96 registers and 10 CTAs 4096 tokens into a 4-bit
+                                    // cache and their gather took 1.2 us more, of 38.2)
 constexpr int kTableThreads = 256;  // of the table's, at most kTableCtas an SM
 constexpr int kTableCtas = 8;       // (131072 x 64 angles: 11.3 us; 12.7 with 4, 12.1 with 16)
 // Rows of an SM below which a warp takes one batch of heads, not two: a decode step's 32 tokens of
@@ -275,20 +273,145 @@ __device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {  // of a 4-
     return w;
 }
 
+// A row's scale, of its largest magnitude. (A zero row's is 0 in a 4-bit cache, 1 in an int8 one.)
+template <int kCache>
+__device__ __forceinline__ float scale_of(float top) {
+    return kCache == PKV_INT4 ? top * kQ4Step : top > 0.f ? __fdiv_rn(top, 127.f) : 1.f;
+}
+// Whether an append's V goes by windows of 16 tokens.
+constexpr bool by_windows(int cache, int batch) { return (cache == PKV_INT4 || cache == PKV_INT8) && batch > 1; }
+
+// Where a byte of a block's V codes (one head) lies while it is put together in shared memory: pieces
+// of 16 bytes change places so that lanes of different octets meet different banks.
+template <int kCache>
+__device__ __forceinline__ int staged(int byte) {
+    const int piece = byte >> 4;
+    return (piece ^ (kCache == PKV_INT4 ? piece >> 3 & 3 : piece >> 3 & 7)) << 4 | (byte & 15);
+}
+// Byte of octet o's dimension 8 o + e (a pair of dimensions of a 4-bit code) of token t.
+template <int kCache>
+__device__ __forceinline__ int v_byte(int o, int e, int t) {
+    return kCache == PKV_INT4 ? q4_v_byte(o, e >> 1, t) : (8 * o + e) * 16 + t;
+}
+
+// V of the 16 tokens from 16 `window` on, one head, quantized. A byte of a block's V codes is one token's, its
+// words are several's: stored token by token, K and V of 4096 tokens of 24 heads take 47.7 us into a 4-bit cache and
+// 115 into an int8 one, so 26.3 and 28.2. Where 16 tokens that follow one another fill a block, the warp whose window holds their first puts
+// the block together in shared memory; tokens of no such block are stored byte by byte.
+template <int D, int kMode, int kCache>
+__device__ __forceinline__ void append_v_window(const RotaryAppendArgs& a, uint32_t window, int head, uint8_t* stage) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kSteps = 16 / kRows;
+    constexpr int kStep = kCache == PKV_INT4 ? 2 : 1;                 // dimensions of a byte
+    constexpr int kBytes = (kCache == PKV_INT4 ? 8 : 16) * D;         // of the block's V codes
+    const int lane32 = threadIdx.x & 31, lane = lane32 % kLanes, row = lane32 / kLanes;
+    const int64_t r0 = static_cast<int64_t>(window) * 16;
+    auto slot_of = [&](int64_t r) -> int64_t {  // -1: nothing is stored
+        if (r < 0 || r >= a.num_tokens) return -1;
+        const int64_t s = a.slots[r];
+        const int pos = kMode == kWhole ? 0 : a.positions[r];
+        return s >= 0 && s < a.num_slots && (kMode == kWhole || (pos >= 0 && pos < a.num_positions)) ? s : -1;
+    };
+    // rows r0 - 16 .. r0 + 31, and which of them go on where the row before left off in its block
+    const int64_t s0 = slot_of(r0 - 16 + lane32), s1 = lane32 < 16 ? slot_of(r0 + 16 + lane32) : -1;
+    int64_t p0 = __shfl_up_sync(0xffffffffu, s0, 1), p1 = __shfl_up_sync(0xffffffffu, s1, 1);
+    const int64_t last = __shfl_sync(0xffffffffu, s0, 31);
+    if (lane32 == 0) p0 = -2, p1 = last;
+    const uint32_t goes0 = __ballot_sync(0xffffffffu, (s0 & 15) != 0 && s0 >= 0 && s0 == p0 + 1 && p0 >= 0);
+    const uint32_t goes1 = __ballot_sync(0xffffffffu, (s1 & 15) != 0 && s1 >= 0 && s1 == p1 + 1 && p1 >= 0);
+    const uint64_t goes = goes0 | static_cast<uint64_t>(goes1) << 32;
+    const uint32_t whole = __ballot_sync(0xffffffffu, s0 >= 0 && (s0 & 15) == 0 && (goes >> (lane32 + 1) & 0x7fff) == 0x7fff);
+    // the window's tokens: some end a block that began before it, some are alone, the rest belongs to a block that begins here
+    const int alone = (whole & 0xfffeu) != 0 ? 31 - __clz(whole & 0xfffeu) : 0;
+    const int begins = whole >> 16 != 0 ? __ffs(whole >> 16) - 1 : 16;
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(a.v) + head * D + 8 * lane;  // octets lane and lane + kLanes
+    uint8_t* pool = static_cast<uint8_t*>(kCache == PKV_INT4 ? a.k_cache : a.v_cache);
+    auto codes_at = [&](int64_t slot) {
+        const int64_t chunk = (slot >> 4) * a.kv_heads + head;
+        return kCache == PKV_INT4 ? pool + chunk * q4_record_bytes(D) + q4_v_offset(D) : pool + chunk * kBytes;
+    };
+    auto scales_at = [&](int64_t slot) {
+        const int64_t chunk = (slot >> 4) * a.kv_heads + head;
+        return (kCache == PKV_INT4 ? reinterpret_cast<float*>(pool + chunk * q4_record_bytes(D) + q4_scales_offset(D)) : a.scales + chunk * 32) + 16;
+    };
+    // a row's codes, byte by byte to put(byte, code); its scale
+    auto quantize = [&](const Eight<__nv_bfloat16>(&x)[2], int t, auto put) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x[0].get(e)), fabsf(x[1].get(e)));
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float scale = scale_of<kCache>(top);
+        const Codes<kCache> code(scale);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; e += kStep)
+                put(v_byte<kCache>(lane + kLanes * i, e, t), kStep == 2 ? code(x[i].get(e)) | code(x[i].get(e + kStep - 1)) << 4 : code(x[i].get(e)));
+        return scale;
+    };
+    if (begins < 16) {
+        const int64_t slot = __shfl_sync(0xffffffffu, s0, 16 + begins);
+        Eight<__nv_bfloat16> x[kSteps][2];
+#pragma unroll
+        for (int b = 0; b < kSteps; ++b) {
+            const __nv_bfloat16* p = from + (r0 + begins + b * kRows + row) * a.v_stride;
+            x[b][0].load(p), x[b][1].load(p + 8 * kLanes);
+        }
+        float* scales = scales_at(slot);
+#pragma unroll
+        for (int b = 0; b < kSteps; ++b) {
+            const int t = b * kRows + row;
+            const float scale = quantize(x[b], t, [&](int byte, uint32_t c) { stage[staged<kCache>(byte)] = static_cast<uint8_t>(c); });
+            if (lane == 0) scales[t] = scale;
+        }
+        __syncwarp();
+        uint8_t* to = codes_at(slot);
+#pragma unroll
+        for (int i = 16 * lane32; i < kBytes; i += 512) *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(stage + staged<kCache>(i));
+    }
+    for (int b = alone; b < begins; b += kRows) {
+        const int64_t slot = __shfl_sync(0xffffffffu, s0, 16 + min(b + row, 15));
+        const bool live = b + row < begins && slot >= 0;
+        Eight<__nv_bfloat16> x[2] = {};
+        if (live) {
+            const __nv_bfloat16* p = from + (r0 + b + row) * a.v_stride;
+            x[0].load(p), x[1].load(p + 8 * kLanes);
+        }
+        uint8_t* to = codes_at(live ? slot : 0);
+        const int t = static_cast<int>(slot & 15);
+        const float scale = quantize(x, t, [&](int byte, uint32_t c) {
+            if (live) to[byte] = static_cast<uint8_t>(c);
+        });
+        if (live && lane == 0) scales_at(slot)[t] = scale;
+    }
+}
+
 // One warp takes a unit: kBatch times kRows heads of one token, all of q, of k or of v, D / 16 lanes a
 // row, all of its loads in flight at once. Units are numbered token by token, so that what runs at
-// a time reads and writes memory that lies together. kCache: the pkv_dtype of the pools, or PKV_INT4.
+// a time reads and writes memory that lies together. Where there are many rows, a quantizing cache's V goes
+// by windows of 16 tokens, which come first. kCache: the pkv_dtype of the pools, or PKV_INT4.
 template <int D, int kMode, int kCache, typename T, int kBatch>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(const RotaryAppendArgs a) {
     constexpr int kLanes = D / 16;
     constexpr int kRows = 32 / kLanes;
     constexpr int kHeads = kBatch * kRows;
+    constexpr bool kWindows = by_windows(kCache, kBatch);
     grid_dependency_wait();  // q, k, v, and a block copied onto the slots' block, come from the kernels before
     allow_dependents();
     const uint32_t lane = threadIdx.x % kLanes, row = threadIdx.x % 32 / kLanes;
     const uint32_t q_units = (a.q_heads + kHeads - 1) / kHeads, kv_units = (a.kv_heads + kHeads - 1) / kHeads;
-    const uint32_t units = q_units + 2 * kv_units;  // of a token
-    const uint32_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const uint32_t units = q_units + (kWindows ? 1 : 2) * kv_units;  // of a token
+    uint32_t w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    if (kWindows) {
+        __shared__ alignas(16) uint8_t stage[kWindows ? kThreads / 32 : 1][kWindows ? (kCache == PKV_INT4 ? 8 : 16) * D : 16];
+        const uint32_t windows = static_cast<uint32_t>((a.num_tokens + 15) / 16) * a.kv_heads;
+        if (w < windows) {
+            const uint32_t window = w / a.kv_heads;
+            append_v_window<D, kMode, kCache>(a, window, w - window * a.kv_heads, stage[threadIdx.x / 32]);
+            return;
+        }
+        w -= windows;
+    }
     const uint32_t token = w / units, unit = w - token * units;
     if (token >= static_cast<uint32_t>(a.num_tokens)) return;
     const Place at = place_of<kMode>(lane, a.rotary_dim);
@@ -357,9 +480,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(co
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (!live) continue;
-        constexpr float kLimit = kCache == PKV_INT4 ? 7.f : 127.f;
-        // (a zero row's scale is 0 in a 4-bit cache, 1 in an int8 one)
-        const float scale = kCache == PKV_INT4 ? top * kQ4Step : top > 0.f ? __fdiv_rn(top, kLimit) : 1.f;
+        const float scale = scale_of<kCache>(top);
         const Codes<kCache> code(scale);
         uint32_t cx[8], cy[8];
 #pragma unroll
@@ -406,13 +527,15 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(co
 template <int D, int kMode, int kCache, typename T, int kBatch>
 cudaError_t run_batch(const RotaryAppendArgs& a, cudaStream_t s) {
     constexpr int kHeads = kBatch * 32 / (D / 16), kWarps = kThreads / 32;
-    const int64_t units = a.num_tokens * ((a.q_heads + kHeads - 1) / kHeads + 2 * ((a.kv_heads + kHeads - 1) / kHeads));
+    constexpr bool kWindows = by_windows(kCache, kBatch);
+    const int64_t units = a.num_tokens * ((a.q_heads + kHeads - 1) / kHeads + (kWindows ? 1 : 2) * ((a.kv_heads + kHeads - 1) / kHeads)) +
+                          (kWindows ? (a.num_tokens + 15) / 16 * a.kv_heads : 0);
     return launch_pdl(append_rotary_kernel<D, kMode, kCache, T, kBatch>, dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, a);
 }
 template <int D, int kMode, int kCache, typename T>
 cudaError_t run_append(const RotaryAppendArgs& a, cudaStream_t s) {
-    // two batches of a warp's loads in flight (4096 tokens of 32 + 2 x 8 heads, a 4-bit cache, with their gather: 38.2 us;
-    // 4.6 more with one, 1.8 with four)
+    // two batches of a warp's loads in flight (4096 tokens of 32 + 2 x 8 heads, a 4-bit cache, with their gather, 38.2 us
+    // then: 4.6 more with one, 1.8 with four)
     constexpr int kBatch = kMode == kAny ? 1 : 2;
     // few rows: every warp takes as few as it can, so that they spread over the SMs
     const int64_t rows = a.num_tokens * (a.q_heads + 2 * a.kv_heads);
