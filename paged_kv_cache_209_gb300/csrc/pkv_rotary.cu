@@ -15,8 +15,8 @@
 //
 // The append is pure streaming by its bytes (q in and out, k and v in, the pools' share
 // out), and bound by its instructions, most of all by the exact rounding. Measured in a
-// captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a 4-bit cache 23.3 us, 88 MB
-// at 3.8 TB/s (27.9 while V's codes went byte by byte); ragged prompts of 24 + 2 x 8 heads into
+// captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a 4-bit cache 21.9 us, 88 MB
+// at 4.0 TB/s (27.9 while V's codes went byte by byte; 16 with the rounding of one float32, inexact); ragged prompts of 24 + 2 x 8 heads into
 // bf16 pools 27.6 us, 5.3 TB/s; a decode step of 32 tokens 2.5 us. A warp that goes from unit
 // to unit with the next one's rows on their way took 1.8 us more for the first, 2.7 for the second.
 #include <math.h>
@@ -143,6 +143,21 @@ __device__ __forceinline__ bool decided(uint64_t r, uint64_t off, uint32_t& word
     return pack_bf16x2(a, b) == word;
 }
 
+// (The pairs that a lane's halves leave open, one at a time: short code, as few lanes come here. 4096 tokens 21.9
+// us, 23.3 with every pair's own code; of neighbours, whose words hold whole pairs, 27.6 so and 28.4 one at a time.)
+__device__ __forceinline__ float pick(const float (&v)[8], int e) {
+    float x = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) x = e == i ? v[i] : x;
+    return x;
+}
+__device__ __forceinline__ uint32_t pick(const uint32_t (&v)[4], int i) { return i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3]; }
+// Two elements' words x and y (their partners) turned by (c0, s0) and (c1, s1).
+__device__ __forceinline__ uint32_t turned_pair(uint32_t x, uint32_t y, float c0, float s0, float c1, float s1) {
+    const float lo = turned_exactly(bf16lo_to_f32(x), c0, bf16lo_to_f32(y), s0), hi = turned_exactly(bf16hi_to_f32(x), c1, bf16hi_to_f32(y), s1);
+    return __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+}
+
 // Turns the lane's vectors of a row of bf16s, two elements at a time. `size`: the largest of the
 // lane's |c| and |s|. With X the larger of a pair's magnitudes, |y s| <= X size and |r| <= 2
 // X size, so r = x c - y s is off by at most 2^-24 (|y s| + |r|) <= 3 2^-24 X size (and 2^-149
@@ -158,16 +173,23 @@ __device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat1
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1), y0 = y.get(2 * i), y1 = y.get(2 * i + 1);
-            const uint64_t xx = f32x2_pack(x0, x1), yy = f32x2_pack(y0, y1), cc = f32x2_pack(c[2 * i], c[2 * i + 1]);
+            const uint64_t xx = f32x2_pack(x0, x1), yy = f32x2_pack(y0, y1), cc = f32x2_pack(c[2 * i], c[2 * i + 1]), ss = f32x2_pack(s[2 * i], s[2 * i + 1]);
             const uint64_t off = f32x2_pack(fmaf(fmaxf(fabsf(x0), fabsf(y0)), k, 2.8026e-45f), fmaf(fmaxf(fabsf(x1), fabsf(y1)), k, 2.8026e-45f));
-            if (!decided(f32x2_fma(xx, cc, f32x2_mul(yy, f32x2_pack(-s[2 * i], -s[2 * i + 1]))), off, a.w[i])) open |= 1u << i;
-            if (!decided(f32x2_fma(yy, cc, f32x2_mul(xx, f32x2_pack(s[2 * i], s[2 * i + 1]))), off, b.w[i])) open |= 16u << i;
+            if (!decided(f32x2_fma(xx, cc, f32x2_mul(yy, f32x2_mul(ss, f32x2_pack(-1.f, -1.f)))), off, a.w[i])) open |= 1u << i;
+            if (!decided(f32x2_fma(yy, cc, f32x2_mul(xx, ss)), off, b.w[i])) open |= 16u << i;
         }
-        if (open) {
+#pragma unroll 1
+        while (open) {
+            const int bit = __ffs(open) - 1, i = bit & 3;
+            open &= open - 1;
+            const bool second = bit >= 4;
+            const uint32_t xw = pick(x.w, i), yw = pick(y.w, i);
+            const float s0 = pick(s, 2 * i), s1 = pick(s, 2 * i + 1);
+            const uint32_t w = turned_pair(second ? yw : xw, second ? xw : yw, pick(c, 2 * i), second ? -s0 : s0, pick(c, 2 * i + 1), second ? -s1 : s1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (open >> (e / 2) & 1) a.set(e, turned_exactly(x.get(e), c[e], y.get(e), s[e]));
-                if (open >> (4 + e / 2) & 1) b.set(e, turned_exactly(y.get(e), c[e], x.get(e), -s[e]));
+            for (int j = 0; j < 4; ++j) {
+                if (bit == j) a.w[j] = w;
+                if (bit == 4 + j) b.w[j] = w;
             }
         }
     } else if (kMode == kNeighbours) {
