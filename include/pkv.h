@@ -596,7 +596,7 @@ PKV_API pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_st
 /*
  * pkv_append_q4 -- quantizing slot-mapped append of bf16 k, v
  * ([num_tokens][num_kv_heads][head_dim]) into the 4-bit cache. Arguments, checks and
- * errors as pkv_append.
+ * errors as pkv_append, but a slot that fast mode meets twice may hold parts of both tokens.
  */
 PKV_API pkv_status pkv_append_q4(const void* k, const void* v, const int64_t* slot_mapping, int64_t num_tokens,
                                  void* cache, const pkv_cache_desc* desc, uint32_t flags, void* stream);
@@ -742,7 +742,8 @@ PKV_API pkv_status pkv_rotary_table(const double* frequencies, int32_t rotary_di
  * A position outside the table leaves its token's rows unwritten and sets
  * PKV_DEVERR_RANGE, as does a slot beyond the pool for k and v; a negative position with
  * a negative slot is padding (nothing is written, no error). With PKV_FLAG_CHECKED these
- * return PKV_ERR_RANGE. Other errors as pkv_append.
+ * return PKV_ERR_RANGE. Other errors as pkv_append; a slot that fast mode meets twice may
+ * hold parts of both tokens.
  */
 PKV_API pkv_status pkv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                      int64_t v_stride, const int32_t* positions, const float* table,

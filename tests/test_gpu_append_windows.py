@@ -128,3 +128,48 @@ def test_bad_rows_in_the_middle_of_a_block(pkv, cache):
         pkv.pkv_append_rotary(q[i], k[i], v[i], pos[i], table, slots[i], *want)
     for x, y in zip(got, want):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("cache", ["q4", "q8"])
+def test_checked_calls_refuse_a_slot_named_twice(pkv, cache):
+    tokens, kv, d, heads = 1400, 2, 128, 8
+    q, k, v = (torch.zeros((tokens, h, d), dtype=torch.bfloat16, device="cuda") for h in (heads, kv, kv))
+    slots, pos = torch.arange(tokens, device="cuda"), torch.arange(tokens, dtype=torch.int32, device="cuda")
+    table = pkv.pkv_rotary_table(pkv.pkv_rotary_frequencies(d).cuda(), tokens)
+    pools, before = pools_of(cache, tokens // B + 1, kv, d, 9), pools_of(cache, tokens // B + 1, kv, d, 9)
+    slots[1000] = 17
+    with pytest.raises(pkv.PkvError, match="PKV_ERR_OVERLAP"):
+        pkv.pkv_append_rotary(q, k, v, pos, table, slots, *pools, flags=pkv.PKV_FLAG_CHECKED)
+    slots[1000] = 1000
+    pos[999] = tokens
+    with pytest.raises(pkv.PkvError, match="PKV_ERR_RANGE"):
+        pkv.pkv_append_rotary(q, k, v, pos, table, slots, *pools, flags=pkv.PKV_FLAG_CHECKED)
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(pools, before))
+    pos[999] = 999
+    pkv.pkv_append_rotary(q, k, v, pos, table, slots, *pools, flags=pkv.PKV_FLAG_CHECKED)
+
+
+@pytest.mark.parametrize("cache", ["q4", "q8"])
+def test_captured(pkv, cache):
+    """A captured append of many rows, replayed on other values and slots."""
+    tokens, kv, d, heads = 1500, 2, 128, 6
+    blocks = 2 * tokens // B + 200
+    g = torch.Generator(device="cuda").manual_seed(10)
+    rows = torch.randn((tokens, (heads + 2 * kv) * d), device="cuda", generator=g).to(torch.bfloat16)
+    q, k, v = (x.view(tokens, -1, d) for x in (rows[:, :heads * d], rows[:, heads * d:(heads + kv) * d], rows[:, (heads + kv) * d:]))
+    slots = torch.from_numpy(slots_of("ragged", tokens, blocks, 11).astype(np.int64)).cuda()
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    table = pkv.pkv_rotary_table(pkv.pkv_rotary_frequencies(d).cuda(), tokens)
+    captured, eager = pools_of(cache, blocks, kv, d, 12), pools_of(cache, blocks, kv, d, 12)
+    out = torch.zeros((tokens, heads, d), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.pkv_append_rotary(q, k, v, pos, table, slots, *captured, q_out=out)
+    for seed in (13, 14):
+        rows.normal_()
+        slots.copy_(torch.from_numpy(slots_of("ragged", tokens, blocks, seed).astype(np.int64)))
+        graph.replay()
+        want = pkv.pkv_append_rotary(q, k, v, pos, table, slots, *eager)
+        assert torch.equal(out, want)
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(captured, eager))
