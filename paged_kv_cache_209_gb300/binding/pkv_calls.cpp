@@ -7,8 +7,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>
@@ -57,7 +56,10 @@ struct Call {
     const int32_t* ints(const char* name, PyObject* o, at::IntArrayRef shape) const {
         return static_cast<const int32_t*>(whole(name, o, at::kInt, shape).const_data_ptr());
     }
-    at::TensorOptions options(at::ScalarType type) const { return at::TensorOptions().dtype(type).device(at::kCUDA, here); }
+    // A fresh tensor (past the dispatcher, which takes as long as the allocation).
+    Tensor fresh(at::ScalarType type, at::IntArrayRef shape) const {
+        return Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(here)), std::nullopt));
+    }
 };
 
 int64_t integer(const char* name, PyObject* o) {
@@ -166,7 +168,7 @@ PyObject* attention_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int32_t* start = decode ? nullptr : c.ints("query_start", a[5], {t.batch + 1});
         const float scale = static_cast<float>(number("scale", a[6]));
         const int32_t most = integer32("max_query_len", a[7]);
-        const Tensor out = a[8] == Py_None ? at::empty_like(q) : c.whole("out", a[8], at::kBFloat16, q.sizes());
+        const Tensor out = a[8] == Py_None ? c.fresh(at::kBFloat16, q.sizes()) : c.whole("out", a[8], at::kBFloat16, q.sizes());
         const Tensor& work = tensor("workspace", a[9]);
         c.whole("workspace", a[9], work.scalar_type());
         const uint32_t flags = static_cast<uint32_t>(integer("flags", a[10]));
@@ -203,7 +205,7 @@ PyObject* gather_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out[2];
         const char* names[2] = {"k_out", "v_out"};
         for (int i = 0; i < 2; ++i)
-            out[i] = a[8 + i] == Py_None ? at::empty(shape, c.options(type_of(dtype))) : c.whole(names[i], a[8 + i], type_of(dtype), shape);
+            out[i] = a[8 + i] == Py_None ? c.fresh(type_of(dtype), shape) : c.whole(names[i], a[8 + i], type_of(dtype), shape);
         const uint32_t flags = static_cast<uint32_t>(integer("flags", a[10]));
         void* stream = pointer(a[11]);
         const int status = call(flags, [&]() -> int {
@@ -284,7 +286,7 @@ PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
             q_at = r.t.const_data_ptr();
             q_stride = r.stride;
             if (a[11] == Py_None) {
-                out = at::empty({tokens, q.size(1), desc.head_dim}, c.options(type));
+                out = c.fresh(type, {tokens, q.size(1), desc.head_dim});
                 out_stride = q.size(1) * desc.head_dim;
             } else {
                 const Rows o = rows_of(c, "q_out", a[11], type, tokens, q.size(1), desc.head_dim);
@@ -316,17 +318,17 @@ PyObject* rotary_table(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (positions < 0) throw Refused("num_positions is at least 0");
         const float factor = static_cast<float>(number("factor", a[4]));
         const int64_t shape[2] = {positions, 2 * f.size(0)};
-        const Tensor out = a[5] == Py_None ? at::empty(shape, c.options(at::kFloat)) : c.whole("out", a[5], at::kFloat, shape);
+        const Tensor out = a[5] == Py_None ? c.fresh(at::kFloat, shape) : c.whole("out", a[5], at::kFloat, shape);
         const int status = pkv_rotary_table(static_cast<const double*>(f.const_data_ptr()), static_cast<int32_t>(shape[1]), first, positions, factor,
                                             static_cast<float*>(out.mutable_data_ptr()), pointer(a[6]));
         return result(a[5] == Py_None ? THPVariable_Wrap(out) : Py_NewRef(a[5]), status);
     });
 }
 
-// `n` elements of a fresh one-dimensional tensor from element `from` on, as a tensor of its own on the same memory. (A view
+// `n` elements of a type in a fresh tensor's memory, from element `from` of that type on, as a tensor of their own. (A view
 // through the dispatcher costs a microsecond.)
-Tensor part_of(const Tensor& whole, int64_t from, int64_t n) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+Tensor part_of(const Tensor& whole, at::ScalarType type, int64_t from, int64_t n) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
     t.unsafeGetTensorImpl()->set_storage_offset(from);
     return t;
@@ -350,11 +352,12 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* at[7];
         Tensor outs[7];
         if (a[9] == Py_None) {
-            outs[0] = at::empty({rows}, c.options(at::kLong));
-            int64_t all = 0;
+            // one allocation: the slots, then the numbers of 32 bits
+            int64_t all = 2 * rows;
             for (int i = 1; i < 7; ++i) all += sizes[i];
-            const Tensor rest = at::empty({all}, c.options(at::kInt));
-            for (int64_t i = 1, from = 0; i < 7; from += sizes[i++]) outs[i] = part_of(rest, from, sizes[i]);
+            const Tensor whole = c.fresh(at::kInt, {all});
+            outs[0] = part_of(whole, at::kLong, 0, rows);
+            for (int64_t i = 1, from = 2 * rows; i < 7; from += sizes[i++]) outs[i] = part_of(whole, at::kInt, from, sizes[i]);
         } else {
             static const char* names[7] = {"slot_mapping", "positions", "query_start", "new_context_lens", "new_held_blocks", "new_free_count", "result"};
             if (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 7)

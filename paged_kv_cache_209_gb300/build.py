@@ -60,7 +60,7 @@ def _binding_command() -> list[str]:
             "-I", INCLUDE, "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING, "-o", CALLS, "-L", os.path.join(home, "lib"),
             # (libpkv's symbols are found when the binding is loaded, beside it)
-            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10"]
 
 
 def _binding_stale() -> bool:
