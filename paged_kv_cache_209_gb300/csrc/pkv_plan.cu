@@ -6,9 +6,10 @@
 // Every CTA reads all lengths (12 bytes a sequence, out of L2) and sums them up in
 // shared memory, so that nothing waits on another CTA; then each writes its share of the
 // rows, of the sequences and of the new table entries, whose sequences it finds by
-// bisection in those sums. Bound by latency: lengths in, three scans, the free blocks'
-// ids, rows out: 5.4 us for 32 sequences, 9.3 for 1000 of which some are prompts (111000
-// rows), in a captured graph; called from Python 11 us, the host's share being 9.
+// bisection in those sums. Bound by latency: lengths in, two scans, a bisection, the
+// block's id, rows out: 3.4 us for 32 sequences, 5.1 for 1000 of which some are prompts, in
+// a captured graph, a row a thread (four, which share a bisection: 5.4 and 9.3); called
+// from Python 8.4 and 9, the host's share being 8.
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -17,7 +18,6 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerThread = 4;
 
 struct Sums {
     int64_t rows;
@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t most = static_cast<int64_t>(a.max_blocks) * 16;
     auto valid = [&](int64_t n, int64_t m, int64_t h) { return n >= 0 && m >= 0 && h >= 0 && h <= a.max_blocks && n <= 16 * h && n + m <= most; };
+    const int64_t left = *a.free_count;
     int64_t rows = 0, need = 0;  // before this turn's sequences
     bool bad = false;
     for (int i0 = 0; i0 < a.batch; i0 += kThreads) {
@@ -93,7 +94,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
         need_sum[a.batch] = static_cast<int32_t>(need);
     }
     __syncthreads();
-    const int64_t left = *a.free_count;
     const bool count_ok = left >= 0 && left <= a.free_capacity;
     const bool planned = count_ok && rows <= a.num_rows && need <= left;
     if (blockIdx.x == 0) {
@@ -125,29 +125,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs a) {
         }
     }
     // ---- rows
-    for (int64_t r0 = at * kRowsPerThread; r0 < a.num_rows; r0 += stride * kRowsPerThread) {
-        int i = -1, n = 0, h = 0;
-        for (int64_t r = r0; r < min(r0 + kRowsPerThread, a.num_rows); ++r) {
-            int64_t slot = -1;
-            int32_t pos = -1;
-            if (planned && r < rows) {
-                if (i < 0 || r >= row_sum[i + 1]) {
-                    i = find(row_sum, a.batch, static_cast<int>(r));
-                    n = a.lens[i];
-                    h = a.held[i];
-                }
-                pos = n + static_cast<int>(r - row_sum[i]);
-                const int b = pos >> 4;
-                const int32_t id = b < h ? a.tables[static_cast<int64_t>(i) * a.max_blocks + b]
-                                         : a.free_blocks[left - 1 - need_sum[i] - (b - h)];
-                if (inside(id))
-                    slot = static_cast<int64_t>(id) * 16 + (pos & 15);
-                else
-                    atomicOr(a.status, PKV_DEVERR_RANGE);
-            }
-            a.slots[r] = slot;
-            a.positions[r] = pos;
+    for (int64_t r = at; r < a.num_rows; r += stride) {
+        int64_t slot = -1;
+        int32_t pos = -1;
+        if (planned && r < rows) {
+            const int i = find(row_sum, a.batch, static_cast<int>(r));
+            const int h = a.held[i];
+            pos = a.lens[i] + static_cast<int>(r - row_sum[i]);
+            const int b = pos >> 4;
+            const int32_t id = b < h ? a.tables[static_cast<int64_t>(i) * a.max_blocks + b]
+                                     : a.free_blocks[left - 1 - need_sum[i] - (b - h)];
+            if (inside(id))
+                slot = static_cast<int64_t>(id) * 16 + (pos & 15);
+            else
+                atomicOr(a.status, PKV_DEVERR_RANGE);
         }
+        a.slots[r] = slot;
+        a.positions[r] = pos;
     }
 }
 
@@ -187,8 +181,7 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
         const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    const int64_t per = static_cast<int64_t>(kThreads) * kRowsPerThread;
-    const int64_t want = (a.num_rows + per - 1) / per, most = device_sm_count();
+    const int64_t want = (a.num_rows + kThreads - 1) / kThreads, most = device_sm_count();
     return launch_pdl(plan_kernel, dim3(static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most)), dim3(kThreads), smem, s, a);
 }
 
