@@ -35,7 +35,7 @@
 // apart, and joining the pieces (3 us). Two queries a sequence take the same; four 85.5 us, 3.3
 // TB/s: bound by its instructions (two row tiles: 300 a block, their pipes busy 37 % each in
 // converting and 34 % in products, which share the issue); eight 154. 64 ragged contexts of up
-// to 8191 tokens, 24 heads: 38.9 us, 3.5 TB/s. One of 1000 tokens: 9.4 us, all of it latency.
+// to 8191 tokens, 24 heads: 38.5 us, 3.6 TB/s. One of 1000 tokens: 9.4 us, all of it latency.
 #include <math.h>
 #include <mutex>
 
@@ -52,9 +52,10 @@ constexpr int kConsumers = 4;
 constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int kIssueLanes = 8;  // stages whose copies are issued together
 // Cost of a segment shorter than kShortBlocks beside its blocks, in blocks, where there are
-// blocks enough for every CTA (64 contexts of 1 to 8191 tokens: 38.9 us, 45.4 without; many
-// equal short ones lose by it, 256 of 100 tokens 33.9 against 30.8, being cut more rarely).
-constexpr int kSegmentCost = 16, kShortBlocks = 256;
+// blocks enough for every CTA (64 contexts of 1 to 8191 tokens: 38.5 us, 45.4 without; 40 of up to 6000
+// with four queries 34.8, 35.9 with 16 and 38 with 12; 256 of up to 16384 231.4, 234 with 28; many equal
+// short ones lose by it, 256 of 100 tokens 33.5 against 30.8, being cut more rarely).
+constexpr int kSegmentCost = 20, kShortBlocks = 256;
 // Where there are not, a CTA gets about this many blocks (one of 1000 tokens: 9.4 us; 11.6
 // with 2, 9.7 with 32; its four queries a sequence 12.3, 16.4 and 14.2).
 constexpr int kLeastBlocks = 8;
