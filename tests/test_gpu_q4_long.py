@@ -152,3 +152,43 @@ def test_two_graphs_on_one_workspace(pkv):
             check(out, *want)
     for c, (want, bound) in zip(cases, wants):
         check(call(c, None), want, bound)
+
+
+def test_every_call_on_another_stream(pkv):
+    """Inputs that become ready on the stream late; outputs that the calls allocate are ready there, and usable on the
+    caller's stream once it waits."""
+    d, kv, heads, tokens, batch = 128, 2, 8, 600, 5
+    g = torch.Generator(device="cuda").manual_seed(9)
+    qkv = torch.randn((tokens, (heads + 2 * kv) * d), device="cuda", generator=g).to(torch.bfloat16)
+    f = pkv.pkv_rotary_frequencies(d).cuda()
+    lens0, held0 = (torch.zeros(batch, dtype=torch.int32, device="cuda") for _ in range(2))
+    new = torch.full((batch,), tokens // batch, dtype=torch.int32, device="cuda")
+    free, left = torch.arange(60, dtype=torch.int32, device="cuda"), torch.tensor([60], dtype=torch.int32, device="cuda")
+
+    def steps(rows, tables, cache, **kw):
+        q, k, v = (x.view(tokens, -1, d) for x in (rows[:, :heads * d], rows[:, heads * d:(heads + kv) * d], rows[:, (heads + kv) * d:]))
+        table = pkv.pkv_rotary_table(f, 200, **kw)
+        slots, pos, start, lens, held, count, result = pkv.pkv_plan_step(lens0, new, held0, free, left, tables, tokens, **kw)
+        turned = pkv.pkv_append_rotary(q, k, v, pos, table, slots, cache, **kw)
+        out = pkv.pkv_multiquery_attention_q4(turned, cache, tables, lens, start, 0.1, tokens // batch, **kw)
+        one = pkv.pkv_decode_attention_q4(turned[:batch], cache, tables, lens, 0.1, **kw)
+        return [table, slots, pos, start, lens, held, count, result, turned, out, one, *pkv.pkv_gather_q4(cache, tables, lens, start, tokens, **kw)]
+
+    fresh = lambda: (torch.full((batch, 10), -1, dtype=torch.int32, device="cuda"),  # noqa: E731
+                     torch.zeros((60, kv, Q.record_bytes(d)), dtype=torch.uint8, device="cuda"))
+    want = steps(qkv, *fresh())
+    side = torch.cuda.Stream()
+    late, tables_cache = torch.zeros_like(qkv), fresh()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            late.zero_()
+            torch.cuda._sleep(2_000_000)
+            late.copy_(qkv)
+            tables_cache[0].fill_(-1)
+            tables_cache[1].zero_()
+        got = steps(late, *tables_cache, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        side.wait_stream(torch.cuda.current_stream())
