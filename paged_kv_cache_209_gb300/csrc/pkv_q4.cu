@@ -35,7 +35,7 @@
 // apart, and joining the pieces (3 us). Two queries a sequence take the same; four 85.5 us, 3.3
 // TB/s: bound by its instructions (two row tiles: 300 a block, their pipes busy 37 % each in
 // converting and 34 % in products, which share the issue); eight 154. 64 ragged contexts of up
-// to 8191 tokens, 24 heads: 38.5 us, 3.6 TB/s. One of 1000 tokens: 9.4 us, all of it latency.
+// to 8191 tokens, 24 heads: 38.5 us, 3.6 TB/s. One of 1000 tokens: 9.1 us, all of it latency.
 #include <math.h>
 #include <mutex>
 
@@ -56,9 +56,11 @@ constexpr int kIssueLanes = 8;  // stages whose copies are issued together
 // with four queries 34.8, 35.9 with 16 and 38 with 12; 256 of up to 16384 231.4, 234 with 28; many equal
 // short ones lose by it, 256 of 100 tokens 33.5 against 30.8, being cut more rarely).
 constexpr int kSegmentCost = 20, kShortBlocks = 256;
-// Where there are not, a CTA gets about this many blocks (one of 1000 tokens: 9.4 us; 11.6
-// with 2, 9.7 with 32; its four queries a sequence 12.3, 16.4 and 14.2).
-constexpr int kLeastBlocks = 8;
+// Where there are not, a CTA gets about this many blocks: of contexts of one length (one of 1000 tokens 9.1
+// us; 9.3 with 8, 11.6 with 2, 9.6 with 24; 14 of 700 10.7, 14.0 with 8; 9 of 700 with four queries 13.7
+// and 20; but 4 of 700 10.1 and 9.5), and of others (14 of up to 1100 19.0 us, 25.5 with 12) or where two
+// warps share a block (one of 1024 tokens with eight queries 15.7, 17.4 with 12).
+constexpr int kLeastAlike = 12, kLeastBlocks = 8;
 
 // The base m of a row: where some P' = 2^(x - m) v would leave f16 it moves to the largest
 // x + log2 |v| less kHeadroom, so that what is rounded to f16 lies high in its range for
@@ -102,7 +104,7 @@ struct M4 {
     static constexpr int kOffPieces = kOffState + kConsumers * kStateFloats * 4;  // per slot; then the cut ones, and their number
     static constexpr int kOffQ = kOffPieces + (kQSlots + 2) * sizeof(Piece4) + 16;
     static size_t smem_bytes(int warps_per_unit, int batch) {
-        return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + (3 * static_cast<size_t>(batch) + 1) * 4;
+        return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + (3 * static_cast<size_t>(batch) + 2) * 4;
     }
     static_assert(kOffBars % 16 == 0 && kOffQ % 16 == 0, "alignment");
 };
@@ -225,11 +227,12 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int blocks = 0, cost = 0, active = 0;
+        int blocks = 0, cost = 0, active = 0, longest = 0;
         for (int base = 0; base < a.batch; base += 32) {
             int x = base + lane < a.batch ? s_pre[base + lane] : 0;
             int y = x > 0 && x < kShortBlocks ? x + kSegmentCost : x;
             active += __popc(__ballot_sync(0xffffffffu, x > 0));
+            longest = max(longest, x);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x1 = __shfl_up_sync(0xffffffffu, x, o), y1 = __shfl_up_sync(0xffffffffu, y, o);
@@ -242,7 +245,8 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
             blocks += __shfl_sync(0xffffffffu, x, 31);
             cost += __shfl_sync(0xffffffffu, y, 31);
         }
-        if (lane == 0) *s_active = active;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) s_active[0] = active, s_active[1] = longest;
     }
     __syncthreads();
     if (a.qstart == nullptr) {
@@ -260,10 +264,12 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
     // Few blocks: fewer CTAs, as many for each segment, whose cuts then fall between segments of one
     // length (a CTA with two pieces takes them one after the other). (No range is empty, so a segment's
     // pieces lie in consecutive CTAs.)
-    long long ctas = U / kLeastBlocks;
+    const bool alike = W == 1 && static_cast<long long>(s_active[0]) * s_active[1] == s_pre[a.batch - 1];
+    // (two divisions by constants: one by either is a loop)
+    long long ctas = alike ? U / kLeastAlike : U / kLeastBlocks;
     const bool few = ctas < gridDim.x;
     if (few) {
-        const long long segments = static_cast<long long>(a.kv_heads) * *s_active;
+        const long long segments = static_cast<long long>(a.kv_heads) * s_active[0];
         ctas = ctas < 1 ? 1 : ctas >= segments ? ctas / segments * segments : ctas;
     } else {
         ctas = gridDim.x;

@@ -204,3 +204,12 @@ def test_refusals_of_the_binding(pkv):
     with pytest.raises(pkv.PkvError, match="PKV_ERR_WORKSPACE"):
         call(w=torch.zeros(128, dtype=torch.uint8, device="cuda"))
     assert call(q=s["q"][:0], t=s["tables"][:0], l=s["lens"][:0]).shape == (0, 8, D)
+
+
+@pytest.mark.parametrize("lens,news,kv", [([700] * 14, [1] * 14, 8), ([700] * 9, [4] * 9, 8), ([1000], [1], 8), ([300] * 8, [1] * 8, 3),
+                                          ([0] * 3 + [320] * 5, [0] * 3 + [2] * 5, 2), ([1024], [8], 8), ([4000], [1], 8),
+                                          ([16] * 30, [1] * 30, 8), ([641, 650, 656], [1] * 3, 8)])
+def test_few_contexts_of_one_length(pkv, lens, news, kv):
+    """(Fewer CTAs than fit, a whole number for each (sequence, KV head).)"""
+    s = make(70, lens, news, 4 * kv, kv, D)
+    check(pkv.pkv_multiquery_attention_q4(s["q"], s["cache"], s["tables"], s["lens"], s["start"], s["scale"], max(news)), *reference(s))
