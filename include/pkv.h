@@ -678,7 +678,10 @@ typedef enum {
                               n_i >= high_turns, f_i / stretch where n_i <= low_turns,
                               between them the mix linear in n_i                       */
     PKV_ROTARY_RAMP = 4    /* the mix linear in i between the dimensions that make
-                              high_turns (rounded down) and low_turns (rounded up)     */
+                              high_turns (rounded down, at least 0) and low_turns
+                              (rounded up, at most R - 1: it may end past the last
+                              pair, R / 2 - 1). Where the second is not above the
+                              first, f_i up to the first and f_i / stretch above it    */
 } pkv_rotary_kind;
 
 typedef struct {

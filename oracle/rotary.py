@@ -31,7 +31,7 @@ def frequencies(dim, base, kind="plain", stretch=1.0, original_context=0.0, low_
         elif kind == "ramp":
             def at(turns):
                 return dim / 2 * math.log(original_context / (2 * math.pi * turns)) / math.log(base)
-            first, last = max(math.floor(at(high_turns)), 0), min(math.ceil(at(low_turns)), dim // 2 - 1)
+            first, last = max(math.floor(at(high_turns)), 0), min(math.ceil(at(low_turns)), dim - 1)
             part = min(max((i - first) / max(last - first, 1e-3), 0), 1)
             f = (1 - part) * f + part * f / stretch
         found.append(f)

@@ -673,7 +673,7 @@ bool rotary_frequencies(int R, double base, const pkv_rotary_scaling* scaling, d
         // f_i makes n turns over the context where i = (R / 2) ln(context / (2 pi n)) / ln(base)
         auto makes = [&](double n) { return R / 2.0 * log(s.original_context / (kTurn * n)) / log(base); };
         first = fmax(floor(makes(s.high_turns)), 0.0);
-        last = fmin(ceil(makes(s.low_turns)), R / 2.0 - 1.0);
+        last = fmin(ceil(makes(s.low_turns)), R - 1.0);  // (past the last pair: the ramp goes on there, and that pair keeps its share)
     }
     for (int i = 0; i < R / 2; ++i) {
         const double f = pow(base, -2.0 * i / R);
