@@ -106,6 +106,7 @@ struct M4 {
     static size_t smem_bytes(int warps_per_unit, int batch) {
         return 128 + kOffQ + kQSlots * kRows * warps_per_unit * D * 2 + (3 * static_cast<size_t>(batch) + 2) * 4;
     }
+    static size_t most_smem_bytes() { return smem_bytes(R, kMaxBatchPerLaunch); }  // (warps_per_unit is at most R)
     static_assert(kOffBars % 16 == 0 && kOffQ % 16 == 0, "alignment");
 };
 
@@ -772,23 +773,29 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
     }
 }
 
+// The kernel's shared-memory limit belongs to the function, which calls of all threads share: every call sets it to
+// the largest launch's, so that none takes it away from another's launch.
+template <int D, int R>
+cudaError_t allow_smem() {
+    return cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(M4<D, R>::most_smem_bytes()));
+}
+
 template <int D, int R>
 cudaError_t run_mq4(const Q4Args& a, cudaStream_t s) {
     using C = M4<D, R>;
     const size_t smem = C::smem_bytes(a.warps_per_unit, a.batch);
-    const cudaError_t e = cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_smem<D, R>();
     if (e != cudaSuccess) return e;
     return launch_pdl(mq4_kernel<D, R>, dim3(a.num_ctas), dim3(kThreads), smem, s, a);
 }
 
-// Resident CTAs of an SM, at the largest launch.
+// Resident CTAs of an SM, at the largest launch; 0 where that could not be found out.
 template <int D, int R>
 int resident(int warps_per_unit) {
     const size_t smem = M4<D, R>::smem_bytes(warps_per_unit, kMaxBatchPerLaunch);
     int n = 0;
-    cudaFuncSetAttribute(mq4_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mq4_kernel<D, R>, kThreads, smem) != cudaSuccess || n < 1) n = 1;
-    return n;
+    if (allow_smem<D, R>() != cudaSuccess) return 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mq4_kernel<D, R>, kThreads, smem) == cudaSuccess && n > 0 ? n : 0;
 }
 
 }  // namespace
@@ -812,7 +819,7 @@ Q4Plan q4_plan(int head_dim, int rows) {
         else
             per_sm = p.row_tiles == 1 ? resident<64, 1>(1) : resident<64, 2>(p.warps_per_unit);
     }
-    p.num_ctas = per_sm * device_sm_count();
+    p.num_ctas = (per_sm > 0 ? per_sm : 1) * device_sm_count();  // (what failed is not kept, and asked for again)
     return p;
 }
 
