@@ -176,9 +176,12 @@ cudaError_t launch_check_plan(const PlanArgs& a, unsigned int* verdict, cudaStre
 }
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
-    const size_t smem = 2 * (static_cast<size_t>(a.batch) + 1) * sizeof(int32_t);
+    auto sums_bytes = [](int batch) { return 2 * (static_cast<size_t>(batch) + 1) * sizeof(int32_t); };
+    const size_t smem = sums_bytes(a.batch);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // (to the largest launch's: the limit is the function's, and another thread may be about to launch)
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(sums_bytes(PKV_MAX_PLAN_BATCH)));
         if (e != cudaSuccess) return e;
     }
     const int64_t want = (a.num_rows + kThreads - 1) / kThreads, most = device_sm_count();

@@ -81,3 +81,23 @@ def test_attention_q4_with_one_and_two_warps_a_block(pkv):
     made = [attention_q4(pkv, 600, 4, 128, 4), attention_q4(pkv, 600, 8, 128, 4)]
     torch.cuda.synchronize()
     in_turn_and_at_once([c for c, _ in made], [o for _, o in made])
+
+
+def plan(pkv, batch):
+    ints = lambda value, n=batch: torch.full((n,), value, dtype=torch.int32, device="cuda")  # noqa: E731
+    lens, new, held, free, left, tables = ints(5), ints(1), ints(1), ints(3, 8), ints(8, 1), ints(2)
+    slots = torch.zeros(batch, dtype=torch.int64, device="cuda")
+    out = [slots, ints(0), ints(0, batch + 1), ints(0), ints(0), ints(0, 1), ints(0, 2)]
+    lib = pkv.load_library()
+
+    def call(stream, keep=(lens, new, held, free, left, tables)):
+        return lib.pkv_plan_step(lens.data_ptr(), new.data_ptr(), held.data_ptr(), free.data_ptr(), 8, left.data_ptr(),
+                                 tables.data_ptr(), 1, batch, batch, 4, *(t.data_ptr() for t in out), 0, stream)
+    return call, out
+
+
+def test_plan_step(pkv):
+    """Batches whose sums take 131 and 48 KB."""
+    made = [plan(pkv, batch) for batch in (16384, 6100)]
+    torch.cuda.synchronize()
+    in_turn_and_at_once([c for c, _ in made], [o for _, o in made])
