@@ -449,6 +449,8 @@ struct Tc {
     static size_t smem_bytes(int G, int batch) {
         return 1024 + kOffScratch + scratch_floats(G) * 4 + 3 * static_cast<size_t>(batch) * 4;
     }
+    // of any launch (with the block offsets of a shared prefix)
+    static size_t most_smem_bytes() { return smem_bytes(8, kMaxBatchPerLaunch) + static_cast<size_t>(kMaxBatchPerLaunch) * 4; }
 };
 
 template <int D, int NST>
@@ -954,9 +956,6 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, int64_t rows, int head_
 
 template <typename K>
 int occupancy(K kernel, int threads, size_t smem) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) n = 0;
     return n;
@@ -980,7 +979,7 @@ int cached_occupancy(int kernel_id, int variant, size_t smem, int threads, const
         if (keys[i].dev == dev && keys[i].kernel == kernel_id && keys[i].variant == variant && keys[i].smem == smem)
             return vals[i];
     const int n = query(fnptr, threads, smem);
-    if (used < 64) {
+    if (used < 64 && n > 0) {  // (what failed is not kept)
         keys[used] = OccKey{dev, kernel_id, variant, smem};
         vals[used] = n;
         ++used;
@@ -988,8 +987,15 @@ int cached_occupancy(int kernel_id, int variant, size_t smem, int threads, const
     return n;
 }
 
+// The limit belongs to the function, which calls of all threads share: always the largest launch's.
+template <int D, int NST>
+cudaError_t allow_tc_smem() {
+    return cudaFuncSetAttribute(decode_tc_kernel<D, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Tc<D, NST>::most_smem_bytes()));
+}
 template <int D, int NST>
 int tc_query(const void*, int threads, size_t smem) {
+    if (allow_tc_smem<D, NST>() != cudaSuccess) return 0;
     return occupancy(decode_tc_kernel<D, NST>, threads, smem);
 }
 template <typename T, int D, int GMAX>
@@ -1006,9 +1012,7 @@ int variant_of(int dtype, int D, int gmax) { return (dtype == PKV_BF16 ? 4 : 0) 
 
 template <typename T, int D, int GMAX>
 cudaError_t run_cc(const DecodeArgs& a, int grid, size_t smem, cudaStream_t s) {
-    if (smem > 48 * 1024)
-        cudaFuncSetAttribute(decode_cc_kernel<T, D, GMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+    static_assert(4 * GMAX * D * 4 + 2 * 4 * GMAX * 4 + 3 * kMaxBatchPerLaunch * 4 <= 48 * 1024, "within the limit that needs no asking");
     return launch_pdl(decode_cc_kernel<T, D, GMAX>, dim3(grid), dim3(128), smem, s, a);
 }
 
@@ -1018,8 +1022,8 @@ cudaError_t run_tc(const DecodeArgs& a, int grid, size_t smem, cudaStream_t s) {
     const int64_t rows = a.num_blocks * a.kv_heads * 16;
     if (!encode_pool_map(&tmK, a.k_cache, rows, D) || !encode_pool_map(&tmV, a.v_cache, rows, D))
         return cudaErrorInvalidValue;
-    cudaFuncSetAttribute(decode_tc_kernel<D, NST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         static_cast<int>(smem));
+    const cudaError_t e = allow_tc_smem<D, NST>();
+    if (e != cudaSuccess) return e;
     return launch_pdl(decode_tc_kernel<D, NST>, dim3(grid), dim3(Tc<D, NST>::kThreads), smem, s, a, tmK, tmV);
 }
 

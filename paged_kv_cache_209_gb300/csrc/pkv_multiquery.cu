@@ -897,11 +897,10 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
 }
 
 template <typename K>
-int mq_occupancy(K kernel, int threads, size_t smem) {
+int mq_occupancy(K kernel, int threads, size_t smem) {  // 0 where it could not be found out
     int n = 0;
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-    return n;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) == cudaSuccess && n > 0 ? n : 0;
 }
 
 // Ring depth (a build-time knob): stages of 2 * 16 * D bytes (bf16) or 16 * D
@@ -939,8 +938,10 @@ cudaError_t run_mq(const MqArgs& a, int grid, cudaStream_t s) {
         tmS = tmK;  // unused by the bf16 path
     }
     const size_t smem = C::smem_bytes(a.batch);
-    cudaFuncSetAttribute(mq_tc_kernel<D, mq_stages<Q8>(), Q8, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         static_cast<int>(smem));
+    // (the limit is the function's, which calls of all threads share: always the largest launch's)
+    const cudaError_t e = cudaFuncSetAttribute(mq_tc_kernel<D, mq_stages<Q8>(), Q8, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(C::smem_bytes(kMaxBatchPerLaunch)));
+    if (e != cudaSuccess) return e;
     return launch_pdl(mq_tc_kernel<D, mq_stages<Q8>(), Q8, Wide>, dim3(grid), dim3(C::kThreads), smem, s, a, tmK, tmV, tmS);
 }
 
@@ -969,7 +970,7 @@ int mq_num_ctas(int head_dim, int batch, const pkv_decode_opts* opts, bool q8) {
             slot = mq_occupancy(mq_tc_kernel<64, kMqStages, false, false>, Mq<64, kMqStages>::kThreads,
                                 Mq<64, kMqStages>::smem_bytes(kMaxBatchPerLaunch));
     }
-    return slot * device_sm_count();
+    return (slot > 0 ? slot : 1) * device_sm_count();  // (what failed is not kept)
 }
 
 size_t mq_workspace_bytes(int batch, int kv_heads, int head_dim, int num_ctas, size_t* counters_offset,

@@ -101,3 +101,53 @@ def test_plan_step(pkv):
     made = [plan(pkv, batch) for batch in (16384, 6100)]
     torch.cuda.synchronize()
     in_turn_and_at_once([c for c, _ in made], [o for _, o in made])
+
+
+def pools_of(pkv, kind, head_dim, g):
+    rows = torch.randn((2, 4, 1, 16, head_dim), device="cuda", generator=g)
+    if kind == "q8":
+        codes = torch.randint(-128, 128, (4, 1, 16, head_dim), dtype=torch.int8, device="cuda", generator=g)
+        return [codes, codes.transpose(2, 3).contiguous(), torch.full((4, 1, 2, 16), 0.01, device="cuda")], pkv.PKV_INT8
+    return [rows[0].to(torch.bfloat16), rows[1].to(torch.bfloat16)], pkv.PKV_BF16
+
+
+def older_attention(pkv, kind, batch, head_dim, new):
+    """Decode (new 0) or multi-query attention over bf16 or int8 pools."""
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    pools, dtype = pools_of(pkv, kind, head_dim, g)
+    rows = batch * max(new, 1)
+    q = torch.randn((rows, 4, head_dim), device="cuda", generator=g).to(torch.bfloat16)
+    tables = torch.full((batch, 1), 2, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), 9, dtype=torch.int32, device="cuda")
+    start = torch.arange(0, rows + 1, max(new, 1), dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(q)
+    desc = pkv.CacheDesc(4, 16, 1, head_dim, dtype)
+    lib = pkv.load_library()
+    at = [p.data_ptr() for p in pools]
+    most = max(new, 1)
+    if kind == "q8":
+        size = lib.pkv_decode_q8_workspace_size(batch, 4, 1, most, ctypes.byref(desc), None)
+    elif new:
+        size = lib.pkv_multiquery_workspace_size(batch, 4, 1, most, ctypes.byref(desc), None)
+    else:
+        size = lib.pkv_decode_workspace_size(batch, 4, 1, ctypes.byref(desc), None)
+    work = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    rest = (0.1, out.data_ptr(), work.data_ptr(), size, ctypes.byref(desc), 0, None)
+
+    def call(stream, keep=(pools, q, tables, lens, start, work)):
+        if kind == "q8":
+            return lib.pkv_decode_attention_q8(q.data_ptr(), *at, tables.data_ptr(), 1, lens.data_ptr(), start.data_ptr(), batch, 4, most,
+                                               *rest, stream)
+        if new:
+            return lib.pkv_multiquery_attention(q.data_ptr(), *at, tables.data_ptr(), 1, lens.data_ptr(), start.data_ptr(), batch, 4, most,
+                                                *rest, stream)
+        return lib.pkv_decode_attention(q.data_ptr(), *at, tables.data_ptr(), 1, lens.data_ptr(), batch, 4, *rest, stream)
+    return call, [out]
+
+
+@pytest.mark.parametrize("kind,head_dim,new", [("bf16", 128, 0), ("bf16", 64, 0), ("bf16", 128, 3), ("bf16", 64, 3), ("q8", 128, 1),
+                                               ("q8", 128, 3)])
+def test_older_attention(pkv, kind, head_dim, new):
+    made = [older_attention(pkv, kind, batch, head_dim, new) for batch in (1024, 1)]
+    torch.cuda.synchronize()
+    in_turn_and_at_once([c for c, _ in made], [o for _, o in made])
