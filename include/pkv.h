@@ -355,6 +355,8 @@ PKV_API pkv_status pkv_multiquery_attention(const void* q, const void* k_cache, 
  * 127. The scale is stored as a float32, computed as float32(max|x|) / 127 in
  * float32; each code is rint(x / scale) in float64 (half to even) against that
  * stored scale, clipped to [-127, 127]. The cached row stands for code * scale.
+ * A row that holds a NaN or an infinity has scale NaN (its codes may be anything):
+ * none of its values is a number.
  * Pools (desc->dtype = PKV_INT8, head_dim 64 or 128 for the append, 128 for
  * the attention, block_size 16), caller-allocated, device:
  *   k_codes   int8  [num_blocks][num_kv_heads][16][head_dim]   (token rows)
@@ -581,8 +583,9 @@ PKV_API pkv_status pkv_verify_drafts(const void* target_probs, int64_t target_st
  * codes, then 16 K scales and 16 V scales in float32. A row (head_dim coordinates of
  * one token of one KV head) is quantized symmetrically: scale = max|x| times
  * float32(1/7), rounded to float32 (0 for a zero row), code = clip(rint(x / scale), -7, 7), the
- * exact quotient rounded half to even; it stands for the values code * scale. A code
- * is the nibble code + 8 (0 .. 15; code -8 is valid where a record comes from
+ * exact quotient rounded half to even; it stands for the values code * scale. A row that
+ * holds a NaN or an infinity has scale NaN (its codes may be anything): none of its values
+ * is a number. A code is the nibble code + 8 (0 .. 15; code -8 is valid where a record comes from
  * elsewhere):
  *     K, token t: word w of its head_dim / 8 words (32 bits, at byte t head_dim / 2 + 4 w)
  *         holds dimension 8 w + 2 (p % 4) + p / 4 in nibble p (bits 4 p .. 4 p + 3);

@@ -34,11 +34,13 @@ def quantize_rows(x: np.ndarray, bits: int = 8):
         raise ValueError("bits must be in [2, 8]")
     limit = 2 ** (bits - 1) - 1
     x = np.asarray(x, dtype=np.float64)
+    bad = ~np.isfinite(x).all(axis=-1)                      # no values: scale NaN
+    x = np.where(bad[..., None], 0.0, x)
     amax = np.max(np.abs(x), axis=-1).astype(np.float32)
     scale = (amax / np.float32(limit)).astype(np.float32)
     scale = np.where(scale == 0, np.float32(1.0), scale).astype(np.float32)
     codes = np.clip(np.rint(x / scale.astype(np.float64)[..., None]), -limit, limit).astype(np.int8)
-    return codes, scale
+    return codes, np.where(bad, np.float32(np.nan), scale)
 
 
 def dequantize_rows(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:

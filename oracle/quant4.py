@@ -5,7 +5,8 @@ Sources: Notebook 10, section 8 (fewer bits per coordinate) and its project demo
 ``fake_quantize_rows`` (symmetric per row, ``limit = 2**(bits-1) - 1``, here 7).
 
 Reading: the cache keeps a float32 scale, ``max|x|`` times ``float32(1/7)`` rounded to
-float32 (0 for a zero row, whose codes are 0); the code is ``rint`` of the exact quotient
+float32 (0 for a zero row, whose codes are 0; NaN for a row that holds a NaN or an
+infinity); the code is ``rint`` of the exact quotient
 ``x / scale``, clipped to +-7, so it is a function of the stored scale. A record (16 tokens
 of one block and KV head) is laid out as include/pkv.h states it; this file packs and
 unpacks it nibble by nibble from that statement.
@@ -31,12 +32,14 @@ def record_bytes(d: int) -> int:
 def quantize_rows4(x):
     """Rows along the last axis -> (int8 codes -7..7, float32 scales)."""
     x = np.asarray(x, dtype=np.float64)
+    bad = ~np.isfinite(x).all(axis=-1)
+    x = np.where(bad[..., None], 0.0, x)
     scale = (np.max(np.abs(x), axis=-1).astype(np.float32) * STEP).astype(np.float32)
     wide = scale.astype(np.float64)[..., None]
     # float64 holds x and the scale exactly; their quotient lies on a border c + 1/2 or at least 2^-25 of
     # itself away from it (24-bit significands), farther than its rounding
     quotient = np.divide(x, wide, out=np.zeros_like(x), where=wide > 0)
-    return np.clip(np.rint(quotient), -LIMIT, LIMIT).astype(np.int8), scale
+    return np.clip(np.rint(quotient), -LIMIT, LIMIT).astype(np.int8), np.where(bad, np.float32(np.nan), scale)
 
 
 def code_exactly(x: float, scale: float) -> int:

@@ -73,15 +73,15 @@ __global__ void __launch_bounds__(64) append_q8_kernel(const __nv_bfloat16* __re
         }
         const __nv_bfloat16* src = (is_v ? v : k) + r * D + lane * kPer;
         float x[kPer];
-        float amax = 0.f;
+        uint32_t top = 0;  // the largest magnitude's bits, which order as the numbers do, infinity and NaN above them all
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             x[e] = __bfloat162float(src[e]);
-            amax = fmaxf(amax, fabsf(x[e]));
+            top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const float scale = amax > 0.f ? __fdiv_rn(amax, 127.0f) : 1.0f;
+        top = __reduce_max_sync(0xffffffffu, top);
+        float scale = top > 0 ? __fdiv_rn(__uint_as_float(top), 127.0f) : 1.0f;
+        if (top >= 0x7f800000u) scale = __uint_as_float(0x7fffffffu);  // NaN: none of the row's values is a number
         int8_t c[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) c[e] = static_cast<int8_t>(code_of(x[e], scale));

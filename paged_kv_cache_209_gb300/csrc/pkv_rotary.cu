@@ -271,21 +271,21 @@ __device__ __forceinline__ void turn_any(Eight<T>& a, Eight<T>& b, const Place& 
 template <int kCache>
 struct Codes {
     float scale, inverse, lift;
-    int half;
+    uint32_t half;
     __device__ __forceinline__ explicit Codes(float s) {
         lift = s < 1e-20f ? 1.2089258e24f : 1.f;  // 2^80
         scale = s * lift;
         inverse = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
-        half = __float_as_int(scale * 0.5f);
+        half = __float_as_uint(scale * 0.5f);
     }
     __device__ __forceinline__ uint32_t operator()(float x) const {
         constexpr float kShift = 12582912.f + (kCache == PKV_INT4 ? 8.f : 0.f);  // 1.5 2^23: an integer sits in its low bits
         x *= lift;
         const float shifted = fmaf(x, inverse, kShift);
         const float rest = fmaf(-(shifted - kShift), scale, x);
-        int c = __float_as_int(shifted);
-        if ((__float_as_int(rest) & 0x7fffffff) + (c & 1) > half) c += __float_as_int(rest) >> 31 | 1;
-        return static_cast<uint32_t>(c) & (kCache == PKV_INT4 ? 15u : 255u);
+        uint32_t c = __float_as_uint(shifted);
+        if ((__float_as_uint(rest) & 0x7fffffffu) + (c & 1u) > half) c += __float_as_int(rest) >> 31 | 1;
+        return c & (kCache == PKV_INT4 ? 15u : 255u);
     }
 };
 __device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {  // of a 4-bit record
@@ -295,10 +295,18 @@ __device__ __forceinline__ uint32_t k_word(const uint32_t (&c)[8]) {  // of a 4-
     return w;
 }
 
-// A row's scale, of its largest magnitude. (A zero row's is 0 in a 4-bit cache, 1 in an int8 one.)
-template <int kCache>
-__device__ __forceinline__ float scale_of(float top) {
-    return kCache == PKV_INT4 ? top * kQ4Step : top > 0.f ? __fdiv_rn(top, 127.f) : 1.f;
+// The scale of the row that D / 16 lanes hold (all lanes of the warp). (A zero row's is 0 in a 4-bit cache, 1 in an int8
+// one, NaN that of a row with a NaN or an infinity, whose values are then no numbers whatever their codes. The codes of
+// such a row cleared as well: 4096 tokens of 24 heads 26.3 us, so 25.7.)
+template <int D, int kCache>
+__device__ __forceinline__ float row_scale(const Eight<__nv_bfloat16>& x, const Eight<__nv_bfloat16>& y) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmax3_nan(top, fabsf(x.get(e)), fabsf(y.get(e)));
+#pragma unroll
+    for (int o = 1; o < D / 16; o <<= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaf(top, 0.f, top);  // NaN for an infinity
+    return kCache == PKV_INT4 ? top * kQ4Step : top == 0.f ? 1.f : __fdiv_rn(top, 127.f);
 }
 // Whether an append's V goes by windows of 16 tokens.
 constexpr bool by_windows(int cache, int batch) { return (cache == PKV_INT4 || cache == PKV_INT8) && batch > 1; }
@@ -357,12 +365,7 @@ __device__ __forceinline__ void append_v_window(const RotaryAppendArgs& a, uint3
     };
     // a row's codes, byte by byte to put(byte, code); its scale
     auto quantize = [&](const Eight<__nv_bfloat16>(&x)[2], int t, auto put) {
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x[0].get(e)), fabsf(x[1].get(e)));
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float scale = scale_of<kCache>(top);
+        const float scale = row_scale<D, kCache>(x[0], x[1]);
         const Codes<kCache> code(scale);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -487,61 +490,56 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(co
             }
             continue;
         }
-        if (kCache == PKV_F32 || kCache == PKV_BF16) {
+        if constexpr (kCache == PKV_F32 || kCache == PKV_BF16) {
             if (live) {
                 T* out = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + (((slot >> 4) * a.kv_heads + head) * 16 + (slot & 15)) * D;
                 x.store(out + 8 * at.va);
                 y.store(out + 8 * at.vb);
             }
-            continue;
-        }
-        // ---- quantized: the row's largest over its lanes (all lanes of the warp are here)
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmax3(top, fabsf(x.get(e)), fabsf(y.get(e)));
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!live) continue;
-        const float scale = scale_of<kCache>(top);
-        const Codes<kCache> code(scale);
-        uint32_t cx[8], cy[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cx[e] = code(x.get(e));
-            cy[e] = code(y.get(e));
-        }
-        const int64_t chunk = (slot >> 4) * a.kv_heads + head;
-        const int t = static_cast<int>(slot & 15);
-        if (kCache == PKV_INT4) {
-            uint8_t* rec = static_cast<uint8_t*>(a.k_cache) + chunk * q4_record_bytes(D);
-            if (is_v) {
-                uint8_t* v = rec + q4_v_offset(D);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[q4_v_byte(at.va, j, t)] = static_cast<uint8_t>(cx[2 * j] | cx[2 * j + 1] << 4);
-                    v[q4_v_byte(at.vb, j, t)] = static_cast<uint8_t>(cy[2 * j] | cy[2 * j + 1] << 4);
-                }
-            } else {
-                uint32_t* k = reinterpret_cast<uint32_t*>(rec + t * (D / 2));
-                k[at.va] = k_word(cx);
-                k[at.vb] = k_word(cy);
-            }
-            if (lane == 0) reinterpret_cast<float*>(rec + q4_scales_offset(D))[(is_v ? 16 : 0) + t] = scale;
         } else {
-            if (is_v) {
-                int8_t* v = static_cast<int8_t*>(a.v_cache) + chunk * D * 16 + t;
+            // ---- quantized (all lanes of the warp are here)
+            const float scale = row_scale<D, kCache>(x, y);
+            if (!live) continue;
+            const Codes<kCache> code(scale);
+            uint32_t cx[8], cy[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[(8 * at.va + e) * 16] = static_cast<int8_t>(cx[e]);
-                    v[(8 * at.vb + e) * 16] = static_cast<int8_t>(cy[e]);
-                }
-            } else {
-                int8_t* k = static_cast<int8_t*>(a.k_cache) + (chunk * 16 + t) * D;
-                auto word = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
-                *reinterpret_cast<uint2*>(k + 8 * at.va) = make_uint2(word(cx), word(cx + 4));
-                *reinterpret_cast<uint2*>(k + 8 * at.vb) = make_uint2(word(cy), word(cy + 4));
+            for (int e = 0; e < 8; ++e) {
+                cx[e] = code(x.get(e));
+                cy[e] = code(y.get(e));
             }
-            if (lane == 0) a.scales[(chunk * 2 + (is_v ? 1 : 0)) * 16 + t] = scale;
+            const int64_t chunk = (slot >> 4) * a.kv_heads + head;
+            const int t = static_cast<int>(slot & 15);
+            if (kCache == PKV_INT4) {
+                uint8_t* rec = static_cast<uint8_t*>(a.k_cache) + chunk * q4_record_bytes(D);
+                if (is_v) {
+                    uint8_t* v = rec + q4_v_offset(D);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[q4_v_byte(at.va, j, t)] = static_cast<uint8_t>(cx[2 * j] | cx[2 * j + 1] << 4);
+                        v[q4_v_byte(at.vb, j, t)] = static_cast<uint8_t>(cy[2 * j] | cy[2 * j + 1] << 4);
+                    }
+                } else {
+                    uint32_t* k = reinterpret_cast<uint32_t*>(rec + t * (D / 2));
+                    k[at.va] = k_word(cx);
+                    k[at.vb] = k_word(cy);
+                }
+                if (lane == 0) reinterpret_cast<float*>(rec + q4_scales_offset(D))[(is_v ? 16 : 0) + t] = scale;
+            } else {
+                if (is_v) {
+                    int8_t* v = static_cast<int8_t*>(a.v_cache) + chunk * D * 16 + t;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[(8 * at.va + e) * 16] = static_cast<int8_t>(cx[e]);
+                        v[(8 * at.vb + e) * 16] = static_cast<int8_t>(cy[e]);
+                    }
+                } else {
+                    int8_t* k = static_cast<int8_t*>(a.k_cache) + (chunk * 16 + t) * D;
+                    auto word = [](const uint32_t* c) { return c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24; };
+                    *reinterpret_cast<uint2*>(k + 8 * at.va) = make_uint2(word(cx), word(cx + 4));
+                    *reinterpret_cast<uint2*>(k + 8 * at.vb) = make_uint2(word(cy), word(cy + 4));
+                }
+                if (lane == 0) a.scales[(chunk * 2 + (is_v ? 1 : 0)) * 16 + t] = scale;
+            }
         }
     }
 }
