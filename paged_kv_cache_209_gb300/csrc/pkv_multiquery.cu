@@ -139,7 +139,7 @@ __device__ void mq_merge(const Piece& pc, const MqArgs& a, long long U, int warp
     const int t = rr / G;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                           (static_cast<long long>(q0 + t) * a.q_heads + pc.head * G + (rr - t * G)) * D;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // (a NaN, of a token that the row sees, stays)
 #pragma unroll
     for (int k = 0; k < D / 4; k += 2)
         *reinterpret_cast<uint32_t*>(orow + d0 + k) = pack_bf16x2(O[k] * inv, O[k + 1] * inv);
@@ -687,11 +687,14 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                     // maximum while every V scale is at most kVScaleF16Safe. A block
                     // with a larger scale (rows with max |v| above ~32 000) runs its
                     // product on P' 2^-k and O 2^-k, and O is scaled back by 2^k
-                    // afterwards: powers of two, exact in fp32. One vote covers both
-                    // rare cases (a new running maximum, a large V scale): a second
-                    // vote and branch per block cost 1.6 % of the call.
+                    // afterwards: powers of two, exact in fp32. A V scale that is no
+                    // number, or infinite, goes into the sum of the rows that see its
+                    // token, and out of the product, where it would meet the others'
+                    // zeros too. One vote covers the three rare cases (a new running
+                    // maximum, a large V scale, one that is no number): a second vote
+                    // and branch per block cost 1.6 % of the call.
                     float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
-                    if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || fmaxf(vA, vB) > kVScaleF16Safe)) {
+                    if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || !(fmax_nan(vA, vB) <= kVScaleF16Safe))) {
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) {
                             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
@@ -707,11 +710,19 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                         l1 *= al1;
                         m0 = mn0;
                         m1 = mn1;
+                        auto spoil = [&](float& v, int p) {
+                            if (fabsf(v) <= 3.402823466e38f) return;
+                            v = 0.f;
+                            if (p <= lim0) l0 = __int_as_float(0x7fffffff);
+                            if (p <= lim1) l1 = __int_as_float(0x7fffffff);
+                        };
+                        spoil(vA, pA);
+                        spoil(vB, pB);
                         // and the block's V-scale shift, folded into the same pass over O
                         float vm = fmaxf(vA, vB);
 #pragma unroll
                         for (int off = 1; off < 32; off <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, off));
-                        if (vm > kVScaleF16Safe && vm <= 3.0e38f) {
+                        if (vm > kVScaleF16Safe) {
                             const int k2 = pow2_shift_to_fit(vm);
                             const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
                             o_back = __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
                     const int t = rr / G;
                     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) +
                                           (static_cast<long long>(q0 + t) * a.q_heads + pc.head * G + (rr - t * G)) * D;
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
                     for (int e = 0; e < D / 4; e += 2)
                         *reinterpret_cast<uint32_t*>(orow + d0 + e) = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
@@ -838,7 +849,7 @@ __global__ void __launch_bounds__(Mq<D, NST, Q8>::kThreads, 2)
         }
         if (!active) continue;
         if (pc.complete) {
-            const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+            const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int rr = rg * 8 + (c ? c1 : c0);

@@ -148,3 +148,37 @@ def test_attention_over_the_4_bit_cache(pkv, new, d, side, bad, where):
     sees[max(0, where - (n - new)):, heads // 2:] = True
     assert got[sees].isnan().all()
     check(got[~sees], want[~sees], bound[~sees])
+
+
+@pytest.mark.parametrize("call", ["decode_q8", "multiquery_q8"])
+@pytest.mark.parametrize("new,n", [(1, 300), (4, 300), (8, 303), (40, 300), (4, 40000)])
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("back", [1, 2, 50, 297])
+def test_attention_over_int8_pools(pkv, call, new, n, side, bad, back):
+    """The same over int8 pools, 40000 tokens on the kernel that splits the cache: a spoilt token `back` from the end."""
+    if call == "decode_q8" and new > 8:
+        pytest.skip("at most 32 query rows")
+    kv, heads, d, where = 2, 8, 128, n - back
+    g = torch.Generator(device="cuda").manual_seed(6)
+    k, v = (torch.randn((n, kv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((new, heads, d), device="cuda", generator=g).to(torch.bfloat16)
+    slots = torch.arange(n, device="cuda")
+    tables = torch.arange(n // B + 1, dtype=torch.int32, device="cuda")[None].contiguous()
+    lens, start = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, new]))
+
+    def attend():
+        pools = [torch.zeros((n // B + 1, kv, B, d), dtype=torch.int8, device="cuda"),
+                 torch.zeros((n // B + 1, kv, d, B), dtype=torch.int8, device="cuda"), torch.zeros((n // B + 1, kv, 2, B), device="cuda")]
+        pkv.pkv_append_q8(k, v, slots, *pools)
+        if call == "decode_q8":
+            return pkv.pkv_decode_attention_q8(q, *pools, tables, lens, 0.1, query_start=start, max_query_len=new)
+        return pkv.pkv_multiquery_attention_q8(q, *pools, tables, lens, start, 0.1, new)
+    want = attend()
+    (k if side == "k" else v)[where, 1, 17] = bad
+    got = attend()
+    sees = torch.zeros((new, heads), dtype=torch.bool, device="cuda")
+    sees[max(0, where - (n - new)):, heads // 2:] = True
+    assert got[sees].isnan().all()
+    # each is off by half a bf16 step and by its f16 weights, 2^-11 of an average of |v| (below 1 here): twice both
+    assert ((got[~sees].double() - want[~sees].double()).abs() <= 2 * (want[~sees].double().abs() * 2.0 ** -8 + 4 * 2.0 ** -11)).all()
