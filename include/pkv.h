@@ -412,8 +412,8 @@ PKV_API size_t pkv_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, 
  * the codes and q (a row that reaches 2^15 scaled down by a power of two) are exact
  * there but for elements of q below 2^-14, the softmax weights times the V scale are
  * rounded to f16 (a product below 2^-25 is lost; pkv_multiquery_attention_q8 takes
- * scales of any size). A token with a scale that is NaN or infinite spoils the rows
- * that see it and no others. head_dim 128, at most
+ * scales of any size). A token with a NaN scale spoils the rows that see it and
+ * no others. head_dim 128, at most
  * 32 query rows per (sequence, KV head). Errors, checked mode and the device
  * status bits as in pkv_multiquery_attention; query_start NULL with
  * max_query_len != 1 is PKV_ERR_SHAPE.

@@ -575,8 +575,12 @@ __device__ __forceinline__ void scale_role(const ChunkArgs& a, uint8_t* smem, in
             }
             if (slow) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g)  // (-inf for a scale of zero)
+                for (int g = 0; g < 4; ++g) {
+                    // (-inf for a scale of zero)
                     if (bare_v[g] && present[g]) tab[4 + 128 + 32 * g + lane] = log2f(fabsf(vs[g])) - static_cast<float>(ev);
+                    // (an infinite K scale becomes a NaN: it may take a score to -inf, where it would go unseen)
+                    if (bare_k[g] && present[g]) tab[4 + 32 * g + lane] = fmaf(ks[g], 0.f, ks[g]);
+                }
             }
             if (lane < 8) reinterpret_cast<int64_t*>(record + 1280)[lane] = row * C::kChunkVecs;
             if (lane == 0) {

@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
                         }
                         const float* scales = reinterpret_cast<const float*>(rec + q4_scales_offset(D));
                         const float ka = scales[gid], kc = scales[gid + 8];
-                        sv[2 * b] = scales[16 + gid];
-                        sv[2 * b + 1] = scales[24 + gid];
+                        // (an infinite K scale makes V's a NaN: it may take a score to -inf, where it would go unseen)
+                        sv[2 * b] = fmaf(ka, 0.f, scales[16 + gid]);
+                        sv[2 * b + 1] = fmaf(kc, 0.f, scales[24 + gid]);
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -584,13 +585,14 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
                             }
                         }
                     };
-                    // what a row does not see has no weight, whatever its scale
+                    // what a row does not see (the scores of -inf above) has no weight, whatever its scale
                     auto mask = [&]() {
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
                             for (int i = 0; i < 2 * kAt; ++i)
-                                p[r][i] &= (e[r][2 * i] > 0.f ? 0x0000ffffu : 0u) | (e[r][2 * i + 1] > 0.f ? 0xffff0000u : 0u);
+                                p[r][i] &= (__float_as_uint(sc[r][i >> 1][2 * (i & 1)]) != 0xff800000u ? 0x0000ffffu : 0u) |
+                                           (__float_as_uint(sc[r][i >> 1][2 * (i & 1) + 1]) != 0xff800000u ? 0xffff0000u : 0u);
                     };
                     weights();
                     if (!whole) mask();
