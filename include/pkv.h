@@ -730,7 +730,8 @@ PKV_API pkv_status pkv_rotary_table(const double* frequencies, int32_t rotary_di
  * PKV_BF16), pkv_append_q8 (PKV_INT8) and pkv_append_q4 (PKV_INT4) put them there. Each y
  * is computed in float64 (the products are exact), rounded to float32 and from there to
  * bf16, whatever the order of work, and a quantizing cache takes the row so rounded: its
- * codes are a function of the inputs. Float32 rows (PKV_F32): off by at most 2^-23 (|x_a c_i| +
+ * codes are a function of the inputs. (A pair with a NaN or an infinity turns into two
+ * values that are not finite.) Float32 rows (PKV_F32): off by at most 2^-23 (|x_a c_i| +
  * |x_b s_i|).
  *
  *   q, k, v       device, rows of num_q_heads (num_kv_heads) heads of head_dim elements,

@@ -57,14 +57,19 @@ __device__ __forceinline__ float turned(__nv_bfloat16, float x, float c, float y
     // each rounding is off by at most 2^-24 of its result (2^-150 below the normal range)
     const float off = fmaf(fabsf(p) + fabsf(r), 1.1920929e-7f, 2.8026e-45f);
     const uint32_t ends = pack_bf16x2(r - off, r + off);
-    if ((ends & 0xffffu) == ends >> 16) return bf16hi_to_f32(ends);
+    if ((ends & 0xffffu) == ends >> 16 && (ends & 0x7f80u) != 0x7f80u) return bf16hi_to_f32(ends);
     return turned_exactly(x, c, y, s);
 }
-// float32 rows: the product's error joins the sum (one rounding, and one of a small term).
+// float32 rows: the product's error joins the sum (one rounding, and one of a small term). Where the result is not
+// finite the product alone may have left the range, or been an infinity's: then float64 (turned_wide).
 __device__ __forceinline__ float turned(float, float x, float c, float y, float s) {
     const float p = y * s;
     return fmaf(x, c, -p) - fmaf(y, s, -p);
 }
+__device__ __noinline__ float turned_wide(float x, float c, float y, float s) {
+    return static_cast<float>(static_cast<double>(x) * c - static_cast<double>(y) * s);
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // Eight elements of a row as they are stored: words of two (bf16), or one each.
 template <typename T>
@@ -161,11 +166,12 @@ __device__ __forceinline__ uint32_t turned_pair(uint32_t x, uint32_t y, float c0
 // Turns the lane's vectors of a row of bf16s, two elements at a time. `size`: the largest of the
 // lane's |c| and |s|. With X the larger of a pair's magnitudes, |y s| <= X size and |r| <= 2
 // X size, so r = x c - y s is off by at most 2^-24 (|y s| + |r|) <= 3 2^-24 X size (and 2^-149
-// below the normal range).
+// below the normal range). Taken as X size first, the bound is infinite, and nothing decided, where a product may leave the
+// range though y does not.
 template <int kMode>
 __device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat16>& b, const float (&c)[8], const float (&s)[8], float size,
                                      const Place& at, int R) {
-    const float k = 2.0e-7f * size;  // (3.36 2^-24)
+    const uint64_t size2 = f32x2_pack(size, size), part = f32x2_pack(2.0e-7f, 2.0e-7f), least = f32x2_pack(2.8026e-45f, 2.8026e-45f);  // (3.36 2^-24)
     if (kMode == kHalves) {
         if (!at.turns) return;
         uint32_t open = 0;
@@ -174,7 +180,7 @@ __device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat1
         for (int i = 0; i < 4; ++i) {
             const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1), y0 = y.get(2 * i), y1 = y.get(2 * i + 1);
             const uint64_t xx = f32x2_pack(x0, x1), yy = f32x2_pack(y0, y1), cc = f32x2_pack(c[2 * i], c[2 * i + 1]), ss = f32x2_pack(s[2 * i], s[2 * i + 1]);
-            const uint64_t off = f32x2_pack(fmaf(fmaxf(fabsf(x0), fabsf(y0)), k, 2.8026e-45f), fmaf(fmaxf(fabsf(x1), fabsf(y1)), k, 2.8026e-45f));
+            const uint64_t off = f32x2_fma(f32x2_mul(f32x2_pack(fmaxf(fabsf(x0), fabsf(y0)), fmaxf(fabsf(x1), fabsf(y1))), size2), part, least);
             if (!decided(f32x2_fma(xx, cc, f32x2_mul(yy, f32x2_mul(ss, f32x2_pack(-1.f, -1.f)))), off, a.w[i])) open |= 1u << i;
             if (!decided(f32x2_fma(yy, cc, f32x2_mul(xx, ss)), off, b.w[i])) open |= 16u << i;
         }
@@ -199,11 +205,16 @@ __device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat1
             if (8 * (u ? at.vb : at.va) >= R) break;
             uint32_t open = 0;
             const Eight<__nv_bfloat16> x = v;
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const uint64_t top = f32x2_pack(fmaxf(fabsf(x.get(2 * i)), fabsf(x.get(2 * i + 1))), fmaxf(fabsf(x.get(2 * i + 2)), fabsf(x.get(2 * i + 3))));
+                f32x2_unpack(f32x2_fma(f32x2_mul(top, size2), part, least), o[i], o[i + 1]);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float x0 = x.get(2 * i), x1 = x.get(2 * i + 1), cc = c[4 * u + i], ss = s[4 * u + i];
-                const float o = fmaf(fmaxf(fabsf(x0), fabsf(x1)), k, 2.8026e-45f);
-                if (!decided(f32x2_fma(f32x2_pack(x0, x1), f32x2_pack(cc, cc), f32x2_mul(f32x2_pack(x1, x0), f32x2_pack(-ss, ss))), f32x2_pack(o, o), v.w[i]))
+                if (!decided(f32x2_fma(f32x2_pack(x0, x1), f32x2_pack(cc, cc), f32x2_mul(f32x2_pack(x1, x0), f32x2_pack(-ss, ss))), f32x2_pack(o[i], o[i]), v.w[i]))
                     open |= 1u << i;
             }
             if (open) {
@@ -218,15 +229,17 @@ __device__ __forceinline__ void turn(Eight<__nv_bfloat16>& a, Eight<__nv_bfloat1
         }
     }
 }
-template <int kMode>
-__device__ __forceinline__ void turn(Eight<float>& a, Eight<float>& b, const float (&c)[8], const float (&s)[8], float, const Place& at, int R) {
+// float32: by turned(), or with kWide by turned_wide().
+template <int kMode, bool kWide>
+__device__ __forceinline__ void turn_f32(Eight<float>& a, Eight<float>& b, const float (&c)[8], const float (&s)[8], const Place& at, int R) {
+    auto one = [](float x, float c, float y, float s) { return kWide ? turned_wide(x, c, y, s) : turned(x, x, c, y, s); };
     if (kMode == kHalves) {
         if (!at.turns) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float x = a.w[e], y = b.w[e];
-            a.w[e] = turned(x, x, c[e], y, s[e]);
-            b.w[e] = turned(x, y, c[e], x, -s[e]);
+            a.w[e] = one(x, c[e], y, s[e]);
+            b.w[e] = one(y, c[e], x, -s[e]);
         }
     } else if (kMode == kNeighbours) {
 #pragma unroll
@@ -236,11 +249,15 @@ __device__ __forceinline__ void turn(Eight<float>& a, Eight<float>& b, const flo
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float x = v.w[2 * e], y = v.w[2 * e + 1];
-                v.w[2 * e] = turned(x, x, c[4 * u + e], y, s[4 * u + e]);
-                v.w[2 * e + 1] = turned(x, y, c[4 * u + e], x, -s[4 * u + e]);
+                v.w[2 * e] = one(x, c[4 * u + e], y, s[4 * u + e]);
+                v.w[2 * e + 1] = one(y, c[4 * u + e], x, -s[4 * u + e]);
             }
         }
     }
+}
+template <int kMode>
+__device__ __forceinline__ void turn(Eight<float>& a, Eight<float>& b, const float (&c)[8], const float (&s)[8], float, const Place& at, int R) {
+    turn_f32<kMode, false>(a, b, c, s, at, R);
 }
 // Any even R: the partner of every dimension is read apart (`row`: the row's first element, `cs`: the table's row).
 template <typename T>
@@ -257,7 +274,9 @@ __device__ __forceinline__ void turn_any(Eight<T>& a, Eight<T>& b, const Place& 
             const bool second = interleaved ? (d & 1) != 0 : d >= half;
             const int other = interleaved ? d ^ 1 : second ? d - half : d + half;
             const float y = value(row[other]), w = cs[half + i];
-            v.set(e, turned(T{}, v.get(e), cs[i], y, second ? -w : w));
+            float r = turned(T{}, v.get(e), cs[i], y, second ? -w : w);
+            if (sizeof(T) == 4 && !finite(r)) r = turned_wide(v.get(e), cs[i], y, second ? -w : w);
+            v.set(e, r);
         }
     }
 }
@@ -479,6 +498,16 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_rotary_kernel(co
                     turn_any<T>(x, y, at, a.rotary_dim, from + b * kRows * D, cs, a.interleaved != 0);
                 else if (kMode != kWhole)
                     turn<kMode>(x, y, c, s, size, at, a.rotary_dim);
+                if constexpr (sizeof(T) == 4 && (kMode == kHalves || kMode == kNeighbours)) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmax3_nan(top, fabsf(x.get(e)), fabsf(y.get(e)));
+                    if (!finite(top)) {  // (the row as it was, read again)
+                        x.load(from + b * kRows * D + 8 * at.va);
+                        y.load(from + b * kRows * D + 8 * at.vb);
+                        turn_f32<kMode, true>(x, y, c, s, at, a.rotary_dim);
+                    }
+                }
             }
         }
         if (kMode == kAny) __syncwarp();  // q may turn in place, its dimensions read by two lanes
