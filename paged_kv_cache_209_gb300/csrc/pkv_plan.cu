@@ -19,11 +19,6 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 
-struct Sums {
-    int64_t rows;
-    int64_t need;
-};
-
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

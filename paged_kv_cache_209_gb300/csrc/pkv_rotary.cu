@@ -594,7 +594,9 @@ cudaError_t run_append(const RotaryAppendArgs& a, cudaStream_t s) {
 template <int D, int kCache, typename T>
 cudaError_t run_mode(const RotaryAppendArgs& a, cudaStream_t s) {
     const int R = a.rotary_dim;
-    if (R == 0) return run_append<D, kWhole, kCache, T>(a, s);
+    if constexpr (kCache == PKV_INT4) {  // pkv_append_q4
+        if (R == 0) return run_append<D, kWhole, kCache, T>(a, s);
+    }
     if (!a.interleaved && R % 16 == 0) return run_append<D, kHalves, kCache, T>(a, s);
     if (a.interleaved && R % 8 == 0) return run_append<D, kNeighbours, kCache, T>(a, s);
     return run_append<D, kAny, kCache, T>(a, s);
