@@ -1,17 +1,20 @@
 """Build libpkv.so in-tree: every .cu (and host-only .cpp) under csrc/,
 compiled for sm_103a; and _pkv_calls.so, the serving calls' binding to torch
-tensors (binding/pkv_calls.cpp, host code, against the installed torch).
+tensors (binding/pkv_calls.cpp, host code, against the installed torch). A user
+of the C ABI alone needs nvcc only: without torch the binding is left out, and
+pkv.py, which is for torch tensors, says so when one of its calls is made.
 
 Usage: ``python -m paged_kv_cache_209_gb300.build`` (or call ``build()``).
 Objects go to ``_build/`` beside this file; the shared library lands next to
 this file as ``libpkv.so``. Translation units compile in parallel; a unit is
-rebuilt only when it or a header is newer than its object.
+rebuilt only when it, a header or this file is newer than its object.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -65,7 +68,7 @@ def _binding_command() -> list[str]:
 
 def _binding_stale() -> bool:
     import torch
-    inputs = [BINDING, torch.version.__file__] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    inputs = [BINDING, torch.version.__file__, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     return not os.path.exists(CALLS) or os.path.getmtime(CALLS) < max(os.path.getmtime(p) for p in inputs)
 
 
@@ -78,7 +81,8 @@ def _build_binding(force: bool) -> None:
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
           defines: dict | None = None, out_dir: str | None = None) -> str:
-    """Compile and link ``libpkv.so``; returns its path. Raises on failure.
+    """Compile and link ``libpkv.so``, and the binding where torch is installed; returns the library's path. Raises on
+    failure.
 
     ``defines`` adds ``-D`` build-time knobs (e.g. ``{"PKV_TC_STAGES": 12}``);
     with ``out_dir`` the objects and the library go there instead of in-tree.
@@ -87,7 +91,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
     lib_path = LIB if out_dir is None else os.path.join(out_dir, "libpkv.so")
     os.makedirs(build_dir, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
-    hdr_time = _newest_header()
+    hdr_time = max(_newest_header(), os.path.getmtime(os.path.abspath(__file__)))  # (and the flags above)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
     extra += [f"-D{k}={v}" for k, v in (defines or {}).items()]
     jobs = []
@@ -101,7 +105,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False,
             jobs.append((src, obj))
     binding = None
     binder = cf.ThreadPoolExecutor(max_workers=1)
-    if out_dir is None:
+    if out_dir is None and importlib.util.find_spec("torch") is not None:
         binding = binder.submit(_build_binding, force)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
