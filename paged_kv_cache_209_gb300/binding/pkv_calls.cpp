@@ -149,6 +149,7 @@ struct Tables {
 Tables tables_of(const Call& c, PyObject* o) {
     const Tensor& t = c.whole("block_tables", o, at::kInt);
     if (t.dim() != 2) throw Refused("block_tables is [batch][max_blocks]");
+    if (t.size(0) > INT32_MAX || t.size(1) > INT32_MAX) throw Refused("batch and max_blocks are 32-bit numbers");
     return {static_cast<const int32_t*>(t.const_data_ptr()), static_cast<int32_t>(t.size(0)), static_cast<int32_t>(t.size(1))};
 }
 
@@ -159,7 +160,7 @@ PyObject* attention_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Call c{integer32("here", a[0])};
         const Q4 p = q4_of(c, a[2]);
         const Tensor& q = c.whole("q", a[1], at::kBFloat16);
-        if (q.dim() != 3 || q.size(2) != p.desc.head_dim) throw Refused("q is bf16 [rows][q_heads][head_dim]");
+        if (q.dim() != 3 || q.size(2) != p.desc.head_dim || q.size(1) > INT32_MAX) throw Refused("q is bf16 [rows][q_heads][head_dim]");
         const Tables t = tables_of(c, a[3]);
         const int64_t rows = q.size(0);
         const bool decode = a[5] == Py_None;
@@ -280,7 +281,7 @@ PyObject* append_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Tensor out;
         if (a[1] != Py_None) {
             const Tensor& q = tensor("q", a[1]);
-            if (q.dim() != 3) throw Refused("q is [tokens][q_heads][head_dim]");
+            if (q.dim() != 3 || q.size(1) > INT32_MAX) throw Refused("q is [tokens][q_heads][head_dim]");
             const Rows r = rows_of(c, "q", a[1], type, tokens, q.size(1), desc.head_dim);
             heads = static_cast<int32_t>(q.size(1));
             q_at = r.t.const_data_ptr();
