@@ -635,7 +635,8 @@ PKV_API size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_hea
 /*
  * pkv_decode_attention_q4 -- pkv_decode_attention over the values the 4-bit cache's
  * rows stand for: q and out are bf16 [batch][num_q_heads][head_dim], a sequence without
- * tokens gives a zero row (rejected by PKV_FLAG_CHECKED). At most 32 query heads per KV
+ * tokens gives a zero row (rejected by PKV_FLAG_CHECKED). out may be q itself, here and in
+ * pkv_multiquery_attention_q4, else it overlaps no input. At most 32 query heads per KV
  * head (else PKV_ERR_UNSUPPORTED). Precision and scales as
  * pkv_multiquery_attention_q4; errors as pkv_decode_attention.
  */
@@ -651,7 +652,8 @@ PKV_API pkv_status pkv_decode_attention_q4(const void* q, const void* cache, con
  * query_start[i+1] - query_start[i] tokens, up to 65536 of them. Arguments, limits,
  * errors, checked mode and the device status bits as pkv_multiquery_attention_q8.
  *
- * fp32 accumulation, one rounding to bf16. K scales may be of any size and spread, V
+ * fp32 accumulation, one rounding to bf16; the same bits for the same inputs. |scale| times
+ * a row's largest |q| lies below 2^116. K scales may be of any size and spread, V
  * scales of any size from 1e-28 on, zero or negative too, as long as those of one
  * sequence lie within 2^100 of each other (values farther apart may be lost).
  * Up to 32 query rows per (sequence, KV head): codes and q (scaled by a power of two per
