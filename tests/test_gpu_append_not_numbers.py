@@ -150,15 +150,15 @@ def test_attention_over_the_4_bit_cache(pkv, new, d, side, bad, where):
     check(got[~sees], want[~sees], bound[~sees])
 
 
-@pytest.mark.parametrize("call", ["decode_q8", "multiquery_q8"])
-@pytest.mark.parametrize("new,n", [(1, 300), (4, 300), (8, 303), (40, 300), (4, 40000)])
+SIZES = [(1, 300), (4, 300), (8, 303), (4, 40000)]
+
+
+@pytest.mark.parametrize("call,new,n", [("decode_q8", *s) for s in SIZES] + [("multiquery_q8", *s) for s in SIZES + [(40, 300)]])
 @pytest.mark.parametrize("side", ["k", "v"])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("back", [1, 2, 50, 297])
 def test_attention_over_int8_pools(pkv, call, new, n, side, bad, back):
     """The same over int8 pools, 40000 tokens on the kernel that splits the cache: a spoilt token `back` from the end."""
-    if call == "decode_q8" and new > 8:
-        pytest.skip("at most 32 query rows")
     kv, heads, d, where = 2, 8, 128, n - back
     g = torch.Generator(device="cuda").manual_seed(6)
     k, v = (torch.randn((n, kv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
