@@ -1,7 +1,7 @@
 // The calls of a serving step's small launches, from Python tensors to libpkv without
 // Python in between: a step of a few sequences runs for 3 to 10 us on the GPU, and
 // checking and marshalling its dozen tensors in Python took 8 to 25 (planning a step 29
-// us, here 8). Checks and outputs are those that pkv.py documents; a function returns
+// us, here 5.5 to 8). Checks and outputs are those that pkv.py documents; a function returns
 // (outputs, status), and pkv.py raises PkvError for a status that is not PKV_OK.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

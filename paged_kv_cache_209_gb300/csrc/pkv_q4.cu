@@ -32,9 +32,11 @@
 // Measured, 32 query heads on 8 of 128, in a captured graph: 32 sequences of 8192 tokens 56.4
 // us, 5.07 TB/s of records (the copy rate is 6.78); per token more 43.5 us for 8192, 6.57
 // TB/s: the rest is the way to the first records (5 us), the CTAs of an SM ending up to 8 us
-// apart, and joining the pieces (3 us). Two queries a sequence take the same; four 85.5 us, 3.3
-// TB/s: bound by its instructions (two row tiles: 300 a block, their pipes busy 37 % each in
-// converting and 34 % in products, which share the issue); eight 154. 64 ragged contexts of up
+// apart, and joining the pieces (3 us). 32 of 131072 692 us, 6.59 TB/s; one of them 36.6. Two queries
+// a sequence take the same; four 86.0 us, 3.3 TB/s, out of L2 as out of HBM: with two row tiles a
+// warp there are two warps a scheduler, and one issues every 4.9 cycles (2.0 of them waiting on
+// the instruction before, 0.7 on loads, 0.8 for its turn or an instruction), 300 times a block of
+// which it takes 108: 81 us. No unit is full (issue slots 41 %, tensor pipe and ALU 37 %). Eight 154. 64 ragged contexts of up
 // to 8191 tokens, 24 heads: 38.5 us, 3.6 TB/s. One of 1000 tokens: 9.1 us, all of it latency.
 #include <math.h>
 #include <mutex>
@@ -54,11 +56,11 @@ constexpr int kIssueLanes = 8;  // stages whose copies are issued together
 // Cost of a segment shorter than kShortBlocks beside its blocks, in blocks, where there are
 // blocks enough for every CTA (64 contexts of 1 to 8191 tokens: 38.5 us, 45.4 without; 40 of up to 6000
 // with four queries 34.8, 35.9 with 16 and 38 with 12; 256 of up to 16384 231.4, 234 with 28; many equal
-// short ones lose by it, 256 of 100 tokens 33.5 against 30.8, being cut more rarely).
+// short ones, which are not exempted, lose by it, 256 of 100 tokens 33.5 against 30.8, being cut more rarely).
 constexpr int kSegmentCost = 20, kShortBlocks = 256;
 // Where there are not, a CTA gets about this many blocks: of contexts of one length (one of 1000 tokens 9.1
 // us; 9.3 with 8, 11.6 with 2, 9.6 with 24; 14 of 700 10.7, 14.0 with 8; 9 of 700 with four queries 13.7
-// and 20; but 4 of 700 10.1 and 9.5), and of others (14 of up to 1100 19.0 us, 25.5 with 12) or where two
+// and 20; but 4 of 700 10.1 and 9.5, which no rule here tells from them), and of others (14 of up to 1100 19.0 us, 25.5 with 12) or where two
 // warps share a block (one of 1024 tokens with eight queries 15.7, 17.4 with 12).
 constexpr int kLeastAlike = 12, kLeastBlocks = 8;
 

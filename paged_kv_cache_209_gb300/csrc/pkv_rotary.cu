@@ -15,10 +15,13 @@
 //
 // The append is pure streaming by its bytes (q in and out, k and v in, the pools' share
 // out), and bound by its instructions, most of all by the exact rounding. Measured in a
-// captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a 4-bit cache 21.9 us, 88 MB
-// at 4.0 TB/s (27.9 while V's codes went byte by byte; 16 with the rounding of one float32, inexact); ragged prompts of 24 + 2 x 8 heads into
-// bf16 pools 27.6 us, 5.3 TB/s; a decode step of 32 tokens 2.5 us. A warp that goes from unit
-// to unit with the next one's rows on their way took 1.8 us more for the first, 2.7 for the second.
+// captured graph: 4096 tokens of 32 + 2 x 8 heads of 128 into a 4-bit cache 22.6 us, 88 MB
+// at 3.9 TB/s (27.9 while V's codes went byte by byte; 16 with the rounding of one float32, inexact), into int8 pools 24.6,
+// bf16 20.3 (101 MB, 5.0 TB/s), float32 31.1 (neighbouring pairs 34.1; 201 MB, 6.5 TB/s). Ragged prompts of 24 + 2 x 8 heads
+// into bf16 pools 27.8 us, 5.3 TB/s; a decode step of 32 tokens 2.4 us. K and V alone, 4096 tokens of 24 heads: 19.6 us into a 4-bit
+// cache without positions (64 MB, floor 9.4), 26.0 with them, 27.7 into int8 pools: 23 instructions an element for the
+// quantizing (issue slots and ALU 71 % busy). A warp that goes from unit to unit with the next one's rows on their way took
+// 1.8 us more for the first, 2.7 for the ragged prompts.
 #include <math.h>
 
 #include "pkv_device.cuh"
@@ -345,7 +348,7 @@ __device__ __forceinline__ int v_byte(int o, int e, int t) {
 
 // V of the 16 tokens from 16 `window` on, one head, quantized. A byte of a block's V codes is one token's, its
 // words are several's: stored token by token, K and V of 4096 tokens of 24 heads take 47.7 us into a 4-bit cache and
-// 115 into an int8 one, so 26.3 and 28.2. Where 16 tokens that follow one another fill a block, the warp whose window holds their first puts
+// 115 into an int8 one, so 26.0 and 27.7. Where 16 tokens that follow one another fill a block, the warp whose window holds their first puts
 // the block together in shared memory; tokens of no such block are stored byte by byte.
 template <int D, int kMode, int kCache>
 __device__ __forceinline__ void append_v_window(const RotaryAppendArgs& a, uint32_t window, int head, uint8_t* stage) {
