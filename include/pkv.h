@@ -316,8 +316,8 @@ PKV_API size_t pkv_multiquery_workspace_size(int32_t batch, int32_t num_q_heads,
  * with K_j / V_j gathered through block_tables[i] as in pkv_decode_attention.
  * One query per sequence is pkv_decode_attention. fp32 accumulation, one
  * rounding to bf16. (A V row of the new tokens that holds a NaN or an infinity
- * spoils all rows of its sequence, those before it too: a weight of zero times it
- * is no number. Slots past the context may hold anything.)
+ * may spoil rows of its sequence before it too: a weight of zero times it is no
+ * number. Slots past the context may hold anything.)
  *
  *   q, out        device, bf16 [query_start[batch]][num_q_heads][head_dim].
  *   query_start   device, int32 [batch + 1], non-decreasing row offsets.
