@@ -653,15 +653,17 @@ PKV_API pkv_status pkv_decode_attention_q4(const void* q, const void* cache, con
  * errors, checked mode and the device status bits as pkv_multiquery_attention_q8.
  *
  * fp32 accumulation, one rounding to bf16; the same bits for the same inputs. |scale| times
- * a row's largest |q| lies below 2^116. K scales may be of any size and spread, V
+ * a row's largest |q| lies below 2^116 (up to 32 query rows per KV head: 2^120). K scales may be of any size and spread, V
  * scales of any size from 1e-28 on, zero or negative too, as long as those of one
  * sequence lie within 2^100 of each other (values farther apart may be lost).
  * Up to 32 query rows per (sequence, KV head): codes and q (scaled by a power of two per
- * row) enter exactly, a score is summed to 2^-15 |scale| (K scale) sum|q|; a softmax weight
+ * row) enter exactly, a score is summed to |scale| (K scale) times 2^-15 sum|q| and 2^-14 of
+ * the largest |q| of each 16 dimensions; a softmax weight
  * times its V scale is rounded to f16 once (11 bits down to 2^-22 of the row's largest
  * such product, fewer to 2^-32), and the sums over tokens, which run over code + 8, are
  * off by at most (n / 4 + 368) 2^-23 of the sum of these products for n tokens (2^-13 at
- * 1400, 2^-8 at 131072; measured at 131072: 2^-16). More rows run in tiles, as those of
+ * 1400, 2^-8 at 131072; measured at 131072: 2^-16) and, for each token, 2^-15 of the largest
+ * of its block's products. More rows run in tiles, as those of
  * pkv_multiquery_attention_q8: a K value is rounded to f16 once, a V value twice, a
  * softmax weight once. A token that is not a number, or infinite, spoils the rows that
  * see it and no others.

@@ -10,18 +10,27 @@
 // of stages of two records (32 tokens); the query rows of a segment come the same way,
 // ahead of its first records. Four consumer warps take stages in turn. Per stage, with
 // the query rows of a (sequence, KV head) in tiles of 8:
-//     S^T[16 tokens][8 rows] = K[16][D] Q^T[D][8]     (mma m16n8k16, f16 -> fp32)
+//     S^T[16 tokens][8 rows] = K[16][D] Q^T[D][8]     (mma m16n8k16, bf16 -> fp32)
 //     x = log2(e) scale S k_p,  P' = 2^(x - m) v_p,  l += 2^(x - m)
-//     O^T[D][8] += V^T[D][16] P'^T[16][8]
+//     O^T[D][8] += V^T[D][16] P'^T[16][8]             (f16 -> fp32)
 // k_p and v_p are the tokens' scales; m is a base, not a maximum, moved only where a P'
 // would leave f16 (below).
 //
-// Codes become f16 by one mask: a nibble n (code + 8) alone in the low bits of an f16 is
-// the subnormal n 2^-24, four bits higher 16 n 2^-24, which the tensor cores take
-// exactly. For K the 8 stays: S = 2^24 S' - 8 sum(q), q's halves over 16 where the codes
-// are 16-fold. For V it goes, by one exact subtraction per pair, because O runs over the
-// whole context, where the sum of the eights would take the low bits of the rest. q rows
-// are scaled by a power of two to a largest magnitude of 2^14 .. 2^15; sums are fp32.
+// Codes become operands by one mask: a nibble n (code + 8) alone in the low bits of a bf16
+// is n 2^-133, of an f16 n 2^-24, four bits higher 16 times that (in bf16 its top bit is the
+// exponent's lowest, whose two ranges share their step). For K the 8 stays: S = 2^133 S' - 8
+// sum(q), q's halves over 16 where the codes are 16-fold. For V it goes, by one subtraction
+// per 256 tokens, because O runs over the whole context, where the sum of the eights would
+// take the low bits of the rest. q rows are scaled by a power of two to a largest magnitude of
+// 2^126 .. 2^127; sums are fp32.
+//
+// The products of such small operands are exact, but their sum is not: the 16 of an
+// instruction are lined up by exponents that take an operand below the normal range for one
+// at its end, and what lies 23 bits or more below the largest is cut. So a product with a code
+// loses what is below 2^-18 of the largest q of its 16 dimensions (bf16, whose low bits are 7
+// below the range's end; with f16's 10, which q would fit as well, 2^-15), and below 2^-15 of the
+// largest P' of its 16 tokens (P' needs f16's bits). Four bits higher it is 16 times less; the
+// eights are summed in both places for that.
 //
 // Three CTAs an SM of four consumer warps (two with two row tiles a warp, for the
 // registers), each with a ring of eight stages, 35 KB: what one CTA of twelve consumers
@@ -123,21 +132,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float f16x2_sum(uint32_t h) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return f.x + f.y;
-}
 // Adds to a counter, ordered after what the warp has written and before what it reads next.
 __device__ __forceinline__ int add_acq_rel(int* p, int v) {
     int old;
     asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
     return old;
 }
-// D = A B + C for f16 A (16 x 16) and B (16 x 8), C and D apart.
-__device__ __forceinline__ void mma_f16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+// D = A B + C for bf16 A (16 x 16) and B (16 x 8), C and D apart.
+__device__ __forceinline__ void mma_bf16_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
                                              float c0, float c1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
         const int rows = pc->rows;
         const bool active = rg * C::kRows < rows;
         uint32_t qf[R][D / 16][2];
-        float cf[R][2], kb[R][2];  // per column: 2^24, the power of two and the scale; what the eights add, 2^-24 of it
+        float cf[R][2], kb[R][2];  // per column: 2^133, the power of two and the scale; what the eights add, 2^-133 of it
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const int rr = rg * C::kRows + r * 8 + gid;
@@ -418,17 +423,22 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
             }
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = max(static_cast<int>(max(top >> 16, top & 0xffffu) >> 7) - 127 - 14, -126);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            float sum = 0.f;  // of the operands as rounded
+            // the largest |q| lies in 2^e .. 2^(e + 1); its row is taken 2^(126 - e) times, by two factors
+            const int e = max(static_cast<int>(max(top >> 16, top & 0xffffu) >> 7) - 127, -126);
+            const int half = (126 - e) >> 1;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + min(e, 127)) << 23), by0 = __uint_as_float(static_cast<uint32_t>(127 + half) << 23),
+                        by1 = __uint_as_float(static_cast<uint32_t>(127 + 126 - e - half) << 23);
+            float sum = 0.f;  // 2^-10 of q's
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t lo = h ? w[c].z : w[c].x, hi = h ? w[c].w : w[c].y;
-                    qf[r][2 * c + h][0] = pack_f16x2(bf16lo_to_f32(lo) * down, bf16hi_to_f32(lo) * down);
-                    qf[r][2 * c + h][1] = pack_f16x2(bf16lo_to_f32(hi) * down * 0.0625f, bf16hi_to_f32(hi) * down * 0.0625f);
-                    sum += f16x2_sum(qf[r][2 * c + h][0]) + 16.f * f16x2_sum(qf[r][2 * c + h][1]);
+                    const float q0 = bf16lo_to_f32(lo) * by0 * by1, q1 = bf16hi_to_f32(lo) * by0 * by1, q2 = bf16lo_to_f32(hi) * by0 * by1,
+                                q3 = bf16hi_to_f32(hi) * by0 * by1;
+                    qf[r][2 * c + h][0] = pack_bf16x2(q0, q1);
+                    qf[r][2 * c + h][1] = pack_bf16x2(q2 * 0.0625f, q3 * 0.0625f);
+                    sum = fmaf(q0, 9.765625e-4f, fmaf(q1, 9.765625e-4f, fmaf(q2, 9.765625e-4f, fmaf(q3, 9.765625e-4f, sum))));
                 }
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -436,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
             // S^T columns 2 tig, 2 tig + 1 are the rows of lanes 8 tig and 8 tig + 4
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                cf[r][c] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * c) * scale_log2 * 16777216.f;
-                kb[r][c] = -4.76837158e-7f * __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * c);  // 2^-21
+                cf[r][c] = __shfl_sync(0xffffffffu, up, 8 * tig + 4 * c) * (scale_log2 * 128.f);  // 2^(133 - 126)
+                kb[r][c] = -7.52316385e-37f * __shfl_sync(0xffffffffu, sum, 8 * tig + 4 * c);     // 8 2^(10 - 133)
             }
         }
         // the last token each of the lane's columns sees
@@ -468,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
                 for (int i = 0; i < D / 16; ++i) {
                     o[r][i][0] -= z[r][0];
                     o[r][i][1] -= z[r][1];
-                    o[r][i][2] = fmaf(-16.f, z[r][0], o[r][i][2]);
-                    o[r][i][3] = fmaf(-16.f, z[r][1], o[r][i][3]);
+                    o[r][i][2] -= z[r][2];
+                    o[r][i][3] -= z[r][3];
                 }
                 z[r][0] = z[r][1] = z[r][2] = z[r][3] = 0.f;
             }
@@ -522,10 +532,10 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
 #pragma unroll
                                 for (int r = 0; r < R; ++r) {
                                     if (c + h == 0)
-                                        mma_f16_from(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][0][0], qf[r][0][1],
+                                        mma_bf16_from(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][0][0], qf[r][0][1],
                                                      kb[r][0], kb[r][1]);
                                     else
-                                        mma_f16_16816(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
+                                        mma_bf16_16816(sc[r][b], u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, qf[r][2 * c + h][0],
                                                       qf[r][2 * c + h][1]);
                                 }
                             }
@@ -640,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, M4<D, R>::kCtas) mq4_kernel(const Q4
 #pragma unroll
                     for (int b = 0; b < kAt; ++b) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r) mma_f16_16816(z[r], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[r][2 * b], p[r][2 * b + 1]);
+                        for (int r = 0; r < R; ++r) mma_f16_16816(z[r], 0x00080008u, 0x00800080u, 0x00080008u, 0x00800080u, p[r][2 * b], p[r][2 * b + 1]);
 #pragma unroll
                         for (int h = 0; h < D / 64; ++h) {
                             const uint32_t w[4] = {vw[b][h].x, vw[b][h].y, vw[b][h].z, vw[b][h].w};
