@@ -1022,7 +1022,7 @@ size_t pkv_multiquery_q4_workspace_size(int32_t batch, int32_t num_q_heads, int3
 // 4-bit multi-query calls: up to kMq4Rows query rows per (sequence, KV head) run on the
 // kernel that splits the cache (pkv_q4.cu), more in tiles (pkv_chunk_q8.cu), whose 128 rows
 // cost the same however many are used. Split / tiles in us, 32 rows of 128 but as noted:
-// 32 sequences of 8192 154 / 209 (16 rows 86 / 211; 16 rows of 64 59 / 184), one of 32768 40 /
+// 32 sequences of 8192 154 / 209 (16 rows 87 / 211; 16 rows of 64 59 / 184), one of 32768 40 /
 // 46, of 1024 15.7 / 18.6, 64 of 300 43 / 48, 4 of 300 16.5 / 14.4 (the one size seen that loses).
 // The call's largest query count decides for all of its sequences: a chunk of 512 beside 31 that
 // decode, all on 8192 tokens, takes 258 us, where the two apart take 72 and 55.

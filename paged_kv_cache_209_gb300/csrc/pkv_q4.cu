@@ -38,11 +38,11 @@
 // that free up in order). With two row tiles 7 to 11 consumers an SM, rings of 12 and 16
 // stages and two blocks at a time are all within 4 us of the 85.5.
 //
-// Measured, 32 query heads on 8 of 128, in a captured graph: 32 sequences of 8192 tokens 56.4
+// Measured, 32 query heads on 8 of 128, in a captured graph: 32 sequences of 8192 tokens 56.5
 // us, 5.07 TB/s of records (the copy rate is 6.78); per token more 43.5 us for 8192, 6.57
 // TB/s: the rest is the way to the first records (5 us), the CTAs of an SM ending up to 8 us
-// apart, and joining the pieces (3 us). 32 of 131072 692 us, 6.59 TB/s; one of them 36.6. Two queries
-// a sequence take the same; four 86.0 us, 3.3 TB/s, out of L2 as out of HBM: with two row tiles a
+// apart, and joining the pieces (3 us). 32 of 131072 692 to 701 us, 6.5 TB/s; one of them 36.8. Two queries
+// a sequence take the same; four 86.7 us, 3.3 TB/s, out of L2 as out of HBM: with two row tiles a
 // warp there are two warps a scheduler, and one issues every 4.9 cycles (2.0 of them waiting on
 // the instruction before, 0.7 on loads, 0.8 for its turn or an instruction), 300 times a block of
 // which it takes 108: 81 us. No unit is full (issue slots 41 %, tensor pipe and ALU 37 %). Eight 154. 64 ragged contexts of up
